@@ -1,7 +1,10 @@
 /*
  * lsc_kv.h -- C ABI of liblsc's attention K/V block pool: page-strided K and V
- * views of every attention layer, and copy_prefix, the device copy that moves a
- * reused prefix's K/V rows into another sequence's blocks.
+ * views of every attention layer; copy_prefix, the device copy that moves a
+ * reused prefix's K/V rows into another sequence's blocks; and the calls of a
+ * step over one layer's blocks: append (write the new tokens' K/V rows,
+ * quantised when the pool holds e4m3), gather (read rows back dense) and
+ * attend (softmax attention of the new tokens over the cached ones).
  *
  * Sources, cited by page title and section:
  *   [VA] "非连续 KV Cache" (vLLM-Ascend design document) §3 (block stride =
@@ -17,6 +20,17 @@
  * block_tokens rows of kv_heads x head_dim elements (token-major, the §3.4
  * order), followed by padding to page_bytes that no call reads or writes.
  * Regions follow one another in layer order.
+ *
+ * E4M3 pools hold one 8-bit code per element and one scale byte per (token row,
+ * kv head): the payload is block_tokens rows of kv_heads x head_dim codes, then,
+ * at byte round_up(codes, 16) of the page, [block_tokens, kv_heads] scale bytes.
+ * Element x of a row is code * 2^(byte - 127); byte 255 marks a row that held a
+ * NaN or an infinity and reads back as NaN.  A written row takes the smallest
+ * power of two, at least 2^-127 (byte 0; a row of zeros too), that brings its
+ * largest magnitude to 448 or less, the largest e4m3 value, and each element is
+ * rounded once, to nearest even.  A power of two keeps the product exact, so the
+ * only error is that one rounding (half a step: 2^-4 of the element, or 2^-10
+ * times the scale below 2^-6 times it).
  *
  * Conventions are those of lsc.h (return codes, host/device pointers, streams,
  * no host sync except create/destroy).
@@ -54,7 +68,7 @@ typedef struct {
   int64_t lane_stride;     /* v - k: num_blocks * page_bytes / es (dim 0 of the merged view) */
   int64_t page_bytes, payload_bytes, row_bytes;
   int32_t dtype;
-  int32_t reserved;
+  int32_t scale_offset;    /* E4M3: byte of a page where its scale bytes begin; 0 for other types */
 } lsc_kv_layer_view;
 
 /* One block of a prefix copy: token rows [0, n_tokens) of src_block go to
@@ -68,23 +82,28 @@ typedef struct {
 
 /* Bytes a pool with this description needs: num_layers * 2 * num_blocks *
  * page_bytes.  Errors: INVALID_ARG, LAYOUT (page smaller than the payload or
- * not a multiple of the element size), MISALIGNED (page not a multiple of 16). */
+ * not a multiple of the element size, or an E4M3 block of 2 GiB or more), MISALIGNED (page not a multiple of 16). */
 int lsc_kv_pool_required_bytes(const lsc_kv_pool_desc *desc, size_t *total_bytes);
 
 /* Create a K/V pool; device_base == NULL allocates (cudaMalloc, owned),
  * otherwise the 256-byte-aligned buffer is borrowed.  Without a GPU a borrowed
- * base gives a host-only pool (views work, copies return CUDA).  Errors: as
- * lsc_kv_pool_required_bytes, plus MISALIGNED (base), NO_MEMORY, CUDA. */
+ * base gives a host-only pool (views work, copies return CUDA).  On a GPU the
+ * library also allocates a 4-byte device status word and a pinned host word.
+ * Errors: as lsc_kv_pool_required_bytes, plus MISALIGNED (base), NO_MEMORY, CUDA. */
 int lsc_kv_pool_create(const lsc_kv_pool_desc *desc, void *device_base, size_t base_bytes, lsc_kv_pool **out);
 int lsc_kv_pool_destroy(lsc_kv_pool *pool);
 /* Errors: OUT_OF_RANGE (layer). */
 int lsc_kv_pool_layer_view(const lsc_kv_pool *pool, int32_t layer, lsc_kv_layer_view *out);
+/* As lsc_pool_status, for the K/V pool's status word: waits for `stream` (host
+ * sync), stores LSC_OK or the first device-side error (OUT_OF_RANGE,
+ * INVALID_ARG, DEV_TIMEOUT) and clears the word. */
+int lsc_kv_pool_status(lsc_kv_pool *pool, void *stream, int32_t *host_status);
 
 /*
  * copy_prefix ([KP] figure 2): for every op with n_tokens > 0, token rows
  * [0, n_tokens) of src_block are copied to dst_block in the K and V lanes of
- * every attention layer; nothing else changes (rows past n_tokens, padding,
- * source blocks, other blocks).  A prefix of T tokens is passed block by block:
+ * every attention layer (with their scale bytes in an E4M3 pool); nothing else
+ * changes (rows past n_tokens, padding, source blocks, other blocks).  A prefix of T tokens is passed block by block:
  * its full blocks with n_tokens = block_tokens, then the partial last one.
  * One persistent launch per 2560 ops, 16-byte vector copies, on `stream`;
  * `done_event` (may be NULL) is recorded after the last launch.  ops is a host
@@ -96,6 +115,133 @@ int lsc_kv_pool_layer_view(const lsc_kv_pool *pool, int32_t layer, lsc_kv_layer_
  */
 int lsc_copy_prefix(lsc_kv_pool *pool, const lsc_kv_copy_op *ops, int32_t n_ops, void *stream,
                     void *done_event, int64_t *bytes_copied);
+
+/* ---- one step over a layer's blocks ----------------------------------------- */
+
+/*
+ * The sequences of a step.  Sequence i brings n_i = cu_seqlens[i+1] -
+ * cu_seqlens[i] new tokens, rows [cu_seqlens[i], cu_seqlens[i+1]) of the dense
+ * arrays, and has kv_lens[i] tokens in the cache, the new ones included: new
+ * token j sits at position kv_lens[i] - n_i + j.  Position p is row
+ * p % block_tokens of block block_table[i][p / block_tokens].  Everything that
+ * varies from step to step is on the device, so a captured graph can be replayed
+ * with new lengths and tables.
+ *
+ * Rows of the dense arrays at and behind cu_seqlens[n_seq] belong to no sequence
+ * and are left as they were.  A token of a negative position (n_i > kv_lens[i])
+ * has no row in the cache: append does not write it, gather gives zeros, and
+ * attend, when causal, gives it an empty row.
+ *
+ * Found on the device, recorded in the pool's status word, never faulting:
+ *  - INVALID_ARG: cu_seqlens that does not begin with 0, decreases or exceeds
+ *    total_tokens.  No call reads or writes outside its arrays then; the batch's
+ *    dense rows (append: its blocks' rows) are unspecified.
+ *  - INVALID_ARG: kv_lens[i] < 0 or > max_blocks * block_tokens.  The sequence
+ *    is taken to have no cached tokens.
+ *  - OUT_OF_RANGE: a block id outside [0, num_blocks) where a position needs it.
+ *    append skips the row, gather gives zeros; what attend gives for that
+ *    sequence is unspecified.
+ */
+typedef struct {
+  int32_t n_seq;
+  int32_t total_tokens;       /* rows of the dense arrays, >= cu_seqlens[n_seq] */
+  int32_t max_blocks;         /* row length of block_table */
+  int32_t reserved;           /* must be 0 */
+  const int32_t *block_table; /* device [n_seq, max_blocks]; entries past a sequence's last block are not read */
+  const int32_t *cu_seqlens;  /* device [n_seq + 1], cu_seqlens[0] == 0, non-decreasing */
+  const int32_t *kv_lens;     /* device [n_seq] */
+} lsc_kv_batch;
+
+typedef struct {
+  lsc_kv_batch batch;
+  const void *k;    /* device [total_tokens, kv_heads, head_dim] at dtype */
+  const void *v;    /* the same */
+  int32_t dtype;    /* F32, BF16 or F16 */
+  int32_t reserved; /* must be 0 */
+  int64_t k_stride; /* elements from a token to the next (a slice of a wider projection); 0 = kv_heads * head_dim */
+  int64_t v_stride;
+} lsc_kv_append_args;
+
+/*
+ * Write the new tokens' K and V rows into layer `layer`'s blocks, in one launch.
+ * The pool's type is the dense type (bit-exact), another float type (each
+ * element rounded to nearest even, beyond the largest value to infinity) or E4M3
+ * (quantised as described at the top; the row's scale byte is written with it).
+ * Nothing else of the pool changes.  When two tokens of a call share a row of a
+ * block, which one stays is unspecified.  Errors: INVALID_ARG (NULL, negative
+ * or zero sizes, reserved != 0, dtype, a stride below kv_heads * head_dim),
+ * OUT_OF_RANGE (layer), MISALIGNED (an array not aligned to its element),
+ * CUDA, WRONG_DEVICE.
+ */
+int lsc_kv_append(lsc_kv_pool *pool, int32_t layer, const lsc_kv_append_args *args, void *stream);
+
+typedef struct {
+  lsc_kv_batch batch;
+  void *k;          /* device [total_tokens, kv_heads, head_dim] at dtype */
+  void *v;
+  int32_t dtype;    /* F32, BF16 or F16 */
+  int32_t reserved; /* must be 0 */
+  int64_t k_stride;
+  int64_t v_stride;
+} lsc_kv_gather_args;
+
+/*
+ * The inverse: the rows that the batch's tokens sit in, dense, in one launch.
+ * With n_i = kv_lens[i] it reads back whole sequences.  Elements are the pool's
+ * values (E4M3: code times scale) rounded once to dtype.  Errors as lsc_kv_append.
+ */
+int lsc_kv_gather(lsc_kv_pool *pool, int32_t layer, const lsc_kv_gather_args *args, void *stream);
+
+typedef struct {
+  lsc_kv_batch batch;
+  int32_t num_q_heads;    /* a multiple of kv_heads: q head h reads kv head h / (num_q_heads / kv_heads) */
+  int32_t dtype;          /* of q and out: F32, BF16 or F16 */
+  const void *q;          /* device [total_tokens, num_q_heads, head_dim] */
+  void *out;              /* device, same shape; overlaps no input */
+  float *lse;             /* device [total_tokens, num_q_heads] or NULL */
+  float scale;            /* of the scores, > 0 */
+  int32_t causal;         /* 1: a token sees positions up to its own; 0: all kv_lens[i] positions */
+  int64_t q_stride;       /* elements from a token to the next; 0 = num_q_heads * head_dim */
+  int64_t out_stride;
+  int32_t max_seq_tokens; /* bound of every n_i that the host knows; 0 = total_tokens */
+  int32_t max_kv_tokens;  /* bound of every kv_lens[i] that the host knows; 0 = max_blocks * block_tokens */
+  void *workspace;        /* device scratch of at least workspace_bytes
+                             (lsc_kv_attend_workspace_bytes), 16-byte aligned, untouched by
+                             others until the call's work on the stream completes; NULL = the
+                             library takes it from the device's stream-ordered pool */
+  size_t workspace_bytes;
+} lsc_kv_attend_args;
+
+/*
+ * Attention of the new tokens over layer `layer`'s cached tokens (the new ones
+ * included: append first):
+ *   s_j = scale q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *   lse = log sum_j exp(s_j)   (natural logarithm)
+ * over the positions j that the token sees.  A token that sees none gets zeros
+ * and lse = -infinity.  Positions it does not see, and rows behind a sequence's
+ * last token, do not enter, whatever they hold.  Sums and softmax statistics
+ * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded to 16 bits
+ * before they meet v.  Two calls with the same inputs give the same bits.
+ * A sequence that exceeds max_seq_tokens or max_kv_tokens is recorded as
+ * INVALID_ARG in the status word and taken to have no cached tokens.  If a bounded
+ * device wait expires (DEV_TIMEOUT in the status word), out and lse are
+ * unspecified.
+ * Supported: head_dim <= 512.  Pools of q's 16-bit type, and E4M3 pools with
+ * 16-bit q, at head_dim 64, 128 and 256, with q and out 16-byte aligned in base
+ * and stride, run on the tensor cores; every other combination (F32, q of
+ * another type than the pool's, other head sizes) on the CUDA cores.
+ * Errors: INVALID_ARG (as lsc_kv_append; num_q_heads no multiple of kv_heads;
+ * scale not positive and finite; causal not 0 or 1; negative bounds; a
+ * workspace that is too small), OUT_OF_RANGE (layer), UNSUPPORTED, MISALIGNED
+ * (an array, or the workspace), NO_MEMORY (no workspace to be had), CUDA,
+ * WRONG_DEVICE.
+ */
+int lsc_kv_attend(lsc_kv_pool *pool, int32_t layer, const lsc_kv_attend_args *args, void *stream);
+
+/* Bytes of workspace lsc_kv_attend needs for these arguments (0: none).  Reads
+ * the sizes only, so one workspace of the largest size serves every layer and
+ * step of a stream.  Errors: as lsc_kv_attend's argument checks. */
+int lsc_kv_attend_workspace_bytes(const lsc_kv_pool *pool, const lsc_kv_attend_args *args, size_t *bytes);
 
 #ifdef __cplusplus
 }

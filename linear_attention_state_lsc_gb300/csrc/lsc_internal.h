@@ -234,9 +234,57 @@ struct KvPlan {
   int64_t region_bytes;  // one attention layer: both lanes
   int64_t lane_bytes;    // num_blocks pages
   int64_t page, row_bytes, chunk_bytes;
-  int32_t num_layers, n_ops, chunks_per_op, pad;
+  int32_t num_layers, n_ops, chunks_per_op;
+  int32_t scale_off;       // E4M3: page offset of the scale bytes, else 0
+  int32_t scale_row;       // E4M3: scale bytes of a token row (kv heads)
   int3 op[kKvPlanMaxOps];  // (src block, dst block, n_tokens > 0)
 };
 cudaError_t launch_kv_copy(const KvPlan &p, int num_sms, cudaStream_t stream);
+
+// ---- one step over a K/V layer's blocks --------------------------------------
+// One attention layer of a K/V pool.
+struct KvLayer {
+  uint8_t *k, *v;       // block 0 of each lane
+  int64_t page;         // bytes from a block to the next
+  int32_t num_blocks, block_tokens, heads, head_dim;
+  int32_t dtype;        // lsc_dtype
+  int32_t scale_off;    // E4M3: page offset of the scale bytes
+  int32_t *status;      // device error word
+};
+
+struct KvBatch {
+  int32_t n_seq, total_tokens, max_blocks;
+  const int32_t *table, *cu, *kv;
+};
+
+struct KvRowsParams {
+  KvLayer L;
+  KvBatch b;
+  void *k, *v;          // dense rows
+  int64_t k_stride, v_stride;
+  int32_t dtype;
+};
+cudaError_t launch_kv_append(const KvRowsParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_gather(const KvRowsParams &p, int num_sms, cudaStream_t stream);
+
+struct KvAttendParams {
+  KvLayer L;
+  KvBatch b;
+  const void *q;
+  void *out;
+  float *lse;           // may be null
+  int64_t q_stride, out_stride;
+  int32_t dtype;        // of q and out
+  int32_t heads;        // q heads
+  int32_t group;        // q heads per kv head
+  int32_t causal;
+  float scale_log2;     // scale * log2(e): the softmax runs in powers of two
+  int32_t max_seq, max_kv;  // host bounds of the lengths
+  uint8_t *ws;
+  uint64_t wait_limit_ns;
+  int32_t num_sms;
+};
+// the CUDA-core kernel: every type, head size and alignment (head_dim <= 512)
+cudaError_t launch_kv_attend_any(const KvAttendParams &p, cudaStream_t stream);
 
 }  // namespace lsc

@@ -1,6 +1,7 @@
 // lsc_kv.cu -- host side of the attention K/V block pool (include/lsc_kv.h):
-// layout, views, and copy_prefix's validation and launch plans.  The copy
-// kernel is kv_copy_kernel in lsc_copy.cu.
+// layout, views, copy_prefix's validation and launch plans, and the argument
+// checks of append, gather and attend.  The copy kernel is kv_copy_kernel in
+// lsc_copy.cu; append and gather are in lsc_kv_rows.cu.
 //
 // Sources, cited by page title and section:
 //   [VA] "非连续 KV Cache" §3, §3.2, §3.4 (page-strided block views, separate K
@@ -9,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <new>
 #include <vector>
@@ -23,6 +25,9 @@ struct lsc_kv_pool {
   uint8_t *base = nullptr;
   bool owns_base = false;
   int64_t es = 0, row_bytes = 0, payload = 0, lane_bytes = 0, region_bytes = 0;
+  int32_t scale_off = 0;        // E4M3: page offset of the scale bytes
+  int32_t *status = nullptr;    // device error word
+  int32_t *h_status = nullptr;  // pinned
 };
 
 namespace {
@@ -32,9 +37,13 @@ int esize(int32_t dtype) {
     case LSC_F32: return 4;
     case LSC_BF16: return 2;
     case LSC_F16: return 2;
+    case LSC_E4M3: return 1;
     default: return 0;
   }
 }
+
+// Bound of every device-side wait (mbarrier), in nanoseconds.
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 // [VA] §3: block stride = physical page size / element size, so the page must
 // hold the logical block and divide by the element size; 16-byte vector copies
@@ -49,10 +58,110 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
   g->es = es;
   g->row_bytes = (int64_t)d->num_kv_heads * d->head_dim * es;
   g->payload = g->row_bytes * d->block_tokens;
+  if (d->dtype == LSC_E4M3) {  // codes, then one scale byte per (row, head) at the next 16 B boundary
+    const int64_t off = (g->payload + 15) / 16 * 16;
+    if (off > INT32_MAX) return LSC_ERR_LAYOUT;
+    g->scale_off = (int32_t)off;
+    g->payload = off + (int64_t)d->block_tokens * d->num_kv_heads;
+  }
   if (d->page_bytes < g->payload || d->page_bytes % es) return LSC_ERR_LAYOUT;
   if (d->page_bytes % 16) return LSC_ERR_MISALIGNED;
   g->lane_bytes = (int64_t)d->num_blocks * d->page_bytes;
   g->region_bytes = 2 * g->lane_bytes;
+  return LSC_OK;
+}
+
+int check_device(const lsc_kv_pool *p) {
+  if (p->device < 0) return LSC_ERR_CUDA;  // host-only pool
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return LSC_ERR_CUDA;
+  }
+  return dev == p->device ? LSC_OK : LSC_ERR_WRONG_DEVICE;
+}
+
+lsc::KvLayer layer_of(const lsc_kv_pool *p, int32_t layer) {
+  lsc::KvLayer L{};
+  L.k = p->base + (int64_t)layer * p->region_bytes;
+  L.v = L.k + p->lane_bytes;
+  L.page = p->d.page_bytes;
+  L.num_blocks = p->d.num_blocks;
+  L.block_tokens = p->d.block_tokens;
+  L.heads = p->d.num_kv_heads;
+  L.head_dim = p->d.head_dim;
+  L.dtype = p->d.dtype;
+  L.scale_off = p->scale_off;
+  L.status = p->status;
+  return L;
+}
+
+bool misaligned(const void *q, uintptr_t a) { return ((uintptr_t)q % a) != 0; }
+
+// The checks every step call shares; out receives the batch.
+int check_batch(const lsc_kv_batch &b, lsc::KvBatch *out) {
+  if (b.n_seq < 0 || b.total_tokens < 0 || b.max_blocks < 0 || b.reserved != 0) return LSC_ERR_INVALID_ARG;
+  if (b.n_seq > 0 && (!b.cu_seqlens || !b.kv_lens || (b.max_blocks > 0 && !b.block_table))) return LSC_ERR_INVALID_ARG;
+  if (misaligned(b.cu_seqlens, 4) || misaligned(b.kv_lens, 4) || misaligned(b.block_table, 4))
+    return LSC_ERR_MISALIGNED;
+  *out = {b.n_seq, b.total_tokens, b.max_blocks, b.block_table, b.cu_seqlens, b.kv_lens};
+  return LSC_OK;
+}
+
+// The dense side of append and gather.
+int check_rows(const lsc_kv_pool *p, int32_t layer, const lsc_kv_batch &b, const void *k, const void *v, int32_t dtype,
+               int32_t reserved, int64_t k_stride, int64_t v_stride, lsc::KvRowsParams *r) {
+  if (layer < 0 || layer >= p->d.num_layers) return LSC_ERR_OUT_OF_RANGE;
+  const int rc = check_batch(b, &r->b);
+  if (rc != LSC_OK) return rc;
+  if (reserved != 0 || (dtype != LSC_F32 && dtype != LSC_BF16 && dtype != LSC_F16)) return LSC_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)p->d.num_kv_heads * p->d.head_dim;
+  if ((k_stride != 0 && k_stride < row) || (v_stride != 0 && v_stride < row)) return LSC_ERR_INVALID_ARG;
+  if (b.n_seq > 0 && b.total_tokens > 0 && (!k || !v)) return LSC_ERR_INVALID_ARG;
+  if (misaligned(k, esize(dtype)) || misaligned(v, esize(dtype))) return LSC_ERR_MISALIGNED;
+  r->L = layer_of(p, layer);
+  r->k = const_cast<void *>(k);
+  r->v = const_cast<void *>(v);
+  r->k_stride = k_stride ? k_stride : row;
+  r->v_stride = v_stride ? v_stride : row;
+  r->dtype = dtype;
+  return check_device(p);
+}
+
+// attend's arguments; out receives the launch parameters without the workspace.
+int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, lsc::KvAttendParams *r) {
+  if (!p || !a) return LSC_ERR_INVALID_ARG;
+  if (layer < 0 || layer >= p->d.num_layers) return LSC_ERR_OUT_OF_RANGE;
+  const int rc = check_batch(a->batch, &r->b);
+  if (rc != LSC_OK) return rc;
+  const int32_t H = p->d.num_kv_heads, D = p->d.head_dim;
+  if (a->num_q_heads <= 0 || a->num_q_heads % H != 0) return LSC_ERR_INVALID_ARG;
+  if (a->dtype != LSC_F32 && a->dtype != LSC_BF16 && a->dtype != LSC_F16) return LSC_ERR_INVALID_ARG;
+  if (!(a->scale > 0.f) || std::isinf(a->scale * 1.44269504088896341f) || (a->causal != 0 && a->causal != 1)) return LSC_ERR_INVALID_ARG;
+  if (a->max_seq_tokens < 0 || a->max_kv_tokens < 0) return LSC_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)a->num_q_heads * D;
+  if ((a->q_stride != 0 && a->q_stride < row) || (a->out_stride != 0 && a->out_stride < row)) return LSC_ERR_INVALID_ARG;
+  if (a->batch.n_seq > 0 && a->batch.total_tokens > 0 && (!a->q || !a->out)) return LSC_ERR_INVALID_ARG;
+  if (D > 512) return LSC_ERR_UNSUPPORTED;
+  if (misaligned(a->q, esize(a->dtype)) || misaligned(a->out, esize(a->dtype)) || misaligned(a->lse, 4) ||
+      misaligned(a->workspace, 16))
+    return LSC_ERR_MISALIGNED;
+  r->L = layer_of(p, layer);
+  r->q = a->q;
+  r->out = a->out;
+  r->lse = a->lse;
+  r->q_stride = a->q_stride ? a->q_stride : row;
+  r->out_stride = a->out_stride ? a->out_stride : row;
+  r->dtype = a->dtype;
+  r->heads = a->num_q_heads;
+  r->group = a->num_q_heads / H;
+  r->causal = a->causal;
+  r->scale_log2 = a->scale * 1.44269504088896341f;
+  r->max_seq = a->max_seq_tokens ? a->max_seq_tokens : a->batch.total_tokens;
+  const int64_t held = (int64_t)a->batch.max_blocks * p->d.block_tokens;
+  r->max_kv = a->max_kv_tokens ? a->max_kv_tokens : (int32_t)std::min<int64_t>(held, INT32_MAX);
+  r->num_sms = p->num_sms;
+  r->wait_limit_ns = kWaitLimitNs;
   return LSC_OK;
 }
 
@@ -107,11 +216,25 @@ int lsc_kv_pool_create(const lsc_kv_pool_desc *desc, void *device_base, size_t b
     delete p;
     return LSC_ERR_CUDA;
   }
+  if (cudaMalloc(&p->status, 256) != cudaSuccess) {
+    cudaGetLastError();
+    delete p;
+    return LSC_ERR_NO_MEMORY;
+  }
+  if (cudaMemset(p->status, 0, 256) != cudaSuccess ||
+      cudaMallocHost(&p->h_status, sizeof(int32_t)) != cudaSuccess) {
+    cudaGetLastError();
+    cudaFree(p->status);
+    delete p;
+    return LSC_ERR_CUDA;
+  }
   if (device_base) {
     p->base = (uint8_t *)device_base;
   } else {
     if (cudaMalloc(&p->base, need) != cudaSuccess) {
       cudaGetLastError();
+      cudaFree(p->status);
+      cudaFreeHost(p->h_status);
       delete p;
       return LSC_ERR_NO_MEMORY;
     }
@@ -124,9 +247,11 @@ int lsc_kv_pool_create(const lsc_kv_pool_desc *desc, void *device_base, size_t b
 int lsc_kv_pool_destroy(lsc_kv_pool *p) {
   if (!p) return LSC_ERR_INVALID_ARG;
   int rc = LSC_OK;
-  if (p->owns_base) {
+  if (p->device >= 0) {
     if (cudaDeviceSynchronize() != cudaSuccess) rc = LSC_ERR_CUDA;
-    cudaFree(p->base);
+    if (p->owns_base) cudaFree(p->base);
+    cudaFree(p->status);
+    cudaFreeHost(p->h_status);
   }
   delete p;
   return rc;
@@ -154,6 +279,20 @@ int lsc_kv_pool_layer_view(const lsc_kv_pool *p, int32_t layer, lsc_kv_layer_vie
   v->payload_bytes = p->payload;
   v->row_bytes = p->row_bytes;
   v->dtype = p->d.dtype;
+  v->scale_offset = p->scale_off;
+  return LSC_OK;
+}
+
+int lsc_kv_pool_status(lsc_kv_pool *p, void *stream, int32_t *host_status) {
+  lsc::TraceRange trace_("lsc_kv_pool_status");
+  if (!p || !host_status) return LSC_ERR_INVALID_ARG;
+  const int rc = check_device(p);
+  if (rc != LSC_OK) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (cudaMemcpyAsync(p->h_status, p->status, sizeof(int32_t), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaMemsetAsync(p->status, 0, sizeof(int32_t), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+    return LSC_ERR_CUDA;
+  *host_status = *p->h_status;
   return LSC_OK;
 }
 
@@ -162,6 +301,7 @@ int lsc_copy_prefix(lsc_kv_pool *p, const lsc_kv_copy_op *ops, int32_t n_ops, vo
   lsc::TraceRange trace_("lsc_copy_prefix");
   if (!p || n_ops < 0 || (n_ops > 0 && !ops)) return LSC_ERR_INVALID_ARG;
   const int32_t B = p->d.num_blocks;
+  const int32_t scale_row = p->d.dtype == LSC_E4M3 ? p->d.num_kv_heads : 0;
   // validate every copying op before enqueueing anything
   std::vector<int32_t> dst_owner;
   try {
@@ -178,19 +318,14 @@ int lsc_copy_prefix(lsc_kv_pool *p, const lsc_kv_copy_op *ops, int32_t n_ops, vo
     if (o.src_block < 0 || o.src_block >= B || o.dst_block < 0 || o.dst_block >= B) return LSC_ERR_OUT_OF_RANGE;
     if (dst_owner[o.dst_block] >= 0) return LSC_ERR_DUP_DST;
     dst_owner[o.dst_block] = r;
-    bytes += (int64_t)o.n_tokens * p->row_bytes * 2 * p->d.num_layers;
+    bytes += (int64_t)o.n_tokens * (p->row_bytes + scale_row) * 2 * p->d.num_layers;
     ++n_copy;
     last_copy = r;
   }
   for (int32_t r = 0; r < n_ops; ++r)
     if (ops[r].n_tokens > 0 && dst_owner[ops[r].src_block] >= 0) return LSC_ERR_SRC_IS_DST;
-  if (p->device < 0) return LSC_ERR_CUDA;
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return LSC_ERR_CUDA;
-  }
-  if (dev != p->device) return LSC_ERR_WRONG_DEVICE;
+  const int rc = check_device(p);
+  if (rc != LSC_OK) return rc;
   cudaStream_t s = (cudaStream_t)stream;
   if (n_copy > 0) {
     static thread_local lsc::KvPlan plan;  // 30 KB: kept off the stack
@@ -201,8 +336,9 @@ int lsc_copy_prefix(lsc_kv_pool *p, const lsc_kv_copy_op *ops, int32_t n_ops, vo
     plan.row_bytes = p->row_bytes;
     plan.chunk_bytes = 32 << 10;
     plan.num_layers = p->d.num_layers;
-    plan.chunks_per_op = (int32_t)((p->payload + plan.chunk_bytes - 1) / plan.chunk_bytes);
-    plan.pad = 0;
+    plan.chunks_per_op = (int32_t)((p->row_bytes * p->d.block_tokens + plan.chunk_bytes - 1) / plan.chunk_bytes);
+    plan.scale_off = p->scale_off;
+    plan.scale_row = scale_row;
     plan.n_ops = 0;
     for (int32_t r = 0; r < n_ops; ++r) {
       if (ops[r].n_tokens == 0) continue;
@@ -221,6 +357,58 @@ int lsc_copy_prefix(lsc_kv_pool *p, const lsc_kv_copy_op *ops, int32_t n_ops, vo
     return LSC_ERR_CUDA;
   }
   if (bytes_copied) *bytes_copied = bytes;
+  return LSC_OK;
+}
+
+int lsc_kv_append(lsc_kv_pool *p, int32_t layer, const lsc_kv_append_args *a, void *stream) {
+  lsc::TraceRange trace_("lsc_kv_append");
+  if (!p || !a) return LSC_ERR_INVALID_ARG;
+  lsc::KvRowsParams r{};
+  const int rc = check_rows(p, layer, a->batch, a->k, a->v, a->dtype, a->reserved, a->k_stride, a->v_stride, &r);
+  if (rc != LSC_OK) return rc;
+  if (r.b.n_seq == 0 || r.b.total_tokens == 0) return LSC_OK;
+  if (lsc::launch_kv_append(r, p->num_sms, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return LSC_ERR_CUDA;
+  }
+  return LSC_OK;
+}
+
+int lsc_kv_gather(lsc_kv_pool *p, int32_t layer, const lsc_kv_gather_args *a, void *stream) {
+  lsc::TraceRange trace_("lsc_kv_gather");
+  if (!p || !a) return LSC_ERR_INVALID_ARG;
+  lsc::KvRowsParams r{};
+  const int rc = check_rows(p, layer, a->batch, a->k, a->v, a->dtype, a->reserved, a->k_stride, a->v_stride, &r);
+  if (rc != LSC_OK) return rc;
+  if (r.b.n_seq == 0 || r.b.total_tokens == 0) return LSC_OK;
+  if (lsc::launch_kv_gather(r, p->num_sms, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return LSC_ERR_CUDA;
+  }
+  return LSC_OK;
+}
+
+int lsc_kv_attend_workspace_bytes(const lsc_kv_pool *p, const lsc_kv_attend_args *a, size_t *bytes) {
+  if (!bytes) return LSC_ERR_INVALID_ARG;
+  lsc::KvAttendParams r{};
+  const int rc = check_attend(p, 0, a, &r);
+  if (rc != LSC_OK) return rc;
+  *bytes = 0;
+  return LSC_OK;
+}
+
+int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, void *stream) {
+  lsc::TraceRange trace_("lsc_kv_attend");
+  lsc::KvAttendParams r{};
+  int rc = check_attend(p, layer, a, &r);
+  if (rc != LSC_OK) return rc;
+  rc = check_device(p);
+  if (rc != LSC_OK) return rc;
+  if (r.b.n_seq == 0 || r.b.total_tokens == 0) return LSC_OK;
+  if (lsc::launch_kv_attend_any(r, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return LSC_ERR_CUDA;
+  }
   return LSC_OK;
 }
 

@@ -1,0 +1,395 @@
+// lsc_kv_rows.cu -- append and gather over a layer of the K/V block pool
+// (include/lsc_kv.h): dense rows of the new tokens -> rows of the sequences'
+// blocks, and back, with the E4M3 quantisation in the same pass.
+//
+// Both only move bytes: each dense element is read (written) once and each
+// element of a block written (read) once, so HBM bounds a large call and the
+// launch a small one.  A CTA takes a run of consecutive tokens, finds the
+// block row of each once (one thread per token: the sequence by a search of
+// cu_seqlens samples in shared memory, then the block table), then streams the
+// K and V rows of the run, kUnroll 16-byte loads in flight per thread.  A
+// (token, head) row is handled by one group of a warp's lanes, 8 elements each,
+// so an E4M3 row's largest magnitude is a shuffle reduction and the row is
+// never read twice.
+#include <cuda_runtime.h>
+
+#include "lsc_internal.h"
+#include "lsc_kv_batch.cuh"
+#include "lsc_ptx.h"
+
+namespace lsc {
+namespace {
+
+using namespace kv;
+
+constexpr int kThreads = 256;
+constexpr int kMaxTok = 16;  // tokens of a CTA's run
+constexpr int kUnroll = 4;   // rows in flight per lane group
+
+struct E4M3 {};
+
+// Where the tokens [t0, t0 + n) sit: page[i] = byte offset of the token's block
+// in a lane, row[i] its row there; row -1: no row in the cache, -2: the token
+// belongs to no sequence.
+struct Places {
+  int64_t page[kMaxTok];
+  int32_t row[kMaxTok];
+  int32_t cu[kThreads];
+};
+
+__device__ __forceinline__ void find_places(const KvLayer &L, const KvBatch &b, int32_t t0, int n, Places &s) {
+  // samples of cu_seqlens, a step of `step` apart: one load per thread
+  const int step = b.n_seq / kThreads + 1;
+  {
+    const int64_t i = (int64_t)threadIdx.x * step;
+    s.cu[threadIdx.x] = b.cu[i < b.n_seq ? i : b.n_seq];
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < n) {
+    const int32_t t = t0 + threadIdx.x;
+    int lo = -1, hi = kThreads;  // the last sample <= t
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (s.cu[m] <= t) lo = m;
+      else hi = m;
+    }
+    int32_t row = -2;
+    int64_t page = 0;
+    if (lo >= 0) {
+      int64_t a = (int64_t)lo * step, z = a + step;  // the last entry <= t is in [a, z)
+      if (a > b.n_seq) a = b.n_seq;
+      if (z > (int64_t)b.n_seq + 1) z = (int64_t)b.n_seq + 1;
+      while (z - a > 1) {
+        const int64_t m = (a + z) >> 1;
+        if (b.cu[m] <= t) a = m;
+        else z = m;
+      }
+      if (a < b.n_seq) {
+        const int32_t c0 = b.cu[a], c1 = b.cu[a + 1];
+        row = -1;
+        if (c0 <= t && t < c1) {
+          const int32_t kv = checked_kv(L, b, b.kv[a]);
+          const int64_t pos = (int64_t)kv - ((int64_t)c1 - c0) + (t - c0);
+          if (pos >= 0) {
+            const int32_t q = (int32_t)pos / L.block_tokens;
+            const int32_t blk = b.table[a * b.max_blocks + q];
+            if (blk >= 0 && blk < L.num_blocks) {
+              row = (int32_t)pos - q * L.block_tokens;
+              page = (int64_t)blk * L.page;
+            } else {
+              report(L.status, LSC_ERR_OUT_OF_RANGE);
+            }
+          }
+        }
+      }
+    }
+    s.row[threadIdx.x] = row;
+    s.page[threadIdx.x] = page;
+  }
+  __syncthreads();
+}
+
+// ---- eight elements of a row ---------------------------------------------------
+template <typename T>
+struct Eight;  // raw vector of 8 elements, and its floats
+template <>
+struct Eight<float> {
+  uint4 a, b;
+  __device__ void load(const void *p) { a = __ldcs((const uint4 *)p), b = __ldcs((const uint4 *)p + 1); }
+  __device__ void store(void *p) const { ((uint4 *)p)[0] = a, ((uint4 *)p)[1] = b; }
+  __device__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  __device__ void get(float (&x)[8]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  }
+  __device__ void put(const float (&x)[8]) {
+    a = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    b = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+  }
+};
+template <typename H2>
+struct Eight16 {
+  uint4 a;
+  __device__ void load(const void *p) { a = __ldcs((const uint4 *)p); }
+  __device__ void store(void *p) const { *(uint4 *)p = a; }
+  __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  static __device__ float2 two(uint32_t w);
+  static __device__ uint32_t pack(float x, float y);
+  __device__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = two(w[i]);
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+  __device__ void put(const float (&x)[8]) {
+    a = make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
+  }
+};
+template <>
+__device__ __forceinline__ float2 Eight16<__nv_bfloat162>::two(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ uint32_t Eight16<__nv_bfloat162>::pack(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ float2 Eight16<__half2>::two(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <>
+__device__ __forceinline__ uint32_t Eight16<__half2>::pack(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+struct Eight<__nv_bfloat16> : Eight16<__nv_bfloat162> {};
+template <>
+struct Eight<__half> : Eight16<__half2> {};
+
+template <typename T>
+constexpr int kSize = (int)sizeof(T);
+template <>
+constexpr int kSize<E4M3> = 1;
+
+template <typename A, typename B>
+struct Same {
+  static constexpr bool value = false;
+};
+template <typename A>
+struct Same<A, A> {
+  static constexpr bool value = true;
+};
+
+// ---- vector kernel: head_dim a multiple of 8 and at most 256 --------------------
+// APPEND: dense -> pool; else pool -> dense.  lanes = lanes of a row's group
+// (a power of two >= head_dim / 8).
+template <bool APPEND, typename D, typename P>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ KvRowsParams p, int tok, int lanes) {
+  __shared__ Places s;
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const KvLayer &L = p.L;
+  if (blockIdx.x == 0) check_cu(L, p.b);
+  const int32_t t0 = (int32_t)blockIdx.x * tok;
+  const int n = p.b.total_tokens - t0 < tok ? p.b.total_tokens - t0 : tok;
+  find_places(L, p.b, t0, n, s);
+  const int groups = kThreads / lanes, g = threadIdx.x / lanes, sub = threadIdx.x & (lanes - 1);
+  const bool on = sub * 8 < L.head_dim;
+  const int rows = n * 2 * L.heads;
+  const int64_t head_bytes = (int64_t)L.head_dim * kSize<P>;
+  for (int r0 = 0; r0 < rows; r0 += groups * kUnroll) {  // the same trips in every thread: the groups shuffle
+    Eight<D> x[kUnroll];
+    uint2 code[kUnroll];
+    uint32_t byte[kUnroll];
+    int32_t row[kUnroll];
+    uint8_t *page[kUnroll];
+    int head[kUnroll];
+    uint8_t *dense[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int r = r0 + u * groups + g;
+      const int i = r / (2 * L.heads), lane = (r / L.heads) & 1;
+      head[u] = r - (r / L.heads) * L.heads;
+      row[u] = r < rows ? s.row[i] : -2;
+      x[u].zero();
+      code[u] = make_uint2(0, 0);
+      byte[u] = 0;
+      if (row[u] == -2) continue;
+      page[u] = (lane ? L.v : L.k) + s.page[i];
+      dense[u] = (uint8_t *)(lane ? p.v : p.k) +
+                 ((int64_t)(t0 + i) * (lane ? p.v_stride : p.k_stride) + (int64_t)head[u] * L.head_dim + sub * 8) *
+                     kSize<D>;
+      if (row[u] == -1 || !on) continue;
+      if constexpr (APPEND) {
+        x[u].load(dense[u]);
+      } else {
+        const uint8_t *src = page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes + sub * 8 * kSize<P>;
+        if constexpr (Same<P, E4M3>::value) {
+          code[u] = __ldcs((const uint2 *)src);
+          byte[u] = __ldcs(page[u] + L.scale_off + (int64_t)row[u] * L.heads + head[u]);
+        } else if constexpr (Same<P, D>::value) {
+          x[u].load(src);
+        } else {
+          Eight<P> y;
+          float f[8];
+          y.load(src);
+          y.get(f);
+          x[u].put(f);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if constexpr (APPEND) {
+        uint8_t *dst = row[u] < 0 ? nullptr : page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes +
+                                                  sub * 8 * kSize<P>;
+        if constexpr (Same<P, E4M3>::value) {
+          float f[8];
+          x[u].get(f);
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+          for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const uint32_t sb = scale_byte(m);
+          const float inv = inv_scale_of(sb);
+          uint2 c = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+          if (sb != 255) {
+            c.x = to_e4m3x2(f[0] * inv, f[1] * inv) | to_e4m3x2(f[2] * inv, f[3] * inv) << 16;
+            c.y = to_e4m3x2(f[4] * inv, f[5] * inv) | to_e4m3x2(f[6] * inv, f[7] * inv) << 16;
+          }
+          if (dst && on) *(uint2 *)dst = c;
+          if (dst && sub == 0) page[u][L.scale_off + (int64_t)row[u] * L.heads + head[u]] = (uint8_t)sb;
+        } else if (dst && on) {
+          if constexpr (Same<P, D>::value) {
+            x[u].store(dst);
+          } else {
+            Eight<P> y;
+            float f[8];
+            x[u].get(f);
+            y.put(f);
+            y.store(dst);
+          }
+        }
+      } else {
+        if (row[u] == -2 || !on) continue;
+        if constexpr (Same<P, E4M3>::value) {
+          if (row[u] >= 0) {
+            const float k = scale_of(byte[u]);
+            const uint32_t w[4] = {code[u].x & 0xffffu, code[u].x >> 16, code[u].y & 0xffffu, code[u].y >> 16};
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 v = e4m3x2_to_float2(w[e]);
+              f[2 * e] = v.x * k, f[2 * e + 1] = v.y * k;
+            }
+            x[u].put(f);
+          }
+        }
+        x[u].store(dense[u]);
+      }
+    }
+  }
+}
+
+// ---- element kernel: any head_dim, types and alignment -------------------------
+// A warp takes a (token, lane, head) row, its lanes stride over the elements.
+__device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype) {
+  if (dtype == LSC_F32) return ((const float *)p)[i];
+  if (dtype == LSC_BF16) return __bfloat162float(((const __nv_bfloat16 *)p)[i]);
+  return __half2float(((const __half *)p)[i]);
+}
+__device__ __forceinline__ void store_any(void *p, int64_t i, int dtype, float x) {
+  if (dtype == LSC_F32) ((float *)p)[i] = x;
+  else if (dtype == LSC_BF16) ((__nv_bfloat16 *)p)[i] = __float2bfloat16_rn(x);
+  else ((__half *)p)[i] = __float2half_rn(x);
+}
+// The same type on both sides moves as bits (a NaN keeps its payload).
+__device__ __forceinline__ void move_any(void *d, int64_t i, const void *s, int64_t j, int dtype) {
+  if (dtype == LSC_F32) ((uint32_t *)d)[i] = ((const uint32_t *)s)[j];
+  else ((uint16_t *)d)[i] = ((const uint16_t *)s)[j];
+}
+
+template <bool APPEND>
+__global__ void __launch_bounds__(kThreads) rows_any_kernel(const __grid_constant__ KvRowsParams p, int tok) {
+  __shared__ Places s;
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const KvLayer &L = p.L;
+  if (blockIdx.x == 0) check_cu(L, p.b);
+  const int32_t t0 = (int32_t)blockIdx.x * tok;
+  const int n = p.b.total_tokens - t0 < tok ? p.b.total_tokens - t0 : tok;
+  find_places(L, p.b, t0, n, s);
+  const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
+  const int rows = n * 2 * L.heads, D = L.head_dim;
+  for (int r = warp; r < rows; r += kThreads / 32) {
+    const int i = r / (2 * L.heads), lane = (r / L.heads) & 1, head = r - (r / L.heads) * L.heads;
+    const int32_t row = s.row[i];
+    if (row == -2 || (APPEND && row == -1)) continue;
+    uint8_t *page = (lane ? L.v : L.k) + s.page[i];
+    const int64_t in = ((int64_t)row * L.heads + head) * D;  // first element within the block
+    void *dense = lane ? p.v : p.k;
+    const int64_t at = (int64_t)(t0 + i) * (lane ? p.v_stride : p.k_stride) + (int64_t)head * D;
+    uint8_t *scale = page + L.scale_off + (int64_t)row * L.heads + head;
+    if (row == -1) {
+      for (int d = ln; d < D; d += 32) store_any(dense, at + d, p.dtype, 0.f);
+    } else if (L.dtype == LSC_E4M3 && APPEND) {
+      uint32_t m = 0;
+      for (int d = ln; d < D; d += 32) m = max(m, __float_as_uint(load_any(dense, at + d, p.dtype)) & 0x7fffffffu);
+      m = __reduce_max_sync(0xffffffffu, m);
+      const uint32_t sb = scale_byte(m);
+      const float inv = inv_scale_of(sb);
+      for (int d = ln; d < D; d += 32)
+        page[in + d] = sb == 255 ? 0x7f : (uint8_t)to_e4m3x2(load_any(dense, at + d, p.dtype) * inv, 0.f);
+      if (ln == 0) *scale = (uint8_t)sb;
+    } else if (L.dtype == LSC_E4M3) {
+      const float k = scale_of(*scale);
+      for (int d = ln; d < D; d += 32) store_any(dense, at + d, p.dtype, e4m3x2_to_float2(page[in + d]).x * k);
+    } else if (L.dtype == p.dtype) {
+      for (int d = ln; d < D; d += 32) {
+        if (APPEND) move_any(page, in + d, dense, at + d, p.dtype);
+        else move_any(dense, at + d, page, in + d, p.dtype);
+      }
+    } else {
+      for (int d = ln; d < D; d += 32) {
+        if (APPEND) store_any(page, in + d, L.dtype, load_any(dense, at + d, p.dtype));
+        else store_any(dense, at + d, p.dtype, load_any(page, in + d, L.dtype));
+      }
+    }
+  }
+}
+
+template <bool APPEND, typename D, typename P>
+cudaError_t launch_typed(const KvRowsParams &p, int grid, int tok, int lanes, cudaStream_t stream) {
+  return launch_pdl(rows_kernel<APPEND, D, P>, grid, kThreads, 0, stream, p, tok, lanes);
+}
+
+template <bool APPEND, typename D>
+cudaError_t launch_dense(const KvRowsParams &p, int grid, int tok, int lanes, cudaStream_t stream) {
+  switch (p.L.dtype) {
+    case LSC_F32: return launch_typed<APPEND, D, float>(p, grid, tok, lanes, stream);
+    case LSC_BF16: return launch_typed<APPEND, D, __nv_bfloat16>(p, grid, tok, lanes, stream);
+    case LSC_F16: return launch_typed<APPEND, D, __half>(p, grid, tok, lanes, stream);
+    default: return launch_typed<APPEND, D, E4M3>(p, grid, tok, lanes, stream);
+  }
+}
+
+template <bool APPEND>
+cudaError_t launch_rows(const KvRowsParams &p, int num_sms, cudaStream_t stream) {
+  const KvLayer &L = p.L;
+  const int64_t T = p.b.total_tokens;
+  // A run of kMaxTok tokens per CTA, shorter while the grid would leave SMs idle.
+  int tok = kMaxTok;
+  while (tok > 1 && (T + tok - 1) / tok < 2 * (int64_t)num_sms) tok >>= 1;
+  const int grid = (int)((T + tok - 1) / tok);
+  const int es = p.dtype == LSC_F32 ? 4 : 2;
+  const bool vec = L.head_dim % 8 == 0 && L.head_dim <= 256 &&
+                   (((uintptr_t)p.k | (uintptr_t)p.v | (uintptr_t)(p.k_stride * es) | (uintptr_t)(p.v_stride * es)) & 15) == 0;
+  cudaError_t e;
+  if (!vec) {
+    e = launch_pdl(rows_any_kernel<APPEND>, grid, kThreads, 0, stream, p, tok);
+  } else {
+    int lanes = 1;
+    while (lanes * 8 < L.head_dim) lanes <<= 1;
+    e = p.dtype == LSC_F32    ? launch_dense<APPEND, float>(p, grid, tok, lanes, stream)
+        : p.dtype == LSC_BF16 ? launch_dense<APPEND, __nv_bfloat16>(p, grid, tok, lanes, stream)
+                              : launch_dense<APPEND, __half>(p, grid, tok, lanes, stream);
+  }
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvRowsParams &p, int num_sms, cudaStream_t stream) {
+  return launch_rows<true>(p, num_sms, stream);
+}
+
+cudaError_t launch_kv_gather(const KvRowsParams &p, int num_sms, cudaStream_t stream) {
+  return launch_rows<false>(p, num_sms, stream);
+}
+
+}  // namespace lsc

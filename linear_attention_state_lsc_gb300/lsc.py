@@ -42,7 +42,7 @@ LSC_SLOT_FREE, LSC_SLOT_LIVE, LSC_SLOT_CHECKPOINT, LSC_SLOT_RESERVED = 0, 1, 2, 
 LSC_LAYER_ATTENTION, LSC_LAYER_GDN = 0, 1
 LSC_RECURRENT_AUTO, LSC_RECURRENT_TOKEN, LSC_RECURRENT_CHUNKED = 0, 1, 2
 LSC_DECODE_EARLY_STATE = 1
-LSC_F32, LSC_BF16, LSC_F16 = 0, 1, 2
+LSC_F32, LSC_BF16, LSC_F16, LSC_E4M3 = 0, 1, 2, 3
 
 
 class LscError(RuntimeError):
@@ -128,7 +128,29 @@ class lsc_kv_layer_view(C.Structure):
     _fields_ = [("region", C.c_void_p), ("region_bytes", C.c_int64), ("k", C.c_void_p), ("v", C.c_void_p),
                 ("shape", C.c_int64 * 4), ("strides", C.c_int64 * 4), ("lane_stride", C.c_int64),
                 ("page_bytes", C.c_int64), ("payload_bytes", C.c_int64), ("row_bytes", C.c_int64),
-                ("dtype", C.c_int32), ("reserved", C.c_int32)]
+                ("dtype", C.c_int32), ("scale_offset", C.c_int32)]
+
+
+class lsc_kv_batch(C.Structure):
+    _fields_ = [("n_seq", C.c_int32), ("total_tokens", C.c_int32), ("max_blocks", C.c_int32), ("reserved", C.c_int32),
+                ("block_table", C.c_void_p), ("cu_seqlens", C.c_void_p), ("kv_lens", C.c_void_p)]
+
+
+class lsc_kv_append_args(C.Structure):
+    _fields_ = [("batch", lsc_kv_batch), ("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int32),
+                ("reserved", C.c_int32), ("k_stride", C.c_int64), ("v_stride", C.c_int64)]
+
+
+class lsc_kv_gather_args(C.Structure):
+    _fields_ = [("batch", lsc_kv_batch), ("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int32),
+                ("reserved", C.c_int32), ("k_stride", C.c_int64), ("v_stride", C.c_int64)]
+
+
+class lsc_kv_attend_args(C.Structure):
+    _fields_ = [("batch", lsc_kv_batch), ("num_q_heads", C.c_int32), ("dtype", C.c_int32), ("q", C.c_void_p),
+                ("out", C.c_void_p), ("lse", C.c_void_p), ("scale", C.c_float), ("causal", C.c_int32),
+                ("q_stride", C.c_int64), ("out_stride", C.c_int64), ("max_seq_tokens", C.c_int32),
+                ("max_kv_tokens", C.c_int32), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
 
 
 # numpy view of an array of lsc_kv_copy_op
@@ -168,6 +190,11 @@ def load():
         "lsc_kv_pool_create": ([C.POINTER(lsc_kv_pool_desc), P, C.c_size_t, C.POINTER(P)], C.c_int),
         "lsc_kv_pool_destroy": ([P], C.c_int),
         "lsc_kv_pool_layer_view": ([P, I32, C.POINTER(lsc_kv_layer_view)], C.c_int),
+        "lsc_kv_pool_status": ([P, P, C.POINTER(I32)], C.c_int),
+        "lsc_kv_append": ([P, I32, C.POINTER(lsc_kv_append_args), P], C.c_int),
+        "lsc_kv_gather": ([P, I32, C.POINTER(lsc_kv_gather_args), P], C.c_int),
+        "lsc_kv_attend": ([P, I32, C.POINTER(lsc_kv_attend_args), P], C.c_int),
+        "lsc_kv_attend_workspace_bytes": ([P, C.POINTER(lsc_kv_attend_args), C.POINTER(C.c_size_t)], C.c_int),
         "lsc_copy_prefix": ([P, P, I32, P, P, C.POINTER(I64)], C.c_int),
         "lsc_pc_create": ([I32, I32, C.POINTER(P)], C.c_int),
         "lsc_pc_destroy": ([P], C.c_int),
@@ -490,6 +517,52 @@ def lsc_copy_prefix(pool, ops, stream=None, done_event=None):
     b = C.c_int64(0)
     rc = load().lsc_copy_prefix(pool, ops.ctypes.data, len(ops), _stream(stream), _event(done_event), C.byref(b))
     return rc, b.value
+
+
+def lsc_kv_pool_status(pool, stream=None):
+    s = C.c_int32(0)
+    rc = load().lsc_kv_pool_status(pool, _stream(stream), C.byref(s))
+    if rc < 0:
+        raise LscError(rc, "lsc_kv_pool_status")
+    return s.value
+
+
+def kv_batch(n_seq, total_tokens, block_table, cu_seqlens, kv_lens, max_blocks):
+    """The sequences of a step; all three arrays are int32 on the device."""
+    return lsc_kv_batch(n_seq, total_tokens, max_blocks, 0, ptr(block_table), ptr(cu_seqlens), ptr(kv_lens))
+
+
+def kv_append_args(batch, k, v, dtype, k_stride=0, v_stride=0):
+    return lsc_kv_append_args(batch, ptr(k), ptr(v), dtype, 0, k_stride, v_stride)
+
+
+def lsc_kv_append(pool, layer, args, stream=None):
+    return load().lsc_kv_append(pool, layer, C.byref(args), _stream(stream))
+
+
+def kv_gather_args(batch, k, v, dtype, k_stride=0, v_stride=0):
+    return lsc_kv_gather_args(batch, ptr(k), ptr(v), dtype, 0, k_stride, v_stride)
+
+
+def lsc_kv_gather(pool, layer, args, stream=None):
+    return load().lsc_kv_gather(pool, layer, C.byref(args), _stream(stream))
+
+
+def kv_attend_args(batch, num_q_heads, q, out, dtype, scale, lse=None, causal=True, q_stride=0, out_stride=0,
+                   max_seq_tokens=0, max_kv_tokens=0, workspace=None, workspace_bytes=0):
+    return lsc_kv_attend_args(batch, num_q_heads, dtype, ptr(q), ptr(out), ptr(lse), scale, int(causal), q_stride,
+                              out_stride, max_seq_tokens, max_kv_tokens, ptr(workspace), workspace_bytes)
+
+
+def lsc_kv_attend_workspace_bytes(pool, args):
+    """Returns (rc, bytes)."""
+    n = C.c_size_t(0)
+    rc = load().lsc_kv_attend_workspace_bytes(pool, C.byref(args), C.byref(n))
+    return rc, n.value
+
+
+def lsc_kv_attend(pool, layer, args, stream=None):
+    return load().lsc_kv_attend(pool, layer, C.byref(args), _stream(stream))
 
 
 # ---- snapshot store (include/lsc_store.h) -------------------------------------
