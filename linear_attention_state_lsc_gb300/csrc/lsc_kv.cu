@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "lsc_internal.h"
+#include "lsc_kv_attend.cuh"
 #include "lsc_kv.h"
 
 struct lsc_kv_pool {
@@ -163,6 +164,28 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
   r->num_sms = p->num_sms;
   r->wait_limit_ns = kWaitLimitNs;
   return LSC_OK;
+}
+
+// Which launches a call takes, by sizes, types and alignment: `rows` for up to
+// kRowsMost packed rows a sequence, the CUDA cores for the rest.
+constexpr int32_t kRowsMost = 64;
+struct AttendForm {
+  bool tensor;  // false: the CUDA-core kernel alone
+  lsc::AttendPlan rows;
+  size_t ws_bytes;
+};
+
+AttendForm attend_form(const lsc::KvAttendParams &r) {
+  AttendForm f{};
+  const int D = r.L.head_dim;
+  const uintptr_t mis = (uintptr_t)r.q | (uintptr_t)r.out | (uintptr_t)(r.q_stride * 2) | (uintptr_t)(r.out_stride * 2);
+  const bool types = r.dtype != LSC_F32 && (r.L.dtype == r.dtype || r.L.dtype == LSC_E4M3);
+  const int64_t most = (int64_t)r.max_seq * r.group;
+  f.tensor = types && (D == 64 || D == 128 || D == 256) && (mis & 15) == 0 && most <= kRowsMost;
+  if (!f.tensor) return f;
+  f.rows = lsc::plan_kv_attend_rows(r, (int32_t)most);
+  f.ws_bytes = f.rows.ws_bytes;
+  return f;
 }
 
 }  // namespace
@@ -393,7 +416,7 @@ int lsc_kv_attend_workspace_bytes(const lsc_kv_pool *p, const lsc_kv_attend_args
   lsc::KvAttendParams r{};
   const int rc = check_attend(p, 0, a, &r);
   if (rc != LSC_OK) return rc;
-  *bytes = 0;
+  *bytes = r.b.n_seq == 0 || r.b.total_tokens == 0 ? 0 : attend_form(r).ws_bytes;
   return LSC_OK;
 }
 
@@ -405,7 +428,28 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
   rc = check_device(p);
   if (rc != LSC_OK) return rc;
   if (r.b.n_seq == 0 || r.b.total_tokens == 0) return LSC_OK;
-  if (lsc::launch_kv_attend_any(r, (cudaStream_t)stream) != cudaSuccess) {
+  const AttendForm f = attend_form(r);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (!f.tensor) {
+    if (lsc::launch_kv_attend_any(r, s) != cudaSuccess) {
+      cudaGetLastError();
+      return LSC_ERR_CUDA;
+    }
+    return LSC_OK;
+  }
+  void *ws = a->workspace;
+  if (f.ws_bytes > 0) {
+    if (ws && a->workspace_bytes < f.ws_bytes) return LSC_ERR_INVALID_ARG;
+    if (!ws && cudaMallocAsync(&ws, f.ws_bytes, s) != cudaSuccess) {
+      cudaGetLastError();
+      return LSC_ERR_NO_MEMORY;
+    }
+    r.ws = (uint8_t *)ws;
+  }
+  cudaError_t e = lsc::launch_kv_attend_rows(r, f.rows, s);
+  if (e == cudaSuccess && f.rows.may_cut) e = lsc::launch_kv_attend_join(r, f.rows, s);
+  if (f.ws_bytes > 0 && !a->workspace && cudaFreeAsync(ws, s) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
+  if (e != cudaSuccess) {
     cudaGetLastError();
     return LSC_ERR_CUDA;
   }

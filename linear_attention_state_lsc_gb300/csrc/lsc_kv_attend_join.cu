@@ -1,0 +1,105 @@
+// lsc_kv_attend_join.cu -- joins the parts of cut units (lsc_kv_attend.cuh).
+//
+// For each run whose last unit goes on in other runs, a warp takes a row: its
+// parts i have maximum m_i, sum l_i and unnormalised row o_i, and
+//   m = max m_i,  l = sum 2^(m_i - m) l_i,  out = sum 2^(m_i - m) o_i / l,
+// in the order of the tiles, so the result does not depend on timing.  It reads
+// what the parts wrote (at most 2 M rows of D floats per run) once: a few us
+// even for 152 runs of 256 rows.
+#include <cuda_runtime.h>
+
+#include "lsc_internal.h"
+#include "lsc_kv_attend.cuh"
+#include "lsc_kv_attend_rows.cuh"
+#include "lsc_ptx.h"
+
+namespace lsc {
+namespace {
+
+using namespace kv;
+
+constexpr int kWarps = 8;
+
+// NV = float4 vectors of a row per lane, head_dim = 128 * NV (64: half the lanes)
+template <int NV>
+__global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant__ KvAttendParams p, int ctas, int M) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const Workspace w = workspace_at(p.ws, ctas, M);
+  const int c = blockIdx.x, D = p.L.head_dim, ln = threadIdx.x & 31;
+  const Cut cut = w.cut[c];
+  if (cut.more == 0) return;
+  const int32_t c0 = p.b.cu[cut.seq], n = p.b.cu[cut.seq + 1] - c0;
+  const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  const int64_t R = (int64_t)cut.block * M + r;
+  if (r >= M || R >= (int64_t)n * p.group) return;
+  auto part = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+  float m = -INFINITY;
+  for (int i = ln; i <= cut.more; i += 32) m = fmaxf(m, w.ml[(int64_t)part(i) * M + r].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 acc[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i <= cut.more; ++i) {
+    const int64_t at = (int64_t)part(i) * M + r;
+    const float2 ml = w.ml[at];
+    const float k = exp2f(ml.x - ref);
+    l += ml.y * k;
+    const float4 *src = (const float4 *)(w.o + at * D);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if ((ln + 32 * v) * 4 >= D) continue;
+      const float4 x = src[ln + 32 * v];
+      acc[v].x += k * x.x, acc[v].y += k * x.y, acc[v].z += k * x.z, acc[v].w += k * x.w;
+    }
+  }
+  const bool empty = l == 0.f;
+  const float inv = empty ? 0.f : 1.f / l;
+  const int64_t t = c0 + R / p.group, h = (int64_t)cut.head * p.group + R % p.group;
+  uint2 *dst = (uint2 *)((uint16_t *)p.out + t * p.out_stride + h * D);
+  const int bf16 = p.dtype == LSC_BF16;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    if ((ln + 32 * v) * 4 < D)
+      dst[ln + 32 * v] = make_uint2(pack2(acc[v].x * inv, acc[v].y * inv, bf16), pack2(acc[v].z * inv, acc[v].w * inv, bf16));
+  if (p.lse && ln == 0) p.lse[t * p.heads + h] = empty ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attend_join(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+  const dim3 grid(plan.ctas, (plan.M + kWarps - 1) / kWarps);
+  const cudaError_t e = p.L.head_dim <= 128
+                            ? launch_pdl(join_kernel<1>, grid, kWarps * 32, 0, stream, p, plan.ctas, plan.M)
+                            : launch_pdl(join_kernel<2>, grid, kWarps * 32, 0, stream, p, plan.ctas, plan.M);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+AttendPlan plan_kv_attend_rows(const KvAttendParams &p, int32_t row_hi) {
+  using namespace kv::rows;
+  const int D = p.L.head_dim, q8 = p.L.dtype == LSC_E4M3;
+  AttendPlan plan{};
+  plan.M = row_hi <= 16 ? 16 : 64;
+  plan.share = {1, row_hi};
+  const int occ = q8 ? (D == 64 ? occ_of<1, 64>(plan.M) : D == 128 ? occ_of<1, 128>(plan.M) : occ_of<1, 256>(plan.M))
+                     : (D == 64 ? occ_of<2, 64>(plan.M) : D == 128 ? occ_of<2, 128>(plan.M) : occ_of<2, 256>(plan.M));
+  const int64_t tiles = ((int64_t)p.max_kv + kTK - 1) / kTK;
+  const int64_t most = (int64_t)p.b.n_seq * p.L.heads * (tiles < 1 ? 1 : tiles);  // tiles there can be
+  plan.ctas = (int)(most < (int64_t)p.num_sms * occ ? most : (int64_t)p.num_sms * occ);
+  plan.may_cut = tiles > 1;
+  plan.ws_bytes = plan.may_cut ? kv::workspace_size(plan.ctas, plan.M, D) : 0;
+  return plan;
+}
+
+cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+  const cudaError_t e = p.L.dtype == LSC_E4M3   ? launch_kv_attend_rows_e4m3(p, plan, stream)
+                        : p.L.dtype == LSC_BF16 ? launch_kv_attend_rows_bf16(p, plan, stream)
+                                                : launch_kv_attend_rows_f16(p, plan, stream);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace lsc

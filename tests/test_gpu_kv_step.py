@@ -256,3 +256,250 @@ def test_attend(lsc, mix, name, shape):
             check_attend(host, 1, b, qx, dtype, scale, causal, again, None)
         assert dev.status() == L.LSC_OK
         np.testing.assert_array_equal(dev.download(), host.bytes)
+
+
+@pytest.mark.parametrize("mix", MIXES, ids=lambda m: NAME[m[0]] + "-" + NAME[m[1]])
+@pytest.mark.parametrize("shape", [(16, 2, 4, 64), (64, 1, 8, 128), (64, 1, 3, 256)], ids=str)
+@pytest.mark.parametrize("n", [3, 90])
+def test_what_a_row_does_not_see_does_not_enter(lsc, mix, shape, n):
+    """K and V of some new tokens are NaN and infinite: earlier rows of the causal chunk are as if they were not there,
+    the rows that see them get what the sum gives (an infinity, or NaN)."""
+    pool, dtype = mix
+    bt, H, G, D = shape
+    rng = np.random.default_rng(n + D)
+    kv = 150
+    b = Batch(rng, [n, 1], [kv, 20], bt, 30)
+    host = filled(rng, b, 30, bt, H, D, pool)
+    bl, r = b.places(0, 0, kv)
+    x = host.read(1, 1, bl, r)
+    first = kv - n + 1 + (n - 2) // 2  # the first position whose v is not finite: the row before it does not see it
+    x[first, :, 3] = np.inf
+    x[first, :, 7] = -np.inf
+    x[-1, :, 3] = -np.inf
+    x[-1, :, 11] = np.nan
+    host.write(1, 1, bl, r, x)
+    k = host.read(1, 0, bl, r)
+    k[-1] = np.nan  # the last token's scores: seen by the last row alone
+    host.write(1, 0, bl, r, k)
+    q, qx = dense(rng.standard_normal((b.T, H * G, D)), dtype)
+    scale = D ** -0.5
+    sees = first - (kv - n)  # new tokens below this one see finite values alone
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, dtype, H * G, scale, True, max_seq_tokens=n)
+    clean = np.r_[0:sees, n]
+    k[-1] = 0  # scores that no clean row sees
+    host.write(1, 0, bl, r, np.nan_to_num(k))
+    host.write(1, 1, bl, r, np.nan_to_num(x, nan=0, posinf=0, neginf=0))
+    check_attend(host, 1, b, qx, dtype, scale, True, out, ls, rows=clean)
+    got = out.float().cpu().numpy().reshape(b.T, H * G, D)
+    if pool == L.LSC_E4M3:  # a row that held one is NaN throughout
+        assert np.isnan(got[sees:n]).all()
+    else:
+        assert np.isnan(got[n - 1]).all()
+        assert (got[sees:n - 1, :, 3] == np.inf).all() and (got[sees:n - 1, :, 7] == -np.inf).all()
+        assert np.isfinite(np.delete(got[sees:n - 1], [3, 7], -1)).all()
+
+
+def test_attend_strides_and_slices(lsc):
+    """q and out as slices of wider arrays, aligned (tensor cores) and not (CUDA cores)."""
+    rng = np.random.default_rng(5)
+    H, G, D, bt = 2, 4, 128, 16
+    b = Batch(rng, [2, 60], [100, 200], bt, 30, spare=1)
+    host = filled(rng, b, 30, bt, H, D, L.LSC_BF16)
+    x = rng.standard_normal((b.T, H * G, D))
+    with DevKv(host) as dev:
+        for stride in (H * G * D + 256, H * G * D + 8, H * G * D + 1):
+            q, qx = dense(x, L.LSC_BF16, stride)
+            out, ls = run_attend(dev, 1, b, q, L.LSC_BF16, H * G, D ** -0.5, True, stride=stride)
+            check_attend(host, 1, b, qx, L.LSC_BF16, D ** -0.5, True, out, ls)
+
+
+def test_bad_batches_are_recorded_and_stay_inside(lsc):
+    """Block ids, lengths and cu_seqlens that do not fit: the status word says so, the other sequences are right, and
+    nothing outside the named rows changes."""
+    rng = np.random.default_rng(6)
+    H, G, D, bt, blocks = 2, 2, 64, 16, 30
+    b = Batch(rng, [1, 3, 2, 1], [40, 50, 60, 33], bt, blocks, wide=1)
+    host = filled(rng, b, blocks, bt, H, D, L.LSC_BF16)
+    q, qx = dense(rng.standard_normal((b.T, H * G, D)), L.LSC_BF16)
+    k, _ = dense(rng.standard_normal((b.T, H, D)), L.LSC_BF16)
+    good = np.r_[0:1, 4:7]  # sequence 1 is the one that breaks
+
+    def calls(dev, batch):
+        out = torch.full((b.T, H * G * D), 7.0, dtype=torch.bfloat16, device="cuda")
+        ls = torch.full((b.T, H * G), 7.0, device="cuda")
+        g = [torch.full((b.T, H * D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        codes = []
+        for call, args in ((L.lsc_kv_attend, L.kv_attend_args(batch, H * G, q, out, L.LSC_BF16, 0.125, lse=ls)),
+                           (L.lsc_kv_gather, L.kv_gather_args(batch, *g, L.LSC_BF16)),
+                           (L.lsc_kv_append, L.kv_append_args(batch, k, k, L.LSC_BF16))):
+            assert call(dev.pool, 1, args, cur()) == L.LSC_OK
+            codes.append(dev.status())
+        return codes, out, ls, g
+
+    for bad in (blocks, -1, 2 ** 31 - 1):
+        b.device()
+        with DevKv(host) as dev:
+            table = b.table.copy()
+            table[1, 50 // bt] = bad  # holds position 49, and 48: the last two of sequence 1's three
+            t = torch.from_numpy(table).cuda()
+            batch = L.kv_batch(4, b.T, t, b.dev[1], b.dev[2], max_blocks=table.shape[1])
+            codes, out, ls, g = calls(dev, batch)
+            assert codes == [L.LSC_ERR_OUT_OF_RANGE] * 3
+            check_attend(host, 1, b, qx, L.LSC_BF16, 0.125, True, out, ls, rows=good)
+            assert (g[0][2:4] == 0).all() and (g[0][1] != 0).any()
+            assert dev.status() == L.LSC_OK  # cleared
+    for kv1 in (-1, 1 << 20, 2 ** 31 - 1):
+        with DevKv(host) as dev:
+            kv = b.kv.astype(np.int32).copy()
+            kv[1] = kv1
+            t = torch.from_numpy(kv).cuda()
+            batch = L.kv_batch(4, b.T, b.dev[0], b.dev[1], t, max_blocks=b.table.shape[1])
+            codes, out, ls, g = calls(dev, batch)
+            assert codes == [L.LSC_ERR_INVALID_ARG] * 3
+            check_attend(host, 1, b, qx, L.LSC_BF16, 0.125, True, out, ls, rows=good)
+            assert (out[1:4] == 0).all() and torch.isinf(ls[1:4]).all() and (g[0][1:4] == 0).all()
+    for cu in ([0, 5, 4, 6, 7], [0, 1, 4, 6, 9], [3, 4, 5, 6, 7], [0, -4, 4, 6, 7], [-2 ** 31, 1, 4, 6, 2 ** 31 - 1]):
+        with DevKv(host) as dev:
+            t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+            batch = L.kv_batch(4, b.T, b.dev[0], t, b.dev[2], max_blocks=b.table.shape[1])
+            codes, out, ls, g = calls(dev, batch)
+            assert codes == [L.LSC_ERR_INVALID_ARG] * 3
+
+
+def test_bounds_that_do_not_hold_are_recorded(lsc):
+    rng = np.random.default_rng(7)
+    b = Batch(rng, [1, 1], [40, 400], 16, 40)
+    host = filled(rng, b, 40, 16, 2, 64, L.LSC_BF16)
+    q, qx = dense(rng.standard_normal((b.T, 4, 64)), L.LSC_BF16)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, L.LSC_BF16, 4, 0.125, True, max_seq_tokens=1, max_kv_tokens=100)
+        assert dev.status() == L.LSC_ERR_INVALID_ARG
+        check_attend(host, 1, b, qx, L.LSC_BF16, 0.125, True, out, ls, rows=np.r_[0:1])
+        assert (out[1] == 0).all() and torch.isinf(ls[1]).all()
+
+
+@pytest.mark.parametrize("pool", [L.LSC_BF16, L.LSC_E4M3], ids=NAME.get)
+def test_a_step_on_its_own_stream_in_a_graph(lsc, pool):
+    """append, attend and gather of each layer, captured once on a side stream and replayed with other lengths, tables
+    and values: two graphs with workspaces of their own, replayed in turn; two calls give the same bits."""
+    rng = np.random.default_rng(8)
+    H, G, D, bt, blocks, S = 2, 8, 256, 64, 200, 5
+    mixes = [([1, 1, 2, 1, 1], [1, 700, 64, 1300, 65]), ([1, 2, 1, 1, 1], [2000, 3, 128, 100, 1])]
+    batches = [Batch(rng, n, kv, bt, blocks) for n, kv in mixes]
+    wide = max(b.table.shape[1] for b in batches)
+    table = torch.zeros(S, wide, dtype=torch.int32, device="cuda")
+    cu, kvl = torch.zeros(S + 1, dtype=torch.int32, device="cuda"), torch.zeros(S, dtype=torch.int32, device="cuda")
+    T = max(b.T for b in batches)
+    q, k, v = (torch.zeros(T, h * D, dtype=torch.bfloat16, device="cuda") for h in (H * G, H, H))
+    host = HostKv(blocks, bt, H, D, pool, layers=2, fill=0)
+    side = torch.cuda.Stream()
+    with DevKv(host) as dev:
+        runs = []
+        for _ in range(2):
+            out = [torch.zeros(T, H * G * D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            gk = [torch.zeros(T, H * D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            batch = L.kv_batch(S, T, table, cu, kvl, max_blocks=wide)
+            a = L.kv_attend_args(batch, H * G, q, out[0], L.LSC_BF16, D ** -0.5, max_seq_tokens=2, max_kv_tokens=2000)
+            rc, need = L.lsc_kv_attend_workspace_bytes(dev.pool, a)
+            ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+            def step(stream):
+                for l in range(2):
+                    ar = L.kv_attend_args(batch, H * G, q, out[l], L.LSC_BF16, D ** -0.5, max_seq_tokens=2,
+                                          max_kv_tokens=2000, workspace=ws, workspace_bytes=need)
+                    assert L.lsc_kv_append(dev.pool, l, L.kv_append_args(batch, k, v, L.LSC_BF16), stream) == L.LSC_OK
+                    assert L.lsc_kv_attend(dev.pool, l, ar, stream) == L.LSC_OK
+                    assert L.lsc_kv_gather(dev.pool, l, L.kv_gather_args(batch, gk[l], gk[l], L.LSC_BF16), stream) == L.LSC_OK
+
+            side.wait_stream(cur())
+            with torch.cuda.stream(side):
+                step(side)  # kernels loaded before the capture
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                step(torch.cuda.current_stream())
+            runs.append((graph, out, gk, ws))
+        for b in batches:
+            x = rng.standard_normal((2, blocks, bt, H, D)) * 2
+            for l in range(2):
+                for lane in (0, 1):
+                    for i in range(S):
+                        bl, r = b.places(i, 0, int(b.kv[i]))
+                        host.write(l, lane, bl, r, x[lane][bl, r] * (l + 1))
+            dev.buf.copy_(torch.from_numpy(host.bytes.reshape(-1)))
+            t = np.zeros((S, wide), np.int32)
+            t[:, :b.table.shape[1]] = b.table
+            table.copy_(torch.from_numpy(t))
+            cu.copy_(torch.from_numpy(b.cu))
+            kvl.copy_(torch.from_numpy(b.kv.astype(np.int32)))
+            (kd, kx), (vd, vx), (qd, qx) = (dense(rng.standard_normal((b.T, h, D)), L.LSC_BF16) for h in (H, H, H * G))
+            for a, s in ((k, kd), (v, vd), (q, qd)):
+                a[:b.T].copy_(s)
+            for graph, out, gk, ws in runs:
+                ws.fill_(255)
+                graph.replay()
+            torch.cuda.synchronize()
+            assert dev.status() == L.LSC_OK
+            for i in range(S):
+                bl, r = b.places(i, int(b.kv[i] - b.n[i]), int(b.kv[i]))
+                for l in range(2):
+                    host.write(l, 0, bl, r, kx[b.cu[i]:b.cu[i + 1]])
+                    host.write(l, 1, bl, r, vx[b.cu[i]:b.cu[i + 1]])
+            np.testing.assert_array_equal(dev.download(), host.bytes)
+            for l in range(2):
+                assert torch.equal(runs[0][1][l], runs[1][1][l])
+                check_attend(host, l, b, qx, L.LSC_BF16, D ** -0.5, True, runs[0][1][l][:b.T], None)
+
+
+def test_workspace_rules(lsc):
+    """Too small a workspace is refused; without one the library finds its own; both give the same bits."""
+    rng = np.random.default_rng(9)
+    b = Batch(rng, [1, 1], [300, 900], 64, 30)
+    host = filled(rng, b, 30, 64, 2, 128, L.LSC_BF16)
+    q, qx = dense(rng.standard_normal((b.T, 8, 128)), L.LSC_BF16)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, L.LSC_BF16, 8, 0.1, True)
+        own = torch.zeros_like(out)
+        args = L.kv_attend_args(b.device(), 8, q, own, L.LSC_BF16, 0.1)
+        rc, need = L.lsc_kv_attend_workspace_bytes(dev.pool, args)
+        assert rc == L.LSC_OK and need > 0
+        assert L.lsc_kv_attend(dev.pool, 1, args, cur()) == L.LSC_OK
+        torch.cuda.synchronize()
+        assert torch.equal(own, out)
+        ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+        args.workspace, args.workspace_bytes = ws.data_ptr(), need - 1
+        assert L.lsc_kv_attend(dev.pool, 1, args, cur()) == L.LSC_ERR_INVALID_ARG
+
+
+def test_many_sequences_and_a_block_far_into_the_pool(lsc):
+    """More sequences than a CTA has threads, empty ones among them; and pages whose byte offset passes 32 bits."""
+    rng = np.random.default_rng(10)
+    S = 700
+    kv = rng.integers(0, 40, S)
+    b = Batch(rng, np.minimum(1, kv), kv, 16, int((-(-kv // 16)).sum()))
+    host = filled(rng, b, int((-(-kv // 16)).sum()), 16, 1, 64, L.LSC_BF16)
+    q, qx = dense(rng.standard_normal((b.T, 2, 64)), L.LSC_BF16)
+    with DevKv(host) as dev:
+        for seen in (True, False):
+            out, ls = run_attend(dev, 1, b, q, L.LSC_BF16, 2, 0.125, seen, max_seq_tokens=1)
+            check_attend(host, 1, b, qx, L.LSC_BF16, 0.125, seen, out, ls)
+    far = HostKv(6, 16, 1, 64, L.LSC_BF16, pad=0, layers=1)
+    page = 1 << 30  # six pages of 1 GiB: lanes of 6 GiB
+    desc = L.lsc_kv_pool_desc(1, 6, 16, 1, 64, L.LSC_BF16, page)
+    buf = torch.empty(12 * page, dtype=torch.uint8, device="cuda")
+    rc, pool = L.lsc_kv_pool_create(desc, buf, buf.numel())
+    assert rc == L.LSC_OK
+    b = Batch(rng, [80], [80], 16, 6)
+    kx, vx = (dense(rng.standard_normal((80, 1, 64)), L.LSC_BF16) for _ in "kv")
+    bl, r = b.places(0, 0, 80)
+    far.write(0, 0, bl, r, kx[1])
+    far.write(0, 1, bl, r, vx[1])
+    q, qx = dense(rng.standard_normal((80, 2, 64)), L.LSC_BF16)
+    batch = b.device()
+    out, ls = torch.zeros(80, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(80, 2, device="cuda")
+    assert L.lsc_kv_append(pool, 0, L.kv_append_args(batch, kx[0], vx[0], L.LSC_BF16), cur()) == L.LSC_OK
+    assert L.lsc_kv_attend(pool, 0, L.kv_attend_args(batch, 2, q, out, L.LSC_BF16, 0.125, lse=ls), cur()) == L.LSC_OK
+    torch.cuda.synchronize()
+    check_attend(far, 0, b, qx, L.LSC_BF16, 0.125, True, out, ls)
+    assert L.lsc_kv_pool_destroy(pool) == L.LSC_OK
