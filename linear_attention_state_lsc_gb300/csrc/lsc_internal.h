@@ -280,8 +280,9 @@ struct KvAttendParams {
   int32_t causal;
   float scale_log2;     // scale * log2(e): the softmax runs in powers of two
   int32_t max_seq, max_kv;  // host bounds of the lengths
-  uint8_t *ws;
-  uint64_t wait_limit_ns;
+  uint8_t *ws;             // null: no unit can be cut
+  uint64_t wait_limit_ns;  // bound of each mbarrier wait (0: give up at once)
+  uint64_t drain_limit_ns; // bound of the wait for issued MMAs at the end
   int32_t num_sms;
 };
 // the CUDA-core kernel: every type, head size and alignment (head_dim <= 512)

@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <new>
 #include <vector>
@@ -45,6 +46,12 @@ int esize(int32_t dtype) {
 
 // Bound of every device-side wait (mbarrier), in nanoseconds.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
+
+// Host-side fault injection for the tests: LSC_FAULT=<name>.
+bool fault(const char *name) {
+  const char *f = getenv("LSC_FAULT");
+  return f && strcmp(f, name) == 0;
+}
 
 // [VA] §3: block stride = physical page size / element size, so the page must
 // hold the logical block and divide by the element size; 16-byte vector copies
@@ -162,16 +169,20 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
   const int64_t held = (int64_t)a->batch.max_blocks * p->d.block_tokens;
   r->max_kv = a->max_kv_tokens ? a->max_kv_tokens : (int32_t)std::min<int64_t>(held, INT32_MAX);
   r->num_sms = p->num_sms;
-  r->wait_limit_ns = kWaitLimitNs;
+  r->wait_limit_ns = fault("timeout0") ? 0 : kWaitLimitNs;
+  r->drain_limit_ns = kWaitLimitNs;
   return LSC_OK;
 }
 
-// Which launches a call takes, by sizes, types and alignment: `rows` for up to
-// kRowsMost packed rows a sequence, the CUDA cores for the rest.
+// Which launches a call takes, by sizes, types and alignment: the few-row kernel
+// for sequences of up to kRowsMost packed rows, the chunk kernel for the others,
+// each only where the host's bounds leave it something; the CUDA cores for what
+// neither takes.
 constexpr int32_t kRowsMost = 64;
 struct AttendForm {
-  bool tensor;  // false: the CUDA-core kernel alone
-  lsc::AttendPlan rows;
+  int launches;  // tensor-core launches in `plan`; 0: the CUDA-core kernel
+  bool chunk[2];
+  lsc::AttendPlan plan[2];
   size_t ws_bytes;
 };
 
@@ -179,12 +190,20 @@ AttendForm attend_form(const lsc::KvAttendParams &r) {
   AttendForm f{};
   const int D = r.L.head_dim;
   const uintptr_t mis = (uintptr_t)r.q | (uintptr_t)r.out | (uintptr_t)(r.q_stride * 2) | (uintptr_t)(r.out_stride * 2);
-  const bool types = r.dtype != LSC_F32 && (r.L.dtype == r.dtype || r.L.dtype == LSC_E4M3);
+  const bool q8 = r.L.dtype == LSC_E4M3;
+  const bool types = r.dtype != LSC_F32 && (r.L.dtype == r.dtype || q8);
+  if (!types || (D != 64 && D != 128 && D != 256) || (mis & 15) != 0) return f;
   const int64_t most = (int64_t)r.max_seq * r.group;
-  f.tensor = types && (D == 64 || D == 128 || D == 256) && (mis & 15) == 0 && most <= kRowsMost;
-  if (!f.tensor) return f;
-  f.rows = lsc::plan_kv_attend_rows(r, (int32_t)most);
-  f.ws_bytes = f.rows.ws_bytes;
+  const bool chunk = most > kRowsMost;
+  if (chunk && q8 && r.dtype != LSC_BF16) return f;  // e4m3 tiles become bf16 there
+  if (!chunk || r.b.n_seq > 1) f.plan[f.launches++] = lsc::plan_kv_attend_rows(r, chunk ? kRowsMost : (int32_t)most);
+  if (chunk) {
+    f.chunk[f.launches] = true;
+    f.plan[f.launches] = lsc::plan_kv_attend_chunk(r, f.launches ? kRowsMost + 1 : 1);
+    ++f.launches;
+  }
+  // one after the other on the stream, each with its join: they share the workspace
+  f.ws_bytes = std::max(f.plan[0].ws_bytes, f.plan[1].ws_bytes);
   return f;
 }
 
@@ -430,7 +449,7 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
   if (r.b.n_seq == 0 || r.b.total_tokens == 0) return LSC_OK;
   const AttendForm f = attend_form(r);
   cudaStream_t s = (cudaStream_t)stream;
-  if (!f.tensor) {
+  if (f.launches == 0) {
     if (lsc::launch_kv_attend_any(r, s) != cudaSuccess) {
       cudaGetLastError();
       return LSC_ERR_CUDA;
@@ -444,10 +463,13 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
       cudaGetLastError();
       return LSC_ERR_NO_MEMORY;
     }
-    r.ws = (uint8_t *)ws;
   }
-  cudaError_t e = lsc::launch_kv_attend_rows(r, f.rows, s);
-  if (e == cudaSuccess && f.rows.may_cut) e = lsc::launch_kv_attend_join(r, f.rows, s);
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < f.launches && e == cudaSuccess; ++i) {
+    r.ws = f.plan[i].may_cut ? (uint8_t *)ws : nullptr;
+    e = f.chunk[i] ? lsc::launch_kv_attend_chunk(r, f.plan[i], s) : lsc::launch_kv_attend_rows(r, f.plan[i], s);
+    if (e == cudaSuccess && f.plan[i].may_cut) e = lsc::launch_kv_attend_join(r, f.plan[i], s);
+  }
   if (f.ws_bytes > 0 && !a->workspace && cudaFreeAsync(ws, s) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
   if (e != cudaSuccess) {
     cudaGetLastError();

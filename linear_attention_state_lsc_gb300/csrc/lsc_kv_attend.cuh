@@ -249,5 +249,7 @@ struct AttendPlan {
 cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_join(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 AttendPlan plan_kv_attend_rows(const KvAttendParams &p, int32_t row_hi);
+cudaError_t launch_kv_attend_chunk(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
+AttendPlan plan_kv_attend_chunk(const KvAttendParams &p, int32_t row_lo);
 
 }  // namespace lsc

@@ -10,6 +10,7 @@
 
 #include "lsc_internal.h"
 #include "lsc_kv_attend.cuh"
+#include "lsc_kv_attend_chunk.cuh"
 #include "lsc_kv_attend_rows.cuh"
 #include "lsc_ptx.h"
 
@@ -99,6 +100,28 @@ cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &pla
   const cudaError_t e = p.L.dtype == LSC_E4M3   ? launch_kv_attend_rows_e4m3(p, plan, stream)
                         : p.L.dtype == LSC_BF16 ? launch_kv_attend_rows_bf16(p, plan, stream)
                                                 : launch_kv_attend_rows_f16(p, plan, stream);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+AttendPlan plan_kv_attend_chunk(const KvAttendParams &p, int32_t row_lo) {
+  using namespace kv::chunk;
+  const int D = p.L.head_dim, TK = D == 256 ? Conf<256>::TK : Conf<128>::TK;
+  AttendPlan plan{};
+  plan.M = D == 256 ? Conf<256>::M : Conf<128>::M;
+  plan.share = {row_lo, INT32_MAX};
+  const int64_t tiles = ((int64_t)p.max_kv + TK - 1) / TK;
+  const int64_t blocks = ((int64_t)p.b.total_tokens * p.group + plan.M - 1) / plan.M + p.b.n_seq;
+  const int64_t most = blocks * p.L.heads * (tiles < 1 ? 1 : tiles);
+  plan.ctas = (int)(most < p.num_sms ? most : p.num_sms);
+  plan.may_cut = tiles > 1;
+  plan.ws_bytes = plan.may_cut ? kv::workspace_size(plan.ctas, plan.M, D) : 0;
+  return plan;
+}
+
+cudaError_t launch_kv_attend_chunk(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+  const cudaError_t e = p.L.dtype == LSC_E4M3   ? launch_kv_attend_chunk_e4m3(p, plan, stream)
+                        : p.L.dtype == LSC_BF16 ? launch_kv_attend_chunk_bf16(p, plan, stream)
+                                                : launch_kv_attend_chunk_f16(p, plan, stream);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

@@ -15,6 +15,10 @@ scale.  The sums of N terms in 32 bits add N 2^-23.  All of that times the sum o
 weight times |v| (`mass`), and the output is rounded once, half a step of the
 result.  exp2 and log2 are good to 2^-21.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -232,6 +236,7 @@ LENGTHS = {
     "chunk": ([40, 1, 0, 129], [40, 300, 17, 200]),
     "ahead": ([20, 70], [12, 66]),                                     # rows that see nothing
     "long": ([3, 1], [1500, 2049]),
+    "whole": ([300, 2, 77], [300, 500, 770]),                          # a first prompt, a decode, a resumed prompt
 }
 
 
@@ -450,6 +455,32 @@ def test_a_step_on_its_own_stream_in_a_graph(lsc, pool):
             for l in range(2):
                 assert torch.equal(runs[0][1][l], runs[1][1][l])
                 check_attend(host, l, b, qx, L.LSC_BF16, D ** -0.5, True, runs[0][1][l][:b.T], None)
+
+
+def test_waits_that_run_out_are_reported(tmp_path):
+    """With the injected fault every bounded wait gives up at once: the chunk kernel returns, the status word says so,
+    and the next call in a clean process is right."""
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import numpy as np, torch
+import test_gpu_kv_step as T
+from _kv import Batch, DevKv
+from linear_attention_state_lsc_gb300 import lsc as L
+rng = np.random.default_rng(3)
+for D in (64, 128, 256):
+    b = Batch(rng, [70], [300], 64, 10)
+    host = T.filled(rng, b, 10, 64, 1, D, L.LSC_BF16)
+    q, _ = T.dense(rng.standard_normal((70, 4, D)), L.LSC_BF16)
+    with DevKv(host) as dev:
+        T.run_attend(dev, 1, b, q, L.LSC_BF16, 4, 0.1, True)
+        assert dev.status() == L.LSC_ERR_DEV_TIMEOUT
+print("reported")
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", code % (os.path.dirname(here), here)], capture_output=True, text=True,
+                       env=dict(os.environ, LSC_FAULT="timeout0"), timeout=300)
+    assert "reported" in r.stdout, r.stderr[-2000:]
 
 
 def test_workspace_rules(lsc):
