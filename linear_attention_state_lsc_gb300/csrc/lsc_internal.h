@@ -1,6 +1,7 @@
 // lsc_internal.h -- shared between the host code and the kernels of liblsc.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 #include <stdint.h>
@@ -280,6 +281,8 @@ struct KvAttendParams {
   int32_t causal;
   float scale_log2;     // scale * log2(e): the softmax runs in powers of two
   int32_t max_seq, max_kv;  // host bounds of the lengths
+  const CUtensorMap *map;  // host: the layer's rows as TMA boxes, or null
+  int32_t box_rows;        // rows of a box; 0 without a map
   uint8_t *ws;             // null: no unit can be cut
   uint64_t wait_limit_ns;  // bound of each mbarrier wait (0: give up at once)
   uint64_t drain_limit_ns; // bound of the wait for issued MMAs at the end

@@ -30,6 +30,8 @@ struct lsc_kv_pool {
   int32_t scale_off = 0;        // E4M3: page offset of the scale bytes
   int32_t *status = nullptr;    // device error word
   int32_t *h_status = nullptr;  // pinned
+  int32_t box_rows = 0;         // rows of a TMA box of `maps`
+  std::vector<CUtensorMap> maps;  // per layer; empty: none
 };
 
 namespace {
@@ -77,6 +79,50 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
   g->lane_bytes = (int64_t)d->num_blocks * d->page_bytes;
   g->region_bytes = 2 * g->lane_bytes;
   return LSC_OK;
+}
+
+// TMA maps of the layers' rows, for the chunk attention: 16-bit elements, 128-byte
+// swizzle, coordinates (element of a column, row of a block, column of 64
+// elements, kv head, block; V's blocks follow K's).  A box never leaves its
+// block: box_rows is the largest power of two that divides block_tokens, up to a
+// tile of positions, and a box of a whole tile takes all columns.  Without maps
+// (odd blocks, other types and sizes) that kernel copies rows itself.
+void make_maps(lsc_kv_pool *p) {
+  const lsc_kv_pool_desc &d = p->d;
+  const int D = d.head_dim;
+  if ((d.dtype != LSC_BF16 && d.dtype != LSC_F16) || (D != 64 && D != 128 && D != 256)) return;
+  int box = d.block_tokens & -d.block_tokens;
+  if (box > (D == 256 ? 64 : 128)) box = D == 256 ? 64 : 128;
+  if (box < 8) return;  // a swizzle pattern is 8 rows
+  void *fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess || !fn) {
+    cudaGetLastError();
+    return;
+  }
+  const auto encode = (CUresult(*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill))fn;
+  std::vector<CUtensorMap> maps;
+  try {
+    maps.resize(d.num_layers);
+  } catch (...) {
+    return;
+  }
+  const bool tile = box == (D == 256 ? 64 : 128);
+  const cuuint64_t dims[5] = {64, (cuuint64_t)d.block_tokens, (cuuint64_t)(D / 64), (cuuint64_t)d.num_kv_heads,
+                              2 * (cuuint64_t)d.num_blocks};
+  const cuuint64_t strides[4] = {(cuuint64_t)p->row_bytes, 128, (cuuint64_t)(D * p->es), (cuuint64_t)d.page_bytes};
+  const cuuint32_t boxes[5] = {64, (cuuint32_t)box, tile ? (cuuint32_t)(D / 64) : 1, 1, 1}, ones[5] = {1, 1, 1, 1, 1};
+  for (int32_t l = 0; l < d.num_layers; ++l)
+    if (encode(&maps[l], d.dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+               p->base + (int64_t)l * p->region_bytes, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return;
+  p->maps.swap(maps);
+  p->box_rows = box;
 }
 
 int check_device(const lsc_kv_pool *p) {
@@ -169,42 +215,33 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
   const int64_t held = (int64_t)a->batch.max_blocks * p->d.block_tokens;
   r->max_kv = a->max_kv_tokens ? a->max_kv_tokens : (int32_t)std::min<int64_t>(held, INT32_MAX);
   r->num_sms = p->num_sms;
+  r->map = p->maps.empty() ? nullptr : &p->maps[layer];
+  r->box_rows = p->box_rows;
   r->wait_limit_ns = fault("timeout0") ? 0 : kWaitLimitNs;
   r->drain_limit_ns = kWaitLimitNs;
   return LSC_OK;
 }
 
-// Which launches a call takes, by sizes, types and alignment: the few-row kernel
-// for sequences of up to kRowsMost packed rows, the chunk kernel for the others,
-// each only where the host's bounds leave it something; the CUDA cores for what
-// neither takes.
+// Which kernel a call takes, by sizes, types and alignment: the few-row kernel
+// when every sequence has kRowsMost packed rows at most, the chunk kernel when
+// one may have more, the CUDA cores for what neither takes.
 constexpr int32_t kRowsMost = 64;
-struct AttendForm {
-  int launches;  // tensor-core launches in `plan`; 0: the CUDA-core kernel
-  bool chunk[2];
-  lsc::AttendPlan plan[2];
-  size_t ws_bytes;
-};
+enum Form { kAny, kRows, kChunk };
 
-AttendForm attend_form(const lsc::KvAttendParams &r) {
-  AttendForm f{};
+Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
+  *plan = lsc::AttendPlan{};
   const int D = r.L.head_dim;
   const uintptr_t mis = (uintptr_t)r.q | (uintptr_t)r.out | (uintptr_t)(r.q_stride * 2) | (uintptr_t)(r.out_stride * 2);
   const bool q8 = r.L.dtype == LSC_E4M3;
   const bool types = r.dtype != LSC_F32 && (r.L.dtype == r.dtype || q8);
-  if (!types || (D != 64 && D != 128 && D != 256) || (mis & 15) != 0) return f;
-  const int64_t most = (int64_t)r.max_seq * r.group;
-  const bool chunk = most > kRowsMost;
-  if (chunk && q8 && r.dtype != LSC_BF16) return f;  // e4m3 tiles become bf16 there
-  if (!chunk || r.b.n_seq > 1) f.plan[f.launches++] = lsc::plan_kv_attend_rows(r, chunk ? kRowsMost : (int32_t)most);
-  if (chunk) {
-    f.chunk[f.launches] = true;
-    f.plan[f.launches] = lsc::plan_kv_attend_chunk(r, f.launches ? kRowsMost + 1 : 1);
-    ++f.launches;
+  if (!types || (D != 64 && D != 128 && D != 256) || (mis & 15) != 0) return kAny;
+  if ((int64_t)r.max_seq * r.group <= kRowsMost) {
+    *plan = lsc::plan_kv_attend_rows(r);
+    return kRows;
   }
-  // one after the other on the stream, each with its join: they share the workspace
-  f.ws_bytes = std::max(f.plan[0].ws_bytes, f.plan[1].ws_bytes);
-  return f;
+  if (q8 && r.dtype != LSC_BF16) return kAny;  // e4m3 tiles become bf16 there
+  *plan = lsc::plan_kv_attend_chunk(r);
+  return kChunk;
 }
 
 }  // namespace
@@ -282,6 +319,7 @@ int lsc_kv_pool_create(const lsc_kv_pool_desc *desc, void *device_base, size_t b
     }
     p->owns_base = true;
   }
+  make_maps(p);
   *out = p;
   return LSC_OK;
 }
@@ -435,7 +473,11 @@ int lsc_kv_attend_workspace_bytes(const lsc_kv_pool *p, const lsc_kv_attend_args
   lsc::KvAttendParams r{};
   const int rc = check_attend(p, 0, a, &r);
   if (rc != LSC_OK) return rc;
-  *bytes = r.b.n_seq == 0 || r.b.total_tokens == 0 ? 0 : attend_form(r).ws_bytes;
+  *bytes = 0;
+  if (r.b.n_seq == 0 || r.b.total_tokens == 0) return LSC_OK;
+  lsc::AttendPlan plan;
+  attend_form(r, &plan);
+  *bytes = plan.ws_bytes;
   return LSC_OK;
 }
 
@@ -447,30 +489,23 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
   rc = check_device(p);
   if (rc != LSC_OK) return rc;
   if (r.b.n_seq == 0 || r.b.total_tokens == 0) return LSC_OK;
-  const AttendForm f = attend_form(r);
+  lsc::AttendPlan plan;
+  const Form form = attend_form(r, &plan);
   cudaStream_t s = (cudaStream_t)stream;
-  if (f.launches == 0) {
-    if (lsc::launch_kv_attend_any(r, s) != cudaSuccess) {
-      cudaGetLastError();
-      return LSC_ERR_CUDA;
-    }
-    return LSC_OK;
-  }
   void *ws = a->workspace;
-  if (f.ws_bytes > 0) {
-    if (ws && a->workspace_bytes < f.ws_bytes) return LSC_ERR_INVALID_ARG;
-    if (!ws && cudaMallocAsync(&ws, f.ws_bytes, s) != cudaSuccess) {
+  if (plan.ws_bytes > 0) {
+    if (ws && a->workspace_bytes < plan.ws_bytes) return LSC_ERR_INVALID_ARG;
+    if (!ws && cudaMallocAsync(&ws, plan.ws_bytes, s) != cudaSuccess) {
       cudaGetLastError();
       return LSC_ERR_NO_MEMORY;
     }
+    r.ws = (uint8_t *)ws;
   }
-  cudaError_t e = cudaSuccess;
-  for (int i = 0; i < f.launches && e == cudaSuccess; ++i) {
-    r.ws = f.plan[i].may_cut ? (uint8_t *)ws : nullptr;
-    e = f.chunk[i] ? lsc::launch_kv_attend_chunk(r, f.plan[i], s) : lsc::launch_kv_attend_rows(r, f.plan[i], s);
-    if (e == cudaSuccess && f.plan[i].may_cut) e = lsc::launch_kv_attend_join(r, f.plan[i], s);
-  }
-  if (f.ws_bytes > 0 && !a->workspace && cudaFreeAsync(ws, s) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
+  cudaError_t e = form == kAny    ? lsc::launch_kv_attend_any(r, s)
+                  : form == kRows ? lsc::launch_kv_attend_rows(r, plan, s)
+                                  : lsc::launch_kv_attend_chunk(r, plan, s);
+  if (e == cudaSuccess && plan.may_cut) e = lsc::launch_kv_attend_join(r, plan, s);
+  if (plan.ws_bytes > 0 && !a->workspace && cudaFreeAsync(ws, s) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
   if (e != cudaSuccess) {
     cudaGetLastError();
     return LSC_ERR_CUDA;

@@ -53,16 +53,10 @@ __host__ __device__ __forceinline__ Workspace workspace_at(uint8_t *ws, int ctas
   return w;
 }
 
-// Which sequences a launch takes: packed rows in [row_lo, row_hi].
-struct Share {
-  int32_t row_lo, row_hi;
-};
-
-// Row blocks of M packed rows of a sequence under this launch.
+// Row blocks of M packed rows of a sequence.
 template <int M>
-__device__ __forceinline__ int32_t row_blocks(const Seq &s, int32_t group, const Share &sh) {
-  const int64_t rows = (int64_t)s.n * group;
-  return rows < sh.row_lo || rows > sh.row_hi || rows == 0 ? 0 : (int32_t)((rows + M - 1) / M);
+__device__ __forceinline__ int32_t row_blocks(const Seq &s, int32_t group) {
+  return (int32_t)(((int64_t)s.n * group + M - 1) / M);
 }
 
 // Tiles of one row block.
@@ -77,8 +71,8 @@ __device__ __forceinline__ int32_t block_tiles(const Seq &s, int32_t group, int3
 }
 
 template <int M, int TK>
-__device__ __forceinline__ int64_t seq_tiles(const Seq &s, int32_t group, int32_t causal, const Share &sh) {
-  const int32_t nb = row_blocks<M>(s, group, sh);
+__device__ __forceinline__ int64_t seq_tiles(const Seq &s, int32_t group, int32_t causal) {
+  const int32_t nb = row_blocks<M>(s, group);
   if (!causal) return nb ? (int64_t)nb * block_tiles<M, TK>(s, group, causal, 0) : 0;
   int64_t t = 0;
   for (int32_t b = 0; b < nb; ++b) t += block_tiles<M, TK>(s, group, causal, b);
@@ -128,13 +122,13 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, RunScratch &sc, int64_t
 
 // The run of CTA `cta` of `ctas`; called by all NT threads.
 template <int NT, int M, int TK>
-__device__ __forceinline__ Run find_run(const KvAttendParams &p, const Share &sh, int cta, int ctas, RunScratch &sc) {
+__device__ __forceinline__ Run find_run(const KvAttendParams &p, int cta, int ctas, RunScratch &sc) {
   const int H = p.L.heads;
   int64_t total = 0, mine = 0, incl = 0;
   for (int32_t i0 = 0; i0 < p.b.n_seq; i0 += NT) {
     const int32_t i = i0 + threadIdx.x;
     mine = i < p.b.n_seq
-               ? seq_tiles<M, TK>(attend_seq(p.L, p.b, i, p.max_seq, p.max_kv), p.group, p.causal, sh)
+               ? seq_tiles<M, TK>(attend_seq(p.L, p.b, i, p.max_seq, p.max_kv), p.group, p.causal)
                : 0;
     total += block_scan<NT>(mine, sc, &incl);
   }
@@ -154,7 +148,7 @@ __device__ __forceinline__ Run find_run(const KvAttendParams &p, const Share &sh
     const int32_t i = i0 + threadIdx.x;
     if (p.b.n_seq > NT) {  // else the first pass left this thread's values
       mine = i < p.b.n_seq
-                 ? seq_tiles<M, TK>(attend_seq(p.L, p.b, i, p.max_seq, p.max_kv), p.group, p.causal, sh)
+                 ? seq_tiles<M, TK>(attend_seq(p.L, p.b, i, p.max_seq, p.max_kv), p.group, p.causal)
                  : 0;
       const int64_t all = block_scan<NT>(mine, sc, &incl);
       if (mine > 0 && (base + incl - mine) * H <= r.pos && r.pos < (base + incl) * H) {
@@ -187,12 +181,12 @@ __device__ __forceinline__ Run find_run(const KvAttendParams &p, const Share &sh
 
 // The next piece of the run; false when it is done.
 template <int M, int TK>
-__device__ __forceinline__ bool next_piece(const KvAttendParams &p, const Share &sh, Run &r, Piece &q) {
+__device__ __forceinline__ bool next_piece(const KvAttendParams &p, Run &r, Piece &q) {
   if (r.pos >= r.end) return false;
   Seq s = attend_seq(p.L, p.b, r.seq, p.max_seq, p.max_kv);
-  while (r.block >= row_blocks<M>(s, p.group, sh)) {  // past this head's blocks (or a sequence of the other launch)
+  while (r.block >= row_blocks<M>(s, p.group)) {  // past this head's blocks (or a sequence without new tokens)
     r.block = 0;
-    if (row_blocks<M>(s, p.group, sh) == 0 || ++r.head == p.L.heads) {
+    if (row_blocks<M>(s, p.group) == 0 || ++r.head == p.L.heads) {
       r.head = 0;
       ++r.seq;
       s = attend_seq(p.L, p.b, r.seq, p.max_seq, p.max_kv);
@@ -242,14 +236,13 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
 struct AttendPlan {
   int32_t ctas;    // runs
   int32_t M;       // rows of a unit
-  kv::Share share;
   size_t ws_bytes; // of this launch's part of the workspace
   bool may_cut;    // false: every unit is one tile, so no run can cut one
 };
 cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_join(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
-AttendPlan plan_kv_attend_rows(const KvAttendParams &p, int32_t row_hi);
+AttendPlan plan_kv_attend_rows(const KvAttendParams &p);
 cudaError_t launch_kv_attend_chunk(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
-AttendPlan plan_kv_attend_chunk(const KvAttendParams &p, int32_t row_lo);
+AttendPlan plan_kv_attend_chunk(const KvAttendParams &p);
 
 }  // namespace lsc

@@ -12,9 +12,15 @@
 //   * one MMA warp: S = Q K^T, O += P V with P as the TMEM operand, issued so that
 //     the products of one tile run while the softmax of another does.
 //   * producer warps: K and V rows through the block table into a shared-memory
-//     ring in the 128-byte-swizzled layout, 16-bit pools with cp.async, E4M3
-//     pools through registers, where codes become bf16 with their scale (exact
-//     above bf16's smallest normal).  Rows behind the last position are zeros.
+//     ring in the 128-byte-swizzled layout.  16-bit pools whose blocks are a
+//     multiple of 8 tokens: tiled TMA boxes of rows x 64 elements (x head_dim /
+//     64 when a block holds the tile: then one box a tile; coordinates
+//     (element, row, column of 64, head, block) of the layer, element always
+//     0); a tile that is not full, and other block sizes: 16-byte cp.async.
+//     E4M3 pools: codes
+//     through a staging ring of each thread, then bf16 with their scale
+//     (exact above bf16's smallest normal).  Rows behind the last position
+//     are zeros.
 // head_dim 64 and 128: two row blocks of 128, each with its own S and O (S 2 x
 // 128, O 2 x head_dim columns of TMEM), Q in shared memory, tiles of 128: one
 // block's softmax runs under the other's products, and a K/V tile is
@@ -27,6 +33,7 @@
 // lsc_kv_attend_rows.cuh; here the softmax threads search such a tile's v.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "lsc_internal.h"
@@ -40,14 +47,15 @@ namespace chunk {
 
 constexpr int kThreads = 512;  // four warpgroups; the last one has the MMA warp and three idle ones
 
-template <int D>
+template <int D, bool Q8>
 struct Conf {
   static constexpr int NQ = D == 256 ? 1 : 2;   // row blocks of 128
   static constexpr int M = 128 * NQ;
   static constexpr int TK = D == 256 ? 64 : 128;
   static constexpr bool QT = D == 256;          // Q in TMEM
   static constexpr int slot = TK * D * 2;       // bytes of a K or V tile
-  static constexpr int NS = D == 64 ? 8 : D == 128 ? 5 : 6;
+  static constexpr int NS = Q8 ? (D == 64 ? 6 : D == 128 ? 4 : 5) : (D == 64 ? 8 : D == 128 ? 5 : 6);
+  static constexpr int SD = D == 128 ? 2 : 3;   // E4M3: stages of codes
   static constexpr int SW = 4 * NQ;             // softmax warps
   static constexpr int PW = D == 256 ? 8 : 4;   // producer warps
   // registers a thread of a softmax, producer and MMA warpgroup keeps of the 128 at launch: 4 * (SW / 4 * soft +
@@ -61,11 +69,12 @@ struct Conf {
   static constexpr int O0 = 256;                // O of row block b at O0 + b * D
 };
 
-template <int D>
+template <int D, bool Q8>
 struct Smem {
-  using C = Conf<D>;
+  using C = Conf<D, Q8>;
   alignas(1024) uint8_t ring[C::NS][C::slot];
   alignas(1024) uint8_t q[C::QT ? 16 : C::M * D * 2];
+  alignas(16) uint4 stage[Q8 ? C::SD : 1][Q8 ? C::TK * D / 16 / (32 * C::PW) : 1][Q8 ? 32 * C::PW : 1];  // E4M3: codes by thread
   int32_t bad[3][D];      // first position whose v is NaN, +inf, -inf
   uint64_t full[C::NS], empty[C::NS], sfull[2], pfull[2], qfull[2], odone[2], fin[2], met[2], drain;
   uint32_t tmem;
@@ -101,26 +110,109 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A bounded wait with one answer for the whole (converged) warp, so that a wait that gave up never splits it.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, int64_t phase, uint64_t limit) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)(phase & 1), limit));
+// Two fp32 values as the operand of the packed instructions, which do two lanes' worth a cycle.
+__device__ __forceinline__ uint64_t two(float x, float y) {
+  return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-// Place of K(j), V(j) of a piece of nt tiles in the order in which the ring is filled and used.
+// Wait for this thread's TMEM loads; v is tied to it, so nothing reads v earlier.
+__device__ __forceinline__ void wait_ld(uint32_t (&v)[32]) {
+#define LSC_R8(i) "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]), \
+                  "+r"(v[i + 6]), "+r"(v[i + 7])
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : LSC_R8(0), LSC_R8(8), LSC_R8(16), LSC_R8(24)::"memory");
+#undef LSC_R8
+}
+
+// Scores of columns at and behind `seen` become -infinity.
+__device__ __forceinline__ void hide(uint32_t (&s)[32], int32_t seen) {
+#pragma unroll
+  for (int y = 0; y < 32; ++y)
+    if (y >= seen) s[y] = 0xff800000u;
+}
+
+__device__ __forceinline__ float top_of(const uint32_t (&s)[32]) {
+  float t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t[i] = __uint_as_float(s[8 * i]);
+#pragma unroll
+    for (int y = 1; y < 8; ++y) t[i] = fmaxf(t[i], __uint_as_float(s[8 * i + y]));
+  }
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// 2^(s c + r) of 32 scores: added to l in 32 bits, rounded to 16 bits in q.
+template <bool BF16>
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint64_t c, uint64_t r, uint64_t &l, uint32_t (&q)[16]) {
+  uint64_t a[2] = {0, 0};
+#pragma unroll
+  for (int y = 0; y < 16; ++y) {
+    const uint64_t x = fma2((uint64_t)s[2 * y] | (uint64_t)s[2 * y + 1] << 32, c, r);
+    const float p0 = ex2(__uint_as_float((uint32_t)x)), p1 = ex2(__uint_as_float((uint32_t)(x >> 32)));
+    a[y & 1] = add2(a[y & 1], two(p0, p1));
+    q[y] = pack2(p0, p1, BF16);
+  }
+  l = add2(l, add2(a[0], a[1]));
+}
+
+// Tiled TMA load of one box (this CTA's shared memory), completing on `bar`.
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+      "[%7];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A bounded wait.  The first tries do without the clock: reading %globaltimer costs about a microsecond, several
+// tiles' worth of waits.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t phase, uint64_t limit) {
+  if (limit == 0) return false;
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, phase & 1)) return true;
+  return mbar_wait_bounded(bar, phase & 1, limit);
+}
+// The same with one answer for the whole (converged) warp, so that a wait that gave up never splits it.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, uint64_t limit) {
+  return __all_sync(0xffffffffu, wait_bar(bar, phase, limit));
+}
+
+// A walk over the ring's slots.  Counting modulo a number that is no power of two, or dividing by a block size, costs a
+// lone warp a hundred cycles and more each time, so the roles step instead.
+template <int NS>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == NS) slot = 0, phase ^= 1;
+  }
+};
+
+// Place of V(j) of a piece of nt tiles in the order in which the ring is filled and used: K(0), V(0), K(1), V(1) ...
+// with two row blocks, K(0), K(1), V(0), K(2), V(1) ... with one.
 template <int NQ>
-__device__ __forceinline__ int64_t k_index(int j) { return NQ == 2 ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
-template <int NQ>
-__device__ __forceinline__ int64_t v_index(int j, int nt) {
+__device__ __forceinline__ int v_index(int j, int nt) {
   return NQ == 2 ? 2 * j + 1 : j < nt - 1 ? 2 * j + 2 : 2 * j + 1;
 }
 
 template <bool BF16, bool Q8, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
-  using C = Conf<D>;
+chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map) {
+  using C = Conf<D, Q8>;
   constexpr int NQ = C::NQ, M = C::M, TK = C::TK, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+  Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31;
   const KvLayer &L = p.L;
   if (w == C::SW + C::PW) {
@@ -142,7 +234,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
   const int ctas = gridDim.x, cta = blockIdx.x;
   if (cta == 0) check_cu(L, p.b);
   tc::fence_before_sync();
-  Run run = find_run<kThreads, M, TK>(p, sh, cta, ctas, sm.run);
+  Run run = find_run<kThreads, M, TK>(p, cta, ctas, sm.run);
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tm = sm.tmem;
@@ -195,11 +287,11 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
       __syncwarp();
       if (ln == 0) mbar_arrive(&sm.qfull[b]);
     };
-    bool have = next_piece<M, TK>(p, sh, run, pc);
+    bool have = next_piece<M, TK>(p, run, pc);
     if (have && b * 128 < rows_of(pc)) load_q(pc);
-    int64_t it = 0;     // tiles this row block has been through
-    int64_t slots = 0;  // ring slots of the pieces before this one
-    int64_t meets = 0, done = 0;
+    uint32_t it = 0;     // tiles this row block has been through
+    uint32_t slots = 0;  // ring slots of the pieces before this one, modulo 2 NS
+    uint32_t meets = 0, done = 0;
     while (have && ok) {
       const int nt = pc.t1 - pc.t0, rows = rows_of(pc);
       const bool mine = b * 128 < rows;
@@ -216,7 +308,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
       const bool mixed = (pc.s.kv < (int64_t)pc.t1 * TK ? pc.s.kv : pc.t1 * TK) > sure;
       for (int j = 0; j < nt && mine; ++j, ++it) {
         const int sb = NQ == 2 ? b : (int)(it & 1);
-        const uint32_t ph = NQ == 2 ? (uint32_t)(it & 1) : (uint32_t)((it >> 1) & 1);
+        const uint32_t ph = NQ == 2 ? it : it >> 1;
         const uint32_t sa = tm + lane + C::S0 + sb * C::SN;
         const int32_t first = (pc.t0 + j) * TK;
         if (!(ok = wait_warp(&sm.sfull[sb], ph, limit))) break;
@@ -225,26 +317,23 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
         const bool mask = first + TK > full_to || !rows_all;
         const int32_t seen = vis - first;
         constexpr int HELD = TK == 64 ? 64 : 32;  // columns in registers at a time
-        uint32_t s[HELD];
+        uint32_t s[HELD], s2[HELD == 64 ? 1 : 32];
         float top = -INFINITY;
+        // the next 32 columns are on their way while these are looked at
+        auto &sa32 = *reinterpret_cast<uint32_t(*)[32]>(&s[0]);
+        auto &sb32 = *reinterpret_cast<uint32_t(*)[32]>(HELD == 64 ? &s[HELD - 32] : &s2[0]);
+        tc::tmem_ld32(sa, sa32);
+        wait_ld(sa32);
 #pragma unroll
-        for (int x = 0; x < TK; x += HELD) {
-#pragma unroll
-          for (int y = 0; y < HELD; y += 32)
-            tc::tmem_ld32(sa + x + y, *reinterpret_cast<uint32_t(*)[32]>(&s[y]));
-          tc::tmem_wait_ld();
-          if (mask) {
-#pragma unroll
-            for (int y = 0; y < HELD; ++y)
-              if (x + y >= seen) s[y] = 0xff800000u;
-          }
-          float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-          for (int y = 0; y < HELD; y += 4) {
-            t0 = fmaxf(t0, fmaxf(__uint_as_float(s[y]), __uint_as_float(s[y + 1])));
-            t1 = fmaxf(t1, fmaxf(__uint_as_float(s[y + 2]), __uint_as_float(s[y + 3])));
-          }
-          top = fmaxf(top, fmaxf(t0, t1));
+        for (int x = 0; x < TK; x += 64) {
+          tc::tmem_ld32(sa + x + 32, sb32);
+          if (mask) hide(sa32, seen - x);
+          top = fmaxf(top, top_of(sa32));
+          wait_ld(sb32);
+          if (x + 64 < TK) tc::tmem_ld32(sa + x + 64, sa32);
+          if (mask) hide(sb32, seen - x - 32);
+          top = fmaxf(top, top_of(sb32));
+          if (x + 64 < TK) wait_ld(sa32);
         }
         const float mt = top * c;  // c > 0
         if (__any_sync(0xffffffffu, mt > m + 8.f)) {  // also the first tile's (m is -inf)
@@ -267,34 +356,36 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float l0 = 0.f, l1 = 0.f;
+        const uint64_t c2 = two(c, c), r2 = two(-ref, -ref);
+        uint64_t l2 = two(0.f, 0.f);
+        uint32_t q[16];
+        if constexpr (HELD == 64) {
+          weights<BF16>(sa32, c2, r2, l2, q);
+          tc::tmem_st16(sa, q);
+          weights<BF16>(sb32, c2, r2, l2, q);
+          tc::tmem_st16(sa + 16, q);
+        } else {
+          tc::tmem_ld32(sa, sa32);
+          wait_ld(sa32);
 #pragma unroll
-        for (int x = 0; x < TK; x += HELD) {
-          if constexpr (HELD < TK) {
-            tc::tmem_ld32(sa + x, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-            tc::tmem_wait_ld();
-            if (mask) {
-#pragma unroll
-              for (int y = 0; y < HELD; ++y)
-                if (x + y >= seen) s[y] = 0xff800000u;
-            }
+          for (int x = 0; x < TK; x += 64) {
+            tc::tmem_ld32(sa + x + 32, sb32);
+            if (mask) hide(sa32, seen - x);
+            weights<BF16>(sa32, c2, r2, l2, q);
+            wait_ld(sb32);
+            tc::tmem_st16(sa + x / 2, q);  // over columns that have been read
+            if (x + 64 < TK) tc::tmem_ld32(sa + x + 64, sa32);
+            if (mask) hide(sb32, seen - x - 32);
+            weights<BF16>(sb32, c2, r2, l2, q);
+            if (x + 64 < TK) wait_ld(sa32);
+            tc::tmem_st16(sa + x / 2 + 16, q);
           }
-          uint32_t q[HELD / 2];
-#pragma unroll
-          for (int y = 0; y < HELD; y += 2) {
-            const float a0 = ex2(fmaf(__uint_as_float(s[y]), c, -ref));
-            const float a1 = ex2(fmaf(__uint_as_float(s[y + 1]), c, -ref));
-            l0 += a0;
-            l1 += a1;
-            q[y / 2] = pack2(a0, a1, BF16);
-          }
-          if constexpr (HELD == 64) tc::tmem_st32(sa, *reinterpret_cast<uint32_t(*)[32]>(&q[0]));
-          else tc::tmem_st16(sa + x / 2, *reinterpret_cast<uint32_t(*)[16]>(&q[0]));
         }
-        l += l0 + l1;
+        const float2 lf = *reinterpret_cast<const float2 *>(&l2);
+        l += lf.x + lf.y;
         const int32_t last = first + TK < pc.s.kv ? first + TK : pc.s.kv;
         if (last > sure) {  // positions [max(first, sure), last): some row of the unit does not see them
-          const int64_t vi = slots + v_index<NQ>(j, nt);
+          const uint32_t vi = slots + v_index<NQ>(j, nt);
           const int slot = (int)(vi % NS);
           if (!(ok = wait_warp(&sm.full[slot], vi / NS, limit))) break;
           const int lo = (sure > first ? sure : first) - first, cnt = last - first - lo;
@@ -333,8 +424,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
       const Piece q = pc;
       const bool ends_here = mine;
       cut = cut_of(run, q, cta);
-      slots += 2 * (int64_t)nt;
-      have = next_piece<M, TK>(p, sh, run, pc);
+      slots = (slots + 2 * (uint32_t)nt) % (2 * NS);
+      have = next_piece<M, TK>(p, run, pc);
       if (have && b * 128 < rows_of(pc)) load_q(pc);  // this piece's score products are done
       if (ends_here) {
         // a barrier of its own: odone may be up to two phases behind here, and a parity tells two apart, not three
@@ -404,99 +495,208 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::prod));
     // ---------------------------------------------------------------- producers
     const int pw = w - C::SW;
-    constexpr int CPR = D / 8;                        // 16-byte chunks of a 16-bit row
-    constexpr int RPW = TK / C::PW;                   // rows of a tile per warp (<= 32)
+    constexpr int RPW = TK / C::PW;  // rows of a tile per warp
     static_assert(RPW <= 32, "a lane finds at most one row");
-    constexpr int LAG = Q8 ? 0 : NS - 3;              // tiles in flight before the first is handed on
-    int64_t n = 0;                                    // tiles issued
-    int64_t handed = 0;
+    Ring<NS> at_n, at_h;             // the next tile to issue, to hand on
+    int pending = 0;                 // issued with cp.async, not handed on yet
+    bool first = true;               // the ring's first turn: every slot is empty
+    int nt = 0, kj = 0, vj = 0;
+    const int64_t row_bytes = (int64_t)L.heads * D * (Q8 ? 1 : 2);
+    // Block i of the piece's sequence, 0 behind its last position; a bad one is recorded and read as block 0.
+    auto load_block = [&](int32_t i) {
+      if ((int64_t)i * L.block_tokens >= pc.s.kv) return 0;
+      int32_t blk = __ldg(p.b.table + (int64_t)pc.seq * p.b.max_blocks + i);
+      if (blk < 0 || blk >= L.num_blocks) {
+        report(L.status, LSC_ERR_OUT_OF_RANGE);
+        blk = 0;
+      }
+      return blk;
+    };
+    // Table entries [base, base + 64) of the piece in the lanes' registers, the second half fetched a window ahead: a
+    // lookup per tile would cost an L2 round trip, about a third of a tile's time (1000 of 3600 cycles measured).
+    // Tiles reach at most 17 entries past V's first one, so two halves of 32 do; smaller blocks look up directly.
+    const bool window = L.block_tokens >= 8;
+    int32_t base_i = 0, near = 0, far = 0;
+    auto block_of = [&](int32_t i) {  // converged; i may differ between lanes
+      if (!window) return load_block(i);
+      const int32_t o = i - base_i;
+      const int32_t x = __shfl_sync(0xffffffffu, near, o & 31), y = __shfl_sync(0xffffffffu, far, o & 31);
+      return o < 32 ? x : y;
+    };
+    // Block and row of a tile's first position (K's and V's walk), stepped by a tile; a lane adds its own offset.
+    const int32_t tk_q = TK / L.block_tokens, tk_r = TK - tk_q * L.block_tokens;
+    int32_t tq[2] = {0, 0}, tr[2] = {0, 0}, q0 = 0, r0 = 0;
+    auto offset = [&](int32_t oq, int32_t orr, int32_t &q, int32_t &r) {
+      q = q0 + oq;
+      r = r0 + orr;
+      if (r >= L.block_tokens) r -= L.block_tokens, ++q;
+    };
+    const int32_t my = pw * RPW + (ln < RPW ? ln : 0), my_q = my / L.block_tokens, my_r = my - my_q * L.block_tokens;
+    // the next tile of the run, in the order of v_index
+    auto next_tile = [&](bool &is_k, int &j) {
+      while (vj >= nt) {
+        if (!next_piece<M, TK>(p, run, pc)) return false;
+        nt = pc.t1 - pc.t0;
+        kj = vj = 0;
+        tq[0] = tq[1] = (int32_t)((int64_t)pc.t0 * TK / L.block_tokens);
+        tr[0] = tr[1] = (int32_t)((int64_t)pc.t0 * TK - (int64_t)tq[0] * L.block_tokens);
+        if (window) {
+          base_i = tq[0];
+          near = load_block(base_i + ln);
+          far = load_block(base_i + 32 + ln);
+        }
+      }
+      is_k = NQ == 2 ? kj == vj : kj < nt && kj <= vj + 1;
+      j = is_k ? kj++ : vj++;
+      q0 = is_k ? tq[0] : tq[1];
+      r0 = is_k ? tr[0] : tr[1];
+      int32_t nq = q0 + tk_q, nr = r0 + tk_r;
+      if (nr >= L.block_tokens) nr -= L.block_tokens, ++nq;
+      if (is_k) tq[0] = nq, tr[0] = nr;
+      else tq[1] = nq, tr[1] = nr;
+      if (window && !is_k && q0 - base_i >= 32) {
+        base_i += 32;
+        near = far;
+        far = load_block(base_i + 32 + ln);
+      }
+      return true;
+    };
+    // lane i's row of this warp's RPW rows of tile j: its byte offset in a lane, -1 behind the last position
+    auto place = [&](int j, uint32_t *sb, bool is_k) {
+      const int32_t pos = (pc.t0 + j) * TK + my;
+      int32_t q, rr;
+      offset(my_q, my_r, q, rr);
+      const int64_t page = (int64_t)block_of(q) * L.page;
+      if (ln >= RPW || pos >= pc.s.kv) return (int64_t)-1;
+      if (Q8) *sb = __ldg((is_k ? L.k : L.v) + page + L.scale_off + (int64_t)rr * L.heads + pc.head);
+      return page + (int64_t)rr * row_bytes + (int64_t)pc.head * D * (Q8 ? 1 : 2);
+    };
     auto hand_on = [&]() {
       fence_proxy_async_smem();
       __syncwarp();
-      if (ln == 0) mbar_arrive(&sm.full[handed % NS]);
-      ++handed;
+      if (ln == 0) mbar_arrive(&sm.full[at_h.slot]);
+      at_h.step();
     };
-    while (ok && next_piece<M, TK>(p, sh, run, pc)) {
-      const int nt = pc.t1 - pc.t0;
-      const int32_t kv = pc.s.kv;
-      const int32_t *table = p.b.table + (int64_t)pc.seq * p.b.max_blocks;
-      const int64_t row_bytes = (int64_t)L.heads * D * (Q8 ? 1 : 2);
-      const int64_t head_off = (int64_t)pc.head * D * (Q8 ? 1 : 2);
-      int kj = 0, vj = 0;
-      while (ok && vj < nt) {
-        // the order of k_index and v_index
-        const bool is_k = NQ == 2 ? kj == vj : kj < nt && kj <= vj + 1;
-        const int j = is_k ? kj++ : vj++;
-        // lane i finds row i of this warp's RPW rows: block offset, row; -1 behind the last position
-        const int32_t pos = (pc.t0 + j) * TK + pw * RPW + ln;
-        int64_t at = -1;
-        uint32_t sb = 127;
-        if (ln < RPW && pos < kv) {
-          const int32_t q = pos / L.block_tokens, rr = pos - q * L.block_tokens;
-          int32_t blk = table[q];
-          if (blk < 0 || blk >= L.num_blocks) {
-            report(L.status, LSC_ERR_OUT_OF_RANGE);
-            blk = 0;
-          }
-          at = (int64_t)blk * L.page + (int64_t)rr * row_bytes + head_off;
-          if constexpr (Q8)
-            sb = (is_k ? L.k : L.v)[(int64_t)blk * L.page + L.scale_off + (int64_t)rr * L.heads + pc.head];
-        }
-        const int slot = (int)(n % NS);
-        if (n >= NS && !(ok = wait_warp(&sm.empty[slot], n / NS - 1, limit))) break;
-        const uint8_t *base = is_k ? L.k : L.v;
+    auto wait_empty = [&](const Ring<NS> &r) { return first || wait_warp(&sm.empty[r.slot], r.phase ^ 1, limit); };
+    auto issued = [&]() {
+      at_n.step();
+      if (at_n.slot == 0) first = false;
+    };
+    bool is_k;
+    int j;
+    if constexpr (!Q8) {
+      constexpr int CPR = D / 8;                        // 16-byte chunks of a row
+      constexpr int RPI = 32 / CPR > 0 ? 32 / CPR : 1;  // rows per instruction
+      constexpr int LAG = NS - 3;                       // cp.async tiles in flight before the first is handed on
+      // TMA: a box of `box` rows and all columns when a block holds the tile, else of one column of 64 elements; the
+      // boxes go over the lanes of all producer warps.  box 0: cp.async alone.
+      const int box = p.box_rows, cols = box == TK ? D / 64 : 1, per = D / 64 / cols;
+      const int boxes = box > 0 ? TK / box * per : 0, bi = ln * C::PW + pw, bc = bi % per;
+      const int br = bi < boxes ? bi / per * box : 0, br_q = br / L.block_tokens, br_r = br - br_q * L.block_tokens;
+      const uint32_t bytes = (uint32_t)((boxes - pw + C::PW - 1) / C::PW) * box * cols * 128;  // this warp's share
+      while (ok && next_tile(is_k, j)) {
+        const int slot = at_n.slot;
         uint8_t *dst = sm.ring[slot];
-        if constexpr (!Q8) {
-          constexpr int RPI = 32 / CPR > 0 ? 32 / CPR : 1;  // rows per instruction
-          const int ch = ln % CPR;
-#pragma unroll
-          for (int i = 0; i < RPW; i += RPI) {
-            const int rl = i + ln / CPR, r = pw * RPW + rl;
-            const int64_t a = __shfl_sync(0xffffffffu, at, rl);
-            cp_async16_or_zero(smem_u32(dst + (ch >> 3) * (TK * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                               base + (a < 0 ? 0 : a) + ch * 16, a >= 0);
+        if (box > 0 && (int64_t)(pc.t0 + j + 1) * TK <= pc.s.kv) {
+          int32_t q, rr;
+          offset(br_q, br_r, q, rr);
+          const int32_t blk = block_of(q);
+          if (!(ok = wait_empty(at_n))) break;
+          if (ln == 0) {
+            if (bytes) mbar_arrive_expect_tx(&sm.full[slot], bytes);
+            else mbar_arrive(&sm.full[slot]);
           }
-          cp_async_commit();
-          ++n;
-          if (n > LAG) {
-            cp_async_wait<LAG>();
-            hand_on();
+          __syncwarp();
+          if (bi < boxes)
+            tma_load_5d(dst + bc * (TK * 128) + br * 128, &map, 0, rr, bc, pc.head, blk + (is_k ? 0 : L.num_blocks),
+                        &sm.full[slot]);
+          if (pending > 0) {  // cp.async tiles before this one
+            cp_async_wait<0>();
+            for (; pending > 0; --pending) hand_on();
           }
-        } else {
-          // 16 codes a lane: two chunks of the 16-bit row
-          constexpr int LPR = D / 16, RPI = 32 / LPR;
-          const int lc = ln % LPR;
-          uint4 code[RPW / RPI];
+          at_h.step();
+          issued();
+          continue;
+        }
+        const int64_t at = place(j, nullptr, is_k);
+        if (!(ok = wait_empty(at_n))) break;
+        const uint8_t *base = is_k ? L.k : L.v;
+        const int ch = ln % CPR;
 #pragma unroll
-          for (int i = 0; i < RPW / RPI; ++i) {
-            const int64_t a = __shfl_sync(0xffffffffu, at, i * RPI + ln / LPR);
-            code[i] = a < 0 ? make_uint4(0, 0, 0, 0) : *(const uint4 *)(base + a + lc * 16);
-          }
-#pragma unroll
-          for (int i = 0; i < RPW / RPI; ++i) {
-            const int rl = i * RPI + ln / LPR, r = pw * RPW + rl;
-            const float k = scale_of(__shfl_sync(0xffffffffu, sb, rl));
-            const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float2 lo = e4m3x2_to_float2(cw[x] & 0xffffu), hi = e4m3x2_to_float2(cw[x] >> 16);
-              o[2 * x] = pack2(lo.x * k, lo.y * k, BF16);
-              o[2 * x + 1] = pack2(hi.x * k, hi.y * k, BF16);
-            }
-            const int ch = 2 * lc;
-            uint8_t *row = dst + (ch >> 3) * (TK * 128) + r * 128;
-            *(uint4 *)(row + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *(uint4 *)(row + ((((ch & 7) + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-          ++n;
+        for (int i = 0; i < RPW; i += RPI) {
+          const int rl = i + ln / CPR, r = pw * RPW + rl;
+          const int64_t a = __shfl_sync(0xffffffffu, at, rl);
+          cp_async16_or_zero(smem_u32(dst + (ch >> 3) * (TK * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                             base + (a < 0 ? 0 : a) + ch * 16, a >= 0);
+        }
+        cp_async_commit();
+        issued();
+        if (++pending > LAG) {
+          cp_async_wait<LAG>();
           hand_on();
+          --pending;
         }
       }
+      cp_async_wait<0>();
+      for (; ok && pending > 0; --pending) hand_on();
+    } else {
+      // 16 codes (two chunks of the 16-bit row) a lane and instruction, through a ring of SD stages that belongs to the
+      // thread: what it copies with cp.async it converts itself, so the copies need no barrier
+      constexpr int SD = C::SD, LPR = D / 16, RPI = 32 / LPR, IT = RPW / RPI;
+      const int lc = ln % LPR, th = pw * 32 + ln;
+      uint32_t sb[SD];
+#pragma unroll
+      for (int i = 0; i < SD; ++i) sb[i] = 127;
+      Ring<SD> st_in, st_out;
+      int left = 0;  // tiles fetched and not converted
+      auto fetch = [&]() {  // the run's next tile into its stage; an empty group when there is none
+        uint32_t byte = 127;
+        if (ok && next_tile(is_k, j)) {
+          const int64_t at = place(j, &byte, is_k);
+          const uint8_t *base = is_k ? L.k : L.v;
+#pragma unroll
+          for (int i = 0; i < IT; ++i) {
+            const int64_t a = __shfl_sync(0xffffffffu, at, i * RPI + ln / LPR);
+            cp_async16_or_zero(smem_u32(&sm.stage[st_in.slot][i][th]), base + (a < 0 ? 0 : a) + lc * 16, a >= 0);
+          }
+          st_in.step();
+          ++left;
+        }
+        cp_async_commit();
+#pragma unroll
+        for (int i = 0; i + 1 < SD; ++i) sb[i] = sb[i + 1];
+        sb[SD - 1] = byte;
+      };
+      for (int g = 0; g < SD; ++g) fetch();
+      for (; left > 0; --left) {
+        cp_async_wait<SD - 1>();
+        if (!(ok = wait_empty(at_n))) break;
+        uint8_t *dst = sm.ring[at_n.slot];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int rl = i * RPI + ln / LPR, r = pw * RPW + rl;
+          const float k = scale_of(__shfl_sync(0xffffffffu, sb[0], rl));
+          const uint4 code = sm.stage[st_out.slot][i][th];
+          const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+          uint32_t o[8];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 lo = e4m3x2_to_float2(cw[x] & 0xffffu), hi = e4m3x2_to_float2(cw[x] >> 16);
+            o[2 * x] = pack2(lo.x * k, lo.y * k, BF16);
+            o[2 * x + 1] = pack2(hi.x * k, hi.y * k, BF16);
+          }
+          const int ch = 2 * lc;
+          uint8_t *row = dst + (ch >> 3) * (TK * 128) + r * 128;
+          *(uint4 *)(row + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *(uint4 *)(row + ((((ch & 7) + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        hand_on();
+        issued();
+        st_out.step();
+        fetch();
+      }
+      cp_async_wait<0>();
     }
-    cp_async_wait<0>();
-    if (!Q8 && ok)
-      while (handed < n) hand_on();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma));
   }
@@ -504,15 +704,23 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
     // ---------------------------------------------------------------- products
     const bool lead = tc::elect_one();
     constexpr uint32_t iqk = idesc_f16(128, TK, BF16, false), ipv = idesc_f16(128, D, BF16, true);
-    int64_t slots = 0, itb[2] = {0, 0}, pieces[2] = {0, 0};
-    auto wait = [&](uint64_t *bar, int64_t phase) {
-      if (ok) ok = mbar_wait_bounded(bar, (uint32_t)(phase & 1), limit);
+    Ring<NS> at;  // the next tile of the ring to wait for
+    uint32_t itb[2] = {0, 0}, pieces[2] = {0, 0};
+    const uint32_t ring0 = smem_u32(sm.ring[0]), q0 = smem_u32(sm.q);
+    auto wait = [&](uint64_t *bar, uint32_t phase) {
+      if (ok) ok = wait_bar(bar, phase, limit);
       return ok;
     };
-    auto slot_wait = [&](int64_t i) { return wait(&sm.full[i % NS], i / NS); };
-    auto scores = [&](int b, int sb, int64_t ki) {  // S[sb] = Q[b] K^T
+    auto next_slot = [&](int &slot) {  // waits for the ring's next tile
+      slot = at.slot;
+      const bool r = wait(&sm.full[at.slot], at.phase);
+      at.step();
+      tc::fence_after_sync();
+      return r;
+    };
+    auto scores = [&](int b, int sb, int slot) {  // S[sb] = Q[b] K^T
       if (lead) {
-        const uint32_t kb = smem_u32(sm.ring[ki % NS]), qb = smem_u32(sm.q) + b * 128 * D * 2;
+        const uint32_t kb = ring0 + slot * C::slot, qb = q0 + b * 128 * D * 2;
         const uint32_t d = tm + C::S0 + sb * C::SN;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -523,9 +731,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
         tc::mma_commit(&sm.sfull[sb]);
       }
     };
-    auto values = [&](int b, int sb, int64_t vi, bool fresh, bool last) {  // O[b] (+)= P[sb] V
+    auto values = [&](int b, int sb, int slot, bool fresh, bool last) {  // O[b] (+)= P[sb] V
       if (lead) {
-        const uint32_t vb = smem_u32(sm.ring[vi % NS]);
+        const uint32_t vb = ring0 + slot * C::slot;
 #pragma unroll
         for (int k = 0; k < TK / 16; ++k)
           mma_ts16(tm + C::O0 + b * D, tm + C::S0 + sb * C::SN + k * 8, desc128(vb + k * 2048, TK * 128, 1024), ipv,
@@ -534,57 +742,51 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
         if (last) tc::mma_commit(&sm.fin[b]);
       }
     };
-    auto release = [&](int64_t i) {
-      if (lead) tc::mma_commit(&sm.empty[i % NS]);
+    auto release = [&](int slot) {
+      if (lead) tc::mma_commit(&sm.empty[slot]);
     };
-    while (ok && next_piece<M, TK>(p, sh, run, pc)) {
+    int ks, vs;
+    while (ok && next_piece<M, TK>(p, run, pc)) {
       const int nt = pc.t1 - pc.t0;
       const int64_t rows = (int64_t)pc.s.n * p.group - (int64_t)pc.block * M;
       const int nb = NQ == 2 && rows > 128 ? 2 : 1;
       for (int b = 0; b < nb; ++b)
         if (!wait(&sm.qfull[b], pieces[b]++)) break;
-      if (!ok || !slot_wait(slots)) break;
-      tc::fence_after_sync();
+      if (!ok || !next_slot(ks)) break;
       if constexpr (NQ == 2) {
-        for (int b = 0; b < nb; ++b) scores(b, b, slots);
-        release(slots);
+        for (int b = 0; b < nb; ++b) scores(b, b, ks);
+        release(ks);
         for (int j = 0; j < nt; ++j) {
-          const int64_t vi = slots + v_index<NQ>(j, nt), ki = slots + k_index<NQ>(j + 1);
-          if (!slot_wait(vi)) break;
+          if (!next_slot(vs)) break;
           for (int b = 0; b < nb; ++b) {
             if (!wait(&sm.pfull[b], itb[b]++)) break;
             tc::fence_after_sync();
-            values(b, b, vi, j == 0, j == nt - 1);
-            if (b == nb - 1) release(vi);
+            values(b, b, vs, j == 0, j == nt - 1);
+            if (b == nb - 1) release(vs);
             if (j + 1 < nt) {
-              if (b == 0 && !slot_wait(ki)) break;
-              tc::fence_after_sync();
-              scores(b, b, ki);
-              if (b == nb - 1) release(ki);
+              if (b == 0 && !next_slot(ks)) break;
+              scores(b, b, ks);
+              if (b == nb - 1) release(ks);
             }
           }
           if (!ok) break;
         }
       } else {
-        int64_t &it = itb[0];
-        scores(0, (int)(it & 1), slots);
-        release(slots);
+        uint32_t &it = itb[0];
+        scores(0, (int)(it & 1), ks);
+        release(ks);
         for (int j = 0; j < nt; ++j, ++it) {
           if (j + 1 < nt) {
-            const int64_t ki = slots + k_index<NQ>(j + 1);
-            if (!slot_wait(ki)) break;
-            tc::fence_after_sync();
-            scores(0, (int)((it + 1) & 1), ki);
-            release(ki);
+            if (!next_slot(ks)) break;
+            scores(0, (int)((it + 1) & 1), ks);
+            release(ks);
           }
-          const int64_t vi = slots + v_index<NQ>(j, nt);
-          if (!slot_wait(vi) || !wait(&sm.pfull[it & 1], it >> 1)) break;
+          if (!next_slot(vs) || !wait(&sm.pfull[it & 1], it >> 1)) break;
           tc::fence_after_sync();
-          values(0, (int)(it & 1), vi, j == 0, j == nt - 1);
-          release(vi);
+          values(0, (int)(it & 1), vs, j == 0, j == nt - 1);
+          release(vs);
         }
       }
-      slots += 2 * (int64_t)nt;
     }
     // everything issued has completed before TMEM is freed
     if (lead) tc::mma_commit(&sm.drain);
@@ -605,10 +807,10 @@ template <bool BF16, bool Q8, int D>
 cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
   static SmemLimit limit;
   auto *k = chunk_attend_kernel<BF16, Q8, D>;
-  const int smem = (int)sizeof(Smem<D>);
+  const int smem = (int)sizeof(Smem<D, Q8>);
   const cudaError_t e = limit.ensure((const void *)k, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, plan.ctas, kThreads, smem, stream, p, plan.share);
+  return launch_pdl(k, plan.ctas, kThreads, smem, stream, p, p.map ? *p.map : CUtensorMap{});
 }
 
 template <bool BF16, bool Q8>

@@ -80,12 +80,11 @@ cudaError_t launch_kv_attend_join(const KvAttendParams &p, const AttendPlan &pla
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-AttendPlan plan_kv_attend_rows(const KvAttendParams &p, int32_t row_hi) {
+AttendPlan plan_kv_attend_rows(const KvAttendParams &p) {
   using namespace kv::rows;
   const int D = p.L.head_dim, q8 = p.L.dtype == LSC_E4M3;
   AttendPlan plan{};
-  plan.M = row_hi <= 16 ? 16 : 64;
-  plan.share = {1, row_hi};
+  plan.M = (int64_t)p.max_seq * p.group <= 16 ? 16 : 64;
   const int occ = q8 ? (D == 64 ? occ_of<1, 64>(plan.M) : D == 128 ? occ_of<1, 128>(plan.M) : occ_of<1, 256>(plan.M))
                      : (D == 64 ? occ_of<2, 64>(plan.M) : D == 128 ? occ_of<2, 128>(plan.M) : occ_of<2, 256>(plan.M));
   const int64_t tiles = ((int64_t)p.max_kv + kTK - 1) / kTK;
@@ -103,12 +102,11 @@ cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &pla
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-AttendPlan plan_kv_attend_chunk(const KvAttendParams &p, int32_t row_lo) {
+AttendPlan plan_kv_attend_chunk(const KvAttendParams &p) {
   using namespace kv::chunk;
-  const int D = p.L.head_dim, TK = D == 256 ? Conf<256>::TK : Conf<128>::TK;
+  const int D = p.L.head_dim, TK = D == 256 ? Conf<256, false>::TK : Conf<128, false>::TK;
   AttendPlan plan{};
-  plan.M = D == 256 ? Conf<256>::M : Conf<128>::M;
-  plan.share = {row_lo, INT32_MAX};
+  plan.M = D == 256 ? Conf<256, false>::M : Conf<128, false>::M;
   const int64_t tiles = ((int64_t)p.max_kv + TK - 1) / TK;
   const int64_t blocks = ((int64_t)p.b.total_tokens * p.group + plan.M - 1) / plan.M + p.b.n_seq;
   const int64_t most = blocks * p.L.heads * (tiles < 1 ? 1 : tiles);

@@ -102,7 +102,7 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 // element (1: E4M3).
 template <bool BF16, int ES, int D, int MT>
 __global__ void __launch_bounds__(kThreads, (Conf<ES, D, MT>::occ))
-rows_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
+rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
   using C = Conf<ES, D, MT>;
   constexpr bool Q8 = ES == 1;
   constexpr int M = 16 * MT, ST = C::ST, RB = C::RB;
@@ -119,10 +119,10 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p, const Share sh) {
   const int ctas = gridDim.x, cta = blockIdx.x;
   if (cta == 0) check_cu(L, p.b);
   const Workspace ws = workspace_at(p.ws, ctas, M);
-  Run run = find_run<kThreads, M, kTK>(p, sh, cta, ctas, sm.run);
+  Run run = find_run<kThreads, M, kTK>(p, cta, ctas, sm.run);
   Piece pc;
   Cut cut = {0, 0, 0, 0};
-  while (next_piece<M, kTK>(p, sh, run, pc)) {
+  while (next_piece<M, kTK>(p, run, pc)) {
     const int R = pc.s.n * p.group < M ? pc.s.n * p.group : M;  // this launch's units have one block
     const int nt = pc.t1 - pc.t0;
     const int32_t kv = pc.s.kv;
@@ -467,7 +467,7 @@ cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStre
   auto *k = rows_attend_kernel<BF16, ES, D, MT>;
   const cudaError_t e = limit.ensure((const void *)k, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, plan.ctas, kThreads, smem, stream, p, plan.share);
+  return launch_pdl(k, plan.ctas, kThreads, smem, stream, p);
 }
 
 // One type's kernels, by head size and rows.
