@@ -4,30 +4,32 @@
 // 4 * head_dim operations a (row, position) pair, and K/V tiles that serve 128 or
 // 256 rows: the 5th-generation tensor cores bound it.  One CTA per SM walks its
 // run of tiles of TK positions with the warps in roles:
-//   * softmax warps, one thread a row: wait for the scores S = Q K^T of a tile in
-//     TMEM, weights 2^(s - m) to 16 bits back into the same TMEM columns, sum in a
-//     register.  m is a reference, not the exact maximum: O is rescaled (in TMEM,
-//     by these threads) only when a row's maximum rose by more than 2^8, so a
-//     weight is at most 2^8 and the rescale is rare after the first tiles.
+//   * two softmax warpgroups, one thread a row: wait for the scores S = Q K^T of a
+//     tile in TMEM, weights 2^(s - m) to 16 bits back into the same TMEM columns,
+//     sum in a register.  m is a reference, not the exact maximum: O is rescaled
+//     (in TMEM, by these threads) only when a row's maximum rose by more than 2^8,
+//     so a weight is at most 2^8 and the rescale is rare after the first tiles.
 //   * one MMA warp: S = Q K^T, O += P V with P as the TMEM operand, issued so that
 //     the products of one tile run while the softmax of another does.
-//   * producer warps: K and V rows through the block table into a shared-memory
-//     ring in the 128-byte-swizzled layout.  16-bit pools whose blocks are a
-//     multiple of 8 tokens: tiled TMA boxes of rows x 64 elements (x head_dim /
-//     64 when a block holds the tile: then one box a tile; coordinates
-//     (element, row, column of 64, head, block) of the layer, element always
-//     0); a tile that is not full, and other block sizes: 16-byte cp.async.
-//     E4M3 pools: codes
-//     through a staging ring of each thread, then bf16 with their scale
-//     (exact above bf16's smallest normal).  Rows behind the last position
-//     are zeros.
-// head_dim 64 and 128: two row blocks of 128, each with its own S and O (S 2 x
-// 128, O 2 x head_dim columns of TMEM), Q in shared memory, tiles of 128: one
-// block's softmax runs under the other's products, and a K/V tile is
-// fetched once for 256 rows.
+//   * producers: K and V rows through the block table into a shared-memory ring
+//     (K(0), V(0), K(1), V(1) ...) in the 128-byte-swizzled layout.  16-bit pools:
+//     a warp for K and one for V.  Blocks that are a multiple of 8 tokens come
+//     as tiled TMA boxes of rows x 64 elements (x head_dim / 64 when a block holds
+//     the tile: then one box a tile; coordinates (element, row, column of 64, head,
+//     block) of the layer, element always 0); a tile that is not full, and other
+//     block sizes, with 16-byte cp.async.  E4M3 pools: two warps each, codes
+//     through a staging buffer of each thread, then bf16 with their scale
+//     (exact above bf16's smallest normal).  Rows behind the last position are
+//     zeros.
+// head_dim 64 and 128: two row blocks of 128, one per softmax warpgroup, each with
+// its own S and O (S 2 x 128, O 2 x head_dim columns of TMEM), Q in shared memory,
+// tiles of 128: one block's softmax runs under the other's products, and a K/V
+// tile is fetched once for 256 rows.
 // head_dim 256: O takes 256 columns, so one row block, tiles of 64 and two S
-// buffers in turn; Q is a TMEM operand (128 columns), which leaves shared
-// memory to K and V and halves what the score products read from it.
+// buffers; the warpgroups take the tiles in turn, so that a tile's softmax has two
+// tiles' time, and hand the reference m on through shared memory.  Q is a TMEM
+// operand (128 columns), which leaves shared memory to K and V and halves what the
+// score products read from it.
 //
 // Positions that only some rows of a unit see may hold infinities and NaN: see
 // lsc_kv_attend_rows.cuh; here the softmax threads search such a tile's v.
@@ -45,8 +47,6 @@ namespace lsc {
 namespace kv {
 namespace chunk {
 
-constexpr int kThreads = 512;  // four warpgroups; the last one has the MMA warp and three idle ones
-
 template <int D, bool Q8>
 struct Conf {
   static constexpr int NQ = D == 256 ? 1 : 2;   // row blocks of 128
@@ -54,15 +54,15 @@ struct Conf {
   static constexpr int TK = D == 256 ? 64 : 128;
   static constexpr bool QT = D == 256;          // Q in TMEM
   static constexpr int slot = TK * D * 2;       // bytes of a K or V tile
-  static constexpr int NS = Q8 ? (D == 64 ? 6 : D == 128 ? 4 : 5) : (D == 64 ? 8 : D == 128 ? 5 : 6);
-  static constexpr int SD = D == 128 ? 2 : 3;   // E4M3: stages of codes
-  static constexpr int SW = 4 * NQ;             // softmax warps
-  static constexpr int PW = D == 256 ? 8 : 4;   // producer warps
-  // registers a thread of a softmax, producer and MMA warpgroup keeps of the 128 at launch: 4 * (SW / 4 * soft +
-  // PW / 4 * prod + mma) <= 16 * 128
-  static constexpr int soft = D == 256 ? 200 : 160, prod = D == 256 ? 104 : 96, mma = D == 256 ? 104 : 96;
-  static_assert(SW / 4 * soft + PW / 4 * prod + mma <= 4 * 128, "more registers than the block has");
-  static_assert(SW + PW == 12, "three warpgroups beside the one of the MMA warp");
+  static constexpr int NS = Q8 ? (D == 64 ? 6 : 4) : (D == 64 ? 8 : D == 128 ? 5 : 6);
+  static constexpr int SD = D == 128 ? 1 : 2;   // E4M3: stages of codes
+  // warps: 0-7 softmax, 8 MMA, 16-bit pools 9 K and 10 V, E4M3 12-13 K and 14-15 V
+  static constexpr int threads = Q8 ? 512 : 384;
+  static constexpr int GW = Q8 ? 2 : 1;         // producer warps of a tile
+  static constexpr bool hold = !Q8 || TK == 64; // a thread keeps all scores of a tile in registers
+  // registers a thread of a softmax warpgroup, the MMA's and E4M3's producers' keeps of those at launch
+  static constexpr int soft = Q8 ? 160 : 208, mma = Q8 ? 64 : 80, prod = 128;
+  static_assert(2 * soft + mma + (Q8 ? prod : 0) <= (Q8 ? 4 * 128 : 3 * 168), "more registers than the block has");
   // TMEM columns
   static constexpr int S0 = 0, SN = TK;         // S buffer b at S0 + b * SN; P in its first half
   static constexpr int Q0 = 128;                // QT only
@@ -74,34 +74,41 @@ struct Smem {
   using C = Conf<D, Q8>;
   alignas(1024) uint8_t ring[C::NS][C::slot];
   alignas(1024) uint8_t q[C::QT ? 16 : C::M * D * 2];
-  alignas(16) uint4 stage[Q8 ? C::SD : 1][Q8 ? C::TK * D / 16 / (32 * C::PW) : 1][Q8 ? 32 * C::PW : 1];  // E4M3: codes by thread
+  alignas(16) uint4 stage[Q8 ? C::SD : 1][Q8 ? C::TK * D / 16 / 64 : 1][Q8 ? 128 : 1];  // E4M3: codes by thread
   int32_t bad[3][D];      // first position whose v is NaN, +inf, -inf
   uint64_t full[C::NS], empty[C::NS], sfull[2], pfull[2], qfull[2], odone[2], fin[2], met[2], drain;
+  uint64_t turn[2][4], swap[2][4];   // one row block: by warpgroup and warp
+  float ref[C::NQ == 1 ? 128 : 1];   // a row's reference m
+  float2 ml[2][2][C::NQ == 1 ? 128 : 1];  // (m, sum) by piece parity and warpgroup
   uint32_t tmem;
   int32_t any_bad;
   RunScratch run;
 };
 
-// Shared-memory matrix descriptor, 128-byte swizzle (bits 61-63 = 2), version 1.
-__device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+// Low word of a shared-memory matrix descriptor: start address and leading byte offset.  The high word is the stride
+// byte offset (1024: groups of 8 rows of 128 bytes), version 1 (bit 46) and the 128-byte swizzle (bits 61-63 = 2).  A
+// descriptor further along is the low word plus bytes / 16, so a product's 16 descriptors need no registers of their own.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16;
 }
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
 // Instruction descriptor of kind::f16 with an fp32 accumulator: both operands f16 (0) or bf16 (1).
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b_mn_major) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(kDescHi),
+      "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(kDescHi),
+      "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -188,26 +195,21 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, uint64_
   return __all_sync(0xffffffffu, wait_bar(bar, phase, limit));
 }
 
-// A walk over the ring's slots.  Counting modulo a number that is no power of two, or dividing by a block size, costs a
-// lone warp a hundred cycles and more each time, so the roles step instead.
+// A walk over the ring's slots of K (from 0) or V (from 1).  Counting modulo a number that is no power of two, or
+// dividing by a block size, costs a lone warp a hundred cycles and more each time, so the roles step instead.
 template <int NS>
 struct Ring {
-  int slot = 0;
+  int slot;
   uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int first) : slot(first) {}
   __device__ __forceinline__ void step() {
-    if (++slot == NS) slot = 0, phase ^= 1;
+    slot += 2;
+    if (slot >= NS) slot -= NS, phase ^= 1;
   }
 };
 
-// Place of V(j) of a piece of nt tiles in the order in which the ring is filled and used: K(0), V(0), K(1), V(1) ...
-// with two row blocks, K(0), K(1), V(0), K(2), V(1) ... with one.
-template <int NQ>
-__device__ __forceinline__ int v_index(int j, int nt) {
-  return NQ == 2 ? 2 * j + 1 : j < nt - 1 ? 2 * j + 2 : 2 * j + 1;
-}
-
 template <bool BF16, bool Q8, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Conf<D, Q8>::threads, 1)
 chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map) {
   using C = Conf<D, Q8>;
   constexpr int NQ = C::NQ, M = C::M, TK = C::TK, NS = C::NS;
@@ -215,26 +217,28 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31;
   const KvLayer &L = p.L;
-  if (w == C::SW + C::PW) {
+  if (w == 8) {
     tc::tmem_alloc(&sm.tmem, 512);
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], C::PW), mbar_init(&sm.empty[i], 1);
-    for (int i = 0; i < 2; ++i)
-      mbar_init(&sm.sfull[i], 1), mbar_init(&sm.pfull[i], 4), mbar_init(&sm.qfull[i], 4), mbar_init(&sm.odone[i], 1), mbar_init(&sm.fin[i], 1),
-          mbar_init(&sm.met[i], 4);
+    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], C::GW), mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.sfull[i], 1), mbar_init(&sm.pfull[i], 4), mbar_init(&sm.qfull[i], NQ == 2 ? 4 : 8);
+      mbar_init(&sm.odone[i], 1), mbar_init(&sm.fin[i], 1), mbar_init(&sm.met[i], 4);
+      for (int x = 0; x < 4; ++x) mbar_init(&sm.turn[i][x], 1), mbar_init(&sm.swap[i][x], 1);
+    }
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
     sm.any_bad = 0;
   }
-  for (int i = tid; i < 3 * D; i += kThreads) (&sm.bad[0][0])[i] = INT32_MAX;
+  for (int i = tid; i < 3 * D; i += C::threads) (&sm.bad[0][0])[i] = INT32_MAX;
   griddep_wait();
   if (tid == 0) griddep_launch_dependents();
   const int ctas = gridDim.x, cta = blockIdx.x;
   if (cta == 0) check_cu(L, p.b);
   tc::fence_before_sync();
-  Run run = find_run<kThreads, M, TK>(p, cta, ctas, sm.run);
+  Run run = find_run<C::threads, M, TK>(p, cta, ctas, sm.run);
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tm = sm.tmem;
@@ -243,19 +247,21 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   Cut cut = {0, 0, 0, 0};
   Piece pc;
 
-  if (w < C::SW) {
+  if (w < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft));
     // ---------------------------------------------------------------- softmax
-    const int b = w >> 2, row = (w & 3) * 32 + ln;  // row block, row in it
-    const uint32_t lane = (uint32_t)((w & 3) * 32) << 16;
+    const int b = w >> 2, pair = w & 3, row = pair * 32 + ln;  // warpgroup; row of its row block
+    const int block = NQ == 2 ? b : 0;                         // row block
+    const uint32_t lane = (uint32_t)(pair * 32) << 16;
     const Workspace ws = workspace_at(p.ws, ctas, M);
     const float c = p.scale_log2;
     auto rows_of = [&](const Piece &q) {  // packed rows of the unit
       const int64_t r = (int64_t)q.s.n * p.group - (int64_t)q.block * M;
       return r < M ? (int)r : M;
     };
+    // two row blocks: this warpgroup's rows to shared memory; one: its half of every row to TMEM
     auto load_q = [&](const Piece &q) {
-      const int r = b * 128 + row;
+      const int r = block * 128 + row;
       const bool on = r < rows_of(q);
       const int64_t R = (int64_t)q.block * M + r;
       const uint4 *src = on ? (const uint4 *)((const uint16_t *)p.q + row_token(q.s, p.group, R) * p.q_stride +
@@ -264,14 +270,14 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const uint4 zero = make_uint4(0, 0, 0, 0);
       if constexpr (C::QT) {
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
+        for (int i = 0; i < D / 128; ++i) {
           uint32_t v[32];
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
-            const uint4 y = on ? src[i * 8 + x] : zero;
+            const uint4 y = on ? src[b * (D / 16) + i * 8 + x] : zero;
             v[4 * x] = y.x, v[4 * x + 1] = y.y, v[4 * x + 2] = y.z, v[4 * x + 3] = y.w;
           }
-          tc::tmem_st32(tm + lane + C::Q0 + 32 * i, v);
+          tc::tmem_st32(tm + lane + C::Q0 + b * (D / 4) + 32 * i, v);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -285,107 +291,116 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (ln == 0) mbar_arrive(&sm.qfull[b]);
+      if (ln == 0) mbar_arrive(&sm.qfull[block]);
     };
     bool have = next_piece<M, TK>(p, run, pc);
-    if (have && b * 128 < rows_of(pc)) load_q(pc);
+    if (have && block * 128 < rows_of(pc)) load_q(pc);
     uint32_t it = 0;     // tiles this row block has been through
     uint32_t slots = 0;  // ring slots of the pieces before this one, modulo 2 NS
-    uint32_t meets = 0, done = 0;
+    uint32_t meets = 0, done = 0, turns = 0;
     while (have && ok) {
       const int nt = pc.t1 - pc.t0, rows = rows_of(pc);
-      const bool mine = b * 128 < rows;
-      const int r = b * 128 + row;
+      const bool mine = block * 128 < rows;
+      const int r = block * 128 + row;
       const int64_t R = (int64_t)pc.block * M + r;
       const int32_t vis = r < rows ? visible(pc.s, (int32_t)(R / p.group), p.causal) : 0;
       const int32_t sure = visible(pc.s, (int32_t)((int64_t)pc.block * M / p.group), p.causal);
-      const int32_t full_to = C::NQ == 2 && b == 1 && mine
+      const int32_t full_to = NQ == 2 && b == 1 && mine
                                   ? visible(pc.s, (int32_t)(((int64_t)pc.block * M + 128) / p.group), p.causal)
                                   : sure;  // every row of this block sees positions below it
-      const bool rows_all = (b + 1) * 128 <= rows;
+      const bool rows_all = (block + 1) * 128 <= rows;
       float m = -INFINITY, l = 0.f;
       // does the piece reach positions that some row of the unit does not see
       const bool mixed = (pc.s.kv < (int64_t)pc.t1 * TK ? pc.s.kv : pc.t1 * TK) > sure;
       for (int j = 0; j < nt && mine; ++j, ++it) {
-        const int sb = NQ == 2 ? b : (int)(it & 1);
-        const uint32_t ph = NQ == 2 ? it : it >> 1;
-        const uint32_t sa = tm + lane + C::S0 + sb * C::SN;
+        if (NQ == 1 && (int)(it & 1) != b) continue;  // the other warpgroup's
+        const uint32_t sa = tm + lane + C::S0 + b * C::SN;
         const int32_t first = (pc.t0 + j) * TK;
-        if (!(ok = wait_warp(&sm.sfull[sb], ph, limit))) break;
+        if (!(ok = wait_warp(&sm.sfull[b], NQ == 2 ? it : it >> 1, limit))) break;
         tc::fence_after_sync();
         // a column is seen when first + column < vis
         const bool mask = first + TK > full_to || !rows_all;
         const int32_t seen = vis - first;
-        constexpr int HELD = TK == 64 ? 64 : 32;  // columns in registers at a time
-        uint32_t s[HELD], s2[HELD == 64 ? 1 : 32];
-        float top = -INFINITY;
-        // the next 32 columns are on their way while these are looked at
-        auto &sa32 = *reinterpret_cast<uint32_t(*)[32]>(&s[0]);
-        auto &sb32 = *reinterpret_cast<uint32_t(*)[32]>(HELD == 64 ? &s[HELD - 32] : &s2[0]);
-        tc::tmem_ld32(sa, sa32);
-        wait_ld(sa32);
+        constexpr int NC = TK / 32;                 // chunks of 32 columns
+        uint32_t s[C::hold ? NC : 2][32];
+        float top;
+        tc::tmem_ld32(sa, s[0]);
+        wait_ld(s[0]);
+        if constexpr (C::hold) {
 #pragma unroll
-        for (int x = 0; x < TK; x += 64) {
-          tc::tmem_ld32(sa + x + 32, sb32);
-          if (mask) hide(sa32, seen - x);
-          top = fmaxf(top, top_of(sa32));
-          wait_ld(sb32);
-          if (x + 64 < TK) tc::tmem_ld32(sa + x + 64, sa32);
-          if (mask) hide(sb32, seen - x - 32);
-          top = fmaxf(top, top_of(sb32));
-          if (x + 64 < TK) wait_ld(sa32);
+          for (int x = 1; x < NC; ++x) tc::tmem_ld32(sa + 32 * x, s[x]);
+          if (mask) hide(s[0], seen);
+          top = top_of(s[0]);
+#pragma unroll
+          for (int x = 1; x < NC; ++x) {
+            wait_ld(s[x]);
+            if (mask) hide(s[x], seen - 32 * x);
+            top = fmaxf(top, top_of(s[x]));
+          }
+        } else {  // twice through TMEM, the next chunk on its way while one is looked at
+          top = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < NC; ++x) {
+            if (x + 1 < NC) tc::tmem_ld32(sa + 32 * x + 32, s[(x + 1) & 1]);
+            if (mask) hide(s[x & 1], seen - 32 * x);
+            top = fmaxf(top, top_of(s[x & 1]));
+            if (x + 1 < NC) wait_ld(s[(x + 1) & 1]);
+          }
+          tc::tmem_ld32(sa, s[0]);
         }
         const float mt = top * c;  // c > 0
+        float old = m;             // the reference that l goes by
+        if (NQ == 1 && j > 0) {
+          if (!(ok = wait_warp(&sm.turn[b][pair], turns++, limit))) break;
+          m = sm.ref[row];
+        }
         if (__any_sync(0xffffffffu, mt > m + 8.f)) {  // also the first tile's (m is -inf)
           const float to = fmaxf(m, mt), f = ex2(m - (to == -INFINITY ? 0.f : to));
           m = to;
-          l *= f;
           if (j > 0) {
-            if (!(ok = wait_warp(&sm.odone[NQ == 2 ? b : 0], it - 1, limit))) break;
+            if (!(ok = wait_warp(&sm.odone[block], it - 1, limit))) break;
             tc::fence_after_sync();
-            const uint32_t oa = tm + lane + C::O0 + b * D;
+            const uint32_t oa = tm + lane + C::O0 + block * D;
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
               uint32_t o[32];
               tc::tmem_ld32(oa + x, o);
-              tc::tmem_wait_ld();
+              wait_ld(o);
 #pragma unroll
               for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
               tc::tmem_st32(oa + x, o);
             }
           }
+          if (NQ == 1) sm.ref[row] = m;
+        }
+        if (NQ == 1 && j + 1 < nt) {  // the other warpgroup's next tile goes by this reference
+          __syncwarp();
+          if (ln == 0) mbar_arrive(&sm.turn[b ^ 1][pair]);
         }
         const float ref = m == -INFINITY ? 0.f : m;
+        if (__any_sync(0xffffffffu, old != m)) l *= ex2(old - ref);
         const uint64_t c2 = two(c, c), r2 = two(-ref, -ref);
         uint64_t l2 = two(0.f, 0.f);
-        uint32_t q[16];
-        if constexpr (HELD == 64) {
-          weights<BF16>(sa32, c2, r2, l2, q);
-          tc::tmem_st16(sa, q);
-          weights<BF16>(sb32, c2, r2, l2, q);
-          tc::tmem_st16(sa + 16, q);
-        } else {
-          tc::tmem_ld32(sa, sa32);
-          wait_ld(sa32);
+        if constexpr (!C::hold) wait_ld(s[0]);
 #pragma unroll
-          for (int x = 0; x < TK; x += 64) {
-            tc::tmem_ld32(sa + x + 32, sb32);
-            if (mask) hide(sa32, seen - x);
-            weights<BF16>(sa32, c2, r2, l2, q);
-            wait_ld(sb32);
-            tc::tmem_st16(sa + x / 2, q);  // over columns that have been read
-            if (x + 64 < TK) tc::tmem_ld32(sa + x + 64, sa32);
-            if (mask) hide(sb32, seen - x - 32);
-            weights<BF16>(sb32, c2, r2, l2, q);
-            if (x + 64 < TK) wait_ld(sa32);
-            tc::tmem_st16(sa + x / 2 + 16, q);
+        for (int x = 0; x < NC; ++x) {
+          uint32_t q[16];
+          auto &sx = s[C::hold ? x : x & 1];
+          if constexpr (!C::hold) {
+            if (x + 1 < NC) tc::tmem_ld32(sa + 32 * x + 32, s[(x + 1) & 1]);
+            if (mask) hide(sx, seen - 32 * x);
           }
+          weights<BF16>(sx, c2, r2, l2, q);
+          if constexpr (!C::hold) {
+            if (x + 1 < NC) wait_ld(s[(x + 1) & 1]);
+          }
+          tc::tmem_st16(sa + 16 * x, q);  // over columns that have been read
         }
         const float2 lf = *reinterpret_cast<const float2 *>(&l2);
         l += lf.x + lf.y;
         const int32_t last = first + TK < pc.s.kv ? first + TK : pc.s.kv;
         if (last > sure) {  // positions [max(first, sure), last): some row of the unit does not see them
-          const uint32_t vi = slots + v_index<NQ>(j, nt);
+          const uint32_t vi = slots + 2 * j + 1;
           const int slot = (int)(vi % NS);
           if (!(ok = wait_warp(&sm.full[slot], vi / NS, limit))) break;
           const int lo = (sure > first ? sure : first) - first, cnt = last - first - lo;
@@ -418,18 +433,29 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (ln == 0) mbar_arrive(&sm.pfull[sb]);
+        if (ln == 0) mbar_arrive(&sm.pfull[b]);
       }
       if (!ok) break;
+      if (NQ == 1) {  // the warpgroups' sums of each row, by the later reference; then both know that Q has been used
+        sm.ml[done & 1][b][row] = make_float2(m, l);
+        __syncwarp();
+        if (ln == 0) mbar_arrive(&sm.swap[b ^ 1][pair]);
+        if (!(ok = wait_warp(&sm.swap[b][pair], done, limit))) break;
+        const float2 x = sm.ml[done & 1][b ^ 1][row];
+        const float to = fmaxf(m, x.x), ref = to == -INFINITY ? 0.f : to;
+        // in the same order in both
+        const float la = (b == 0 ? l : x.y) * ex2((b == 0 ? m : x.x) - ref), lb = (b == 0 ? x.y : l) * ex2((b == 0 ? x.x : m) - ref);
+        l = la + lb;
+        m = to;
+      }
       const Piece q = pc;
-      const bool ends_here = mine;
       cut = cut_of(run, q, cta);
       slots = (slots + 2 * (uint32_t)nt) % (2 * NS);
       have = next_piece<M, TK>(p, run, pc);
-      if (have && b * 128 < rows_of(pc)) load_q(pc);  // this piece's score products are done
-      if (ends_here) {
+      if (have && block * 128 < rows_of(pc)) load_q(pc);  // this piece's score products are done
+      if (mine) {
         // a barrier of its own: odone may be up to two phases behind here, and a parity tells two apart, not three
-        if (!(ok = wait_warp(&sm.fin[b], done++, limit))) break;
+        if (!(ok = wait_warp(&sm.fin[block], done++, limit))) break;
         tc::fence_after_sync();
         const bool whole = q.t0 == 0 && q.t1 == q.tiles;
         const bool empty = l == 0.f;
@@ -440,12 +466,13 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         const bool look = mixed && *(volatile int32_t *)&sm.any_bad != 0;
         uint16_t *out = (uint16_t *)p.out + t * p.out_stride + h * D;
         float *part = ws.o + slot * D;
-        const uint32_t oa = tm + lane + C::O0 + b * D;
+        const uint32_t oa = tm + lane + C::O0 + block * D;
+        constexpr int half = NQ == 1 ? D / 2 : D;  // one row block: each warpgroup writes half of a row
 #pragma unroll 1
-        for (int x = 0; x < D; x += 32) {
+        for (int x = NQ == 1 ? b * half : 0, end = x + half; x < end; x += 32) {
           uint32_t o[32];
           tc::tmem_ld32(oa + x, o);
-          tc::tmem_wait_ld();
+          wait_ld(o);
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
           if (look) {
@@ -474,7 +501,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           }
           __syncwarp();
         }
-        if (on) {
+        if (on && (NQ == 2 || b == 0)) {
           if (!whole) ws.ml[slot] = make_float2(m, l);
           else if (p.lse) p.lse[t * p.heads + h] = empty ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
         }
@@ -483,24 +510,22 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       if (mixed) {  // the next unit starts with a clean list: all softmax warps meet before and after it is cleared
         for (int round = 0; round < 2 && ok; ++round, ++meets) {
           if (round == 1 && *(volatile int32_t *)&sm.any_bad)
-            for (int i = b * 128 + row; i < 3 * D; i += M) (&sm.bad[0][0])[i] = INT32_MAX;
+            for (int i = tid; i < 3 * D; i += 256) (&sm.bad[0][0])[i] = INT32_MAX;
           __syncwarp();
           if (ln == 0) mbar_arrive(&sm.met[b]);
-          for (int x = 0; x < NQ && ok; ++x) ok = wait_warp(&sm.met[x], meets, limit);
+          for (int x = 0; x < 2 && ok; ++x) ok = wait_warp(&sm.met[x], meets, limit);
         }
       }
-      if (!ok) break;
     }
-  } else if (w < C::SW + C::PW) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::prod));
+  } else if (w < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma));
+  }
+  if ((!Q8 && (w == 9 || w == 10)) || (Q8 && w >= 12)) {
+    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::prod));
     // ---------------------------------------------------------------- producers
-    const int pw = w - C::SW;
-    constexpr int RPW = TK / C::PW;  // rows of a tile per warp
-    static_assert(RPW <= 32, "a lane finds at most one row");
-    Ring<NS> at_n, at_h;             // the next tile to issue, to hand on
-    int pending = 0;                 // issued with cp.async, not handed on yet
-    bool first = true;               // the ring's first turn: every slot is empty
-    int nt = 0, kj = 0, vj = 0;
+    const bool is_k = Q8 ? w < 14 : w == 9;
+    const uint8_t *base = is_k ? L.k : L.v;
+    Ring<NS> at(is_k ? 0 : 1);
     const int64_t row_bytes = (int64_t)L.heads * D * (Q8 ? 1 : 2);
     // Block i of the piece's sequence, 0 behind its last position; a bad one is recorded and read as block 0.
     auto load_block = [&](int32_t i) {
@@ -512,9 +537,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       }
       return blk;
     };
-    // Table entries [base, base + 64) of the piece in the lanes' registers, the second half fetched a window ahead: a
-    // lookup per tile would cost an L2 round trip, about a third of a tile's time (1000 of 3600 cycles measured).
-    // Tiles reach at most 17 entries past V's first one, so two halves of 32 do; smaller blocks look up directly.
+    // Table entries [base_i, base_i + 64) of the piece in the lanes' registers, the second half fetched a window ahead:
+    // a lookup per tile would cost an L2 round trip.  A tile reaches at most 16 entries; smaller blocks look up directly.
     const bool window = L.block_tokens >= 8;
     int32_t base_i = 0, near = 0, far = 0;
     auto block_of = [&](int32_t i) {  // converged; i may differ between lanes
@@ -523,160 +547,163 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const int32_t x = __shfl_sync(0xffffffffu, near, o & 31), y = __shfl_sync(0xffffffffu, far, o & 31);
       return o < 32 ? x : y;
     };
-    // Block and row of a tile's first position (K's and V's walk), stepped by a tile; a lane adds its own offset.
+    // Block and row of a tile's first position, stepped by a tile; a lane adds its own offset.
     const int32_t tk_q = TK / L.block_tokens, tk_r = TK - tk_q * L.block_tokens;
-    int32_t tq[2] = {0, 0}, tr[2] = {0, 0}, q0 = 0, r0 = 0;
-    auto offset = [&](int32_t oq, int32_t orr, int32_t &q, int32_t &r) {
-      q = q0 + oq;
-      r = r0 + orr;
-      if (r >= L.block_tokens) r -= L.block_tokens, ++q;
-    };
-    const int32_t my = pw * RPW + (ln < RPW ? ln : 0), my_q = my / L.block_tokens, my_r = my - my_q * L.block_tokens;
-    // the next tile of the run, in the order of v_index
-    auto next_tile = [&](bool &is_k, int &j) {
-      while (vj >= nt) {
-        if (!next_piece<M, TK>(p, run, pc)) return false;
-        nt = pc.t1 - pc.t0;
-        kj = vj = 0;
-        tq[0] = tq[1] = (int32_t)((int64_t)pc.t0 * TK / L.block_tokens);
-        tr[0] = tr[1] = (int32_t)((int64_t)pc.t0 * TK - (int64_t)tq[0] * L.block_tokens);
-        if (window) {
-          base_i = tq[0];
-          near = load_block(base_i + ln);
-          far = load_block(base_i + 32 + ln);
-        }
+    int32_t q0 = 0, r0 = 0;
+    auto start = [&]() {
+      q0 = (int32_t)((int64_t)pc.t0 * TK / L.block_tokens);
+      r0 = (int32_t)((int64_t)pc.t0 * TK - (int64_t)q0 * L.block_tokens);
+      if (window) {
+        base_i = q0;
+        near = load_block(base_i + ln);
+        far = load_block(base_i + 32 + ln);
       }
-      is_k = NQ == 2 ? kj == vj : kj < nt && kj <= vj + 1;
-      j = is_k ? kj++ : vj++;
-      q0 = is_k ? tq[0] : tq[1];
-      r0 = is_k ? tr[0] : tr[1];
-      int32_t nq = q0 + tk_q, nr = r0 + tk_r;
-      if (nr >= L.block_tokens) nr -= L.block_tokens, ++nq;
-      if (is_k) tq[0] = nq, tr[0] = nr;
-      else tq[1] = nq, tr[1] = nr;
-      if (window && !is_k && q0 - base_i >= 32) {
+    };
+    auto step = [&]() {
+      q0 += tk_q;
+      r0 += tk_r;
+      if (r0 >= L.block_tokens) r0 -= L.block_tokens, ++q0;
+      if (window && q0 - base_i >= 32) {
         base_i += 32;
         near = far;
         far = load_block(base_i + 32 + ln);
       }
-      return true;
     };
-    // lane i's row of this warp's RPW rows of tile j: its byte offset in a lane, -1 behind the last position
-    auto place = [&](int j, uint32_t *sb, bool is_k) {
-      const int32_t pos = (pc.t0 + j) * TK + my;
-      int32_t q, rr;
-      offset(my_q, my_r, q, rr);
+    // byte offset in a lane of the row of position `off` of tile j, (oq, orr) = off by blocks; -1 behind the last position
+    auto place = [&](int j, int32_t off, int32_t oq, int32_t orr, uint32_t *sb) {
+      int32_t q = q0 + oq, rr = r0 + orr;
+      if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
       const int64_t page = (int64_t)block_of(q) * L.page;
-      if (ln >= RPW || pos >= pc.s.kv) return (int64_t)-1;
-      if (Q8) *sb = __ldg((is_k ? L.k : L.v) + page + L.scale_off + (int64_t)rr * L.heads + pc.head);
+      if ((pc.t0 + j) * TK + off >= pc.s.kv) return (int64_t)-1;
+      if (Q8) *sb = __ldg(base + page + L.scale_off + (int64_t)rr * L.heads + pc.head);
       return page + (int64_t)rr * row_bytes + (int64_t)pc.head * D * (Q8 ? 1 : 2);
     };
-    auto hand_on = [&]() {
+    auto hand_on = [&](int slot) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (ln == 0) mbar_arrive(&sm.full[at_h.slot]);
-      at_h.step();
+      if (ln == 0) mbar_arrive(&sm.full[slot]);
     };
-    auto wait_empty = [&](const Ring<NS> &r) { return first || wait_warp(&sm.empty[r.slot], r.phase ^ 1, limit); };
-    auto issued = [&]() {
-      at_n.step();
-      if (at_n.slot == 0) first = false;
-    };
-    bool is_k;
-    int j;
+    // the ring's first turn passes at once: the phase before a fresh barrier's first one counts as complete
+    auto wait_empty = [&]() { return wait_warp(&sm.empty[at.slot], at.phase ^ 1, limit); };
     if constexpr (!Q8) {
-      constexpr int CPR = D / 8;                        // 16-byte chunks of a row
-      constexpr int RPI = 32 / CPR > 0 ? 32 / CPR : 1;  // rows per instruction
-      constexpr int LAG = NS - 3;                       // cp.async tiles in flight before the first is handed on
-      // TMA: a box of `box` rows and all columns when a block holds the tile, else of one column of 64 elements; the
-      // boxes go over the lanes of all producer warps.  box 0: cp.async alone.
+      constexpr int CPR = D / 8, RPI = 32 / CPR > 0 ? 32 / CPR : 1;  // 16-byte chunks of a row, rows an instruction
+      constexpr int LAG = (NS - 1) / 2;  // cp.async tiles in flight before the first is handed on
+      // TMA: a box of `box` rows and all columns when a block holds the tile, else of one column of 64 elements, a box a
+      // lane.  box 0: cp.async alone.
       const int box = p.box_rows, cols = box == TK ? D / 64 : 1, per = D / 64 / cols;
-      const int boxes = box > 0 ? TK / box * per : 0, bi = ln * C::PW + pw, bc = bi % per;
-      const int br = bi < boxes ? bi / per * box : 0, br_q = br / L.block_tokens, br_r = br - br_q * L.block_tokens;
-      const uint32_t bytes = (uint32_t)((boxes - pw + C::PW - 1) / C::PW) * box * cols * 128;  // this warp's share
-      while (ok && next_tile(is_k, j)) {
-        const int slot = at_n.slot;
-        uint8_t *dst = sm.ring[slot];
-        if (box > 0 && (int64_t)(pc.t0 + j + 1) * TK <= pc.s.kv) {
-          int32_t q, rr;
-          offset(br_q, br_r, q, rr);
-          const int32_t blk = block_of(q);
-          if (!(ok = wait_empty(at_n))) break;
-          if (ln == 0) {
-            if (bytes) mbar_arrive_expect_tx(&sm.full[slot], bytes);
-            else mbar_arrive(&sm.full[slot]);
+      const int boxes = box > 0 ? TK / box * per : 0, bc = ln % per, br = ln < boxes ? ln / per * box : 0;
+      const int br_q = br / L.block_tokens, br_r = br - br_q * L.block_tokens;
+      int pending = 0;
+      Ring<NS> at_h = at;  // the next tile to hand on
+      while (ok && next_piece<M, TK>(p, run, pc)) {
+        const int nt = pc.t1 - pc.t0;
+        start();
+        for (int j = 0; j < nt; ++j, at.step(), step()) {
+          uint8_t *dst = sm.ring[at.slot];
+          if (box > 0 && (int64_t)(pc.t0 + j + 1) * TK <= pc.s.kv) {
+            int32_t q = q0 + br_q, rr = r0 + br_r;
+            if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
+            const int32_t blk = block_of(q);
+            if (!(ok = wait_empty())) break;
+            if (ln == 0) mbar_arrive_expect_tx(&sm.full[at.slot], C::slot);
+            __syncwarp();
+            if (ln < boxes)
+              tma_load_5d(dst + bc * (TK * 128) + br * 128, &map, 0, rr, bc, pc.head, blk + (is_k ? 0 : L.num_blocks),
+                          &sm.full[at.slot]);
+            if (pending > 0) {  // cp.async tiles before this one
+              cp_async_wait<0>();
+              for (; pending > 0; --pending, at_h.step()) hand_on(at_h.slot);
+            }
+            at_h.step();
+            continue;
           }
-          __syncwarp();
-          if (bi < boxes)
-            tma_load_5d(dst + bc * (TK * 128) + br * 128, &map, 0, rr, bc, pc.head, blk + (is_k ? 0 : L.num_blocks),
-                        &sm.full[slot]);
-          if (pending > 0) {  // cp.async tiles before this one
-            cp_async_wait<0>();
-            for (; pending > 0; --pending) hand_on();
-          }
-          at_h.step();
-          issued();
-          continue;
-        }
-        const int64_t at = place(j, nullptr, is_k);
-        if (!(ok = wait_empty(at_n))) break;
-        const uint8_t *base = is_k ? L.k : L.v;
-        const int ch = ln % CPR;
+          int64_t row_at[TK / 32];
 #pragma unroll
-        for (int i = 0; i < RPW; i += RPI) {
-          const int rl = i + ln / CPR, r = pw * RPW + rl;
-          const int64_t a = __shfl_sync(0xffffffffu, at, rl);
-          cp_async16_or_zero(smem_u32(dst + (ch >> 3) * (TK * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                             base + (a < 0 ? 0 : a) + ch * 16, a >= 0);
-        }
-        cp_async_commit();
-        issued();
-        if (++pending > LAG) {
-          cp_async_wait<LAG>();
-          hand_on();
-          --pending;
+          for (int g = 0; g < TK / 32; ++g) {
+            const int32_t off = g * 32 + ln, oq = off / L.block_tokens;
+            row_at[g] = place(j, off, oq, off - oq * L.block_tokens, nullptr);
+          }
+          if (!(ok = wait_empty())) break;
+          const int ch = ln % CPR;
+#pragma unroll
+          for (int g = 0; g < TK / 32; ++g)
+#pragma unroll 4
+            for (int i = 0; i < 32; i += RPI) {
+              const int r = i + ln / CPR;
+              const int64_t a = __shfl_sync(0xffffffffu, row_at[g], r);
+              cp_async16_or_zero(smem_u32(dst + (ch >> 3) * (TK * 128) + (g * 32 + r) * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                                 base + (a < 0 ? 0 : a) + ch * 16, a >= 0);
+            }
+          cp_async_commit();
+          if (++pending > LAG) {
+            cp_async_wait<LAG>();
+            hand_on(at_h.slot);
+            at_h.step();
+            --pending;
+          }
         }
       }
       cp_async_wait<0>();
-      for (; ok && pending > 0; --pending) hand_on();
+      for (; ok && pending > 0; --pending, at_h.step()) hand_on(at_h.slot);
     } else {
-      // 16 codes (two chunks of the 16-bit row) a lane and instruction, through a ring of SD stages that belongs to the
-      // thread: what it copies with cp.async it converts itself, so the copies need no barrier
-      constexpr int SD = C::SD, LPR = D / 16, RPI = 32 / LPR, IT = RPW / RPI;
-      const int lc = ln % LPR, th = pw * 32 + ln;
-      uint32_t sb[SD];
+      // 16 codes (two chunks of the 16-bit row) a lane and pass, through SD stages that belong to the thread: what it
+      // copies with cp.async it converts itself, so the copies need no barrier
+      constexpr int SD = C::SD, LPR = D / 16, RPI = 32 / LPR, RPW = TK / 2, RG = RPW / 32;
+      const int lc = ln % LPR, th = tid - 384, r_first = (w & 1) * RPW;
+      int32_t oq[RG], orr[RG];
 #pragma unroll
-      for (int i = 0; i < SD; ++i) sb[i] = 127;
-      Ring<SD> st_in, st_out;
-      int left = 0;  // tiles fetched and not converted
+      for (int g = 0; g < RG; ++g) {
+        const int32_t off = r_first + g * 32 + ln;
+        oq[g] = off / L.block_tokens;
+        orr[g] = off - oq[g] * L.block_tokens;
+      }
+      uint32_t sb[SD][RG];
+      int nt = 0, j = 0, in = 0, out = 0, left = 0;  // stages to fill and to convert; tiles fetched and not converted
       auto fetch = [&]() {  // the run's next tile into its stage; an empty group when there is none
-        uint32_t byte = 127;
-        if (ok && next_tile(is_k, j)) {
-          const int64_t at = place(j, &byte, is_k);
-          const uint8_t *base = is_k ? L.k : L.v;
+        uint32_t byte[RG];
 #pragma unroll
-          for (int i = 0; i < IT; ++i) {
-            const int64_t a = __shfl_sync(0xffffffffu, at, i * RPI + ln / LPR);
-            cp_async16_or_zero(smem_u32(&sm.stage[st_in.slot][i][th]), base + (a < 0 ? 0 : a) + lc * 16, a >= 0);
+        for (int g = 0; g < RG; ++g) byte[g] = 127;
+        if (ok && (j < nt || next_piece<M, TK>(p, run, pc))) {
+          if (j >= nt) {
+            nt = pc.t1 - pc.t0;
+            j = 0;
+            start();
           }
-          st_in.step();
+          int64_t row_at[RG];
+#pragma unroll
+          for (int g = 0; g < RG; ++g) row_at[g] = place(j, r_first + g * 32 + ln, oq[g], orr[g], &byte[g]);
+#pragma unroll
+          for (int g = 0; g < RG; ++g)
+#pragma unroll 4
+            for (int i = 0; i < 32 / RPI; ++i) {
+              const int64_t a = __shfl_sync(0xffffffffu, row_at[g], i * RPI + ln / LPR);
+              cp_async16_or_zero(smem_u32(&sm.stage[in][g * (32 / RPI) + i][th]), base + (a < 0 ? 0 : a) + lc * 16, a >= 0);
+            }
+          if (++in == SD) in = 0;
           ++left;
+          ++j;
+          step();
         }
         cp_async_commit();
 #pragma unroll
-        for (int i = 0; i + 1 < SD; ++i) sb[i] = sb[i + 1];
-        sb[SD - 1] = byte;
+        for (int g = 0; g < RG; ++g) {
+#pragma unroll
+          for (int i = 0; i + 1 < SD; ++i) sb[i][g] = sb[i + 1][g];
+          sb[SD - 1][g] = byte[g];
+        }
       };
       for (int g = 0; g < SD; ++g) fetch();
-      for (; left > 0; --left) {
+      for (; left > 0; --left, at.step()) {
         cp_async_wait<SD - 1>();
-        if (!(ok = wait_empty(at_n))) break;
-        uint8_t *dst = sm.ring[at_n.slot];
+        if (!(ok = wait_empty())) break;
+        uint8_t *dst = sm.ring[at.slot];
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          const int rl = i * RPI + ln / LPR, r = pw * RPW + rl;
-          const float k = scale_of(__shfl_sync(0xffffffffu, sb[0], rl));
-          const uint4 code = sm.stage[st_out.slot][i][th];
+        for (int g = 0; g < RG; ++g)
+#pragma unroll 4
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int rl = i * RPI + ln / LPR, r = r_first + g * 32 + rl;
+          const float k = scale_of(__shfl_sync(0xffffffffu, sb[0][g], rl));
+          const uint4 code = sm.stage[out][g * (32 / RPI) + i][th];
           const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
           uint32_t o[8];
 #pragma unroll
@@ -690,28 +717,25 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           *(uint4 *)(row + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           *(uint4 *)(row + ((((ch & 7) + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        hand_on();
-        issued();
-        st_out.step();
+        hand_on(at.slot);
+        if (++out == SD) out = 0;
         fetch();
       }
       cp_async_wait<0>();
     }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma));
   }
-  if (w == C::SW + C::PW) {
+  if (w == 8) {
     // ---------------------------------------------------------------- products
     const bool lead = tc::elect_one();
     constexpr uint32_t iqk = idesc_f16(128, TK, BF16, false), ipv = idesc_f16(128, D, BF16, true);
-    Ring<NS> at;  // the next tile of the ring to wait for
+    Ring<NS> rk(0), rv(1);  // the next K and V tile to wait for
     uint32_t itb[2] = {0, 0}, pieces[2] = {0, 0};
     const uint32_t ring0 = smem_u32(sm.ring[0]), q0 = smem_u32(sm.q);
     auto wait = [&](uint64_t *bar, uint32_t phase) {
       if (ok) ok = wait_bar(bar, phase, limit);
       return ok;
     };
-    auto next_slot = [&](int &slot) {  // waits for the ring's next tile
+    auto next_slot = [&](Ring<NS> &at, int &slot) {  // waits for the ring's next K or V tile
       slot = at.slot;
       const bool r = wait(&sm.full[at.slot], at.phase);
       at.step();
@@ -720,24 +744,23 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     };
     auto scores = [&](int b, int sb, int slot) {  // S[sb] = Q[b] K^T
       if (lead) {
-        const uint32_t kb = ring0 + slot * C::slot, qb = q0 + b * 128 * D * 2;
+        const uint32_t kd = desc_lo(ring0 + slot * C::slot, 16), qd = desc_lo(q0 + b * 128 * D * 2, 16);
         const uint32_t d = tm + C::S0 + sb * C::SN;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint64_t bd = desc128(kb + (k >> 2) * (TK * 128) + (k & 3) * 32, 16, 1024);
-          if constexpr (C::QT) mma_ts16(d, tm + C::Q0 + k * 8, bd, iqk, k > 0);
-          else mma_ss16(d, desc128(qb + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024), bd, iqk, k > 0);
+          const uint32_t kk = kd + ((k >> 2) * (TK * 128) + (k & 3) * 32) / 16;
+          if constexpr (C::QT) mma_ts16(d, tm + C::Q0 + k * 8, kk, iqk, k > 0);
+          else mma_ss16(d, qd + ((k >> 2) * 16384 + (k & 3) * 32) / 16, kk, iqk, k > 0);
         }
         tc::mma_commit(&sm.sfull[sb]);
       }
     };
     auto values = [&](int b, int sb, int slot, bool fresh, bool last) {  // O[b] (+)= P[sb] V
       if (lead) {
-        const uint32_t vb = ring0 + slot * C::slot;
+        const uint32_t vd = desc_lo(ring0 + slot * C::slot, TK * 128);
 #pragma unroll
         for (int k = 0; k < TK / 16; ++k)
-          mma_ts16(tm + C::O0 + b * D, tm + C::S0 + sb * C::SN + k * 8, desc128(vb + k * 2048, TK * 128, 1024), ipv,
-                   !(fresh && k == 0));
+          mma_ts16(tm + C::O0 + b * D, tm + C::S0 + sb * C::SN + k * 8, vd + k * (2048 / 16), ipv, !(fresh && k == 0));
         tc::mma_commit(&sm.odone[b]);
         if (last) tc::mma_commit(&sm.fin[b]);
       }
@@ -752,19 +775,19 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const int nb = NQ == 2 && rows > 128 ? 2 : 1;
       for (int b = 0; b < nb; ++b)
         if (!wait(&sm.qfull[b], pieces[b]++)) break;
-      if (!ok || !next_slot(ks)) break;
+      if (!ok || !next_slot(rk, ks)) break;
       if constexpr (NQ == 2) {
         for (int b = 0; b < nb; ++b) scores(b, b, ks);
         release(ks);
         for (int j = 0; j < nt; ++j) {
-          if (!next_slot(vs)) break;
+          if (!next_slot(rv, vs)) break;
           for (int b = 0; b < nb; ++b) {
             if (!wait(&sm.pfull[b], itb[b]++)) break;
             tc::fence_after_sync();
             values(b, b, vs, j == 0, j == nt - 1);
             if (b == nb - 1) release(vs);
             if (j + 1 < nt) {
-              if (b == 0 && !next_slot(ks)) break;
+              if (b == 0 && !next_slot(rk, ks)) break;
               scores(b, b, ks);
               if (b == nb - 1) release(ks);
             }
@@ -777,11 +800,11 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         release(ks);
         for (int j = 0; j < nt; ++j, ++it) {
           if (j + 1 < nt) {
-            if (!next_slot(ks)) break;
+            if (!next_slot(rk, ks)) break;
             scores(0, (int)((it + 1) & 1), ks);
             release(ks);
           }
-          if (!next_slot(vs) || !wait(&sm.pfull[it & 1], it >> 1)) break;
+          if (!next_slot(rv, vs) || !wait(&sm.pfull[it & 1], it >> 1)) break;
           tc::fence_after_sync();
           values(0, (int)(it & 1), vs, j == 0, j == nt - 1);
           release(vs);
@@ -797,7 +820,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   if (tid == 0 && p.ws) workspace_at(p.ws, ctas, M).cut[cta] = cut;
   tc::fence_before_sync();
   __syncthreads();
-  if (w == C::SW + C::PW) {
+  if (w == 8) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tm, 512);
   }
@@ -810,7 +833,7 @@ cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStre
   const int smem = (int)sizeof(Smem<D, Q8>);
   const cudaError_t e = limit.ensure((const void *)k, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, plan.ctas, kThreads, smem, stream, p, p.map ? *p.map : CUtensorMap{});
+  return launch_pdl(k, plan.ctas, Conf<D, Q8>::threads, smem, stream, p, p.map ? *p.map : CUtensorMap{});
 }
 
 template <bool BF16, bool Q8>
