@@ -172,6 +172,17 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[32], uint64_t c, uin
   l = add2(l, add2(a[0], a[1]));
 }
 
+// Codes in the high bytes of two halves -> bf16 bits with the same sign, exponent field and mantissa, worth the codes
+// times 2^-120: the exponent bias of e4m3 is 7, of bf16 127, and a subnormal code becomes a subnormal bf16.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2_bits(uint32_t x) {
+  return ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Tiled TMA load of one box (this CTA's shared memory), completing on `bar`.
 __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
                                             uint64_t *bar) {
@@ -657,10 +668,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         oq[g] = off / L.block_tokens;
         orr[g] = off - oq[g] * L.block_tokens;
       }
-      uint32_t sb[SD][RG];
-      int nt = 0, j = 0, in = 0, out = 0, left = 0;  // stages to fill and to convert; tiles fetched and not converted
-      auto fetch = [&]() {  // the run's next tile into its stage; an empty group when there is none
-        uint32_t byte[RG];
+      uint32_t sb[SD][RG];  // scale bytes by stage; a load's result stays where it lands, so nothing waits for it early
+      int nt = 0, j = 0, left = 0;  // tiles fetched and not converted
+      auto fetch = [&](int st, uint32_t (&byte)[RG]) {  // the run's next tile into a stage; an empty group when there is none
 #pragma unroll
         for (int g = 0; g < RG; ++g) byte[g] = 127;
         if (ok && (j < nt || next_piece<M, TK>(p, run, pc))) {
@@ -672,54 +682,62 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           int64_t row_at[RG];
 #pragma unroll
           for (int g = 0; g < RG; ++g) row_at[g] = place(j, r_first + g * 32 + ln, oq[g], orr[g], &byte[g]);
+          const uint32_t stage = smem_u32(&sm.stage[st][0][th]);
 #pragma unroll
           for (int g = 0; g < RG; ++g)
-#pragma unroll 4
+#pragma unroll
             for (int i = 0; i < 32 / RPI; ++i) {
               const int64_t a = __shfl_sync(0xffffffffu, row_at[g], i * RPI + ln / LPR);
-              cp_async16_or_zero(smem_u32(&sm.stage[in][g * (32 / RPI) + i][th]), base + (a < 0 ? 0 : a) + lc * 16, a >= 0);
+              cp_async16_or_zero(stage + (g * (32 / RPI) + i) * 128 * 16, base + (a < 0 ? 0 : a) + lc * 16, a >= 0);
             }
-          if (++in == SD) in = 0;
           ++left;
           ++j;
           step();
         }
         cp_async_commit();
-#pragma unroll
-        for (int g = 0; g < RG; ++g) {
-#pragma unroll
-          for (int i = 0; i + 1 < SD; ++i) sb[i][g] = sb[i + 1][g];
-          sb[SD - 1][g] = byte[g];
-        }
       };
-      for (int g = 0; g < SD; ++g) fetch();
-      for (; left > 0; --left, at.step()) {
-        cp_async_wait<SD - 1>();
-        if (!(ok = wait_empty())) break;
-        uint8_t *dst = sm.ring[at.slot];
+      auto convert = [&](int st, const uint32_t (&byte)[RG], uint8_t *dst, const bool wide) {
 #pragma unroll
         for (int g = 0; g < RG; ++g)
 #pragma unroll 4
-        for (int i = 0; i < 32 / RPI; ++i) {
-          const int rl = i * RPI + ln / LPR, r = r_first + g * 32 + rl;
-          const float k = scale_of(__shfl_sync(0xffffffffu, sb[0][g], rl));
-          const uint4 code = sm.stage[out][g * (32 / RPI) + i][th];
-          const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
-          uint32_t o[8];
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int rl = i * RPI + ln / LPR, r = r_first + g * 32 + rl;
+            const uint32_t e = __shfl_sync(0xffffffffu, byte[g], rl);
+            // 2^(120 + e - 127) as two bf16; beyond bf16's range 2^120, and the rest in a second product (255: NaN)
+            const uint32_t k1 = wide && e > 134 ? 0x7b807b80u : (e + 120) * 0x00800080u;
+            const uint32_t k2 = e > 134 ? (e == 255 ? 0x7fc07fc0u : e * 0x00800080u) : 0x3f803f80u;
+            const uint4 code = sm.stage[st][g * (32 / RPI) + i][th];
+            const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+            uint32_t o[8];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 lo = e4m3x2_to_float2(cw[x] & 0xffffu), hi = e4m3x2_to_float2(cw[x] >> 16);
-            o[2 * x] = pack2(lo.x * k, lo.y * k, BF16);
-            o[2 * x + 1] = pack2(hi.x * k, hi.y * k, BF16);
+            for (int x = 0; x < 8; ++x) {
+              o[x] = mul_bf16x2(e4m3x2_to_bf16x2_bits(__byte_perm(cw[x >> 1], 0, x & 1 ? 0x3424 : 0x1404)), k1);
+              if (wide) o[x] = mul_bf16x2(o[x], k2);
+            }
+            const int ch = 2 * lc;
+            uint8_t *row = dst + (ch >> 3) * (TK * 128) + r * 128;
+            *(uint4 *)(row + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *(uint4 *)(row + ((((ch & 7) + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
-          const int ch = 2 * lc;
-          uint8_t *row = dst + (ch >> 3) * (TK * 128) + r * 128;
-          *(uint4 *)(row + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *(uint4 *)(row + ((((ch & 7) + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      };
+#pragma unroll
+      for (int st = 0; st < SD; ++st) fetch(st, sb[st]);
+      while (ok && left > 0) {
+#pragma unroll
+        for (int st = 0; st < SD; ++st) {
+          if (!ok || left == 0) break;
+          cp_async_wait<SD - 1>();
+          if (!(ok = wait_empty())) break;
+          uint32_t most = 0;
+#pragma unroll
+          for (int g = 0; g < RG; ++g) most = max(most, sb[st][g]);
+          if (__any_sync(0xffffffffu, most > 134)) convert(st, sb[st], sm.ring[at.slot], true);
+          else convert(st, sb[st], sm.ring[at.slot], false);
+          hand_on(at.slot);
+          --left;
+          at.step();
+          fetch(st, sb[st]);
         }
-        hand_on(at.slot);
-        if (++out == SD) out = 0;
-        fetch();
       }
       cp_async_wait<0>();
     }
