@@ -85,12 +85,14 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
 // swizzle, coordinates (element of a column, row of a block, column of 64
 // elements, kv head, block; V's blocks follow K's).  A box never leaves its
 // block: box_rows is the largest power of two that divides block_tokens, up to a
-// tile of positions, and a box of a whole tile takes all columns.  Without maps
+// tile of positions, and a box of a whole tile takes all columns.  E4M3: bytes,
+// not swizzled, (code, row, kv head, block), boxes of whole rows.  Without maps
 // (odd blocks, other types and sizes) that kernel copies rows itself.
 void make_maps(lsc_kv_pool *p) {
   const lsc_kv_pool_desc &d = p->d;
   const int D = d.head_dim;
-  if ((d.dtype != LSC_BF16 && d.dtype != LSC_F16) || (D != 64 && D != 128 && D != 256)) return;
+  if (d.dtype == LSC_F32 || (D != 64 && D != 128 && D != 256)) return;
+  const bool q8 = d.dtype == LSC_E4M3;
   int box = d.block_tokens & -d.block_tokens;
   if (box > (D == 256 ? 64 : 128)) box = D == 256 ? 64 : 128;
   if (box < 8) return;  // a swizzle pattern is 8 rows
@@ -111,16 +113,23 @@ void make_maps(lsc_kv_pool *p) {
     return;
   }
   const bool tile = box == (D == 256 ? 64 : 128);
-  const cuuint64_t dims[5] = {64, (cuuint64_t)d.block_tokens, (cuuint64_t)(D / 64), (cuuint64_t)d.num_kv_heads,
-                              2 * (cuuint64_t)d.num_blocks};
-  const cuuint64_t strides[4] = {(cuuint64_t)p->row_bytes, 128, (cuuint64_t)(D * p->es), (cuuint64_t)d.page_bytes};
+  const cuuint64_t blocks = 2 * (cuuint64_t)d.num_blocks, row = (cuuint64_t)p->row_bytes, page = (cuuint64_t)d.page_bytes;
+  const cuuint64_t dims[5] = {64, (cuuint64_t)d.block_tokens, (cuuint64_t)(D / 64), (cuuint64_t)d.num_kv_heads, blocks};
+  const cuuint64_t strides[4] = {row, 128, (cuuint64_t)(D * p->es), page};
   const cuuint32_t boxes[5] = {64, (cuuint32_t)box, tile ? (cuuint32_t)(D / 64) : 1, 1, 1}, ones[5] = {1, 1, 1, 1, 1};
-  for (int32_t l = 0; l < d.num_layers; ++l)
-    if (encode(&maps[l], d.dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
-               p->base + (int64_t)l * p->region_bytes, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t dims8[4] = {(cuuint64_t)D, (cuuint64_t)d.block_tokens, (cuuint64_t)d.num_kv_heads, blocks};
+  const cuuint64_t strides8[3] = {row, (cuuint64_t)D, page};
+  const cuuint32_t boxes8[4] = {(cuuint32_t)D, (cuuint32_t)box, 1, 1};
+  for (int32_t l = 0; l < d.num_layers; ++l) {
+    const CUtensorMapDataType type = q8                      ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : d.dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (encode(&maps[l], type, q8 ? 4 : 5, p->base + (int64_t)l * p->region_bytes, q8 ? dims8 : dims,
+               q8 ? strides8 : strides, q8 ? boxes8 : boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return;
+  }
   p->maps.swap(maps);
   p->box_rows = box;
 }

@@ -17,8 +17,8 @@
 //     as tiled TMA boxes of rows x 64 elements (x head_dim / 64 when a block holds
 //     the tile: then one box a tile; coordinates (element, row, column of 64, head,
 //     block) of the layer, element always 0); a tile that is not full, and other
-//     block sizes, with 16-byte cp.async.  E4M3 pools: two warps each, codes
-//     through a staging buffer of each thread, then bf16 with their scale
+//     block sizes, with 16-byte cp.async.  E4M3 pools: four warps each, codes
+//     the same two ways into a staging buffer, then bf16 with their scale
 //     (exact above bf16's smallest normal).  Rows behind the last position are
 //     zeros.
 // head_dim 64 and 128: two row blocks of 128, one per softmax warpgroup, each with
@@ -56,13 +56,13 @@ struct Conf {
   static constexpr int slot = TK * D * 2;       // bytes of a K or V tile
   static constexpr int NS = Q8 ? (D == 64 ? 6 : 4) : (D == 64 ? 8 : D == 128 ? 5 : 6);
   static constexpr int SD = D == 128 ? 1 : 2;   // E4M3: stages of codes
-  // warps: 0-7 softmax, 8 MMA, 16-bit pools 9 K and 10 V, E4M3 12-13 K and 14-15 V
-  static constexpr int threads = Q8 ? 512 : 384;
-  static constexpr int GW = Q8 ? 2 : 1;         // producer warps of a tile
+  // warps: 0-7 softmax, 8 MMA, 16-bit pools 9 K and 10 V, E4M3 12-15 K and 16-19 V
+  static constexpr int threads = Q8 ? 640 : 384;
+  static constexpr int GW = Q8 ? 4 : 1;         // producer warps of a tile
   static constexpr bool hold = !Q8 || TK == 64; // a thread keeps all scores of a tile in registers
   // registers a thread of a softmax warpgroup, the MMA's and E4M3's producers' keeps of those at launch
-  static constexpr int soft = Q8 ? 160 : 208, mma = Q8 ? 64 : 80, prod = 128;
-  static_assert(2 * soft + mma + (Q8 ? prod : 0) <= (Q8 ? 4 * 128 : 3 * 168), "more registers than the block has");
+  static constexpr int soft = Q8 ? 144 : 208, mma = Q8 ? 56 : 80, prod = 64;
+  static_assert(2 * soft + mma + (Q8 ? 2 * prod : 0) <= (Q8 ? 5 * 96 : 3 * 168), "more registers than the block has");
   // TMEM columns
   static constexpr int S0 = 0, SN = TK;         // S buffer b at S0 + b * SN; P in its first half
   static constexpr int Q0 = 128;                // QT only
@@ -74,9 +74,10 @@ struct Smem {
   using C = Conf<D, Q8>;
   alignas(1024) uint8_t ring[C::NS][C::slot];
   alignas(1024) uint8_t q[C::QT ? 16 : C::M * D * 2];
-  alignas(16) uint4 stage[Q8 ? C::SD : 1][Q8 ? C::TK * D / 16 / 64 : 1][Q8 ? 128 : 1];  // E4M3: codes by thread
+  alignas(128) uint8_t stage[2][Q8 ? C::SD : 1][Q8 ? C::TK * D : 16];  // E4M3: tiles of codes, K's and V's
   int32_t bad[3][D];      // first position whose v is NaN, +inf, -inf
   uint64_t full[C::NS], empty[C::NS], sfull[2], pfull[2], qfull[2], odone[2], fin[2], met[2], drain;
+  uint64_t ready[2][2], freed[2][2];  // E4M3: by K or V and stage
   uint64_t turn[2][4], swap[2][4];   // one row block: by warpgroup and warp
   float ref[C::NQ == 1 ? 128 : 1];   // a row's reference m
   float2 ml[2][2][C::NQ == 1 ? 128 : 1];  // (m, sum) by piece parity and warpgroup
@@ -193,6 +194,15 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, i
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // A bounded wait.  The first tries do without the clock: reading %globaltimer costs about a microsecond, several
 // tiles' worth of waits.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t phase, uint64_t limit) {
@@ -237,6 +247,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.sfull[i], 1), mbar_init(&sm.pfull[i], 4), mbar_init(&sm.qfull[i], NQ == 2 ? 4 : 8);
       mbar_init(&sm.odone[i], 1), mbar_init(&sm.fin[i], 1), mbar_init(&sm.met[i], 4);
+      for (int x = 0; x < 2; ++x) mbar_init(&sm.ready[i][x], 1), mbar_init(&sm.freed[i][x], C::GW);
       for (int x = 0; x < 4; ++x) mbar_init(&sm.turn[i][x], 1), mbar_init(&sm.swap[i][x], 1);
     }
     mbar_init(&sm.drain, 1);
@@ -532,9 +543,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma));
   }
   if ((!Q8 && (w == 9 || w == 10)) || (Q8 && w >= 12)) {
-    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::prod));
+    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::prod));
     // ---------------------------------------------------------------- producers
-    const bool is_k = Q8 ? w < 14 : w == 9;
+    const bool is_k = Q8 ? w < 16 : w == 9;
     const uint8_t *base = is_k ? L.k : L.v;
     Ring<NS> at(is_k ? 0 : 1);
     const int64_t row_bytes = (int64_t)L.heads * D * (Q8 ? 1 : 2);
@@ -605,6 +616,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const int boxes = box > 0 ? TK / box * per : 0, bc = ln % per, br = ln < boxes ? ln / per * box : 0;
       const int br_q = br / L.block_tokens, br_r = br - br_q * L.block_tokens;
       int pending = 0;
+      uint32_t flying = 0;  // slots that TMA has filled (low byte), in which phase last (the next byte)
       Ring<NS> at_h = at;  // the next tile to hand on
       while (ok && next_piece<M, TK>(p, run, pc)) {
         const int nt = pc.t1 - pc.t0;
@@ -621,6 +633,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
             if (ln < boxes)
               tma_load_5d(dst + bc * (TK * 128) + br * 128, &map, 0, rr, bc, pc.head, blk + (is_k ? 0 : L.num_blocks),
                           &sm.full[at.slot]);
+            flying = flying & ~(0x101u << at.slot) | (1u | at.phase << 8) << at.slot;
             if (pending > 0) {  // cp.async tiles before this one
               cp_async_wait<0>();
               for (; pending > 0; --pending, at_h.step()) hand_on(at_h.slot);
@@ -656,89 +669,107 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       }
       cp_async_wait<0>();
       for (; ok && pending > 0; --pending, at_h.step()) hand_on(at_h.slot);
+      if (!ok)  // a wait gave up: nothing may be in flight when the CTA leaves
+        for (int i = 0; i < NS; ++i)
+          if (flying >> i & 1) wait_warp(&sm.full[i], flying >> (8 + i), p.drain_limit_ns);
     } else {
-      // 16 codes (two chunks of the 16-bit row) a lane and pass, through SD stages that belong to the thread: what it
-      // copies with cp.async it converts itself, so the copies need no barrier
-      constexpr int SD = C::SD, LPR = D / 16, RPI = 32 / LPR, RPW = TK / 2, RG = RPW / 32;
-      const int lc = ln % LPR, th = tid - 384, r_first = (w & 1) * RPW;
-      int32_t oq[RG], orr[RG];
-#pragma unroll
-      for (int g = 0; g < RG; ++g) {
-        const int32_t off = r_first + g * 32 + ln;
-        oq[g] = off / L.block_tokens;
-        orr[g] = off - oq[g] * L.block_tokens;
-      }
-      uint32_t sb[SD][RG];  // scale bytes by stage; a load's result stays where it lands, so nothing waits for it early
+      // 16 codes (two chunks of the 16-bit row) a lane and pass, through SD stages of codes per kind.  A whole tile comes
+      // by TMA (the first warp of the four), another one with cp.async: each thread copies what it converts itself, so
+      // those copies need no barrier.
+      constexpr int SD = C::SD, LPR = D / 16, RPI = 32 / LPR, RPW = TK / 4, IT = RPW / RPI;
+      const int kind = is_k ? 0 : 1, gw = w & 3, lc = ln % LPR, r_first = gw * RPW;
+      const int32_t off = r_first + (ln < RPW ? ln : 0), oq = off / L.block_tokens, orr = off - oq * L.block_tokens;
+      const int box = p.box_rows, boxes = box > 0 ? TK / box : 0, br = ln < boxes ? ln * box : 0;
+      const int br_q = br / L.block_tokens, br_r = br - br_q * L.block_tokens;
+      uint32_t sb[SD], uses[SD];  // scale bytes by stage (a load's result stays where it lands, so nothing waits for it early)
+      bool tma[SD];
       int nt = 0, j = 0, left = 0;  // tiles fetched and not converted
-      auto fetch = [&](int st, uint32_t (&byte)[RG]) {  // the run's next tile into a stage; an empty group when there is none
 #pragma unroll
-        for (int g = 0; g < RG; ++g) byte[g] = 127;
+      for (int st = 0; st < SD; ++st) uses[st] = 0, tma[st] = false;
+      auto fetch = [&](int st) {  // the run's next tile into a stage; an empty cp.async group when there is none
+        sb[st] = 127;
         if (ok && (j < nt || next_piece<M, TK>(p, run, pc))) {
           if (j >= nt) {
             nt = pc.t1 - pc.t0;
             j = 0;
             start();
           }
-          int64_t row_at[RG];
-#pragma unroll
-          for (int g = 0; g < RG; ++g) row_at[g] = place(j, r_first + g * 32 + ln, oq[g], orr[g], &byte[g]);
-          const uint32_t stage = smem_u32(&sm.stage[st][0][th]);
-#pragma unroll
-          for (int g = 0; g < RG; ++g)
-#pragma unroll
-            for (int i = 0; i < 32 / RPI; ++i) {
-              const int64_t a = __shfl_sync(0xffffffffu, row_at[g], i * RPI + ln / LPR);
-              cp_async16_or_zero(stage + (g * (32 / RPI) + i) * 128 * 16, base + (a < 0 ? 0 : a) + lc * 16, a >= 0);
+          const int64_t row_at = place(j, off, oq, orr, &sb[st]);
+          tma[st] = box > 0 && (int64_t)(pc.t0 + j + 1) * TK <= pc.s.kv;
+          if (tma[st]) {
+            int32_t q = q0 + br_q, rr = r0 + br_r;
+            if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
+            const int32_t blk = block_of(q);
+            if (gw == 0) {  // all four warps have read the stage's last tile
+              ok = wait_warp(&sm.freed[kind][st], uses[st] ^ 1, limit);
+              if (ok && ln == 0) mbar_arrive_expect_tx(&sm.ready[kind][st], TK * D);
+              __syncwarp();
+              if (ok && ln < boxes)
+                tma_load_4d(&sm.stage[kind][st][br * D], &map, 0, rr, pc.head, blk + (is_k ? 0 : L.num_blocks),
+                            &sm.ready[kind][st]);
             }
+          } else {
+            if (gw == 0) {  // keeps in step with the stage's phases
+              ok = wait_warp(&sm.freed[kind][st], uses[st] ^ 1, limit);
+              if (ok && ln == 0) mbar_arrive(&sm.ready[kind][st]);
+            }
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+              const int rl = i * RPI + ln / LPR;
+              const int64_t a = __shfl_sync(0xffffffffu, row_at, rl);
+              cp_async16_or_zero(smem_u32(&sm.stage[kind][st][(r_first + rl) * D + lc * 16]), base + (a < 0 ? 0 : a) + lc * 16,
+                                 a >= 0);
+            }
+          }
           ++left;
           ++j;
           step();
         }
         cp_async_commit();
       };
-      auto convert = [&](int st, const uint32_t (&byte)[RG], uint8_t *dst, const bool wide) {
-#pragma unroll
-        for (int g = 0; g < RG; ++g)
+      auto convert = [&](int st, uint8_t *dst, const bool wide) {
 #pragma unroll 4
-          for (int i = 0; i < 32 / RPI; ++i) {
-            const int rl = i * RPI + ln / LPR, r = r_first + g * 32 + rl;
-            const uint32_t e = __shfl_sync(0xffffffffu, byte[g], rl);
-            // 2^(120 + e - 127) as two bf16; beyond bf16's range 2^120, and the rest in a second product (255: NaN)
-            const uint32_t k1 = wide && e > 134 ? 0x7b807b80u : (e + 120) * 0x00800080u;
-            const uint32_t k2 = e > 134 ? (e == 255 ? 0x7fc07fc0u : e * 0x00800080u) : 0x3f803f80u;
-            const uint4 code = sm.stage[st][g * (32 / RPI) + i][th];
-            const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
-            uint32_t o[8];
+        for (int i = 0; i < IT; ++i) {
+          const int rl = i * RPI + ln / LPR, r = r_first + rl;
+          const uint32_t e = __shfl_sync(0xffffffffu, sb[st], rl);
+          // 2^(120 + e - 127) as two bf16; beyond bf16's range 2^120, and the rest in a second product (255: NaN)
+          const uint32_t k1 = wide && e > 134 ? 0x7b807b80u : (e + 120) * 0x00800080u;
+          const uint32_t k2 = e > 134 ? (e == 255 ? 0x7fc07fc0u : e * 0x00800080u) : 0x3f803f80u;
+          const uint4 code = *(const uint4 *)&sm.stage[kind][st][r * D + lc * 16];
+          const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+          uint32_t o[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              o[x] = mul_bf16x2(e4m3x2_to_bf16x2_bits(__byte_perm(cw[x >> 1], 0, x & 1 ? 0x3424 : 0x1404)), k1);
-              if (wide) o[x] = mul_bf16x2(o[x], k2);
-            }
-            const int ch = 2 * lc;
-            uint8_t *row = dst + (ch >> 3) * (TK * 128) + r * 128;
-            *(uint4 *)(row + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *(uint4 *)(row + ((((ch & 7) + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          for (int x = 0; x < 8; ++x) {
+            o[x] = mul_bf16x2(e4m3x2_to_bf16x2_bits(__byte_perm(cw[x >> 1], 0, x & 1 ? 0x3424 : 0x1404)), k1);
+            if (wide) o[x] = mul_bf16x2(o[x], k2);
           }
+          const int ch = 2 * lc;
+          uint8_t *row = dst + (ch >> 3) * (TK * 128) + r * 128;
+          *(uint4 *)(row + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *(uint4 *)(row + ((((ch & 7) + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
       };
 #pragma unroll
-      for (int st = 0; st < SD; ++st) fetch(st, sb[st]);
+      for (int st = 0; st < SD; ++st) fetch(st);
       while (ok && left > 0) {
 #pragma unroll
         for (int st = 0; st < SD; ++st) {
           if (!ok || left == 0) break;
           cp_async_wait<SD - 1>();
-          if (!(ok = wait_empty())) break;
-          uint32_t most = 0;
-#pragma unroll
-          for (int g = 0; g < RG; ++g) most = max(most, sb[st][g]);
-          if (__any_sync(0xffffffffu, most > 134)) convert(st, sb[st], sm.ring[at.slot], true);
-          else convert(st, sb[st], sm.ring[at.slot], false);
+          if (!(ok = wait_warp(&sm.ready[kind][st], uses[st], limit)) || !(ok = wait_empty())) break;
+          if (__any_sync(0xffffffffu, sb[st] > 134)) convert(st, sm.ring[at.slot], true);
+          else convert(st, sm.ring[at.slot], false);
           hand_on(at.slot);
+          if (ln == 0) mbar_arrive(&sm.freed[kind][st]);
+          uses[st] ^= 1;
           --left;
           at.step();
-          fetch(st, sb[st]);
+          fetch(st);
         }
       }
+      if (!ok && gw == 0)  // a wait gave up: nothing may be in flight when the CTA leaves
+        for (int st = 0; st < SD; ++st)
+          if (tma[st]) wait_warp(&sm.ready[kind][st], uses[st], p.drain_limit_ns);
       cp_async_wait<0>();
     }
   }
