@@ -243,6 +243,21 @@ struct KvPlan {
 cudaError_t launch_kv_copy(const KvPlan &p, int num_sms, cudaStream_t stream);
 
 // ---- one step over a K/V layer's blocks --------------------------------------
+// n / d for 0 <= n < 2^31 by a multiplication: d = 2^s rounded up, mul = ceil(2^(31+s) / d), so mul d - 2^(31+s) < 2^s
+// and the quotient's error stays below 1 / d.  A division by a runtime value is some 40 instructions; kernels that run
+// for microseconds fetch each of them from L2 once.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __host__ void set(uint32_t by) {
+    uint32_t s = 0;
+    while ((1ull << s) < by) ++s;
+    d = by;
+    shift = 31 + s;
+    mul = (uint32_t)(((1ull << shift) + by - 1) / by);
+  }
+  __device__ __forceinline__ int32_t div(int32_t n) const { return (int32_t)(((uint64_t)(uint32_t)n * mul) >> shift); }
+};
+
 // One attention layer of a K/V pool.
 struct KvLayer {
   uint8_t *k, *v;       // block 0 of each lane
@@ -251,10 +266,12 @@ struct KvLayer {
   int32_t dtype;        // lsc_dtype
   int32_t scale_off;    // E4M3: page offset of the scale bytes
   int32_t *status;      // device error word
+  FastDiv by_block;     // by block_tokens
 };
 
 struct KvBatch {
   int32_t n_seq, total_tokens, max_blocks;
+  int32_t held;         // tokens that max_blocks blocks hold (at most 2^31 - 1)
   const int32_t *table, *cu, *kv;
 };
 
@@ -278,6 +295,7 @@ struct KvAttendParams {
   int32_t dtype;        // of q and out
   int32_t heads;        // q heads
   int32_t group;        // q heads per kv head
+  FastDiv by_group;
   int32_t causal;
   float scale_log2;     // scale * log2(e): the softmax runs in powers of two
   int32_t max_seq, max_kv;  // host bounds of the lengths

@@ -156,18 +156,21 @@ lsc::KvLayer layer_of(const lsc_kv_pool *p, int32_t layer) {
   L.dtype = p->d.dtype;
   L.scale_off = p->scale_off;
   L.status = p->status;
+  L.by_block.set((uint32_t)p->d.block_tokens);
   return L;
 }
 
 bool misaligned(const void *q, uintptr_t a) { return ((uintptr_t)q % a) != 0; }
 
 // The checks every step call shares; out receives the batch.
-int check_batch(const lsc_kv_batch &b, lsc::KvBatch *out) {
+int check_batch(const lsc_kv_pool *p, const lsc_kv_batch &b, lsc::KvBatch *out) {
   if (b.n_seq < 0 || b.total_tokens < 0 || b.max_blocks < 0 || b.reserved != 0) return LSC_ERR_INVALID_ARG;
   if (b.n_seq > 0 && (!b.cu_seqlens || !b.kv_lens || (b.max_blocks > 0 && !b.block_table))) return LSC_ERR_INVALID_ARG;
   if (misaligned(b.cu_seqlens, 4) || misaligned(b.kv_lens, 4) || misaligned(b.block_table, 4))
     return LSC_ERR_MISALIGNED;
-  *out = {b.n_seq, b.total_tokens, b.max_blocks, b.block_table, b.cu_seqlens, b.kv_lens};
+  const int64_t held = (int64_t)b.max_blocks * p->d.block_tokens;
+  *out = {b.n_seq, b.total_tokens, b.max_blocks, (int32_t)std::min<int64_t>(held, INT32_MAX),
+          b.block_table, b.cu_seqlens, b.kv_lens};
   return LSC_OK;
 }
 
@@ -175,7 +178,7 @@ int check_batch(const lsc_kv_batch &b, lsc::KvBatch *out) {
 int check_rows(const lsc_kv_pool *p, int32_t layer, const lsc_kv_batch &b, const void *k, const void *v, int32_t dtype,
                int32_t reserved, int64_t k_stride, int64_t v_stride, lsc::KvRowsParams *r) {
   if (layer < 0 || layer >= p->d.num_layers) return LSC_ERR_OUT_OF_RANGE;
-  const int rc = check_batch(b, &r->b);
+  const int rc = check_batch(p, b, &r->b);
   if (rc != LSC_OK) return rc;
   if (reserved != 0 || (dtype != LSC_F32 && dtype != LSC_BF16 && dtype != LSC_F16)) return LSC_ERR_INVALID_ARG;
   const int64_t row = (int64_t)p->d.num_kv_heads * p->d.head_dim;
@@ -195,7 +198,7 @@ int check_rows(const lsc_kv_pool *p, int32_t layer, const lsc_kv_batch &b, const
 int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, lsc::KvAttendParams *r) {
   if (!p || !a) return LSC_ERR_INVALID_ARG;
   if (layer < 0 || layer >= p->d.num_layers) return LSC_ERR_OUT_OF_RANGE;
-  const int rc = check_batch(a->batch, &r->b);
+  const int rc = check_batch(p, a->batch, &r->b);
   if (rc != LSC_OK) return rc;
   const int32_t H = p->d.num_kv_heads, D = p->d.head_dim;
   if (a->num_q_heads <= 0 || a->num_q_heads % H != 0) return LSC_ERR_INVALID_ARG;
@@ -221,8 +224,8 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
   r->causal = a->causal;
   r->scale_log2 = a->scale * 1.44269504088896341f;
   r->max_seq = a->max_seq_tokens ? a->max_seq_tokens : a->batch.total_tokens;
-  const int64_t held = (int64_t)a->batch.max_blocks * p->d.block_tokens;
-  r->max_kv = a->max_kv_tokens ? a->max_kv_tokens : (int32_t)std::min<int64_t>(held, INT32_MAX);
+  r->max_kv = a->max_kv_tokens ? std::min(a->max_kv_tokens, r->b.held) : r->b.held;
+  r->by_group.set((uint32_t)r->group);
   r->num_sms = p->num_sms;
   r->map = p->maps.empty() ? nullptr : &p->maps[layer];
   r->box_rows = p->box_rows;
@@ -244,7 +247,12 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   const bool q8 = r.L.dtype == LSC_E4M3;
   const bool types = r.dtype != LSC_F32 && (r.L.dtype == r.dtype || q8);
   if (!types || (D != 64 && D != 128 && D != 256) || (mis & 15) != 0) return kAny;
-  if ((int64_t)r.max_seq * r.group <= kRowsMost) {
+  // the tensor-core kernels count packed rows, positions and tiles in 31 bits
+  const int64_t rows = (int64_t)std::min(r.max_seq, r.b.total_tokens) * r.group;
+  const int64_t units = (int64_t)r.b.total_tokens * r.group / 16 + r.b.n_seq;
+  if (rows > INT32_MAX - 1024 || r.max_kv > INT32_MAX - 1024 || units * r.L.heads > INT32_MAX / (r.max_kv / 64 + 1))
+    return kAny;
+  if (rows <= kRowsMost) {
     *plan = lsc::plan_kv_attend_rows(r);
     return kRows;
   }

@@ -53,35 +53,37 @@ __host__ __device__ __forceinline__ Workspace workspace_at(uint8_t *ws, int ctas
   return w;
 }
 
+// Counts here are below 2^31 (the host sends larger calls to the CUDA cores).
+
 // Row blocks of M packed rows of a sequence.
 template <int M>
 __device__ __forceinline__ int32_t row_blocks(const Seq &s, int32_t group) {
-  return (int32_t)(((int64_t)s.n * group + M - 1) / M);
+  return (s.n * group + M - 1) / M;
 }
 
 // Tiles of one row block.
 template <int M, int TK>
-__device__ __forceinline__ int32_t block_tiles(const Seq &s, int32_t group, int32_t causal, int32_t block) {
-  int64_t last = (int64_t)(block + 1) * M - 1;
-  const int64_t rows = (int64_t)s.n * group;
-  if (last >= rows) last = rows - 1;
-  int32_t v = visible(s, (int32_t)(last / group), causal);
-  const int32_t t = (int32_t)(((int64_t)v + TK - 1) / TK);
+__device__ __forceinline__ int32_t block_tiles(const KvAttendParams &p, const Seq &s, int32_t block) {
+  const int32_t rows = s.n * p.group, last = (block + 1) * M < rows ? (block + 1) * M - 1 : rows - 1;
+  const int32_t t = (visible(s, p.by_group.div(last), p.causal) + TK - 1) / TK;
   return t < 1 ? 1 : t;
 }
 
+// Tiles of one kv head of a sequence.
 template <int M, int TK>
-__device__ __forceinline__ int64_t seq_tiles(const Seq &s, int32_t group, int32_t causal) {
-  const int32_t nb = row_blocks<M>(s, group);
-  if (!causal) return nb ? (int64_t)nb * block_tiles<M, TK>(s, group, causal, 0) : 0;
-  int64_t t = 0;
-  for (int32_t b = 0; b < nb; ++b) t += block_tiles<M, TK>(s, group, causal, b);
+__device__ __forceinline__ int32_t seq_tiles(const KvAttendParams &p, int32_t i) {
+  if (i >= p.b.n_seq) return 0;
+  const Seq s = attend_seq(p.L, p.b, i, p.max_seq, p.max_kv);
+  const int32_t nb = row_blocks<M>(s, p.group);
+  int32_t t = 0;
+#pragma unroll 1
+  for (int32_t b = 0; b < nb; ++b) t += block_tiles<M, TK>(p, s, b);
   return t;
 }
 
 // Where a CTA's run is: the walk over its pieces.
 struct Run {
-  int64_t pos, end, chunk;  // tile indexes in the order of all tiles; pos == end: done
+  int32_t pos, end, chunk;  // tile indexes in the order of all tiles; pos == end: done
   int32_t seq, head, block, tile;
 };
 
@@ -92,29 +94,23 @@ struct Piece {
 };
 
 struct RunScratch {
-  int64_t warp_sum[32];
-  int64_t total, before;
-  int32_t seq;
+  int32_t warp_sum[32];
+  int32_t total, before, seq;
 };
 
-// Sum over the block of x; every thread gets the total.  NT threads, all present.
+// Inclusive sum over the block of x, and the block's total.  NT threads, all present.
 template <int NT>
-__device__ __forceinline__ int64_t block_scan(int64_t x, RunScratch &sc, int64_t *inclusive) {
+__device__ __forceinline__ int32_t block_scan(int32_t x, RunScratch &sc, int32_t *inclusive) {
   const int ln = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (ln >= o) x += y;
   }
   if (ln == 31) sc.warp_sum[w] = x;
   __syncthreads();
-  int64_t before = 0, all = 0;
-#pragma unroll
-  for (int i = 0; i < NT / 32; ++i) {
-    const int64_t y = sc.warp_sum[i];
-    if (i < w) before += y;
-    all += y;
-  }
+  const int32_t ws = ln < NT / 32 ? sc.warp_sum[ln] : 0;
+  const int32_t before = __reduce_add_sync(0xffffffffu, ln < w ? ws : 0), all = __reduce_add_sync(0xffffffffu, ws);
   __syncthreads();
   *inclusive = before + x;
   return all;
@@ -124,58 +120,52 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, RunScratch &sc, int64_t
 template <int NT, int M, int TK>
 __device__ __forceinline__ Run find_run(const KvAttendParams &p, int cta, int ctas, RunScratch &sc) {
   const int H = p.L.heads;
-  int64_t total = 0, mine = 0, incl = 0;
+  int32_t total = 0, mine = 0, incl = 0;
+#pragma unroll 1
   for (int32_t i0 = 0; i0 < p.b.n_seq; i0 += NT) {
-    const int32_t i = i0 + threadIdx.x;
-    mine = i < p.b.n_seq
-               ? seq_tiles<M, TK>(attend_seq(p.L, p.b, i, p.max_seq, p.max_kv), p.group, p.causal)
-               : 0;
+    mine = seq_tiles<M, TK>(p, i0 + threadIdx.x);
     total += block_scan<NT>(mine, sc, &incl);
   }
   total *= H;
   Run r;
   r.chunk = (total + ctas - 1) / ctas;
   if (r.chunk < 1) r.chunk = 1;
-  r.pos = (int64_t)cta * r.chunk;
+  r.pos = cta * r.chunk;
   r.end = r.pos + r.chunk < total ? r.pos + r.chunk : total;
   r.seq = r.head = r.block = r.tile = 0;
   if (r.pos >= r.end) {
     r.pos = r.end;
     return r;
   }
-  int64_t base = 0;
+  int32_t base = 0;
+#pragma unroll 1
   for (int32_t i0 = 0; i0 < p.b.n_seq; i0 += NT) {
-    const int32_t i = i0 + threadIdx.x;
+    int32_t all = 0;
     if (p.b.n_seq > NT) {  // else the first pass left this thread's values
-      mine = i < p.b.n_seq
-                 ? seq_tiles<M, TK>(attend_seq(p.L, p.b, i, p.max_seq, p.max_kv), p.group, p.causal)
-                 : 0;
-      const int64_t all = block_scan<NT>(mine, sc, &incl);
-      if (mine > 0 && (base + incl - mine) * H <= r.pos && r.pos < (base + incl) * H) {
-        sc.seq = i;
-        sc.before = (base + incl - mine) * H;
-        sc.total = mine;
-      }
-      base += all;
-    } else if (mine > 0 && (incl - mine) * H <= r.pos && r.pos < incl * H) {
-      sc.seq = i;
-      sc.before = (incl - mine) * H;
+      mine = seq_tiles<M, TK>(p, i0 + threadIdx.x);
+      all = block_scan<NT>(mine, sc, &incl);
+    }
+    if (mine > 0 && (base + incl - mine) * H <= r.pos && r.pos < (base + incl) * H) {
+      sc.seq = i0 + threadIdx.x;
+      sc.before = (base + incl - mine) * H;
       sc.total = mine;
     }
+    base += all;
   }
   __syncthreads();
   r.seq = sc.seq;
-  const int64_t off = r.pos - sc.before;
-  r.head = (int32_t)(off / sc.total);
-  int64_t rem = off - (int64_t)r.head * sc.total;
+  int32_t rem = r.pos - sc.before;
+  r.head = rem / sc.total;
+  rem -= r.head * sc.total;
   const Seq s = attend_seq(p.L, p.b, r.seq, p.max_seq, p.max_kv);
+#pragma unroll 1
   for (;;) {
-    const int32_t t = block_tiles<M, TK>(s, p.group, p.causal, r.block);
+    const int32_t t = block_tiles<M, TK>(p, s, r.block);
     if (rem < t) break;
     rem -= t;
     ++r.block;
   }
-  r.tile = (int32_t)rem;
+  r.tile = rem;
   return r;
 }
 
@@ -184,9 +174,10 @@ template <int M, int TK>
 __device__ __forceinline__ bool next_piece(const KvAttendParams &p, Run &r, Piece &q) {
   if (r.pos >= r.end) return false;
   Seq s = attend_seq(p.L, p.b, r.seq, p.max_seq, p.max_kv);
+#pragma unroll 1
   while (r.block >= row_blocks<M>(s, p.group)) {  // past this head's blocks (or a sequence without new tokens)
     r.block = 0;
-    if (row_blocks<M>(s, p.group) == 0 || ++r.head == p.L.heads) {
+    if (s.n == 0 || ++r.head == p.L.heads) {
       r.head = 0;
       ++r.seq;
       s = attend_seq(p.L, p.b, r.seq, p.max_seq, p.max_kv);
@@ -196,10 +187,10 @@ __device__ __forceinline__ bool next_piece(const KvAttendParams &p, Run &r, Piec
   q.seq = r.seq;
   q.head = r.head;
   q.block = r.block;
-  q.tiles = block_tiles<M, TK>(s, p.group, p.causal, r.block);
+  q.tiles = block_tiles<M, TK>(p, s, r.block);
   q.t0 = r.tile;
-  const int64_t left = r.end - r.pos;
-  q.t1 = q.tiles - q.t0 <= left ? q.tiles : q.t0 + (int32_t)left;
+  const int32_t left = r.end - r.pos;
+  q.t1 = q.tiles - q.t0 <= left ? q.tiles : q.t0 + left;
   r.pos += q.t1 - q.t0;
   r.tile = 0;
   ++r.block;
@@ -209,12 +200,9 @@ __device__ __forceinline__ bool next_piece(const KvAttendParams &p, Run &r, Piec
 // The CTA's record, given its last piece (after next_piece moved past it).
 __device__ __forceinline__ Cut cut_of(const Run &r, const Piece &q, int cta) {
   Cut c = {q.seq, q.head, q.block, 0};
-  if (q.t0 == 0 && q.t1 < q.tiles) c.more = (int32_t)((r.pos + (q.tiles - q.t1) - 1) / r.chunk) - cta;
+  if (q.t0 == 0 && q.t1 < q.tiles) c.more = (r.pos + (q.tiles - q.t1) - 1) / r.chunk - cta;
   return c;
 }
-
-// Dense addresses of a packed row.
-__device__ __forceinline__ int64_t row_token(const Seq &s, int32_t group, int64_t R) { return s.row0 + R / group; }
 
 __device__ __forceinline__ uint32_t pack2(float x, float y, int bf16) {
   if (bf16) {

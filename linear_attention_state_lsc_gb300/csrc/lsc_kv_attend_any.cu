@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(const __grid_co
     const int32_t i = seq_of_row(p.b, t);
     if (i < 0) continue;  // the whole CTA
     const Seq s = attend_seq(L, p.b, i, p.max_seq, p.max_kv);
-    const int32_t vis = visible(s, t - s.row0, p.causal), kh = h / p.group;
+    const int32_t vis = visible(s, t - s.row0, p.causal), kh = p.by_group.div(h);
     const int32_t *table = p.b.table + (int64_t)i * p.b.max_blocks;
     float q[NE], o[NE], m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(const __grid_co
         vs[c] = 1.f;
         const int32_t j = j0 + c;
         if (j < vis) {
-          const int32_t blk = table[j / L.block_tokens], row = j - j / L.block_tokens * L.block_tokens;
+          const int32_t jb = L.by_block.div(j), blk = table[jb], row = j - jb * L.block_tokens;
           if (blk >= 0 && blk < L.num_blocks) {
             const uint8_t *page = L.k + (int64_t)blk * L.page;
             at[c] = (int64_t)blk * L.page;
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(const __grid_co
         if (at[c] < 0) continue;
         const float w = exp2f(sc[c] - ref);
         l += w;
-        const int32_t j = j0 + c, row = j - j / L.block_tokens * L.block_tokens;
+        const int32_t j = j0 + c, row = j - L.by_block.div(j) * L.block_tokens;
 #pragma unroll
         for (int e = 0; e < NE; ++e)
           if (ln + 32 * e < D)

@@ -278,20 +278,20 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     const Workspace ws = workspace_at(p.ws, ctas, M);
     const float c = p.scale_log2;
     auto rows_of = [&](const Piece &q) {  // packed rows of the unit
-      const int64_t r = (int64_t)q.s.n * p.group - (int64_t)q.block * M;
-      return r < M ? (int)r : M;
+      const int32_t r = q.s.n * p.group - q.block * M;
+      return r < M ? r : M;
     };
     // two row blocks: this warpgroup's rows to shared memory; one: its half of every row to TMEM
     auto load_q = [&](const Piece &q) {
       const int r = block * 128 + row;
       const bool on = r < rows_of(q);
-      const int64_t R = (int64_t)q.block * M + r;
-      const uint4 *src = on ? (const uint4 *)((const uint16_t *)p.q + row_token(q.s, p.group, R) * p.q_stride +
-                                              ((int64_t)q.head * p.group + R % p.group) * D)
+      const int32_t R = q.block * M + r, tok = p.by_group.div(R);
+      const uint4 *src = on ? (const uint4 *)((const uint16_t *)p.q + (int64_t)(q.s.row0 + tok) * p.q_stride +
+                                              (int64_t)(q.head * p.group + (R - tok * p.group)) * D)
                             : nullptr;
       const uint4 zero = make_uint4(0, 0, 0, 0);
       if constexpr (C::QT) {
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < D / 128; ++i) {
           uint32_t v[32];
 #pragma unroll
@@ -305,10 +305,13 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         tc::fence_before_sync();
       } else {
         uint8_t *dst = sm.q + b * 128 * D * 2 + row * 128;
+#pragma unroll 1
+        for (int i = 0; i < D / 8; i += 8) {  // small code: it runs once a piece
+          uint4 y[8];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 y = on ? src[i] : zero;
-          *(uint4 *)(dst + (i >> 3) * 16384 + (((i & 7) ^ (row & 7)) << 4)) = y;
+          for (int x = 0; x < 8; ++x) y[x] = on ? src[i + x] : zero;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) *(uint4 *)(dst + (i >> 3) * 16384 + ((x ^ (row & 7)) << 4)) = y[x];
         }
         fence_proxy_async_smem();
       }
@@ -324,16 +327,16 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const int nt = pc.t1 - pc.t0, rows = rows_of(pc);
       const bool mine = block * 128 < rows;
       const int r = block * 128 + row;
-      const int64_t R = (int64_t)pc.block * M + r;
-      const int32_t vis = r < rows ? visible(pc.s, (int32_t)(R / p.group), p.causal) : 0;
-      const int32_t sure = visible(pc.s, (int32_t)((int64_t)pc.block * M / p.group), p.causal);
+      const int32_t R = pc.block * M + r, tok = p.by_group.div(R);
+      const int32_t vis = r < rows ? visible(pc.s, tok, p.causal) : 0;
+      const int32_t sure = visible(pc.s, p.by_group.div(pc.block * M), p.causal);
       const int32_t full_to = NQ == 2 && b == 1 && mine
-                                  ? visible(pc.s, (int32_t)(((int64_t)pc.block * M + 128) / p.group), p.causal)
+                                  ? visible(pc.s, p.by_group.div(pc.block * M + 128), p.causal)
                                   : sure;  // every row of this block sees positions below it
       const bool rows_all = (block + 1) * 128 <= rows;
       float m = -INFINITY, l = 0.f;
       // does the piece reach positions that some row of the unit does not see
-      const bool mixed = (pc.s.kv < (int64_t)pc.t1 * TK ? pc.s.kv : pc.t1 * TK) > sure;
+      const bool mixed = (pc.s.kv < pc.t1 * TK ? pc.s.kv : pc.t1 * TK) > sure;
       for (int j = 0; j < nt && mine; ++j, ++it) {
         if (NQ == 1 && (int)(it & 1) != b) continue;  // the other warpgroup's
         const uint32_t sa = tm + lane + C::S0 + b * C::SN;
@@ -482,7 +485,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         const bool whole = q.t0 == 0 && q.t1 == q.tiles;
         const bool empty = l == 0.f;
         const float inv = whole ? (empty ? 0.f : 1.f / l) : 1.f;
-        const int64_t h = (int64_t)q.head * p.group + R % p.group, t = row_token(q.s, p.group, R);
+        const int64_t h = q.head * p.group + (R - tok * p.group), t = q.s.row0 + tok;
         const int64_t slot = (int64_t)(2 * cta + (q.t0 == 0 ? 1 : 0)) * M + r;
         const bool on = r < rows;
         const bool look = mixed && *(volatile int32_t *)&sm.any_bad != 0;
@@ -549,9 +552,10 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     const uint8_t *base = is_k ? L.k : L.v;
     Ring<NS> at(is_k ? 0 : 1);
     const int64_t row_bytes = (int64_t)L.heads * D * (Q8 ? 1 : 2);
+    int32_t blocks_held = 0;  // of the piece's sequence
     // Block i of the piece's sequence, 0 behind its last position; a bad one is recorded and read as block 0.
     auto load_block = [&](int32_t i) {
-      if ((int64_t)i * L.block_tokens >= pc.s.kv) return 0;
+      if (i >= blocks_held) return 0;
       int32_t blk = __ldg(p.b.table + (int64_t)pc.seq * p.b.max_blocks + i);
       if (blk < 0 || blk >= L.num_blocks) {
         report(L.status, LSC_ERR_OUT_OF_RANGE);
@@ -570,11 +574,12 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       return o < 32 ? x : y;
     };
     // Block and row of a tile's first position, stepped by a tile; a lane adds its own offset.
-    const int32_t tk_q = TK / L.block_tokens, tk_r = TK - tk_q * L.block_tokens;
+    const int32_t tk_q = L.by_block.div(TK), tk_r = TK - tk_q * L.block_tokens;
     int32_t q0 = 0, r0 = 0;
     auto start = [&]() {
-      q0 = (int32_t)((int64_t)pc.t0 * TK / L.block_tokens);
-      r0 = (int32_t)((int64_t)pc.t0 * TK - (int64_t)q0 * L.block_tokens);
+      blocks_held = L.by_block.div(pc.s.kv + L.block_tokens - 1);
+      q0 = L.by_block.div(pc.t0 * TK);
+      r0 = pc.t0 * TK - q0 * L.block_tokens;
       if (window) {
         base_i = q0;
         near = load_block(base_i + ln);
@@ -614,7 +619,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       // lane.  box 0: cp.async alone.
       const int box = p.box_rows, cols = box == TK ? D / 64 : 1, per = D / 64 / cols;
       const int boxes = box > 0 ? TK / box * per : 0, bc = ln % per, br = ln < boxes ? ln / per * box : 0;
-      const int br_q = br / L.block_tokens, br_r = br - br_q * L.block_tokens;
+      const int br_q = L.by_block.div(br), br_r = br - br_q * L.block_tokens;
       int pending = 0;
       uint32_t flying = 0;  // slots that TMA has filled (low byte), in which phase last (the next byte)
       Ring<NS> at_h = at;  // the next tile to hand on
@@ -623,7 +628,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         start();
         for (int j = 0; j < nt; ++j, at.step(), step()) {
           uint8_t *dst = sm.ring[at.slot];
-          if (box > 0 && (int64_t)(pc.t0 + j + 1) * TK <= pc.s.kv) {
+          if (box > 0 && (pc.t0 + j + 1) * TK <= pc.s.kv) {
             int32_t q = q0 + br_q, rr = r0 + br_r;
             if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
             const int32_t blk = block_of(q);
@@ -644,7 +649,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           int64_t row_at[TK / 32];
 #pragma unroll
           for (int g = 0; g < TK / 32; ++g) {
-            const int32_t off = g * 32 + ln, oq = off / L.block_tokens;
+            const int32_t off = g * 32 + ln, oq = L.by_block.div(off);
             row_at[g] = place(j, off, oq, off - oq * L.block_tokens, nullptr);
           }
           if (!(ok = wait_empty())) break;
@@ -678,9 +683,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       // those copies need no barrier.
       constexpr int SD = C::SD, LPR = D / 16, RPI = 32 / LPR, RPW = TK / 4, IT = RPW / RPI;
       const int kind = is_k ? 0 : 1, gw = w & 3, lc = ln % LPR, r_first = gw * RPW;
-      const int32_t off = r_first + (ln < RPW ? ln : 0), oq = off / L.block_tokens, orr = off - oq * L.block_tokens;
+      const int32_t off = r_first + (ln < RPW ? ln : 0), oq = L.by_block.div(off), orr = off - oq * L.block_tokens;
       const int box = p.box_rows, boxes = box > 0 ? TK / box : 0, br = ln < boxes ? ln * box : 0;
-      const int br_q = br / L.block_tokens, br_r = br - br_q * L.block_tokens;
+      const int br_q = L.by_block.div(br), br_r = br - br_q * L.block_tokens;
       uint32_t sb[SD], uses[SD];  // scale bytes by stage (a load's result stays where it lands, so nothing waits for it early)
       bool tma[SD];
       int nt = 0, j = 0, left = 0;  // tiles fetched and not converted
@@ -695,7 +700,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
             start();
           }
           const int64_t row_at = place(j, off, oq, orr, &sb[st]);
-          tma[st] = box > 0 && (int64_t)(pc.t0 + j + 1) * TK <= pc.s.kv;
+          tma[st] = box > 0 && (pc.t0 + j + 1) * TK <= pc.s.kv;
           if (tma[st]) {
             int32_t q = q0 + br_q, rr = r0 + br_r;
             if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
@@ -820,7 +825,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     int ks, vs;
     while (ok && next_piece<M, TK>(p, run, pc)) {
       const int nt = pc.t1 - pc.t0;
-      const int64_t rows = (int64_t)pc.s.n * p.group - (int64_t)pc.block * M;
+      const int32_t rows = pc.s.n * p.group - pc.block * M;
       const int nb = NQ == 2 && rows > 128 ? 2 : 1;
       for (int b = 0; b < nb; ++b)
         if (!wait(&sm.qfull[b], pieces[b]++)) break;

@@ -32,8 +32,8 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
   if (cut.more == 0) return;
   const int32_t c0 = p.b.cu[cut.seq], n = p.b.cu[cut.seq + 1] - c0;
   const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  const int64_t R = (int64_t)cut.block * M + r;
-  if (r >= M || R >= (int64_t)n * p.group) return;
+  const int32_t R = cut.block * M + r;
+  if (r >= M || R >= n * p.group) return;
   auto part = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
   float m = -INFINITY;
   for (int i = ln; i <= cut.more; i += 32) m = fmaxf(m, w.ml[(int64_t)part(i) * M + r].x);
@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
   }
   const bool empty = l == 0.f;
   const float inv = empty ? 0.f : 1.f / l;
-  const int64_t t = c0 + R / p.group, h = (int64_t)cut.head * p.group + R % p.group;
+  const int32_t tok = p.by_group.div(R);
+  const int64_t t = c0 + tok, h = (int64_t)cut.head * p.group + (R - tok * p.group);
   uint2 *dst = (uint2 *)((uint16_t *)p.out + t * p.out_stride + h * D);
   const int bf16 = p.dtype == LSC_BF16;
 #pragma unroll

@@ -133,7 +133,7 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
     auto place = [&](int tile, int i) -> int64_t {
       const int32_t key = (pc.t0 + tile) * kTK + i;
       if (tile >= nt || key >= kv) return -1;
-      const int32_t b = key / L.block_tokens;
+      const int32_t b = L.by_block.div(key);
       int32_t blk = table[b];
       if (blk < 0 || blk >= L.num_blocks) {
         report(L.status, LSC_ERR_OUT_OF_RANGE);
@@ -163,7 +163,7 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
       const int key = tid & (kTK - 1);
       const int32_t pos = (pc.t0 + tile) * kTK + key;
       if (pos >= kv) return 127;
-      const int32_t b = pos / L.block_tokens;
+      const int32_t b = L.by_block.div(pos);
       const int32_t blk = table[b];
       if (blk < 0 || blk >= L.num_blocks) return 127;
       const uint8_t *lane = (tid < kTK ? L.k : L.v) + (int64_t)blk * L.page + L.scale_off;
@@ -177,7 +177,7 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
     if (tid < kTK)
 #pragma unroll
       for (int s = 0; s < ST - 1; ++s) sm.at[s][tid] = place(s, tid);
-    if (tid < M) sm.vis[tid] = tid < R ? visible(pc.s, tid / p.group, p.causal) : 0;
+    if (tid < M) sm.vis[tid] = tid < R ? visible(pc.s, p.by_group.div(tid), p.causal) : 0;
     if (!Q8)
       for (int i = tid; i < 3 * D; i += kThreads) (&sm.bad[0][0])[i] = INT32_MAX;
     // q: rows of 16-bit elements, for E4M3 as f16 times a power of two and with the elements of each group of 16 in
@@ -185,8 +185,9 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
     uint16_t *sq = MT == 1 ? (uint16_t *)sm.ring[ST - 1] : &sm.q[0][0];
     constexpr int QS = D + 8;
     for (int r = w; r < M; r += kThreads / 32) {
-      const uint16_t *src = (const uint16_t *)p.q + (int64_t)(pc.s.row0 + r / p.group) * p.q_stride +
-                            (int64_t)(pc.head * p.group + r % p.group) * D;
+      const int32_t tok = p.by_group.div(r);
+      const uint16_t *src = (const uint16_t *)p.q + (int64_t)(pc.s.row0 + tok) * p.q_stride +
+                            (int64_t)(pc.head * p.group + (r - tok * p.group)) * D;
       if constexpr (!Q8) {
         for (int c = ln; c < D / 8; c += 32)
           *(uint4 *)(sq + r * QS + c * 8) = r < R ? *(const uint4 *)(src + c * 8) : make_uint4(0, 0, 0, 0);
@@ -421,7 +422,8 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
         for (int x = 0; x < 8; ++x) sum += sm.part[x][r];
         const bool empty = sum == 0.f;
         const float inv = whole ? (empty ? 0.f : 1.f / sum) : 1.f;
-        const int64_t t = pc.s.row0 + r / p.group, hd = (int64_t)pc.head * p.group + r % p.group;
+        const int32_t tok = p.by_group.div(r);
+        const int64_t t = pc.s.row0 + tok, hd = (int64_t)pc.head * p.group + (r - tok * p.group);
         if (w == 0 && tq == 0) {
           if (!whole) ws.ml[slot + r] = make_float2(m[i][h], sum);
           else if (p.lse) p.lse[t * p.heads + hd] = empty ? -INFINITY : (m[i][h] + log2f(sum)) * 0.693147180559945309f;

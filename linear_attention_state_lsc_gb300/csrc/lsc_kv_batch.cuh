@@ -12,14 +12,14 @@
 namespace lsc {
 namespace kv {
 
-__device__ __forceinline__ void report(int32_t *status, int32_t code) {
+static __device__ __noinline__ void report(int32_t *status, int32_t code) {
   if (status) atomicCAS(status, 0, code);
 }
 
 // A sequence's lengths as the kernels use them: kv outside what its table holds
 // counts as an empty cache (and is recorded).
 __device__ __forceinline__ int32_t checked_kv(const KvLayer &L, const KvBatch &b, int32_t kv) {
-  if (kv < 0 || (int64_t)kv > (int64_t)b.max_blocks * L.block_tokens) {
+  if ((uint32_t)kv > (uint32_t)b.held) {
     report(L.status, LSC_ERR_INVALID_ARG);
     return 0;
   }
@@ -38,20 +38,22 @@ __device__ __forceinline__ int32_t seq_of_row(const KvBatch &b, int32_t t) {
 }
 
 // A sequence as attend sees it: its first dense row, its new tokens and its
-// cached tokens (none when a length is outside the host's bounds).
+// cached tokens.  Lengths outside the host's bounds are recorded: too many
+// cached tokens count as none, too many new ones as none.
 struct Seq {
   int32_t row0, n, kv;
 };
 __device__ __forceinline__ Seq attend_seq(const KvLayer &L, const KvBatch &b, int32_t i, int32_t max_seq,
                                           int32_t max_kv) {
   Seq s;
-  const int32_t c0 = b.cu[i], c1 = b.cu[i + 1];
+  const int32_t c0 = b.cu[i], c1 = b.cu[i + 1], kv = b.kv[i];
   s.row0 = c0;
   s.n = c0 >= 0 && c1 >= c0 && c1 <= b.total_tokens ? c1 - c0 : 0;  // else: recorded by check_cu
-  s.kv = checked_kv(L, b, b.kv[i]);
-  if (s.n > max_seq || s.kv > max_kv) {
+  s.kv = kv;
+  if ((uint32_t)kv > (uint32_t)max_kv || s.n > max_seq) {
     report(L.status, LSC_ERR_INVALID_ARG);
-    s.kv = 0;
+    if ((uint32_t)kv > (uint32_t)max_kv) s.kv = 0;
+    if (s.n > max_seq) s.n = 0;
   }
   return s;
 }

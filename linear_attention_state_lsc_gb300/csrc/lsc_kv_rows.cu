@@ -71,7 +71,7 @@ __device__ __forceinline__ void find_places(const KvLayer &L, const KvBatch &b, 
           const int32_t kv = checked_kv(L, b, b.kv[a]);
           const int64_t pos = (int64_t)kv - ((int64_t)c1 - c0) + (t - c0);
           if (pos >= 0) {
-            const int32_t q = (int32_t)pos / L.block_tokens;
+            const int32_t q = L.by_block.div((int32_t)pos);
             const int32_t blk = b.table[a * b.max_blocks + q];
             if (blk >= 0 && blk < L.num_blocks) {
               row = (int32_t)pos - q * L.block_tokens;
