@@ -54,7 +54,7 @@ struct Conf {
   static constexpr int TK = D == 256 ? 64 : 128;
   static constexpr bool QT = D == 256;          // Q in TMEM
   static constexpr int slot = TK * D * 2;       // bytes of a K or V tile
-  static constexpr int NS = Q8 ? (D == 64 ? 6 : 4) : (D == 64 ? 8 : D == 128 ? 5 : 6);
+  static constexpr int NS = Q8 ? (D == 64 ? 6 : D == 128 ? 3 : 4) : (D == 64 ? 8 : D == 128 ? 4 : 6);
   static constexpr int SD = D == 128 ? 1 : 2;   // E4M3: stages of codes
   // warps: 0-7 softmax, 8 MMA, 16-bit pools 9 K and 10 V, E4M3 12-15 K and 16-19 V
   static constexpr int threads = Q8 ? 640 : 384;
@@ -75,6 +75,7 @@ struct Smem {
   alignas(1024) uint8_t ring[C::NS][C::slot];
   alignas(1024) uint8_t q[C::QT ? 16 : C::M * D * 2];
   alignas(128) uint8_t stage[2][Q8 ? C::SD : 1][Q8 ? C::TK * D : 16];  // E4M3: tiles of codes, K's and V's
+  alignas(16) uint8_t rows[8][32][80];  // by softmax warp: 64 bytes of each of its rows, between TMEM and memory
   int32_t bad[3][D];      // first position whose v is NaN, +inf, -inf
   uint64_t full[C::NS], empty[C::NS], sfull[2], pfull[2], qfull[2], odone[2], fin[2], met[2], drain;
   uint64_t ready[2][2], freed[2][2];  // E4M3: by K or V and stage
@@ -281,38 +282,52 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const int32_t r = q.s.n * p.group - q.block * M;
       return r < M ? r : M;
     };
+    // Rows of Q and of the result move 64 bytes a row and 8 rows an instruction: a lane a row would touch 32 sectors
+    // with 16 bytes each (8000 cycles for a unit's rows, measured on short chunks).
+    uint8_t(&mine_rows)[32][80] = sm.rows[w];
+    const int oct = ln >> 2, part16 = (ln & 3) * 16;
     // two row blocks: this warpgroup's rows to shared memory; one: its half of every row to TMEM
     auto load_q = [&](const Piece &q) {
       const int r = block * 128 + row;
-      const bool on = r < rows_of(q);
       const int32_t R = q.block * M + r, tok = p.by_group.div(R);
-      const uint4 *src = on ? (const uint4 *)((const uint16_t *)p.q + (int64_t)(q.s.row0 + tok) * p.q_stride +
-                                              (int64_t)(q.head * p.group + (R - tok * p.group)) * D)
-                            : nullptr;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      if constexpr (C::QT) {
-#pragma unroll 1
-        for (int i = 0; i < D / 128; ++i) {
-          uint32_t v[32];
+      const uint8_t *src = r < rows_of(q) ? (const uint8_t *)p.q + 2 * ((int64_t)(q.s.row0 + tok) * p.q_stride +
+                                                                        (int64_t)(q.head * p.group + (R - tok * p.group)) * D)
+                                          : nullptr;
+      if (C::QT && src) src += b * D;
+      const uint8_t *from[4];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const uint4 y = on ? src[b * (D / 16) + i * 8 + x] : zero;
-            v[4 * x] = y.x, v[4 * x + 1] = y.y, v[4 * x + 2] = y.z, v[4 * x + 3] = y.w;
+      for (int i = 0; i < 4; ++i) from[i] = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)src, i * 8 + oct);
+#pragma unroll 2
+      for (int x = 0; x < (C::QT ? D : 2 * D); x += 64) {  // bytes of a row
+        uint4 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          y[i] = from[i] ? *(const uint4 *)(from[i] + x + part16) : make_uint4(0, 0, 0, 0);
+        if constexpr (C::QT) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *(uint4 *)&mine_rows[i * 8 + oct][part16] = y[i];
+          __syncwarp();
+          uint32_t v[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 z = *(const uint4 *)&mine_rows[ln][i * 16];
+            v[4 * i] = z.x, v[4 * i + 1] = z.y, v[4 * i + 2] = z.z, v[4 * i + 3] = z.w;
           }
-          tc::tmem_st32(tm + lane + C::Q0 + b * (D / 4) + 32 * i, v);
+          tc::tmem_st16(tm + lane + C::Q0 + b * (D / 4) + x / 4, v);
+        } else {
+          uint8_t *dst = sm.q + b * 128 * D * 2 + (x >> 7) * 16384;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = pair * 32 + i * 8 + oct, ch = ((x >> 4) & 4) + (ln & 3);
+            *(uint4 *)(dst + rr * 128 + ((ch ^ (rr & 7)) << 4)) = y[i];
+          }
         }
+      }
+      if constexpr (C::QT) {
         tc::tmem_wait_st();
         tc::fence_before_sync();
       } else {
-        uint8_t *dst = sm.q + b * 128 * D * 2 + row * 128;
-#pragma unroll 1
-        for (int i = 0; i < D / 8; i += 8) {  // small code: it runs once a piece
-          uint4 y[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) y[x] = on ? src[i + x] : zero;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) *(uint4 *)(dst + (i >> 3) * 16384 + ((x ^ (row & 7)) << 4)) = y[x];
-        }
         fence_proxy_async_smem();
       }
       __syncwarp();
@@ -489,8 +504,10 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         const int64_t slot = (int64_t)(2 * cta + (q.t0 == 0 ? 1 : 0)) * M + r;
         const bool on = r < rows;
         const bool look = mixed && *(volatile int32_t *)&sm.any_bad != 0;
-        uint16_t *out = (uint16_t *)p.out + t * p.out_stride + h * D;
-        float *part = ws.o + slot * D;
+        uint8_t *dst = !on ? nullptr : whole ? (uint8_t *)((uint16_t *)p.out + t * p.out_stride + h * D) : (uint8_t *)(ws.o + slot * D);
+        uint8_t *to[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = (uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)dst, i * 8 + oct);
         const uint32_t oa = tm + lane + C::O0 + block * D;
         constexpr int half = NQ == 1 ? D / 2 : D;  // one row block: each warpgroup writes half of a row
 #pragma unroll 1
@@ -510,19 +527,28 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
               o[y] = __float_as_uint(v);
             }
           }
-          if (on && whole) {
+          auto rows_out = [&](const uint32_t (&v)[16], int at) {  // 64 bytes of every row
+            __syncwarp();
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) {
-              uint4 v;
-              v.x = pack2(__uint_as_float(o[y]), __uint_as_float(o[y + 1]), BF16);
-              v.y = pack2(__uint_as_float(o[y + 2]), __uint_as_float(o[y + 3]), BF16);
-              v.z = pack2(__uint_as_float(o[y + 4]), __uint_as_float(o[y + 5]), BF16);
-              v.w = pack2(__uint_as_float(o[y + 6]), __uint_as_float(o[y + 7]), BF16);
-              *(uint4 *)(out + x + y) = v;
-            }
-          } else if (on) {
+            for (int i = 0; i < 4; ++i)
+              *(uint4 *)&mine_rows[ln][i * 16] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            __syncwarp();
 #pragma unroll
-            for (int y = 0; y < 32; y += 4) *(uint4 *)(part + x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            for (int i = 0; i < 4; ++i)
+              if (to[i]) *(uint4 *)(to[i] + at + part16) = *(const uint4 *)&mine_rows[i * 8 + oct][part16];
+          };
+          uint32_t v[16];
+          if (whole) {
+#pragma unroll
+            for (int y = 0; y < 16; ++y) v[y] = pack2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]), BF16);
+            rows_out(v, x * 2);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 16; ++y) v[y] = o[y];
+            rows_out(v, x * 4);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) v[y] = o[16 + y];
+            rows_out(v, x * 4 + 64);
           }
           __syncwarp();
         }
