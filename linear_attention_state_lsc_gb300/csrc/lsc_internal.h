@@ -301,7 +301,9 @@ struct KvAttendParams {
   int32_t max_seq, max_kv;  // host bounds of the lengths
   const CUtensorMap *map;  // host: the layer's rows as TMA boxes, or null
   int32_t box_rows;        // rows of a box; 0 without a map
-  uint8_t *ws;             // null: no unit can be cut
+  int32_t whole;           // 1: units are not cut
+  int32_t min_run;         // tiles of a run at least
+  uint8_t *ws;             // null: no unit is cut
   uint64_t wait_limit_ns;  // bound of each mbarrier wait (0: give up at once)
   uint64_t drain_limit_ns; // bound of the wait for issued MMAs at the end
   int32_t num_sms;

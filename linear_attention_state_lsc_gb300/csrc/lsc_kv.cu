@@ -518,6 +518,8 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
     }
     r.ws = (uint8_t *)ws;
   }
+  r.whole = !plan.may_cut;
+  r.min_run = plan.min_run;
   cudaError_t e = form == kAny    ? lsc::launch_kv_attend_any(r, s)
                   : form == kRows ? lsc::launch_kv_attend_rows(r, plan, s)
                                   : lsc::launch_kv_attend_chunk(r, plan, s);

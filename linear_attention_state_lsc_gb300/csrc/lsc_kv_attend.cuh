@@ -12,6 +12,11 @@
 // over all of them.  The cut is computed on the device from the lengths, so a
 // captured graph follows them.
 //
+// Units that are short for everybody (p.whole: by the host's bound of the
+// lengths) are not cut: each counts as one in the order above, and a run is of
+// whole units.  Joining the parts of a 256-row unit costs as much time as eight of
+// its tiles.
+//
 // A run that holds all tiles of a unit writes its rows; parts of a cut unit go
 // to the workspace as (maximum, sum, unnormalised fp32 row), and a second launch
 // joins them in tile order.  A CTA has at most two parts: slot 0, the rest of a
@@ -76,6 +81,7 @@ __device__ __forceinline__ int32_t seq_tiles(const KvAttendParams &p, int32_t i)
   const Seq s = attend_seq(p.L, p.b, i, p.max_seq, p.max_kv);
   const int32_t nb = row_blocks<M>(s, p.group);
   int32_t t = 0;
+  if (p.whole) return nb;
 #pragma unroll 1
   for (int32_t b = 0; b < nb; ++b) t += block_tiles<M, TK>(p, s, b);
   return t;
@@ -129,7 +135,7 @@ __device__ __forceinline__ Run find_run(const KvAttendParams &p, int cta, int ct
   total *= H;
   Run r;
   r.chunk = (total + ctas - 1) / ctas;
-  if (r.chunk < 1) r.chunk = 1;
+  if (r.chunk < p.min_run) r.chunk = p.min_run;
   r.pos = cta * r.chunk;
   r.end = r.pos + r.chunk < total ? r.pos + r.chunk : total;
   r.seq = r.head = r.block = r.tile = 0;
@@ -157,6 +163,10 @@ __device__ __forceinline__ Run find_run(const KvAttendParams &p, int cta, int ct
   int32_t rem = r.pos - sc.before;
   r.head = rem / sc.total;
   rem -= r.head * sc.total;
+  if (p.whole) {
+    r.block = rem;
+    return r;
+  }
   const Seq s = attend_seq(p.L, p.b, r.seq, p.max_seq, p.max_kv);
 #pragma unroll 1
   for (;;) {
@@ -190,8 +200,8 @@ __device__ __forceinline__ bool next_piece(const KvAttendParams &p, Run &r, Piec
   q.tiles = block_tiles<M, TK>(p, s, r.block);
   q.t0 = r.tile;
   const int32_t left = r.end - r.pos;
-  q.t1 = q.tiles - q.t0 <= left ? q.tiles : q.t0 + left;
-  r.pos += q.t1 - q.t0;
+  q.t1 = p.whole || q.tiles - q.t0 <= left ? q.tiles : q.t0 + left;
+  r.pos += p.whole ? 1 : q.t1 - q.t0;
   r.tile = 0;
   ++r.block;
   return true;
@@ -224,8 +234,9 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
 struct AttendPlan {
   int32_t ctas;    // runs
   int32_t M;       // rows of a unit
-  size_t ws_bytes; // of this launch's part of the workspace
-  bool may_cut;    // false: every unit is one tile, so no run can cut one
+  size_t ws_bytes;
+  bool may_cut;    // false: units are not cut
+  int32_t min_run; // tiles of a run at least
 };
 cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_join(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);

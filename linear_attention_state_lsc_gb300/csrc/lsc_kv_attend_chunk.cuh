@@ -16,11 +16,11 @@
 //     a warp for K and one for V.  Blocks that are a multiple of 8 tokens come
 //     as tiled TMA boxes of rows x 64 elements (x head_dim / 64 when a block holds
 //     the tile: then one box a tile; coordinates (element, row, column of 64, head,
-//     block) of the layer, element always 0); a tile that is not full, and other
-//     block sizes, with 16-byte cp.async.  E4M3 pools: four warps each, codes
-//     the same two ways into a staging buffer, then bf16 with their scale
-//     (exact above bf16's smallest normal).  Rows behind the last position are
-//     zeros.
+//     block) of the layer, element always 0); other block sizes with 16-byte
+//     cp.async.  E4M3 pools: four warps each, codes the same two ways into a staging
+//     buffer, then bf16 with their scale (exact above bf16's smallest normal).  V
+//     rows behind the last position become zeros: here, where they are copied or
+//     converted, else by the softmax threads.
 // head_dim 64 and 128: two row blocks of 128, one per softmax warpgroup, each with
 // its own S and O (S 2 x 128, O 2 x head_dim columns of TMEM), Q in shared memory,
 // tiles of 128: one block's softmax runs under the other's products, and a K/V
@@ -297,7 +297,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const uint8_t *from[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) from[i] = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)src, i * 8 + oct);
-#pragma unroll 2
+#pragma unroll 4
       for (int x = 0; x < (C::QT ? D : 2 * D); x += 64) {  // bytes of a row
         uint4 y[4];
 #pragma unroll
@@ -439,11 +439,18 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         const float2 lf = *reinterpret_cast<const float2 *>(&l2);
         l += lf.x + lf.y;
         const int32_t last = first + TK < pc.s.kv ? first + TK : pc.s.kv;
-        if (last > sure) {  // positions [max(first, sure), last): some row of the unit does not see them
+        // positions [max(first, sure), last): some row of the unit does not see them; behind last: a 16-bit block's rows
+        // came as they were
+        if (last > sure || (!Q8 && last < first + TK)) {
           const uint32_t vi = slots + 2 * j + 1;
           const int slot = (int)(vi % NS);
           if (!(ok = wait_warp(&sm.full[slot], vi / NS, limit))) break;
-          const int lo = (sure > first ? sure : first) - first, cnt = last - first - lo;
+          if (!Q8)
+            for (int i = row; i < (first + TK - last) * (D / 8); i += 128) {
+              const int key = last - first + i / (D / 8), ch = i % (D / 8);
+              *(uint4 *)(sm.ring[slot] + (ch >> 3) * (TK * 128) + key * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+          const int lo = (sure > first ? sure : first) - first, cnt = last - first - lo;  // cnt <= 0: nothing to search
           constexpr uint32_t E = BF16 ? 0x7f80 : 0x7c00;
           for (int i = row; i < cnt * (D / 8); i += 128) {
             const int key = lo + i / (D / 8), ch = i % (D / 8);
@@ -654,7 +661,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         start();
         for (int j = 0; j < nt; ++j, at.step(), step()) {
           uint8_t *dst = sm.ring[at.slot];
-          if (box > 0 && (pc.t0 + j + 1) * TK <= pc.s.kv) {
+          if (box > 0) {
             int32_t q = q0 + br_q, rr = r0 + br_r;
             if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
             const int32_t blk = block_of(q);
@@ -704,9 +711,10 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         for (int i = 0; i < NS; ++i)
           if (flying >> i & 1) wait_warp(&sm.full[i], flying >> (8 + i), p.drain_limit_ns);
     } else {
-      // 16 codes (two chunks of the 16-bit row) a lane and pass, through SD stages of codes per kind.  A whole tile comes
-      // by TMA (the first warp of the four), another one with cp.async: each thread copies what it converts itself, so
-      // those copies need no barrier.
+      // 16 codes (two chunks of the 16-bit row) a lane and pass, through SD stages of codes per kind.  Tiles come by TMA
+      // (the first warp of the four) or with cp.async: each thread copies what it converts itself, so those copies need
+      // no barrier.
+      constexpr uint32_t kNoRow = 256;
       constexpr int SD = C::SD, LPR = D / 16, RPI = 32 / LPR, RPW = TK / 4, IT = RPW / RPI;
       const int kind = is_k ? 0 : 1, gw = w & 3, lc = ln % LPR, r_first = gw * RPW;
       const int32_t off = r_first + (ln < RPW ? ln : 0), oq = L.by_block.div(off), orr = off - oq * L.block_tokens;
@@ -726,7 +734,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
             start();
           }
           const int64_t row_at = place(j, off, oq, orr, &sb[st]);
-          tma[st] = box > 0 && (pc.t0 + j + 1) * TK <= pc.s.kv;
+          if (row_at < 0) sb[st] = kNoRow;
+          tma[st] = box > 0;
           if (tma[st]) {
             int32_t q = q0 + br_q, rr = r0 + br_r;
             if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
@@ -764,8 +773,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           const int rl = i * RPI + ln / LPR, r = r_first + rl;
           const uint32_t e = __shfl_sync(0xffffffffu, sb[st], rl);
           // 2^(120 + e - 127) as two bf16; beyond bf16's range 2^120, and the rest in a second product (255: NaN)
-          const uint32_t k1 = wide && e > 134 ? 0x7b807b80u : (e + 120) * 0x00800080u;
-          const uint32_t k2 = e > 134 ? (e == 255 ? 0x7fc07fc0u : e * 0x00800080u) : 0x3f803f80u;
+          // a row behind the last position: 0 times whatever finite bits the block holds
+          const uint32_t k1 = e == kNoRow ? 0 : wide && e > 134 ? 0x7b807b80u : (e + 120) * 0x00800080u;
+          const uint32_t k2 = e > 134 && e != kNoRow ? (e == 255 ? 0x7fc07fc0u : e * 0x00800080u) : 0x3f803f80u;
           const uint4 code = *(const uint4 *)&sm.stage[kind][st][r * D + lc * 16];
           const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
           uint32_t o[8];
@@ -788,7 +798,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           if (!ok || left == 0) break;
           cp_async_wait<SD - 1>();
           if (!(ok = wait_warp(&sm.ready[kind][st], uses[st], limit)) || !(ok = wait_empty())) break;
-          if (__any_sync(0xffffffffu, sb[st] > 134)) convert(st, sm.ring[at.slot], true);
+          if (__any_sync(0xffffffffu, sb[st] > 134 && sb[st] != kNoRow)) convert(st, sm.ring[at.slot], true);
           else convert(st, sm.ring[at.slot], false);
           hand_on(at.slot);
           if (ln == 0) mbar_arrive(&sm.freed[kind][st]);

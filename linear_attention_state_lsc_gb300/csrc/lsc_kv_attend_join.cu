@@ -89,9 +89,10 @@ AttendPlan plan_kv_attend_rows(const KvAttendParams &p) {
   const int occ = q8 ? (D == 64 ? occ_of<1, 64>(plan.M) : D == 128 ? occ_of<1, 128>(plan.M) : occ_of<1, 256>(plan.M))
                      : (D == 64 ? occ_of<2, 64>(plan.M) : D == 128 ? occ_of<2, 128>(plan.M) : occ_of<2, 256>(plan.M));
   const int64_t tiles = ((int64_t)p.max_kv + kTK - 1) / kTK;
-  const int64_t most = (int64_t)p.b.n_seq * p.L.heads * (tiles < 1 ? 1 : tiles);  // tiles there can be
-  plan.ctas = (int)(most < (int64_t)p.num_sms * occ ? most : (int64_t)p.num_sms * occ);
+  const int64_t units = (int64_t)p.b.n_seq * p.L.heads, most = units * (tiles < 1 ? 1 : tiles);
   plan.may_cut = tiles > 1;
+  plan.min_run = 1;
+  plan.ctas = (int)(most < (int64_t)p.num_sms * occ ? most : (int64_t)p.num_sms * occ);
   plan.ws_bytes = plan.may_cut ? kv::workspace_size(plan.ctas, plan.M, D) : 0;
   return plan;
 }
@@ -103,16 +104,21 @@ cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &pla
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+constexpr int kWhole = 8, kMinRun = 4;  // in tiles of 128 positions
+
 AttendPlan plan_kv_attend_chunk(const KvAttendParams &p) {
   using namespace kv::chunk;
   const int D = p.L.head_dim, TK = D == 256 ? Conf<256, false>::TK : Conf<128, false>::TK;
   AttendPlan plan{};
   plan.M = D == 256 ? Conf<256, false>::M : Conf<128, false>::M;
   const int64_t tiles = ((int64_t)p.max_kv + TK - 1) / TK;
-  const int64_t blocks = ((int64_t)p.b.total_tokens * p.group + plan.M - 1) / plan.M + p.b.n_seq;
-  const int64_t most = blocks * p.L.heads * (tiles < 1 ? 1 : tiles);
+  const int64_t units = (((int64_t)p.b.total_tokens * p.group + plan.M - 1) / plan.M + p.b.n_seq) * p.L.heads;
+  // Uncut up to kWhole tiles of 128 positions: at 5 tiles a unit, 256 rows of 128, cutting each over 5 CTAs took 33 us
+  // and leaving them whole WHOLE_US.
+  plan.may_cut = tiles > kWhole * 128 / TK;
+  plan.min_run = plan.may_cut ? kMinRun * 128 / TK : 1;
+  const int64_t most = plan.may_cut ? units * tiles / plan.min_run + 1 : units;
   plan.ctas = (int)(most < p.num_sms ? most : p.num_sms);
-  plan.may_cut = tiles > 1;
   plan.ws_bytes = plan.may_cut ? kv::workspace_size(plan.ctas, plan.M, D) : 0;
   return plan;
 }
