@@ -451,28 +451,32 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
               *(uint4 *)(sm.ring[slot] + (ch >> 3) * (TK * 128) + key * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
             }
           const int lo = (sure > first ? sure : first) - first, cnt = last - first - lo;  // cnt <= 0: nothing to search
-          constexpr uint32_t E = BF16 ? 0x7f80 : 0x7c00;
-          for (int i = row; i < cnt * (D / 8); i += 128) {
+          // an exponent field of ones carries into the sign's place
+          constexpr uint32_t E = BF16 ? 0x7f80 : 0x7c00, up = (0x8000 - E) * 0x10001u;
+          auto vec = [&](int i) {
             const int key = lo + i / (D / 8), ch = i % (D / 8);
-            uint4 *at = (uint4 *)(sm.ring[slot] + (ch >> 3) * (TK * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
-            uint4 v = *at;
-            uint32_t e[4] = {v.x, v.y, v.z, v.w};
-            bool hit = false;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t u = (e[x] >> (16 * h)) & 0xffffu;
-                if ((u & E) == E) {
-                  hit = true;
-                  atomicMin(&sm.bad[(u & (E ^ 0x7fff)) ? 0 : (u & 0x8000) ? 2 : 1][ch * 8 + 2 * x + h], first + key);
-                  e[x] &= ~(0xffffu << (16 * h));
-                }
+            return (uint4 *)(sm.ring[slot] + (ch >> 3) * (TK * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+          };
+          uint32_t carry = 0;
+#pragma unroll 2
+          for (int i = row; i < cnt * (D / 8); i += 128) {
+            const uint4 v = *vec(i);
+            carry |= ((v.x & 0x7fff7fffu) + up) | ((v.y & 0x7fff7fffu) + up) | ((v.z & 0x7fff7fffu) + up) |
+                     ((v.w & 0x7fff7fffu) + up);
+          }
+          if (carry & 0x80008000u) {
+#pragma unroll 1
+            for (int i = row; i < cnt * (D / 8); i += 128) {
+              uint16_t *e = (uint16_t *)vec(i);
+#pragma unroll 1
+              for (int x = 0; x < 8; ++x) {
+                const uint32_t u = e[x];
+                if ((u & E) != E) continue;
+                atomicMin(&sm.bad[(u & (E ^ 0x7fff)) ? 0 : (u & 0x8000) ? 2 : 1][i % (D / 8) * 8 + x], first + lo + i / (D / 8));
+                e[x] = 0;
               }
-            if (hit) {
-              sm.any_bad = 1;
-              *at = make_uint4(e[0], e[1], e[2], e[3]);
             }
+            sm.any_bad = 1;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -565,7 +569,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         }
         tc::fence_before_sync();  // these reads before the next piece's products, through pfull
       }
-      if (mixed) {  // the next unit starts with a clean list: all softmax warps meet before and after it is cleared
+      if (mixed && have) {  // the next unit starts with a clean list: all softmax warps meet before and after it is cleared
         for (int round = 0; round < 2 && ok; ++round, ++meets) {
           if (round == 1 && *(volatile int32_t *)&sm.any_bad)
             for (int i = tid; i < 3 * D; i += 256) (&sm.bad[0][0])[i] = INT32_MAX;
