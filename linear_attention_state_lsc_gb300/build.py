@@ -17,10 +17,11 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblsc.so")
 SOURCES = ["lsc_host.cu", "lsc_copy.cu", "lsc_gdn.cu", "lsc_rec128.cu", "lsc_chunked_tc.cu", "lsc_chunk_prep.cu", "lsc_noalloc.cu", "lsc_decode_f32.cu", "lsc_decode_bf16.cu",
            "lsc_prefill.cu", "lsc_kv.cu", "lsc_kv_rows.cu", "lsc_kv_attend_any.cu", "lsc_kv_attend_join.cu",
+           "lsc_kv_attend_decode_bf16.cu", "lsc_kv_attend_decode_f16.cu", "lsc_kv_attend_decode_e4m3.cu",
            "lsc_kv_attend_rows_bf16.cu", "lsc_kv_attend_rows_f16.cu", "lsc_kv_attend_rows_e4m3.cu",
            "lsc_kv_attend_chunk_bf16.cu", "lsc_kv_attend_chunk_f16.cu", "lsc_kv_attend_chunk_e4m3.cu", "lsc_prefix_cache.cpp", "lsc_store.cpp"]
 HEADERS = [os.path.join(CSRC, h) for h in ("lsc_internal.h", "lsc_ptx.h", "lsc_tc.h", "lsc_chunk.h", "lsc_gdn_common.cuh", "lsc_decode.cuh", "lsc_kv_batch.cuh", "lsc_kv_attend.cuh",
-                                              "lsc_kv_attend_rows.cuh", "lsc_kv_attend_chunk.cuh")] + \
+                                              "lsc_kv_attend_rows.cuh", "lsc_kv_attend_decode.cuh", "lsc_kv_attend_chunk.cuh")] + \
     [os.path.join(INCLUDE, h) for h in ("lsc.h", "lsc_prefix_cache.h", "lsc_kv.h", "lsc_store.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -258,6 +258,11 @@ struct FastDiv {
   __device__ __forceinline__ int32_t div(int32_t n) const { return (int32_t)(((uint64_t)(uint32_t)n * mul) >> shift); }
 };
 
+// Positions of a decode sub-tile: 8 to 16 KB of K and V rows.
+__host__ __device__ constexpr int kv_decode_keys(int head_dim, int element) {
+  return element == 2 && head_dim >= 128 ? 16 : 32;
+}
+
 // One attention layer of a K/V pool.
 struct KvLayer {
   uint8_t *k, *v;       // block 0 of each lane
@@ -301,6 +306,8 @@ struct KvAttendParams {
   int32_t max_seq, max_kv;  // host bounds of the lengths
   const CUtensorMap *map;  // host: the layer's rows as TMA boxes, or null
   int32_t box_rows;        // rows of a box; 0 without a map
+  const CUtensorMap *map_decode;  // the same for the decode kernel
+  int32_t box_decode;
   int32_t whole;           // 1: units are not cut
   int32_t min_run;         // tiles of a run at least
   uint8_t *ws;             // null: no unit is cut

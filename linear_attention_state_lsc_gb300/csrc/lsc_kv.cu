@@ -31,7 +31,8 @@ struct lsc_kv_pool {
   int32_t *status = nullptr;    // device error word
   int32_t *h_status = nullptr;  // pinned
   int32_t box_rows = 0;         // rows of a TMA box of `maps`
-  std::vector<CUtensorMap> maps;  // per layer; empty: none
+  int32_t box_decode = 0;       // and of `maps_decode`
+  std::vector<CUtensorMap> maps, maps_decode;  // per layer; empty: none
 };
 
 namespace {
@@ -81,21 +82,46 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
   return LSC_OK;
 }
 
-// TMA maps of the layers' rows, for the chunk attention: 16-bit elements, 128-byte
-// swizzle, coordinates (element of a column, row of a block, column of 64
-// elements, kv head, block; V's blocks follow K's).  A box never leaves its
-// block: box_rows is the largest power of two that divides block_tokens, up to a
-// tile of positions, and a box of a whole tile takes all columns.  E4M3: bytes,
-// not swizzled, (code, row, kv head, block), boxes of whole rows.  Without maps
-// (odd blocks, other types and sizes) that kernel copies rows itself.
+// TMA maps of the layers' rows, for attend: coordinates (element of a column, row
+// of a block, column of 128 bytes, kv head, block; V's blocks follow K's), a box
+// of one column, or of all when it has a whole tile's rows.  A box never leaves its
+// block: its rows are the largest power of two that divides block_tokens, up to
+// the tile's.  128-byte swizzle (64 bytes a row: 64-byte) but for the chunk kernel's
+// E4M3 maps, where a box is plain rows of codes.  Without maps (blocks that are
+// no multiple of 8 tokens, other types and sizes) the kernels copy rows themselves.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool encode_maps(const lsc_kv_pool *p, EncodeTiled encode, int tile, bool plain, int box, std::vector<CUtensorMap> *out) {
+  const lsc_kv_pool_desc &d = p->d;
+  const int row = d.head_dim * (int)p->es, col = plain || row < 128 ? row : 128;  // bytes
+  const CUtensorMapDataType type = d.dtype == LSC_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : d.dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapSwizzle swizzle = plain ? CU_TENSOR_MAP_SWIZZLE_NONE : col == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const cuuint64_t dims[5] = {(cuuint64_t)(col / p->es), (cuuint64_t)d.block_tokens, (cuuint64_t)(row / col),
+                              (cuuint64_t)d.num_kv_heads, 2 * (cuuint64_t)d.num_blocks};
+  const cuuint64_t strides[4] = {(cuuint64_t)p->row_bytes, (cuuint64_t)col, (cuuint64_t)row, (cuuint64_t)d.page_bytes};
+  const cuuint32_t boxes[5] = {(cuuint32_t)(col / p->es), (cuuint32_t)box, box == tile ? (cuuint32_t)(row / col) : 1, 1, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  try {
+    out->resize(d.num_layers);
+  } catch (...) {
+    return false;
+  }
+  for (int32_t l = 0; l < d.num_layers; ++l)
+    if (encode(&(*out)[l], type, 5, p->base + (int64_t)l * p->region_bytes, dims, strides, boxes, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
 void make_maps(lsc_kv_pool *p) {
   const lsc_kv_pool_desc &d = p->d;
-  const int D = d.head_dim;
-  if (d.dtype == LSC_F32 || (D != 64 && D != 128 && D != 256)) return;
-  const bool q8 = d.dtype == LSC_E4M3;
-  int box = d.block_tokens & -d.block_tokens;
-  if (box > (D == 256 ? 64 : 128)) box = D == 256 ? 64 : 128;
-  if (box < 8) return;  // a swizzle pattern is 8 rows
+  const int D = d.head_dim, most = d.block_tokens & -d.block_tokens;
+  if (d.dtype == LSC_F32 || (D != 64 && D != 128 && D != 256) || most < 8) return;  // a swizzle pattern is 8 rows
   void *fn = nullptr;
   cudaDriverEntryPointQueryResult found;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
@@ -103,35 +129,16 @@ void make_maps(lsc_kv_pool *p) {
     cudaGetLastError();
     return;
   }
-  const auto encode = (CUresult(*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill))fn;
-  std::vector<CUtensorMap> maps;
-  try {
-    maps.resize(d.num_layers);
-  } catch (...) {
+  const int tile = D == 256 ? 64 : 128, keys = lsc::kv_decode_keys(D, (int)p->es);
+  const int box = std::min(most, tile), box_decode = std::min(most, keys);
+  std::vector<CUtensorMap> maps, decode;
+  if (!encode_maps(p, (EncodeTiled)fn, tile, d.dtype == LSC_E4M3, box, &maps) ||
+      !encode_maps(p, (EncodeTiled)fn, keys, false, box_decode, &decode))
     return;
-  }
-  const bool tile = box == (D == 256 ? 64 : 128);
-  const cuuint64_t blocks = 2 * (cuuint64_t)d.num_blocks, row = (cuuint64_t)p->row_bytes, page = (cuuint64_t)d.page_bytes;
-  const cuuint64_t dims[5] = {64, (cuuint64_t)d.block_tokens, (cuuint64_t)(D / 64), (cuuint64_t)d.num_kv_heads, blocks};
-  const cuuint64_t strides[4] = {row, 128, (cuuint64_t)(D * p->es), page};
-  const cuuint32_t boxes[5] = {64, (cuuint32_t)box, tile ? (cuuint32_t)(D / 64) : 1, 1, 1}, ones[5] = {1, 1, 1, 1, 1};
-  const cuuint64_t dims8[4] = {(cuuint64_t)D, (cuuint64_t)d.block_tokens, (cuuint64_t)d.num_kv_heads, blocks};
-  const cuuint64_t strides8[3] = {row, (cuuint64_t)D, page};
-  const cuuint32_t boxes8[4] = {(cuuint32_t)D, (cuuint32_t)box, 1, 1};
-  for (int32_t l = 0; l < d.num_layers; ++l) {
-    const CUtensorMapDataType type = q8                      ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : d.dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    if (encode(&maps[l], type, q8 ? 4 : 5, p->base + (int64_t)l * p->region_bytes, q8 ? dims8 : dims,
-               q8 ? strides8 : strides, q8 ? boxes8 : boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return;
-  }
   p->maps.swap(maps);
+  p->maps_decode.swap(decode);
   p->box_rows = box;
+  p->box_decode = box_decode;
 }
 
 int check_device(const lsc_kv_pool *p) {
@@ -229,16 +236,19 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
   r->num_sms = p->num_sms;
   r->map = p->maps.empty() ? nullptr : &p->maps[layer];
   r->box_rows = p->box_rows;
+  r->map_decode = p->maps_decode.empty() ? nullptr : &p->maps_decode[layer];
+  r->box_decode = p->box_decode;
   r->wait_limit_ns = fault("timeout0") ? 0 : kWaitLimitNs;
   r->drain_limit_ns = kWaitLimitNs;
   return LSC_OK;
 }
 
-// Which kernel a call takes, by sizes, types and alignment: the few-row kernel
-// when every sequence has kRowsMost packed rows at most, the chunk kernel when
-// one may have more, the CUDA cores for what neither takes.
-constexpr int32_t kRowsMost = 64;
-enum Form { kAny, kRows, kChunk };
+// Which kernel a call takes, by sizes, types and alignment: the decode kernel when
+// every sequence has kDecodeMost packed rows at most and the blocks have TMA maps,
+// else the few-row kernel up to kRowsMost, the chunk kernel when a sequence may
+// have more, the CUDA cores for what none of them takes.
+constexpr int32_t kDecodeMost = 16, kRowsMost = 64;
+enum Form { kAny, kDecode, kRows, kChunk };
 
 Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   *plan = lsc::AttendPlan{};
@@ -252,6 +262,10 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   const int64_t units = (int64_t)r.b.total_tokens * r.group / 16 + r.b.n_seq;
   if (rows > INT32_MAX - 1024 || r.max_kv > INT32_MAX - 1024 || units * r.L.heads > INT32_MAX / (r.max_kv / 64 + 1))
     return kAny;
+  if (rows <= kDecodeMost && r.box_decode > 0) {
+    *plan = lsc::plan_kv_attend_decode(r);
+    return kDecode;
+  }
   if (rows <= kRowsMost) {
     *plan = lsc::plan_kv_attend_rows(r);
     return kRows;
@@ -521,6 +535,7 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
   r.whole = !plan.may_cut;
   r.min_run = plan.min_run;
   cudaError_t e = form == kAny    ? lsc::launch_kv_attend_any(r, s)
+                  : form == kDecode ? lsc::launch_kv_attend_decode(r, plan, s)
                   : form == kRows ? lsc::launch_kv_attend_rows(r, plan, s)
                                   : lsc::launch_kv_attend_chunk(r, plan, s);
   if (e == cudaSuccess && plan.may_cut) e = lsc::launch_kv_attend_join(r, plan, s);

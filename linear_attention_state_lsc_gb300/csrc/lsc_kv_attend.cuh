@@ -239,6 +239,8 @@ struct AttendPlan {
   int32_t min_run; // tiles of a run at least
 };
 cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
+cudaError_t launch_kv_attend_decode(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
+AttendPlan plan_kv_attend_decode(const KvAttendParams &p);
 cudaError_t launch_kv_attend_join(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 AttendPlan plan_kv_attend_rows(const KvAttendParams &p);
 cudaError_t launch_kv_attend_chunk(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);

@@ -195,15 +195,6 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, i
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                            uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // A bounded wait.  The first tries do without the clock: reading %globaltimer costs about a microsecond, several
 // tiles' worth of waits.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t phase, uint64_t limit) {
@@ -749,7 +740,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
               if (ok && ln == 0) mbar_arrive_expect_tx(&sm.ready[kind][st], TK * D);
               __syncwarp();
               if (ok && ln < boxes)
-                tma_load_4d(&sm.stage[kind][st][br * D], &map, 0, rr, pc.head, blk + (is_k ? 0 : L.num_blocks),
+                tma_load_5d(&sm.stage[kind][st][br * D], &map, 0, rr, 0, pc.head, blk + (is_k ? 0 : L.num_blocks),
                             &sm.ready[kind][st]);
             }
           } else {

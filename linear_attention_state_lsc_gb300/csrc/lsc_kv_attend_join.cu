@@ -11,6 +11,7 @@
 #include "lsc_internal.h"
 #include "lsc_kv_attend.cuh"
 #include "lsc_kv_attend_chunk.cuh"
+#include "lsc_kv_attend_decode.cuh"
 #include "lsc_kv_attend_rows.cuh"
 #include "lsc_ptx.h"
 
@@ -95,6 +96,29 @@ AttendPlan plan_kv_attend_rows(const KvAttendParams &p) {
   plan.ctas = (int)(most < (int64_t)p.num_sms * occ ? most : (int64_t)p.num_sms * occ);
   plan.ws_bytes = plan.may_cut ? kv::workspace_size(plan.ctas, plan.M, D) : 0;
   return plan;
+}
+
+AttendPlan plan_kv_attend_decode(const KvAttendParams &p) {
+  using namespace kv::decode;
+  const int D = p.L.head_dim, q8 = p.L.dtype == LSC_E4M3;
+  AttendPlan plan{};
+  plan.M = 16;
+  const int occ = q8 ? (D == 64 ? Conf<1, 64>::occ : D == 128 ? Conf<1, 128>::occ : Conf<1, 256>::occ)
+                     : (D == 64 ? Conf<2, 64>::occ : D == 128 ? Conf<2, 128>::occ : Conf<2, 256>::occ);
+  const int64_t tiles = ((int64_t)p.max_kv + kTK - 1) / kTK;
+  const int64_t units = (int64_t)p.b.n_seq * p.L.heads, most = units * (tiles < 1 ? 1 : tiles);
+  plan.may_cut = tiles > 1;
+  plan.min_run = 1;
+  plan.ctas = (int)(most < (int64_t)p.num_sms * occ ? most : (int64_t)p.num_sms * occ);
+  plan.ws_bytes = plan.may_cut ? kv::workspace_size(plan.ctas, plan.M, D) : 0;
+  return plan;
+}
+
+cudaError_t launch_kv_attend_decode(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+  const cudaError_t e = p.L.dtype == LSC_E4M3   ? launch_kv_attend_decode_e4m3(p, plan, stream)
+                        : p.L.dtype == LSC_BF16 ? launch_kv_attend_decode_bf16(p, plan, stream)
+                                                : launch_kv_attend_decode_f16(p, plan, stream);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
