@@ -85,6 +85,12 @@ __device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int r
       : "memory");
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The first tries do without the clock (reading %globaltimer is slow); one answer for the whole warp.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, uint64_t limit) {
   bool ok = limit != 0;
@@ -136,17 +142,18 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
     const int32_t kv = pc.s.kv, lo = pc.t0 * kTK, hi = kv < pc.t1 * kTK ? kv : pc.t1 * kTK;
     const int32_t *table = p.b.table + (int64_t)pc.seq * p.b.max_blocks;
     const int nsub = hi > lo ? (hi - lo + KEYS - 1) / KEYS : 0, mine = nsub > w ? (nsub - w + kWarps - 1) / kWarps : 0;
-    auto block_at = [&](int32_t pos) {  // block of a position, 0 behind the last one; a bad one is recorded, read as 0
-      int32_t blk = pos < kv ? __ldg(table + L.by_block.div(pos)) : 0;
-      if (blk < 0 || blk >= L.num_blocks) {
-        report(L.status, LSC_ERR_OUT_OF_RANGE);
-        blk = 0;
-      }
-      return blk;
+    // Block of a position, 0 behind the last one.  Looked up a sub-tile ahead and checked only where it is used (a bad
+    // one is recorded and read as 0): a look at it any earlier would wait for the load.
+    auto block_at = [&](int32_t pos) { return pos < kv ? __ldg(table + L.by_block.div(pos)) : 0; };
+    auto checked = [&](int32_t blk) {
+      if ((uint32_t)blk < (uint32_t)L.num_blocks) return blk;
+      report(L.status, LSC_ERR_OUT_OF_RANGE);
+      return 0;
     };
     auto first_of = [&](int i) { return lo + (i * kWarps + w) * KEYS; };  // first position of this warp's sub-tile i
     auto issue = [&](int i, int st, int32_t blk) {
       const int32_t pos = first_of(i) + br;
+      blk = checked(blk);
       if (ln == 0) mbar_arrive_expect_tx(&sm.full[w][st], 2 * C::half);
       __syncwarp();
       if (bi < boxes)
@@ -159,7 +166,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
       const int32_t pos = first_of(i) + ln;
       kb = vb = 127;
       if (Q8 && i < mine && pos < hi) {
-        const int64_t at = (int64_t)blk * L.page + L.scale_off +
+        const int64_t at = (int64_t)checked(blk) * L.page + L.scale_off +
                            (int64_t)(pos - L.by_block.div(pos) * L.block_tokens) * L.heads + pc.head;
         kb = __ldg(L.k + at);
         vb = __ldg(L.v + at);
@@ -275,24 +282,35 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
         __syncwarp();
       }
       // ---- scores: lane (g, tq) gets rows g, g + 8 and positions 2 tq, 2 tq + 1 of each 8
-      float s[NK][4];
+      // (two sums a tile, all tiles in turn: a product waits some 30 cycles for the one before it in its sum)
+      float s[NK][4], s2[NK][4];
 #pragma unroll
-      for (int n = 0; n < NK; ++n) {
-        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        constexpr int PER = Q8 ? 4 : 2;  // k steps per ldmatrix.x4
+      for (int n = 0; n < NK; ++n)
 #pragma unroll
-        for (int k0 = 0; k0 < KS; k0 += PER) {
+        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+      constexpr int PER = Q8 ? 4 : 2;  // k steps per ldmatrix.x4
+#pragma unroll
+      for (int k0 = 0; k0 < KS; k0 += PER)
+#pragma unroll
+        for (int n = 0; n < NK; ++n) {
           uint32_t b[4];
           ldsm4(b, ka + chunk_at<RB, KEYS>(8 * n + (ln & 7), k0 * 2 / (Q8 ? 2 : 1) + (ln >> 3)));
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
-            if constexpr (Q8) mma<false>(s[n], qf[k0 + k], e4m3x2_to_f16x2(b[k] & 0xffffu), e4m3x2_to_f16x2(b[k] >> 16));
-            else mma<BF16>(s[n], qf[k0 + k], b[2 * k], b[2 * k + 1]);
+            float(&c)[4] = k & 1 ? s2[n] : s[n];
+            if constexpr (Q8) mma<false>(c, qf[k0 + k], e4m3x2_to_f16x2(b[k] & 0xffffu), e4m3x2_to_f16x2(b[k] >> 16));
+            else mma<BF16>(c, qf[k0 + k], b[2 * k], b[2 * k + 1]);
           }
         }
-      }
+#pragma unroll
+      for (int n = 0; n < NK; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
       // ---- weights
       float vx[Q8 ? NK : 1][2];
+      const float k_up = Q8 ? scale_of(kb_now) : 1.f, v_up = Q8 ? scale_of(vb_now) : 1.f;  // of position `lane`
+      // bounds keep the sum of 2^(s - m) a normal number
+      const float v_ex = Q8 ? (float)(vb_now < 87 ? -40 : vb_now > 227 ? 100 : (int)vb_now - 127) : 0.f;
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int n = 0; n < NK; ++n)
@@ -301,10 +319,9 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
           const int key = 8 * n + 2 * tq + e;
           float kx = 1.f, ve = 0.f;
           if constexpr (Q8) {
-            kx = scale_of(__shfl_sync(0xffffffffu, kb_now, key));
-            const int vb = (int)__shfl_sync(0xffffffffu, vb_now, key);
-            vx[n][e] = scale_of(vb);
-            ve = (float)(vb < 87 ? -40 : vb > 227 ? 100 : vb - 127);  // bounds keep the sum of 2^(s - m) a normal number
+            kx = __shfl_sync(0xffffffffu, k_up, key);
+            vx[n][e] = __shfl_sync(0xffffffffu, v_up, key);
+            ve = __shfl_sync(0xffffffffu, v_ex, key);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -323,7 +340,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
       if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {  // also the first one's (m is -inf)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float to = fmaxf(m[h], top[h]), f = exp2f(m[h] - (to == -INFINITY ? 0.f : to));
+          const float to = fmaxf(m[h], top[h]), f = ex2(m[h] - (to == -INFINITY ? 0.f : to));
           m[h] = to;
           l[h] *= f;
 #pragma unroll
@@ -336,7 +353,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
         const float ref = m[h] == -INFINITY ? 0.f : m[h];
 #pragma unroll
         for (int n = 0; n < NK; ++n) {
-          const float p0 = exp2f(s[n][2 * h] - ref), p1 = exp2f(s[n][2 * h + 1] - ref);
+          const float p0 = ex2(s[n][2 * h] - ref), p1 = ex2(s[n][2 * h + 1] - ref);
           l[h] += p0 + p1;
           // a position that the row does not see has weight 0 whatever its scale
           const int key = first + 8 * n + 2 * tq;
