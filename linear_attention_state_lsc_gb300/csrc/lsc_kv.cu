@@ -534,6 +534,7 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
   }
   r.whole = !plan.may_cut;
   r.min_run = plan.min_run;
+  r.groups = r.L.heads / std::max(plan.together, 1);
   cudaError_t e = form == kAny    ? lsc::launch_kv_attend_any(r, s)
                   : form == kDecode ? lsc::launch_kv_attend_decode(r, plan, s)
                   : form == kRows ? lsc::launch_kv_attend_rows(r, plan, s)

@@ -1,7 +1,7 @@
 // lsc_kv_attend.cuh -- what the tensor-core forms of lsc_kv_attend share: how the
 // work is cut, where parts of a cut unit go, and how they are joined.
 //
-// A unit is one kv head of a sequence with up to M packed rows: packed row R of
+// A unit is one kv head of a sequence (decode: a group of up to four) with up to M packed rows: packed row R of
 // a (sequence, kv head) is q head R % group of new token R / group, so the heads
 // that share K and V are rows of one tile and K/V is read once for all of
 // them.  A unit's work is its tiles of TK positions, up to the last one that
@@ -125,7 +125,7 @@ __device__ __forceinline__ int32_t block_scan(int32_t x, RunScratch &sc, int32_t
 // The run of CTA `cta` of `ctas`; called by all NT threads.
 template <int NT, int M, int TK>
 __device__ __forceinline__ Run find_run(const KvAttendParams &p, int cta, int ctas, RunScratch &sc) {
-  const int H = p.L.heads;
+  const int H = p.groups;
   int32_t total = 0, mine = 0, incl = 0;
 #pragma unroll 1
   for (int32_t i0 = 0; i0 < p.b.n_seq; i0 += NT) {
@@ -187,7 +187,7 @@ __device__ __forceinline__ bool next_piece(const KvAttendParams &p, Run &r, Piec
 #pragma unroll 1
   while (r.block >= row_blocks<M>(s, p.group)) {  // past this head's blocks (or a sequence without new tokens)
     r.block = 0;
-    if (s.n == 0 || ++r.head == p.L.heads) {
+    if (s.n == 0 || ++r.head == p.groups) {
       r.head = 0;
       ++r.seq;
       s = attend_seq(p.L, p.b, r.seq, p.max_seq, p.max_kv);
@@ -233,7 +233,8 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
 // ---- launches (lsc_kv_attend_rows_*.cu, lsc_kv_attend_chunk.cu, lsc_kv_attend_join.cu) ----
 struct AttendPlan {
   int32_t ctas;    // runs
-  int32_t M;       // rows of a unit
+  int32_t M;       // rows of a unit, `together` heads' worth
+  int32_t together;  // kv heads of a unit
   size_t ws_bytes;
   bool may_cut;    // false: units are not cut
   int32_t min_run; // tiles of a run at least

@@ -6,12 +6,13 @@
 // want 128 rows and a trip through TMEM each way.  What matters is that nothing
 // holds up the stream: a first version with block-wide tiles and cp.async spent
 // 1420 of a tile's 3300 cycles in the copies' issue and another 700 in barriers
-// (75 % of the copy rate).  So each of the four warps works alone: it takes every
-// fourth sub-tile of KEYS positions of the CTA's run, loads it with tiled TMA
+// (75 % of the copy rate).  So each of the four warps works alone: it takes one of
+// the unit's 4, 2 or 1 kv heads and every 1st, 2nd or 4th sub-tile of KEYS
+// positions of the CTA's run, loads it with tiled TMA
 // into a ring of its own (boxes through the block table, swizzled rows, so
 // ldmatrix meets no bank twice), and keeps its own running maximum, sum and
 // weighted rows of all columns; scores become the weights' operand without leaving
-// the registers.  The warps meet at the end of a piece, where their parts are
+// the registers.  The warps meet at the end of a piece, where a head's parts are
 // joined in order.  The maximum is a reference that moves only when a row's
 // maximum rose by more than 2^8 (weights are 2^8 at most), so the weighted rows are
 // rarely rescaled.
@@ -62,7 +63,7 @@ struct Smem {
   float2 ml[kWarps][16];
   float qs[16];
   int32_t vis[16];
-  int32_t bad[ES == 1 ? 1 : 3][ES == 1 ? 1 : D];
+  int32_t bad[ES == 1 ? 1 : kWarps][ES == 1 ? 1 : 3][ES == 1 ? 1 : D];  // by head of the unit
   int32_t any_bad;
   uint64_t full[kWarps][C::ST];
   RunScratch run;
@@ -104,7 +105,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, uint64_
 
 template <bool BF16, int ES, int D>
 __global__ void __launch_bounds__(kThreads, (Conf<ES, D>::occ))
-decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map) {
+decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map, int together) {
   using C = Conf<ES, D>;
   constexpr bool Q8 = ES == 1;
   constexpr int M = 16, KEYS = C::KEYS, ST = C::ST, RB = C::RB;
@@ -121,10 +122,12 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
   const KvLayer &L = p.L;
   const int ctas = gridDim.x, cta = blockIdx.x;
   if (cta == 0) check_cu(L, p.b);
-  const Workspace ws = workspace_at(p.ws, ctas, M);
+  const int MU = M * together, splits = kWarps / together;  // rows of a unit; warps of a head
+  const int wh = w & (together - 1), wsp = w / together;    // this warp's head of the unit, its share of the sub-tiles
+  const Workspace ws = workspace_at(p.ws, ctas, MU);
   if (tid == 0) sm.any_bad = 0;
   if (!Q8)
-    for (int i = tid; i < 3 * D; i += kThreads) (&sm.bad[0][0])[i] = INT32_MAX;
+    for (int i = tid; i < kWarps * 3 * D; i += kThreads) (&sm.bad[0][0][0])[i] = INT32_MAX;
   Run run = find_run<kThreads, M, kTK>(p, cta, ctas, sm.run);
   Piece pc;
   Cut cut = {0, 0, 0, 0};
@@ -141,7 +144,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
     const int R = pc.s.n * p.group < M ? pc.s.n * p.group : M;  // this launch's units have one block
     const int32_t kv = pc.s.kv, lo = pc.t0 * kTK, hi = kv < pc.t1 * kTK ? kv : pc.t1 * kTK;
     const int32_t *table = p.b.table + (int64_t)pc.seq * p.b.max_blocks;
-    const int nsub = hi > lo ? (hi - lo + KEYS - 1) / KEYS : 0, mine = nsub > w ? (nsub - w + kWarps - 1) / kWarps : 0;
+    const int nsub = hi > lo ? (hi - lo + KEYS - 1) / KEYS : 0, mine = nsub > wsp ? (nsub - wsp + splits - 1) / splits : 0, head = pc.head * together + wh;
     // Block of a position, 0 behind the last one.  Looked up a sub-tile ahead and checked only where it is used (a bad
     // one is recorded and read as 0): a look at it any earlier would wait for the load.
     auto block_at = [&](int32_t pos) { return pos < kv ? __ldg(table + L.by_block.div(pos)) : 0; };
@@ -150,7 +153,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
       report(L.status, LSC_ERR_OUT_OF_RANGE);
       return 0;
     };
-    auto first_of = [&](int i) { return lo + (i * kWarps + w) * KEYS; };  // first position of this warp's sub-tile i
+    auto first_of = [&](int i) { return lo + (i * splits + wsp) * KEYS; };  // first position of this warp's sub-tile i
     auto issue = [&](int i, int st, int32_t blk) {
       const int32_t pos = first_of(i) + br;
       blk = checked(blk);
@@ -158,7 +161,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
       __syncwarp();
       if (bi < boxes)
         tma_box(ring + (st * 2 + (ln >> 4)) * C::half + bc * (KEYS * 128) + br * (RB < 128 ? RB : 128), &map,
-                pos - L.by_block.div(pos) * L.block_tokens, bc, pc.head, blk + (ln < 16 ? 0 : L.num_blocks),
+                pos - L.by_block.div(pos) * L.block_tokens, bc, head, blk + (ln < 16 ? 0 : L.num_blocks),
                 &sm.full[w][st]);
     };
     // E4M3: lane i's scale bytes of position i of a sub-tile, 127 behind the last one
@@ -167,7 +170,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
       kb = vb = 127;
       if (Q8 && i < mine && pos < hi) {
         const int64_t at = (int64_t)checked(blk) * L.page + L.scale_off +
-                           (int64_t)(pos - L.by_block.div(pos) * L.block_tokens) * L.heads + pc.head;
+                           (int64_t)(pos - L.by_block.div(pos) * L.block_tokens) * L.heads + head;
         kb = __ldg(L.k + at);
         vb = __ldg(L.v + at);
       }
@@ -194,7 +197,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
     for (int h = 0; h < 2; ++h) {
       const int r = 8 * h + g, tok = p.by_group.div(r);
       const uint16_t *src = (const uint16_t *)p.q + (int64_t)(pc.s.row0 + tok) * p.q_stride +
-                            (int64_t)(pc.head * p.group + (r - tok * p.group)) * D;
+                            (int64_t)(head * p.group + (r - tok * p.group)) * D;
       qsc[h] = p.scale_log2;
       if constexpr (!Q8) {
 #pragma unroll
@@ -274,7 +277,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
             uint16_t *v = (uint16_t *)(vs + chunk_at<RB, KEYS>(key, d >> 3) + (d & 7) * 2);
             const uint32_t u = *v;
             if ((u & E) != E) continue;
-            atomicMin(&sm.bad[(u & (E ^ 0x7fff)) ? 0 : (u & 0x8000) ? 2 : 1][d], first + key);
+            atomicMin(&sm.bad[wh][(u & (E ^ 0x7fff)) ? 0 : (u & 0x8000) ? 2 : 1][d], first + key);
             sm.any_bad = 1;
             *v = 0;
           }
@@ -432,18 +435,17 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
     }
     __syncthreads();
     const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
-    const int64_t slot0 = (int64_t)(2 * cta + (pc.t0 == 0 ? 1 : 0)) * M;
+    const int64_t slot0 = (int64_t)(2 * cta + (pc.t0 == 0 ? 1 : 0)) * MU;
     const bool look = !Q8 && sm.any_bad != 0;
 #pragma unroll 1
-    for (int x = tid; x < R * (D / 4); x += kThreads) {
-      const int r = x / (D / 4), d = x % (D / 4) * 4, tok = p.by_group.div(r);
+    for (int x = tid; x < together * M * (D / 4); x += kThreads) {
+      const int hr = x / (D / 4), d = x % (D / 4) * 4, r = hr & (M - 1), hw = hr / M, tok = p.by_group.div(r);
+      if (r >= R) continue;
       float mm = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, sm.ml[i][r].x);
+      for (int i = hw; i < kWarps; i += together) mm = fmaxf(mm, sm.ml[i][r].x);
       const float ref = mm == -INFINITY ? 0.f : mm;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
+      for (int i = hw; i < kWarps; i += together) {
         const float2 ml = sm.ml[i][r];
         const float k = exp2f(ml.x - ref);
         const float4 z = *(const float4 *)(parts + (i * M + r) * PS + d);
@@ -457,27 +459,27 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
         if (look) {
           float *v = &y.x;
           for (int e = 0; e < 4; ++e) {
-            if (sm.bad[1][d + e] < sm.vis[r]) v[e] += INFINITY;
-            if (sm.bad[2][d + e] < sm.vis[r]) v[e] -= INFINITY;
-            if (sm.bad[0][d + e] < sm.vis[r]) v[e] = __uint_as_float(0x7fc00000u);
+            if (sm.bad[hw][1][d + e] < sm.vis[r]) v[e] += INFINITY;
+            if (sm.bad[hw][2][d + e] < sm.vis[r]) v[e] -= INFINITY;
+            if (sm.bad[hw][0][d + e] < sm.vis[r]) v[e] = __uint_as_float(0x7fc00000u);
           }
         }
       }
-      const int64_t t = pc.s.row0 + tok, hd = (int64_t)pc.head * p.group + (r - tok * p.group);
+      const int64_t t = pc.s.row0 + tok, hd = (int64_t)(pc.head * together + hw) * p.group + (r - tok * p.group);
       if (whole) {
         const int bf = p.dtype == LSC_BF16;
         *(uint2 *)((uint16_t *)p.out + t * p.out_stride + hd * D + d) = make_uint2(pack2(y.x, y.y, bf), pack2(y.z, y.w, bf));
         if (d == 0 && p.lse) p.lse[t * p.heads + hd] = empty ? -INFINITY : (mm + log2f(sum)) * 0.693147180559945309f;
       } else {
-        *(float4 *)(ws.o + (slot0 + r) * D + d) = y;
-        if (d == 0) ws.ml[slot0 + r] = make_float2(mm, sum);
+        *(float4 *)(ws.o + (slot0 + hr) * D + d) = y;
+        if (d == 0) ws.ml[slot0 + hr] = make_float2(mm, sum);
       }
     }
     cut = cut_of(run, pc, cta);
     fence_proxy_async_smem();  // the parts were written where the next piece's boxes land
     __syncthreads();
     if (look) {
-      for (int i = tid; i < 3 * D; i += kThreads) (&sm.bad[0][0])[i] = INT32_MAX;
+      for (int i = tid; i < kWarps * 3 * D; i += kThreads) (&sm.bad[0][0][0])[i] = INT32_MAX;
       if (tid == 0) sm.any_bad = 0;
       __syncthreads();
     }
@@ -492,7 +494,7 @@ cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStre
   auto *k = decode_attend_kernel<BF16, ES, D>;
   const cudaError_t e = limit.ensure((const void *)k, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, plan.ctas, kThreads, smem, stream, p, *p.map_decode);
+  return launch_pdl(k, plan.ctas, kThreads, smem, stream, p, *p.map_decode, plan.together);
 }
 
 template <bool BF16, int ES>
