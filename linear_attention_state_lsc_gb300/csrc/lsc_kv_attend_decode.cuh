@@ -1,8 +1,11 @@
 // lsc_kv_attend_decode.cuh -- attention over a layer of the K/V block pool for
 // sequences of up to 16 packed rows (lsc_kv_attend.cuh): decode steps.
 //
-// K and V are read once, so HBM bounds it; 16 rows are one m16n8k16 tile of
-// mma.sync, which keeps scores, weights and sums in registers, where tcgen05 would
+// K and V are read once, so HBM bounds it.  The products run transposed, S^T = K Q^T
+// and O^T = V^T P^T, as m16n8k16 tiles of mma.sync with positions and columns in the
+// 16 and the packed rows in the 8: the usual 8 or fewer rows fill a tile (with rows
+// in the 16, half of each product went to padding and 64 products a sub-tile were
+// what bounded it), and scores, weights and sums stay in registers.  tcgen05 would
 // want 128 rows and a trip through TMEM each way.  What matters is that nothing
 // holds up the stream: a first version with block-wide tiles and cp.async spent
 // 1420 of a tile's 3300 cycles in the copies' issue and another 700 in barriers
@@ -12,7 +15,7 @@
 // into a ring of its own (boxes through the block table, swizzled rows, so
 // ldmatrix meets no bank twice), and keeps its own running maximum, sum and
 // weighted rows of all columns; scores become the weights' operand without leaving
-// the registers.  The warps meet at the end of a piece, where a head's parts are
+// the registers (a transposition of 8 x 8 each).  The warps meet at the end of a piece, where a head's parts are
 // joined in order.  The maximum is a reference that moves only when a row's
 // maximum rose by more than 2^8 (weights are 2^8 at most), so the weighted rows are
 // rarely rescaled.
@@ -61,7 +64,6 @@ struct Smem {
   using C = Conf<ES, D>;
   alignas(1024) uint8_t ring[kWarps][C::ST][2][C::half];  // at a piece's end: the warps' weighted rows
   float2 ml[kWarps][16];
-  float qs[16];
   int32_t vis[16];
   int32_t bad[ES == 1 ? 1 : kWarps][ES == 1 ? 1 : 3][ES == 1 ? 1 : D];  // by head of the unit
   int32_t any_bad;
@@ -92,6 +94,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// An 8 x 8 matrix of 16-bit values over the lanes (row g, columns 2 tq, 2 tq + 1), transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // The first tries do without the clock (reading %globaltimer is slow); one answer for the whole warp.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, uint64_t limit) {
   bool ok = limit != 0;
@@ -103,15 +112,15 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, uint64_
   return __all_sync(0xffffffffu, ok);
 }
 
-template <bool BF16, int ES, int D>
+template <bool BF16, int ES, int D, int NR>
 __global__ void __launch_bounds__(kThreads, (Conf<ES, D>::occ))
 decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map, int together) {
   using C = Conf<ES, D>;
   constexpr bool Q8 = ES == 1;
-  constexpr int M = 16, KEYS = C::KEYS, ST = C::ST, RB = C::RB;
-  constexpr int KS = D / 16;        // k steps of a score
-  constexpr int NK = KEYS / 8;      // score tiles of 8 positions
-  constexpr int NT = D / 8;         // output tiles of 8 columns
+  constexpr int M = 8 * NR;         // rows of a head, NR tiles of 8
+  constexpr int KEYS = C::KEYS, ST = C::ST, RB = C::RB;
+  constexpr int KS = D / 16;        // k steps of a score, output tiles of 16 columns
+  constexpr int NK = KEYS / 16;     // score tiles of 16 positions
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem<ES, D> &sm = *reinterpret_cast<Smem<ES, D> *>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31, g = ln >> 2, tq = ln & 3;
@@ -189,30 +198,30 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
     if (Q8 && mine > 1) blk_scale = block_at(first_of(1) + ln);
 
     if (tid < M) sm.vis[tid] = tid < R ? visible(pc.s, p.by_group.div(tid), p.causal) : 0;
-    // q as operand registers: rows g and g + 8.  16 bits: elements 2 tq, 2 tq + 1 and 8 further of each 16.  E4M3: a lane
+    // q as operand registers: row g of each 8.  16 bits: elements 2 tq, 2 tq + 1 and 8 further of each 16.  E4M3: a lane
     // meets 4 consecutive codes, so it holds elements 4 tq .. 4 tq + 3, as f16 times a power of two.
-    uint32_t qf[KS][4];
-    float qsc[2];
+    uint32_t qf[NR][KS][2];
+    float q_up[NR];  // of row g: scale * log2 e, times that power
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < NR; ++h) {
       const int r = 8 * h + g, tok = p.by_group.div(r);
       const uint16_t *src = (const uint16_t *)p.q + (int64_t)(pc.s.row0 + tok) * p.q_stride +
                             (int64_t)(head * p.group + (r - tok * p.group)) * D;
-      qsc[h] = p.scale_log2;
+      q_up[h] = p.scale_log2;
       if constexpr (!Q8) {
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          qf[k][h] = r < R ? *(const uint32_t *)(src + k * 16 + 2 * tq) : 0;
-          qf[k][h + 2] = r < R ? *(const uint32_t *)(src + k * 16 + 8 + 2 * tq) : 0;
+          qf[h][k][0] = r < R ? *(const uint32_t *)(src + k * 16 + 2 * tq) : 0;
+          qf[h][k][1] = r < R ? *(const uint32_t *)(src + k * 16 + 8 + 2 * tq) : 0;
         }
       } else {
-        uint2 x[KS];
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          x[k] = r < R ? *(const uint2 *)(src + k * 16 + 4 * tq) : make_uint2(0, 0);
+          const uint2 x = r < R ? *(const uint2 *)(src + k * 16 + 4 * tq) : make_uint2(0, 0);
+          qf[h][k][0] = x.x, qf[h][k][1] = x.y;
           // magnitudes of 16-bit floats order as whole numbers
-          top = __vmaxu2(top, __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu));
+          top = __vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
         }
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -222,26 +231,35 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
         const uint32_t ex = f >> 23;  // 2^k <= the largest magnitude < 2^(k + 1), where that is a normal number
         const bool plain = ex == 0 || ex == 255;
         const float down = plain ? 1.f : inv_scale_of(ex);
-        if (!plain) qsc[h] *= __uint_as_float(ex << 23);
+        if (!plain) q_up[h] *= __uint_as_float(ex << 23);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          float y[4];
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t b = (e < 2 ? x[k].x : x[k].y) >> (16 * (e & 1)) & 0xffffu;
-            y[e] = (bf ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((uint16_t)b))) * down;
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t b = qf[h][k][e];
+            const float lo16 = bf ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((uint16_t)b));
+            const float hi16 = bf ? __uint_as_float(b & 0xffff0000u) : __half2float(__ushort_as_half((uint16_t)(b >> 16)));
+            qf[h][k][e] = pack2(lo16 * down, hi16 * down, 0);
           }
-          qf[k][h] = pack2(y[0], y[1], 0);
-          qf[k][h + 2] = pack2(y[2], y[3], 0);
-        }
       }
     }
-    __syncthreads();  // vis; and the last piece's shared memory is free
-    int32_t vis[2] = {sm.vis[g], sm.vis[g + 8]};
-    const int32_t sure = visible(pc.s, 0, p.causal);  // every row sees positions below this
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[NT][4];
+    // scores come with rows 2 tq, 2 tq + 1 of each 8
+    float qsc[NR][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qsc[h][e] = __shfl_sync(0xffffffffu, q_up[h], (2 * tq + e) * 4);
+    __syncthreads();  // vis; and the last piece's shared memory is free
+    const int32_t sure = visible(pc.s, 0, p.causal);  // every row sees positions below this
+    int32_t vis[NR][2];
+    float m[NR][2], l[NR][2], o[NR][KS][4];
+#pragma unroll
+    for (int h = 0; h < NR; ++h) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) vis[h][e] = sm.vis[8 * h + 2 * tq + e], m[h][e] = -INFINITY, l[h][e] = 0.f;
+#pragma unroll
+      for (int n = 0; n < KS; ++n) o[h][n][0] = o[h][n][1] = o[h][n][2] = o[h][n][3] = 0.f;
+    }
 
     int i = 0;
 #pragma unroll 1
@@ -282,119 +300,137 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
             *v = 0;
           }
         }
+        fence_proxy_async_smem();  // before the box that lands here next
         __syncwarp();
       }
-      // ---- scores: lane (g, tq) gets rows g, g + 8 and positions 2 tq, 2 tq + 1 of each 8
+      // ---- scores: lane (g, tq) gets positions g, g + 8 of each 16 and rows 2 tq, 2 tq + 1 of each 8
       // (two sums a tile, all tiles in turn: a product waits some 30 cycles for the one before it in its sum)
-      float s[NK][4], s2[NK][4];
+      float s[NK][NR][4], s2[NK][NR][4];
 #pragma unroll
       for (int n = 0; n < NK; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
-      constexpr int PER = Q8 ? 4 : 2;  // k steps per ldmatrix.x4
+        for (int h = 0; h < NR; ++h)
 #pragma unroll
-      for (int k0 = 0; k0 < KS; k0 += PER)
+          for (int e = 0; e < 4; ++e) s[n][h][e] = s2[n][h][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; k += 2)
 #pragma unroll
         for (int n = 0; n < NK; ++n) {
-          uint32_t b[4];
-          ldsm4(b, ka + chunk_at<RB, KEYS>(8 * n + (ln & 7), k0 * 2 / (Q8 ? 2 : 1) + (ln >> 3)));
+          uint32_t x[2][4];
+          if constexpr (Q8) {  // a chunk is a k step
+            uint32_t b[4];
+            ldsm4(b, ka + chunk_at<RB, KEYS>(16 * n + (ln & 15), k + (ln >> 4)));
 #pragma unroll
-          for (int k = 0; k < PER; ++k) {
-            float(&c)[4] = k & 1 ? s2[n] : s[n];
-            if constexpr (Q8) mma<false>(c, qf[k0 + k], e4m3x2_to_f16x2(b[k] & 0xffffu), e4m3x2_to_f16x2(b[k] >> 16));
-            else mma<BF16>(c, qf[k0 + k], b[2 * k], b[2 * k + 1]);
+            for (int y = 0; y < 2; ++y) {
+              x[y][0] = e4m3x2_to_f16x2(b[2 * y] & 0xffffu), x[y][1] = e4m3x2_to_f16x2(b[2 * y + 1] & 0xffffu);
+              x[y][2] = e4m3x2_to_f16x2(b[2 * y] >> 16), x[y][3] = e4m3x2_to_f16x2(b[2 * y + 1] >> 16);
+            }
+          } else {
+            ldsm4(x[0], ka + chunk_at<RB, KEYS>(16 * n + (ln & 15), 2 * k + (ln >> 4)));
+            ldsm4(x[1], ka + chunk_at<RB, KEYS>(16 * n + (ln & 15), 2 * k + 2 + (ln >> 4)));
+          }
+#pragma unroll
+          for (int h = 0; h < NR; ++h) {
+            mma<BF16>(s[n][h], x[0], qf[h][k][0], qf[h][k][1]);
+            mma<BF16>(s2[n][h], x[1], qf[h][k + 1][0], qf[h][k + 1][1]);
           }
         }
-#pragma unroll
-      for (int n = 0; n < NK; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
       // ---- weights
-      float vx[Q8 ? NK : 1][2];
+      float vx[NK][2];
       const float k_up = Q8 ? scale_of(kb_now) : 1.f, v_up = Q8 ? scale_of(vb_now) : 1.f;  // of position `lane`
       // bounds keep the sum of 2^(s - m) a normal number
       const float v_ex = Q8 ? (float)(vb_now < 87 ? -40 : vb_now > 227 ? 100 : (int)vb_now - 127) : 0.f;
-      float top[2] = {-INFINITY, -INFINITY};
+      float top[NR][2];
+#pragma unroll
+      for (int h = 0; h < NR; ++h) top[h][0] = top[h][1] = -INFINITY;
 #pragma unroll
       for (int n = 0; n < NK; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int key = 8 * n + 2 * tq + e;
+        for (int y = 0; y < 2; ++y) {
+          const int key = 16 * n + 8 * y + g;
           float kx = 1.f, ve = 0.f;
+          vx[n][y] = 1.f;
           if constexpr (Q8) {
             kx = __shfl_sync(0xffffffffu, k_up, key);
-            vx[n][e] = __shfl_sync(0xffffffffu, v_up, key);
+            vx[n][y] = __shfl_sync(0xffffffffu, v_up, key);
             ve = __shfl_sync(0xffffffffu, v_ex, key);
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x = s[n][2 * h + e] * qsc[h];
-            if constexpr (Q8) x *= kx;
-            x = first + key < vis[h] ? x : -INFINITY;
-            s[n][2 * h + e] = x;
-            top[h] = fmaxf(top[h], x + ve);
+          for (int h = 0; h < NR; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = (s[n][h][2 * y + e] + s2[n][h][2 * y + e]) * qsc[h][e];
+              if constexpr (Q8) x *= kx;
+              x = first + key < vis[h][e] ? x : -INFINITY;
+              s[n][h][2 * y + e] = x;
+              top[h][e] = fmaxf(top[h][e], x + ve);
+            }
+        }
+      bool rise = false;
+#pragma unroll
+      for (int h = 0; h < NR; ++h) rise |= top[h][0] > m[h][0] + 8.f || top[h][1] > m[h][1] + 8.f;
+      if (__any_sync(0xffffffffu, rise)) {  // also the first one's (m is -inf)
+#pragma unroll
+        for (int h = 0; h < NR; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = top[h][e];
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            const float to = fmaxf(m[h][e], t), f = ex2(m[h][e] - (to == -INFINITY ? 0.f : to));
+            m[h][e] = to;
+            l[h][e] *= f;
+#pragma unroll
+            for (int n = 0; n < KS; ++n) o[h][n][e] *= f, o[h][n][2 + e] *= f;
           }
-        }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
       }
-      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {  // also the first one's (m is -inf)
+      uint32_t a[NK][NR][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float to = fmaxf(m[h], top[h]), f = ex2(m[h] - (to == -INFINITY ? 0.f : to));
-          m[h] = to;
-          l[h] *= f;
+      for (int h = 0; h < NR; ++h) {
+        const float r0 = m[h][0] == -INFINITY ? 0.f : m[h][0], r1 = m[h][1] == -INFINITY ? 0.f : m[h][1];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
-        }
-      }
-      uint32_t a[NK / 2][4];
+        for (int n = 0; n < NK; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float ref = m[h] == -INFINITY ? 0.f : m[h];
-#pragma unroll
-        for (int n = 0; n < NK; ++n) {
-          const float p0 = ex2(s[n][2 * h] - ref), p1 = ex2(s[n][2 * h + 1] - ref);
-          l[h] += p0 + p1;
-          // a position that the row does not see has weight 0 whatever its scale
-          const int key = first + 8 * n + 2 * tq;
-          const float w0 = Q8 ? (key < vis[h] ? p0 * vx[Q8 ? n : 0][0] : 0.f) : p0;
-          const float w1 = Q8 ? (key + 1 < vis[h] ? p1 * vx[Q8 ? n : 0][1] : 0.f) : p1;
-          a[n >> 1][h + 2 * (n & 1)] = pack2(w0, w1, BF16);
-        }
-      }
-      // ---- weights times V
-#pragma unroll
-      for (int y = 0; y < NK / 2; y += Q8 ? 2 : 1) {
-        if constexpr (Q8) {  // 32 positions; 16 columns a chunk, the even ones in one output tile, the odd ones in the next
-#pragma unroll
-          for (int c = 0; c < RB / 16; ++c) {
-            uint32_t b[4];
-            ldsm4t(b, va + chunk_at<RB, KEYS>(y * 16 + ln, c));
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-#pragma unroll
-              for (int odd = 0; odd < 2; ++odd) {
-                const uint32_t sel = odd ? 0x31 : 0x20;
-                mma<false>(o[2 * c + odd], a[y + z], e4m3x2_to_f16x2(__byte_perm(b[2 * z], 0, sel) & 0xffffu),
-                           e4m3x2_to_f16x2(__byte_perm(b[2 * z + 1], 0, sel) & 0xffffu));
-              }
+          for (int y = 0; y < 2; ++y) {
+            float p0 = ex2(s[n][h][2 * y] - r0), p1 = ex2(s[n][h][2 * y + 1] - r1);
+            l[h][0] += p0;
+            l[h][1] += p1;
+            if constexpr (Q8) {  // a position that the row does not see has weight 0 whatever its scale
+              const int key = first + 16 * n + 8 * y + g;
+              p0 = key < vis[h][0] ? p0 * vx[n][y] : 0.f;
+              p1 = key < vis[h][1] ? p1 * vx[n][y] : 0.f;
+            }
+            a[n][h][y] = transposed(pack2(p0, p1, BF16));
           }
-        } else {  // 16 positions, two chunks of 8 columns a load
+      }
+      // ---- V^T times weights
 #pragma unroll
-          for (int c = 0; c < RB / 16; c += 2) {
-            uint32_t b[4];
-            ldsm4t(b, va + chunk_at<RB, KEYS>(y * 16 + (ln & 15), c + (ln >> 4)));
-            mma<BF16>(o[c], a[y], b[0], b[1]);
-            mma<BF16>(o[c + 1], a[y], b[2], b[3]);
+      for (int c = 0; c < KS; ++c) {  // 16 columns
+        if constexpr (Q8) {  // a chunk of 32 positions; m index g: column 2 g, m index g + 8: column 2 g + 1
+          uint32_t b[4];
+          ldsm4t(b, va + chunk_at<RB, KEYS>(ln, c));
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t x[4] = {e4m3x2_to_f16x2(__byte_perm(b[2 * n], 0, 0x20) & 0xffffu),
+                                   e4m3x2_to_f16x2(__byte_perm(b[2 * n], 0, 0x31) & 0xffffu),
+                                   e4m3x2_to_f16x2(__byte_perm(b[2 * n + 1], 0, 0x20) & 0xffffu),
+                                   e4m3x2_to_f16x2(__byte_perm(b[2 * n + 1], 0, 0x31) & 0xffffu)};
+#pragma unroll
+            for (int h = 0; h < NR; ++h) mma<false>(o[h][c], x, a[n][h][0], a[n][h][1]);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NK; ++n) {
+            uint32_t x[4];
+            ldsm4t(x, va + chunk_at<RB, KEYS>(16 * n + ((ln >> 4) << 3) + (ln & 7), 2 * c + ((ln >> 3) & 1)));
+#pragma unroll
+            for (int h = 0; h < NR; ++h) mma<BF16>(o[h][c], x, a[n][h][0], a[n][h][1]);
           }
         }
       }
       // ---- the slot's next sub-tile
       if (i + ST < mine) {
-        fence_proxy_async_smem();
         __syncwarp();
         issue(i + ST, slot, next_blk);
         next_blk = i + ST + 1 < mine ? block_at(first_of(i + ST + 1) + br) : 0;
@@ -410,29 +446,34 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
     }
     // ---- the piece's end: the warps' parts through shared memory, then rows out or to the workspace
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if (tq == 0) sm.ml[w][8 * h + g] = make_float2(m[h], l[h]);
-    }
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 4);
+        l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 8);
+        l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 16);
+        if (g == 0) sm.ml[w][8 * h + 2 * tq + e] = make_float2(m[h][e], l[h][e]);
+      }
     ok = __syncthreads_and(ok);
     if (!ok) break;
     // [row][column] of 32 bits, rows padded by 4 (D + 4: no bank twice in what follows); the rings are empty
     constexpr int PS = D + 4;
-    static_assert(sizeof(sm.ring) >= (size_t)kWarps * M * PS * 4, "the parts fit");
+    static_assert(sizeof(sm.ring) >= (size_t)kWarps * 16 * PS * 4, "the parts fit");
     float *parts = (float *)sm.ring;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 8 * h + g;
-      if (r < R) {
-        float *row = parts + (w * M + r) * PS;
+    for (int h = 0; h < NR; ++h)
 #pragma unroll
-        for (int n = 0; n < NT; n += Q8 ? 2 : 1) {
-          if constexpr (Q8) *(float4 *)(row + n * 8 + 4 * tq) = make_float4(o[n][2 * h], o[n + 1][2 * h], o[n][2 * h + 1], o[n + 1][2 * h + 1]);
-          else *(float2 *)(row + n * 8 + 2 * tq) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * h + 2 * tq + e;
+        if (r < R) {
+          float *row = parts + (w * M + r) * PS;
+#pragma unroll
+          for (int n = 0; n < KS; ++n) {
+            if constexpr (Q8) *(float2 *)(row + n * 16 + 2 * g) = make_float2(o[h][n][e], o[h][n][2 + e]);
+            else row[n * 16 + g] = o[h][n][e], row[n * 16 + 8 + g] = o[h][n][2 + e];
+          }
         }
       }
-    }
     __syncthreads();
     const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
     const int64_t slot0 = (int64_t)(2 * cta + (pc.t0 == 0 ? 1 : 0)) * MU;
@@ -487,22 +528,28 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
   if (tid == 0 && p.ws) ws.cut[cta] = cut;
 }
 
-template <bool BF16, int ES, int D>
+template <bool BF16, int ES, int D, int NR>
 cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
   static SmemLimit limit;
   const int smem = (int)sizeof(Smem<ES, D>);
-  auto *k = decode_attend_kernel<BF16, ES, D>;
+  auto *k = decode_attend_kernel<BF16, ES, D, NR>;
   const cudaError_t e = limit.ensure((const void *)k, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, plan.ctas, kThreads, smem, stream, p, *p.map_decode, plan.together);
 }
 
+template <bool BF16, int ES, int D>
+cudaError_t launch_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+  return plan.M == 8 * plan.together ? launch_one<BF16, ES, D, 1>(p, plan, stream)
+                                     : launch_one<BF16, ES, D, 2>(p, plan, stream);
+}
+
 template <bool BF16, int ES>
 cudaError_t launch_type(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
   switch (p.L.head_dim) {
-    case 64: return launch_one<BF16, ES, 64>(p, plan, stream);
-    case 128: return launch_one<BF16, ES, 128>(p, plan, stream);
-    default: return launch_one<BF16, ES, 256>(p, plan, stream);
+    case 64: return launch_rows<BF16, ES, 64>(p, plan, stream);
+    case 128: return launch_rows<BF16, ES, 128>(p, plan, stream);
+    default: return launch_rows<BF16, ES, 256>(p, plan, stream);
   }
 }
 
