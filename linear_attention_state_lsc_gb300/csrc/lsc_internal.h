@@ -286,6 +286,7 @@ struct KvRowsParams {
   void *k, *v;          // dense rows
   int64_t k_stride, v_stride;
   int32_t dtype;
+  FastDiv by_heads;
 };
 cudaError_t launch_kv_append(const KvRowsParams &p, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_gather(const KvRowsParams &p, int num_sms, cudaStream_t stream);

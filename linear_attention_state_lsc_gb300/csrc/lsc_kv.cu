@@ -198,6 +198,7 @@ int check_rows(const lsc_kv_pool *p, int32_t layer, const lsc_kv_batch &b, const
   r->k_stride = k_stride ? k_stride : row;
   r->v_stride = v_stride ? v_stride : row;
   r->dtype = dtype;
+  r->by_heads.set((uint32_t)p->d.num_kv_heads);
   return check_device(p);
 }
 

@@ -7,7 +7,8 @@
 // launch a small one.  A CTA takes a run of consecutive tokens, finds the
 // block row of each once (one thread per token: the sequence by a search of
 // cu_seqlens samples in shared memory, then the block table), then streams the
-// K and V rows of the run, kUnroll 16-byte loads in flight per thread.  A
+// K and V rows of the run, kUnroll 16-byte loads in flight per thread; append's
+// first loads, whose addresses need no search, are issued before it.  A
 // (token, head) row is handled by one group of a warp's lanes, 8 elements each,
 // so an E4M3 row's largest magnitude is a shuffle reduction and the row is
 // never read twice.
@@ -24,7 +25,12 @@ using namespace kv;
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 16;  // tokens of a CTA's run
-constexpr int kUnroll = 4;   // rows in flight per lane group
+// Rows in flight per lane group, and CTAs per SM.  Append computes (the quantisation) and wants few address steps,
+// gather waits for memory and wants threads: 4 rows, 4 CTAs 216 us for 176,644 e4m3 rows, 2 and 8 205 us.
+template <bool APPEND>
+constexpr int kUnroll = APPEND ? 4 : 2;
+template <bool APPEND>
+constexpr int kOcc = APPEND ? 4 : 8;
 
 struct E4M3 {};
 
@@ -103,6 +109,15 @@ struct Eight<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
   }
+  // the largest magnitude as a whole number that orders like it (NaN above infinity), and that as fp32 bits
+  __device__ uint32_t top() const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+    return m;
+  }
+  static __device__ uint32_t bits(uint32_t m) { return m; }
   __device__ void put(const float (&x)[8]) {
     a = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     b = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
@@ -115,6 +130,11 @@ struct Eight16 {
   __device__ void store(void *p) const { *(uint4 *)p = a; }
   __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
   static __device__ float2 two(uint32_t w);
+  __device__ uint32_t top() const {  // two magnitudes a word
+    const uint32_t k = 0x7fff7fffu, m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
+    return max(m & 0xffffu, m >> 16);
+  }
+  static __device__ uint32_t bits(uint32_t m) { return __float_as_uint(two(m).x); }
   static __device__ uint32_t pack(float x, float y);
   __device__ void get(float (&x)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -169,7 +189,7 @@ struct Same<A, A> {
 // APPEND: dense -> pool; else pool -> dense.  lanes = lanes of a row's group
 // (a power of two >= head_dim / 8).
 template <bool APPEND, typename D, typename P>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ KvRowsParams p, int tok, int lanes) {
+__global__ void __launch_bounds__(kThreads, kOcc<APPEND>) rows_kernel(const __grid_constant__ KvRowsParams p, int tok, int lanes) {
   __shared__ Places s;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -177,37 +197,64 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   if (blockIdx.x == 0) check_cu(L, p.b);
   const int32_t t0 = (int32_t)blockIdx.x * tok;
   const int n = p.b.total_tokens - t0 < tok ? p.b.total_tokens - t0 : tok;
-  find_places(L, p.b, t0, n, s);
+  constexpr int kUnroll = lsc::kUnroll<APPEND>;
   const int groups = kThreads / lanes, g = threadIdx.x / lanes, sub = threadIdx.x & (lanes - 1);
   const bool on = sub * 8 < L.head_dim;
   const int rows = n * 2 * L.heads;
   const int64_t head_bytes = (int64_t)L.head_dim * kSize<P>;
+  // Row r of the run is head r % heads of lane (r / heads) % 2 (K, V) of token r / (2 heads); a group's rows are `groups`
+  // apart, so its walk steps by a whole number of tokens and a rest.
+  const int per = 2 * L.heads, step_i = groups / per, step_w = groups - step_i * per;
+  struct Walk {
+    int i, w;  // token of the run; row of the token
+  };
+  auto next = [&](Walk &x) {
+    x.w += step_w;
+    x.i += step_i;
+    if (x.w >= per) x.w -= per, ++x.i;
+  };
+  auto dense_at = [&](const Walk &x) {
+    const int lane = x.w >= L.heads;
+    return (uint8_t *)(lane ? p.v : p.k) + ((int64_t)(t0 + x.i) * (lane ? p.v_stride : p.k_stride) +
+                                            (x.w - lane * L.heads) * L.head_dim + sub * 8) *
+                                               kSize<D>;
+  };
+  Walk ahead, at;
+  ahead.i = g / per;
+  ahead.w = g - ahead.i * per;
+  at = ahead;
+  Eight<D> x[kUnroll];
+  auto load_dense = [&]() {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      x[u].zero();
+      if (ahead.i < n && on) x[u].load(dense_at(ahead));
+      next(ahead);
+    }
+  };
+  if (APPEND) load_dense();
+  find_places(L, p.b, t0, n, s);
   for (int r0 = 0; r0 < rows; r0 += groups * kUnroll) {  // the same trips in every thread: the groups shuffle
-    Eight<D> x[kUnroll];
     uint2 code[kUnroll];
     uint32_t byte[kUnroll];
     int32_t row[kUnroll];
     uint8_t *page[kUnroll];
     int head[kUnroll];
     uint8_t *dense[kUnroll];
+    if (APPEND && r0 > 0) load_dense();
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * groups + g;
-      const int i = r / (2 * L.heads), lane = (r / L.heads) & 1;
-      head[u] = r - (r / L.heads) * L.heads;
-      row[u] = r < rows ? s.row[i] : -2;
-      x[u].zero();
+    for (int u = 0; u < kUnroll; ++u, next(at)) {
+      const int i = at.i, lane = at.w >= L.heads;
+      head[u] = at.w - lane * L.heads;
+      if (!APPEND) dense[u] = dense_at(at);
+      row[u] = i < n ? s.row[i] : -2;
       code[u] = make_uint2(0, 0);
       byte[u] = 0;
       if (row[u] == -2) continue;
       page[u] = (lane ? L.v : L.k) + s.page[i];
-      dense[u] = (uint8_t *)(lane ? p.v : p.k) +
-                 ((int64_t)(t0 + i) * (lane ? p.v_stride : p.k_stride) + (int64_t)head[u] * L.head_dim + sub * 8) *
-                     kSize<D>;
-      if (row[u] == -1 || !on) continue;
-      if constexpr (APPEND) {
-        x[u].load(dense[u]);
-      } else {
+      if constexpr (!APPEND) {
+        x[u].zero();
+        if (row[u] == -1 || !on) continue;
         const uint8_t *src = page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes + sub * 8 * kSize<P>;
         if constexpr (Same<P, E4M3>::value) {
           code[u] = __ldcs((const uint2 *)src);
@@ -229,18 +276,18 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
         uint8_t *dst = row[u] < 0 ? nullptr : page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes +
                                                   sub * 8 * kSize<P>;
         if constexpr (Same<P, E4M3>::value) {
+          uint32_t m = x[u].top();
+          if (lanes == 32) m = __reduce_max_sync(0xffffffffu, m);
+          else
+            for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const uint32_t sb = scale_byte(x[u].bits(m));
+          const float inv = inv_scale_of(sb);
           float f[8];
           x[u].get(f);
-          uint32_t m = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
-          for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const uint32_t sb = scale_byte(m);
-          const float inv = inv_scale_of(sb);
           uint2 c = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
           if (sb != 255) {
-            c.x = to_e4m3x2(f[0] * inv, f[1] * inv) | to_e4m3x2(f[2] * inv, f[3] * inv) << 16;
-            c.y = to_e4m3x2(f[4] * inv, f[5] * inv) | to_e4m3x2(f[6] * inv, f[7] * inv) << 16;
+            c.x = __byte_perm(to_e4m3x2(f[0] * inv, f[1] * inv), to_e4m3x2(f[2] * inv, f[3] * inv), 0x5410);
+            c.y = __byte_perm(to_e4m3x2(f[4] * inv, f[5] * inv), to_e4m3x2(f[6] * inv, f[7] * inv), 0x5410);
           }
           if (dst && on) *(uint2 *)dst = c;
           if (dst && sub == 0) page[u][L.scale_off + (int64_t)row[u] * L.heads + head[u]] = (uint8_t)sb;
