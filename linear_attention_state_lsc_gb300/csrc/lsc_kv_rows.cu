@@ -9,7 +9,9 @@
 // cu_seqlens samples in shared memory, then the block table), then streams the
 // K and V rows of the run, kUnroll 16-byte loads in flight per thread; append's
 // first loads, whose addresses need no search, are issued before it.  A
-// (token, head) row is handled by one group of a warp's lanes, 8 elements each,
+// (token, head) row is handled by one group of a warp's lanes, 8 elements each
+// (16 to and from E4M3: append issued 195 instructions a row and 256 elements with
+// 8, most of them addresses, and that bounded it),
 // so an E4M3 row's largest magnitude is a shuffle reduction and the row is
 // never read twice.
 #include <cuda_runtime.h>
@@ -25,12 +27,13 @@ using namespace kv;
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 16;  // tokens of a CTA's run
+constexpr int kStagedHeads = 64;
 // Rows in flight per lane group, and CTAs per SM.  Append computes (the quantisation) and wants few address steps,
 // gather waits for memory and wants threads: 4 rows, 4 CTAs 216 us for 176,644 e4m3 rows, 2 and 8 205 us.
-template <bool APPEND>
-constexpr int kUnroll = APPEND ? 4 : 2;
-template <bool APPEND>
-constexpr int kOcc = APPEND ? 4 : 8;
+template <bool APPEND, int NV>
+constexpr int kUnroll = (APPEND ? 4 : 2) / (APPEND ? NV : 1);
+template <bool APPEND, int NV>
+constexpr int kOcc = APPEND ? 4 : NV == 1 ? 8 : 6;
 
 struct E4M3 {};
 
@@ -186,20 +189,23 @@ struct Same<A, A> {
 };
 
 // ---- vector kernel: head_dim a multiple of 8 and at most 256 --------------------
-// APPEND: dense -> pool; else pool -> dense.  lanes = lanes of a row's group
-// (a power of two >= head_dim / 8).
-template <bool APPEND, typename D, typename P>
-__global__ void __launch_bounds__(kThreads, kOcc<APPEND>) rows_kernel(const __grid_constant__ KvRowsParams p, int tok, int lanes) {
+// APPEND: dense -> pool; else pool -> dense.  A lane has NV vectors of 8 elements,
+// lanes = lanes of a row's group (a power of two >= head_dim / (8 NV)).
+template <bool APPEND, typename D, typename P, int NV>
+__global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(const __grid_constant__ KvRowsParams p, int tok, int lanes) {
   __shared__ Places s;
+  // scale bytes on their way out, [lane][token][head]: a byte a store would touch a sector each
+  __shared__ uint8_t s_scale[APPEND && Same<P, E4M3>::value ? 2 * kMaxTok * kStagedHeads : 1];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const KvLayer &L = p.L;
   if (blockIdx.x == 0) check_cu(L, p.b);
   const int32_t t0 = (int32_t)blockIdx.x * tok;
   const int n = p.b.total_tokens - t0 < tok ? p.b.total_tokens - t0 : tok;
-  constexpr int kUnroll = lsc::kUnroll<APPEND>;
+  const bool staged = L.heads <= kStagedHeads;
+  constexpr int kUnroll = lsc::kUnroll<APPEND, NV>, EV = 8 * NV;
   const int groups = kThreads / lanes, g = threadIdx.x / lanes, sub = threadIdx.x & (lanes - 1);
-  const bool on = sub * 8 < L.head_dim;
+  const bool on = sub * EV < L.head_dim;
   const int rows = n * 2 * L.heads;
   const int64_t head_bytes = (int64_t)L.head_dim * kSize<P>;
   // Row r of the run is head r % heads of lane (r / heads) % 2 (K, V) of token r / (2 heads); a group's rows are `groups`
@@ -216,57 +222,69 @@ __global__ void __launch_bounds__(kThreads, kOcc<APPEND>) rows_kernel(const __gr
   auto dense_at = [&](const Walk &x) {
     const int lane = x.w >= L.heads;
     return (uint8_t *)(lane ? p.v : p.k) + ((int64_t)(t0 + x.i) * (lane ? p.v_stride : p.k_stride) +
-                                            (x.w - lane * L.heads) * L.head_dim + sub * 8) *
+                                            (x.w - lane * L.heads) * L.head_dim + sub * EV) *
                                                kSize<D>;
   };
   Walk ahead, at;
   ahead.i = g / per;
   ahead.w = g - ahead.i * per;
   at = ahead;
-  Eight<D> x[kUnroll];
+  Eight<D> x[kUnroll][NV];
   auto load_dense = [&]() {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      x[u].zero();
-      if (ahead.i < n && on) x[u].load(dense_at(ahead));
+      const uint8_t *src = dense_at(ahead);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        x[u][v].zero();
+        if (ahead.i < n && on) x[u][v].load(src + v * 8 * kSize<D>);
+      }
       next(ahead);
     }
   };
   if (APPEND) load_dense();
   find_places(L, p.b, t0, n, s);
   for (int r0 = 0; r0 < rows; r0 += groups * kUnroll) {  // the same trips in every thread: the groups shuffle
-    uint2 code[kUnroll];
+    uint2 code[kUnroll][NV];
     uint32_t byte[kUnroll];
     int32_t row[kUnroll];
     uint8_t *page[kUnroll];
-    int head[kUnroll];
+    int head[kUnroll], where[kUnroll];
     uint8_t *dense[kUnroll];
     if (APPEND && r0 > 0) load_dense();
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u, next(at)) {
       const int i = at.i, lane = at.w >= L.heads;
       head[u] = at.w - lane * L.heads;
+      where[u] = lane * n + i;
       if (!APPEND) dense[u] = dense_at(at);
       row[u] = i < n ? s.row[i] : -2;
-      code[u] = make_uint2(0, 0);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) code[u][v] = make_uint2(0, 0);
       byte[u] = 0;
       if (row[u] == -2) continue;
       page[u] = (lane ? L.v : L.k) + s.page[i];
       if constexpr (!APPEND) {
-        x[u].zero();
+#pragma unroll
+        for (int v = 0; v < NV; ++v) x[u][v].zero();
         if (row[u] == -1 || !on) continue;
-        const uint8_t *src = page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes + sub * 8 * kSize<P>;
+        const uint8_t *src = page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes + sub * EV * kSize<P>;
         if constexpr (Same<P, E4M3>::value) {
-          code[u] = __ldcs((const uint2 *)src);
+          if constexpr (NV == 2) {
+            const uint4 c = __ldcs((const uint4 *)src);
+            code[u][0] = make_uint2(c.x, c.y), code[u][1] = make_uint2(c.z, c.w);
+          } else {
+            code[u][0] = __ldcs((const uint2 *)src);
+          }
           byte[u] = __ldcs(page[u] + L.scale_off + (int64_t)row[u] * L.heads + head[u]);
         } else if constexpr (Same<P, D>::value) {
-          x[u].load(src);
+          x[u][0].load(src);
         } else {
           Eight<P> y;
           float f[8];
           y.load(src);
           y.get(f);
-          x[u].put(f);
+          x[u][0].put(f);
         }
       }
     }
@@ -274,30 +292,39 @@ __global__ void __launch_bounds__(kThreads, kOcc<APPEND>) rows_kernel(const __gr
     for (int u = 0; u < kUnroll; ++u) {
       if constexpr (APPEND) {
         uint8_t *dst = row[u] < 0 ? nullptr : page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes +
-                                                  sub * 8 * kSize<P>;
+                                                  sub * EV * kSize<P>;
         if constexpr (Same<P, E4M3>::value) {
-          uint32_t m = x[u].top();
+          uint32_t m = x[u][0].top();
+          if constexpr (NV == 2) m = max(m, x[u][1].top());
           if (lanes == 32) m = __reduce_max_sync(0xffffffffu, m);
           else
             for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const uint32_t sb = scale_byte(x[u].bits(m));
+          const uint32_t sb = scale_byte(x[u][0].bits(m));
           const float inv = inv_scale_of(sb);
-          float f[8];
-          x[u].get(f);
-          uint2 c = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-          if (sb != 255) {
-            c.x = __byte_perm(to_e4m3x2(f[0] * inv, f[1] * inv), to_e4m3x2(f[2] * inv, f[3] * inv), 0x5410);
-            c.y = __byte_perm(to_e4m3x2(f[4] * inv, f[5] * inv), to_e4m3x2(f[6] * inv, f[7] * inv), 0x5410);
+          uint2 c[NV];
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            float f[8];
+            x[u][v].get(f);
+            c[v].x = __byte_perm(to_e4m3x2(f[0] * inv, f[1] * inv), to_e4m3x2(f[2] * inv, f[3] * inv), 0x5410);
+            c[v].y = __byte_perm(to_e4m3x2(f[4] * inv, f[5] * inv), to_e4m3x2(f[6] * inv, f[7] * inv), 0x5410);
+            if (sb == 255) c[v] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
           }
-          if (dst && on) *(uint2 *)dst = c;
-          if (dst && sub == 0) page[u][L.scale_off + (int64_t)row[u] * L.heads + head[u]] = (uint8_t)sb;
+          if (dst && on) {
+            if constexpr (NV == 2) *(uint4 *)dst = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+            else *(uint2 *)dst = c[0];
+          }
+          if (dst && sub == 0) {
+            if (staged) s_scale[where[u] * L.heads + head[u]] = (uint8_t)sb;
+            else page[u][L.scale_off + (int64_t)row[u] * L.heads + head[u]] = (uint8_t)sb;
+          }
         } else if (dst && on) {
           if constexpr (Same<P, D>::value) {
-            x[u].store(dst);
+            x[u][0].store(dst);
           } else {
             Eight<P> y;
             float f[8];
-            x[u].get(f);
+            x[u][0].get(f);
             y.put(f);
             y.store(dst);
           }
@@ -307,18 +334,31 @@ __global__ void __launch_bounds__(kThreads, kOcc<APPEND>) rows_kernel(const __gr
         if constexpr (Same<P, E4M3>::value) {
           if (row[u] >= 0) {
             const float k = scale_of(byte[u]);
-            const uint32_t w[4] = {code[u].x & 0xffffu, code[u].x >> 16, code[u].y & 0xffffu, code[u].y >> 16};
-            float f[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 v = e4m3x2_to_float2(w[e]);
-              f[2 * e] = v.x * k, f[2 * e + 1] = v.y * k;
+            for (int v = 0; v < NV; ++v) {
+              const uint32_t w[4] = {code[u][v].x & 0xffffu, code[u][v].x >> 16, code[u][v].y & 0xffffu, code[u][v].y >> 16};
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 y = e4m3x2_to_float2(w[e]);
+                f[2 * e] = y.x * k, f[2 * e + 1] = y.y * k;
+              }
+              x[u][v].put(f);
             }
-            x[u].put(f);
           }
         }
-        x[u].store(dense[u]);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) x[u][v].store(dense[u] + v * 8 * kSize<D>);
       }
+    }
+  }
+  if constexpr (APPEND && Same<P, E4M3>::value) {
+    if (!staged) return;
+    __syncthreads();
+    for (int j = threadIdx.x; j < 2 * n * L.heads; j += kThreads) {
+      const int w = p.by_heads.div(j), lane = w >= n, i = w - lane * n;
+      if (s.row[i] >= 0)
+        ((lane ? L.v : L.k) + s.page[i])[L.scale_off + (int64_t)s.row[i] * L.heads + (j - w * L.heads)] = s_scale[j];
     }
   }
 }
@@ -390,18 +430,22 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const __grid_constan
   }
 }
 
-template <bool APPEND, typename D, typename P>
-cudaError_t launch_typed(const KvRowsParams &p, int grid, int tok, int lanes, cudaStream_t stream) {
-  return launch_pdl(rows_kernel<APPEND, D, P>, grid, kThreads, 0, stream, p, tok, lanes);
+template <bool APPEND, typename D, typename P, int NV>
+cudaError_t launch_typed(const KvRowsParams &p, int grid, int tok, cudaStream_t stream) {
+  int lanes = 1;
+  while (lanes * 8 * NV < p.L.head_dim) lanes <<= 1;
+  return launch_pdl(rows_kernel<APPEND, D, P, NV>, grid, kThreads, 0, stream, p, tok, lanes);
 }
 
 template <bool APPEND, typename D>
-cudaError_t launch_dense(const KvRowsParams &p, int grid, int tok, int lanes, cudaStream_t stream) {
+cudaError_t launch_dense(const KvRowsParams &p, int grid, int tok, cudaStream_t stream) {
   switch (p.L.dtype) {
-    case LSC_F32: return launch_typed<APPEND, D, float>(p, grid, tok, lanes, stream);
-    case LSC_BF16: return launch_typed<APPEND, D, __nv_bfloat16>(p, grid, tok, lanes, stream);
-    case LSC_F16: return launch_typed<APPEND, D, __half>(p, grid, tok, lanes, stream);
-    default: return launch_typed<APPEND, D, E4M3>(p, grid, tok, lanes, stream);
+    case LSC_F32: return launch_typed<APPEND, D, float, 1>(p, grid, tok, stream);
+    case LSC_BF16: return launch_typed<APPEND, D, __nv_bfloat16, 1>(p, grid, tok, stream);
+    case LSC_F16: return launch_typed<APPEND, D, __half, 1>(p, grid, tok, stream);
+    default:
+      return p.L.head_dim % 16 == 0 ? launch_typed<APPEND, D, E4M3, 2>(p, grid, tok, stream)
+                                    : launch_typed<APPEND, D, E4M3, 1>(p, grid, tok, stream);
   }
 }
 
@@ -420,11 +464,9 @@ cudaError_t launch_rows(const KvRowsParams &p, int num_sms, cudaStream_t stream)
   if (!vec) {
     e = launch_pdl(rows_any_kernel<APPEND>, grid, kThreads, 0, stream, p, tok);
   } else {
-    int lanes = 1;
-    while (lanes * 8 < L.head_dim) lanes <<= 1;
-    e = p.dtype == LSC_F32    ? launch_dense<APPEND, float>(p, grid, tok, lanes, stream)
-        : p.dtype == LSC_BF16 ? launch_dense<APPEND, __nv_bfloat16>(p, grid, tok, lanes, stream)
-                              : launch_dense<APPEND, __half>(p, grid, tok, lanes, stream);
+    e = p.dtype == LSC_F32    ? launch_dense<APPEND, float>(p, grid, tok, stream)
+        : p.dtype == LSC_BF16 ? launch_dense<APPEND, __nv_bfloat16>(p, grid, tok, stream)
+                              : launch_dense<APPEND, __half>(p, grid, tok, stream);
   }
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
