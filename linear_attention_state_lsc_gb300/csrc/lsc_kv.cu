@@ -86,20 +86,19 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
 // of a block, column of 128 bytes, kv head, block; V's blocks follow K's), a box
 // of one column, or of all when it has a whole tile's rows.  A box never leaves its
 // block: its rows are the largest power of two that divides block_tokens, up to
-// the tile's.  128-byte swizzle (64 bytes a row: 64-byte) but for the chunk kernel's
-// E4M3 maps, where a box is plain rows of codes.  Without maps (blocks that are
+// the tile's.  128-byte swizzle (64 bytes a row: 64-byte).  Without maps (blocks that are
 // no multiple of 8 tokens, other types and sizes) the kernels copy rows themselves.
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-bool encode_maps(const lsc_kv_pool *p, EncodeTiled encode, int tile, bool plain, int box, std::vector<CUtensorMap> *out) {
+bool encode_maps(const lsc_kv_pool *p, EncodeTiled encode, int tile, int box, std::vector<CUtensorMap> *out) {
   const lsc_kv_pool_desc &d = p->d;
-  const int row = d.head_dim * (int)p->es, col = plain || row < 128 ? row : 128;  // bytes
+  const int row = d.head_dim * (int)p->es, col = row < 128 ? row : 128;  // bytes
   const CUtensorMapDataType type = d.dtype == LSC_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : d.dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const CUtensorMapSwizzle swizzle = plain ? CU_TENSOR_MAP_SWIZZLE_NONE : col == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUtensorMapSwizzle swizzle = col == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   const cuuint64_t dims[5] = {(cuuint64_t)(col / p->es), (cuuint64_t)d.block_tokens, (cuuint64_t)(row / col),
                               (cuuint64_t)d.num_kv_heads, 2 * (cuuint64_t)d.num_blocks};
   const cuuint64_t strides[4] = {(cuuint64_t)p->row_bytes, (cuuint64_t)col, (cuuint64_t)row, (cuuint64_t)d.page_bytes};
@@ -132,8 +131,8 @@ void make_maps(lsc_kv_pool *p) {
   const int tile = D == 256 ? 64 : 128, keys = lsc::kv_decode_keys(D, (int)p->es);
   const int box = std::min(most, tile), box_decode = std::min(most, keys);
   std::vector<CUtensorMap> maps, decode;
-  if (!encode_maps(p, (EncodeTiled)fn, tile, d.dtype == LSC_E4M3, box, &maps) ||
-      !encode_maps(p, (EncodeTiled)fn, keys, false, box_decode, &decode))
+  if (!encode_maps(p, (EncodeTiled)fn, tile, box, &maps) ||
+      !encode_maps(p, (EncodeTiled)fn, keys, box_decode, &decode))
     return;
   p->maps.swap(maps);
   p->maps_decode.swap(decode);

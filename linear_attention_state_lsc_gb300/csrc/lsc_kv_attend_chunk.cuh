@@ -17,10 +17,18 @@
 //     as tiled TMA boxes of rows x 64 elements (x head_dim / 64 when a block holds
 //     the tile: then one box a tile; coordinates (element, row, column of 64, head,
 //     block) of the layer, element always 0); other block sizes with 16-byte
-//     cp.async.  E4M3 pools: four warps each, codes the same two ways into a staging
-//     buffer, then bf16 with their scale (exact above bf16's smallest normal).  V
-//     rows behind the last position become zeros: here, where they are copied or
-//     converted, else by the softmax threads.
+//     cp.async.  V rows behind the last position become zeros: here, where they
+//     are copied, else by the softmax threads.
+// E4M3 pools run on the 8-bit products as they are (converting the codes to bf16 in
+// front of the tensor cores took 2.4 ms where this takes FP8_MS, bound by the integer
+// pipes).  A row of q, times a power of two that brings it to [128, 256), is the sum
+// of two e4m3 rows: four significant bits each, so bf16 is exact down to 2^-9 of the
+// row's largest magnitude and off by 2^-18 of it below.  Scores take K's scale per
+// position.  A weight is p 2^e with V's scale 2^e, as f16 relative to the row's
+// largest contribution (the reference is that of s + e; the sum takes p), and an f16
+// is the sum of three e5m2 numbers: its upper byte, the upper byte of the rest, and
+// what is left rounded to nearest, together nine bits or more.  So Q K^T takes two
+// 8-bit products, P V three, at twice bf16's rate.
 // head_dim 64 and 128: two row blocks of 128, one per softmax warpgroup, each with
 // its own S and O (S 2 x 128, O 2 x head_dim columns of TMEM), Q in shared memory,
 // tiles of 128: one block's softmax runs under the other's products, and a K/V
@@ -53,16 +61,15 @@ struct Conf {
   static constexpr int M = 128 * NQ;
   static constexpr int TK = D == 256 ? 64 : 128;
   static constexpr bool QT = D == 256;          // Q in TMEM
-  static constexpr int slot = TK * D * 2;       // bytes of a K or V tile
-  static constexpr int NS = Q8 ? (D == 64 ? 6 : D == 128 ? 3 : 4) : (D == 64 ? 8 : D == 128 ? 4 : 6);
-  static constexpr int SD = D == 128 ? 1 : 2;   // E4M3: stages of codes
-  // warps: 0-7 softmax, 8 MMA, 16-bit pools 9 K and 10 V, E4M3 12-15 K and 16-19 V
-  static constexpr int threads = Q8 ? 640 : 384;
-  static constexpr int GW = Q8 ? 4 : 1;         // producer warps of a tile
-  static constexpr bool hold = !Q8 || TK == 64; // a thread keeps all scores of a tile in registers
-  // registers a thread of a softmax warpgroup, the MMA's and E4M3's producers' keeps of those at launch
-  static constexpr int soft = Q8 ? 144 : 208, mma = Q8 ? 56 : 80, prod = 64;
-  static_assert(2 * soft + mma + (Q8 ? 2 * prod : 0) <= (Q8 ? 5 * 96 : 3 * 168), "more registers than the block has");
+  static constexpr int ES = Q8 ? 1 : 2;         // bytes of an element
+  static constexpr int row = D * ES, line = row < 128 ? row : 128;  // bytes of a row, of a swizzled line of it
+  static constexpr int slot = TK * row;         // bytes of a K or V tile
+  static constexpr int NS = Q8 ? (D == 128 ? 6 : 8) : (D == 64 ? 8 : D == 128 ? 4 : 6);
+  static constexpr int SR = Q8 ? 8 : 1;         // E4M3: tiles whose scales are held
+  static constexpr int threads = 384;           // warps: 0-7 softmax, 8 MMA, 9 K, 10 V
+  // registers a thread of a softmax warpgroup and of the others' keeps of the 168 at launch
+  static constexpr int soft = 208, mma = 80;
+  static_assert(2 * soft + mma <= 3 * 168, "more registers than the block has");
   // TMEM columns
   static constexpr int S0 = 0, SN = TK;         // S buffer b at S0 + b * SN; P in its first half
   static constexpr int Q0 = 128;                // QT only
@@ -74,11 +81,13 @@ struct Smem {
   using C = Conf<D, Q8>;
   alignas(1024) uint8_t ring[C::NS][C::slot];
   alignas(1024) uint8_t q[C::QT ? 16 : C::M * D * 2];
-  alignas(128) uint8_t stage[2][Q8 ? C::SD : 1][Q8 ? C::TK * D : 16];  // E4M3: tiles of codes, K's and V's
+  // E4M3, by tile and position: K's scale, V's exponent (bounded) and V's scale
+  alignas(16) float ks[C::SR][Q8 ? C::TK : 4], ve[C::SR][Q8 ? C::TK : 4], vs[C::SR][Q8 ? C::TK : 4];
+  float up[8][32];        // E4M3, by softmax warp: the power of two of a row of q
   alignas(16) uint8_t rows[8][32][80];  // by softmax warp: 64 bytes of each of its rows, between TMEM and memory
-  int32_t bad[3][D];      // first position whose v is NaN, +inf, -inf
+  int32_t bad[Q8 ? 1 : 3][Q8 ? 1 : D];  // first position whose v is NaN, +inf, -inf
   uint64_t full[C::NS], empty[C::NS], sfull[2], pfull[2], qfull[2], odone[2], fin[2], met[2], drain;
-  uint64_t ready[2][2], freed[2][2];  // E4M3: by K or V and stage
+  uint64_t scaled[C::SR];             // E4M3: a tile's scales are there
   uint64_t turn[2][4], swap[2][4];   // one row block: by warpgroup and warp
   float ref[C::NQ == 1 ? 128 : 1];   // a row's reference m
   float2 ml[2][2][C::NQ == 1 ? 128 : 1];  // (m, sum) by piece parity and warpgroup
@@ -93,26 +102,40 @@ struct Smem {
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
   return ((saddr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16;
 }
-constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
-// Instruction descriptor of kind::f16 with an fp32 accumulator: both operands f16 (0) or bf16 (1).
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b_mn_major) {
-  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// (64-byte lines: groups of 512 bytes, 64-byte swizzle.)
+template <int LINE>
+constexpr uint32_t kDescHi = LINE == 64 ? (512 >> 4) | 1u << 14 | 4u << 29 : (1024 >> 4) | 1u << 14 | 2u << 29;
+// Instruction descriptor with an fp32 accumulator.  kind::f16: a, b = 0 f16, 1 bf16; kind::f8f6f4: 0 e4m3, 1 e5m2.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, uint32_t a, uint32_t b, bool b_mn_major) {
+  return (1u << 4) | a << 7 | b << 10 | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(kDescHi),
-      "r"(acc)
-      : "memory");
+#define LSC_MMA(NAME, KIND)                                                                                          \
+  __device__ __forceinline__ void NAME##_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t id, uint32_t acc) { \
+    asm volatile(                                                                                                    \
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %4};\n\t"                     \
+        "mov.b64 b, {%2, %4};\n\ttcgen05.mma.cta_group::1.kind::" KIND " [%0], a, b, %3, p;\n\t}" ::"r"(d),        \
+        "r"(a), "r"(b), "r"(id), "r"(hi), "r"(acc)                                                                   \
+        : "memory");                                                                                                 \
+  }                                                                                                                  \
+  __device__ __forceinline__ void NAME##_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t id, uint32_t acc) { \
+    asm volatile(                                                                                                    \
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %4};\n\t"                       \
+        "tcgen05.mma.cta_group::1.kind::" KIND " [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(id),      \
+        "r"(hi), "r"(acc)                                                                                            \
+        : "memory");                                                                                                 \
+  }
+LSC_MMA(mma16, "f16")
+LSC_MMA(mma8, "f8f6f4")
+#undef LSC_MMA
+
+// Byte of 16-byte chunk ch of row r in a swizzled tile of `rows` rows.
+template <int LINE>
+__device__ __forceinline__ uint32_t chunk_at(int rows, int r, int ch) {
+  if constexpr (LINE == 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+  else return (ch >> 3) * (rows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
-__device__ __forceinline__ void mma_ts16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(kDescHi),
-      "r"(acc)
-      : "memory");
-}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -174,15 +197,77 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[32], uint64_t c, uin
   l = add2(l, add2(a[0], a[1]));
 }
 
-// Codes in the high bytes of two halves -> bf16 bits with the same sign, exponent field and mantissa, worth the codes
-// times 2^-120: the exponent bias of e4m3 is 7, of bf16 127, and a subnormal code becomes a subnormal bf16.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2_bits(uint32_t x) {
-  return ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+// v[0..7] -> 8 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ float lo_f(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_f(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+
+// E4M3: 32 scores times K's scales (kept in s); returns the largest of s c + e over the seen ones.
+__device__ __forceinline__ float scale8(uint32_t (&s)[32], const float *ks, const float *ve, uint64_t c, bool mask,
+                                        int32_t seen) {
+#pragma unroll
+  for (int y = 0; y < 32; y += 4) {
+    const ulonglong2 k = *(const ulonglong2 *)(ks + y);
+    const uint64_t a = mul2((uint64_t)s[y] | (uint64_t)s[y + 1] << 32, k.x);
+    const uint64_t b = mul2((uint64_t)s[y + 2] | (uint64_t)s[y + 3] << 32, k.y);
+    s[y] = (uint32_t)a, s[y + 1] = (uint32_t)(a >> 32), s[y + 2] = (uint32_t)b, s[y + 3] = (uint32_t)(b >> 32);
+  }
+  if (mask) hide(s, seen);
+  float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+  for (int y = 0; y < 32; y += 4) {
+    const ulonglong2 e = *(const ulonglong2 *)(ve + y);
+    const uint64_t a = fma2((uint64_t)s[y] | (uint64_t)s[y + 1] << 32, c, e.x);
+    const uint64_t b = fma2((uint64_t)s[y + 2] | (uint64_t)s[y + 3] << 32, c, e.y);
+    t0 = fmaxf(t0, fmaxf(lo_f(a), hi_f(a)));
+    t1 = fmaxf(t1, fmaxf(lo_f(b), hi_f(b)));
+  }
+  return fmaxf(t0, t1);
+}
+
+// E4M3: p = 2^(s c + r) of 32 scores, added to l; p times V's scale as three e5m2 numbers, four a word in q[0..2].
+__device__ __forceinline__ void weights8(const uint32_t (&s)[32], const float *vs, uint64_t c, uint64_t r, bool mask,
+                                         int32_t seen, uint64_t &l, uint32_t (&q)[3][8]) {
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int y = 0; y < 8; ++y) {
+    const ulonglong2 v = *(const ulonglong2 *)(vs + 4 * y);
+    uint32_t h[2], t2[2];
+    uint32_t t0[2], t1[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const int i = 4 * y + 2 * z;
+      const uint64_t x = fma2((uint64_t)s[i] | (uint64_t)s[i + 1] << 32, c, r);
+      const uint64_t p = two(ex2(lo_f(x)), ex2(hi_f(x)));
+      sum[z] = add2(sum[z], p);
+      uint64_t w = mul2(p, z ? v.y : v.x);
+      if (mask) {  // 0 whatever the scale
+        if (i >= seen) w &= 0xffffffff00000000ull;
+        if (i + 1 >= seen) w &= 0xffffffffull;
+      }
+      h[z] = pack2(lo_f(w), hi_f(w), 0);
+      t0[z] = h[z] & 0xff00ff00u;
+      __half2 rest = __hsub2(*reinterpret_cast<const __half2 *>(&h[z]), *reinterpret_cast<const __half2 *>(&t0[z]));
+      t1[z] = *reinterpret_cast<const uint32_t *>(&rest) & 0xff00ff00u;
+      rest = __hsub2(rest, *reinterpret_cast<const __half2 *>(&t1[z]));
+      uint16_t e;
+      asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e) : "r"(*reinterpret_cast<const uint32_t *>(&rest)));
+      t2[z] = e;
+    }
+    q[0][y] = __byte_perm(t0[0], t0[1], 0x7531);
+    q[1][y] = __byte_perm(t1[0], t1[1], 0x7531);
+    q[2][y] = __byte_perm(t2[0], t2[1], 0x5410);
+  }
+  l = add2(l, add2(sum[0], sum[1]));
 }
 
 // Tiled TMA load of one box (this CTA's shared memory), completing on `bar`.
@@ -235,18 +320,19 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], C::GW), mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], 1), mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < C::SR; ++i) mbar_init(&sm.scaled[i], 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.sfull[i], 1), mbar_init(&sm.pfull[i], 4), mbar_init(&sm.qfull[i], NQ == 2 ? 4 : 8);
       mbar_init(&sm.odone[i], 1), mbar_init(&sm.fin[i], 1), mbar_init(&sm.met[i], 4);
-      for (int x = 0; x < 2; ++x) mbar_init(&sm.ready[i][x], 1), mbar_init(&sm.freed[i][x], C::GW);
       for (int x = 0; x < 4; ++x) mbar_init(&sm.turn[i][x], 1), mbar_init(&sm.swap[i][x], 1);
     }
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
     sm.any_bad = 0;
   }
-  for (int i = tid; i < 3 * D; i += C::threads) (&sm.bad[0][0])[i] = INT32_MAX;
+  if (!Q8)
+    for (int i = tid; i < 3 * D; i += C::threads) (&sm.bad[0][0])[i] = INT32_MAX;
   griddep_wait();
   if (tid == 0) griddep_launch_dependents();
   const int ctas = gridDim.x, cta = blockIdx.x;
@@ -268,7 +354,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     const int block = NQ == 2 ? b : 0;                         // row block
     const uint32_t lane = (uint32_t)(pair * 32) << 16;
     const Workspace ws = workspace_at(p.ws, ctas, M);
-    const float c = p.scale_log2;
+    float c = p.scale_log2, c_next = c;  // of this thread's row (E4M3: with q's power of two)
     auto rows_of = [&](const Piece &q) {  // packed rows of the unit
       const int32_t r = q.s.n * p.group - q.block * M;
       return r < M ? r : M;
@@ -284,34 +370,101 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const uint8_t *src = r < rows_of(q) ? (const uint8_t *)p.q + 2 * ((int64_t)(q.s.row0 + tok) * p.q_stride +
                                                                         (int64_t)(q.head * p.group + (R - tok * p.group)) * D)
                                           : nullptr;
-      if (C::QT && src) src += b * D;
       const uint8_t *from[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) from[i] = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)src, i * 8 + oct);
-#pragma unroll 4
-      for (int x = 0; x < (C::QT ? D : 2 * D); x += 64) {  // bytes of a row
-        uint4 y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          y[i] = from[i] ? *(const uint4 *)(from[i] + x + part16) : make_uint4(0, 0, 0, 0);
-        if constexpr (C::QT) {
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) *(uint4 *)&mine_rows[i * 8 + oct][part16] = y[i];
-          __syncwarp();
-          uint32_t v[16];
+      auto load = [&](int i, int x) { return from[i] ? *(const uint4 *)(from[i] + x + part16) : make_uint4(0, 0, 0, 0); };
+      constexpr int bytes = C::QT ? D : 2 * D;     // of a row, this warpgroup's share
+      const int begin = C::QT ? b * D : 0;
+      if constexpr (Q8) {
+        uint32_t top[4] = {0, 0, 0, 0};  // magnitudes of bf16 order as whole numbers, two a word
+#pragma unroll 2
+        for (int x = 0; x < 2 * D; x += 64)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint4 z = *(const uint4 *)&mine_rows[ln][i * 16];
-            v[4 * i] = z.x, v[4 * i + 1] = z.y, v[4 * i + 2] = z.z, v[4 * i + 3] = z.w;
+            const uint4 y = load(i, x);
+            const uint32_t k = 0x7fff7fffu;
+            top[i] = __vmaxu2(top[i], __vmaxu2(__vmaxu2(y.x & k, y.y & k), __vmaxu2(y.z & k, y.w & k)));
           }
-          tc::tmem_st16(tm + lane + C::Q0 + b * (D / 4) + x / 4, v);
-        } else {
-          uint8_t *dst = sm.q + b * 128 * D * 2 + (x >> 7) * 16384;
+        float down[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t t = max(top[i] & 0xffffu, top[i] >> 16);
+          t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
+          t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+          const uint32_t ex = t >> 7;  // 2^(ex - 127) <= the largest magnitude: brought to 2^7, where both powers are normal
+          const bool plain = ex < 8 || ex == 255;
+          down[i] = plain ? 1.f : __uint_as_float((261 - ex) << 23);
+          if ((ln & 3) == 0) sm.up[w][i * 8 + oct] = plain ? 1.f : __uint_as_float((ex - 7) << 23);
+        }
+        __syncwarp();
+        c_next = p.scale_log2 * sm.up[w][ln];
+#pragma unroll 1
+        for (int x = 0; x < bytes; x += 64) {  // 32 elements: 32 bytes of each part
+          uint2 part[4][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int rr = pair * 32 + i * 8 + oct, ch = ((x >> 4) & 4) + (ln & 3);
-            *(uint4 *)(dst + rr * 128 + ((ch ^ (rr & 7)) << 4)) = y[i];
+            const uint4 y = load(i, begin + x);
+            const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float f0 = __uint_as_float(in[e] << 16) * down[i], f1 = __uint_as_float(in[e] & 0xffff0000u) * down[i];
+              hi[e] = to_e4m3x2(f0, f1);
+              const float2 back = e4m3x2_to_float2(hi[e]);
+              lo[e] = to_e4m3x2(f0 - back.x, f1 - back.y);
+            }
+            part[i][0] = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            part[i][1] = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+          }
+          if constexpr (C::QT) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) *(uint2 *)&mine_rows[i * 8 + oct][t * 32 + (ln & 3) * 8] = part[i][t];
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const uint4 y = *(const uint4 *)&mine_rows[ln][t * 32], z = *(const uint4 *)&mine_rows[ln][t * 32 + 16];
+              const uint32_t v[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+              tmem_st8(tm + lane + C::Q0 + t * (D / 4) + (begin + x) / 8, v);
+            }
+          } else {
+            const int at = x / 2 + (ln & 3) * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                *(uint2 *)(sm.q + b * 128 * D * 2 + t * 128 * D +
+                           chunk_at<C::line>(128, pair * 32 + i * 8 + oct, at >> 4) + (at & 8)) = part[i][t];
+          }
+        }
+      } else {
+#pragma unroll 4
+        for (int x = 0; x < bytes; x += 64) {
+          uint4 y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = load(i, begin + x);
+          if constexpr (C::QT) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *(uint4 *)&mine_rows[i * 8 + oct][part16] = y[i];
+            __syncwarp();
+            uint32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 z = *(const uint4 *)&mine_rows[ln][i * 16];
+              v[4 * i] = z.x, v[4 * i + 1] = z.y, v[4 * i + 2] = z.z, v[4 * i + 3] = z.w;
+            }
+            tc::tmem_st16(tm + lane + C::Q0 + b * (D / 4) + x / 4, v);
+          } else {
+            uint8_t *dst = sm.q + b * 128 * D * 2 + (x >> 7) * 16384;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rr = pair * 32 + i * 8 + oct, ch = ((x >> 4) & 4) + (ln & 3);
+              *(uint4 *)(dst + rr * 128 + ((ch ^ (rr & 7)) << 4)) = y[i];
+            }
           }
         }
       }
@@ -328,8 +481,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     if (have && block * 128 < rows_of(pc)) load_q(pc);
     uint32_t it = 0;     // tiles this row block has been through
     uint32_t slots = 0;  // ring slots of the pieces before this one, modulo 2 NS
-    uint32_t meets = 0, done = 0, turns = 0;
+    uint32_t meets = 0, done = 0, turns = 0, tiles = 0;  // tiles: of the pieces before this one
     while (have && ok) {
+      c = c_next;
       const int nt = pc.t1 - pc.t0, rows = rows_of(pc);
       const bool mine = block * 128 < rows;
       const int r = block * 128 + row;
@@ -353,33 +507,52 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         const bool mask = first + TK > full_to || !rows_all;
         const int32_t seen = vis - first;
         constexpr int NC = TK / 32;                 // chunks of 32 columns
-        uint32_t s[C::hold ? NC : 2][32];
+        const uint32_t tile = tiles + j, sr = tile % C::SR;  // E4M3: where its scales are
+        const int32_t last = first + TK < pc.s.kv ? first + TK : pc.s.kv;
+        if (Q8 && !(ok = wait_warp(&sm.scaled[sr], tile / C::SR, limit))) break;
+        if (Q8 && (last > sure || last < first + TK)) {
+          // Codes of NaN where some row does not see the position, and whatever lies behind the last one, become zeros;
+          // the scale says NaN to the rows that see it.  Every warp looks at the whole tile, so none waits for another.
+          const uint32_t vi = slots + 2 * j + 1;
+          const int slot = (int)(vi % NS);
+          if (!(ok = wait_warp(&sm.full[slot], vi / NS, limit))) break;
+          constexpr int CH = C::row / 16;
+#pragma unroll 1
+          for (int i = (sure > first ? sure - first : 0) * CH + ln; i < TK * CH; i += 32) {
+            const int key = i / CH;
+            uint4 *at = (uint4 *)(sm.ring[slot] + chunk_at<C::line>(TK, key, i % CH));
+            const uint4 v = *at;
+            const uint32_t k = 0x7f7f7f7fu, one = 0x01010101u;
+            const bool nan = ((((v.x & k) + one) | ((v.y & k) + one) | ((v.z & k) + one) | ((v.w & k) + one)) & 0x80808080u) != 0;
+            if (key < last - first && !nan) continue;
+            if (key < last - first) {
+              *(volatile float *)&sm.vs[sr][key] = __uint_as_float(0x7fc00000u);
+              __threadfence_block();
+            }
+            *at = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const uint64_t c2 = two(c, c);
+        uint32_t s[NC][32];
         float top;
         tc::tmem_ld32(sa, s[0]);
         wait_ld(s[0]);
-        if constexpr (C::hold) {
 #pragma unroll
-          for (int x = 1; x < NC; ++x) tc::tmem_ld32(sa + 32 * x, s[x]);
-          if (mask) hide(s[0], seen);
-          top = top_of(s[0]);
+        for (int x = 1; x < NC; ++x) tc::tmem_ld32(sa + 32 * x, s[x]);
+        auto look_at = [&](int x) {
+          if constexpr (Q8) return scale8(s[x], &sm.ks[sr][32 * x], &sm.ve[sr][32 * x], c2, mask, seen - 32 * x);
+          if (mask) hide(s[x], seen - 32 * x);
+          return top_of(s[x]);
+        };
+        top = look_at(0);
 #pragma unroll
-          for (int x = 1; x < NC; ++x) {
-            wait_ld(s[x]);
-            if (mask) hide(s[x], seen - 32 * x);
-            top = fmaxf(top, top_of(s[x]));
-          }
-        } else {  // twice through TMEM, the next chunk on its way while one is looked at
-          top = -INFINITY;
-#pragma unroll
-          for (int x = 0; x < NC; ++x) {
-            if (x + 1 < NC) tc::tmem_ld32(sa + 32 * x + 32, s[(x + 1) & 1]);
-            if (mask) hide(s[x & 1], seen - 32 * x);
-            top = fmaxf(top, top_of(s[x & 1]));
-            if (x + 1 < NC) wait_ld(s[(x + 1) & 1]);
-          }
-          tc::tmem_ld32(sa, s[0]);
+        for (int x = 1; x < NC; ++x) {
+          wait_ld(s[x]);
+          top = fmaxf(top, look_at(x));
         }
-        const float mt = top * c;  // c > 0
+        const float mt = Q8 ? top : top * c;  // c > 0
         float old = m;             // the reference that l goes by
         if (NQ == 1 && j > 0) {
           if (!(ok = wait_warp(&sm.turn[b][pair], turns++, limit))) break;
@@ -410,37 +583,35 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         }
         const float ref = m == -INFINITY ? 0.f : m;
         if (__any_sync(0xffffffffu, old != m)) l *= ex2(old - ref);
-        const uint64_t c2 = two(c, c), r2 = two(-ref, -ref);
+        const uint64_t r2 = two(-ref, -ref);
         uint64_t l2 = two(0.f, 0.f);
-        if constexpr (!C::hold) wait_ld(s[0]);
 #pragma unroll
         for (int x = 0; x < NC; ++x) {
-          uint32_t q[16];
-          auto &sx = s[C::hold ? x : x & 1];
-          if constexpr (!C::hold) {
-            if (x + 1 < NC) tc::tmem_ld32(sa + 32 * x + 32, s[(x + 1) & 1]);
-            if (mask) hide(sx, seen - 32 * x);
+          if constexpr (Q8) {
+            uint32_t q[3][8];
+            weights8(s[x], &sm.vs[sr][32 * x], c2, r2, mask, seen - 32 * x, l2, q);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) tmem_st8(sa + t * (TK / 4) + 8 * x, q[t]);
+          } else {
+            uint32_t q[16];
+            weights<BF16>(s[x], c2, r2, l2, q);
+            tc::tmem_st16(sa + 16 * x, q);  // over columns that have been read
           }
-          weights<BF16>(sx, c2, r2, l2, q);
-          if constexpr (!C::hold) {
-            if (x + 1 < NC) wait_ld(s[(x + 1) & 1]);
-          }
-          tc::tmem_st16(sa + 16 * x, q);  // over columns that have been read
         }
         const float2 lf = *reinterpret_cast<const float2 *>(&l2);
         l += lf.x + lf.y;
-        const int32_t last = first + TK < pc.s.kv ? first + TK : pc.s.kv;
-        // positions [max(first, sure), last): some row of the unit does not see them; behind last: a 16-bit block's rows
-        // came as they were
-        if (last > sure || (!Q8 && last < first + TK)) {
+        // positions [max(first, sure), last): some row of the unit does not see them; behind last: a block's rows came as
+        // they were
+        if (!Q8 && (last > sure || last < first + TK)) {
           const uint32_t vi = slots + 2 * j + 1;
           const int slot = (int)(vi % NS);
           if (!(ok = wait_warp(&sm.full[slot], vi / NS, limit))) break;
-          if (!Q8)
+          {
             for (int i = row; i < (first + TK - last) * (D / 8); i += 128) {
               const int key = last - first + i / (D / 8), ch = i % (D / 8);
               *(uint4 *)(sm.ring[slot] + (ch >> 3) * (TK * 128) + key * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
             }
+          }
           const int lo = (sure > first ? sure : first) - first, cnt = last - first - lo;  // cnt <= 0: nothing to search
           // an exponent field of ones carries into the sign's place
           constexpr uint32_t E = BF16 ? 0x7f80 : 0x7c00, up = (0x8000 - E) * 0x10001u;
@@ -493,6 +664,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const Piece q = pc;
       cut = cut_of(run, q, cta);
       slots = (slots + 2 * (uint32_t)nt) % (2 * NS);
+      tiles += nt;
       have = next_piece<M, TK>(p, run, pc);
       if (have && block * 128 < rows_of(pc)) load_q(pc);  // this piece's score products are done
       if (mine) {
@@ -505,7 +677,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         const int64_t h = q.head * p.group + (R - tok * p.group), t = q.s.row0 + tok;
         const int64_t slot = (int64_t)(2 * cta + (q.t0 == 0 ? 1 : 0)) * M + r;
         const bool on = r < rows;
-        const bool look = mixed && *(volatile int32_t *)&sm.any_bad != 0;
+        const bool look = !Q8 && mixed && *(volatile int32_t *)&sm.any_bad != 0;
         uint8_t *dst = !on ? nullptr : whole ? (uint8_t *)((uint16_t *)p.out + t * p.out_stride + h * D) : (uint8_t *)(ws.o + slot * D);
         uint8_t *to[4];
 #pragma unroll
@@ -519,14 +691,16 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           wait_ld(o);
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
-          if (look) {
+          if constexpr (!Q8) {
+            if (look) {
 #pragma unroll
-            for (int y = 0; y < 32; ++y) {
-              float v = __uint_as_float(o[y]);
-              if (sm.bad[1][x + y] < vis) v += INFINITY;
-              if (sm.bad[2][x + y] < vis) v -= INFINITY;
-              if (sm.bad[0][x + y] < vis) v = __uint_as_float(0x7fc00000u);
-              o[y] = __float_as_uint(v);
+              for (int y = 0; y < 32; ++y) {
+                float v = __uint_as_float(o[y]);
+                if (sm.bad[1][x + y] < vis) v += INFINITY;
+                if (sm.bad[2][x + y] < vis) v -= INFINITY;
+                if (sm.bad[0][x + y] < vis) v = __uint_as_float(0x7fc00000u);
+                o[y] = __float_as_uint(v);
+              }
             }
           }
           auto rows_out = [&](const uint32_t (&v)[16], int at) {  // 64 bytes of every row
@@ -560,7 +734,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         }
         tc::fence_before_sync();  // these reads before the next piece's products, through pfull
       }
-      if (mixed && have) {  // the next unit starts with a clean list: all softmax warps meet before and after it is cleared
+      if (!Q8 && mixed && have) {  // the next unit starts with a clean list: all softmax warps meet before and after it is cleared
         for (int round = 0; round < 2 && ok; ++round, ++meets) {
           if (round == 1 && *(volatile int32_t *)&sm.any_bad)
             for (int i = tid; i < 3 * D; i += 256) (&sm.bad[0][0])[i] = INT32_MAX;
@@ -573,13 +747,12 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   } else if (w < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma));
   }
-  if ((!Q8 && (w == 9 || w == 10)) || (Q8 && w >= 12)) {
-    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::prod));
+  if (w == 9 || w == 10) {
     // ---------------------------------------------------------------- producers
-    const bool is_k = Q8 ? w < 16 : w == 9;
+    const bool is_k = w == 9;
     const uint8_t *base = is_k ? L.k : L.v;
     Ring<NS> at(is_k ? 0 : 1);
-    const int64_t row_bytes = (int64_t)L.heads * D * (Q8 ? 1 : 2);
+    const int64_t row_bytes = (int64_t)L.heads * C::row;
     int32_t blocks_held = 0;  // of the piece's sequence
     // Block i of the piece's sequence, 0 behind its last position; a bad one is recorded and read as block 0.
     auto load_block = [&](int32_t i) {
@@ -624,14 +797,39 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         far = load_block(base_i + 32 + ln);
       }
     };
+    // E4M3: the scale bytes of a tile's positions lane, lane + 32 ... 127 behind the last one; looked up a tile ahead
+    uint32_t sb[TK / 32];
+    auto load_scales = [&](int j) {
+#pragma unroll
+      for (int g = 0; g < TK / 32; ++g) {
+        const int32_t off = g * 32 + ln, oq = L.by_block.div(off);
+        int32_t q = q0 + oq, rr = r0 + off - oq * L.block_tokens;
+        if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
+        const int64_t page = (int64_t)block_of(q) * L.page;
+        sb[g] = (pc.t0 + j) * TK + off < pc.s.kv ? __ldg(base + page + L.scale_off + (int64_t)rr * L.heads + pc.head) : 127;
+      }
+    };
+    // into tile slot sr of the scales
+    auto put_scales = [&](int sr) {
+#pragma unroll
+      for (int g = 0; g < TK / 32; ++g) {
+        if (is_k) {
+          sm.ks[sr][g * 32 + ln] = scale_of(sb[g]);
+        } else {  // bounds keep the sum of 2^(s - m) a normal number
+          sm.vs[sr][g * 32 + ln] = scale_of(sb[g]);
+          sm.ve[sr][g * 32 + ln] = (float)(sb[g] < 87 ? -40 : sb[g] > 227 ? 100 : (int)sb[g] - 127);
+        }
+      }
+      __syncwarp();
+      if (ln == 0) mbar_arrive(&sm.scaled[sr]);
+    };
     // byte offset in a lane of the row of position `off` of tile j, (oq, orr) = off by blocks; -1 behind the last position
-    auto place = [&](int j, int32_t off, int32_t oq, int32_t orr, uint32_t *sb) {
+    auto place = [&](int j, int32_t off, int32_t oq, int32_t orr) {
       int32_t q = q0 + oq, rr = r0 + orr;
       if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
       const int64_t page = (int64_t)block_of(q) * L.page;
       if ((pc.t0 + j) * TK + off >= pc.s.kv) return (int64_t)-1;
-      if (Q8) *sb = __ldg(base + page + L.scale_off + (int64_t)rr * L.heads + pc.head);
-      return page + (int64_t)rr * row_bytes + (int64_t)pc.head * D * (Q8 ? 1 : 2);
+      return page + (int64_t)rr * row_bytes + (int64_t)pc.head * C::row;
     };
     auto hand_on = [&](int slot) {
       fence_proxy_async_smem();
@@ -640,45 +838,40 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     };
     // the ring's first turn passes at once: the phase before a fresh barrier's first one counts as complete
     auto wait_empty = [&]() { return wait_warp(&sm.empty[at.slot], at.phase ^ 1, limit); };
-    if constexpr (!Q8) {
-      constexpr int CPR = D / 8, RPI = 32 / CPR > 0 ? 32 / CPR : 1;  // 16-byte chunks of a row, rows an instruction
-      constexpr int LAG = (NS - 1) / 2;  // cp.async tiles in flight before the first is handed on
-      // TMA: a box of `box` rows and all columns when a block holds the tile, else of one column of 64 elements, a box a
-      // lane.  box 0: cp.async alone.
-      const int box = p.box_rows, cols = box == TK ? D / 64 : 1, per = D / 64 / cols;
-      const int boxes = box > 0 ? TK / box * per : 0, bc = ln % per, br = ln < boxes ? ln / per * box : 0;
-      const int br_q = L.by_block.div(br), br_r = br - br_q * L.block_tokens;
-      int pending = 0;
-      uint32_t flying = 0;  // slots that TMA has filled (low byte), in which phase last (the next byte)
-      Ring<NS> at_h = at;  // the next tile to hand on
-      while (ok && next_piece<M, TK>(p, run, pc)) {
-        const int nt = pc.t1 - pc.t0;
-        start();
-        for (int j = 0; j < nt; ++j, at.step(), step()) {
-          uint8_t *dst = sm.ring[at.slot];
-          if (box > 0) {
-            int32_t q = q0 + br_q, rr = r0 + br_r;
-            if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
-            const int32_t blk = block_of(q);
-            if (!(ok = wait_empty())) break;
-            if (ln == 0) mbar_arrive_expect_tx(&sm.full[at.slot], C::slot);
-            __syncwarp();
-            if (ln < boxes)
-              tma_load_5d(dst + bc * (TK * 128) + br * 128, &map, 0, rr, bc, pc.head, blk + (is_k ? 0 : L.num_blocks),
-                          &sm.full[at.slot]);
-            flying = flying & ~(0x101u << at.slot) | (1u | at.phase << 8) << at.slot;
-            if (pending > 0) {  // cp.async tiles before this one
-              cp_async_wait<0>();
-              for (; pending > 0; --pending, at_h.step()) hand_on(at_h.slot);
-            }
-            at_h.step();
-            continue;
-          }
+    constexpr int CPR = C::row / 16, RPI = 32 / CPR > 0 ? 32 / CPR : 1;  // 16-byte chunks of a row, rows an instruction
+    constexpr int LAG = (NS - 1) / 2;  // cp.async tiles in flight before the first is handed on
+    // TMA: a box of `box` rows and all lines when a block holds the tile, else of one line, a box a lane.  box 0: cp.async.
+    constexpr int LINES = C::row / C::line;
+    const int box = p.box_rows, per = box == TK ? 1 : LINES;
+    const int boxes = box > 0 ? TK / box * per : 0, bc = ln % per, br = ln < boxes ? ln / per * box : 0;
+    const int br_q = L.by_block.div(br), br_r = br - br_q * L.block_tokens;
+    int pending = 0;
+    uint32_t flying = 0;  // slots that TMA has filled (low byte), in which phase last (the next byte)
+    Ring<NS> at_h = at;   // the next tile to hand on
+    int sr = 0;
+    while (ok && next_piece<M, TK>(p, run, pc)) {
+      const int nt = pc.t1 - pc.t0;
+      start();
+      if (Q8) load_scales(0);
+      for (int j = 0; j < nt; ++j, at.step()) {
+        uint8_t *dst = sm.ring[at.slot];
+        if (box > 0) {
+          int32_t q = q0 + br_q, rr = r0 + br_r;
+          if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
+          const int32_t blk = block_of(q);
+          if (!(ok = wait_empty())) break;
+          if (ln == 0) mbar_arrive_expect_tx(&sm.full[at.slot], C::slot);
+          __syncwarp();
+          if (ln < boxes)
+            tma_load_5d(dst + bc * (TK * 128) + br * C::line, &map, 0, rr, bc, pc.head, blk + (is_k ? 0 : L.num_blocks),
+                        &sm.full[at.slot]);
+          flying = flying & ~(0x101u << at.slot) | (1u | at.phase << 8) << at.slot;
+        } else {
           int64_t row_at[TK / 32];
 #pragma unroll
           for (int g = 0; g < TK / 32; ++g) {
             const int32_t off = g * 32 + ln, oq = L.by_block.div(off);
-            row_at[g] = place(j, off, oq, off - oq * L.block_tokens, nullptr);
+            row_at[g] = place(j, off, oq, off - oq * L.block_tokens);
           }
           if (!(ok = wait_empty())) break;
           const int ch = ln % CPR;
@@ -688,8 +881,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
             for (int i = 0; i < 32; i += RPI) {
               const int r = i + ln / CPR;
               const int64_t a = __shfl_sync(0xffffffffu, row_at[g], r);
-              cp_async16_or_zero(smem_u32(dst + (ch >> 3) * (TK * 128) + (g * 32 + r) * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                                 base + (a < 0 ? 0 : a) + ch * 16, a >= 0);
+              cp_async16_or_zero(smem_u32(dst + chunk_at<C::line>(TK, g * 32 + r, ch)), base + (a < 0 ? 0 : a) + ch * 16, a >= 0);
             }
           cp_async_commit();
           if (++pending > LAG) {
@@ -699,120 +891,26 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
             --pending;
           }
         }
+        if (Q8) {
+          put_scales(sr);
+          if (++sr == C::SR) sr = 0;
+        }
+        step();
+        if (Q8 && j + 1 < nt) load_scales(j + 1);
       }
-      cp_async_wait<0>();
-      for (; ok && pending > 0; --pending, at_h.step()) hand_on(at_h.slot);
-      if (!ok)  // a wait gave up: nothing may be in flight when the CTA leaves
-        for (int i = 0; i < NS; ++i)
-          if (flying >> i & 1) wait_warp(&sm.full[i], flying >> (8 + i), p.drain_limit_ns);
-    } else {
-      // 16 codes (two chunks of the 16-bit row) a lane and pass, through SD stages of codes per kind.  Tiles come by TMA
-      // (the first warp of the four) or with cp.async: each thread copies what it converts itself, so those copies need
-      // no barrier.
-      constexpr uint32_t kNoRow = 256;
-      constexpr int SD = C::SD, LPR = D / 16, RPI = 32 / LPR, RPW = TK / 4, IT = RPW / RPI;
-      const int kind = is_k ? 0 : 1, gw = w & 3, lc = ln % LPR, r_first = gw * RPW;
-      const int32_t off = r_first + (ln < RPW ? ln : 0), oq = L.by_block.div(off), orr = off - oq * L.block_tokens;
-      const int box = p.box_rows, boxes = box > 0 ? TK / box : 0, br = ln < boxes ? ln * box : 0;
-      const int br_q = L.by_block.div(br), br_r = br - br_q * L.block_tokens;
-      uint32_t sb[SD], uses[SD];  // scale bytes by stage (a load's result stays where it lands, so nothing waits for it early)
-      bool tma[SD];
-      int nt = 0, j = 0, left = 0;  // tiles fetched and not converted
-#pragma unroll
-      for (int st = 0; st < SD; ++st) uses[st] = 0, tma[st] = false;
-      auto fetch = [&](int st) {  // the run's next tile into a stage; an empty cp.async group when there is none
-        sb[st] = 127;
-        if (ok && (j < nt || next_piece<M, TK>(p, run, pc))) {
-          if (j >= nt) {
-            nt = pc.t1 - pc.t0;
-            j = 0;
-            start();
-          }
-          const int64_t row_at = place(j, off, oq, orr, &sb[st]);
-          if (row_at < 0) sb[st] = kNoRow;
-          tma[st] = box > 0;
-          if (tma[st]) {
-            int32_t q = q0 + br_q, rr = r0 + br_r;
-            if (rr >= L.block_tokens) rr -= L.block_tokens, ++q;
-            const int32_t blk = block_of(q);
-            if (gw == 0) {  // all four warps have read the stage's last tile
-              ok = wait_warp(&sm.freed[kind][st], uses[st] ^ 1, limit);
-              if (ok && ln == 0) mbar_arrive_expect_tx(&sm.ready[kind][st], TK * D);
-              __syncwarp();
-              if (ok && ln < boxes)
-                tma_load_5d(&sm.stage[kind][st][br * D], &map, 0, rr, 0, pc.head, blk + (is_k ? 0 : L.num_blocks),
-                            &sm.ready[kind][st]);
-            }
-          } else {
-            if (gw == 0) {  // keeps in step with the stage's phases
-              ok = wait_warp(&sm.freed[kind][st], uses[st] ^ 1, limit);
-              if (ok && ln == 0) mbar_arrive(&sm.ready[kind][st]);
-            }
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-              const int rl = i * RPI + ln / LPR;
-              const int64_t a = __shfl_sync(0xffffffffu, row_at, rl);
-              cp_async16_or_zero(smem_u32(&sm.stage[kind][st][(r_first + rl) * D + lc * 16]), base + (a < 0 ? 0 : a) + lc * 16,
-                                 a >= 0);
-            }
-          }
-          ++left;
-          ++j;
-          step();
-        }
-        cp_async_commit();
-      };
-      auto convert = [&](int st, uint8_t *dst, const bool wide) {
-#pragma unroll 4
-        for (int i = 0; i < IT; ++i) {
-          const int rl = i * RPI + ln / LPR, r = r_first + rl;
-          const uint32_t e = __shfl_sync(0xffffffffu, sb[st], rl);
-          // 2^(120 + e - 127) as two bf16; beyond bf16's range 2^120, and the rest in a second product (255: NaN)
-          // a row behind the last position: 0 times whatever finite bits the block holds
-          const uint32_t k1 = e == kNoRow ? 0 : wide && e > 134 ? 0x7b807b80u : (e + 120) * 0x00800080u;
-          const uint32_t k2 = e > 134 && e != kNoRow ? (e == 255 ? 0x7fc07fc0u : e * 0x00800080u) : 0x3f803f80u;
-          const uint4 code = *(const uint4 *)&sm.stage[kind][st][r * D + lc * 16];
-          const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
-          uint32_t o[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            o[x] = mul_bf16x2(e4m3x2_to_bf16x2_bits(__byte_perm(cw[x >> 1], 0, x & 1 ? 0x3424 : 0x1404)), k1);
-            if (wide) o[x] = mul_bf16x2(o[x], k2);
-          }
-          const int ch = 2 * lc;
-          uint8_t *row = dst + (ch >> 3) * (TK * 128) + r * 128;
-          *(uint4 *)(row + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *(uint4 *)(row + ((((ch & 7) + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-      };
-#pragma unroll
-      for (int st = 0; st < SD; ++st) fetch(st);
-      while (ok && left > 0) {
-#pragma unroll
-        for (int st = 0; st < SD; ++st) {
-          if (!ok || left == 0) break;
-          cp_async_wait<SD - 1>();
-          if (!(ok = wait_warp(&sm.ready[kind][st], uses[st], limit)) || !(ok = wait_empty())) break;
-          if (__any_sync(0xffffffffu, sb[st] > 134 && sb[st] != kNoRow)) convert(st, sm.ring[at.slot], true);
-          else convert(st, sm.ring[at.slot], false);
-          hand_on(at.slot);
-          if (ln == 0) mbar_arrive(&sm.freed[kind][st]);
-          uses[st] ^= 1;
-          --left;
-          at.step();
-          fetch(st);
-        }
-      }
-      if (!ok && gw == 0)  // a wait gave up: nothing may be in flight when the CTA leaves
-        for (int st = 0; st < SD; ++st)
-          if (tma[st]) wait_warp(&sm.ready[kind][st], uses[st], p.drain_limit_ns);
-      cp_async_wait<0>();
     }
+    cp_async_wait<0>();
+    for (; ok && pending > 0; --pending, at_h.step()) hand_on(at_h.slot);
+    if (!ok)  // a wait gave up: nothing may be in flight when the CTA leaves
+      for (int i = 0; i < NS; ++i)
+        if (flying >> i & 1) wait_warp(&sm.full[i], flying >> (8 + i), p.drain_limit_ns);
   }
   if (w == 8) {
     // ---------------------------------------------------------------- products
     const bool lead = tc::elect_one();
-    constexpr uint32_t iqk = idesc_f16(128, TK, BF16, false), ipv = idesc_f16(128, D, BF16, true);
+    constexpr uint32_t hi = kDescHi<C::line>;
+    constexpr uint32_t ty = BF16 && !Q8 ? 1 : 0;  // Q8: q and K e4m3, weights e5m2
+    constexpr uint32_t iqk = idesc(128, TK, ty, ty, false), ipv = idesc(128, D, Q8 ? 1 : ty, ty, true);
     Ring<NS> rk(0), rv(1);  // the next K and V tile to wait for
     uint32_t itb[2] = {0, 0}, pieces[2] = {0, 0};
     const uint32_t ring0 = smem_u32(sm.ring[0]), q0 = smem_u32(sm.q);
@@ -831,11 +929,22 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       if (lead) {
         const uint32_t kd = desc_lo(ring0 + slot * C::slot, 16), qd = desc_lo(q0 + b * 128 * D * 2, 16);
         const uint32_t d = tm + C::S0 + sb * C::SN;
+        if constexpr (Q8) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t kk = kd + ((k >> 2) * (TK * 128) + (k & 3) * 32) / 16;
-          if constexpr (C::QT) mma_ts16(d, tm + C::Q0 + k * 8, kk, iqk, k > 0);
-          else mma_ss16(d, qd + ((k >> 2) * 16384 + (k & 3) * 32) / 16, kk, iqk, k > 0);
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              const uint32_t kk = kd + ((k >> 2) * (TK * 128) + (k & 3) * 32) / 16;
+              if constexpr (C::QT) mma8_ts(d, tm + C::Q0 + t * (D / 4) + k * 8, kk, hi, iqk, t + k > 0);
+              else mma8_ss(d, qd + (t * 128 * D + k * 32) / 16, kk, hi, iqk, t + k > 0);
+            }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t kk = kd + ((k >> 2) * (TK * 128) + (k & 3) * 32) / 16;
+            if constexpr (C::QT) mma16_ts(d, tm + C::Q0 + k * 8, kk, hi, iqk, k > 0);
+            else mma16_ss(d, qd + ((k >> 2) * 16384 + (k & 3) * 32) / 16, kk, hi, iqk, k > 0);
+          }
         }
         tc::mma_commit(&sm.sfull[sb]);
       }
@@ -843,9 +952,17 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     auto values = [&](int b, int sb, int slot, bool fresh, bool last) {  // O[b] (+)= P[sb] V
       if (lead) {
         const uint32_t vd = desc_lo(ring0 + slot * C::slot, TK * 128);
+        const uint32_t od = tm + C::O0 + b * D, pa = tm + C::S0 + sb * C::SN;
+        if constexpr (Q8) {
 #pragma unroll
-        for (int k = 0; k < TK / 16; ++k)
-          mma_ts16(tm + C::O0 + b * D, tm + C::S0 + sb * C::SN + k * 8, vd + k * (2048 / 16), ipv, !(fresh && k == 0));
+          for (int t = 0; t < 3; ++t)
+#pragma unroll
+            for (int k = 0; k < TK / 32; ++k)
+              mma8_ts(od, pa + t * (TK / 4) + k * 8, vd + k * (32 * C::line / 16), hi, ipv, !(fresh && t + k == 0));
+        } else {
+#pragma unroll
+          for (int k = 0; k < TK / 16; ++k) mma16_ts(od, pa + k * 8, vd + k * (2048 / 16), hi, ipv, !(fresh && k == 0));
+        }
         tc::mma_commit(&sm.odone[b]);
         if (last) tc::mma_commit(&sm.fin[b]);
       }
