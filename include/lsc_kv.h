@@ -222,9 +222,10 @@ typedef struct {
  * last token, do not enter, whatever they hold.  Sums and softmax statistics
  * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded to 16 bits
  * before they meet v.  Two calls with the same inputs give the same bits.
- * A sequence that exceeds max_seq_tokens or max_kv_tokens is recorded as
- * INVALID_ARG in the status word and taken to have no cached tokens.  If a bounded
- * device wait expires (DEV_TIMEOUT in the status word), out and lse are
+ * A sequence that exceeds max_kv_tokens is recorded as INVALID_ARG in the status
+ * word and taken to have no cached tokens; one that exceeds max_seq_tokens is
+ * recorded too, and its rows of out and lse stay as they are.  If a bounded device
+ * wait expires (DEV_TIMEOUT in the status word), out and lse are
  * unspecified.
  * Supported: head_dim <= 512.  Pools of q's 16-bit type, and E4M3 pools with
  * 16-bit q, at head_dim 64, 128 and 256, with q and out 16-byte aligned in base

@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(const __grid_co
     const int32_t i = seq_of_row(p.b, t);
     if (i < 0) continue;  // the whole CTA
     const Seq s = attend_seq(L, p.b, i, p.max_seq, p.max_kv);
+    if (t - s.row0 >= s.n) continue;  // a sequence with lengths that were recorded: its rows stay as they are
     const int32_t vis = visible(s, t - s.row0, p.causal), kh = p.by_group.div(h);
     const int32_t *table = p.b.table + (int64_t)i * p.b.max_blocks;
     float q[NE], o[NE], m = -INFINITY, l = 0.f;

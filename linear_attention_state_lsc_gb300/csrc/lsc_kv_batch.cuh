@@ -39,7 +39,8 @@ __device__ __forceinline__ int32_t seq_of_row(const KvBatch &b, int32_t t) {
 
 // A sequence as attend sees it: its first dense row, its new tokens and its
 // cached tokens.  Lengths outside the host's bounds are recorded: too many
-// cached tokens count as none, too many new ones as none.
+// cached tokens count as none (its rows see nothing), and a sequence of too many
+// new ones has no rows (they stay as they are).
 struct Seq {
   int32_t row0, n, kv;
 };
@@ -58,7 +59,7 @@ __device__ __forceinline__ Seq attend_seq(const KvLayer &L, const KvBatch &b, in
   return s;
 }
 
-// Positions that new token j of the sequence sees: [0, result).
+// Positions that new token j (< n) of the sequence sees: [0, result), result <= kv.
 __device__ __forceinline__ int32_t visible(const Seq &s, int32_t j, int32_t causal) {
   if (!causal) return s.kv;
   const int32_t v = s.kv - s.n + j + 1;  // both lengths are below 2^31 and j < n

@@ -384,6 +384,23 @@ def test_bounds_that_do_not_hold_are_recorded(lsc):
         assert (out[1] == 0).all() and torch.isinf(ls[1]).all()
 
 
+@pytest.mark.parametrize("pool,dtype,G,bound", [(L.LSC_F32, L.LSC_F32, 2, 1), (L.LSC_BF16, L.LSC_BF16, 4, 2),
+                                                (L.LSC_E4M3, L.LSC_F16, 8, 2), (L.LSC_F16, L.LSC_F16, 32, 2),
+                                                (L.LSC_BF16, L.LSC_BF16, 64, 2), (L.LSC_E4M3, L.LSC_BF16, 64, 2)])
+def test_a_sequence_of_too_many_new_tokens_stays_as_it_was(lsc, pool, dtype, G, bound):
+    """Every form of the kernel; the sequence's table row is the last one and full, so reading on would leave it."""
+    rng = np.random.default_rng(70)
+    b = Batch(rng, [bound, 9], [40, 16 * 12], 16, 40)
+    assert b.table.shape[1] == 12
+    host = filled(rng, b, 40, 16, 1, 64, pool)
+    q, qx = dense(rng.standard_normal((b.T, G, 64)), dtype)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, dtype, G, 0.125, True, max_seq_tokens=bound)
+        assert dev.status() == L.LSC_ERR_INVALID_ARG
+        check_attend(host, 1, b, qx, dtype, 0.125, True, out, ls, rows=np.r_[0:bound])
+        assert (out[bound:] == 7).all() and (ls[bound:] == 7).all()
+
+
 @pytest.mark.parametrize("pool", [L.LSC_BF16, L.LSC_E4M3], ids=NAME.get)
 def test_a_step_on_its_own_stream_in_a_graph(lsc, pool):
     """append, attend and gather of each layer, captured once on a side stream and replayed with other lengths, tables
