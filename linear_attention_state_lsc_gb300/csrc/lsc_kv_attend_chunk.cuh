@@ -4,11 +4,12 @@
 // 4 * head_dim operations a (row, position) pair, and K/V tiles that serve 128 or
 // 256 rows: the 5th-generation tensor cores bound it.  One CTA per SM walks its
 // run of tiles of TK positions with the warps in roles:
-//   * two softmax warpgroups, one thread a row: wait for the scores S = Q K^T of a
-//     tile in TMEM, weights 2^(s - m) to 16 bits back into the same TMEM columns,
-//     sum in a register.  m is a reference, not the exact maximum: O is rescaled
-//     (in TMEM, by these threads) only when a row's maximum rose by more than 2^8,
-//     so a weight is at most 2^8 and the rescale is rare after the first tiles.
+//   * two softmax warpgroups: a thread waits for the scores S = Q K^T of its row in
+//     TMEM, puts weights 2^(s - m) at 16 bits back into the same TMEM columns and
+//     keeps the sum in a register.  m is a reference, not the exact maximum: O is
+//     rescaled (in TMEM, by these threads) only when a row's maximum rose by more
+//     than 2^8, so a weight is at most 2^8 and the rescale is rare after the first
+//     tiles.
 //   * one MMA warp: S = Q K^T, O += P V with P as the TMEM operand, issued so that
 //     the products of one tile run while the softmax of another does.
 //   * producers: K and V rows through the block table into a shared-memory ring
@@ -20,7 +21,7 @@
 //     cp.async.  V rows behind the last position become zeros: here, where they
 //     are copied, else by the softmax threads.
 // E4M3 pools run on the 8-bit products as they are (converting the codes to bf16 in
-// front of the tensor cores took 2.4 ms where this takes FP8_MS, bound by the integer
+// front of the tensor cores took 2.4 ms where this takes 1.60 ms, bound by the integer
 // pipes).  A row of q, times a power of two that brings it to [128, 256), is the sum
 // of two e4m3 rows: four significant bits each, so bf16 is exact down to 2^-9 of the
 // row's largest magnitude and off by 2^-18 of it below.  Scores take K's scale per
@@ -29,15 +30,18 @@
 // is the sum of three e5m2 numbers: its upper byte, the upper byte of the rest, and
 // what is left rounded to nearest, together nine bits or more.  So Q K^T takes two
 // 8-bit products, P V three, at twice bf16's rate.
-// head_dim 64 and 128: two row blocks of 128, one per softmax warpgroup, each with
-// its own S and O (S 2 x 128, O 2 x head_dim columns of TMEM), Q in shared memory,
-// tiles of 128: one block's softmax runs under the other's products, and a K/V
-// tile is fetched once for 256 rows.
+// head_dim 64 and 128: two row blocks of 128, one warpgroup and a thread a row
+// each, with its own S and O (S 2 x 128, O 2 x head_dim columns of TMEM), Q in
+// shared memory, tiles of 128: one block's softmax runs under the other's
+// products, and a K/V tile is fetched once for 256 rows.
 // head_dim 256: O takes 256 columns, so one row block, tiles of 64 and two S
-// buffers; the warpgroups take the tiles in turn, so that a tile's softmax has two
-// tiles' time, and hand the reference m on through shared memory.  Q is a TMEM
-// operand (128 columns), which leaves shared memory to K and V and halves what the
-// score products read from it.
+// buffers in turn; Q is a TMEM operand (128 columns), which leaves shared memory
+// to K and V and halves what the score products read from it.  The way from S to
+// P is what the products wait for here, so it is made short: both warpgroups take
+// each tile, a thread half the columns of a row, and tell each other the largest
+// of their halves (bf16, four prompts on a 16k prefix, 12 q heads a kv head: 819
+// us; 890 with a thread a row and the tiles in turn; the pair of head_dim 128
+// with sixteen softmax warps of 104 registers: 1928 us against 1350, so not there).
 //
 // Positions that only some rows of a unit see may hold infinities and NaN: see
 // lsc_kv_attend_rows.cuh; here the softmax threads search such a tile's v.
@@ -66,7 +70,9 @@ struct Conf {
   static constexpr int slot = TK * row;         // bytes of a K or V tile
   static constexpr int NS = Q8 ? (D == 128 ? 6 : 8) : (D == 64 ? 8 : D == 128 ? 4 : 6);
   static constexpr int SR = Q8 ? 8 : 1;         // E4M3: tiles whose scales are held
-  static constexpr int threads = 384;           // warps: 0-7 softmax, 8 MMA, 9 K, 10 V
+  static constexpr int threads = 384;           // warps: 0-7 softmax, 8 MMA, 9 K, 10 V, 11 idle
+  static constexpr int NH = 2 / NQ;             // threads of a row
+  static constexpr int HC = TK / NH;            // columns of a thread
   // registers a thread of a softmax warpgroup and of the others' keeps of the 168 at launch
   static constexpr int soft = 208, mma = 80;
   static_assert(2 * soft + mma <= 3 * 168, "more registers than the block has");
@@ -86,11 +92,10 @@ struct Smem {
   float up[8][32];        // E4M3, by softmax warp: the power of two of a row of q
   alignas(16) uint8_t rows[8][32][80];  // by softmax warp: 64 bytes of each of its rows, between TMEM and memory
   int32_t bad[Q8 ? 1 : 3][Q8 ? 1 : D];  // first position whose v is NaN, +inf, -inf
-  uint64_t full[C::NS], empty[C::NS], sfull[2], pfull[2], qfull[2], odone[2], fin[2], met[2], drain;
+  uint64_t full[C::NS], empty[C::NS], sfull[2], pfull[2], qfull[2], odone[2], fin[2], met, drain;
   uint64_t scaled[C::SR];             // E4M3: a tile's scales are there
-  uint64_t turn[2][4], swap[2][4];   // one row block: by warpgroup and warp
-  float ref[C::NQ == 1 ? 128 : 1];   // a row's reference m
-  float2 ml[2][2][C::NQ == 1 ? 128 : 1];  // (m, sum) by piece parity and warpgroup
+  uint64_t turn[8];             // a warp's partner has told its part of a row's maximum or sum
+  float told[2][8][32];         // those, by turn
   uint32_t tmem;
   int32_t any_bad;
   RunScratch run;
@@ -323,10 +328,11 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], 1), mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < C::SR; ++i) mbar_init(&sm.scaled[i], 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.sfull[i], 1), mbar_init(&sm.pfull[i], 4), mbar_init(&sm.qfull[i], NQ == 2 ? 4 : 8);
-      mbar_init(&sm.odone[i], 1), mbar_init(&sm.fin[i], 1), mbar_init(&sm.met[i], 4);
-      for (int x = 0; x < 4; ++x) mbar_init(&sm.turn[i][x], 1), mbar_init(&sm.swap[i][x], 1);
+      mbar_init(&sm.sfull[i], 1), mbar_init(&sm.pfull[i], 4 * C::NH), mbar_init(&sm.qfull[i], 4 * C::NH);
+      mbar_init(&sm.odone[i], 1), mbar_init(&sm.fin[i], 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&sm.turn[i], 1);
+    mbar_init(&sm.met, 8);
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
     sm.any_bad = 0;
@@ -350,9 +356,10 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   if (w < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft));
     // ---------------------------------------------------------------- softmax
-    const int b = w >> 2, pair = w & 3, row = pair * 32 + ln;  // warpgroup; row of its row block
-    const int block = NQ == 2 ? b : 0;                         // row block
-    const uint32_t lane = (uint32_t)(pair * 32) << 16;
+    const int block = NQ == 2 ? w >> 2 : 0, half = NQ == 2 ? 0 : w >> 2;  // row block; which half of the columns
+    const int quad = w & 3, row = quad * 32 + ln;  // row of the block
+    const int partner = w ^ 4;                     // NH == 2: the warp with the other half of the same rows
+    const uint32_t lane = (uint32_t)(quad * 32) << 16;
     const Workspace ws = workspace_at(p.ws, ctas, M);
     float c = p.scale_log2, c_next = c;  // of this thread's row (E4M3: with q's power of two)
     auto rows_of = [&](const Piece &q) {  // packed rows of the unit
@@ -374,8 +381,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
 #pragma unroll
       for (int i = 0; i < 4; ++i) from[i] = (const uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)src, i * 8 + oct);
       auto load = [&](int i, int x) { return from[i] ? *(const uint4 *)(from[i] + x + part16) : make_uint4(0, 0, 0, 0); };
-      constexpr int bytes = C::QT ? D : 2 * D;     // of a row, this warpgroup's share
-      const int begin = C::QT ? b * D : 0;
+      constexpr int bytes = 2 * D / C::NH;         // of a row, this warpgroup's share
+      const int begin = half * bytes;
       if constexpr (Q8) {
         uint32_t top[4] = {0, 0, 0, 0};  // magnitudes of bf16 order as whole numbers, two a word
 #pragma unroll 2
@@ -431,13 +438,13 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
               tmem_st8(tm + lane + C::Q0 + t * (D / 4) + (begin + x) / 8, v);
             }
           } else {
-            const int at = x / 2 + (ln & 3) * 8;
+            const int at = (begin + x) / 2 + (ln & 3) * 8;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int t = 0; t < 2; ++t)
-                *(uint2 *)(sm.q + b * 128 * D * 2 + t * 128 * D +
-                           chunk_at<C::line>(128, pair * 32 + i * 8 + oct, at >> 4) + (at & 8)) = part[i][t];
+                *(uint2 *)(sm.q + block * 128 * D * 2 + t * 128 * D +
+                           chunk_at<C::line>(128, quad * 32 + i * 8 + oct, at >> 4) + (at & 8)) = part[i][t];
           }
         }
       } else {
@@ -457,12 +464,12 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
               const uint4 z = *(const uint4 *)&mine_rows[ln][i * 16];
               v[4 * i] = z.x, v[4 * i + 1] = z.y, v[4 * i + 2] = z.z, v[4 * i + 3] = z.w;
             }
-            tc::tmem_st16(tm + lane + C::Q0 + b * (D / 4) + x / 4, v);
+            tc::tmem_st16(tm + lane + C::Q0 + (begin + x) / 4, v);
           } else {
-            uint8_t *dst = sm.q + b * 128 * D * 2 + (x >> 7) * 16384;
+            uint8_t *dst = sm.q + block * 128 * D * 2 + ((begin + x) >> 7) * 16384;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int rr = pair * 32 + i * 8 + oct, ch = ((x >> 4) & 4) + (ln & 3);
+              const int rr = quad * 32 + i * 8 + oct, ch = (((begin + x) >> 4) & 4) + (ln & 3);
               *(uint4 *)(dst + rr * 128 + ((ch ^ (rr & 7)) << 4)) = y[i];
             }
           }
@@ -482,6 +489,14 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     uint32_t it = 0;     // tiles this row block has been through
     uint32_t slots = 0;  // ring slots of the pieces before this one, modulo 2 NS
     uint32_t meets = 0, done = 0, turns = 0, tiles = 0;  // tiles: of the pieces before this one
+    auto exchange = [&](float x, float &other) {  // with the thread that has the other half of the row
+      sm.told[turns & 1][w][ln] = x;  // read two turns ago: the partner has arrived for the last one since
+      __syncwarp();
+      if (ln == 0) mbar_arrive(&sm.turn[partner]);
+      if (!wait_warp(&sm.turn[w], turns, limit)) return false;
+      other = sm.told[turns++ & 1][partner][ln];
+      return true;
+    };
     while (have && ok) {
       c = c_next;
       const int nt = pc.t1 - pc.t0, rows = rows_of(pc);
@@ -490,7 +505,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const int32_t R = pc.block * M + r, tok = p.by_group.div(R);
       const int32_t vis = r < rows ? visible(pc.s, tok, p.causal) : 0;
       const int32_t sure = visible(pc.s, p.by_group.div(pc.block * M), p.causal);
-      const int32_t full_to = NQ == 2 && b == 1 && mine
+      const int32_t full_to = NQ == 2 && block == 1 && mine
                                   ? visible(pc.s, p.by_group.div(pc.block * M + 128), p.causal)
                                   : sure;  // every row of this block sees positions below it
       const bool rows_all = (block + 1) * 128 <= rows;
@@ -498,15 +513,15 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       // does the piece reach positions that some row of the unit does not see
       const bool mixed = (pc.s.kv < pc.t1 * TK ? pc.s.kv : pc.t1 * TK) > sure;
       for (int j = 0; j < nt && mine; ++j, ++it) {
-        if (NQ == 1 && (int)(it & 1) != b) continue;  // the other warpgroup's
-        const uint32_t sa = tm + lane + C::S0 + b * C::SN;
+        const int sb = NQ == 2 ? block : (int)(it & 1);
+        const uint32_t s0 = tm + lane + C::S0 + sb * C::SN, sa = s0 + half * C::HC;
         const int32_t first = (pc.t0 + j) * TK;
-        if (!(ok = wait_warp(&sm.sfull[b], NQ == 2 ? it : it >> 1, limit))) break;
+        if (!(ok = wait_warp(&sm.sfull[sb], NQ == 2 ? it : it >> 1, limit))) break;
         tc::fence_after_sync();
         // a column is seen when first + column < vis
         const bool mask = first + TK > full_to || !rows_all;
-        const int32_t seen = vis - first;
-        constexpr int NC = TK / 32;                 // chunks of 32 columns
+        const int32_t seen = vis - first - half * C::HC;  // of this thread's columns
+        constexpr int NC = C::HC / 32;              // chunks of 32 columns
         const uint32_t tile = tiles + j, sr = tile % C::SR;  // E4M3: where its scales are
         const int32_t last = first + TK < pc.s.kv ? first + TK : pc.s.kv;
         if (Q8 && !(ok = wait_warp(&sm.scaled[sr], tile / C::SR, limit))) break;
@@ -542,7 +557,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
 #pragma unroll
         for (int x = 1; x < NC; ++x) tc::tmem_ld32(sa + 32 * x, s[x]);
         auto look_at = [&](int x) {
-          if constexpr (Q8) return scale8(s[x], &sm.ks[sr][32 * x], &sm.ve[sr][32 * x], c2, mask, seen - 32 * x);
+          if constexpr (Q8) return scale8(s[x], &sm.ks[sr][half * C::HC + 32 * x], &sm.ve[sr][half * C::HC + 32 * x], c2, mask, seen - 32 * x);
           if (mask) hide(s[x], seen - 32 * x);
           return top_of(s[x]);
         };
@@ -552,21 +567,22 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           wait_ld(s[x]);
           top = fmaxf(top, look_at(x));
         }
-        const float mt = Q8 ? top : top * c;  // c > 0
-        float old = m;             // the reference that l goes by
-        if (NQ == 1 && j > 0) {
-          if (!(ok = wait_warp(&sm.turn[b][pair], turns++, limit))) break;
-          m = sm.ref[row];
+        if (C::NH == 2) {  // the partner's half of the row (it has read its scores too, so the weights may go over them)
+          float other;
+          if (!(ok = exchange(top, other))) break;
+          top = fmaxf(top, other);
         }
-        if (__any_sync(0xffffffffu, mt > m + 8.f)) {  // also the first tile's (m is -inf)
+        const float mt = Q8 ? top : top * c;  // c > 0
+        if (__any_sync(0xffffffffu, mt > m + 8.f)) {  // also the first tile's (m is -inf); the same in both halves
           const float to = fmaxf(m, mt), f = ex2(m - (to == -INFINITY ? 0.f : to));
           m = to;
+          l *= f;
           if (j > 0) {
             if (!(ok = wait_warp(&sm.odone[block], it - 1, limit))) break;
             tc::fence_after_sync();
-            const uint32_t oa = tm + lane + C::O0 + block * D;
+            const uint32_t oa = tm + lane + C::O0 + block * D + half * (D / C::NH);
 #pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
+            for (int x = 0; x < D / C::NH; x += 32) {
               uint32_t o[32];
               tc::tmem_ld32(oa + x, o);
               wait_ld(o);
@@ -575,27 +591,21 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
               tc::tmem_st32(oa + x, o);
             }
           }
-          if (NQ == 1) sm.ref[row] = m;
-        }
-        if (NQ == 1 && j + 1 < nt) {  // the other warpgroup's next tile goes by this reference
-          __syncwarp();
-          if (ln == 0) mbar_arrive(&sm.turn[b ^ 1][pair]);
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        if (__any_sync(0xffffffffu, old != m)) l *= ex2(old - ref);
         const uint64_t r2 = two(-ref, -ref);
         uint64_t l2 = two(0.f, 0.f);
 #pragma unroll
         for (int x = 0; x < NC; ++x) {
           if constexpr (Q8) {
             uint32_t q[3][8];
-            weights8(s[x], &sm.vs[sr][32 * x], c2, r2, mask, seen - 32 * x, l2, q);
+            weights8(s[x], &sm.vs[sr][half * C::HC + 32 * x], c2, r2, mask, seen - 32 * x, l2, q);
 #pragma unroll
-            for (int t = 0; t < 3; ++t) tmem_st8(sa + t * (TK / 4) + 8 * x, q[t]);
+            for (int t = 0; t < 3; ++t) tmem_st8(s0 + t * (TK / 4) + half * (C::HC / 4) + 8 * x, q[t]);
           } else {
             uint32_t q[16];
             weights<BF16>(s[x], c2, r2, l2, q);
-            tc::tmem_st16(sa + 16 * x, q);  // over columns that have been read
+            tc::tmem_st16(s0 + half * (C::HC / 2) + 16 * x, q);
           }
         }
         const float2 lf = *reinterpret_cast<const float2 *>(&l2);
@@ -607,7 +617,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           const int slot = (int)(vi % NS);
           if (!(ok = wait_warp(&sm.full[slot], vi / NS, limit))) break;
           {
-            for (int i = row; i < (first + TK - last) * (D / 8); i += 128) {
+            for (int i = half * 128 + row; i < (first + TK - last) * (D / 8); i += 128 * C::NH) {
               const int key = last - first + i / (D / 8), ch = i % (D / 8);
               *(uint4 *)(sm.ring[slot] + (ch >> 3) * (TK * 128) + key * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
             }
@@ -621,14 +631,14 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           };
           uint32_t carry = 0;
 #pragma unroll 2
-          for (int i = row; i < cnt * (D / 8); i += 128) {
+          for (int i = half * 128 + row; i < cnt * (D / 8); i += 128 * C::NH) {
             const uint4 v = *vec(i);
             carry |= ((v.x & 0x7fff7fffu) + up) | ((v.y & 0x7fff7fffu) + up) | ((v.z & 0x7fff7fffu) + up) |
                      ((v.w & 0x7fff7fffu) + up);
           }
           if (carry & 0x80008000u) {
 #pragma unroll 1
-            for (int i = row; i < cnt * (D / 8); i += 128) {
+            for (int i = half * 128 + row; i < cnt * (D / 8); i += 128 * C::NH) {
               uint16_t *e = (uint16_t *)vec(i);
 #pragma unroll 1
               for (int x = 0; x < 8; ++x) {
@@ -646,20 +656,13 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (ln == 0) mbar_arrive(&sm.pfull[b]);
+        if (ln == 0) mbar_arrive(&sm.pfull[sb]);
       }
       if (!ok) break;
-      if (NQ == 1) {  // the warpgroups' sums of each row, by the later reference; then both know that Q has been used
-        sm.ml[done & 1][b][row] = make_float2(m, l);
-        __syncwarp();
-        if (ln == 0) mbar_arrive(&sm.swap[b ^ 1][pair]);
-        if (!(ok = wait_warp(&sm.swap[b][pair], done, limit))) break;
-        const float2 x = sm.ml[done & 1][b ^ 1][row];
-        const float to = fmaxf(m, x.x), ref = to == -INFINITY ? 0.f : to;
-        // in the same order in both
-        const float la = (b == 0 ? l : x.y) * ex2((b == 0 ? m : x.x) - ref), lb = (b == 0 ? x.y : l) * ex2((b == 0 ? x.x : m) - ref);
-        l = la + lb;
-        m = to;
+      if (C::NH == 2) {  // the halves' sums; then both know that Q has been used
+        float other;
+        if (!(ok = exchange(l, other))) break;
+        l += other;  // the same in both
       }
       const Piece q = pc;
       cut = cut_of(run, q, cta);
@@ -683,9 +686,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
 #pragma unroll
         for (int i = 0; i < 4; ++i) to[i] = (uint8_t *)__shfl_sync(0xffffffffu, (unsigned long long)dst, i * 8 + oct);
         const uint32_t oa = tm + lane + C::O0 + block * D;
-        constexpr int half = NQ == 1 ? D / 2 : D;  // one row block: each warpgroup writes half of a row
 #pragma unroll 1
-        for (int x = NQ == 1 ? b * half : 0, end = x + half; x < end; x += 32) {
+        for (int x = half * (D / C::NH), end = x + D / C::NH; x < end; x += 32) {
           uint32_t o[32];
           tc::tmem_ld32(oa + x, o);
           wait_ld(o);
@@ -728,7 +730,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           }
           __syncwarp();
         }
-        if (on && (NQ == 2 || b == 0)) {
+        if (on && half == 0) {
           if (!whole) ws.ml[slot] = make_float2(m, l);
           else if (p.lse) p.lse[t * p.heads + h] = empty ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
         }
@@ -739,12 +741,12 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           if (round == 1 && *(volatile int32_t *)&sm.any_bad)
             for (int i = tid; i < 3 * D; i += 256) (&sm.bad[0][0])[i] = INT32_MAX;
           __syncwarp();
-          if (ln == 0) mbar_arrive(&sm.met[b]);
-          for (int x = 0; x < 2 && ok; ++x) ok = wait_warp(&sm.met[x], meets, limit);
+          if (ln == 0) mbar_arrive(&sm.met);
+          ok = wait_warp(&sm.met, meets, limit);
         }
       }
     }
-  } else if (w < 12) {
+  } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma));
   }
   if (w == 9 || w == 10) {
