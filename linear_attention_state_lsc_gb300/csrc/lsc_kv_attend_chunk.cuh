@@ -21,15 +21,16 @@
 //     cp.async.  V rows behind the last position become zeros: here, where they
 //     are copied, else by the softmax threads.
 // E4M3 pools run on the 8-bit products as they are (converting the codes to bf16 in
-// front of the tensor cores took 2.4 ms where this takes 1.60 ms, bound by the integer
+// front of the tensor cores took 2.4 ms where this takes 1.52 ms, bound by the integer
 // pipes).  A row of q, times a power of two that brings it to [128, 256), is the sum
 // of two e4m3 rows: four significant bits each, so bf16 is exact down to 2^-9 of the
 // row's largest magnitude and off by 2^-18 of it below.  Scores take K's scale per
 // position.  A weight is p 2^e with V's scale 2^e, as f16 relative to the row's
 // largest contribution (the reference is that of s + e; the sum takes p), and an f16
 // is the sum of three e5m2 numbers: its upper byte, the upper byte of the rest, and
-// what is left rounded to nearest, together nine bits or more.  So Q K^T takes two
-// 8-bit products, P V three, at twice bf16's rate.
+// what is left rounded to nearest (in whole numbers: the conversion took 5 % more
+// time), together nine bits or more.  So Q K^T takes two 8-bit products, P V three,
+// at twice bf16's rate.
 // head_dim 64 and 128: two row blocks of 128, one warpgroup and a thread a row
 // each, with its own S and O (S 2 x 128, O 2 x head_dim columns of TMEM), Q in
 // shared memory, tiles of 128: one block's softmax runs under the other's
@@ -39,9 +40,13 @@
 // to K and V and halves what the score products read from it.  The way from S to
 // P is what the products wait for here, so it is made short: both warpgroups take
 // each tile, a thread half the columns of a row, and tell each other the largest
-// of their halves (bf16, four prompts on a 16k prefix, 12 q heads a kv head: 819
-// us; 890 with a thread a row and the tiles in turn; the pair of head_dim 128
-// with sixteen softmax warps of 104 registers: 1928 us against 1350, so not there).
+// of their halves (bf16, four prompts on a 16k prefix, 12 q heads a kv head: 817
+// us; 890 with a thread a row and the tiles in turn; 849 when each thread looks at
+// the whole row for the maximum and computes half the weights; the pair of
+// head_dim 128 with sixteen softmax warps of 104 registers: 1928 us against 1350,
+// so not there).
+// Two row blocks: half a tile's weights go to the products while the other half
+// is computed (head_dim 128, 4096 tokens behind 28000: 1361 -> 1320 us).
 //
 // Positions that only some rows of a unit see may hold infinities and NaN: see
 // lsc_kv_attend_rows.cuh; here the softmax threads search such a tile's v.
@@ -92,10 +97,9 @@ struct Smem {
   float up[8][32];        // E4M3, by softmax warp: the power of two of a row of q
   alignas(16) uint8_t rows[8][32][80];  // by softmax warp: 64 bytes of each of its rows, between TMEM and memory
   int32_t bad[Q8 ? 1 : 3][Q8 ? 1 : D];  // first position whose v is NaN, +inf, -inf
-  uint64_t full[C::NS], empty[C::NS], sfull[2], pfull[2], qfull[2], odone[2], fin[2], met, drain;
+  uint64_t full[C::NS], empty[C::NS], sfull[2], phalf[2], pfull[2], qfull[2], odone[2], fin[2], met, drain;
   uint64_t scaled[C::SR];             // E4M3: a tile's scales are there
-  uint64_t turn[8];             // a warp's partner has told its part of a row's maximum or sum
-  float told[2][8][32];         // those, by turn
+  uint64_t told[2][8][32];      // NH == 2: a half's part of a row's maximum or sum, behind the turn's number
   uint32_t tmem;
   int32_t any_bad;
   RunScratch run;
@@ -264,13 +268,11 @@ __device__ __forceinline__ void weights8(const uint32_t (&s)[32], const float *v
       __half2 rest = __hsub2(*reinterpret_cast<const __half2 *>(&h[z]), *reinterpret_cast<const __half2 *>(&t0[z]));
       t1[z] = *reinterpret_cast<const uint32_t *>(&rest) & 0xff00ff00u;
       rest = __hsub2(rest, *reinterpret_cast<const __half2 *>(&t1[z]));
-      uint16_t e;
-      asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(e) : "r"(*reinterpret_cast<const uint32_t *>(&rest)));
-      t2[z] = e;
+      t2[z] = *reinterpret_cast<const uint32_t *>(&rest) + 0x00800080u;  // rest >= 0: to nearest in whole numbers
     }
     q[0][y] = __byte_perm(t0[0], t0[1], 0x7531);
     q[1][y] = __byte_perm(t1[0], t1[1], 0x7531);
-    q[2][y] = __byte_perm(t2[0], t2[1], 0x5410);
+    q[2][y] = __byte_perm(t2[0], t2[1], 0x7531);
   }
   l = add2(l, add2(sum[0], sum[1]));
 }
@@ -324,14 +326,15 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     tc::tmem_alloc(&sm.tmem, 512);
     tc::tmem_relinquish();
   }
+  if (C::NH == 2)
+    for (int i = tid; i < 2 * 8 * 32; i += C::threads) (&sm.told[0][0][0])[i] = ~0ull;  // no turn's number
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], 1), mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < C::SR; ++i) mbar_init(&sm.scaled[i], 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.sfull[i], 1), mbar_init(&sm.pfull[i], 4 * C::NH), mbar_init(&sm.qfull[i], 4 * C::NH);
+      mbar_init(&sm.sfull[i], 1), mbar_init(&sm.phalf[i], 4), mbar_init(&sm.pfull[i], 4 * C::NH), mbar_init(&sm.qfull[i], 4 * C::NH);
       mbar_init(&sm.odone[i], 1), mbar_init(&sm.fin[i], 1);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&sm.turn[i], 1);
     mbar_init(&sm.met, 8);
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
@@ -489,13 +492,28 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     uint32_t it = 0;     // tiles this row block has been through
     uint32_t slots = 0;  // ring slots of the pieces before this one, modulo 2 NS
     uint32_t meets = 0, done = 0, turns = 0, tiles = 0;  // tiles: of the pieces before this one
-    auto exchange = [&](float x, float &other) {  // with the thread that has the other half of the row
-      sm.told[turns & 1][w][ln] = x;  // read two turns ago: the partner has arrived for the last one since
-      __syncwarp();
-      if (ln == 0) mbar_arrive(&sm.turn[partner]);
-      if (!wait_warp(&sm.turn[w], turns, limit)) return false;
-      other = sm.told[turns++ & 1][partner][ln];
-      return true;
+    // x for the thread that has the other half of the row, against its own.  Value and turn number are one 64-bit word,
+    // so a thread itself sees when it is there (a warp's barrier instead: the same with bf16, 1.4 % slower with E4M3).
+    // The word was read two turns ago: the partner has told the last turn's since.
+    auto exchange = [&](float x, float &other) {
+      const uint32_t mine = smem_u32(&sm.told[turns & 1][w][ln]), its = smem_u32(&sm.told[turns & 1][partner][ln]);
+      asm volatile("st.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(mine), "l"((uint64_t)turns << 32 | __float_as_uint(x))
+                   : "memory");
+      uint64_t v, t0 = 0;
+      bool there;
+      for (uint32_t i = 0;; ++i) {
+        asm volatile("ld.relaxed.cta.shared::cta.b64 %0, [%1];" : "=l"(v) : "r"(its) : "memory");
+        there = __all_sync(0xffffffffu, (uint32_t)(v >> 32) == turns);
+        if (there) break;
+        if ((i & 255) == 255) {  // reading the clock takes a microsecond
+          const uint64_t t = global_timer_ns();
+          if (t0 == 0) t0 = t;
+          if (__any_sync(0xffffffffu, t - t0 >= limit)) break;
+        }
+      }
+      other = __uint_as_float((uint32_t)v);
+      ++turns;
+      return there;
     };
     while (have && ok) {
       c = c_next;
@@ -525,7 +543,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         const uint32_t tile = tiles + j, sr = tile % C::SR;  // E4M3: where its scales are
         const int32_t last = first + TK < pc.s.kv ? first + TK : pc.s.kv;
         if (Q8 && !(ok = wait_warp(&sm.scaled[sr], tile / C::SR, limit))) break;
-        if (Q8 && (last > sure || last < first + TK)) {
+        const bool edge = last > sure || last < first + TK;  // rows of v may have to be cleared
+        if (Q8 && edge) {
           // Codes of NaN where some row does not see the position, and whatever lies behind the last one, become zeros;
           // the scale says NaN to the rows that see it.  Every warp looks at the whole tile, so none waits for another.
           const uint32_t vi = slots + 2 * j + 1;
@@ -592,6 +611,12 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
             }
           }
         }
+        auto hand = [&](uint64_t *bar) {  // the weights up to here (and the rescaled O) to the products
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (ln == 0) mbar_arrive(bar);
+        };
         const float ref = m == -INFINITY ? 0.f : m;
         const uint64_t r2 = two(-ref, -ref);
         uint64_t l2 = two(0.f, 0.f);
@@ -607,12 +632,13 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
             weights<BF16>(s[x], c2, r2, l2, q);
             tc::tmem_st16(s0 + half * (C::HC / 2) + 16 * x, q);
           }
+          if (NQ == 2 && x == NC / 2 - 1 && !edge) hand(&sm.phalf[sb]);
         }
         const float2 lf = *reinterpret_cast<const float2 *>(&l2);
         l += lf.x + lf.y;
         // positions [max(first, sure), last): some row of the unit does not see them; behind last: a block's rows came as
         // they were
-        if (!Q8 && (last > sure || last < first + TK)) {
+        if (!Q8 && edge) {
           const uint32_t vi = slots + 2 * j + 1;
           const int slot = (int)(vi % NS);
           if (!(ok = wait_warp(&sm.full[slot], vi / NS, limit))) break;
@@ -653,10 +679,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           fence_proxy_async_smem();
           __syncwarp();
         }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (ln == 0) mbar_arrive(&sm.pfull[sb]);
+        if (NQ == 2 && edge) hand(&sm.phalf[sb]);
+        hand(&sm.pfull[sb]);
       }
       if (!ok) break;
       if (C::NH == 2) {  // the halves' sums; then both know that Q has been used
@@ -951,22 +975,25 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         tc::mma_commit(&sm.sfull[sb]);
       }
     };
-    auto values = [&](int b, int sb, int slot, bool fresh, bool last) {  // O[b] (+)= P[sb] V
+    // O[b] (+)= P[sb] V over half `part` of the tile's positions (NQ == 2: else all)
+    auto values = [&](int b, int sb, int slot, int part, bool fresh, bool last) {
       if (lead) {
         const uint32_t vd = desc_lo(ring0 + slot * C::slot, TK * 128);
         const uint32_t od = tm + C::O0 + b * D, pa = tm + C::S0 + sb * C::SN;
-        if constexpr (Q8) {
+        constexpr int step = Q8 ? 32 : 16, KN = TK / step / NQ;
+        const int k0 = part * KN;
 #pragma unroll
-          for (int t = 0; t < 3; ++t)
+        for (int t = 0; t < (Q8 ? 3 : 1); ++t)
 #pragma unroll
-            for (int k = 0; k < TK / 32; ++k)
-              mma8_ts(od, pa + t * (TK / 4) + k * 8, vd + k * (32 * C::line / 16), hi, ipv, !(fresh && t + k == 0));
-        } else {
-#pragma unroll
-          for (int k = 0; k < TK / 16; ++k) mma16_ts(od, pa + k * 8, vd + k * (2048 / 16), hi, ipv, !(fresh && k == 0));
+          for (int k = 0; k < KN; ++k) {
+            const uint32_t acc = !(fresh && part + t + k == 0);
+            if constexpr (Q8) mma8_ts(od, pa + t * (TK / 4) + (k0 + k) * 8, vd + (k0 + k) * (32 * C::line / 16), hi, ipv, acc);
+            else mma16_ts(od, pa + (k0 + k) * 8, vd + (k0 + k) * (2048 / 16), hi, ipv, acc);
+          }
+        if (part == NQ - 1) {
+          tc::mma_commit(&sm.odone[b]);
+          if (last) tc::mma_commit(&sm.fin[b]);
         }
-        tc::mma_commit(&sm.odone[b]);
-        if (last) tc::mma_commit(&sm.fin[b]);
       }
     };
     auto release = [&](int slot) {
@@ -986,9 +1013,12 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         for (int j = 0; j < nt; ++j) {
           if (!next_slot(rv, vs)) break;
           for (int b = 0; b < nb; ++b) {
+            if (!wait(&sm.phalf[b], itb[b])) break;
+            tc::fence_after_sync();
+            values(b, b, vs, 0, j == 0, j == nt - 1);
             if (!wait(&sm.pfull[b], itb[b]++)) break;
             tc::fence_after_sync();
-            values(b, b, vs, j == 0, j == nt - 1);
+            values(b, b, vs, 1, j == 0, j == nt - 1);
             if (b == nb - 1) release(vs);
             if (j + 1 < nt) {
               if (b == 0 && !next_slot(rk, ks)) break;
@@ -1010,7 +1040,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           }
           if (!next_slot(rv, vs) || !wait(&sm.pfull[it & 1], it >> 1)) break;
           tc::fence_after_sync();
-          values(0, (int)(it & 1), vs, j == 0, j == nt - 1);
+          values(0, (int)(it & 1), vs, 0, j == 0, j == nt - 1);
           release(vs);
         }
       }
