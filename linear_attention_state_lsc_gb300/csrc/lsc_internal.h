@@ -311,6 +311,7 @@ struct KvAttendParams {
   int32_t box_decode;
   int32_t whole;           // 1: units are not cut
   int32_t min_run;         // tiles of a run at least
+  int32_t lead;            // tiles' worth of time that a unit takes besides its tiles
   int32_t groups;          // units of a row block of a sequence: kv heads, or groups of them
   uint8_t *ws;             // null: no unit is cut
   uint64_t wait_limit_ns;  // bound of each mbarrier wait (0: give up at once)

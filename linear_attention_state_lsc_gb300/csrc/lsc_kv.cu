@@ -257,10 +257,10 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   const bool q8 = r.L.dtype == LSC_E4M3;
   const bool types = r.dtype != LSC_F32 && (r.L.dtype == r.dtype || q8);
   if (!types || (D != 64 && D != 128 && D != 256) || (mis & 15) != 0) return kAny;
-  // the tensor-core kernels count packed rows, positions and tiles in 31 bits
+  // the tensor-core kernels count packed rows, positions and tiles (and up to 64 for each unit) in 31 bits
   const int64_t rows = (int64_t)std::min(r.max_seq, r.b.total_tokens) * r.group;
   const int64_t units = (int64_t)r.b.total_tokens * r.group / 16 + r.b.n_seq;
-  if (rows > INT32_MAX - 1024 || r.max_kv > INT32_MAX - 1024 || units * r.L.heads > INT32_MAX / (r.max_kv / 64 + 1))
+  if (rows > INT32_MAX - 1024 || r.max_kv > INT32_MAX - 1024 || units * r.L.heads > INT32_MAX / (r.max_kv / 64 + 1 + 64))
     return kAny;
   if (rows <= kDecodeMost && r.box_decode > 0) {
     *plan = lsc::plan_kv_attend_decode(r);
@@ -534,6 +534,7 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
   }
   r.whole = !plan.may_cut;
   r.min_run = plan.min_run;
+  r.lead = plan.lead;
   r.groups = r.L.heads / std::max(plan.together, 1);
   cudaError_t e = form == kAny    ? lsc::launch_kv_attend_any(r, s)
                   : form == kDecode ? lsc::launch_kv_attend_decode(r, plan, s)

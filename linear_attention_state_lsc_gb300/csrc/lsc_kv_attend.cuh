@@ -6,8 +6,9 @@
 // that share K and V are rows of one tile and K/V is read once for all of
 // them.  A unit's work is its tiles of TK positions, up to the last one that
 // any of its rows sees (at least one, so that a unit that sees nothing still
-// writes its zeros).  All tiles of all units, in the order (sequence, kv head,
-// row block, tile), are cut into equal runs, one per CTA: lengths that differ
+// writes its zeros).  Before its tiles a unit has `lead` counts for the time that
+// it takes besides them.  All counts of all units, in the order (sequence, kv head,
+// row block, count), are cut into equal runs, one per CTA: lengths that differ
 // between sequences do not leave SMs idle, and a single long sequence spreads
 // over all of them.  The cut is computed on the device from the lengths, so a
 // captured graph follows them.
@@ -74,7 +75,7 @@ __device__ __forceinline__ int32_t block_tiles(const KvAttendParams &p, const Se
   return t < 1 ? 1 : t;
 }
 
-// Tiles of one kv head of a sequence.
+// Counts of one kv head of a sequence.
 template <int M, int TK>
 __device__ __forceinline__ int32_t seq_tiles(const KvAttendParams &p, int32_t i) {
   if (i >= p.b.n_seq) return 0;
@@ -83,14 +84,14 @@ __device__ __forceinline__ int32_t seq_tiles(const KvAttendParams &p, int32_t i)
   int32_t t = 0;
   if (p.whole) return nb;
 #pragma unroll 1
-  for (int32_t b = 0; b < nb; ++b) t += block_tiles<M, TK>(p, s, b);
+  for (int32_t b = 0; b < nb; ++b) t += p.lead + block_tiles<M, TK>(p, s, b);
   return t;
 }
 
 // Where a CTA's run is: the walk over its pieces.
 struct Run {
-  int32_t pos, end, chunk;  // tile indexes in the order of all tiles; pos == end: done
-  int32_t seq, head, block, tile;
+  int32_t pos, end, chunk;  // in the order of all counts; pos == end: done
+  int32_t seq, head, block, count;
 };
 
 struct Piece {
@@ -138,7 +139,7 @@ __device__ __forceinline__ Run find_run(const KvAttendParams &p, int cta, int ct
   if (r.chunk < p.min_run) r.chunk = p.min_run;
   r.pos = cta * r.chunk;
   r.end = r.pos + r.chunk < total ? r.pos + r.chunk : total;
-  r.seq = r.head = r.block = r.tile = 0;
+  r.seq = r.head = r.block = r.count = 0;
   if (r.pos >= r.end) {
     r.pos = r.end;
     return r;
@@ -170,12 +171,12 @@ __device__ __forceinline__ Run find_run(const KvAttendParams &p, int cta, int ct
   const Seq s = attend_seq(p.L, p.b, r.seq, p.max_seq, p.max_kv);
 #pragma unroll 1
   for (;;) {
-    const int32_t t = block_tiles<M, TK>(p, s, r.block);
+    const int32_t t = p.lead + block_tiles<M, TK>(p, s, r.block);
     if (rem < t) break;
     rem -= t;
     ++r.block;
   }
-  r.tile = rem;
+  r.count = rem;
   return r;
 }
 
@@ -198,11 +199,19 @@ __device__ __forceinline__ bool next_piece(const KvAttendParams &p, Run &r, Piec
   q.head = r.head;
   q.block = r.block;
   q.tiles = block_tiles<M, TK>(p, s, r.block);
-  q.t0 = r.tile;
-  const int32_t left = r.end - r.pos;
-  q.t1 = p.whole || q.tiles - q.t0 <= left ? q.tiles : q.t0 + left;
-  r.pos += p.whole ? 1 : q.t1 - q.t0;
-  r.tile = 0;
+  if (p.whole) {
+    q.t0 = 0;
+    q.t1 = q.tiles;
+    r.pos += 1;
+  } else {
+    const int32_t c0 = r.count - p.lead, rest = q.tiles - c0, left = r.end - r.pos;
+    const int32_t c = rest < left ? rest : left;
+    q.t0 = c0 > 0 ? c0 : 0;
+    q.t1 = c0 + c;
+    r.pos += c;
+    if (q.t1 <= 0) return false;  // the run ends before the unit's first tile
+  }
+  r.count = 0;
   ++r.block;
   return true;
 }
@@ -238,6 +247,7 @@ struct AttendPlan {
   size_t ws_bytes;
   bool may_cut;    // false: units are not cut
   int32_t min_run; // tiles of a run at least
+  int32_t lead;    // tiles' worth of time that a unit takes besides its tiles
 };
 cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_decode(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);

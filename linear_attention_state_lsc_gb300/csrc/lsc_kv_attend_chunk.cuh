@@ -21,7 +21,7 @@
 //     cp.async.  V rows behind the last position become zeros: here, where they
 //     are copied, else by the softmax threads.
 // E4M3 pools run on the 8-bit products as they are (converting the codes to bf16 in
-// front of the tensor cores took 2.4 ms where this takes 1.52 ms, bound by the integer
+// front of the tensor cores took 2.4 ms where this took 1.52, bound by the integer
 // pipes).  A row of q, times a power of two that brings it to [128, 256), is the sum
 // of two e4m3 rows: four significant bits each, so bf16 is exact down to 2^-9 of the
 // row's largest magnitude and off by 2^-18 of it below.  Scores take K's scale per
@@ -40,11 +40,11 @@
 // to K and V and halves what the score products read from it.  The way from S to
 // P is what the products wait for here, so it is made short: both warpgroups take
 // each tile, a thread half the columns of a row, and tell each other the largest
-// of their halves (bf16, four prompts on a 16k prefix, 12 q heads a kv head: 817
-// us; 890 with a thread a row and the tiles in turn; 849 when each thread looks at
-// the whole row for the maximum and computes half the weights; the pair of
-// head_dim 128 with sixteen softmax warps of 104 registers: 1928 us against 1350,
-// so not there).
+// of their halves (bf16, 36 sequences of 1 to 2048 tokens behind up to 8192, runs
+// by tiles alone: 817 us; 890 with a thread a row and the tiles in turn; 849 when
+// each thread looks at the whole row for the maximum and computes half the
+// weights; the pair of head_dim 128 with sixteen softmax warps of 104 registers:
+// 1928 us against 1350, so not there).
 // Two row blocks: half a tile's weights go to the products while the other half
 // is computed (head_dim 128, 4096 tokens behind 28000: 1361 -> 1320 us).
 //

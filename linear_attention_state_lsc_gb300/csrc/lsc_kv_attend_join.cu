@@ -136,7 +136,7 @@ cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &pla
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-constexpr int kWhole = 8, kMinRun = 4;  // in tiles of 128 positions
+constexpr int kWhole = 8, kMinRun = 4, kLead = 4;  // in tiles of 128 positions
 
 AttendPlan plan_kv_attend_chunk(const KvAttendParams &p) {
   using namespace kv::chunk;
@@ -147,9 +147,14 @@ AttendPlan plan_kv_attend_chunk(const KvAttendParams &p) {
   const int64_t tiles = ((int64_t)p.max_kv + TK - 1) / TK;
   const int64_t units = (((int64_t)p.b.total_tokens * p.group + plan.M - 1) / plan.M + p.b.n_seq) * p.L.heads;
   // Uncut up to kWhole tiles of 128 positions: at 5 tiles a unit, 256 rows of 128, cutting each over 5 CTAs took 33 us
-  // and leaving them whole WHOLE_US.
+  // and leaving them whole 25.
   plan.may_cut = tiles > kWhole * 128 / TK;
   plan.min_run = plan.may_cut ? kMinRun * 128 / TK : 1;
+  // A unit's queries, its first tile on the way through empty pipes, its clearing of v and its result take 15000 cycles,
+  // ten tiles of 64 at head_dim 256: with tiles alone counted, runs of many short units took up to twice the time of the
+  // others.  Counted as 0, 256, 512 and 1024 positions: bf16, 36 sequences of 1 to 2048 tokens behind up to 8192, 818,
+  // 740, 690 and 684 us; E4M3, 8 of 64 to 2048 behind up to 16384, 1515, 1177, 1004 and 1045.
+  plan.lead = plan.may_cut ? kLead * 128 / TK : 0;
   const int64_t most = plan.may_cut ? units * tiles / plan.min_run + 1 : units;
   plan.ctas = (int)(most < p.num_sms ? most : p.num_sms);
   plan.ws_bytes = plan.may_cut ? kv::workspace_size(plan.ctas, plan.M, D) : 0;

@@ -305,6 +305,23 @@ def test_what_a_row_does_not_see_does_not_enter(lsc, mix, shape, n):
         assert np.isfinite(np.delete(got[sees:n - 1], [3, 7], -1)).all()
 
 
+@pytest.mark.parametrize("pool,D", [(L.LSC_BF16, 64), (L.LSC_BF16, 256), (L.LSC_E4M3, 128), (L.LSC_E4M3, 256)])
+@pytest.mark.parametrize("S", [3, 31, 80])
+def test_runs_that_begin_and_end_anywhere(lsc, pool, D, S):
+    """Many short units beside long ones: runs end before, inside and behind a unit's tiles."""
+    rng = np.random.default_rng(71 + S)
+    n = rng.integers(0, 12, S)
+    kv = np.where(rng.random(S) < 0.3, rng.integers(1100, 2500, S), rng.integers(1, 300, S)) + n
+    blocks = int((-(-kv // 64)).sum())
+    b = Batch(rng, n, kv, 64, blocks, spare=1)
+    host = filled(rng, b, blocks, 64, 2, D, pool)
+    q, qx = dense(2 * rng.standard_normal((b.T, 32, D)), L.LSC_BF16)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, L.LSC_BF16, 32, D ** -0.5, True)
+        check_attend(host, 1, b, qx, L.LSC_BF16, D ** -0.5, True, out, ls)
+        assert dev.status() == L.LSC_OK
+
+
 def test_attend_strides_and_slices(lsc):
     """q and out as slices of wider arrays, aligned (tensor cores) and not (CUDA cores)."""
     rng = np.random.default_rng(5)
