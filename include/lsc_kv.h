@@ -221,7 +221,8 @@ typedef struct {
  * and lse = -infinity.  Positions it does not see, and rows behind a sequence's
  * last token, do not enter, whatever they hold.  Sums and softmax statistics
  * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded to 16 bits
- * before they meet v.  Two calls with the same inputs give the same bits.
+ * (E4M3 pools, more than 64 rows of q a kv head: to nine significant bits or
+ * more) before they meet v.  Two calls with the same inputs give the same bits.
  * A sequence that exceeds max_kv_tokens is recorded as INVALID_ARG in the status
  * word and taken to have no cached tokens; one that exceeds max_seq_tokens is
  * recorded too, and its rows of out and lse stay as they are.  If a bounded device
@@ -229,7 +230,8 @@ typedef struct {
  * unspecified.
  * Supported: head_dim <= 512.  Pools of q's 16-bit type, and E4M3 pools with
  * 16-bit q, at head_dim 64, 128 and 256, with q and out 16-byte aligned in base
- * and stride, run on the tensor cores; every other combination (F32, q of
+ * and stride, run on the tensor cores (E4M3 pools with F16 q: up to 64 rows of q
+ * a kv head, max_seq_tokens times the group); every other combination (F32, q of
  * another type than the pool's, other head sizes) on the CUDA cores.
  * Errors: INVALID_ARG (as lsc_kv_append; num_q_heads no multiple of kv_heads;
  * scale not positive and finite; causal not 0 or 1; negative bounds; a

@@ -40,7 +40,7 @@
 // to K and V and halves what the score products read from it.  The way from S to
 // P is what the products wait for here, so it is made short: both warpgroups take
 // each tile, a thread half the columns of a row, and tell each other the largest
-// of their halves (bf16, 36 sequences of 1 to 2048 tokens behind up to 8192, runs
+// of their halves (bf16, 24 sequences of 1 to 2048 tokens behind up to 8192, runs
 // by tiles alone: 817 us; 890 with a thread a row and the tiles in turn; 849 when
 // each thread looks at the whole row for the maximum and computes half the
 // weights; the pair of head_dim 128 with sixteen softmax warps of 104 registers:
