@@ -21,7 +21,7 @@
 //     cp.async.  V rows behind the last position become zeros: here, where they
 //     are copied, else by the softmax threads.
 // E4M3 pools run on the 8-bit products as they are (converting the codes to bf16 in
-// front of the tensor cores took 2.4 ms where this took 1.52, bound by the integer
+// front of the tensor cores took 2.4 ms where this took 1.77, bound by the integer
 // pipes).  A row of q, times a power of two that brings it to [128, 256), is the sum
 // of two e4m3 rows: four significant bits each, so bf16 is exact down to 2^-9 of the
 // row's largest magnitude and off by 2^-18 of it below.  Scores take K's scale per
@@ -386,16 +386,34 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       auto load = [&](int i, int x) { return from[i] ? *(const uint4 *)(from[i] + x + part16) : make_uint4(0, 0, 0, 0); };
       constexpr int bytes = 2 * D / C::NH;         // of a row, this warpgroup's share
       const int begin = half * bytes;
+      // all loads before the first use: a unit's queries are its first latency (head_dim 256: 3300 cycles, 4100 a piece at
+      // a time; E4M3, whose scale takes the whole row, 6600 and 9900)
+      uint4 own[bytes / 64][4];
+#pragma unroll
+      for (int x = 0; x < bytes / 64; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own[x][i] = load(i, begin + 64 * x);
       if constexpr (Q8) {
         uint32_t top[4] = {0, 0, 0, 0};  // magnitudes of bf16 order as whole numbers, two a word
-#pragma unroll 2
-        for (int x = 0; x < 2 * D; x += 64)
+        auto look = [&](int i, const uint4 &y) {
+          const uint32_t k = 0x7fff7fffu;
+          top[i] = __vmaxu2(top[i], __vmaxu2(__vmaxu2(y.x & k, y.y & k), __vmaxu2(y.z & k, y.w & k)));
+        };
+        if constexpr (C::NH == 2) {
+          uint4 rest[bytes / 64][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 y = load(i, x);
-            const uint32_t k = 0x7fff7fffu;
-            top[i] = __vmaxu2(top[i], __vmaxu2(__vmaxu2(y.x & k, y.y & k), __vmaxu2(y.z & k, y.w & k)));
-          }
+          for (int x = 0; x < bytes / 64; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rest[x][i] = load(i, (half ^ 1) * bytes + 64 * x);
+#pragma unroll
+          for (int x = 0; x < bytes / 64; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) look(i, rest[x][i]);
+        }
+#pragma unroll
+        for (int x = 0; x < bytes / 64; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) look(i, own[x][i]);
         float down[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -409,12 +427,12 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         }
         __syncwarp();
         c_next = p.scale_log2 * sm.up[w][ln];
-#pragma unroll 1
+#pragma unroll
         for (int x = 0; x < bytes; x += 64) {  // 32 elements: 32 bytes of each part
           uint2 part[4][2];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint4 y = load(i, begin + x);
+            const uint4 y = own[x / 64][i];
             const uint32_t in[4] = {y.x, y.y, y.z, y.w};
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -451,11 +469,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           }
         }
       } else {
-#pragma unroll 4
-        for (int x = 0; x < bytes; x += 64) {
-          uint4 y[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = load(i, begin + x);
+        for (int x = 0; x < bytes; x += 64) {
+          const uint4(&y)[4] = own[x / 64];
           if constexpr (C::QT) {
             __syncwarp();
 #pragma unroll
@@ -545,25 +561,23 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         if (Q8 && !(ok = wait_warp(&sm.scaled[sr], tile / C::SR, limit))) break;
         const bool edge = last > sure || last < first + TK;  // rows of v may have to be cleared
         if (Q8 && edge) {
-          // Codes of NaN where some row does not see the position, and whatever lies behind the last one, become zeros;
-          // the scale says NaN to the rows that see it.  Every warp looks at the whole tile, so none waits for another.
+          // Codes of NaN where some row does not see the position become zeros; the scale says NaN to the rows that see it.
+          // Every warp looks at all of them, so none waits for another.  So does whatever lies behind the last position,
+          // a share of it by each warp of the row block.
           const uint32_t vi = slots + 2 * j + 1;
           const int slot = (int)(vi % NS);
           if (!(ok = wait_warp(&sm.full[slot], vi / NS, limit))) break;
           constexpr int CH = C::row / 16;
+          auto chunk = [&](int i) { return (uint4 *)(sm.ring[slot] + chunk_at<C::line>(TK, i / CH, i % CH)); };
+          for (int i = (last - first) * CH + half * 128 + row; i < TK * CH; i += 128 * C::NH) *chunk(i) = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-          for (int i = (sure > first ? sure - first : 0) * CH + ln; i < TK * CH; i += 32) {
-            const int key = i / CH;
-            uint4 *at = (uint4 *)(sm.ring[slot] + chunk_at<C::line>(TK, key, i % CH));
-            const uint4 v = *at;
+          for (int i = (sure > first ? sure - first : 0) * CH + ln; i < (last - first) * CH; i += 32) {
+            const uint4 v = *chunk(i);
             const uint32_t k = 0x7f7f7f7fu, one = 0x01010101u;
-            const bool nan = ((((v.x & k) + one) | ((v.y & k) + one) | ((v.z & k) + one) | ((v.w & k) + one)) & 0x80808080u) != 0;
-            if (key < last - first && !nan) continue;
-            if (key < last - first) {
-              *(volatile float *)&sm.vs[sr][key] = __uint_as_float(0x7fc00000u);
-              __threadfence_block();
-            }
-            *at = make_uint4(0, 0, 0, 0);
+            if (((((v.x & k) + one) | ((v.y & k) + one) | ((v.z & k) + one) | ((v.w & k) + one)) & 0x80808080u) == 0) continue;
+            *(volatile float *)&sm.vs[sr][i / CH] = __uint_as_float(0x7fc00000u);
+            __threadfence_block();
+            *chunk(i) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();

@@ -150,7 +150,7 @@ AttendPlan plan_kv_attend_chunk(const KvAttendParams &p) {
   // and leaving them whole 25.
   plan.may_cut = tiles > kWhole * 128 / TK;
   plan.min_run = plan.may_cut ? kMinRun * 128 / TK : 1;
-  // A unit's queries, its first tile on the way through empty pipes, its clearing of v and its result take 15000 cycles,
+  // A unit's queries, its first tile on the way through empty pipes, its clearing of v and its result took 15000 cycles,
   // ten tiles of 64 at head_dim 256: with tiles alone counted, runs of many short units took up to twice the time of the
   // others.  Counted as 0, 256, 512 and 1024 positions: bf16, 24 sequences of 1 to 2048 tokens behind up to 8192, 818,
   // 740, 690 and 684 us; E4M3, 8 of 64 to 2048 behind up to 16384, 1515, 1177, 1004 and 1045.
