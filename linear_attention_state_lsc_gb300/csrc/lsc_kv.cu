@@ -270,7 +270,7 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
     *plan = lsc::plan_kv_attend_rows(r);
     return kRows;
   }
-  if (q8 && r.dtype != LSC_BF16) return kAny;  // e4m3 tiles become bf16 there
+  if (q8 && r.dtype != LSC_BF16) return kAny;  // q is two e4m3 rows there, too few bits for f16
   *plan = lsc::plan_kv_attend_chunk(r);
   return kChunk;
 }

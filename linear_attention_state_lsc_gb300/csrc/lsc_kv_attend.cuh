@@ -128,12 +128,17 @@ template <int NT, int M, int TK>
 __device__ __forceinline__ Run find_run(const KvAttendParams &p, int cta, int ctas, RunScratch &sc) {
   const int H = p.groups;
   int32_t total = 0, mine = 0, incl = 0;
+  bool down = false;
 #pragma unroll 1
   for (int32_t i0 = 0; i0 < p.b.n_seq; i0 += NT) {
-    mine = seq_tiles<M, TK>(p, i0 + threadIdx.x);
+    const int32_t i = i0 + threadIdx.x;
+    down |= i < p.b.n_seq && p.b.cu[i + 1] < p.b.cu[i];
+    mine = seq_tiles<M, TK>(p, i);
     total += block_scan<NT>(mine, sc, &incl);
   }
   total *= H;
+  // Sequences that overlap (recorded by check_cu) could count past 31 bits: no work then.
+  if (__syncthreads_or(down)) total = 0;
   Run r;
   r.chunk = (total + ctas - 1) / ctas;
   if (r.chunk < p.min_run) r.chunk = p.min_run;

@@ -401,6 +401,25 @@ def test_bounds_that_do_not_hold_are_recorded(lsc):
         assert (out[1] == 0).all() and torch.isinf(ls[1]).all()
 
 
+def test_overlapping_sequences_that_count_past_31_bits_stay_inside(lsc):
+    """cu_seqlens goes up and down, so that one set of rows counts 130056 times: 32 units of 1024 tiles and 8 more counts
+    each are 2^32 + 2048.  It is recorded and nothing is written."""
+    S, T, G, D, bt = 2 * 130056, 64, 64, 256, 65536
+    assert (S // 2 * 32 * (1024 + 8)) % 2 ** 32 == 2048
+    for kv in (bt, bt - 3 * 64):
+        with DevKv(HostKv(1, bt, 1, D, L.LSC_BF16, pad=0, layers=1)) as dev:
+            cu = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+            cu[1::2] = T
+            table = torch.zeros((S, 1), dtype=torch.int32, device="cuda")
+            lens = torch.full((S,), kv, dtype=torch.int32, device="cuda")
+            q = torch.zeros((T, G * D), dtype=torch.bfloat16, device="cuda")
+            out = torch.full_like(q, 7)
+            args = L.kv_attend_args(L.kv_batch(S, T, table, cu, lens, max_blocks=1), G, q, out, L.LSC_BF16, 0.125,
+                                    causal=False)
+            assert L.lsc_kv_attend(dev.pool, 0, args, cur()) == L.LSC_OK
+            assert dev.status() == L.LSC_ERR_INVALID_ARG and (out == 7).all()
+
+
 @pytest.mark.parametrize("pool,dtype,G,bound", [(L.LSC_F32, L.LSC_F32, 2, 1), (L.LSC_BF16, L.LSC_BF16, 4, 2),
                                                 (L.LSC_E4M3, L.LSC_F16, 8, 2), (L.LSC_F16, L.LSC_F16, 32, 2),
                                                 (L.LSC_BF16, L.LSC_BF16, 64, 2), (L.LSC_E4M3, L.LSC_BF16, 64, 2)])
