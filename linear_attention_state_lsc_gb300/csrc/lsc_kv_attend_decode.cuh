@@ -18,7 +18,9 @@
 // the registers (a transposition of 8 x 8 each).  The warps meet at the end of a piece, where a head's parts are
 // joined in order.  The maximum is a reference that moves only when a row's
 // maximum rose by more than 2^8 (weights are 2^8 at most), so the weighted rows are
-// rarely rescaled.
+// rarely rescaled.  Measured, 16 q heads, 64 tokens behind 64 to 16384, bf16, 2 heads of 256:
+// 1018 MB in 160 us (6.4 TB/s, 95 % of a copy's rate); E4M3, 32 q heads, 128 tokens
+// behind 500 to 8000, 8 heads of 128: 1060 MB in 178 us (6.0 TB/s, 89 %).
 //
 // E4M3 pools: codes go to f16 exactly (one conversion per two codes), so the
 // products run in f16; K's scale multiplies the scores.  V's scale 2^e joins the

