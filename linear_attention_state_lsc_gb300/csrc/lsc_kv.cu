@@ -245,8 +245,11 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
 
 // Which kernel a call takes, by sizes, types and alignment: the decode kernel when
 // every sequence has kDecodeMost packed rows at most and the blocks have TMA maps,
-// else the few-row kernel up to kRowsMost, the chunk kernel when a sequence may
-// have more, the CUDA cores for what none of them takes.
+// else the few-row kernel up to kDecodeMost (E4M3 pools: kRowsMost), the chunk
+// kernel when a sequence may have more, the CUDA cores for what none of them
+// takes.  64 sequences of 8 tokens behind 64 to 16384, 64 packed rows: bf16, few-row
+// kernel 398 us, chunk kernel 193; of 3 tokens, 24 rows: 382 and 189; one sequence
+// of 4 behind 1000: 23 and 25; E4M3, 128 sequences of 8 tokens, 32 rows: 1121 and 1131.
 constexpr int32_t kDecodeMost = 16, kRowsMost = 64;
 enum Form { kAny, kDecode, kRows, kChunk };
 
@@ -266,7 +269,7 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
     *plan = lsc::plan_kv_attend_decode(r);
     return kDecode;
   }
-  if (rows <= kRowsMost) {
+  if (rows <= (q8 ? kRowsMost : kDecodeMost)) {
     *plan = lsc::plan_kv_attend_rows(r);
     return kRows;
   }

@@ -1,7 +1,7 @@
 // lsc_kv_attend_rows.cuh -- attention over a layer of the K/V block pool for
-// sequences with few packed rows (lsc_kv_attend.cuh): a few speculated tokens,
-// short chunks, and decode steps where blocks do not fit TMA boxes.  Up to
-// 16 * MT rows a unit.
+// sequences with few packed rows (lsc_kv_attend.cuh): decode steps where blocks do
+// not fit TMA boxes, and over E4M3 pools a few speculated tokens and short chunks.
+// Up to 16 * MT rows a unit.
 //
 // K and V are read once, so HBM bounds it: 4 * head_dim bytes a position and kv
 // head at 16 bits against 4 * head_dim * rows operations, at 16 rows 16
