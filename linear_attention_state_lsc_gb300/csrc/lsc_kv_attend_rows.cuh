@@ -20,9 +20,10 @@
 //     adds them to its part of the sum, and writes them, 16-bit, to shared memory,
 //   * multiplies all weights of the tile with its share of v's columns.
 // Every warp rescales its own columns when m grew; the sums meet at the end.
-// Measured, bf16, 64 sequences of 4 tokens behind 64 to 16384, 16 q heads, 2 heads of
-// 256 (32 rows a unit): 1.02 GB in 384 us, 2.7 TB/s, 40 % of a copy's rate; 8 tokens (64
-// rows): 398 us.  The barriers of a tile and the copies' issue bound it.
+// Measured, E4M3, 128 sequences of 8 tokens behind 500 to 8000, 32 q heads, 8 heads of
+// 128 (32 rows a unit): 1.08 GB in 1121 us, 1.0 TB/s, 14 % of a copy's rate (bf16, 2
+// heads of 256, 64 sequences of 4: 384 us, where the chunk kernel takes 190).  The
+// barriers of a tile and the copies' issue bound it.
 //
 // E4M3 pools: codes go to f16 exactly (one conversion per two codes), so the
 // products run in f16; K's scale multiplies the scores.  V's scale 2^e joins the
