@@ -222,7 +222,8 @@ typedef struct {
  * last token, do not enter, whatever they hold.  Sums and softmax statistics
  * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded to 16 bits
  * (E4M3 pools, more than 64 rows of q a kv head: to nine significant bits or
- * more) before they meet v.  Two calls with the same inputs give the same bits.
+ * more down to 2^-17 of a row's largest weight, to a multiple of 2^-25 of it
+ * below) before they meet v.  Two calls with the same inputs give the same bits.
  * A sequence that exceeds max_kv_tokens is recorded as INVALID_ARG in the status
  * word and taken to have no cached tokens; one that exceeds max_seq_tokens is
  * recorded too, and its rows of out and lse stay as they are.  If a bounded device

@@ -8,8 +8,8 @@
 //     TMEM, puts weights 2^(s - m) at 16 bits back into the same TMEM columns and
 //     keeps the sum in a register.  m is a reference, not the exact maximum: O is
 //     rescaled (in TMEM, by these threads) only when a row's maximum rose by more
-//     than 2^8, so a weight is at most 2^8 and the rescale is rare after the first
-//     tiles.
+//     than 2^lag, and m then lies 2^lift below it, so a weight is at most
+//     2^(lag + lift) and the rescale is rare after the first tiles.
 //   * one MMA warp: S = Q K^T, O += P V with P as the TMEM operand, issued so that
 //     the products of one tile run while the softmax of another does.
 //   * producers: K and V rows through the block table into a shared-memory ring
@@ -29,8 +29,12 @@
 // largest contribution (the reference is that of s + e; the sum takes p), and an f16
 // is the sum of three e5m2 numbers: its upper byte, the upper byte of the rest, and
 // what is left rounded to nearest (in whole numbers: the conversion took 5 % more
-// time), together nine bits or more.  So Q K^T takes two 8-bit products, P V three,
-// at twice bf16's rate.
+// time), together nine bits or more.  The smallest e5m2 number is 2^-16, so weights
+// take the room above 1 (2^15 at most): a weight is off by half of its ninth bit or
+// by 2^-26 of the row's largest, and a long flat tail behind one large score keeps
+// its share (lag 8 and lift 7, 2^-24: 975 us; 6 and 9: 988; 4 and 11, 2^-28, more
+// rescaling: 1036; 8 chunks behind up to 16384 as below, with pauses).  So Q K^T takes two 8-bit products, P V three, at
+// twice bf16's rate.
 // head_dim 64 and 128: two row blocks of 128, one warpgroup and a thread a row
 // each, with its own S and O (S 2 x 128, O 2 x head_dim columns of TMEM), Q in
 // shared memory, tiles of 128: one block's softmax runs under the other's
@@ -86,6 +90,9 @@ struct Conf {
   // registers a thread of a softmax warpgroup and of the others' keeps of the 168 at launch
   static constexpr int soft = 208, mma = 80;
   static_assert(2 * soft + mma <= 3 * 168, "more registers than the block has");
+  // powers of two: how far a row's maximum may rise above the one that set the reference, and how far the reference
+  // lies below that
+  static constexpr float lag = Q8 ? 6.f : 8.f, lift = Q8 ? 9.f : 0.f;
   // TMEM columns
   static constexpr int S0 = 0, SN = TK;         // S buffer b at S0 + b * SN; P in its first half
   static constexpr int Q0 = 128;                // QT only
@@ -611,8 +618,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           top = fmaxf(top, other);
         }
         const float mt = Q8 ? top : top * c;  // c > 0
-        if (__any_sync(0xffffffffu, mt > m + 8.f)) {  // also the first tile's (m is -inf); the same in both halves
-          const float to = fmaxf(m, mt), f = ex2(m - (to == -INFINITY ? 0.f : to));
+        // also the first tile's (m is -inf); the same in both halves
+        if (__any_sync(0xffffffffu, mt > m + (C::lag + C::lift))) {
+          const float to = fmaxf(m, mt - C::lift), f = ex2(m - (to == -INFINITY ? 0.f : to));
           m = to;
           l *= f;
           if (j > 0) {

@@ -1,0 +1,88 @@
+"""GPU: append, attend and copy_prefix over the K/V block pool where they are easiest to get wrong: flat tails behind
+one large score, queries and scores that are not finite, V far from 1, blocks that fit no TMA box, decode batches
+large enough to read several kv heads side by side, one workspace for many steps, pools made while a graph is being
+captured, and waits that run out.  Plain 64-bit forms and tolerances are those of test_gpu_kv_step.py (where a test
+needs another bound, its own comment derives it)."""
+import functools
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_state_lsc_gb300 import lsc as L
+
+import _kv
+from _kv import NAME, TORCH, Batch, DevKv, HostKv
+from test_gpu_kv_step import HALF, check_attend, cur, dense, filled, run_attend
+
+pytestmark = pytest.mark.gpu
+
+BF, F16, E4 = L.LSC_BF16, L.LSC_F16, L.LSC_E4M3
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+def fill(host, layer, lane, block, row, x):
+    """HostKv.write, all rows at once."""
+    if host.dtype == E4:
+        code, up = _kv.quantise(x)
+        host.rows(layer, lane)[block, row] = code
+        host.scales(layer, lane)[block, row] = up
+    else:
+        host.rows(layer, lane)[block, row] = _kv.to_bytes(x, host.dtype)
+
+
+def shared(S, n, kv, bt):
+    """S sequences of n new tokens that all read the same kv cached ones, in blocks 0, 1, 2 ..."""
+    b = Batch(np.random.default_rng(0), [n] * S, [0] * S, bt, 0)
+    b.kv = np.full(S, kv)
+    b.table = np.tile(np.arange(-(-kv // bt), dtype=np.int32), (S, 1))
+    return b
+
+
+@functools.lru_cache(4)
+def one_and_flat(pool, bt, D, kv):
+    """Rows whose key is zero and whose v is 1, behind one whose key is e_0 and whose v is 1 in even columns and 0 in odd."""
+    host = HostKv(-(-kv // bt), bt, 1, D, pool, layers=1)
+    k, v = np.zeros((2, 1, 1, D)), np.ones((2, 1, 1, D))
+    k[0, 0, 0, 0] = 1
+    v[0, 0, 0, 1::2] = 0
+    at = np.arange(kv)
+    for lane, x in enumerate((k, v)):
+        fill(host, 0, lane, at[1:] // bt, at[1:] % bt, x[1])
+        fill(host, 0, lane, [0], [0], x[0])
+    return host
+
+
+def flat_tail(pool, dtype, n, bt, D, gap, floor, kv=32768, G=4, S=160):
+    """One position with a score `gap` (in powers of two) above all others, which are equal.  v is 1 everywhere but in
+    the large one's odd columns, where it is 0: even columns give 1, odd ones the share of the others' weights.  A
+    weight is off by half a step of its bits (E4M3 chunks: nine significant ones) or by `floor` times the largest."""
+    b, host = shared(S, n, kv, bt), one_and_flat(pool, bt, D, kv)
+    x = np.zeros((b.T, G, D))
+    x[:, :, 0] = gap * np.log(2) * 8
+    q, qx = dense(x, dtype)
+    s = float(qx[0, 0, 0]) / 8
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 0, b, q, dtype, G, 0.125, False, max_seq_tokens=n)
+        assert dev.status() == L.LSC_OK
+    rest = (kv - 1) * np.exp(-s)
+    want = np.where(np.arange(D) % 2, rest, 1 + rest) / (1 + rest)
+    weight = HALF[dtype] if pool != E4 else 2.0 ** -9 if n * G > 64 else 2.0 ** -11
+    err = (weight + (kv + 8) * 2.0 ** -23 + 2.0 ** -20) * want + kv * floor
+    bound = err + HALF[dtype] * (want + err)
+    got = out.double().cpu().numpy().reshape(-1, D)
+    over = np.abs(got - want) / bound
+    assert over.max() <= 1, (over.max(), got[over.argmax() // D, :2], want[:2])
+    # a score is off by less than 2^-20 of itself here, the sum of kv terms by kv 2^-23 of itself
+    assert (np.abs(ls.double().cpu().numpy() - s - np.log1p(rest)) <= (1 + s) * 2.0 ** -20 + (kv + 8) * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("gap", [3.0, 16.9, 17.1, 20.3, 25.1])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_flat_tail_counts_in_e4m3_chunks(lsc, D, gap):
+    """Weights go to the products as e5m2 numbers, multiples of 2^-16, beside a largest one of 2^9 or more: 2^-26 of it
+    is the most that one is off."""
+    flat_tail(E4, BF, 40, 64, D, gap, 2.0 ** -26)
