@@ -435,7 +435,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           const uint32_t ex = t >> 7;  // 2^(ex - 127) <= the largest magnitude: brought to 2^7, where both powers are normal
           const bool plain = ex < 8 || ex == 255;
           down[i] = plain ? 1.f : __uint_as_float((261 - ex) << 23);
-          if ((ln & 3) == 0) sm.up[w][i * 8 + oct] = plain ? 1.f : __uint_as_float((ex - 7) << 23);
+          // an infinity would become a code of 448: a row that is not finite has NaN for its power
+          if ((ln & 3) == 0) sm.up[w][i * 8 + oct] = ex < 8 ? 1.f : __uint_as_float(ex == 255 ? 0x7fc00000u : (ex - 7) << 23);
         }
         __syncwarp();
         c_next = p.scale_log2 * sm.up[w][ln];
@@ -550,6 +551,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       const int r = block * 128 + row;
       const int32_t R = pc.block * M + r, tok = p.by_group.div(R);
       const int32_t vis = r < rows ? visible(pc.s, tok, p.causal) : 0;
+      if (Q8 && vis == 0) c = 1.f;  // sees nothing: zeros, whatever q is (a hidden score is -infinity times c)
       const int32_t sure = visible(pc.s, p.by_group.div(pc.block * M), p.causal);
       const int32_t full_to = NQ == 2 && block == 1 && mine
                                   ? visible(pc.s, p.by_group.div(pc.block * M + 128), p.causal)

@@ -86,3 +86,40 @@ def test_a_flat_tail_counts_in_e4m3_chunks(lsc, D, gap):
     """Weights go to the products as e5m2 numbers, multiples of 2^-16, beside a largest one of 2^9 or more: 2^-26 of it
     is the most that one is off."""
     flat_tail(E4, BF, 40, 64, D, gap, 2.0 ** -26)
+
+
+FORMS = [(BF, BF, 40, 64), (F16, F16, 40, 64), (E4, BF, 40, 64), (BF, BF, 40, 12), (BF, BF, 2, 64), (F16, F16, 2, 12),
+         (E4, BF, 2, 64), (E4, F16, 2, 64), (E4, BF, 2, 12), (E4, BF, 12, 64), (L.LSC_F32, L.LSC_F32, 5, 64)]
+FORM_IDS = ["chunk-bf16", "chunk-f16", "chunk-e4m3", "chunk-bf16-12", "decode-bf16", "rows-f16", "decode-e4m3", "decode-e4m3-f16",
+            "rows-e4m3", "rows-e4m3-48", "f32"]
+
+
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("pool,dtype,n,bt", FORMS, ids=FORM_IDS)
+def test_a_query_that_is_not_finite_is_nan_alone(lsc, pool, dtype, n, bt, D):
+    """An infinity or NaN in a row of q: that row is NaN (a score is infinite or NaN), the rows beside it are as if it
+    were not there."""
+    rng = np.random.default_rng(n + D)
+    S, G = 4, 4
+    b = Batch(rng, [n] * (S + 1), [n + 60, 150, 300, 77, 0], bt, 60, spare=1)
+    host = filled(rng, b, 60, bt, 2, D, pool)
+    x = 2 * rng.standard_normal((b.T, 2 * G, D))
+    x[S * n:S * n + n, :, 3] = np.inf  # the last sequence sees nothing: zeros all the same
+    sick = [(0, 1, np.inf), (n, 0, -np.inf), (2 * n + 1, 5, np.nan), (3 * n, 7, np.inf)]  # (row, head, what)
+    for t, h, what in sick:
+        x[t, h, 2:20] *= 300  # the finite elements of such a row may be large too
+        x[t, h, 5] = what
+    q, qx = dense(x, dtype)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, dtype, 2 * G, D ** -0.5, True, max_seq_tokens=n)
+        assert dev.status() == L.LSC_OK
+    got = out.view(b.T, 2 * G, D)
+    for t, h, _ in sick:
+        assert torch.isnan(got[t, h]).all(), (t, h)
+        assert not torch.isfinite(ls[t, h])
+        # the plain form of a row of zeros in its place, so that all the others are compared
+        qx[t, h] = 0
+        want, lse = (a[t, h] for a in _kv.attend(host, 1, b, qx, D ** -0.5, True)[:2])
+        got[t, h] = torch.from_numpy(want).to(got)
+        ls[t, h] = float(lse)
+    check_attend(host, 1, b, qx, dtype, D ** -0.5, True, out, ls)
