@@ -222,10 +222,12 @@ typedef struct {
  * of q that holds one of them or -infinity gives such scores; its lse is not
  * finite.  Positions it does not see, and rows behind a sequence's
  * last token, do not enter, whatever they hold.  Sums and softmax statistics
- * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded to 16 bits
- * (E4M3 pools, more than 64 rows of q a kv head: to nine significant bits or
- * more down to 2^-17 of a row's largest weight, to a multiple of 2^-25 of it
- * below) before they meet v.  Two calls with the same inputs give the same bits.
+ * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded before they
+ * meet v: to bf16 in bf16 pools; to f16 in f16 and E4M3 pools, in full down to
+ * 2^-21 of a row's largest weight and to a multiple of 2^-31 of it below (E4M3
+ * pools, more than 64 rows of q a kv head: to nine significant bits or more down
+ * to 2^-17 of it, to a multiple of 2^-25 of it below; in E4M3 pools a weight is one
+ * times the scale of its row of v).  Two calls with the same inputs give the same bits.
  * A sequence that exceeds max_kv_tokens is recorded as INVALID_ARG in the status
  * word and taken to have no cached tokens; one that exceeds max_seq_tokens is
  * recorded too, and its rows of out and lse stay as they are.  If a bounded device

@@ -73,7 +73,7 @@ namespace lsc {
 namespace kv {
 namespace chunk {
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool BF16 = true>
 struct Conf {
   static constexpr int NQ = D == 256 ? 1 : 2;   // row blocks of 128
   static constexpr int M = 128 * NQ;
@@ -91,8 +91,8 @@ struct Conf {
   static constexpr int soft = 208, mma = 80;
   static_assert(2 * soft + mma <= 3 * 168, "more registers than the block has");
   // powers of two: how far a row's maximum may rise above the one that set the reference, and how far the reference
-  // lies below that
-  static constexpr float lag = Q8 ? 6.f : 8.f, lift = Q8 ? 9.f : 0.f;
+  // lies below that (f16 weights, whose smallest is 2^-24, take the room up to 2^15; bf16 has the exponents as it is)
+  static constexpr float lag = Q8 ? 6.f : 8.f, lift = Q8 ? 9.f : BF16 ? 0.f : 7.f;
   // TMEM columns
   static constexpr int S0 = 0, SN = TK;         // S buffer b at S0 + b * SN; P in its first half
   static constexpr int Q0 = 128;                // QT only
@@ -328,7 +328,7 @@ struct Ring {
 template <bool BF16, bool Q8, int D>
 __global__ void __launch_bounds__(Conf<D, Q8>::threads, 1)
 chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map) {
-  using C = Conf<D, Q8>;
+  using C = Conf<D, Q8, BF16>;
   constexpr int NQ = C::NQ, M = C::M, TK = C::TK, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>(smem_raw);

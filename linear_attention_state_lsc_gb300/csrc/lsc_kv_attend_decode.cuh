@@ -17,8 +17,8 @@
 // weighted rows of all columns; scores become the weights' operand without leaving
 // the registers (a transposition of 8 x 8 each).  The warps meet at the end of a piece, where a head's parts are
 // joined in order.  The maximum is a reference that moves only when a row's
-// maximum rose by more than 2^8 (weights are 2^8 at most), so the weighted rows are
-// rarely rescaled.  Measured, 16 q heads, 64 tokens behind 64 to 16384, bf16, 2 heads of 256:
+// maximum rose by more than 2^8 (bf16 weights are 2^8 at most; f16 ones, whose smallest
+// is 2^-24, take the room up to 2^15), so the weighted rows are rarely rescaled.  Measured, 16 q heads, 64 tokens behind 64 to 16384, bf16, 2 heads of 256:
 // 1018 MB in 160 us (6.4 TB/s, 95 % of a copy's rate); E4M3, 32 q heads, 128 tokens
 // behind 500 to 8000, 8 heads of 128: 1060 MB in 178 us (6.0 TB/s, 89 %).
 //
@@ -123,6 +123,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
   constexpr int KEYS = C::KEYS, ST = C::ST, RB = C::RB;
   constexpr int KS = D / 16;        // k steps of a score, output tiles of 16 columns
   constexpr int NK = KEYS / 16;     // score tiles of 16 positions
+  constexpr float lift = BF16 ? 0.f : 7.f;  // powers of two that the reference lies below the maximum that set it
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem<ES, D> &sm = *reinterpret_cast<Smem<ES, D> *>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31, g = ln >> 2, tq = ln & 3;
@@ -370,7 +371,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
         }
       bool rise = false;
 #pragma unroll
-      for (int h = 0; h < NR; ++h) rise |= top[h][0] > m[h][0] + 8.f || top[h][1] > m[h][1] + 8.f;
+      for (int h = 0; h < NR; ++h) rise |= top[h][0] > m[h][0] + (8.f + lift) || top[h][1] > m[h][1] + (8.f + lift);
       if (__any_sync(0xffffffffu, rise)) {  // also the first one's (m is -inf)
 #pragma unroll
         for (int h = 0; h < NR; ++h)
@@ -380,7 +381,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            const float to = fmaxf(m[h][e], t), f = ex2(m[h][e] - (to == -INFINITY ? 0.f : to));
+            const float to = fmaxf(m[h][e], t - lift), f = ex2(m[h][e] - (to == -INFINITY ? 0.f : to));
             m[h][e] = to;
             l[h][e] *= f;
 #pragma unroll

@@ -16,8 +16,9 @@
 // each of the 8 warps
 //   * multiplies the rows of q with its 8 positions (scores in registers), takes
 //     the largest of each row and shares it through shared memory,
-//   * forms the weights 2^(s - m) against the running maximum m of all warps,
-//     adds them to its part of the sum, and writes them, 16-bit, to shared memory,
+//   * forms the weights 2^(s - m) against the running maximum of all warps (m lies
+//     2^15 below it for f16 weights, whose smallest is 2^-24), adds them to its part
+//     of the sum, and writes them, 16-bit, to shared memory,
 //   * multiplies all weights of the tile with its share of v's columns.
 // Every warp rescales its own columns when m grew; the sums meet at the end.
 // Measured, E4M3, 128 sequences of 8 tokens behind 500 to 8000, 32 q heads, 8 heads of
@@ -27,7 +28,7 @@
 //
 // E4M3 pools: codes go to f16 exactly (one conversion per two codes), so the
 // products run in f16; K's scale multiplies the scores.  V's scale 2^e joins the
-// weight: the running maximum is that of s + e, the weight 2^(s + e - m) <= 1 is
+// weight: the running maximum is that of s + e, the weight 2^(s + e - m) is
 // rounded to f16 relative to the largest contribution, and the sum takes
 // 2^(s - m).  q's rows are brought to [1, 2) by a power of two that the
 // scores take back, so bf16 q loses nothing that counts in f16.
@@ -115,6 +116,7 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
   constexpr int KS = D / 16;                     // k steps of a score
   constexpr int PV_WARPS = Q8 && D == 64 ? 4 : 8;  // warps that share v's columns (16 at least for E4M3)
   constexpr int COLS = D / PV_WARPS, NT = COLS / 8;
+  constexpr float lift = BF16 ? 0.f : 15.f;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem<ES, D, MT> &sm = *reinterpret_cast<Smem<ES, D, MT> *>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31, g = ln >> 2, tq = ln & 3;
@@ -341,7 +343,7 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
           }
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-          if (tq == 0) sm.top[w][16 * i + 8 * h + g] = t;
+          if (tq == 0) sm.top[w][16 * i + 8 * h + g] = t - lift;
         }
       __syncthreads();
 #pragma unroll

@@ -88,6 +88,16 @@ def test_a_flat_tail_counts_in_e4m3_chunks(lsc, D, gap):
     flat_tail(E4, BF, 40, 64, D, gap, 2.0 ** -26)
 
 
+@pytest.mark.parametrize("gap", [3.0, 17.1, 24.9, 25.1])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("pool,dtype,n,bt", [(F16, F16, 40, 64), (F16, F16, 1, 64), (F16, F16, 1, 12), (E4, F16, 1, 64),
+                                             (E4, BF, 1, 64), (E4, F16, 1, 12), (E4, F16, 8, 64), (BF, BF, 1, 64)],
+                         ids=["chunk", "decode", "rows", "decode8", "decode8-bf16", "rows8", "rows8-32", "bf16"])
+def test_a_flat_tail_counts_in_f16_weights(lsc, pool, dtype, n, bt, D, gap):
+    """f16 weights are multiples of 2^-24 beside a largest one of 2^7 or more: off by 2^-32 of it at most."""
+    flat_tail(pool, dtype, n, bt, D, gap, 0 if dtype == pool == BF else 2.0 ** -32)
+
+
 FORMS = [(BF, BF, 40, 64), (F16, F16, 40, 64), (E4, BF, 40, 64), (BF, BF, 40, 12), (BF, BF, 2, 64), (F16, F16, 2, 12),
          (E4, BF, 2, 64), (E4, F16, 2, 64), (E4, BF, 2, 12), (E4, BF, 12, 64), (L.LSC_F32, L.LSC_F32, 5, 64)]
 FORM_IDS = ["chunk-bf16", "chunk-f16", "chunk-e4m3", "chunk-bf16-12", "decode-bf16", "rows-f16", "decode-e4m3", "decode-e4m3-f16",
