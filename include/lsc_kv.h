@@ -227,7 +227,9 @@ typedef struct {
  * 2^-21 of a row's largest weight and to a multiple of 2^-31 of it below (E4M3
  * pools, more than 64 rows of q a kv head: to nine significant bits or more down
  * to 2^-17 of it, to a multiple of 2^-25 of it below; in E4M3 pools a weight is one
- * times the scale of its row of v).  Two calls with the same inputs give the same bits.
+ * times the scale of its row of v).  E4M3 rows of v with a scale below 2^-76 add an
+ * absolute error of up to 2^-93 a position; beside rows with a scale of 2^e above
+ * 2^100, positions lighter than 2^(e - 133) of the heaviest drop out of the sums.  Two calls with the same inputs give the same bits.
  * A sequence that exceeds max_kv_tokens is recorded as INVALID_ARG in the status
  * word and taken to have no cached tokens; one that exceeds max_seq_tokens is
  * recorded too, and its rows of out and lse stay as they are.  If a bounded device

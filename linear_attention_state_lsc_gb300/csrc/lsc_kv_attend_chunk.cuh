@@ -870,9 +870,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       for (int g = 0; g < TK / 32; ++g) {
         if (is_k) {
           sm.ks[sr][g * 32 + ln] = scale_of(sb[g]);
-        } else {  // bounds keep the sum of 2^(s - m) a normal number
+        } else {
           sm.vs[sr][g * 32 + ln] = scale_of(sb[g]);
-          sm.ve[sr][g * 32 + ln] = (float)(sb[g] < 87 ? -40 : sb[g] > 227 ? 100 : (int)sb[g] - 127);
+          sm.ve[sr][g * 32 + ln] = v_exponent(sb[g]);
         }
       }
       __syncwarp();

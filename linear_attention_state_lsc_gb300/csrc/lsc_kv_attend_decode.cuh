@@ -341,8 +341,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
       // ---- weights
       float vx[NK][2];
       const float k_up = Q8 ? scale_of(kb_now) : 1.f, v_up = Q8 ? scale_of(vb_now) : 1.f;  // of position `lane`
-      // bounds keep the sum of 2^(s - m) a normal number
-      const float v_ex = Q8 ? (float)(vb_now < 87 ? -40 : vb_now > 227 ? 100 : (int)vb_now - 127) : 0.f;
+      const float v_ex = Q8 ? v_exponent(vb_now) : 0.f;
       float top[NR][2];
 #pragma unroll
       for (int h = 0; h < NR; ++h) top[h][0] = top[h][1] = -INFINITY;

@@ -324,8 +324,7 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
         for (int e = 0; e < 2; ++e) {
           kx[e] = sm.ks[st][kp + e];
           vx[e] = sm.vs[st][kp + e];
-          const int ex = (int)((__float_as_uint(vx[e]) >> 23) & 255) - 127;
-          ve[e] = (float)(ex < -40 ? -40 : ex > 100 ? 100 : ex);  // bounds keep the sum of 2^(s - m) a normal number
+          ve[e] = v_exponent((__float_as_uint(vx[e]) >> 23) & 255);
         }
       }
 #pragma unroll

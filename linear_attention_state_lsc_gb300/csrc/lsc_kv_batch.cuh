@@ -83,6 +83,15 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
 }
 
+// The exponent e of V's scale as attend's reference m counts it, at least -76:
+// weights 2^(s + e - m) are 2^15 at most, so a position adds 2^(15 + 76) at most to
+// the sum of 2^(s - m), and 2^31 of them stay finite.  Rows of a smaller scale come
+// out with weights smaller by the difference; their error is 2^-93 (half an e5m2
+// step, 2^-17, times 448 over a sum of 2^(9 + 76)).  At the other end the heaviest
+// position adds 2^(7 - e) at least, and what is below 2^-126 is lost: positions
+// lighter than 2^(e - 133) of it.
+__device__ __forceinline__ float v_exponent(uint32_t byte) { return byte < 51 ? -76.f : (float)((int)byte - 127); }
+
 // The scale byte of a row whose largest magnitude has these fp32 bits (as an
 // unsigned number, so NaN counts as the largest): the smallest power of two
 // that brings m * 2^k (1 <= m < 2) to 448 = 1.75 * 2^8 is 2^(k - 8), or

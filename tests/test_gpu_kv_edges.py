@@ -133,3 +133,22 @@ def test_a_query_that_is_not_finite_is_nan_alone(lsc, pool, dtype, n, bt, D):
         got[t, h] = torch.from_numpy(want).to(got)
         ls[t, h] = float(lse)
     check_attend(host, 1, b, qx, dtype, D ** -0.5, True, out, ls)
+
+
+@pytest.mark.parametrize("power", [-70, -50, 60, 100, 124])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,bt", [(40, 64), (2, 64), (2, 12), (12, 64)], ids=["chunk", "decode", "rows", "rows-48"])
+def test_v_far_from_one(lsc, n, bt, D, power):
+    """E4M3 pools whose V rows are all tiny or all huge: the bounds of test_attend, relative to V's size."""
+    rng = np.random.default_rng(power + 2 * D)
+    b = Batch(rng, [n] * 2, [300, 1400], bt, 160)
+    host = HostKv(160, bt, 1, D, E4)
+    for i in range(2):
+        bl, r = b.places(i, 0, int(b.kv[i]))
+        for lane, up in ((0, 0), (1, power)):
+            fill(host, 1, lane, bl, r, rng.standard_normal((len(r), 1, D)) * 2.0 ** up)
+    q, qx = dense(rng.standard_normal((b.T, 4, D)), BF)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, BF, 4, D ** -0.5, True, max_seq_tokens=n)
+        assert dev.status() == L.LSC_OK
+    check_attend(host, 1, b, qx, BF, D ** -0.5, True, out, ls)
