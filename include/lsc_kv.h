@@ -218,9 +218,9 @@ typedef struct {
  *   s_j = scale q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j),
  *   lse = log sum_j exp(s_j)   (natural logarithm)
  * over the positions j that the token sees.  A token that sees none gets zeros
- * and lse = -infinity.  A score of NaN or +infinity makes the row NaN, and a row
- * of q that holds one of them or -infinity gives such scores; its lse is not
- * finite.  Positions it does not see, and rows behind a sequence's
+ * and lse = -infinity.  A score of NaN or +infinity makes the row NaN, and so do
+ * scores of -infinity alone; a row of q that holds one of the three gives such
+ * scores.  Its lse is not finite.  Positions it does not see, and rows behind a sequence's
  * last token, do not enter, whatever they hold.  Sums and softmax statistics
  * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded before they
  * meet v: to bf16 in bf16 pools; to f16 in f16 and E4M3 pools, in full down to

@@ -728,7 +728,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         if (!(ok = wait_warp(&sm.fin[block], done++, limit))) break;
         tc::fence_after_sync();
         const bool whole = q.t0 == 0 && q.t1 == q.tiles;
-        const bool empty = l == 0.f;
+        const bool empty = vis == 0;
         const float inv = whole ? (empty ? 0.f : 1.f / l) : 1.f;
         const int64_t h = q.head * p.group + (R - tok * p.group), t = q.s.row0 + tok;
         const int64_t slot = (int64_t)(2 * cta + (q.t0 == 0 ? 1 : 0)) * M + r;

@@ -495,7 +495,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
         sum += ml.y * k;
         y.x += z.x * k, y.y += z.y * k, y.z += z.z * k, y.w += z.w * k;
       }
-      const bool empty = sum == 0.f;
+      const bool empty = sm.vis[r] == 0;
       const float inv = whole ? (empty ? 0.f : 1.f / sum) : 1.f;
       y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
       if constexpr (!Q8) {

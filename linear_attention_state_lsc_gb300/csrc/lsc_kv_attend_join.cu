@@ -31,11 +31,11 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
   const int c = blockIdx.x, D = p.L.head_dim, ln = threadIdx.x & 31;
   const Cut cut = w.cut[c];
   if (cut.more == 0) return;
-  const int32_t c0 = p.b.cu[cut.seq], n = p.b.cu[cut.seq + 1] - c0;
+  const Seq s = attend_seq(p.L, p.b, cut.seq, p.max_seq, p.max_kv);
   const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
   const int MR = M / together, hr = r / MR;  // rows of a head; which head of the unit
   const int32_t R = cut.block * MR + r - hr * MR;
-  if (r >= M || R >= n * p.group) return;
+  if (r >= M || R >= s.n * p.group) return;
   auto part = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
   float m = -INFINITY;
   for (int i = ln; i <= cut.more; i += 32) m = fmaxf(m, w.ml[(int64_t)part(i) * M + r].x);
@@ -60,10 +60,10 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
       acc[v].x += k * x.x, acc[v].y += k * x.y, acc[v].z += k * x.z, acc[v].w += k * x.w;
     }
   }
-  const bool empty = l == 0.f;
-  const float inv = empty ? 0.f : 1.f / l;
   const int32_t tok = p.by_group.div(R);
-  const int64_t t = c0 + tok, h = (int64_t)(cut.head * together + hr) * p.group + (R - tok * p.group);
+  const bool empty = visible(s, tok, p.causal) == 0;
+  const float inv = empty ? 0.f : 1.f / l;
+  const int64_t t = s.row0 + tok, h = (int64_t)(cut.head * together + hr) * p.group + (R - tok * p.group);
   uint2 *dst = (uint2 *)((uint16_t *)p.out + t * p.out_stride + h * D);
   const int bf16 = p.dtype == LSC_BF16;
 #pragma unroll

@@ -426,7 +426,7 @@ rows_attend_kernel(const __grid_constant__ KvAttendParams p) {
         float sum = 0.f;
 #pragma unroll
         for (int x = 0; x < 8; ++x) sum += sm.part[x][r];
-        const bool empty = sum == 0.f;
+        const bool empty = vis[i][h] == 0;
         const float inv = whole ? (empty ? 0.f : 1.f / sum) : 1.f;
         const int32_t tok = p.by_group.div(r);
         const int64_t t = pc.s.row0 + tok, hd = (int64_t)pc.head * p.group + (r - tok * p.group);

@@ -135,6 +135,39 @@ def test_a_query_that_is_not_finite_is_nan_alone(lsc, pool, dtype, n, bt, D):
     check_attend(host, 1, b, qx, dtype, D ** -0.5, True, out, ls)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pool,dtype,n,bt", [f for f in FORMS if f[0] != E4],
+                         ids=[i for f, i in zip(FORMS, FORM_IDS) if f[0] != E4])
+def test_a_row_whose_scores_are_all_minus_infinity_is_nan(lsc, pool, dtype, n, bt, D):
+    """exp(-inf) / 0: not the zeros of a row that sees nothing.  One sequence whose parts are joined, one that is not,
+    one that sees finite scores beside the infinite ones, and one that sees nothing."""
+    rng = np.random.default_rng(n * D)
+    b = Batch(rng, [n] * 4, [n, 2600, 90, 0], bt, 300, spare=1)
+    host = filled(rng, b, 300, bt, 1, D, pool)
+    for i, finite in ((0, 0), (1, 0), (2, 30)):
+        bl, r = b.places(i, 0, int(b.kv[i]) - finite)
+        k = host.read(1, 0, bl, r)
+        k[:, 0, 3] = -np.inf
+        fill(host, 1, 0, bl, r, k)
+    x = rng.standard_normal((b.T, 4, D))
+    x[:, :, 3] = 1
+    q, qx = dense(x, dtype)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, dtype, 4, D ** -0.5, False, max_seq_tokens=n)
+        assert dev.status() == L.LSC_OK
+    assert torch.isnan(out[:2 * n]).all() and (ls[:2 * n] == -np.inf).all()
+    assert (out[3 * n:4 * n] == 0).all() and (ls[3 * n:4 * n] == -np.inf).all()
+    # the third: the positions of -infinity have weight 0; as if they held the largest negative scores
+    bl, r = b.places(2, 0, 60)
+    k = host.read(1, 0, bl, r)
+    k[:, 0, 3] = -30000.0
+    fill(host, 1, 0, bl, r, k)
+    want = _kv.attend(host, 1, b, qx, D ** -0.5, False)[0]
+    got = out.double().cpu().numpy().reshape(b.T, 4, D)
+    assert np.isfinite(got[2 * n:3 * n]).all()
+    assert np.abs(got - want)[2 * n:3 * n].max() <= 2.0 ** -6 * np.abs(want[2 * n:3 * n]).max()
+
+
 @pytest.mark.parametrize("power", [-70, -50, 60, 100, 124])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("n,bt", [(40, 64), (2, 64), (2, 12), (12, 64)], ids=["chunk", "decode", "rows", "rows-48"])
