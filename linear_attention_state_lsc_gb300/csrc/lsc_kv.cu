@@ -230,7 +230,7 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
   r->group = a->num_q_heads / H;
   r->causal = a->causal;
   r->scale_log2 = a->scale * 1.44269504088896341f;
-  r->max_seq = a->max_seq_tokens ? a->max_seq_tokens : a->batch.total_tokens;
+  r->max_seq = a->max_seq_tokens ? std::min(a->max_seq_tokens, a->batch.total_tokens) : a->batch.total_tokens;
   r->max_kv = a->max_kv_tokens ? std::min(a->max_kv_tokens, r->b.held) : r->b.held;
   r->by_group.set((uint32_t)r->group);
   r->num_sms = p->num_sms;
@@ -261,7 +261,7 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   const bool types = r.dtype != LSC_F32 && (r.L.dtype == r.dtype || q8);
   if (!types || (D != 64 && D != 128 && D != 256) || (mis & 15) != 0) return kAny;
   // the tensor-core kernels count packed rows, positions and tiles (and up to 64 for each unit) in 31 bits
-  const int64_t rows = (int64_t)std::min(r.max_seq, r.b.total_tokens) * r.group;
+  const int64_t rows = (int64_t)r.max_seq * r.group;
   const int64_t units = (int64_t)r.b.total_tokens * r.group / 16 + r.b.n_seq;
   if (rows > INT32_MAX - 1024 || r.max_kv > INT32_MAX - 1024 || units * r.L.heads > INT32_MAX / (r.max_kv / 64 + 1 + 64))
     return kAny;

@@ -1,7 +1,7 @@
 // lsc_kv_attend_rows.cuh -- attention over a layer of the K/V block pool for
 // sequences with few packed rows (lsc_kv_attend.cuh): decode steps where blocks do
 // not fit TMA boxes, and over E4M3 pools a few speculated tokens and short chunks.
-// Up to 16 * MT rows a unit.
+// Up to 16 * MT rows a unit, MT 1 (and 4 for E4M3).
 //
 // K and V are read once, so HBM bounds it: 4 * head_dim bytes a position and kv
 // head at 16 bits against 4 * head_dim * rows operations, at 16 rows 16
@@ -59,7 +59,7 @@ struct Conf {
   static constexpr int RB = D * ES + 16;           // bytes of a K or V row in the ring
   static constexpr int stage = 2 * kTK * RB;
   static constexpr int occ = MT == 1 && D * ES <= 256 ? 2 : 1;
-  static constexpr int ST = D * ES >= 512 ? (MT == 1 ? 3 : 2) : D * ES == 256 ? (MT == 1 ? 3 : 5) : D * ES == 128 ? 5 : 6;
+  static constexpr int ST = D * ES >= 256 ? (MT == 1 ? 3 : 5) : D * ES == 128 ? 5 : 6;
 };
 
 template <int ES, int D, int MT>
@@ -479,18 +479,24 @@ cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStre
 }
 
 // One type's kernels, by head size and rows.
+template <bool BF16, int ES, int D>
+cudaError_t launch_size(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+  if constexpr (ES == 1)  // 16-bit pools: more than 16 rows are the chunk kernel's
+    if (plan.M > 16) return launch_one<BF16, ES, D, 4>(p, plan, stream);
+  return launch_one<BF16, ES, D, 1>(p, plan, stream);
+}
+
 template <bool BF16, int ES>
 cudaError_t launch_type(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
-  const bool one = plan.M == 16;
   switch (p.L.head_dim) {
-    case 64: return one ? launch_one<BF16, ES, 64, 1>(p, plan, stream) : launch_one<BF16, ES, 64, 4>(p, plan, stream);
-    case 128: return one ? launch_one<BF16, ES, 128, 1>(p, plan, stream) : launch_one<BF16, ES, 128, 4>(p, plan, stream);
-    default: return one ? launch_one<BF16, ES, 256, 1>(p, plan, stream) : launch_one<BF16, ES, 256, 4>(p, plan, stream);
+    case 64: return launch_size<BF16, ES, 64>(p, plan, stream);
+    case 128: return launch_size<BF16, ES, 128>(p, plan, stream);
+    default: return launch_size<BF16, ES, 256>(p, plan, stream);
   }
 }
 
 template <int ES, int D>
-constexpr int occ_of(int M) { return M == 16 ? Conf<ES, D, 1>::occ : Conf<ES, D, 4>::occ; }
+constexpr int occ_of(int M) { return M == 16 ? Conf<ES, D, 1>::occ : Conf<ES, D, ES == 1 ? 4 : 1>::occ; }
 
 }  // namespace rows
 }  // namespace kv

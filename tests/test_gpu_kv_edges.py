@@ -185,3 +185,23 @@ def test_v_far_from_one(lsc, n, bt, D, power):
         out, ls = run_attend(dev, 1, b, q, BF, 4, D ** -0.5, True, max_seq_tokens=n)
         assert dev.status() == L.LSC_OK
     check_attend(host, 1, b, qx, BF, D ** -0.5, True, out, ls)
+
+
+@pytest.mark.parametrize("bt", [64, 12])
+@pytest.mark.parametrize("pool,dtype", [(BF, BF), (F16, F16), (E4, BF)], ids=["bf16", "f16", "e4m3"])
+def test_a_bound_above_the_step_s_tokens(lsc, pool, dtype, bt):
+    """max_seq_tokens as a constant of the program, above what this step brings: the same bits as with the step's own."""
+    rng = np.random.default_rng(14)
+    b = Batch(rng, [1], [700], bt, 70)
+    host = filled(rng, b, 70, bt, 2, 128, pool)
+    q, qx = dense(rng.standard_normal((1, 16, 128)), dtype)
+    with DevKv(host) as dev:
+        own = run_attend(dev, 1, b, q, dtype, 16, 0.1, True, max_seq_tokens=1)
+        for bound in (16, 1 << 30):
+            out, ls = run_attend(dev, 1, b, q, dtype, 16, 0.1, True, max_seq_tokens=bound)
+            check_attend(host, 1, b, qx, dtype, 0.1, True, out, ls)
+            assert torch.equal(out, own[0]) and torch.equal(ls, own[1])
+        assert dev.status() == L.LSC_OK
+        need = [L.lsc_kv_attend_workspace_bytes(dev.pool, L.kv_attend_args(b.device(), 16, q, out, dtype, 0.1, max_seq_tokens=m))[1]
+                for m in (1, 16, 1 << 30)]
+    assert need[0] == need[1] == need[2]  # the same rows a tile
