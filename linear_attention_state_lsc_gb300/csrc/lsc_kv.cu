@@ -251,6 +251,7 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
 // kernel 398 us, chunk kernel 193; of 3 tokens, 24 rows: 382 and 189; one sequence
 // of 4 behind 1000: 23 and 25; E4M3, 128 sequences of 8 tokens, 32 rows: 1121 and 1131.
 constexpr int32_t kDecodeMost = 16, kRowsMost = 64;
+constexpr int64_t kMostCounts = 1 << 30;
 enum Form { kAny, kDecode, kRows, kChunk };
 
 Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
@@ -260,22 +261,26 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   const bool q8 = r.L.dtype == LSC_E4M3;
   const bool types = r.dtype != LSC_F32 && (r.L.dtype == r.dtype || q8);
   if (!types || (D != 64 && D != 128 && D != 256) || (mis & 15) != 0) return kAny;
-  // the tensor-core kernels count packed rows, positions and tiles (and up to 64 for each unit) in 31 bits
+  // the tensor-core kernels count packed rows, positions and the units' tiles in 31 bits
   const int64_t rows = (int64_t)r.max_seq * r.group;
-  const int64_t units = (int64_t)r.b.total_tokens * r.group / 16 + r.b.n_seq;
-  if (rows > INT32_MAX - 1024 || r.max_kv > INT32_MAX - 1024 || units * r.L.heads > INT32_MAX / (r.max_kv / 64 + 1 + 64))
-    return kAny;
+  if (rows > INT32_MAX - 1024 || r.max_kv > INT32_MAX - 1024) return kAny;
+  Form form = kChunk;
+  int64_t blocks = r.b.n_seq;  // row blocks of all sequences at most; the two forms for few rows have one a sequence
   if (rows <= kDecodeMost && r.box_decode > 0) {
+    form = kDecode;
     *plan = lsc::plan_kv_attend_decode(r);
-    return kDecode;
-  }
-  if (rows <= (q8 ? kRowsMost : kDecodeMost)) {
+  } else if (rows <= (q8 ? kRowsMost : kDecodeMost)) {
+    form = kRows;
     *plan = lsc::plan_kv_attend_rows(r);
-    return kRows;
+  } else {
+    if (q8 && r.dtype != LSC_BF16) return kAny;  // q is two e4m3 rows there, too few bits for f16
+    *plan = lsc::plan_kv_attend_chunk(r);
+    blocks += (int64_t)r.b.total_tokens * r.group / plan->M;
   }
-  if (q8 && r.dtype != LSC_BF16) return kAny;  // q is two e4m3 rows there, too few bits for f16
-  *plan = lsc::plan_kv_attend_chunk(r);
-  return kChunk;
+  // a run ends one run's length behind the last count at most
+  if (blocks * r.L.heads <= kMostCounts / (r.max_kv / plan->TK + 1 + plan->lead)) return form;
+  *plan = lsc::AttendPlan{};
+  return kAny;
 }
 
 }  // namespace

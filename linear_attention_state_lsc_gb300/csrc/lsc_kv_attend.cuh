@@ -248,6 +248,7 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
 struct AttendPlan {
   int32_t ctas;    // runs
   int32_t M;       // rows of a unit, `together` heads' worth
+  int32_t TK;      // positions of a tile
   int32_t together;  // kv heads of a unit
   size_t ws_bytes;
   bool may_cut;    // false: units are not cut

@@ -88,6 +88,7 @@ AttendPlan plan_kv_attend_rows(const KvAttendParams &p) {
   const int D = p.L.head_dim, q8 = p.L.dtype == LSC_E4M3;
   AttendPlan plan{};
   plan.together = 1;
+  plan.TK = kTK;
   plan.M = (int64_t)p.max_seq * p.group <= 16 ? 16 : 64;
   const int occ = q8 ? (D == 64 ? occ_of<1, 64>(plan.M) : D == 128 ? occ_of<1, 128>(plan.M) : occ_of<1, 256>(plan.M))
                      : (D == 64 ? occ_of<2, 64>(plan.M) : D == 128 ? occ_of<2, 128>(plan.M) : occ_of<2, 256>(plan.M));
@@ -104,6 +105,7 @@ AttendPlan plan_kv_attend_decode(const KvAttendParams &p) {
   using namespace kv::decode;
   const int D = p.L.head_dim, q8 = p.L.dtype == LSC_E4M3;
   AttendPlan plan{};
+  plan.TK = kTK;
   // Heads that lie side by side in a row are read side by side, up to 1 KB of them: 128 bytes at a time left the memory
   // at 61 % of the copy rate.  Not where that would leave CTAs without a tile: one sequence of 1001 tokens over 2 heads
   // took 17 us on 32 CTAs and 22 on 16.
@@ -143,6 +145,7 @@ AttendPlan plan_kv_attend_chunk(const KvAttendParams &p) {
   const int D = p.L.head_dim, TK = D == 256 ? Conf<256, false>::TK : Conf<128, false>::TK;
   AttendPlan plan{};
   plan.together = 1;
+  plan.TK = TK;
   plan.M = D == 256 ? Conf<256, false>::M : Conf<128, false>::M;
   const int64_t tiles = ((int64_t)p.max_kv + TK - 1) / TK;
   const int64_t units = (((int64_t)p.b.total_tokens * p.group + plan.M - 1) / plan.M + p.b.n_seq) * p.L.heads;

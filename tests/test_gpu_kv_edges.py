@@ -187,6 +187,33 @@ def test_v_far_from_one(lsc, n, bt, D, power):
     check_attend(host, 1, b, qx, BF, D ** -0.5, True, out, ls)
 
 
+def test_a_large_bound_stays_on_the_tensor_cores(lsc):
+    """131072 rows of 16 q heads over 2 kv heads and a bound of 2^20 positions count 67 million tiles: far from 31 bits.
+    With the injected fault every bounded wait gives up at once, so the status word tells the tensor-core kernel (which
+    waits) from the CUDA-core one (which does not).  One sequence of 100 tokens is all that is there."""
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+from _kv import DevKv, HostKv
+from linear_attention_state_lsc_gb300 import lsc as L
+T, H, G, D, bt = 131072, 2, 8, 128, 64
+with DevKv(HostKv(4, bt, H, D, L.LSC_BF16, layers=1, fill=0)) as dev:
+    table = torch.zeros((1, 16384), dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+    kv = torch.tensor([200], dtype=torch.int32, device="cuda")
+    q = torch.zeros((T, H * G * D), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(q)
+    a = L.kv_attend_args(L.kv_batch(1, T, table, cu, kv, max_blocks=16384), H * G, q, out, L.LSC_BF16, 0.1)
+    assert L.lsc_kv_attend(dev.pool, 0, a, torch.cuda.current_stream()) == L.LSC_OK
+    assert dev.status() == L.LSC_ERR_DEV_TIMEOUT, dev.status()
+print("reported")
+"""
+    r = subprocess.run([sys.executable, "-c", code % (os.path.dirname(HERE), HERE)], capture_output=True, text=True,
+                       env=dict(os.environ, LSC_FAULT="timeout0"), timeout=300)
+    assert "reported" in r.stdout, r.stderr[-2000:]
+
+
 @pytest.mark.parametrize("bt", [64, 12])
 @pytest.mark.parametrize("pool,dtype", [(BF, BF), (F16, F16), (E4, BF)], ids=["bf16", "f16", "e4m3"])
 def test_a_bound_above_the_step_s_tokens(lsc, pool, dtype, bt):
