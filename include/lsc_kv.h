@@ -205,8 +205,8 @@ typedef struct {
   int64_t out_stride;
   int32_t max_seq_tokens; /* bound of every n_i that the host knows; 0 = total_tokens */
   int32_t max_kv_tokens;  /* bound of every kv_lens[i] that the host knows; 0 = max_blocks * block_tokens */
-  void *workspace;        /* device scratch of at least workspace_bytes
-                             (lsc_kv_attend_workspace_bytes), 16-byte aligned, untouched by
+  void *workspace;        /* device scratch of workspace_bytes, what
+                             lsc_kv_attend_workspace_bytes says or more, 16-byte aligned, untouched by
                              others until the call's work on the stream completes; NULL = the
                              library takes it from the device's stream-ordered pool */
   size_t workspace_bytes;
@@ -248,9 +248,13 @@ typedef struct {
  */
 int lsc_kv_attend(lsc_kv_pool *pool, int32_t layer, const lsc_kv_attend_args *args, void *stream);
 
-/* Bytes of workspace lsc_kv_attend needs for these arguments (0: none).  Reads
- * the sizes only, so one workspace of the largest size serves every layer and
- * step of a stream.  Errors: as lsc_kv_attend's argument checks. */
+/* Bytes of workspace that lsc_kv_attend asks for with these arguments, and that
+ * serve every call over this pool of the same types and heads whose n_seq,
+ * total_tokens, max_seq_tokens and max_kv_tokens (0 meaning total_tokens and
+ * max_blocks * block_tokens) are no larger: asked once with the largest sizes, one
+ * workspace serves every layer and step of a stream, prefill and decode alike.
+ * 0: none.  The pointers are checked and do not matter otherwise.  Errors: as
+ * lsc_kv_attend's argument checks; CUDA (a host-only pool). */
 int lsc_kv_attend_workspace_bytes(const lsc_kv_pool *pool, const lsc_kv_attend_args *args, size_t *bytes);
 
 #ifdef __cplusplus

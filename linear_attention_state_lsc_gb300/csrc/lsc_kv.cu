@@ -254,13 +254,16 @@ constexpr int32_t kDecodeMost = 16, kRowsMost = 64;
 constexpr int64_t kMostCounts = 1 << 30;
 enum Form { kAny, kDecode, kRows, kChunk };
 
+bool tensor_core_types(const lsc::KvAttendParams &r) {
+  const int D = r.L.head_dim;
+  return r.dtype != LSC_F32 && (r.L.dtype == r.dtype || r.L.dtype == LSC_E4M3) && (D == 64 || D == 128 || D == 256);
+}
+
 Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   *plan = lsc::AttendPlan{};
-  const int D = r.L.head_dim;
   const uintptr_t mis = (uintptr_t)r.q | (uintptr_t)r.out | (uintptr_t)(r.q_stride * 2) | (uintptr_t)(r.out_stride * 2);
   const bool q8 = r.L.dtype == LSC_E4M3;
-  const bool types = r.dtype != LSC_F32 && (r.L.dtype == r.dtype || q8);
-  if (!types || (D != 64 && D != 128 && D != 256) || (mis & 15) != 0) return kAny;
+  if (!tensor_core_types(r) || (mis & 15) != 0) return kAny;
   // the tensor-core kernels count packed rows, positions and the units' tiles in 31 bits
   const int64_t rows = (int64_t)r.max_seq * r.group;
   if (rows > INT32_MAX - 1024 || r.max_kv > INT32_MAX - 1024) return kAny;
@@ -281,6 +284,27 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   if (blocks * r.L.heads <= kMostCounts / (r.max_kv / plan->TK + 1 + plan->lead)) return form;
   *plan = lsc::AttendPlan{};
   return kAny;
+}
+
+// What every call of these sizes or smaller ones needs: the most over the forms that one of them may take, each at its
+// largest sizes.  A form's need grows with every size; for decode with and without heads side by side, which smaller
+// sizes may do without.
+size_t attend_workspace(lsc::KvAttendParams r) {
+  if (!tensor_core_types(r)) return 0;
+  const bool q8 = r.L.dtype == LSC_E4M3;
+  const int32_t max_seq = r.max_seq, few = q8 ? kRowsMost : kDecodeMost;
+  size_t most = 0;
+  auto rows_up_to = [&](int32_t rows) {
+    r.max_seq = std::min(max_seq, rows / r.group);
+    return r.max_seq > 0;
+  };
+  if (r.box_decode > 0 && rows_up_to(kDecodeMost))
+    most = std::max(lsc::plan_kv_attend_decode(r).ws_bytes, lsc::plan_kv_attend_decode(r, false).ws_bytes);
+  if ((q8 || r.box_decode == 0) && rows_up_to(few)) most = std::max(most, lsc::plan_kv_attend_rows(r).ws_bytes);
+  r.max_seq = max_seq;
+  if ((int64_t)max_seq * r.group > few && !(q8 && r.dtype != LSC_BF16))
+    most = std::max(most, lsc::plan_kv_attend_chunk(r).ws_bytes);
+  return most;
 }
 
 }  // namespace
@@ -512,11 +536,8 @@ int lsc_kv_attend_workspace_bytes(const lsc_kv_pool *p, const lsc_kv_attend_args
   lsc::KvAttendParams r{};
   const int rc = check_attend(p, 0, a, &r);
   if (rc != LSC_OK) return rc;
-  *bytes = 0;
-  if (r.b.n_seq == 0 || r.b.total_tokens == 0) return LSC_OK;
-  lsc::AttendPlan plan;
-  attend_form(r, &plan);
-  *bytes = plan.ws_bytes;
+  if (p->device < 0) return LSC_ERR_CUDA;  // host-only pool: the need depends on the device
+  *bytes = r.b.n_seq == 0 || r.b.total_tokens == 0 ? 0 : attend_workspace(r);
   return LSC_OK;
 }
 
@@ -533,7 +554,7 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
   cudaStream_t s = (cudaStream_t)stream;
   void *ws = a->workspace;
   if (plan.ws_bytes > 0) {
-    if (ws && a->workspace_bytes < plan.ws_bytes) return LSC_ERR_INVALID_ARG;
+    if (ws && a->workspace_bytes < attend_workspace(r)) return LSC_ERR_INVALID_ARG;
     if (!ws && cudaMallocAsync(&ws, plan.ws_bytes, s) != cudaSuccess) {
       cudaGetLastError();
       return LSC_ERR_NO_MEMORY;

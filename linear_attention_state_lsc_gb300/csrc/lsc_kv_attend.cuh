@@ -257,7 +257,7 @@ struct AttendPlan {
 };
 cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_decode(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
-AttendPlan plan_kv_attend_decode(const KvAttendParams &p);
+AttendPlan plan_kv_attend_decode(const KvAttendParams &p, bool side_by_side = true);
 cudaError_t launch_kv_attend_join(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 AttendPlan plan_kv_attend_rows(const KvAttendParams &p);
 cudaError_t launch_kv_attend_chunk(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);

@@ -101,7 +101,7 @@ AttendPlan plan_kv_attend_rows(const KvAttendParams &p) {
   return plan;
 }
 
-AttendPlan plan_kv_attend_decode(const KvAttendParams &p) {
+AttendPlan plan_kv_attend_decode(const KvAttendParams &p, bool side_by_side) {
   using namespace kv::decode;
   const int D = p.L.head_dim, q8 = p.L.dtype == LSC_E4M3;
   AttendPlan plan{};
@@ -110,7 +110,7 @@ AttendPlan plan_kv_attend_decode(const KvAttendParams &p) {
   // at 61 % of the copy rate.  Not where that would leave CTAs without a tile: one sequence of 1001 tokens over 2 heads
   // took 17 us on 32 CTAs and 22 on 16.
   const int row = D * (q8 ? 1 : 2), H = p.L.heads;
-  plan.together = H % 4 == 0 && row <= 256 ? 4 : H % 2 == 0 && row <= 512 ? 2 : 1;
+  plan.together = !side_by_side ? 1 : H % 4 == 0 && row <= 256 ? 4 : H % 2 == 0 && row <= 512 ? 2 : 1;
   if ((int64_t)p.b.n_seq * (H / plan.together) * p.max_kv < (int64_t)p.num_sms * 4 * kTK) plan.together = 1;
   plan.M = ((int64_t)p.max_seq * p.group <= 8 ? 8 : 16) * plan.together;
   const int occ = q8 ? (D == 64 ? Conf<1, 64>::occ : D == 128 ? Conf<1, 128>::occ : Conf<1, 256>::occ)

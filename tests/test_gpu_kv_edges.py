@@ -187,6 +187,51 @@ def test_v_far_from_one(lsc, n, bt, D, power):
     check_attend(host, 1, b, qx, BF, D ** -0.5, True, out, ls)
 
 
+@pytest.mark.parametrize("pool,H,G,D,bt", [(BF, 8, 4, 128, 16), (BF, 2, 8, 256, 64), (E4, 8, 4, 128, 64), (F16, 4, 2, 64, 12),
+                                           (E4, 2, 16, 64, 5)])
+def test_one_workspace_serves_every_smaller_step(lsc, pool, H, G, D, bt):
+    """What the query answers for the largest sizes is enough for any step within them, whichever kernel it takes and
+    however q and out are aligned; a small one of each kind is run in it."""
+    rng = np.random.default_rng(13)
+    dtype = F16 if pool == F16 else BF
+    S, most, kv = 64, 40, 1024
+    host = HostKv(20, bt, H, D, pool, layers=1)
+    pad = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    dev_ints = torch.zeros(1 << 12, dtype=torch.int32, device="cuda")
+
+    def need(dev, n_seq, total, max_seq, max_kv, off=0):
+        b = L.kv_batch(n_seq, total, dev_ints, dev_ints, dev_ints, max_blocks=-(-kv // bt))
+        at = pad.data_ptr() + off
+        a = L.kv_attend_args(b, H * G, at, at, dtype, 0.125, max_seq_tokens=max_seq, max_kv_tokens=max_kv)
+        rc, bytes_ = L.lsc_kv_attend_workspace_bytes(dev.pool, a)
+        assert rc == L.LSC_OK
+        return bytes_
+
+    with DevKv(host) as dev:
+        top = need(dev, S, S * most, most, kv)
+        assert top == need(dev, S, S * most, most, kv, off=2)  # the pointers do not matter
+        for _ in range(300):
+            s = int(rng.integers(1, S + 1))
+            m = int(rng.integers(1, most + 1)) if rng.random() < 0.7 else 1
+            t = int(rng.integers(1, s * m + 1))
+            assert need(dev, s, t, m, int(rng.integers(1, kv + 1)), off=2 * int(rng.integers(0, 2))) <= top
+    ws = torch.full((top,), 0xFF, dtype=torch.uint8, device="cuda")
+    for n, kvs in (([40, 1, 9], [40, 900, 9]), ([1] * 6, [1, 600, 64, 65, 200, 0]), ([3, 1], [500, 77]), ([1], [1000])):
+        blocks = int(sum(-(-x // bt) for x in kvs)) + 1
+        b = Batch(rng, n, kvs, bt, blocks)
+        host = filled(rng, b, blocks, bt, H, D, pool, layers=1, layer=0)
+        q, qx = dense(rng.standard_normal((b.T, H * G, D)), dtype)
+        out = torch.full_like(q, 7.0)
+        ls = torch.full((b.T, H * G), 7.0, device="cuda")
+        with DevKv(host) as dev:
+            a = L.kv_attend_args(b.device(), H * G, q, out, dtype, D ** -0.5, lse=ls, max_seq_tokens=max(n),
+                                 workspace=ws, workspace_bytes=top)
+            assert L.lsc_kv_attend(dev.pool, 0, a, cur()) == L.LSC_OK
+            torch.cuda.synchronize()
+            assert dev.status() == L.LSC_OK
+        check_attend(host, 0, b, qx, dtype, D ** -0.5, True, out, ls)
+
+
 def test_a_large_bound_stays_on_the_tensor_cores(lsc):
     """131072 rows of 16 q heads over 2 kv heads and a bound of 2^20 positions count 67 million tiles: far from 31 bits.
     With the injected fault every bounded wait gives up at once, so the status word tells the tensor-core kernel (which
