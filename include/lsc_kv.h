@@ -88,7 +88,8 @@ int lsc_kv_pool_required_bytes(const lsc_kv_pool_desc *desc, size_t *total_bytes
 /* Create a K/V pool; device_base == NULL allocates (cudaMalloc, owned),
  * otherwise the 256-byte-aligned buffer is borrowed.  Without a GPU a borrowed
  * base gives a host-only pool (views work, copies return CUDA).  On a GPU the
- * library also allocates a 4-byte device status word and a pinned host word.
+ * library also allocates a device status word.  A pool may be created, and one on a
+ * borrowed base destroyed, while the thread captures a stream into a graph.
  * Errors: as lsc_kv_pool_required_bytes, plus MISALIGNED (base), NO_MEMORY, CUDA. */
 int lsc_kv_pool_create(const lsc_kv_pool_desc *desc, void *device_base, size_t base_bytes, lsc_kv_pool **out);
 int lsc_kv_pool_destroy(lsc_kv_pool *pool);

@@ -29,7 +29,6 @@ struct lsc_kv_pool {
   int64_t es = 0, row_bytes = 0, payload = 0, lane_bytes = 0, region_bytes = 0;
   int32_t scale_off = 0;        // E4M3: page offset of the scale bytes
   int32_t *status = nullptr;    // device error word
-  int32_t *h_status = nullptr;  // pinned
   int32_t box_rows = 0;         // rows of a TMA box of `maps`
   int32_t box_decode = 0;       // and of `maps_decode`
   std::vector<CUtensorMap> maps, maps_decode;  // per layer; empty: none
@@ -138,6 +137,28 @@ void make_maps(lsc_kv_pool *p) {
   p->maps_decode.swap(decode);
   p->box_rows = box;
   p->box_decode = box_decode;
+}
+
+// Allocations by a thread that is capturing a stream: allowed while this lives (they touch no stream).
+struct WhileCapturing {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  WhileCapturing() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~WhileCapturing() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// The status word, cleared on a stream of its own: the default stream may be waiting for one that is being captured.
+int32_t *make_status() {
+  int32_t *word = nullptr;
+  if (cudaMalloc(&word, 256) != cudaSuccess) return nullptr;
+  cudaStream_t s;
+  bool ok = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess;
+  if (ok) {
+    ok = cudaMemsetAsync(word, 0, 256, s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+    cudaStreamDestroy(s);
+  }
+  if (ok) return word;
+  cudaFree(word);
+  return nullptr;
 }
 
 int check_device(const lsc_kv_pool *p) {
@@ -358,17 +379,12 @@ int lsc_kv_pool_create(const lsc_kv_pool_desc *desc, void *device_base, size_t b
     delete p;
     return LSC_ERR_CUDA;
   }
-  if (cudaMalloc(&p->status, 256) != cudaSuccess) {
+  const WhileCapturing allowed;
+  p->status = make_status();
+  if (!p->status) {
     cudaGetLastError();
     delete p;
     return LSC_ERR_NO_MEMORY;
-  }
-  if (cudaMemset(p->status, 0, 256) != cudaSuccess ||
-      cudaMallocHost(&p->h_status, sizeof(int32_t)) != cudaSuccess) {
-    cudaGetLastError();
-    cudaFree(p->status);
-    delete p;
-    return LSC_ERR_CUDA;
   }
   if (device_base) {
     p->base = (uint8_t *)device_base;
@@ -376,7 +392,6 @@ int lsc_kv_pool_create(const lsc_kv_pool_desc *desc, void *device_base, size_t b
     if (cudaMalloc(&p->base, need) != cudaSuccess) {
       cudaGetLastError();
       cudaFree(p->status);
-      cudaFreeHost(p->h_status);
       delete p;
       return LSC_ERR_NO_MEMORY;
     }
@@ -391,10 +406,13 @@ int lsc_kv_pool_destroy(lsc_kv_pool *p) {
   if (!p) return LSC_ERR_INVALID_ARG;
   int rc = LSC_OK;
   if (p->device >= 0) {
-    if (cudaDeviceSynchronize() != cudaSuccess) rc = LSC_ERR_CUDA;
+    if (p->owns_base && cudaDeviceSynchronize() != cudaSuccess) rc = LSC_ERR_CUDA;
+    const WhileCapturing allowed;
     if (p->owns_base) cudaFree(p->base);
-    cudaFree(p->status);
-    cudaFreeHost(p->h_status);
+    if (cudaFree(p->status) != cudaSuccess) {  // waits for the work that may still write it
+      cudaGetLastError();
+      rc = LSC_ERR_CUDA;
+    }
   }
   delete p;
   return rc;
@@ -432,10 +450,11 @@ int lsc_kv_pool_status(lsc_kv_pool *p, void *stream, int32_t *host_status) {
   const int rc = check_device(p);
   if (rc != LSC_OK) return rc;
   cudaStream_t s = (cudaStream_t)stream;
-  if (cudaMemcpyAsync(p->h_status, p->status, sizeof(int32_t), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+  int32_t word = 0;
+  if (cudaMemcpyAsync(&word, p->status, sizeof(int32_t), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
       cudaMemsetAsync(p->status, 0, sizeof(int32_t), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
     return LSC_ERR_CUDA;
-  *host_status = *p->h_status;
+  *host_status = word;
   return LSC_OK;
 }
 

@@ -187,6 +187,38 @@ def test_v_far_from_one(lsc, n, bt, D, power):
     check_attend(host, 1, b, qx, BF, D ** -0.5, True, out, ls)
 
 
+def test_a_pool_is_made_and_used_while_a_graph_is_captured(lsc):
+    """A pool on a borrowed buffer, made and one destroyed on the thread that is capturing a stream (the default, strict
+    mode), as before the pool had a status word."""
+    rng = np.random.default_rng(12)
+    b = Batch(rng, [3, 1], [70, 20], 16, 10)
+    host = HostKv(10, 16, 2, 64, BF, layers=1)
+    buf = torch.from_numpy(host.bytes.reshape(-1).copy()).cuda()
+    (k, kx), (v, vx) = (dense(rng.standard_normal((b.T, 2, 64)), BF) for _ in "kv")
+    args = L.kv_append_args(b.device(), k, v, BF)
+    rc, warm = L.lsc_kv_pool_create(host.desc, buf, buf.numel())  # the kernel is loaded before the capture
+    assert rc == L.LSC_OK and L.lsc_kv_append(warm, 0, args, cur()) == L.LSC_OK
+    torch.cuda.synchronize()
+    buf.copy_(torch.from_numpy(host.bytes.reshape(-1)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rc, pool = L.lsc_kv_pool_create(host.desc, buf, buf.numel())
+        made = rc
+        gone = L.lsc_kv_pool_destroy(warm)
+        call = L.lsc_kv_append(pool, 0, args, cur()) if rc == L.LSC_OK else rc
+    assert (made, gone, call) == (L.LSC_OK,) * 3
+    graph.replay()
+    torch.cuda.synchronize()
+    assert L.lsc_kv_pool_status(pool, cur()) == L.LSC_OK
+    for i in range(2):
+        bl, r = b.places(i, int(b.kv[i] - b.n[i]), int(b.kv[i]))
+        host.write(0, 0, bl, r, kx[b.cu[i]:b.cu[i + 1]])
+        host.write(0, 1, bl, r, vx[b.cu[i]:b.cu[i + 1]])
+    np.testing.assert_array_equal(buf.cpu().numpy().reshape(host.bytes.shape), host.bytes)
+    del graph
+    assert L.lsc_kv_pool_destroy(pool) == L.LSC_OK
+
+
 @pytest.mark.parametrize("pool,H,G,D,bt", [(BF, 8, 4, 128, 16), (BF, 2, 8, 256, 64), (E4, 8, 4, 128, 64), (F16, 4, 2, 64, 12),
                                            (E4, 2, 16, 64, 5)])
 def test_one_workspace_serves_every_smaller_step(lsc, pool, H, G, D, bt):
