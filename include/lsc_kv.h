@@ -137,12 +137,14 @@ int lsc_copy_prefix(lsc_kv_pool *pool, const lsc_kv_copy_op *ops, int32_t n_ops,
  *  - INVALID_ARG: cu_seqlens that does not begin with 0, decreases or exceeds
  *    total_tokens.  No call reads or writes outside its arrays then; the batch's
  *    dense rows (append: its blocks' rows) are unspecified.
- *  - INVALID_ARG: kv_lens[i] < 0 or > max_blocks * block_tokens.  The sequence
- *    is taken to have no cached tokens.
+ *  - INVALID_ARG: kv_lens[i] < 0, > max_blocks * block_tokens or >
+ *    LSC_KV_MAX_TOKENS.  The sequence is taken to have no cached tokens.
  *  - OUT_OF_RANGE: a block id outside [0, num_blocks) where a position needs it.
  *    append skips the row, gather gives zeros; what attend gives for that
  *    sequence is unspecified.
  */
+#define LSC_KV_MAX_TOKENS (0x7fffffff - 1024)
+
 typedef struct {
   int32_t n_seq;
   int32_t total_tokens;       /* rows of the dense arrays, >= cu_seqlens[n_seq] */

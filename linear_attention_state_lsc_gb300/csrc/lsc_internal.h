@@ -276,7 +276,7 @@ struct KvLayer {
 
 struct KvBatch {
   int32_t n_seq, total_tokens, max_blocks;
-  int32_t held;         // tokens that max_blocks blocks hold (at most 2^31 - 1)
+  int32_t held;         // tokens that max_blocks blocks hold (at most LSC_KV_MAX_TOKENS)
   const int32_t *table, *cu, *kv;
 };
 

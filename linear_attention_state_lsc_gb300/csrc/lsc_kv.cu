@@ -195,9 +195,9 @@ int check_batch(const lsc_kv_pool *p, const lsc_kv_batch &b, lsc::KvBatch *out) 
   if (b.n_seq > 0 && (!b.cu_seqlens || !b.kv_lens || (b.max_blocks > 0 && !b.block_table))) return LSC_ERR_INVALID_ARG;
   if (misaligned(b.cu_seqlens, 4) || misaligned(b.kv_lens, 4) || misaligned(b.block_table, 4))
     return LSC_ERR_MISALIGNED;
-  const int64_t held = (int64_t)b.max_blocks * p->d.block_tokens;
-  *out = {b.n_seq, b.total_tokens, b.max_blocks, (int32_t)std::min<int64_t>(held, INT32_MAX),
-          b.block_table, b.cu_seqlens, b.kv_lens};
+  // the kernels step past the last position by up to a few tiles, in 32 bits
+  const int64_t held = std::min<int64_t>((int64_t)b.max_blocks * p->d.block_tokens, LSC_KV_MAX_TOKENS);
+  *out = {b.n_seq, b.total_tokens, b.max_blocks, (int32_t)held, b.block_table, b.cu_seqlens, b.kv_lens};
   return LSC_OK;
 }
 
@@ -285,9 +285,9 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   const uintptr_t mis = (uintptr_t)r.q | (uintptr_t)r.out | (uintptr_t)(r.q_stride * 2) | (uintptr_t)(r.out_stride * 2);
   const bool q8 = r.L.dtype == LSC_E4M3;
   if (!tensor_core_types(r) || (mis & 15) != 0) return kAny;
-  // the tensor-core kernels count packed rows, positions and the units' tiles in 31 bits
+  // the tensor-core kernels count packed rows and the units' tiles in 31 bits
   const int64_t rows = (int64_t)r.max_seq * r.group;
-  if (rows > INT32_MAX - 1024 || r.max_kv > INT32_MAX - 1024) return kAny;
+  if (rows > INT32_MAX - 1024) return kAny;
   Form form = kChunk;
   int64_t blocks = r.b.n_seq;  // row blocks of all sequences at most; the two forms for few rows have one a sequence
   if (rows <= kDecodeMost && r.box_decode > 0) {

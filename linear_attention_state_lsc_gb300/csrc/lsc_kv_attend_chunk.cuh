@@ -833,7 +833,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     const int32_t tk_q = L.by_block.div(TK), tk_r = TK - tk_q * L.block_tokens;
     int32_t q0 = 0, r0 = 0;
     auto start = [&]() {
-      blocks_held = L.by_block.div(pc.s.kv + L.block_tokens - 1);
+      blocks_held = pc.s.kv > 0 ? L.by_block.div(pc.s.kv - 1) + 1 : 0;  // block_tokens more could pass 31 bits
       q0 = L.by_block.div(pc.t0 * TK);
       r0 = pc.t0 * TK - q0 * L.block_tokens;
       if (window) {

@@ -187,6 +187,26 @@ def test_v_far_from_one(lsc, n, bt, D, power):
     check_attend(host, 1, b, qx, BF, D ** -0.5, True, out, ls)
 
 
+def test_lengths_at_the_end_of_31_bits_are_recorded(lsc):
+    """Positions are counted in 31 bits with room for a tile: a longer sequence is recorded and has no cached tokens, in
+    every form, though its table would hold it.  One block stands in all entries of the table."""
+    bt = 1 << 16
+    for pool, dtype, D, G, n in ((L.LSC_F32, L.LSC_F32, 8, 2, 1), (BF, BF, 64, 4, 1), (BF, BF, 64, 4, 40), (E4, BF, 64, 4, 12)):
+        host = HostKv(1, bt, 1, D, pool, pad=0, layers=1, fill=0)
+        for kv in (2 ** 31 - 1, 2 ** 31 - 1024):
+            with DevKv(host) as dev:
+                table = torch.zeros((1, 1 << 15), dtype=torch.int32, device="cuda")
+                cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+                lens = torch.tensor([kv], dtype=torch.int32, device="cuda")
+                q, out = (torch.full((n, G * D), 7.0, dtype=TORCH[dtype], device="cuda") for _ in "qo")
+                ls = torch.full((n, G), 7.0, device="cuda")
+                batch = L.kv_batch(1, n, table, cu, lens, max_blocks=1 << 15)
+                args = L.kv_attend_args(batch, G, q, out, dtype, 0.125, lse=ls)
+                assert L.lsc_kv_attend(dev.pool, 0, args, cur()) == L.LSC_OK
+                assert dev.status() == L.LSC_ERR_INVALID_ARG
+                assert (out == 0).all() and torch.isinf(ls).all()
+
+
 def test_a_pool_is_made_and_used_while_a_graph_is_captured(lsc):
     """A pool on a borrowed buffer, made and one destroyed on the thread that is capturing a stream (the default, strict
     mode), as before the pool had a status word."""
