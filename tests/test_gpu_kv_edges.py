@@ -329,3 +329,43 @@ def test_a_bound_above_the_step_s_tokens(lsc, pool, dtype, bt):
         need = [L.lsc_kv_attend_workspace_bytes(dev.pool, L.kv_attend_args(b.device(), 16, q, out, dtype, 0.1, max_seq_tokens=m))[1]
                 for m in (1, 16, 1 << 30)]
     assert need[0] == need[1] == need[2]  # the same rows a tile
+
+
+@pytest.mark.parametrize("lengths", [([1, 1, 1, 1], [1, 13, 300, 0]), ([2, 1], [900, 61]), ([70, 0, 130, 3], [70, 5, 400, 1]),
+                                     ([9, 30], [4, 700])], ids=["decode", "few", "chunk", "ahead"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bt", [12, 5, 1])
+@pytest.mark.parametrize("pool,dtype", [(BF, BF), (F16, F16), (E4, BF), (E4, F16)], ids=["bf16", "f16", "e4m3", "e4m3-f16"])
+def test_blocks_that_fit_no_box(lsc, pool, dtype, bt, D, lengths):
+    """Block sizes that are no multiple of 8 tokens: rows come one by one; below 8 the table is looked up directly."""
+    n, kv = lengths
+    rng = np.random.default_rng(bt * D + len(n))
+    blocks = int(sum(-(-k // bt) for k in kv)) + 3
+    b = Batch(rng, n, kv, bt, blocks, spare=2, wide=1)
+    host = filled(rng, b, blocks, bt, 2, D, pool)
+    q, qx = dense(2 * rng.standard_normal((b.T, 8, D)), dtype)
+    with DevKv(host) as dev:
+        for causal in (True, False):
+            out, ls = run_attend(dev, 1, b, q, dtype, 8, D ** -0.5, causal, max_seq_tokens=max(n))
+            check_attend(host, 1, b, qx, dtype, D ** -0.5, causal, out, ls)
+        assert dev.status() == L.LSC_OK
+        np.testing.assert_array_equal(dev.download(), host.bytes)
+
+
+@pytest.mark.parametrize("pool,D", [(BF, 64), (BF, 256), (E4, 64), (E4, 128)])
+@pytest.mark.parametrize("bt", [12, 5])
+@pytest.mark.parametrize("few", [False, True])
+def test_runs_that_begin_and_end_anywhere_without_boxes(lsc, pool, D, bt, few):
+    """Many short units beside long ones, cut between, inside and behind a unit's tiles."""
+    rng = np.random.default_rng(bt + D)
+    S = 31
+    n = rng.integers(0, 3 if few else 12, S)
+    kv = np.where(rng.random(S) < 0.3, rng.integers(1100, 2500, S), rng.integers(1, 300, S)) + n
+    blocks = int((-(-kv // bt)).sum())
+    b = Batch(rng, n, kv, bt, blocks, spare=1)
+    host = filled(rng, b, blocks, bt, 2, D, pool)
+    q, qx = dense(2 * rng.standard_normal((b.T, 16, D)), BF)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, BF, 16, D ** -0.5, True, max_seq_tokens=int(n.max()))
+        check_attend(host, 1, b, qx, BF, D ** -0.5, True, out, ls)
+        assert dev.status() == L.LSC_OK
