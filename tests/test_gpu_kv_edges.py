@@ -369,3 +369,20 @@ def test_runs_that_begin_and_end_anywhere_without_boxes(lsc, pool, D, bt, few):
         out, ls = run_attend(dev, 1, b, q, BF, 16, D ** -0.5, True, max_seq_tokens=int(n.max()))
         check_attend(host, 1, b, qx, BF, D ** -0.5, True, out, ls)
         assert dev.status() == L.LSC_OK
+
+
+@pytest.mark.parametrize("pool,dtype", [(BF, BF), (F16, F16), (E4, BF)], ids=["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("D,bt", [(256, 8), (256, 16), (256, 32), (256, 48), (256, 128), (64, 8), (64, 32), (64, 128), (64, 200),
+                                  (128, 8), (128, 48), (128, 128), (128, 256)])
+def test_every_shape_of_box(lsc, pool, dtype, D, bt):
+    """Boxes of 8 rows to a whole tile, of one 128-byte column and of all, for single tokens and for chunks."""
+    rng = np.random.default_rng(bt + D)
+    for n, kv in (([1, 2, 1], [1, 333, 700]), ([70, 3], [150, 530])):
+        blocks = int(sum(-(-k // bt) for k in kv)) + 2
+        b = Batch(rng, n, kv, bt, blocks, spare=1)
+        host = filled(rng, b, blocks, bt, 2, D, pool)
+        q, qx = dense(2 * rng.standard_normal((b.T, 8, D)), dtype)
+        with DevKv(host) as dev:
+            out, ls = run_attend(dev, 1, b, q, dtype, 8, D ** -0.5, True, max_seq_tokens=max(n))
+            check_attend(host, 1, b, qx, dtype, D ** -0.5, True, out, ls)
+            assert dev.status() == L.LSC_OK
