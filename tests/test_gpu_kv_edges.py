@@ -386,3 +386,59 @@ def test_every_shape_of_box(lsc, pool, dtype, D, bt):
             out, ls = run_attend(dev, 1, b, q, dtype, 8, D ** -0.5, True, max_seq_tokens=max(n))
             check_attend(host, 1, b, qx, dtype, D ** -0.5, True, out, ls)
             assert dev.status() == L.LSC_OK
+
+
+def together(H, row):
+    """Heads that the decode kernel reads side by side in a large batch: up to 1 KB of a position's row."""
+    return 4 if H % 4 == 0 and row <= 256 else 2 if H % 2 == 0 and row <= 512 else 1
+
+
+@pytest.mark.parametrize("n", [1, 2])
+@pytest.mark.parametrize("pool,dtype,H,G,D", [(BF, BF, 2, 2, 256), (BF, BF, 4, 5, 128), (BF, BF, 8, 1, 64), (BF, BF, 2, 8, 128),
+                                              (F16, F16, 2, 4, 128), (F16, F16, 4, 2, 64), (E4, BF, 8, 2, 128),
+                                              (E4, BF, 4, 4, 256), (E4, BF, 2, 4, 256), (E4, F16, 4, 3, 64), (E4, F16, 2, 7, 128)])
+def test_decode_batches_with_heads_side_by_side(lsc, pool, dtype, H, G, D, n):
+    """Batches large enough for it (the rule's condition is checked), whole and cut units, and V that is not finite in one
+    head of some sequences: neither the other heads nor the rows that do not see it change."""
+    rng = np.random.default_rng(H * D + n)
+    side = together(H, D * _kv.ES[pool])
+    assert side > 1
+    S, bt, most = 48, 32, 1700
+    kv = rng.integers(1, 300, S) + n
+    kv[[3, 17, 40]] = [most, 1100, 900]
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert S * (H // side) * most >= sms * 4 * 64
+    new = np.where(rng.random(S) < 0.2, 0, n)
+    new[[3, 17]] = n
+    blocks = int((-(-kv // bt)).sum())
+    b = Batch(rng, new, kv, bt, blocks, spare=1)
+    host = filled(rng, b, blocks, bt, H, D, pool)
+    sick = H - 1
+    for i in (3, 17):  # the last token's v, seen by its own row alone
+        bl, r = b.places(i, kv[i] - 1, kv[i])
+        x = host.read(1, 1, bl, r)
+        x[0, sick, 5], x[0, sick, 9], x[0, sick, 12] = np.inf, -np.inf, np.nan
+        fill(host, 1, 1, bl, r, x)
+    q, qx = dense(2 * rng.standard_normal((b.T, H * G, D)), dtype)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, dtype, H * G, D ** -0.5, True, max_seq_tokens=n, max_kv_tokens=most)
+        again, _ = run_attend(dev, 1, b, q, dtype, H * G, D ** -0.5, True, max_seq_tokens=n, max_kv_tokens=most)
+        assert dev.status() == L.LSC_OK
+    assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
+    got = out.view(b.T, H * G, D)
+    heads = slice(sick * G, (sick + 1) * G)
+    for i in (3, 17):
+        t, (bl, r) = int(b.cu[i + 1]) - 1, b.places(i, kv[i] - 1, kv[i])
+        if pool == E4:  # a row that held one is NaN throughout
+            assert torch.isnan(got[t, heads]).all()
+        else:
+            assert (got[t, heads, 5] == np.inf).all() and (got[t, heads, 9] == -np.inf).all()
+            assert torch.isnan(got[t, heads, 12]).all()
+            keep = np.delete(np.arange(D), [5, 9, 12])
+            assert torch.isfinite(got[t, heads][:, keep]).all()
+        x = np.nan_to_num(host.read(1, 1, bl, r), nan=0, posinf=0, neginf=0)
+        fill(host, 1, 1, bl, r, x)
+        want = _kv.attend(host, 1, b, qx, D ** -0.5, True)[0][t, heads]
+        cols = np.arange(D) if pool == E4 else np.array([5, 9, 12])
+        got[t, heads][:, cols] = torch.from_numpy(want[:, cols]).to(got)
+    check_attend(host, 1, b, qx, dtype, D ** -0.5, True, out, ls)
