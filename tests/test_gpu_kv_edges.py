@@ -442,3 +442,38 @@ def test_decode_batches_with_heads_side_by_side(lsc, pool, dtype, H, G, D, n):
         cols = np.arange(D) if pool == E4 else np.array([5, 9, 12])
         got[t, heads][:, cols] = torch.from_numpy(want[:, cols]).to(got)
     check_attend(host, 1, b, qx, dtype, D ** -0.5, True, out, ls)
+
+
+def test_waits_that_run_out_in_every_form(lsc):
+    """As the test of the chunk kernel's waits: a decode batch with cut units, E4M3 chunks, and blocks without boxes give
+    up, report it and return; the same call without the fault is right."""
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import test_gpu_kv_edges as E
+for case in E.EXPIRING:
+    E.expiring_call(*case, expired=True)
+print("reported")
+"""
+    r = subprocess.run([sys.executable, "-c", code % (os.path.dirname(HERE), HERE)], capture_output=True, text=True,
+                       env=dict(os.environ, LSC_FAULT="timeout0"), timeout=300)
+    assert "reported" in r.stdout, r.stderr[-2000:]
+    for case in EXPIRING:
+        expiring_call(*case, expired=False)
+
+
+EXPIRING = [(BF, 64, 1, 64), (BF, 256, 1, 64), (E4, 128, 1, 64), (E4, 64, 70, 64), (E4, 128, 70, 64), (E4, 256, 70, 64),
+            (BF, 128, 70, 12), (E4, 256, 70, 12)]
+
+
+def expiring_call(pool, D, n, bt, expired):
+    rng = np.random.default_rng(D + n)
+    b = Batch(rng, [n] * 3, [300, 2600, n], bt, 300)
+    host = filled(rng, b, 300, bt, 2, D, pool)
+    q, qx = dense(rng.standard_normal((b.T, 8, D)), BF)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, BF, 8, 0.1, True, max_seq_tokens=n)
+        assert dev.status() == (L.LSC_ERR_DEV_TIMEOUT if expired else L.LSC_OK)
+        np.testing.assert_array_equal(dev.download(), host.bytes)
+    if not expired:
+        check_attend(host, 1, b, qx, BF, 0.1, True, out, ls)
