@@ -477,3 +477,25 @@ def expiring_call(pool, D, n, bt, expired):
         np.testing.assert_array_equal(dev.download(), host.bytes)
     if not expired:
         check_attend(host, 1, b, qx, BF, 0.1, True, out, ls)
+
+
+@pytest.mark.parametrize("shape", [(2, 24, 16, 2, 64, 48), (3, 20, 5, 3, 7, 16), (1, 12, 64, 8, 128, 512), (2, 9, 7, 1, 33, 0)],
+                         ids=str)
+def test_copy_prefix_moves_the_scale_bytes(lsc, shape):
+    """E4M3 pools: the codes and the scale bytes of rows [0, n) and nothing else of the destination pages."""
+    layers, blocks, bt, H, D, pad = shape
+    rng = np.random.default_rng(D)
+    host = HostKv(blocks, bt, H, D, E4, pad=pad, layers=layers)
+    host.bytes[:] = rng.integers(0, 256, host.bytes.shape, dtype=np.uint8)
+    perm = rng.permutation(blocks)
+    dst, src = perm[:6], rng.choice(perm[6:], 6)
+    count = np.array([0, 1, bt, bt - 1, max(1, bt // 2), bt])
+    with DevKv(host) as dev:
+        rc, moved = L.lsc_copy_prefix(dev.pool, L.kv_ops(src, dst, count), cur())
+        assert rc == L.LSC_OK
+        got = dev.download()
+    assert moved == int(count.sum()) * (H * D + H) * 2 * layers
+    for s, d, n in zip(src, dst, count):
+        for at, w in ((0, n * H * D), (host.scale_off, n * H)):
+            host.bytes[:, :, d, at:at + w] = host.bytes[:, :, s, at:at + w]
+    np.testing.assert_array_equal(got, host.bytes)
