@@ -89,8 +89,11 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
 // out with weights smaller by the difference; their error is 2^-93 (half an e5m2
 // step, 2^-17, times 448 over a sum of 2^(9 + 76)).  At the other end the heaviest
 // position adds 2^(7 - e) at least, and what is below 2^-126 is lost: positions
-// lighter than 2^(e - 133) of it.
-__device__ __forceinline__ float v_exponent(uint32_t byte) { return byte < 51 ? -76.f : (float)((int)byte - 127); }
+// lighter than 2^(e - 133) of it.  A row of NaN (255) counts as 1: the sum, and lse,
+// do not depend on what v holds.
+__device__ __forceinline__ float v_exponent(uint32_t byte) {
+  return byte < 51 ? -76.f : byte == 255 ? 0.f : (float)((int)byte - 127);
+}
 
 // The scale byte of a row whose largest magnitude has these fp32 bits (as an
 // unsigned number, so NaN counts as the largest): the smallest power of two

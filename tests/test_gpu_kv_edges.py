@@ -187,6 +187,36 @@ def test_v_far_from_one(lsc, n, bt, D, power):
     check_attend(host, 1, b, qx, BF, D ** -0.5, True, out, ls)
 
 
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("n,bt", [(40, 64), (2, 64), (2, 12), (12, 64)], ids=["chunk", "decode", "rows", "rows-48"])
+def test_the_sum_does_not_depend_on_a_v_row_of_nan(lsc, n, bt, D):
+    """E4M3 pools: out is NaN where a row's scale byte says so, lse is what the scores give; scores from -80 to 80 (powers
+    of two), the NaN row's among the smallest."""
+    rng = np.random.default_rng(D + n)
+    b = Batch(rng, [n] * 2, [200, 1400], bt, 160)
+    host = HostKv(160, bt, 1, D, E4)
+    for i in range(2):
+        bl, r = b.places(i, 0, int(b.kv[i]))
+        k, v = np.zeros((2, len(r), 1, D))
+        k[:, 0, 0] = rng.integers(-10, 11, len(r))
+        k[60, 0, 0] = -10
+        v[:] = 1
+        v[60, 0, 3] = np.nan
+        fill(host, 1, 0, bl, r, k)
+        fill(host, 1, 1, bl, r, v)
+    x = np.zeros((b.T, 4, D))
+    x[:, :, 0] = 8
+    q, qx = dense(x, BF)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, BF, 4, np.log(2), True, max_seq_tokens=n)
+        assert dev.status() == L.LSC_OK
+    assert torch.isnan(out).all()
+    with np.errstate(invalid="ignore"):
+        want = _kv.attend(host, 1, b, qx, float(np.float32(np.log(2))), True)[1]
+    # scores up to 56 and sums of up to 1400 terms in 32 bits
+    assert (np.abs(ls.double().cpu().numpy() - want) <= 56 * 2.0 ** -20 + 1408 * 2.0 ** -23).all()
+
+
 def test_lengths_at_the_end_of_31_bits_are_recorded(lsc):
     """Positions are counted in 31 bits with room for a tile: a longer sequence is recorded and has no cached tokens, in
     every form, though its table would hold it.  One block stands in all entries of the table."""
