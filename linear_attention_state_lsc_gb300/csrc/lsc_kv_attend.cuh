@@ -25,6 +25,7 @@
 // on in the next.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -242,9 +243,46 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Byte of 16-byte chunk ch of row r in a swizzled tile of `rows` rows: columns of LINE bytes, chunks xor the row's low bits
+// (lines of 64 bytes: pairs of rows share 128).
+template <int LINE>
+__device__ __forceinline__ uint32_t chunk_at(int rows, int r, int ch) {
+  if constexpr (LINE == 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+  else return (ch >> 3) * (rows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+}
+
+// Tiled TMA load of one box of a layer's rows (this CTA's shared memory), completing on `bar`.
+__device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int row, int col, int head, int block,
+                                        uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+      "[%7];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(0), "r"(row), "r"(col), "r"(head), "r"(block), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A bounded wait.  The first tries do without the clock: reading %globaltimer costs about a microsecond, several
+// tiles' worth of waits.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t phase, uint64_t limit) {
+  if (limit == 0) return false;
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, phase & 1)) return true;
+  return mbar_wait_bounded(bar, phase & 1, limit);
+}
+// The same with one answer for the whole (converged) warp, so that a wait that gave up never splits it.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, uint64_t limit) {
+  return __all_sync(0xffffffffu, wait_bar(bar, phase, limit));
+}
+
 }  // namespace kv
 
-// ---- launches (lsc_kv_attend_rows_*.cu, lsc_kv_attend_chunk.cu, lsc_kv_attend_join.cu) ----
+// ---- plans and launches (lsc_kv_attend_join.cu; a type's kernels in lsc_kv_attend_{decode,rows,chunk}_*.cu) ----
 struct AttendPlan {
   int32_t ctas;    // runs
   int32_t M;       // rows of a unit, `together` heads' worth

@@ -150,19 +150,6 @@ LSC_MMA(mma16, "f16")
 LSC_MMA(mma8, "f8f6f4")
 #undef LSC_MMA
 
-// Byte of 16-byte chunk ch of row r in a swizzled tile of `rows` rows.
-template <int LINE>
-__device__ __forceinline__ uint32_t chunk_at(int rows, int r, int ch) {
-  if constexpr (LINE == 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
-  else return (ch >> 3) * (rows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two fp32 values as the operand of the packed instructions, which do two lanes' worth a cycle.
 __device__ __forceinline__ uint64_t two(float x, float y) {
   return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
@@ -287,29 +274,6 @@ __device__ __forceinline__ void weights8(const uint32_t (&s)[32], const float *v
     q[2][y] = __byte_perm(t2[0], t2[1], 0x7531);
   }
   l = add2(l, add2(sum[0], sum[1]));
-}
-
-// Tiled TMA load of one box (this CTA's shared memory), completing on `bar`.
-__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
-                                            uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-      "[%7];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// A bounded wait.  The first tries do without the clock: reading %globaltimer costs about a microsecond, several
-// tiles' worth of waits.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t phase, uint64_t limit) {
-  if (limit == 0) return false;
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try_wait(bar, phase & 1)) return true;
-  return mbar_wait_bounded(bar, phase & 1, limit);
-}
-// The same with one answer for the whole (converged) warp, so that a wait that gave up never splits it.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, uint64_t limit) {
-  return __all_sync(0xffffffffu, wait_bar(bar, phase, limit));
 }
 
 // A walk over the ring's slots of K (from 0) or V (from 1).  Counting modulo a number that is no power of two, or
@@ -918,8 +882,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           if (ln == 0) mbar_arrive_expect_tx(&sm.full[at.slot], C::slot);
           __syncwarp();
           if (ln < boxes)
-            tma_load_5d(dst + bc * (TK * 128) + br * C::line, &map, 0, rr, bc, pc.head, blk + (is_k ? 0 : L.num_blocks),
-                        &sm.full[at.slot]);
+            tma_box(dst + bc * (TK * 128) + br * C::line, &map, rr, bc, pc.head, blk + (is_k ? 0 : L.num_blocks),
+                    &sm.full[at.slot]);
           flying = flying & ~(0x101u << at.slot) | (1u | at.phase << 8) << at.slot;
         } else {
           int64_t row_at[TK / 32];

@@ -73,45 +73,11 @@ struct Smem {
   RunScratch run;
 };
 
-// Byte of 16-byte chunk c of row r in a swizzled sub-tile of KEYS rows: columns of 128 bytes, chunks xor the row's low
-// bits (rows of 64 bytes: pairs of rows share 128).
-template <int RB, int KEYS>
-__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-  if constexpr (RB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  else return (c >> 3) * (KEYS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
-
-__device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int row, int col, int head, int block,
-                                        uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-      "[%7];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(0), "r"(row), "r"(col), "r"(head), "r"(block), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // An 8 x 8 matrix of 16-bit values over the lanes (row g, columns 2 tq, 2 tq + 1), transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// The first tries do without the clock (reading %globaltimer is slow); one answer for the whole warp.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, uint64_t limit) {
-  bool ok = limit != 0;
-  if (ok) {
-    ok = false;
-    for (int i = 0; i < 16 && !ok; ++i) ok = mbar_try_wait(bar, phase & 1);
-    if (!ok) ok = mbar_wait_bounded(bar, phase & 1, limit);
-  }
-  return __all_sync(0xffffffffu, ok);
 }
 
 template <bool BF16, int ES, int D, int NR>
@@ -120,7 +86,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
   using C = Conf<ES, D>;
   constexpr bool Q8 = ES == 1;
   constexpr int M = 8 * NR;         // rows of a head, NR tiles of 8
-  constexpr int KEYS = C::KEYS, ST = C::ST, RB = C::RB;
+  constexpr int KEYS = C::KEYS, ST = C::ST, RB = C::RB, LINE = RB < 128 ? RB : 128;
   constexpr int KS = D / 16;        // k steps of a score, output tiles of 16 columns
   constexpr int NK = KEYS / 16;     // score tiles of 16 positions
   constexpr float lift = BF16 ? 0.f : 7.f;  // powers of two that the reference lies below the maximum that set it
@@ -280,12 +246,12 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
       if (first + KEYS > hi || first + KEYS > sure) {  // (some of) V's rows need a look before they meet a weight of 0
         const int past = hi - first < KEYS ? hi - first : KEYS, from = sure > first ? sure - first : 0;
         for (int x = past * (RB / 16) + ln; x < KEYS * (RB / 16); x += 32)
-          *(uint4 *)(vs + chunk_at<RB, KEYS>(x / (RB / 16), x % (RB / 16))) = make_uint4(0, 0, 0, 0);
+          *(uint4 *)(vs + chunk_at<LINE>(KEYS, x / (RB / 16), x % (RB / 16))) = make_uint4(0, 0, 0, 0);
         if constexpr (Q8) {
           bool nan = false;
           if (ln >= from && ln < past)
             for (int c = 0; c < RB / 16; ++c) {
-              uint32_t *v = (uint32_t *)(vs + chunk_at<RB, KEYS>(ln, c));
+              uint32_t *v = (uint32_t *)(vs + chunk_at<LINE>(KEYS, ln, c));
               for (int y = 0; y < 4; ++y)
                 for (int z = 0; z < 32; z += 8)
                   if ((v[y] >> z & 0x7f) == 0x7f) nan = true, v[y] &= ~(0xffu << z);
@@ -295,7 +261,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
           constexpr uint32_t E = BF16 ? 0x7f80 : 0x7c00;
           for (int x = from * D + ln; x < past * D; x += 32) {
             const int key = x / D, d = x % D;
-            uint16_t *v = (uint16_t *)(vs + chunk_at<RB, KEYS>(key, d >> 3) + (d & 7) * 2);
+            uint16_t *v = (uint16_t *)(vs + chunk_at<LINE>(KEYS, key, d >> 3) + (d & 7) * 2);
             const uint32_t u = *v;
             if ((u & E) != E) continue;
             atomicMin(&sm.bad[wh][(u & (E ^ 0x7fff)) ? 0 : (u & 0x8000) ? 2 : 1][d], first + key);
@@ -322,15 +288,15 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
           uint32_t x[2][4];
           if constexpr (Q8) {  // a chunk is a k step
             uint32_t b[4];
-            ldsm4(b, ka + chunk_at<RB, KEYS>(16 * n + (ln & 15), k + (ln >> 4)));
+            ldsm4(b, ka + chunk_at<LINE>(KEYS, 16 * n + (ln & 15), k + (ln >> 4)));
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               x[y][0] = e4m3x2_to_f16x2(b[2 * y] & 0xffffu), x[y][1] = e4m3x2_to_f16x2(b[2 * y + 1] & 0xffffu);
               x[y][2] = e4m3x2_to_f16x2(b[2 * y] >> 16), x[y][3] = e4m3x2_to_f16x2(b[2 * y + 1] >> 16);
             }
           } else {
-            ldsm4(x[0], ka + chunk_at<RB, KEYS>(16 * n + (ln & 15), 2 * k + (ln >> 4)));
-            ldsm4(x[1], ka + chunk_at<RB, KEYS>(16 * n + (ln & 15), 2 * k + 2 + (ln >> 4)));
+            ldsm4(x[0], ka + chunk_at<LINE>(KEYS, 16 * n + (ln & 15), 2 * k + (ln >> 4)));
+            ldsm4(x[1], ka + chunk_at<LINE>(KEYS, 16 * n + (ln & 15), 2 * k + 2 + (ln >> 4)));
           }
 #pragma unroll
           for (int h = 0; h < NR; ++h) {
@@ -411,7 +377,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
       for (int c = 0; c < KS; ++c) {  // 16 columns
         if constexpr (Q8) {  // a chunk of 32 positions; m index g: column 2 g, m index g + 8: column 2 g + 1
           uint32_t b[4];
-          ldsm4t(b, va + chunk_at<RB, KEYS>(ln, c));
+          ldsm4t(b, va + chunk_at<LINE>(KEYS, ln, c));
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const uint32_t x[4] = {e4m3x2_to_f16x2(__byte_perm(b[2 * n], 0, 0x20) & 0xffffu),
@@ -425,7 +391,7 @@ decode_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_cons
 #pragma unroll
           for (int n = 0; n < NK; ++n) {
             uint32_t x[4];
-            ldsm4t(x, va + chunk_at<RB, KEYS>(16 * n + ((ln >> 4) << 3) + (ln & 7), 2 * c + ((ln >> 3) & 1)));
+            ldsm4t(x, va + chunk_at<LINE>(KEYS, 16 * n + ((ln >> 4) << 3) + (ln & 7), 2 * c + ((ln >> 3) & 1)));
 #pragma unroll
             for (int h = 0; h < NR; ++h) mma<BF16>(o[h][c], x, a[n][h][0], a[n][h][1]);
           }
