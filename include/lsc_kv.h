@@ -171,7 +171,8 @@ typedef struct {
  * element rounded to nearest even, beyond the largest value to infinity) or E4M3
  * (quantised as described at the top; the row's scale byte is written with it).
  * Nothing else of the pool changes.  When two tokens of a call share a row of a
- * block, which one stays is unspecified.  Errors: INVALID_ARG (NULL, negative
+ * block, what it holds then is unspecified: heads, elements and (E4M3) scale bytes
+ * of either, in any mixture.  Errors: INVALID_ARG (NULL, negative
  * or zero sizes, reserved != 0, dtype, a stride below kv_heads * head_dim),
  * OUT_OF_RANGE (layer), MISALIGNED (an array not aligned to its element),
  * CUDA, WRONG_DEVICE.
@@ -206,8 +207,10 @@ typedef struct {
   int32_t causal;         /* 1: a token sees positions up to its own; 0: all kv_lens[i] positions */
   int64_t q_stride;       /* elements from a token to the next; 0 = num_q_heads * head_dim */
   int64_t out_stride;
-  int32_t max_seq_tokens; /* bound of every n_i that the host knows; 0 = total_tokens */
-  int32_t max_kv_tokens;  /* bound of every kv_lens[i] that the host knows; 0 = max_blocks * block_tokens */
+  int32_t max_seq_tokens; /* bound of every n_i that the host knows; 0 = total_tokens.  It picks the kernel: give a
+                             decode step its 1 (or its few speculated tokens), or a prefill kernel serves it */
+  int32_t max_kv_tokens;  /* bound of every kv_lens[i] that the host knows; 0 = max_blocks * block_tokens.  It says
+                             how far work is cut and how large the workspace is */
   void *workspace;        /* device scratch of workspace_bytes, what
                              lsc_kv_attend_workspace_bytes says or more, 16-byte aligned, untouched by
                              others until the call's work on the stream completes; NULL = the
@@ -229,10 +232,13 @@ typedef struct {
  * meet v: to bf16 in bf16 pools; to f16 in f16 and E4M3 pools, in full down to
  * 2^-21 of a row's largest weight and to a multiple of 2^-31 of it below (E4M3
  * pools, more than 64 rows of q a kv head: to nine significant bits or more down
- * to 2^-17 of it, to a multiple of 2^-25 of it below; in E4M3 pools a weight is one
- * times the scale of its row of v).  E4M3 rows of v with a scale below 2^-76 add an
+ * to 2^-17 of it, to a multiple of 2^-25 of it below, and elements of q below 2^-9
+ * of their row's largest are off by up to 2^-18 of it; in E4M3 pools a weight is
+ * one times the scale of its row of v).  E4M3 rows of v with a scale below 2^-76 add an
  * absolute error of up to 2^-93 a position; beside rows with a scale of 2^e above
- * 2^100, positions lighter than 2^(e - 133) of the heaviest drop out of the sums.  Two calls with the same inputs give the same bits.
+ * 2^100, positions lighter than 2^(e - 133) of the heaviest drop out of the sums,
+ * and rows of k with such a scale may overflow their scores.
+ * Two calls with the same inputs give the same bits.
  * A sequence that exceeds max_kv_tokens is recorded as INVALID_ARG in the status
  * word and taken to have no cached tokens; one that exceeds max_seq_tokens is
  * recorded too, and its rows of out and lse stay as they are.  If a bounded device
