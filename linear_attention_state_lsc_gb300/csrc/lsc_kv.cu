@@ -270,7 +270,10 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
 // kernel when a sequence may have more, the CUDA cores for what none of them
 // takes.  64 sequences of 8 tokens behind 64 to 16384, 64 packed rows: bf16, few-row
 // kernel 398 us, chunk kernel 193; of 3 tokens, 24 rows: 382 and 189; one sequence
-// of 4 behind 1000: 23 and 25; E4M3, 128 sequences of 8 tokens, 32 rows: 1121 and 1131.
+// of 4 behind 1000: 23 and 25.  bf16, 128 sequences of 8 tokens behind 500 to 8000, 8
+// heads, 32 rows: head_dim 64, 829 and 386, head_dim 128, 1068 and 436; 4 such
+// sequences of 5: 46 and 34, 56 and 38; one of 8 behind 1000: 22 and 24, 23 and 27.
+// E4M3, 128 sequences of 8 tokens, head_dim 128: 1115 and 1131.
 constexpr int32_t kDecodeMost = 16, kRowsMost = 64;
 constexpr int64_t kMostCounts = 1 << 30;
 enum Form { kAny, kDecode, kRows, kChunk };

@@ -53,9 +53,11 @@
 // is computed (head_dim 128, 4096 tokens behind 28000: 1361 -> 1320 us).
 //
 // Measured, calls back to back (bf16 products 1923 TFLOP/s): head_dim 128, 4096
-// tokens behind 28000, 32 q heads: 1487 us, 1356 TFLOP/s (1312 us with pauses, when
-// the power limit is not met); head_dim 256, mixed as above: 819 us, 1138 TFLOP/s
-// (687 with pauses); E4M3, 8 chunks behind up to 16384: 1024 us, 968 TFLOP/s.
+// tokens behind 28000, 32 q heads: 1482 us, 1361 TFLOP/s (1300 us with pauses, when
+// the power limit is not met; head_dim 64: 1168 us with pauses, 863 TFLOP/s, where
+// the softmax has twice the work a product); head_dim 256, mixed as above: 832 us,
+// 1120 TFLOP/s (687 with pauses; 2160 over blocks of 12, whose rows are copied one by
+// one); E4M3, 8 chunks behind up to 16384: 1039 us, 954 TFLOP/s (996 with pauses).
 //
 // Positions that only some rows of a unit see may hold infinities and NaN: see
 // lsc_kv_attend_rows.cuh; here the softmax threads search such a tile's v.
