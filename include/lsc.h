@@ -61,8 +61,9 @@ extern "C" {
 
 /* ---- enums -------------------------------------------------------------- */
 typedef enum { LSC_LAYER_ATTENTION = 0, LSC_LAYER_GDN = 1 } lsc_layer_kind;
-/* F16: copies and the K/V pool (lsc_kv.h); E4M3 (8-bit float, 3 mantissa bits): K/V pools only */
-typedef enum { LSC_F32 = 0, LSC_BF16 = 1, LSC_F16 = 2, LSC_E4M3 = 3 } lsc_dtype;
+/* F16: copies and the K/V pool (lsc_kv.h); E4M3 (8-bit float, 3 mantissa bits) and E2M1 (4-bit float, 1 mantissa bit):
+ * K/V pools only */
+typedef enum { LSC_F32 = 0, LSC_BF16 = 1, LSC_F16 = 2, LSC_E4M3 = 3, LSC_E2M1 = 4 } lsc_dtype;
 
 /* Content fingerprint of a prefix; opaque to the library, 0 = "not requested".
  * [XN] §6, §6.1. */

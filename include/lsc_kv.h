@@ -4,7 +4,8 @@
  * reused prefix's K/V rows into another sequence's blocks; and the calls of a
  * step over one layer's blocks: append (write the new tokens' K/V rows,
  * quantised when the pool holds e4m3), gather (read rows back dense) and
- * attend (softmax attention of the new tokens over the cached ones).
+ * attend (softmax attention of the new tokens over the cached ones).  Pools hold
+ * K and V at 32, 16, 8 (e4m3) or 4 bits (e2m1) an element.
  *
  * Sources, cited by page title and section:
  *   [VA] "非连续 KV Cache" (vLLM-Ascend design document) §3 (block stride =
@@ -31,6 +32,23 @@
  * rounded once, to nearest even.  A power of two keeps the product exact, so the
  * only error is that one rounding (half a step: 2^-4 of the element, or 2^-10
  * times the scale below 2^-6 times it).
+ *
+ * E2M1 pools hold 4 bits per element and one scale byte per 16 elements of a (token
+ * row, kv head); head_dim is a multiple of 16.  The payload is block_tokens rows of
+ * kv_heads x head_dim codes, two a byte with the lower nibble first, then, at byte
+ * round_up(codes, 16) of the page, [block_tokens, kv_heads, head_dim / 16] scale
+ * bytes.  A code is a sign (bit 3) and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6; a scale
+ * byte b is the value of the f16 whose bits are b << 7 (5 exponent bits, 3 mantissa
+ * bits, no sign: multiples of 2^-17 below 2^-14), and an element is code * scale,
+ * which f16 and bf16 hold exactly.  A written group takes the smallest scale, 10240
+ * (byte 226) at most, with 6 * scale at least its largest magnitude, and each element
+ * is rounded once to the nearest code times that scale, ties to the even code.  An
+ * element is off by 3/16 of its group's largest magnitude at most (half the step from
+ * 4 to 6, times a scale that is up to an eighth larger than that magnitude needs) or,
+ * where the scale is below 2^-14, by the scale.  Magnitudes above 61440 become 61440.
+ * A group of zeros has byte 0 and codes of 0 whatever the zeros' signs.  Byte 255 marks a group that held a NaN or an infinity (codes of
+ * 0); its 16 elements read back as NaN.  What bytes 227 to 254, which append does not
+ * write, read back as is unspecified.
  *
  * Conventions are those of lsc.h (return codes, host/device pointers, streams,
  * no host sync except create/destroy).
@@ -64,11 +82,11 @@ typedef struct {
   void *k;                 /* device: block 0 of the K lane */
   void *v;                 /* device: block 0 of the V lane */
   int64_t shape[4];        /* num_blocks, block_tokens, kv_heads, head_dim */
-  int64_t strides[4];      /* page_bytes / es, kv_heads * head_dim, head_dim, 1 */
+  int64_t strides[4];      /* page_bytes / es, kv_heads * head_dim, head_dim, 1 (E2M1: es is half a byte) */
   int64_t lane_stride;     /* v - k: num_blocks * page_bytes / es (dim 0 of the merged view) */
   int64_t page_bytes, payload_bytes, row_bytes;
   int32_t dtype;
-  int32_t scale_offset;    /* E4M3: byte of a page where its scale bytes begin; 0 for other types */
+  int32_t scale_offset;    /* E4M3, E2M1: byte of a page where its scale bytes begin; 0 for other types */
 } lsc_kv_layer_view;
 
 /* One block of a prefix copy: token rows [0, n_tokens) of src_block go to
@@ -82,7 +100,8 @@ typedef struct {
 
 /* Bytes a pool with this description needs: num_layers * 2 * num_blocks *
  * page_bytes.  Errors: INVALID_ARG, LAYOUT (page smaller than the payload or
- * not a multiple of the element size, or an E4M3 block of 2 GiB or more), MISALIGNED (page not a multiple of 16). */
+ * not a multiple of the element size, an E4M3 or E2M1 block of 2 GiB or more, or an
+ * E2M1 head_dim that is no multiple of 16), MISALIGNED (page not a multiple of 16). */
 int lsc_kv_pool_required_bytes(const lsc_kv_pool_desc *desc, size_t *total_bytes);
 
 /* Create a K/V pool; device_base == NULL allocates (cudaMalloc, owned),
@@ -103,7 +122,7 @@ int lsc_kv_pool_status(lsc_kv_pool *pool, void *stream, int32_t *host_status);
 /*
  * copy_prefix ([KP] figure 2): for every op with n_tokens > 0, token rows
  * [0, n_tokens) of src_block are copied to dst_block in the K and V lanes of
- * every attention layer (with their scale bytes in an E4M3 pool); nothing else
+ * every attention layer (with their scale bytes in an E4M3 or E2M1 pool); nothing else
  * changes (rows past n_tokens, padding, source blocks, other blocks).  A prefix of T tokens is passed block by block:
  * its full blocks with n_tokens = block_tokens, then the partial last one.
  * One persistent launch per 2560 ops, 16-byte vector copies, on `stream`;
@@ -168,16 +187,87 @@ typedef struct {
 /*
  * Write the new tokens' K and V rows into layer `layer`'s blocks, in one launch.
  * The pool's type is the dense type (bit-exact), another float type (each
- * element rounded to nearest even, beyond the largest value to infinity) or E4M3
- * (quantised as described at the top; the row's scale byte is written with it).
+ * element rounded to nearest even, beyond the largest value to infinity), E4M3 or
+ * E2M1 (quantised as described at the top; the row's scale bytes are written with it).
  * Nothing else of the pool changes.  When two tokens of a call share a row of a
- * block, what it holds then is unspecified: heads, elements and (E4M3) scale bytes
+ * block, what it holds then is unspecified: heads, elements and (E4M3, E2M1) scale bytes
  * of either, in any mixture.  Errors: INVALID_ARG (NULL, negative
  * or zero sizes, reserved != 0, dtype, a stride below kv_heads * head_dim),
  * OUT_OF_RANGE (layer), MISALIGNED (an array not aligned to its element),
  * CUDA, WRONG_DEVICE.
  */
 int lsc_kv_append(lsc_kv_pool *pool, int32_t layer, const lsc_kv_append_args *args, void *stream);
+
+/* ---- rotary positions ----------------------------------------------------------- */
+
+#define LSC_ROTARY_MAX_AXES 8
+
+/*
+ * How rows of a head are turned by their tokens' positions.  The leading rotary_dim
+ * elements form rotary_dim / 2 pairs, (i, i + rotary_dim / 2) or, interleaved,
+ * (2 i, 2 i + 1); pair i of token t is turned by the angle
+ *   a = positions[pair_axis[i]][t] * inv_freq[i]:
+ *   (x, y) -> scale * (x cos a - y sin a, x sin a + y cos a).
+ * The elements behind rotary_dim stay as they are.  Several axes (time, height and
+ * width of an image or video token) are given to the pairs in any pattern; text takes
+ * the same position on each.  Angles are exact to 2^-31 turns or so at every position
+ * of 32 bits, negative ones too, and cosines and sines to 2^-22; elements are turned in
+ * 32 bits and rounded once.  With negated frequencies the turn is undone (and a
+ * gradient of what came out becomes that of what went in).
+ */
+typedef struct {
+  int32_t rotary_dim;        /* even, 2 .. head_dim, at most 512 */
+  int32_t axes;              /* 1 .. LSC_ROTARY_MAX_AXES */
+  int32_t interleaved;       /* 0 or 1 */
+  float scale;               /* of cosines and sines; 1 for plain rotary positions; finite */
+  const double *inv_freq;    /* host [rotary_dim / 2], radians a position, -65536 .. 65536; read during the call */
+  const uint8_t *pair_axis;  /* host [rotary_dim / 2], below axes; read during the call; NULL: axis 0 for all */
+  const int32_t *positions;  /* device [axes, total_tokens] */
+  int64_t axis_stride;       /* elements from an axis to the next; 0 = total_tokens */
+} lsc_rotary;
+
+typedef struct {
+  int32_t total_tokens;
+  int32_t num_heads;
+  int32_t head_dim;
+  int32_t dtype;      /* F32, BF16 or F16 */
+  const void *x;      /* device [total_tokens, num_heads, head_dim] */
+  void *out;          /* device, same shape: x itself (with the same stride), or overlaps no input */
+  int64_t x_stride;   /* elements from a token to the next; 0 = num_heads * head_dim */
+  int64_t out_stride;
+  lsc_rotary rotary;
+} lsc_rotate_args;
+
+/*
+ * Turn dense rows, every token's, in one launch on the current device.  q's and k's
+ * heads that lie side by side in a projection are one call.  Errors: INVALID_ARG
+ * (NULL, negative sizes, a stride below num_heads * head_dim, out == x with another
+ * stride, a field of rotary outside what it says, dtype), MISALIGNED (an array not
+ * aligned to its element), UNSUPPORTED (more than 2^24 heads), CUDA.
+ */
+int lsc_rotate(const lsc_rotate_args *args, void *stream);
+
+typedef struct {
+  lsc_kv_append_args append;
+  lsc_rotary rotary;
+  int32_t num_q_heads;    /* 0: k alone is turned */
+  int32_t reserved;       /* must be 0 */
+  const void *q;          /* device [total_tokens, num_q_heads, head_dim] at append.dtype */
+  void *q_out;            /* device, same shape: q itself (with the same stride), or overlaps no input */
+  int64_t q_stride;       /* elements from a token to the next; 0 = num_q_heads * head_dim */
+  int64_t q_out_stride;
+} lsc_kv_append_rotated_args;
+
+/*
+ * lsc_kv_append with k's rows turned on their way into the pool (rounded to its type
+ * once, from 32 bits; E4M3 and E2M1: quantised from them), and the step's q rows
+ * turned dense to dense in the same launch, ready for lsc_kv_attend.  positions has
+ * total_tokens entries an axis; those of rows behind the last sequence are not read,
+ * and these rows of q_out stay as they were.  A token without a row in the cache has
+ * its q turned all the same.  The positions need not be the cache's (a token's
+ * position in its image, say).  Errors as lsc_kv_append and lsc_rotate.
+ */
+int lsc_kv_append_rotated(lsc_kv_pool *pool, int32_t layer, const lsc_kv_append_rotated_args *args, void *stream);
 
 typedef struct {
   lsc_kv_batch batch;
@@ -192,7 +282,7 @@ typedef struct {
 /*
  * The inverse: the rows that the batch's tokens sit in, dense, in one launch.
  * With n_i = kv_lens[i] it reads back whole sequences.  Elements are the pool's
- * values (E4M3: code times scale) rounded once to dtype.  Errors as lsc_kv_append.
+ * values (E4M3, E2M1: code times scale) rounded once to dtype.  Errors as lsc_kv_append.
  */
 int lsc_kv_gather(lsc_kv_pool *pool, int32_t layer, const lsc_kv_gather_args *args, void *stream);
 

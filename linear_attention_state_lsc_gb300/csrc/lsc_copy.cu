@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) kv_copy_kernel(const __grid_constant
     const int64_t len = span - off < p.chunk_bytes ? span - off : p.chunk_bytes;
     uint8_t *lane_base = p.base + (int64_t)l * p.region_bytes + (int64_t)lane * p.lane_bytes;
     copy_span(lane_base + (int64_t)op.y * p.page + off, lane_base + (int64_t)op.x * p.page + off, len);
-    if (p.scale_row != 0 && c == 0)  // E4M3: the rows' scale bytes, one span behind the codes
+    if (p.scale_row != 0 && c == 0)  // E4M3, E2M1: the rows' scale bytes, one span behind the codes
       copy_span(lane_base + (int64_t)op.y * p.page + p.scale_off, lane_base + (int64_t)op.x * p.page + p.scale_off,
                 (int64_t)op.z * p.scale_row);
   }

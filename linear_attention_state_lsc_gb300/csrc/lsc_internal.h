@@ -236,8 +236,8 @@ struct KvPlan {
   int64_t lane_bytes;    // num_blocks pages
   int64_t page, row_bytes, chunk_bytes;
   int32_t num_layers, n_ops, chunks_per_op;
-  int32_t scale_off;       // E4M3: page offset of the scale bytes, else 0
-  int32_t scale_row;       // E4M3: scale bytes of a token row (kv heads)
+  int32_t scale_off;       // E4M3, E2M1: page offset of the scale bytes, else 0
+  int32_t scale_row;       // E4M3, E2M1: scale bytes of a token row
   int3 op[kKvPlanMaxOps];  // (src block, dst block, n_tokens > 0)
 };
 cudaError_t launch_kv_copy(const KvPlan &p, int num_sms, cudaStream_t stream);
@@ -259,8 +259,8 @@ struct FastDiv {
 };
 
 // Positions of a decode sub-tile: 8 to 16 KB of K and V rows.
-__host__ __device__ constexpr int kv_decode_keys(int head_dim, int element) {
-  return element == 2 && head_dim >= 128 ? 16 : 32;
+__host__ __device__ constexpr int kv_decode_keys(int head_dim, int bits) {
+  return bits == 16 && head_dim >= 128 ? 16 : 32;
 }
 
 // One attention layer of a K/V pool.
@@ -269,7 +269,7 @@ struct KvLayer {
   int64_t page;         // bytes from a block to the next
   int32_t num_blocks, block_tokens, heads, head_dim;
   int32_t dtype;        // lsc_dtype
-  int32_t scale_off;    // E4M3: page offset of the scale bytes
+  int32_t scale_off;    // E4M3, E2M1: page offset of the scale bytes
   int32_t *status;      // device error word
   FastDiv by_block;     // by block_tokens
 };
@@ -290,6 +290,29 @@ struct KvRowsParams {
 };
 cudaError_t launch_kv_append(const KvRowsParams &p, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_gather(const KvRowsParams &p, int num_sms, cudaStream_t stream);
+
+// Rotary positions: a pair's angle is positions[axis * axis_stride + t] * turns 2^-64 whole turns.
+constexpr int kRotaryPairs = 256;
+struct Rotary {
+  const int32_t *positions;
+  int64_t axis_stride;
+  float scale;                   // of cosines and sines
+  int32_t half, interleaved;     // pairs of a head; 1: neighbours are pairs
+  uint64_t turns[kRotaryPairs];
+  uint8_t axis[kRotaryPairs];
+};
+struct KvRotaryParams {
+  KvLayer L;            // L.k null: rows of x alone
+  KvBatch b;            // then total_tokens alone
+  const void *x;        // dense rows that are turned dense to dense (a step's q)
+  void *out;
+  const void *k, *v;
+  int64_t x_stride, out_stride, k_stride, v_stride;
+  int32_t dtype, heads, head_dim;  // heads: of x
+  Rotary r;
+  FastDiv by_half;
+};
+cudaError_t launch_kv_rotary(const KvRotaryParams &p, int num_sms, cudaStream_t stream);
 
 struct KvAttendParams {
   KvLayer L;

@@ -26,8 +26,9 @@ struct lsc_kv_pool {
   int num_sms = 0;
   uint8_t *base = nullptr;
   bool owns_base = false;
-  int64_t es = 0, row_bytes = 0, payload = 0, lane_bytes = 0, region_bytes = 0;
-  int32_t scale_off = 0;        // E4M3: page offset of the scale bytes
+  int64_t bits = 0, row_bytes = 0, payload = 0, lane_bytes = 0, region_bytes = 0;
+  int32_t scale_off = 0;        // E4M3, E2M1: page offset of the scale bytes
+  int32_t scale_row = 0;        // and scale bytes of a token row
   int32_t *status = nullptr;    // device error word
   int32_t box_rows = 0;         // rows of a TMA box of `maps`
   int32_t box_decode = 0;       // and of `maps_decode`
@@ -46,6 +47,8 @@ int esize(int32_t dtype) {
   }
 }
 
+int bits_of(int32_t dtype) { return dtype == LSC_E2M1 ? 4 : 8 * esize(dtype); }
+
 // Bound of every device-side wait (mbarrier), in nanoseconds.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
@@ -62,19 +65,24 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
   if (!d || d->num_layers <= 0 || d->num_blocks <= 0 || d->block_tokens <= 0 || d->num_kv_heads <= 0 ||
       d->head_dim <= 0)
     return LSC_ERR_INVALID_ARG;
-  const int es = esize(d->dtype);
-  if (!es) return LSC_ERR_INVALID_ARG;
+  const int bits = bits_of(d->dtype);
+  if (!bits) return LSC_ERR_INVALID_ARG;
+  if (d->dtype == LSC_E2M1 && d->head_dim % 16 != 0) return LSC_ERR_LAYOUT;
   g->d = *d;
-  g->es = es;
-  g->row_bytes = (int64_t)d->num_kv_heads * d->head_dim * es;
+  g->bits = bits;
+  const int64_t elements = (int64_t)d->num_kv_heads * d->head_dim;
+  g->row_bytes = bits == 4 ? elements / 2 : elements * (bits / 8);
   g->payload = g->row_bytes * d->block_tokens;
-  if (d->dtype == LSC_E4M3) {  // codes, then one scale byte per (row, head) at the next 16 B boundary
+  if (bits <= 8) {  // codes, then one scale byte per (row, head), or per 16 elements of it, at the next 16 B boundary
     const int64_t off = (g->payload + 15) / 16 * 16;
     if (off > INT32_MAX) return LSC_ERR_LAYOUT;
     g->scale_off = (int32_t)off;
-    g->payload = off + (int64_t)d->block_tokens * d->num_kv_heads;
+    const int64_t scales = bits == 8 ? d->num_kv_heads : elements / 16;
+    if (bits == 4 && scales > (INT32_MAX - off) / d->block_tokens) return LSC_ERR_LAYOUT;
+    g->scale_row = (int32_t)scales;
+    g->payload = off + scales * d->block_tokens;
   }
-  if (d->page_bytes < g->payload || d->page_bytes % es) return LSC_ERR_LAYOUT;
+  if (d->page_bytes < g->payload || (bits > 8 && d->page_bytes % (bits / 8))) return LSC_ERR_LAYOUT;
   if (d->page_bytes % 16) return LSC_ERR_MISALIGNED;
   g->lane_bytes = (int64_t)d->num_blocks * d->page_bytes;
   g->region_bytes = 2 * g->lane_bytes;
@@ -93,15 +101,16 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
 
 bool encode_maps(const lsc_kv_pool *p, EncodeTiled encode, int tile, int box, std::vector<CUtensorMap> *out) {
   const lsc_kv_pool_desc &d = p->d;
-  const int row = d.head_dim * (int)p->es, col = row < 128 ? row : 128;  // bytes
-  const CUtensorMapDataType type = d.dtype == LSC_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+  const int row = d.head_dim * (int)p->bits / 8, col = row < 128 ? row : 128;  // bytes
+  const int es = p->bits == 16 ? 2 : 1;  // of the map's elements
+  const CUtensorMapDataType type = es == 1               ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : d.dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUtensorMapSwizzle swizzle = col == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  const cuuint64_t dims[5] = {(cuuint64_t)(col / p->es), (cuuint64_t)d.block_tokens, (cuuint64_t)(row / col),
+  const cuuint64_t dims[5] = {(cuuint64_t)(col / es), (cuuint64_t)d.block_tokens, (cuuint64_t)(row / col),
                               (cuuint64_t)d.num_kv_heads, 2 * (cuuint64_t)d.num_blocks};
   const cuuint64_t strides[4] = {(cuuint64_t)p->row_bytes, (cuuint64_t)col, (cuuint64_t)row, (cuuint64_t)d.page_bytes};
-  const cuuint32_t boxes[5] = {(cuuint32_t)(col / p->es), (cuuint32_t)box, box == tile ? (cuuint32_t)(row / col) : 1, 1, 1};
+  const cuuint32_t boxes[5] = {(cuuint32_t)(col / es), (cuuint32_t)box, box == tile ? (cuuint32_t)(row / col) : 1, 1, 1};
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   try {
     out->resize(d.num_layers);
@@ -119,7 +128,7 @@ bool encode_maps(const lsc_kv_pool *p, EncodeTiled encode, int tile, int box, st
 void make_maps(lsc_kv_pool *p) {
   const lsc_kv_pool_desc &d = p->d;
   const int D = d.head_dim, most = d.block_tokens & -d.block_tokens;
-  if (d.dtype == LSC_F32 || (D != 64 && D != 128 && D != 256) || most < 8) return;  // a swizzle pattern is 8 rows
+  if (d.dtype == LSC_F32 || d.dtype == LSC_E2M1 || (D != 64 && D != 128 && D != 256) || most < 8) return;  // a swizzle pattern is 8 rows
   void *fn = nullptr;
   cudaDriverEntryPointQueryResult found;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
@@ -127,7 +136,7 @@ void make_maps(lsc_kv_pool *p) {
     cudaGetLastError();
     return;
   }
-  const int tile = D == 256 ? 64 : 128, keys = lsc::kv_decode_keys(D, (int)p->es);
+  const int tile = D == 256 ? 64 : 128, keys = lsc::kv_decode_keys(D, (int)p->bits);
   const int box = std::min(most, tile), box_decode = std::min(most, keys);
   std::vector<CUtensorMap> maps, decode;
   if (!encode_maps(p, (EncodeTiled)fn, tile, box, &maps) ||
@@ -220,6 +229,61 @@ int check_rows(const lsc_kv_pool *p, int32_t layer, const lsc_kv_batch &b, const
   r->dtype = dtype;
   r->by_heads.set((uint32_t)p->d.num_kv_heads);
   return check_device(p);
+}
+
+// 2^64 times the fraction of a turn in an angle of f radians, rounded: f / (2 pi) as a sum of two doubles (the product
+// with 1 / (2 pi), itself two doubles, and what its rounding left).
+uint64_t turns_of(double f) {
+  constexpr double kInv2Pi = 0x1.45f306dc9c883p-3, kInv2PiLow = -0x1.6b01ec5417056p-57;
+  if (f < 0) return 0 - turns_of(-f);
+  const double hi = f * kInv2Pi, lo = std::fma(f, kInv2Pi, -hi) + f * kInv2PiLow;  // |lo| < 2^-38: see kMostFreq
+  return (uint64_t)std::ldexp(hi - std::floor(hi), 64) + (uint64_t)(int64_t)std::ldexp(lo, 64);
+}
+constexpr double kMostFreq = 65536.0;
+
+// head_dim, and whether any rows are to be turned; out receives the launch parameters.
+int check_rotary(const lsc_rotary &a, int32_t head_dim, int32_t total_tokens, bool any, lsc::KvRotaryParams *r) {
+  const int32_t half = a.rotary_dim / 2;
+  if (a.rotary_dim <= 0 || a.rotary_dim % 2 != 0 || a.rotary_dim > head_dim || half > lsc::kRotaryPairs)
+    return LSC_ERR_INVALID_ARG;
+  if (a.axes <= 0 || a.axes > LSC_ROTARY_MAX_AXES || (a.interleaved != 0 && a.interleaved != 1) ||
+      !std::isfinite(a.scale) || !a.inv_freq || (a.axis_stride != 0 && a.axis_stride < total_tokens) ||
+      (any && !a.positions))
+    return LSC_ERR_INVALID_ARG;
+  if ((uintptr_t)a.positions % 4 != 0) return LSC_ERR_MISALIGNED;
+  for (int32_t i = 0; i < half; ++i) {
+    if (!(std::fabs(a.inv_freq[i]) <= kMostFreq) || (a.pair_axis && a.pair_axis[i] >= a.axes)) return LSC_ERR_INVALID_ARG;
+    r->r.turns[i] = turns_of(a.inv_freq[i]);
+    r->r.axis[i] = a.pair_axis ? a.pair_axis[i] : 0;
+  }
+  r->r.positions = a.positions;
+  r->r.axis_stride = a.axis_stride ? a.axis_stride : total_tokens;
+  r->r.scale = a.scale;
+  r->r.half = half;
+  r->r.interleaved = a.interleaved;
+  r->by_half.set((uint32_t)half);
+  return LSC_OK;
+}
+
+// Rows of a token that one call of the rotary kernel takes at most.
+constexpr int64_t kRotaryHeads = 1 << 24;
+
+// The dense rows that are turned dense to dense.
+int check_turned(const void *x, const void *out, int32_t heads, int32_t head_dim, int32_t dtype, int64_t x_stride,
+                 int64_t out_stride, bool any, lsc::KvRotaryParams *r) {
+  const int64_t row = (int64_t)heads * head_dim;
+  if ((x_stride != 0 && x_stride < row) || (out_stride != 0 && out_stride < row)) return LSC_ERR_INVALID_ARG;
+  r->x_stride = x_stride ? x_stride : row;
+  r->out_stride = out_stride ? out_stride : row;
+  if (any && (!x || !out)) return LSC_ERR_INVALID_ARG;
+  if (x == out && r->x_stride != r->out_stride) return LSC_ERR_INVALID_ARG;
+  if (misaligned(x, esize(dtype)) || misaligned(out, esize(dtype))) return LSC_ERR_MISALIGNED;
+  r->x = x;
+  r->out = const_cast<void *>(out);
+  r->heads = heads;
+  r->head_dim = head_dim;
+  r->dtype = dtype;
+  return LSC_OK;
 }
 
 // attend's arguments; out receives the launch parameters without the workspace.
@@ -434,11 +498,11 @@ int lsc_kv_pool_layer_view(const lsc_kv_pool *p, int32_t layer, lsc_kv_layer_vie
   v->shape[1] = p->d.block_tokens;
   v->shape[2] = p->d.num_kv_heads;
   v->shape[3] = p->d.head_dim;
-  v->strides[0] = p->d.page_bytes / p->es;
+  v->strides[0] = p->d.page_bytes * 8 / p->bits;
   v->strides[1] = (int64_t)p->d.num_kv_heads * p->d.head_dim;
   v->strides[2] = p->d.head_dim;
   v->strides[3] = 1;
-  v->lane_stride = p->lane_bytes / p->es;
+  v->lane_stride = p->lane_bytes * 8 / p->bits;
   v->page_bytes = p->d.page_bytes;
   v->payload_bytes = p->payload;
   v->row_bytes = p->row_bytes;
@@ -466,7 +530,6 @@ int lsc_copy_prefix(lsc_kv_pool *p, const lsc_kv_copy_op *ops, int32_t n_ops, vo
   lsc::TraceRange trace_("lsc_copy_prefix");
   if (!p || n_ops < 0 || (n_ops > 0 && !ops)) return LSC_ERR_INVALID_ARG;
   const int32_t B = p->d.num_blocks;
-  const int32_t scale_row = p->d.dtype == LSC_E4M3 ? p->d.num_kv_heads : 0;
   // validate every copying op before enqueueing anything
   std::vector<int32_t> dst_owner;
   try {
@@ -483,7 +546,7 @@ int lsc_copy_prefix(lsc_kv_pool *p, const lsc_kv_copy_op *ops, int32_t n_ops, vo
     if (o.src_block < 0 || o.src_block >= B || o.dst_block < 0 || o.dst_block >= B) return LSC_ERR_OUT_OF_RANGE;
     if (dst_owner[o.dst_block] >= 0) return LSC_ERR_DUP_DST;
     dst_owner[o.dst_block] = r;
-    bytes += (int64_t)o.n_tokens * (p->row_bytes + scale_row) * 2 * p->d.num_layers;
+    bytes += (int64_t)o.n_tokens * (p->row_bytes + p->scale_row) * 2 * p->d.num_layers;
     ++n_copy;
     last_copy = r;
   }
@@ -503,7 +566,7 @@ int lsc_copy_prefix(lsc_kv_pool *p, const lsc_kv_copy_op *ops, int32_t n_ops, vo
     plan.num_layers = p->d.num_layers;
     plan.chunks_per_op = (int32_t)((p->row_bytes * p->d.block_tokens + plan.chunk_bytes - 1) / plan.chunk_bytes);
     plan.scale_off = p->scale_off;
-    plan.scale_row = scale_row;
+    plan.scale_row = p->scale_row;
     plan.n_ops = 0;
     for (int32_t r = 0; r < n_ops; ++r) {
       if (ops[r].n_tokens == 0) continue;
@@ -533,6 +596,62 @@ int lsc_kv_append(lsc_kv_pool *p, int32_t layer, const lsc_kv_append_args *a, vo
   if (rc != LSC_OK) return rc;
   if (r.b.n_seq == 0 || r.b.total_tokens == 0) return LSC_OK;
   if (lsc::launch_kv_append(r, p->num_sms, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return LSC_ERR_CUDA;
+  }
+  return LSC_OK;
+}
+
+int lsc_kv_append_rotated(lsc_kv_pool *p, int32_t layer, const lsc_kv_append_rotated_args *a, void *stream) {
+  lsc::TraceRange trace_("lsc_kv_append_rotated");
+  if (!p || !a) return LSC_ERR_INVALID_ARG;
+  const lsc_kv_append_args &k = a->append;
+  lsc::KvRowsParams rows{};
+  lsc::KvRotaryParams r{};
+  int rc = check_rows(p, layer, k.batch, k.k, k.v, k.dtype, k.reserved, k.k_stride, k.v_stride, &rows);
+  if (rc != LSC_OK && rc != LSC_ERR_CUDA && rc != LSC_ERR_WRONG_DEVICE) return rc;
+  const int device_rc = rc;  // after the arguments
+  const bool any = k.batch.n_seq > 0 && k.batch.total_tokens > 0;
+  if (a->num_q_heads < 0 || a->reserved != 0) return LSC_ERR_INVALID_ARG;
+  rc = check_turned(a->q, a->q_out, a->num_q_heads, p->d.head_dim, k.dtype, a->q_stride, a->q_out_stride,
+                    any && a->num_q_heads > 0, &r);
+  if (rc == LSC_OK) rc = check_rotary(a->rotary, p->d.head_dim, k.batch.total_tokens, any, &r);
+  if (rc != LSC_OK) return rc;
+  if ((int64_t)a->num_q_heads + 2 * (int64_t)p->d.num_kv_heads > kRotaryHeads) return LSC_ERR_UNSUPPORTED;
+  if (device_rc != LSC_OK) return device_rc;
+  if (!any) return LSC_OK;
+  r.L = rows.L;
+  r.b = rows.b;
+  r.k = rows.k;
+  r.v = rows.v;
+  r.k_stride = rows.k_stride;
+  r.v_stride = rows.v_stride;
+  if (lsc::launch_kv_rotary(r, p->num_sms, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return LSC_ERR_CUDA;
+  }
+  return LSC_OK;
+}
+
+int lsc_rotate(const lsc_rotate_args *a, void *stream) {
+  lsc::TraceRange trace_("lsc_rotate");
+  if (!a || a->total_tokens < 0 || a->num_heads <= 0 || a->head_dim <= 0) return LSC_ERR_INVALID_ARG;
+  if (a->dtype != LSC_F32 && a->dtype != LSC_BF16 && a->dtype != LSC_F16) return LSC_ERR_INVALID_ARG;
+  lsc::KvRotaryParams r{};
+  const bool any = a->total_tokens > 0;
+  int rc = check_turned(a->x, a->out, a->num_heads, a->head_dim, a->dtype, a->x_stride, a->out_stride, any, &r);
+  if (rc == LSC_OK) rc = check_rotary(a->rotary, a->head_dim, a->total_tokens, any, &r);
+  if (rc != LSC_OK) return rc;
+  if (a->num_heads > kRotaryHeads) return LSC_ERR_UNSUPPORTED;
+  int device = -1, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+    cudaGetLastError();
+    return LSC_ERR_CUDA;
+  }
+  if (!any) return LSC_OK;
+  r.b.total_tokens = a->total_tokens;
+  if (lsc::launch_kv_rotary(r, sms, (cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
     return LSC_ERR_CUDA;
   }

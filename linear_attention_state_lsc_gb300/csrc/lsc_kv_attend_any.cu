@@ -33,6 +33,10 @@ __device__ __forceinline__ float load_el(const void *p, int64_t i, int dtype) {
     default: return e4m3x2_to_float2(((const uint8_t *)p)[i]).x;
   }
 }
+// Element i of a pool block; E4M3 without its scale.
+__device__ __forceinline__ float load_row(const KvLayer &L, const uint8_t *page, int64_t i) {
+  return L.dtype == LSC_E2M1 ? e2m1_element(page, L.scale_off, i) : load_el(page, i, L.dtype);
+}
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(const __grid_co
 #pragma unroll
             for (int e = 0; e < NE; ++e)
               if (ln + 32 * e < D)
-                sc[c] += q[e] * load_el(page, ((int64_t)row * L.heads + kh) * D + ln + 32 * e, L.dtype);
+                sc[c] += q[e] * load_row(L, page, ((int64_t)row * L.heads + kh) * D + ln + 32 * e);
             if (L.dtype == LSC_E4M3) {
               const int64_t so = L.scale_off + (int64_t)row * L.heads + kh;
               sc[c] *= scale_of(page[so]);
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(kWarps * 32) attend_any_kernel(const __grid_co
 #pragma unroll
         for (int e = 0; e < NE; ++e)
           if (ln + 32 * e < D)
-            o[e] += w * vs[c] * load_el(L.v + at[c], ((int64_t)row * L.heads + kh) * D + ln + 32 * e, L.dtype);
+            o[e] += w * vs[c] * load_row(L, L.v + at[c], ((int64_t)row * L.heads + kh) * D + ln + 32 * e);
       }
     }
     __syncthreads();  // the last row's parts have been read

@@ -55,7 +55,7 @@ constexpr int kThreads = 32 * kWarps;
 template <int ES, int D>
 struct Conf {
   static constexpr int RB = D * ES;                    // bytes of a row
-  static constexpr int KEYS = kv_decode_keys(D, ES);   // positions of a sub-tile
+  static constexpr int KEYS = kv_decode_keys(D, 8 * ES);   // positions of a sub-tile
   static constexpr int half = KEYS * RB;               // bytes of its K or V rows
   static constexpr int ST = half >= 4096 ? 3 : 6;      // sub-tiles in flight per warp
   static constexpr int occ = half >= 8192 ? 1 : 2;     // CTAs per SM: 192 KB of rings

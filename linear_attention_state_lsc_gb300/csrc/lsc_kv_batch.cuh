@@ -1,5 +1,5 @@
 // lsc_kv_batch.cuh -- device helpers shared by the K/V step kernels: reading the
-// batch description (include/lsc_kv.h, lsc_kv_batch) and the E4M3 row format.
+// batch description (include/lsc_kv.h, lsc_kv_batch) and the E4M3 and E2M1 row formats.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -128,6 +128,90 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
   const uint32_t h = e4m3x2_to_f16x2(two);
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// ---- E2M1 rows: groups of 16 elements ------------------------------------------
+constexpr uint32_t kE2M1Top = 226;  // scale byte of 10240: six times it is the largest magnitude that f16 holds
+
+// The group's scale byte for its largest magnitude, as fp32 bits (NaN counts as the
+// largest): the smallest scale s with 6 s >= top.  top / 6 is off by a rounding or
+// two, so the scale just below it is looked at: 6 s has 6 bits, the comparison is exact.
+__device__ __forceinline__ uint32_t e2m1_scale_byte(uint32_t top_bits) {
+  if (top_bits >= 0x7f800000u) return 255;
+  const float top = __uint_as_float(top_bits);
+  uint32_t b = __half_as_ushort(__float2half_rz(top * (1.f / 6.f))) >> 7;
+  b = b < kE2M1Top ? b : kE2M1Top;
+  return b + (b < kE2M1Top && 6.f * __half2float(__ushort_as_half((uint16_t)(b << 7))) < top ? 1 : 0);
+}
+
+// Two magnitudes over their scale -> codes (lo in the low nibble), to nearest even, 6 at most.
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// What an element x over its scale s is rounded from, r = 1 / s.  x r is off by less than 2^-22 of itself; rounded to 20
+// bits, a quotient that is a tie (three bits) becomes that tie again.  Elements of 16-bit types have 11 bits and scales
+// 4: a quotient that is no tie is 2^-12 or more away from each, so that is enough.  With 32 bits (FULL) a quotient may
+// be nearer to a tie than that: then the sign of x - tie s, exact in one fma, moves it to the right side.
+template <bool FULL>
+__device__ __forceinline__ float e2m1_quotient(float x, float s, float r) {
+  const float a = fabsf(x);
+  uint32_t t = (__float_as_uint(a * r) + 4) & ~7u;
+  if constexpr (FULL) {
+    const float d = __fmaf_rn(-__uint_as_float(t), s, a);
+    t += (d > 0.f ? 1 : 0) - (d < 0.f ? 1 : 0);
+  }
+  return __uint_as_float(t | (__float_as_uint(x) & 0x80000000u));
+}
+
+// 16 elements with their scale byte -> 64 bits of codes.
+template <bool FULL>
+__device__ __forceinline__ uint2 to_e2m1x16(const float (&x)[16], uint32_t byte) {
+  if (byte == 0 || byte == 255) return make_uint2(0, 0);
+  const float s = __half2float(__ushort_as_half((uint16_t)(byte << 7))), r = __frcp_rn(s);
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = to_e2m1x2(e2m1_quotient<FULL>(x[8 * h + 2 * i], s, r), e2m1_quotient<FULL>(x[8 * h + 2 * i + 1], s, r));
+    w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Eight codes -> four pairs of halves, exactly.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// A scale byte as both halves of a pair.
+__device__ __forceinline__ __half2 e2m1_scale2(uint32_t byte) {
+  const uint32_t x = (byte | byte << 16) << 7;
+  return *reinterpret_cast<const __half2 *>(&x);
+}
+
+// Eight codes times their scale as four pairs of halves: 6 bits at most, exact.
+__device__ __forceinline__ void e2m1x8_times(uint32_t w, __half2 scale, uint32_t (&h)[4]) {
+  e2m1x8_to_f16(w, h);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h[i]), scale);
+    h[i] = *reinterpret_cast<const uint32_t *>(&y);
+  }
+}
+
+// Element i of a block (its rows' elements in order), in 32 bits.
+__device__ __forceinline__ float e2m1_element(const uint8_t *page, int32_t scale_off, int64_t i) {
+  uint32_t h[4];
+  e2m1x8_times((uint32_t)page[i >> 1] >> (4 * (i & 1)), e2m1_scale2(page[scale_off + (i >> 4)]), h);
+  return __low2float(*reinterpret_cast<const __half2 *>(&h[0]));
 }
 
 }  // namespace kv

@@ -20,6 +20,7 @@
 
 #include "lsc_internal.h"
 #include "lsc_kv_batch.cuh"
+#include "lsc_kv_rows.cuh"
 #include "lsc_ptx.h"
 
 namespace lsc {
@@ -27,8 +28,8 @@ namespace {
 
 using namespace kv;
 
-constexpr int kThreads = 256;
-constexpr int kMaxTok = 16;  // tokens of a CTA's run
+using namespace kv::row;
+
 constexpr int kStagedHeads = 64;
 // Rows in flight per lane group, and CTAs per SM.  Append computes (the quantisation) and wants few address steps,
 // gather waits for memory and wants threads: from E4M3, 24 contexts, 8 heads of 128: 4 rows and 4 CTAs 224 us, 2 and 6
@@ -37,159 +38,6 @@ template <bool APPEND, int NV>
 constexpr int kUnroll = (APPEND ? 4 : 2) / (APPEND ? NV : 1);
 template <bool APPEND, int NV>
 constexpr int kOcc = APPEND ? 4 : NV == 1 ? 8 : 6;
-
-struct E4M3 {};
-
-// Where the tokens [t0, t0 + n) sit: page[i] = byte offset of the token's block
-// in a lane, row[i] its row there; row -1: no row in the cache, -2: the token
-// belongs to no sequence.
-struct Places {
-  int64_t page[kMaxTok];
-  int32_t row[kMaxTok];
-  int32_t cu[kThreads];
-};
-
-__device__ __forceinline__ void find_places(const KvLayer &L, const KvBatch &b, int32_t t0, int n, Places &s) {
-  // samples of cu_seqlens, a step of `step` apart: one load per thread
-  const int step = b.n_seq / kThreads + 1;
-  {
-    const int64_t i = (int64_t)threadIdx.x * step;
-    s.cu[threadIdx.x] = b.cu[i < b.n_seq ? i : b.n_seq];
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < n) {
-    const int32_t t = t0 + threadIdx.x;
-    int lo = -1, hi = kThreads;  // the last sample <= t
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (s.cu[m] <= t) lo = m;
-      else hi = m;
-    }
-    int32_t row = -2;
-    int64_t page = 0;
-    if (lo >= 0) {
-      int64_t a = (int64_t)lo * step, z = a + step;  // the last entry <= t is in [a, z)
-      if (a > b.n_seq) a = b.n_seq;
-      if (z > (int64_t)b.n_seq + 1) z = (int64_t)b.n_seq + 1;
-      while (z - a > 1) {
-        const int64_t m = (a + z) >> 1;
-        if (b.cu[m] <= t) a = m;
-        else z = m;
-      }
-      if (a < b.n_seq) {
-        const int32_t c0 = b.cu[a], c1 = b.cu[a + 1];
-        row = -1;
-        if (c0 <= t && t < c1) {
-          const int32_t kv = checked_kv(L, b, b.kv[a]);
-          const int64_t pos = (int64_t)kv - ((int64_t)c1 - c0) + (t - c0);
-          if (pos >= 0) {
-            const int32_t q = L.by_block.div((int32_t)pos);
-            const int32_t blk = b.table[a * b.max_blocks + q];
-            if (blk >= 0 && blk < L.num_blocks) {
-              row = (int32_t)pos - q * L.block_tokens;
-              page = (int64_t)blk * L.page;
-            } else {
-              report(L.status, LSC_ERR_OUT_OF_RANGE);
-            }
-          }
-        }
-      }
-    }
-    s.row[threadIdx.x] = row;
-    s.page[threadIdx.x] = page;
-  }
-  __syncthreads();
-}
-
-// ---- eight elements of a row ---------------------------------------------------
-template <typename T>
-struct Eight;  // raw vector of 8 elements, and its floats
-template <>
-struct Eight<float> {
-  uint4 a, b;
-  __device__ void load(const void *p) { a = __ldcs((const uint4 *)p), b = __ldcs((const uint4 *)p + 1); }
-  __device__ void store(void *p) const { ((uint4 *)p)[0] = a, ((uint4 *)p)[1] = b; }
-  __device__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
-  __device__ void get(float (&x)[8]) const {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
-  }
-  // the largest magnitude as a whole number that orders like it (NaN above infinity), and that as fp32 bits
-  __device__ uint32_t top() const {
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
-    return m;
-  }
-  static __device__ uint32_t bits(uint32_t m) { return m; }
-  __device__ void put(const float (&x)[8]) {
-    a = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-    b = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
-  }
-};
-template <typename H2>
-struct Eight16 {
-  uint4 a;
-  __device__ void load(const void *p) { a = __ldcs((const uint4 *)p); }
-  __device__ void store(void *p) const { *(uint4 *)p = a; }
-  __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
-  static __device__ float2 two(uint32_t w);
-  __device__ uint32_t top() const {  // two magnitudes a word
-    const uint32_t k = 0x7fff7fffu, m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
-    return max(m & 0xffffu, m >> 16);
-  }
-  static __device__ uint32_t bits(uint32_t m) { return __float_as_uint(two(m).x); }
-  static __device__ uint32_t pack(float x, float y);
-  __device__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = two(w[i]);
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
-  }
-  __device__ void put(const float (&x)[8]) {
-    a = make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
-  }
-};
-template <>
-__device__ __forceinline__ float2 Eight16<__nv_bfloat162>::two(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-template <>
-__device__ __forceinline__ uint32_t Eight16<__nv_bfloat162>::pack(float x, float y) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-template <>
-__device__ __forceinline__ float2 Eight16<__half2>::two(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-template <>
-__device__ __forceinline__ uint32_t Eight16<__half2>::pack(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-template <>
-struct Eight<__nv_bfloat16> : Eight16<__nv_bfloat162> {};
-template <>
-struct Eight<__half> : Eight16<__half2> {};
-
-template <typename T>
-constexpr int kSize = (int)sizeof(T);
-template <>
-constexpr int kSize<E4M3> = 1;
-
-template <typename A, typename B>
-struct Same {
-  static constexpr bool value = false;
-};
-template <typename A>
-struct Same<A, A> {
-  static constexpr bool value = true;
-};
 
 // ---- vector kernel: head_dim a multiple of 8 and at most 256 --------------------
 // APPEND: dense -> pool; else pool -> dense.  A lane has NV vectors of 8 elements,
@@ -210,7 +58,8 @@ __global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(cons
   const int groups = kThreads / lanes, g = threadIdx.x / lanes, sub = threadIdx.x & (lanes - 1);
   const bool on = sub * EV < L.head_dim;
   const int rows = n * 2 * L.heads;
-  const int64_t head_bytes = (int64_t)L.head_dim * kSize<P>;
+  const int64_t head_bytes = held<P>(L.head_dim);
+  const int scales = L.head_dim / 16;  // E2M1: of a head's row
   // Row r of the run is head r % heads of lane (r / heads) % 2 (K, V) of token r / (2 heads); a group's rows are `groups`
   // apart, so its walk steps by a whole number of tokens and a rest.
   const int per = 2 * L.heads, step_i = groups / per, step_w = groups - step_i * per;
@@ -271,8 +120,11 @@ __global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(cons
 #pragma unroll
         for (int v = 0; v < NV; ++v) x[u][v].zero();
         if (row[u] == -1 || !on) continue;
-        const uint8_t *src = page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes + sub * EV * kSize<P>;
-        if constexpr (Same<P, E4M3>::value) {
+        const uint8_t *src = page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes + held<P>(sub * EV);
+        if constexpr (Same<P, E2M1>::value) {
+          code[u][0] = __ldcs((const uint2 *)src);
+          byte[u] = __ldcs(page[u] + L.scale_off + ((int64_t)row[u] * L.heads + head[u]) * scales + sub);
+        } else if constexpr (Same<P, E4M3>::value) {
           if constexpr (NV == 2) {
             const uint4 c = __ldcs((const uint4 *)src);
             code[u][0] = make_uint2(c.x, c.y), code[u][1] = make_uint2(c.z, c.w);
@@ -295,8 +147,19 @@ __global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(cons
     for (int u = 0; u < kUnroll; ++u) {
       if constexpr (APPEND) {
         uint8_t *dst = row[u] < 0 ? nullptr : page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes +
-                                                  sub * EV * kSize<P>;
-        if constexpr (Same<P, E4M3>::value) {
+                                                  held<P>(sub * EV);
+        if constexpr (Same<P, E2M1>::value) {  // a lane has a group
+          const uint32_t sb = e2m1_scale_byte(x[u][0].bits(max(x[u][0].top(), x[u][1].top())));
+          if (dst && on) {
+            float lo[8], hi[8], f[16];
+            x[u][0].get(lo);
+            x[u][1].get(hi);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = lo[e], f[8 + e] = hi[e];
+            *(uint2 *)dst = to_e2m1x16<Same<D, float>::value>(f, sb);
+            page[u][L.scale_off + ((int64_t)row[u] * L.heads + head[u]) * scales + sub] = (uint8_t)sb;
+          }
+        } else if constexpr (Same<P, E4M3>::value) {
           uint32_t m = x[u][0].top();
           if constexpr (NV == 2) m = max(m, x[u][1].top());
           if (lanes == 32) m = __reduce_max_sync(0xffffffffu, m);
@@ -334,6 +197,13 @@ __global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(cons
         }
       } else {
         if (row[u] == -2 || !on) continue;
+        if constexpr (Same<P, E2M1>::value) {
+          if (row[u] >= 0) {
+            const __half2 k = e2m1_scale2(byte[u]);
+            e2m1_to<D>(code[u][0].x, k, x[u][0]);
+            e2m1_to<D>(code[u][0].y, k, x[u][1]);
+          }
+        }
         if constexpr (Same<P, E4M3>::value) {
           if (row[u] >= 0) {
             const float k = scale_of(byte[u]);
@@ -368,22 +238,6 @@ __global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(cons
 
 // ---- element kernel: any head_dim, types and alignment -------------------------
 // A warp takes a (token, lane, head) row, its lanes stride over the elements.
-__device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype) {
-  if (dtype == LSC_F32) return ((const float *)p)[i];
-  if (dtype == LSC_BF16) return __bfloat162float(((const __nv_bfloat16 *)p)[i]);
-  return __half2float(((const __half *)p)[i]);
-}
-__device__ __forceinline__ void store_any(void *p, int64_t i, int dtype, float x) {
-  if (dtype == LSC_F32) ((float *)p)[i] = x;
-  else if (dtype == LSC_BF16) ((__nv_bfloat16 *)p)[i] = __float2bfloat16_rn(x);
-  else ((__half *)p)[i] = __float2half_rn(x);
-}
-// The same type on both sides moves as bits (a NaN keeps its payload).
-__device__ __forceinline__ void move_any(void *d, int64_t i, const void *s, int64_t j, int dtype) {
-  if (dtype == LSC_F32) ((uint32_t *)d)[i] = ((const uint32_t *)s)[j];
-  else ((uint16_t *)d)[i] = ((const uint16_t *)s)[j];
-}
-
 template <bool APPEND>
 __global__ void __launch_bounds__(kThreads) rows_any_kernel(const __grid_constant__ KvRowsParams p, int tok) {
   __shared__ Places s;
@@ -407,6 +261,21 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const __grid_constan
     uint8_t *scale = page + L.scale_off + (int64_t)row * L.heads + head;
     if (row == -1) {
       for (int d = ln; d < D; d += 32) store_any(dense, at + d, p.dtype, 0.f);
+    } else if (L.dtype == LSC_E2M1 && APPEND) {
+      for (int j = ln; j < D / 16; j += 32) {  // a lane has a group
+        float x[16];
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e] = load_any(dense, at + 16 * j + e, p.dtype);
+          m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+        }
+        const uint32_t sb = e2m1_scale_byte(m);
+        *(uint2 *)(page + (in >> 1) + 8 * j) = to_e2m1x16<true>(x, sb);
+        page[L.scale_off + (in >> 4) + j] = (uint8_t)sb;
+      }
+    } else if (L.dtype == LSC_E2M1) {
+      for (int d = ln; d < D; d += 32) store_any(dense, at + d, p.dtype, e2m1_element(page, L.scale_off, in + d));
     } else if (L.dtype == LSC_E4M3 && APPEND) {
       uint32_t m = 0;
       for (int d = ln; d < D; d += 32) m = max(m, __float_as_uint(load_any(dense, at + d, p.dtype)) & 0x7fffffffu);
@@ -446,6 +315,7 @@ cudaError_t launch_dense(const KvRowsParams &p, int grid, int tok, cudaStream_t 
     case LSC_F32: return launch_typed<APPEND, D, float, 1>(p, grid, tok, stream);
     case LSC_BF16: return launch_typed<APPEND, D, __nv_bfloat16, 1>(p, grid, tok, stream);
     case LSC_F16: return launch_typed<APPEND, D, __half, 1>(p, grid, tok, stream);
+    case LSC_E2M1: return launch_typed<APPEND, D, E2M1, 2>(p, grid, tok, stream);
     default:
       return p.L.head_dim % 16 == 0 ? launch_typed<APPEND, D, E4M3, 2>(p, grid, tok, stream)
                                     : launch_typed<APPEND, D, E4M3, 1>(p, grid, tok, stream);

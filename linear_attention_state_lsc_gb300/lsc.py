@@ -42,7 +42,7 @@ LSC_SLOT_FREE, LSC_SLOT_LIVE, LSC_SLOT_CHECKPOINT, LSC_SLOT_RESERVED = 0, 1, 2, 
 LSC_LAYER_ATTENTION, LSC_LAYER_GDN = 0, 1
 LSC_RECURRENT_AUTO, LSC_RECURRENT_TOKEN, LSC_RECURRENT_CHUNKED = 0, 1, 2
 LSC_DECODE_EARLY_STATE = 1
-LSC_F32, LSC_BF16, LSC_F16, LSC_E4M3 = 0, 1, 2, 3
+LSC_F32, LSC_BF16, LSC_F16, LSC_E4M3, LSC_E2M1 = 0, 1, 2, 3, 4
 
 
 class LscError(RuntimeError):
@@ -141,6 +141,24 @@ class lsc_kv_append_args(C.Structure):
                 ("reserved", C.c_int32), ("k_stride", C.c_int64), ("v_stride", C.c_int64)]
 
 
+class lsc_rotary(C.Structure):
+    _fields_ = [("rotary_dim", C.c_int32), ("axes", C.c_int32), ("interleaved", C.c_int32), ("scale", C.c_float),
+                ("inv_freq", C.c_void_p), ("pair_axis", C.c_void_p), ("positions", C.c_void_p),
+                ("axis_stride", C.c_int64)]
+
+
+class lsc_rotate_args(C.Structure):
+    _fields_ = [("total_tokens", C.c_int32), ("num_heads", C.c_int32), ("head_dim", C.c_int32), ("dtype", C.c_int32),
+                ("x", C.c_void_p), ("out", C.c_void_p), ("x_stride", C.c_int64), ("out_stride", C.c_int64),
+                ("rotary", lsc_rotary)]
+
+
+class lsc_kv_append_rotated_args(C.Structure):
+    _fields_ = [("append", lsc_kv_append_args), ("rotary", lsc_rotary), ("num_q_heads", C.c_int32),
+                ("reserved", C.c_int32), ("q", C.c_void_p), ("q_out", C.c_void_p), ("q_stride", C.c_int64),
+                ("q_out_stride", C.c_int64)]
+
+
 class lsc_kv_gather_args(C.Structure):
     _fields_ = [("batch", lsc_kv_batch), ("k", C.c_void_p), ("v", C.c_void_p), ("dtype", C.c_int32),
                 ("reserved", C.c_int32), ("k_stride", C.c_int64), ("v_stride", C.c_int64)]
@@ -192,6 +210,8 @@ def load():
         "lsc_kv_pool_layer_view": ([P, I32, C.POINTER(lsc_kv_layer_view)], C.c_int),
         "lsc_kv_pool_status": ([P, P, C.POINTER(I32)], C.c_int),
         "lsc_kv_append": ([P, I32, C.POINTER(lsc_kv_append_args), P], C.c_int),
+        "lsc_kv_append_rotated": ([P, I32, C.POINTER(lsc_kv_append_rotated_args), P], C.c_int),
+        "lsc_rotate": ([C.POINTER(lsc_rotate_args), P], C.c_int),
         "lsc_kv_gather": ([P, I32, C.POINTER(lsc_kv_gather_args), P], C.c_int),
         "lsc_kv_attend": ([P, I32, C.POINTER(lsc_kv_attend_args), P], C.c_int),
         "lsc_kv_attend_workspace_bytes": ([P, C.POINTER(lsc_kv_attend_args), C.POINTER(C.c_size_t)], C.c_int),
@@ -538,6 +558,46 @@ def kv_append_args(batch, k, v, dtype, k_stride=0, v_stride=0):
 
 def lsc_kv_append(pool, layer, args, stream=None):
     return load().lsc_kv_append(pool, layer, C.byref(args), _stream(stream))
+
+
+def rotary(rotary_dim, positions, inv_freq, pair_axis=None, interleaved=False, scale=1.0, axes=None, axis_stride=0):
+    """Rotary positions.  positions: an int32 device tensor, [tokens] or [axes, tokens] (rows may be further apart), or
+    an address with `axes` and `axis_stride`; inv_freq and pair_axis: host values of the rotary_dim / 2 pairs."""
+    freq = np.ascontiguousarray(inv_freq, np.float64)
+    axis = None if pair_axis is None else np.ascontiguousarray(pair_axis, np.uint8)
+    for a in (freq, axis):
+        if a is not None and a.shape != (rotary_dim // 2,):
+            raise ValueError(f"rotary_dim {rotary_dim} has {rotary_dim // 2} pairs, not {a.shape}")
+    if hasattr(positions, "dim"):
+        if str(positions.dtype) != "torch.int32" or positions.dim() not in (1, 2) or (positions.shape[-1] > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions: int32 [tokens] or [axes, tokens], tokens side by side")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        axis_stride = positions.stride(0) if axes > 1 else 0
+    r = lsc_rotary(rotary_dim, 1 if axes is None else axes, int(interleaved), scale, freq.ctypes.data,
+                   None if axis is None else axis.ctypes.data, ptr(positions), axis_stride)
+    r._host = (freq, axis)  # the addresses above
+    return r
+
+
+def rotate_args(total_tokens, num_heads, head_dim, dtype, x, out, rotary, x_stride=0, out_stride=0):
+    a = lsc_rotate_args(total_tokens, num_heads, head_dim, dtype, ptr(x), ptr(out), x_stride, out_stride, rotary)
+    a._rotary = rotary
+    return a
+
+
+def lsc_rotate(args, stream=None):
+    return load().lsc_rotate(C.byref(args), _stream(stream))
+
+
+def kv_append_rotated_args(append, rotary, num_q_heads=0, q=None, q_out=None, q_stride=0, q_out_stride=0):
+    """append: kv_append_args; q is of its dtype."""
+    a = lsc_kv_append_rotated_args(append, rotary, num_q_heads, 0, ptr(q), ptr(q_out), q_stride, q_out_stride)
+    a._rotary = rotary
+    return a
+
+
+def lsc_kv_append_rotated(pool, layer, args, stream=None):
+    return load().lsc_kv_append_rotated(pool, layer, C.byref(args), _stream(stream))
 
 
 def kv_gather_args(batch, k, v, dtype, k_stride=0, v_stride=0):
