@@ -93,7 +93,7 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
 // of a block, column of 128 bytes, kv head, block; V's blocks follow K's), a box
 // of one column, or of all when it has a whole tile's rows.  A box never leaves its
 // block: its rows are the largest power of two that divides block_tokens, up to
-// the tile's.  128-byte swizzle (64 bytes a row: 64-byte).  Without maps (blocks that are
+// the tile's.  128-byte swizzle (rows of 64 or 32 bytes: 64- or 32-byte).  Without maps (blocks that are
 // no multiple of 8 tokens, other types and sizes) the kernels copy rows themselves.
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -106,7 +106,9 @@ bool encode_maps(const lsc_kv_pool *p, EncodeTiled encode, int tile, int box, st
   const CUtensorMapDataType type = es == 1               ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : d.dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const CUtensorMapSwizzle swizzle = col == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUtensorMapSwizzle swizzle = col == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                     : col == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                 : CU_TENSOR_MAP_SWIZZLE_128B;
   const cuuint64_t dims[5] = {(cuuint64_t)(col / es), (cuuint64_t)d.block_tokens, (cuuint64_t)(row / col),
                               (cuuint64_t)d.num_kv_heads, 2 * (cuuint64_t)d.num_blocks};
   const cuuint64_t strides[4] = {(cuuint64_t)p->row_bytes, (cuuint64_t)col, (cuuint64_t)row, (cuuint64_t)d.page_bytes};
@@ -128,7 +130,7 @@ bool encode_maps(const lsc_kv_pool *p, EncodeTiled encode, int tile, int box, st
 void make_maps(lsc_kv_pool *p) {
   const lsc_kv_pool_desc &d = p->d;
   const int D = d.head_dim, most = d.block_tokens & -d.block_tokens;
-  if (d.dtype == LSC_F32 || d.dtype == LSC_E2M1 || (D != 64 && D != 128 && D != 256) || most < 8) return;  // a swizzle pattern is 8 rows
+  if (d.dtype == LSC_F32 || (D != 64 && D != 128 && D != 256) || most < 8) return;  // a swizzle pattern is 8 rows
   void *fn = nullptr;
   cudaDriverEntryPointQueryResult found;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
@@ -139,12 +141,12 @@ void make_maps(lsc_kv_pool *p) {
   const int tile = D == 256 ? 64 : 128, keys = lsc::kv_decode_keys(D, (int)p->bits);
   const int box = std::min(most, tile), box_decode = std::min(most, keys);
   std::vector<CUtensorMap> maps, decode;
-  if (!encode_maps(p, (EncodeTiled)fn, tile, box, &maps) ||
+  if ((d.dtype != LSC_E2M1 && !encode_maps(p, (EncodeTiled)fn, tile, box, &maps)) ||  // E2M1: decode alone takes boxes
       !encode_maps(p, (EncodeTiled)fn, keys, box_decode, &decode))
     return;
   p->maps.swap(maps);
   p->maps_decode.swap(decode);
-  p->box_rows = box;
+  p->box_rows = p->maps.empty() ? 0 : box;
   p->box_decode = box_decode;
 }
 
@@ -344,7 +346,7 @@ enum Form { kAny, kDecode, kRows, kChunk };
 
 bool tensor_core_types(const lsc::KvAttendParams &r) {
   const int D = r.L.head_dim;
-  return r.dtype != LSC_F32 && (r.L.dtype == r.dtype || r.L.dtype == LSC_E4M3) && (D == 64 || D == 128 || D == 256);
+  return r.dtype != LSC_F32 && (r.L.dtype == r.dtype || r.L.dtype == LSC_E4M3 || r.L.dtype == LSC_E2M1) && (D == 64 || D == 128 || D == 256);
 }
 
 Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
@@ -360,6 +362,8 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   if (rows <= kDecodeMost && r.box_decode > 0) {
     form = kDecode;
     *plan = lsc::plan_kv_attend_decode(r);
+  } else if (r.L.dtype == LSC_E2M1) {
+    return kAny;
   } else if (rows <= (q8 ? kRowsMost : kDecodeMost)) {
     form = kRows;
     *plan = lsc::plan_kv_attend_rows(r);
@@ -388,6 +392,7 @@ size_t attend_workspace(lsc::KvAttendParams r) {
   };
   if (r.box_decode > 0 && rows_up_to(kDecodeMost))
     most = std::max(lsc::plan_kv_attend_decode(r).ws_bytes, lsc::plan_kv_attend_decode(r, false).ws_bytes);
+  if (r.L.dtype == LSC_E2M1) return most;
   if ((q8 || r.box_decode == 0) && rows_up_to(few)) most = std::max(most, lsc::plan_kv_attend_rows(r).ws_bytes);
   r.max_seq = max_seq;
   if ((int64_t)max_seq * r.group > few && !(q8 && r.dtype != LSC_BF16))

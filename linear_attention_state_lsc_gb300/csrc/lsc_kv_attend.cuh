@@ -250,10 +250,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Byte of 16-byte chunk ch of row r in a swizzled tile of `rows` rows: columns of LINE bytes, chunks xor the row's low bits
-// (lines of 64 bytes: pairs of rows share 128).
+// (lines of 64 bytes: pairs of rows share 128; of 32: four do).
 template <int LINE>
 __device__ __forceinline__ uint32_t chunk_at(int rows, int r, int ch) {
-  if constexpr (LINE == 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+  if constexpr (LINE == 32) return r * 32 + ((ch ^ ((r >> 2) & 1)) << 4);
+  else if constexpr (LINE == 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
   else return (ch >> 3) * (rows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
 

@@ -1,0 +1,479 @@
+// lsc_kv_attend_decode4.cuh -- attention over an E2M1 layer of the K/V block pool for
+// sequences of up to 16 packed rows (lsc_kv_attend.cuh): decode steps.
+//
+// The plan is that of lsc_kv_attend_decode.cuh: warps that work alone, each with a
+// ring of TMA sub-tiles, transposed products S^T = K Q^T and O^T = V^T P^T on
+// mma.sync, a reference instead of a maximum, joined at a piece's end.  A quarter of
+// the bytes of 16 bits come in, so what is done to them counts for four times as much:
+//   * K: a 32-bit word of a lane is 8 codes of one position and one scale.  Four
+//     conversions give four pairs of halves, four products with the scale leave K's
+//     exact values (6 bits), and they are the operands of two products as they are: which
+//     element of a head a product's place holds does not matter as long as q has the same.
+//   * V: ldmatrix transposes pairs of bytes, so a word is 4 columns of two neighbouring
+//     positions; the conversions pair columns, a byte permutation for each pairs
+//     positions, and the products with both positions' scales follow.
+//   * scales come with 4- to 16-byte cp.async, a position a lane, into a ring beside the codes'.
+// q goes to f16: bf16 rows are brought to [2^14, 2^15) by a power of two that the scores
+// take back, so what bf16 holds down to 2^-28 of a row's largest is exact.
+//
+// Positions that only some rows see, or none (what a block holds behind the last one):
+// the code of a hidden position is finite whatever it is, so clearing the scale clears
+// the element; a scale that may make it infinite or NaN is noted and added again, as
+// NaN, to the rows that see the position.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "lsc_internal.h"
+#include "lsc_kv_attend.cuh"
+#include "lsc_kv_attend_decode.cuh"
+#include "lsc_ptx.h"
+
+namespace lsc {
+namespace kv {
+namespace decode4 {
+
+using decode::transposed;
+using rows::ldsm4;
+using rows::ldsm4t;
+using rows::mma;
+
+constexpr int kTK = decode::kTK;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int KEYS = 32;  // positions of a sub-tile: one a lane
+
+template <int D>
+struct Conf {
+  static_assert(kv_decode_keys(D, 4) == KEYS, "what the boxes are made for");
+  static constexpr int RB = D / 2, SB = D / 16;  // bytes of a row's codes and scales
+  static constexpr int half = KEYS * RB;         // bytes of a sub-tile's K or V codes
+  static constexpr int ST = D == 64 ? 4 : 3;     // sub-tiles in flight per warp
+  static constexpr int occ = D == 256 ? 2 : D == 128 ? 3 : 4;  // CTAs per SM
+};
+
+template <int D>
+struct Smem {
+  using C = Conf<D>;
+  alignas(1024) uint8_t ring[kWarps][C::ST][2][C::half];  // at a piece's end: the warps' weighted rows
+  alignas(16) uint8_t scale[kWarps][C::ST][2][KEYS][C::SB];
+  float2 ml[kWarps][16];
+  int32_t vis[16];
+  int32_t bad[kWarps][C::SB];  // by head of the unit and group: the first position whose v is NaN
+  int32_t any_bad;
+  uint64_t full[kWarps][C::ST];
+  RunScratch run;
+};
+
+// N bytes global -> shared, or zeros when `on` is false (nothing is read then).
+template <int N>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
+}
+
+// SB scale bytes of a position, in 32-bit words.
+template <int SB>
+__device__ __forceinline__ void load_scales(uint32_t (&w)[SB / 4], const uint8_t *p) {
+  if constexpr (SB == 4) w[0] = *(const uint32_t *)p;
+  if constexpr (SB == 8) {
+    const uint2 x = *(const uint2 *)p;
+    w[0] = x.x, w[1] = x.y;
+  }
+  if constexpr (SB == 16) {
+    const uint4 x = *(const uint4 *)p;
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  }
+}
+
+__device__ __forceinline__ uint32_t times(uint32_t h, uint32_t s) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&s));
+  return *reinterpret_cast<const uint32_t *>(&y);
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kThreads, (Conf<D>::occ))
+decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map, int together) {
+  using C = Conf<D>;
+  constexpr int M = 8 * NR;         // rows of a head, NR tiles of 8
+  constexpr int ST = C::ST, RB = C::RB, SB = C::SB, NC = D / 32;  // NC: 16-byte chunks of a row, 32 elements each
+  constexpr int KS = D / 16;        // output tiles of 16 columns
+  constexpr float lift = 7.f;       // powers of two that the reference lies below the maximum that set it
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+  const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31, g = ln >> 2, tq = ln & 3;
+  if (tid < kWarps * ST) mbar_init(&sm.full[tid / ST][tid % ST], 1);
+  fence_mbar_init();
+  griddep_wait();
+  if (tid == 0) griddep_launch_dependents();
+  const KvLayer &L = p.L;
+  const int ctas = gridDim.x, cta = blockIdx.x;
+  if (cta == 0) check_cu(L, p.b);
+  const int MU = M * together, splits = kWarps / together;  // rows of a unit; warps of a head
+  const int wh = w & (together - 1), wsp = w / together;    // this warp's head of the unit, its share of the sub-tiles
+  const Workspace ws = workspace_at(p.ws, ctas, MU);
+  if (tid == 0) sm.any_bad = 0;
+  for (int i = tid; i < kWarps * SB; i += kThreads) (&sm.bad[0][0])[i] = INT32_MAX;
+  Run run = find_run<kThreads, M, kTK>(p, cta, ctas, sm.run);
+  Piece pc;
+  Cut cut = {0, 0, 0, 0};
+  bool ok = true;
+  // TMA boxes of `box` rows: K's on lanes 0-15, V's on 16-31
+  const int box = p.box_decode, boxes = KEYS / box;
+  const int bi = ln & 15, br = bi < boxes ? bi * box : 0;
+  uint8_t *const ring = sm.ring[w][0][0];
+  // where a lane's scale bytes are in a word: its group of a chunk (K: by tq, V: by g), for even and odd chunks
+  const uint32_t kh = tq >> 1, vh = g >> 2;
+  const uint32_t ksel[2] = {0x4040u | kh | kh << 8, 0x4040u | (kh + 2) | (kh + 2) << 8};
+  const uint32_t vsel[2] = {vh | (vh + 4) << 8, (vh + 2) | (vh + 6) << 8};
+  int slot = 0;
+  uint32_t phase = 0;
+  __syncthreads();
+  while (ok && next_piece<M, kTK>(p, run, pc)) {
+    const int R = pc.s.n * p.group < M ? pc.s.n * p.group : M;  // this launch's units have one block
+    const int32_t kv = pc.s.kv, lo = pc.t0 * kTK, hi = kv < pc.t1 * kTK ? kv : pc.t1 * kTK;
+    const int32_t *table = p.b.table + (int64_t)pc.seq * p.b.max_blocks;
+    const int nsub = hi > lo ? (hi - lo + KEYS - 1) / KEYS : 0, mine = nsub > wsp ? (nsub - wsp + splits - 1) / splits : 0, head = pc.head * together + wh;
+    auto first_of = [&](int i) { return lo + (i * splits + wsp) * KEYS; };  // first position of this warp's sub-tile i
+    // Block of this lane's position of sub-tile i, 0 behind the last one.  Looked up a sub-tile ahead and checked only
+    // where it is used (a bad one is recorded and read as 0): a look at it any earlier would wait for the load.
+    auto block_at = [&](int i) {
+      const int32_t pos = first_of(i) + ln;
+      return i < mine && pos < kv ? __ldg(table + L.by_block.div(pos)) : 0;
+    };
+    auto issue = [&](int i, int st, int32_t blk) {
+      if ((uint32_t)blk >= (uint32_t)L.num_blocks) {
+        report(L.status, LSC_ERR_OUT_OF_RANGE);
+        blk = 0;
+      }
+      const int32_t pos = first_of(i) + ln, row = pos - L.by_block.div(pos) * L.block_tokens;
+      if (ln == 0) mbar_arrive_expect_tx(&sm.full[w][st], 2 * C::half);
+      __syncwarp();
+      const int32_t box_blk = __shfl_sync(0xffffffffu, blk, br), box_row = __shfl_sync(0xffffffffu, row, br);
+      if (bi < boxes)
+        tma_box(ring + (st * 2 + (ln >> 4)) * C::half + br * RB, &map, box_row, 0, head,
+                box_blk + (ln < 16 ? 0 : L.num_blocks), &sm.full[w][st]);
+      const int64_t at = (int64_t)blk * L.page + L.scale_off + ((int64_t)row * L.heads + head) * SB;
+      const bool on = pos < kv;
+      cp_async_or_zero<SB>(smem_u32(sm.scale[w][st][0][ln]), L.k + (on ? at : 0), on);
+      cp_async_or_zero<SB>(smem_u32(sm.scale[w][st][1][ln]), L.v + (on ? at : 0), on);
+    };
+    int st_in = slot;
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+      if (i < mine) {
+        issue(i, st_in, block_at(i));
+        if (++st_in == ST) st_in = 0;
+      }
+      cp_async_commit();
+    }
+    int32_t next_blk = block_at(ST);
+
+    if (tid < M) sm.vis[tid] = tid < R ? visible(pc.s, p.by_group.div(tid), p.causal) : 0;
+    // q as operand registers: row g of each 8, elements 8 tq .. 8 tq + 7 of each 32, as f16
+    uint32_t qf[NR][NC][4];
+    float q_up[NR];  // of row g: scale * log2 e, times the power of two that bf16 rows were brought down by
+#pragma unroll
+    for (int h = 0; h < NR; ++h) {
+      const int r = 8 * h + g, tok = p.by_group.div(r);
+      const uint16_t *src = (const uint16_t *)p.q + (int64_t)(pc.s.row0 + tok) * p.q_stride +
+                            (int64_t)(head * p.group + (r - tok * p.group)) * D;
+      q_up[h] = p.scale_log2;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const uint4 x = r < R ? *(const uint4 *)(src + c * 32 + 8 * tq) : make_uint4(0, 0, 0, 0);
+        qf[h][c][0] = x.x, qf[h][c][1] = x.y, qf[h][c][2] = x.z, qf[h][c][3] = x.w;
+      }
+      if (p.dtype == LSC_BF16) {
+        uint32_t top = 0;  // magnitudes of 16-bit floats order as whole numbers
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = __vmaxu2(top, qf[h][c][e] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t ex = top >> 7;  // 2^k <= the largest magnitude < 2^(k + 1), where that is a normal number
+        const bool plain = ex == 0 || ex == 255;
+        const float down = plain ? 1.f : inv_scale_of(ex), more = plain ? 1.f : 16384.f;
+        if (!plain) q_up[h] = q_up[h] * __uint_as_float(ex << 23) * (1.f / 16384.f);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t b = qf[h][c][e];
+            qf[h][c][e] = pack2(__uint_as_float(b << 16) * down * more, __uint_as_float(b & 0xffff0000u) * down * more, 0);
+          }
+      }
+    }
+    // scores come with rows 2 tq, 2 tq + 1 of each 8
+    float qsc[NR][2];
+#pragma unroll
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qsc[h][e] = __shfl_sync(0xffffffffu, q_up[h], (2 * tq + e) * 4);
+    __syncthreads();  // vis; and the last piece's shared memory is free
+    const int32_t sure = visible(pc.s, 0, p.causal);  // every row sees positions below this
+    int32_t vis[NR][2];
+    float m[NR][2], l[NR][2], o[NR][KS][4];
+#pragma unroll
+    for (int h = 0; h < NR; ++h) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) vis[h][e] = sm.vis[8 * h + 2 * tq + e], m[h][e] = -INFINITY, l[h][e] = 0.f;
+#pragma unroll
+      for (int n = 0; n < KS; ++n) o[h][n][0] = o[h][n][1] = o[h][n][2] = o[h][n][3] = 0.f;
+    }
+
+    int i = 0;
+#pragma unroll 1
+    for (; i < mine; ++i) {
+      const int32_t first = first_of(i);
+      cp_async_wait<ST - 1>();
+      if (!(ok = wait_warp(&sm.full[w][slot], phase, p.wait_limit_ns))) break;
+      __syncwarp();
+      const uint32_t ka = smem_u32(ring + slot * 2 * C::half), va = ka + C::half;
+      const uint8_t *kscale = sm.scale[w][slot][0][0], *vscale = sm.scale[w][slot][1][0];
+      if (first + KEYS > sure) {  // (some of) V's scales need a look before they meet a weight of 0
+        if (first + ln >= sure && first + ln < hi) {
+          uint8_t *v = sm.scale[w][slot][1][ln];
+#pragma unroll 1
+          for (int x = 0; x < SB; ++x)
+            if (v[x] > kE2M1Top) {
+              atomicMin(&sm.bad[wh][x], first + ln);
+              sm.any_bad = 1;
+              v[x] = 0;
+            }
+        }
+        __syncwarp();
+      }
+      // ---- scores: lane (g, tq) gets positions g, g + 8 of each 16 and rows 2 tq, 2 tq + 1 of each 8
+      // (two sums a tile, all tiles in turn: a product waits for the one before it in its sum)
+      float s[2][NR][4], s2[2][NR][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < NR; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][h][e] = s2[n][h][e] = 0.f;
+      {
+        uint32_t ks[4][SB / 4];  // of positions g + 8 y
+#pragma unroll
+        for (int y = 0; y < 4; ++y) load_scales<SB>(ks[y], kscale + (g + 8 * y) * SB);
+#pragma unroll
+        for (int c = 0; c < NC; c += 2)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            uint32_t b[4];
+            ldsm4(b, ka + chunk_at<RB>(KEYS, 16 * n + (ln & 15), c + (ln >> 4)));
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {  // chunk c + y
+              uint32_t x[2][4];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {  // positions g, g + 8
+                const uint32_t sc = __byte_perm(ks[2 * n + z][c >> 1], 0, ksel[y]) << 7;
+                e2m1x8_times(b[2 * y + z], *reinterpret_cast<const __half2 *>(&sc), x[z]);
+              }
+              const uint32_t a0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]}, a1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
+#pragma unroll
+              for (int h = 0; h < NR; ++h) {
+                mma<false>(s[n][h], a0, qf[h][c + y][0], qf[h][c + y][1]);
+                mma<false>(s2[n][h], a1, qf[h][c + y][2], qf[h][c + y][3]);
+              }
+            }
+          }
+      }
+      // ---- weights
+      float top[NR][2];
+#pragma unroll
+      for (int h = 0; h < NR; ++h) top[h][0] = top[h][1] = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int key = 16 * n + 8 * y + g;
+#pragma unroll
+          for (int h = 0; h < NR; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = (s[n][h][2 * y + e] + s2[n][h][2 * y + e]) * qsc[h][e];
+              x = first + key < vis[h][e] ? x : -INFINITY;
+              s[n][h][2 * y + e] = x;
+              top[h][e] = fmaxf(top[h][e], x);
+            }
+        }
+      bool rise = false;
+#pragma unroll
+      for (int h = 0; h < NR; ++h) rise |= top[h][0] > m[h][0] + (8.f + lift) || top[h][1] > m[h][1] + (8.f + lift);
+      if (__any_sync(0xffffffffu, rise)) {  // also the first one's (m is -inf)
+#pragma unroll
+        for (int h = 0; h < NR; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = top[h][e];
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            const float to = fmaxf(m[h][e], t - lift), f = ex2(m[h][e] - (to == -INFINITY ? 0.f : to));
+            m[h][e] = to;
+            l[h][e] *= f;
+#pragma unroll
+            for (int n = 0; n < KS; ++n) o[h][n][e] *= f, o[h][n][2 + e] *= f;
+          }
+      }
+      uint32_t a[2][NR][2];
+#pragma unroll
+      for (int h = 0; h < NR; ++h) {
+        const float r0 = m[h][0] == -INFINITY ? 0.f : m[h][0], r1 = m[h][1] == -INFINITY ? 0.f : m[h][1];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float p0 = ex2(s[n][h][2 * y] - r0), p1 = ex2(s[n][h][2 * y + 1] - r1);
+            l[h][0] += p0;
+            l[h][1] += p1;
+            a[n][h][y] = transposed(pack2(p0, p1, 0));
+          }
+      }
+      // ---- V^T times weights
+      {
+        uint32_t vs[8][SB / 4];  // of positions 8 x + 2 tq, + 1
+#pragma unroll
+        for (int x = 0; x < 8; ++x) load_scales<SB>(vs[x], vscale + (8 * (x >> 1) + 2 * tq + (x & 1)) * SB);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {  // 32 columns: m index g is column 4 g (+ 2), m index g + 8 the one behind it
+          uint32_t b[4];
+          ldsm4t(b, va + chunk_at<RB>(KEYS, ln, c));
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            uint32_t x[2][4];  // columns 4 g .. 4 g + 3 of positions 2 tq, 2 tq + 1 and 8 further
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              uint32_t h[4];
+              e2m1x8_to_f16(b[2 * n + y], h);
+              // the group's bytes of both positions, in the lower byte of a half each
+              const uint32_t sv = (__byte_perm(vs[4 * n + 2 * y][c >> 1], vs[4 * n + 2 * y + 1][c >> 1], vsel[c & 1]) & 0x00ff00ffu) << 7;
+              x[y][0] = times(__byte_perm(h[0], h[2], 0x5410), sv);
+              x[y][1] = times(__byte_perm(h[0], h[2], 0x7632), sv);
+              x[y][2] = times(__byte_perm(h[1], h[3], 0x5410), sv);
+              x[y][3] = times(__byte_perm(h[1], h[3], 0x7632), sv);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t v[4] = {x[0][2 * z], x[0][2 * z + 1], x[1][2 * z], x[1][2 * z + 1]};
+#pragma unroll
+              for (int h = 0; h < NR; ++h) mma<false>(o[h][2 * c + z], v, a[n][h][0], a[n][h][1]);
+            }
+          }
+        }
+      }
+      // ---- the slot's next sub-tile
+      __syncwarp();
+      if (i + ST < mine) {
+        issue(i + ST, slot, next_blk);
+        next_blk = block_at(i + ST + 1);
+      }
+      cp_async_commit();
+      if (++slot == ST) slot = 0, phase ^= 1;
+    }
+    if (!ok) {  // nothing may be in flight when the CTA leaves: every slot that was filled
+      for (int x = i; x < mine && x < i + ST; ++x) {
+        wait_warp(&sm.full[w][slot], phase, p.drain_limit_ns);
+        if (++slot == ST) slot = 0, phase ^= 1;
+      }
+      cp_async_wait<0>();
+      if (ln == 0) report(L.status, LSC_ERR_DEV_TIMEOUT);
+    }
+    // ---- the piece's end: the warps' parts through shared memory, then rows out or to the workspace
+#pragma unroll
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 4);
+        l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 8);
+        l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 16);
+        if (g == 0) sm.ml[w][8 * h + 2 * tq + e] = make_float2(m[h][e], l[h][e]);
+      }
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+    // [row][column] of 32 bits, rows padded by 4 (D + 4: no bank twice in what follows); the rings are empty
+    constexpr int PS = D + 4;
+    static_assert(sizeof(sm.ring) >= (size_t)kWarps * 16 * PS * 4, "the parts fit");
+    float *parts = (float *)sm.ring;
+#pragma unroll
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * h + 2 * tq + e;
+        if (r < R) {
+          float *row = parts + (w * M + r) * PS;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)  // columns 4 g .. 4 g + 3 of 32
+            *(float4 *)(row + c * 32 + 4 * g) = make_float4(o[h][2 * c][e], o[h][2 * c][2 + e], o[h][2 * c + 1][e], o[h][2 * c + 1][2 + e]);
+        }
+      }
+    __syncthreads();
+    const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
+    const int64_t slot0 = (int64_t)(2 * cta + (pc.t0 == 0 ? 1 : 0)) * MU;
+    const bool look = sm.any_bad != 0;
+#pragma unroll 1
+    for (int x = tid; x < together * M * (D / 4); x += kThreads) {
+      const int hr = x / (D / 4), d = x % (D / 4) * 4, r = hr & (M - 1), hw = hr / M, tok = p.by_group.div(r);
+      if (r >= R) continue;
+      float mm = -INFINITY, sum = 0.f;
+      for (int i = hw; i < kWarps; i += together) mm = fmaxf(mm, sm.ml[i][r].x);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = hw; i < kWarps; i += together) {
+        const float2 ml = sm.ml[i][r];
+        const float k = exp2f(ml.x - ref);
+        const float4 z = *(const float4 *)(parts + (i * M + r) * PS + d);
+        sum += ml.y * k;
+        y.x += z.x * k, y.y += z.y * k, y.z += z.z * k, y.w += z.w * k;
+      }
+      const bool empty = sm.vis[r] == 0;
+      const float inv = whole ? (empty ? 0.f : 1.f / sum) : 1.f;
+      y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
+      if (look && sm.bad[hw][d / 16] < sm.vis[r]) y.x = y.y = y.z = y.w = __uint_as_float(0x7fc00000u);
+      const int64_t t = pc.s.row0 + tok, hd = (int64_t)(pc.head * together + hw) * p.group + (r - tok * p.group);
+      if (whole) {
+        const int bf = p.dtype == LSC_BF16;
+        *(uint2 *)((uint16_t *)p.out + t * p.out_stride + hd * D + d) = make_uint2(pack2(y.x, y.y, bf), pack2(y.z, y.w, bf));
+        if (d == 0 && p.lse) p.lse[t * p.heads + hd] = empty ? -INFINITY : (mm + log2f(sum)) * 0.693147180559945309f;
+      } else {
+        *(float4 *)(ws.o + (slot0 + hr) * D + d) = y;
+        if (d == 0) ws.ml[slot0 + hr] = make_float2(mm, sum);
+      }
+    }
+    cut = cut_of(run, pc, cta);
+    fence_proxy_async_smem();  // the parts were written where the next piece's boxes land
+    __syncthreads();
+    if (look) {
+      for (int i = tid; i < kWarps * SB; i += kThreads) (&sm.bad[0][0])[i] = INT32_MAX;
+      if (tid == 0) sm.any_bad = 0;
+      __syncthreads();
+    }
+  }
+  if (tid == 0 && p.ws) ws.cut[cta] = cut;
+}
+
+template <int D, int NR>
+cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+  static SmemLimit limit;
+  const int smem = (int)sizeof(Smem<D>);
+  auto *k = decode4_attend_kernel<D, NR>;
+  const cudaError_t e = limit.ensure((const void *)k, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, plan.ctas, kThreads, smem, stream, p, *p.map_decode, plan.together);
+}
+
+template <int D>
+cudaError_t launch_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+  return plan.M == 8 * plan.together ? launch_one<D, 1>(p, plan, stream) : launch_one<D, 2>(p, plan, stream);
+}
+
+}  // namespace decode4
+}  // namespace kv
+
+cudaError_t launch_kv_attend_decode_e2m1(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
+
+}  // namespace lsc

@@ -12,6 +12,7 @@
 #include "lsc_kv_attend.cuh"
 #include "lsc_kv_attend_chunk.cuh"
 #include "lsc_kv_attend_decode.cuh"
+#include "lsc_kv_attend_decode4.cuh"
 #include "lsc_kv_attend_rows.cuh"
 #include "lsc_ptx.h"
 
@@ -103,17 +104,18 @@ AttendPlan plan_kv_attend_rows(const KvAttendParams &p) {
 
 AttendPlan plan_kv_attend_decode(const KvAttendParams &p, bool side_by_side) {
   using namespace kv::decode;
-  const int D = p.L.head_dim, q8 = p.L.dtype == LSC_E4M3;
+  const int D = p.L.head_dim, q8 = p.L.dtype == LSC_E4M3, q4 = p.L.dtype == LSC_E2M1;
   AttendPlan plan{};
   plan.TK = kTK;
   // Heads that lie side by side in a row are read side by side, up to 1 KB of them: 128 bytes at a time left the memory
   // at 61 % of the copy rate.  Not where that would leave CTAs without a tile: one sequence of 1001 tokens over 2 heads
   // took 17 us on 32 CTAs and 22 on 16.
-  const int row = D * (q8 ? 1 : 2), H = p.L.heads;
+  const int row = q4 ? D / 2 : q8 ? D : 2 * D, H = p.L.heads;
   plan.together = !side_by_side ? 1 : H % 4 == 0 && row <= 256 ? 4 : H % 2 == 0 && row <= 512 ? 2 : 1;
   if ((int64_t)p.b.n_seq * (H / plan.together) * p.max_kv < (int64_t)p.num_sms * 4 * kTK) plan.together = 1;
   plan.M = ((int64_t)p.max_seq * p.group <= 8 ? 8 : 16) * plan.together;
-  const int occ = q8 ? (D == 64 ? Conf<1, 64>::occ : D == 128 ? Conf<1, 128>::occ : Conf<1, 256>::occ)
+  const int occ = q4   ? (D == 64 ? kv::decode4::Conf<64>::occ : D == 128 ? kv::decode4::Conf<128>::occ : kv::decode4::Conf<256>::occ)
+                  : q8 ? (D == 64 ? Conf<1, 64>::occ : D == 128 ? Conf<1, 128>::occ : Conf<1, 256>::occ)
                      : (D == 64 ? Conf<2, 64>::occ : D == 128 ? Conf<2, 128>::occ : Conf<2, 256>::occ);
   const int64_t tiles = ((int64_t)p.max_kv + kTK - 1) / kTK;
   const int64_t units = (int64_t)p.b.n_seq * (H / plan.together), most = units * (tiles < 1 ? 1 : tiles);
@@ -125,7 +127,8 @@ AttendPlan plan_kv_attend_decode(const KvAttendParams &p, bool side_by_side) {
 }
 
 cudaError_t launch_kv_attend_decode(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
-  const cudaError_t e = p.L.dtype == LSC_E4M3   ? launch_kv_attend_decode_e4m3(p, plan, stream)
+  const cudaError_t e = p.L.dtype == LSC_E2M1   ? launch_kv_attend_decode_e2m1(p, plan, stream)
+                        : p.L.dtype == LSC_E4M3 ? launch_kv_attend_decode_e4m3(p, plan, stream)
                         : p.L.dtype == LSC_BF16 ? launch_kv_attend_decode_bf16(p, plan, stream)
                                                 : launch_kv_attend_decode_f16(p, plan, stream);
   return e == cudaSuccess ? cudaGetLastError() : e;
