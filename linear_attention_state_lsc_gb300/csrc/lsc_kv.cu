@@ -339,7 +339,8 @@ int check_attend(const lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *
 // of 4 behind 1000: 23 and 25.  bf16, 128 sequences of 8 tokens behind 500 to 8000, 8
 // heads, 32 rows: head_dim 64, 829 and 386, head_dim 128, 1068 and 436; 4 such
 // sequences of 5: 46 and 34, 56 and 38; one of 8 behind 1000: 22 and 24, 23 and 27.
-// E4M3, 128 sequences of 8 tokens, head_dim 128: 1115 and 1131.
+// E4M3, 128 sequences of 8 tokens, head_dim 128: 1115 and 1131.  E2M1 pools have no
+// few-row kernel: the chunk kernel takes what the decode kernel does not.
 constexpr int32_t kDecodeMost = 16, kRowsMost = 64;
 constexpr int64_t kMostCounts = 1 << 30;
 enum Form { kAny, kDecode, kRows, kChunk };
@@ -362,9 +363,7 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   if (rows <= kDecodeMost && r.box_decode > 0) {
     form = kDecode;
     *plan = lsc::plan_kv_attend_decode(r);
-  } else if (r.L.dtype == LSC_E2M1) {
-    return kAny;
-  } else if (rows <= (q8 ? kRowsMost : kDecodeMost)) {
+  } else if (rows <= (q8 ? kRowsMost : kDecodeMost) && r.L.dtype != LSC_E2M1) {  // E2M1: the chunk kernel copies any blocks
     form = kRows;
     *plan = lsc::plan_kv_attend_rows(r);
   } else {
@@ -383,7 +382,7 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
 // sizes may do without.
 size_t attend_workspace(lsc::KvAttendParams r) {
   if (!tensor_core_types(r)) return 0;
-  const bool q8 = r.L.dtype == LSC_E4M3;
+  const bool q8 = r.L.dtype == LSC_E4M3, q4 = r.L.dtype == LSC_E2M1;
   const int32_t max_seq = r.max_seq, few = q8 ? kRowsMost : kDecodeMost;
   size_t most = 0;
   auto rows_up_to = [&](int32_t rows) {
@@ -392,10 +391,9 @@ size_t attend_workspace(lsc::KvAttendParams r) {
   };
   if (r.box_decode > 0 && rows_up_to(kDecodeMost))
     most = std::max(lsc::plan_kv_attend_decode(r).ws_bytes, lsc::plan_kv_attend_decode(r, false).ws_bytes);
-  if (r.L.dtype == LSC_E2M1) return most;
-  if ((q8 || r.box_decode == 0) && rows_up_to(few)) most = std::max(most, lsc::plan_kv_attend_rows(r).ws_bytes);
+  if ((q8 || r.box_decode == 0) && !q4 && rows_up_to(few)) most = std::max(most, lsc::plan_kv_attend_rows(r).ws_bytes);
   r.max_seq = max_seq;
-  if ((int64_t)max_seq * r.group > few && !(q8 && r.dtype != LSC_BF16))
+  if (((int64_t)max_seq * r.group > few && !(q8 && r.dtype != LSC_BF16)) || (q4 && r.box_decode == 0))
     most = std::max(most, lsc::plan_kv_attend_chunk(r).ws_bytes);
   return most;
 }

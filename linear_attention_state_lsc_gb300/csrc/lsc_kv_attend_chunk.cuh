@@ -75,7 +75,7 @@ namespace lsc {
 namespace kv {
 namespace chunk {
 
-template <int D, bool Q8, bool BF16 = true>
+template <int D, bool Q8, bool BF16 = true, bool Q4 = false>
 struct Conf {
   static constexpr int NQ = D == 256 ? 1 : 2;   // row blocks of 128
   static constexpr int M = 128 * NQ;
@@ -84,14 +84,18 @@ struct Conf {
   static constexpr int ES = Q8 ? 1 : 2;         // bytes of an element
   static constexpr int row = D * ES, line = row < 128 ? row : 128;  // bytes of a row, of a swizzled line of it
   static constexpr int slot = TK * row;         // bytes of a K or V tile
-  static constexpr int NS = Q8 ? (D == 128 ? 6 : 8) : (D == 64 ? 8 : D == 128 ? 4 : 6);
+  static constexpr int NS = Q8 ? (D == 128 ? 6 : 8) : Q4 ? (D == 64 ? 8 : D == 128 ? 3 : 5) : (D == 64 ? 8 : D == 128 ? 4 : 6);
   static constexpr int SR = Q8 ? 8 : 1;         // E4M3: tiles whose scales are held
-  static constexpr int threads = 384;           // warps: 0-7 softmax, 8 MMA, 9 K, 10 V, 11 idle
+  static constexpr int threads = Q4 ? 512 : 384;  // warps: 0-7 softmax, 8 MMA, 9 K, 10 V, 11 idle; E2M1: 12-15 K and V
   static constexpr int NH = 2 / NQ;             // threads of a row
   static constexpr int HC = TK / NH;            // columns of a thread
-  // registers a thread of a softmax warpgroup and of the others' keeps of the 168 at launch
-  static constexpr int soft = 208, mma = 80;
-  static_assert(2 * soft + mma <= 3 * 168, "more registers than the block has");
+  // registers a thread of a softmax warpgroup and of the others' keeps of what it has at launch
+  static constexpr int soft = Q4 ? 192 : 208, mma = Q4 ? 64 : 80;
+  static constexpr int groups = threads / 128, launch = 65536 / threads / 8 * 8;
+  static_assert(2 * soft + (groups - 2) * mma <= groups * launch, "more registers than the block has");
+  // E2M1: of a warp's 32 lanes, a 16-byte piece of a row's codes each, 2 lanes side by side, 4 rows, the other pieces, rows
+  static constexpr int pieces = D / 32, RW = 32 / pieces, units = Q4 ? TK / (4 * RW) : 1;
+  static constexpr int LAG = Q4 ? (D == 256 ? 2 : 3) : 0;  // K or V tiles of codes on the way
   // powers of two: how far a row's maximum may rise above the one that set the reference, and how far the reference
   // lies below that (f16 weights, whose smallest is 2^-24, take the room up to 2^15; bf16 has the exponents as it is)
   static constexpr float lag = Q8 ? 6.f : 8.f, lift = Q8 ? 9.f : BF16 ? 0.f : 7.f;
@@ -101,19 +105,21 @@ struct Conf {
   static constexpr int O0 = 256;                // O of row block b at O0 + b * D
 };
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool Q4 = false>
 struct Smem {
-  using C = Conf<D, Q8>;
+  using C = Conf<D, Q8, true, Q4>;
   alignas(1024) uint8_t ring[C::NS][C::slot];
   alignas(1024) uint8_t q[C::QT ? 16 : C::M * D * 2];
   // E4M3, by tile and position: K's scale, V's exponent (bounded) and V's scale
   alignas(16) float ks[C::SR][Q8 ? C::TK : 4], ve[C::SR][Q8 ? C::TK : 4], vs[C::SR][Q8 ? C::TK : 4];
-  float up[8][32];        // E4M3, by softmax warp: the power of two of a row of q
+  float up[8][32];        // E4M3, E2M1, by softmax warp: the power of two of a row of q
+  alignas(16) uint4 codes[C::LAG + 1][C::units][Q4 ? 128 : 1];  // E2M1, by producer thread: its pieces, and the words that
+  uint32_t words[C::LAG + 1][C::units][Q4 ? 128 : 1];           // hold their scale bytes
   alignas(16) uint8_t rows[8][32][80];  // by softmax warp: 64 bytes of each of its rows, between TMEM and memory
   int32_t bad[Q8 ? 1 : 3][Q8 ? 1 : D];  // first position whose v is NaN, +inf, -inf
   uint64_t full[C::NS], empty[C::NS], sfull[2], phalf[2], pfull[2], qfull[2], odone[2], fin[2], met, drain;
   uint64_t scaled[C::SR];             // E4M3: a tile's scales are there
-  uint64_t told[2][8][32];      // NH == 2: a half's part of a row's maximum or sum, behind the turn's number
+  uint64_t told[2][8][C::NH == 2 ? 32 : 1];  // NH == 2: a half's part of a row's maximum or sum, behind the turn's number
   uint32_t tmem;
   int32_t any_bad;
   RunScratch run;
@@ -291,15 +297,17 @@ struct Ring {
   }
 };
 
-template <bool BF16, bool Q8, int D>
-__global__ void __launch_bounds__(Conf<D, Q8>::threads, 1)
+// BF16: the products' type (f16 for E2M1 pools).  Q8: E4M3 pools.  Q4: E2M1 pools.
+template <bool BF16, bool Q8, int D, bool Q4>
+__global__ void __launch_bounds__((Conf<D, Q8, BF16, Q4>::threads), 1)
 chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map) {
-  using C = Conf<D, Q8, BF16>;
+  using C = Conf<D, Q8, BF16, Q4>;
   constexpr int NQ = C::NQ, M = C::M, TK = C::TK, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<D, Q8> &sm = *reinterpret_cast<Smem<D, Q8> *>(smem_raw);
+  Smem<D, Q8, Q4> &sm = *reinterpret_cast<Smem<D, Q8, Q4> *>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31;
   const KvLayer &L = p.L;
+  const bool out_bf16 = Q4 ? p.dtype == LSC_BF16 : BF16;
   if (w == 8) {
     tc::tmem_alloc(&sm.tmem, 512);
     tc::tmem_relinquish();
@@ -307,7 +315,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   if (C::NH == 2)
     for (int i = tid; i < 2 * 8 * 32; i += C::threads) (&sm.told[0][0][0])[i] = ~0ull;  // no turn's number
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], 1), mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], Q4 ? 4 : 1), mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < C::SR; ++i) mbar_init(&sm.scaled[i], 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.sfull[i], 1), mbar_init(&sm.phalf[i], 4), mbar_init(&sm.pfull[i], 4 * C::NH), mbar_init(&sm.qfull[i], 4 * C::NH);
@@ -342,7 +350,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     const int partner = w ^ 4;                     // NH == 2: the warp with the other half of the same rows
     const uint32_t lane = (uint32_t)(quad * 32) << 16;
     const Workspace ws = workspace_at(p.ws, ctas, M);
-    float c = p.scale_log2, c_next = c;  // of this thread's row (E4M3: with q's power of two)
+    float c = p.scale_log2, c_next = c;  // of this thread's row (E4M3, E2M1: with q's power of two)
     auto rows_of = [&](const Piece &q) {  // packed rows of the unit
       const int32_t r = q.s.n * p.group - q.block * M;
       return r < M ? r : M;
@@ -371,7 +379,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
       for (int x = 0; x < bytes / 64; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) own[x][i] = load(i, begin + 64 * x);
-      if constexpr (Q8) {
+      float down[4] = {1.f, 1.f, 1.f, 1.f};
+      auto find_powers = [&]() {  // bf16 rows: what a row is multiplied by, and what its scores take back
         uint32_t top[4] = {0, 0, 0, 0};  // magnitudes of bf16 order as whole numbers, two a word
         auto look = [&](int i, const uint4 &y) {
           const uint32_t k = 0x7fff7fffu;
@@ -392,20 +401,45 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         for (int x = 0; x < bytes / 64; ++x)
 #pragma unroll
           for (int i = 0; i < 4; ++i) look(i, own[x][i]);
-        float down[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t t = max(top[i] & 0xffffu, top[i] >> 16);
           t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
           t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
           const uint32_t ex = t >> 7;  // 2^(ex - 127) <= the largest magnitude: brought to 2^7, where both powers are normal
-          const bool plain = ex < 8 || ex == 255;
-          down[i] = plain ? 1.f : __uint_as_float((261 - ex) << 23);
-          // an infinity would become a code of 448: a row that is not finite has NaN for its power
-          if ((ln & 3) == 0) sm.up[w][i * 8 + oct] = ex < 8 ? 1.f : __uint_as_float(ex == 255 ? 0x7fc00000u : (ex - 7) << 23);
+          if constexpr (Q4) {  // to 2^14, the last that f16 has: elements down to 2^-28 of the row's largest keep their bits
+            const bool plain = ex < 16 || ex == 255;
+            down[i] = plain ? 1.f : __uint_as_float((268 - ex) << 23);
+            if ((ln & 3) == 0) sm.up[w][i * 8 + oct] = plain ? 1.f : __uint_as_float((ex - 14) << 23);
+          } else {
+            const bool plain = ex < 8 || ex == 255;
+            down[i] = plain ? 1.f : __uint_as_float((261 - ex) << 23);
+            // an infinity would become a code of 448: a row that is not finite has NaN for its power
+            if ((ln & 3) == 0) sm.up[w][i * 8 + oct] = ex < 8 ? 1.f : __uint_as_float(ex == 255 ? 0x7fc00000u : (ex - 7) << 23);
+          }
         }
         __syncwarp();
         c_next = p.scale_log2 * sm.up[w][ln];
+      };
+      if constexpr (Q4) {
+        if (p.dtype == LSC_BF16) {
+          find_powers();
+          // a score that is hidden is -infinity times this, so it may not be 0; products of q and k are below 2^39
+          c_next = fmaxf(c_next, 0x1p-120f);
+#pragma unroll
+          for (int x = 0; x < bytes / 64; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t in[4] = {own[x][i].x, own[x][i].y, own[x][i].z, own[x][i].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                in[e] = pack2(__uint_as_float(in[e] << 16) * down[i], __uint_as_float(in[e] & 0xffff0000u) * down[i], 0);
+              own[x][i] = make_uint4(in[0], in[1], in[2], in[3]);
+            }
+        }
+      }
+      if constexpr (Q8) {
+        find_powers();
 #pragma unroll
         for (int x = 0; x < bytes; x += 64) {  // 32 elements: 32 bytes of each part
           uint2 part[4][2];
@@ -637,7 +671,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           const uint32_t vi = slots + 2 * j + 1;
           const int slot = (int)(vi % NS);
           if (!(ok = wait_warp(&sm.full[slot], vi / NS, limit))) break;
-          {
+          if (!Q4) {  // E2M1: the producers wrote zeros
             for (int i = half * 128 + row; i < (first + TK - last) * (D / 8); i += 128 * C::NH) {
               const int key = last - first + i / (D / 8), ch = i % (D / 8);
               *(uint4 *)(sm.ring[slot] + (ch >> 3) * (TK * 128) + key * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -737,7 +771,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           uint32_t v[16];
           if (whole) {
 #pragma unroll
-            for (int y = 0; y < 16; ++y) v[y] = pack2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]), BF16);
+            for (int y = 0; y < 16; ++y) v[y] = pack2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]), out_bf16);
             rows_out(v, x * 2);
           } else {
 #pragma unroll
@@ -768,7 +802,89 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma));
   }
-  if (w == 9 || w == 10) {
+  if constexpr (Q4) {
+    if (w >= 12) {
+      // -------------------------------------------------------------- producers, E2M1
+      // A thread has the same 16 bytes of codes (32 elements) in `units` rows of each K and V tile: it copies them, and the
+      // words with their scale bytes, to shared memory of its own (LAG tiles ahead, so no other thread has to be waited
+      // for), and writes them out as f16, whose rows of 4 and pieces side by side meet no bank twice.
+      const int pt = tid - 384, cb = C::pieces == 8 ? 2 : C::pieces == 4 ? 1 : 0, rest = ln >> 3;
+      const int piece = (ln & 1) + 2 * (rest & ((1 << cb) - 1)), row0 = (ln >> 1 & 3) + 4 * (rest >> cb) + C::RW * (w - 12);
+      int slot = 0, pending = 0, in = 0, out = 0;
+      uint32_t phase = 0;
+      int32_t at[C::units], blk[C::units];  // a row's place in its block, -1 behind the last position; the next tile's blocks
+      int64_t page[C::units];
+      const int64_t row_bytes = (int64_t)L.heads * (D / 2), row_scales = (int64_t)L.heads * (D / 16);
+      auto look_up = [&](int j) {  // the blocks of tile j's rows; looked at one tile later
+#pragma unroll
+        for (int u = 0; u < C::units; ++u) {
+          const int32_t pos = (pc.t0 + j) * TK + row0 + 4 * C::RW * u;
+          blk[u] = pos < pc.s.kv ? __ldg(p.b.table + (int64_t)pc.seq * p.b.max_blocks + L.by_block.div(pos)) : 0;
+        }
+      };
+      // the oldest tile on the way, as f16 into the ring
+      auto convert = [&]() {
+        if (!(ok = wait_warp(&sm.empty[slot], phase ^ 1, limit))) return;
+        uint8_t *dst = sm.ring[slot];
+#pragma unroll
+        for (int u = 0; u < C::units; ++u) {
+          const uint4 c = sm.codes[out][u][pt];
+          const uint32_t sw = sm.words[out][u][pt] >> (piece & 1) * 16, w4[4] = {c.x, c.y, c.z, c.w};
+          const int r = row0 + 4 * C::RW * u;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t h[4];
+            e2m1x8_times(w4[x], e2m1_scale2(x < 2 ? sw & 0xffu : sw >> 8 & 0xffu), h);
+            *(uint4 *)(dst + chunk_at<128>(TK, r, piece * 4 + x)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ln == 0) mbar_arrive(&sm.full[slot]);
+        if (++slot == NS) slot = 0, phase ^= 1;
+        if (++out == C::LAG + 1) out = 0;
+        --pending;
+      };
+      while (ok && next_piece<M, TK>(p, run, pc)) {
+        const int nt = pc.t1 - pc.t0;
+        look_up(0);
+        for (int j = 0; j < nt && ok; ++j) {
+#pragma unroll
+          for (int u = 0; u < C::units; ++u) {
+            const int32_t pos = (pc.t0 + j) * TK + row0 + 4 * C::RW * u, r = pos - L.by_block.div(pos) * L.block_tokens;
+            if ((uint32_t)blk[u] >= (uint32_t)L.num_blocks) {
+              report(L.status, LSC_ERR_OUT_OF_RANGE);
+              blk[u] = 0;
+            }
+            at[u] = pos < pc.s.kv ? r : -1;
+            page[u] = (int64_t)blk[u] * L.page;
+          }
+          if (j + 1 < nt) look_up(j + 1);
+#pragma unroll 1
+          for (int lane = 0; lane < 2 && ok; ++lane) {
+            const uint8_t *base = lane ? L.v : L.k;
+#pragma unroll
+            for (int u = 0; u < C::units; ++u) {
+              const bool on = at[u] >= 0;
+              const int64_t r = on ? at[u] : 0;
+              cp_async16_or_zero(smem_u32(&sm.codes[in][u][pt]), base + page[u] + r * row_bytes + pc.head * (D / 2) + piece * 16, on);
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sm.words[in][u][pt])),
+                           "l"(base + page[u] + L.scale_off + r * row_scales + pc.head * (D / 16) + (piece >> 1) * 4), "r"(on ? 4 : 0)
+                           : "memory");
+            }
+            cp_async_commit();
+            if (++in == C::LAG + 1) in = 0;
+            if (++pending > C::LAG) {
+              cp_async_wait<C::LAG>();
+              convert();
+            }
+          }
+        }
+      }
+      cp_async_wait<0>();
+      while (ok && pending > 0) convert();
+    }
+  } else if (w == 9 || w == 10) {
     // ---------------------------------------------------------------- producers
     const bool is_k = w == 9;
     const uint8_t *base = is_k ? L.k : L.v;
@@ -1055,22 +1171,23 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   }
 }
 
-template <bool BF16, bool Q8, int D>
+template <bool BF16, bool Q8, int D, bool Q4>
 cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
   static SmemLimit limit;
-  auto *k = chunk_attend_kernel<BF16, Q8, D>;
-  const int smem = (int)sizeof(Smem<D, Q8>);
+  auto *k = chunk_attend_kernel<BF16, Q8, D, Q4>;
+  const int smem = (int)sizeof(Smem<D, Q8, Q4>);
+  static_assert(sizeof(Smem<D, Q8, Q4>) <= 227 * 1024, "more shared memory than a block has");
   const cudaError_t e = limit.ensure((const void *)k, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, plan.ctas, Conf<D, Q8>::threads, smem, stream, p, p.map ? *p.map : CUtensorMap{});
+  return launch_pdl(k, plan.ctas, Conf<D, Q8, BF16, Q4>::threads, smem, stream, p, p.map ? *p.map : CUtensorMap{});
 }
 
-template <bool BF16, bool Q8>
+template <bool BF16, bool Q8, bool Q4 = false>
 cudaError_t launch_type(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
   switch (p.L.head_dim) {
-    case 64: return launch_one<BF16, Q8, 64>(p, plan, stream);
-    case 128: return launch_one<BF16, Q8, 128>(p, plan, stream);
-    default: return launch_one<BF16, Q8, 256>(p, plan, stream);
+    case 64: return launch_one<BF16, Q8, 64, Q4>(p, plan, stream);
+    case 128: return launch_one<BF16, Q8, 128, Q4>(p, plan, stream);
+    default: return launch_one<BF16, Q8, 256, Q4>(p, plan, stream);
   }
 }
 
@@ -1080,5 +1197,6 @@ cudaError_t launch_type(const KvAttendParams &p, const AttendPlan &plan, cudaStr
 cudaError_t launch_kv_attend_chunk_bf16(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_chunk_f16(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_chunk_e4m3(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
+cudaError_t launch_kv_attend_chunk_e2m1(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 
 }  // namespace lsc
