@@ -319,7 +319,8 @@ typedef struct {
  * scores.  Its lse is not finite.  Positions it does not see, and rows behind a sequence's
  * last token, do not enter, whatever they hold.  Sums and softmax statistics
  * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded before they
- * meet v: to bf16 in bf16 pools; to f16 in f16 and E4M3 pools, in full down to
+ * meet v: to bf16 in bf16 pools, and in E2M1 pools where many rows of BF16 q read them
+ * (there the batch's rows are first made 16 bits wide in the workspace); to f16 in f16, E4M3 and other E2M1 calls, in full down to
  * 2^-21 of a row's largest weight and to a multiple of 2^-31 of it below (E4M3
  * pools, more than 64 rows of q a kv head: to nine significant bits or more down
  * to 2^-17 of it, to a multiple of 2^-25 of it below, and elements of q below 2^-9

@@ -341,6 +341,17 @@ struct KvAttendParams {
   uint64_t drain_limit_ns; // bound of the wait for issued MMAs at the end
   int32_t num_sms;
 };
+// A batch's cached rows of an E2M1 layer at 16 bits, in blocks of kExpandTokens positions (lsc_kv_expand.cu).
+constexpr int kExpandTokens = 128;
+struct KvExpand {
+  uint16_t *k, *v;           // [n_seq * blocks][kExpandTokens][kv heads][head_dim]
+  int32_t *table;            // [n_seq, blocks]
+  int32_t blocks;            // of a sequence
+  int32_t bf16;              // 1: bf16, 0: f16
+  int32_t chunks;            // set by the launch
+  FastDiv by_chunks, by_units;
+};
+cudaError_t launch_kv_expand(const KvAttendParams &p, KvExpand x, cudaStream_t stream);
 // the CUDA-core kernel: every type, head size and alignment (head_dim <= 512)
 cudaError_t launch_kv_attend_any(const KvAttendParams &p, cudaStream_t stream);
 

@@ -20,6 +20,10 @@
 #include "lsc_kv_attend.cuh"
 #include "lsc_kv.h"
 
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
 struct lsc_kv_pool {
   lsc_kv_pool_desc d;
   int device = -1;  // -1: host-only pool (no GPU when created)
@@ -33,6 +37,7 @@ struct lsc_kv_pool {
   int32_t box_rows = 0;         // rows of a TMA box of `maps`
   int32_t box_decode = 0;       // and of `maps_decode`
   std::vector<CUtensorMap> maps, maps_decode;  // per layer; empty: none
+  EncodeTiled encode = nullptr;                // null: no maps to be had
 };
 
 namespace {
@@ -95,42 +100,47 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
 // block: its rows are the largest power of two that divides block_tokens, up to
 // the tile's.  128-byte swizzle (rows of 64 or 32 bytes: 64- or 32-byte).  Without maps (blocks that are
 // no multiple of 8 tokens, other types and sizes) the kernels copy rows themselves.
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-bool encode_maps(const lsc_kv_pool *p, EncodeTiled encode, int tile, int box, std::vector<CUtensorMap> *out) {
-  const lsc_kv_pool_desc &d = p->d;
-  const int row = d.head_dim * (int)p->bits / 8, col = row < 128 ? row : 128;  // bytes
-  const int es = p->bits == 16 ? 2 : 1;  // of the map's elements
-  const CUtensorMapDataType type = es == 1               ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : d.dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+// One region's map: `blocks` pages of each lane, heads of head_dim elements of `bits` bits.
+bool encode_map(EncodeTiled encode, CUtensorMap *map, void *region, int32_t dtype, int bits, int32_t block_tokens,
+                int32_t heads, int32_t head_dim, int64_t page, int64_t blocks, int tile, int box) {
+  const int row = head_dim * bits / 8, col = row < 128 ? row : 128;  // bytes
+  const int es = bits == 16 ? 2 : 1;  // of the map's elements
+  const CUtensorMapDataType type = es == 1             ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == LSC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const CUtensorMapSwizzle swizzle = col == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
                                      : col == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                  : CU_TENSOR_MAP_SWIZZLE_128B;
-  const cuuint64_t dims[5] = {(cuuint64_t)(col / es), (cuuint64_t)d.block_tokens, (cuuint64_t)(row / col),
-                              (cuuint64_t)d.num_kv_heads, 2 * (cuuint64_t)d.num_blocks};
-  const cuuint64_t strides[4] = {(cuuint64_t)p->row_bytes, (cuuint64_t)col, (cuuint64_t)row, (cuuint64_t)d.page_bytes};
+  const cuuint64_t dims[5] = {(cuuint64_t)(col / es), (cuuint64_t)block_tokens, (cuuint64_t)(row / col),
+                              (cuuint64_t)heads, 2 * (cuuint64_t)blocks};
+  const cuuint64_t strides[4] = {(cuuint64_t)heads * row, (cuuint64_t)col, (cuuint64_t)row, (cuuint64_t)page};
   const cuuint32_t boxes[5] = {(cuuint32_t)(col / es), (cuuint32_t)box, box == tile ? (cuuint32_t)(row / col) : 1, 1, 1};
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return encode(map, type, 5, region, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_maps(const lsc_kv_pool *p, EncodeTiled encode, int tile, int box, std::vector<CUtensorMap> *out) {
+  const lsc_kv_pool_desc &d = p->d;
   try {
     out->resize(d.num_layers);
   } catch (...) {
     return false;
   }
   for (int32_t l = 0; l < d.num_layers; ++l)
-    if (encode(&(*out)[l], type, 5, p->base + (int64_t)l * p->region_bytes, dims, strides, boxes, ones,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (!encode_map(encode, &(*out)[l], p->base + (int64_t)l * p->region_bytes, d.dtype, (int)p->bits, d.block_tokens,
+                    d.num_kv_heads, d.head_dim, d.page_bytes, d.num_blocks, tile, box))
       return false;
   return true;
 }
 
+// Positions of a chunk kernel's tile.
+int chunk_tile(int head_dim) { return head_dim == 256 ? 64 : 128; }
+
 void make_maps(lsc_kv_pool *p) {
   const lsc_kv_pool_desc &d = p->d;
   const int D = d.head_dim, most = d.block_tokens & -d.block_tokens;
-  if (d.dtype == LSC_F32 || (D != 64 && D != 128 && D != 256) || most < 8) return;  // a swizzle pattern is 8 rows
+  if (d.dtype == LSC_F32 || (D != 64 && D != 128 && D != 256)) return;
   void *fn = nullptr;
   cudaDriverEntryPointQueryResult found;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
@@ -138,11 +148,13 @@ void make_maps(lsc_kv_pool *p) {
     cudaGetLastError();
     return;
   }
-  const int tile = D == 256 ? 64 : 128, keys = lsc::kv_decode_keys(D, (int)p->bits);
+  p->encode = (EncodeTiled)fn;
+  if (most < 8) return;  // a swizzle pattern is 8 rows
+  const int tile = chunk_tile(D), keys = lsc::kv_decode_keys(D, (int)p->bits);
   const int box = std::min(most, tile), box_decode = std::min(most, keys);
   std::vector<CUtensorMap> maps, decode;
-  if ((d.dtype != LSC_E2M1 && !encode_maps(p, (EncodeTiled)fn, tile, box, &maps)) ||  // E2M1: decode alone takes boxes
-      !encode_maps(p, (EncodeTiled)fn, keys, box_decode, &decode))
+  if ((d.dtype != LSC_E2M1 && !encode_maps(p, p->encode, tile, box, &maps)) ||  // E2M1: decode alone takes boxes
+      !encode_maps(p, p->encode, keys, box_decode, &decode))
     return;
   p->maps.swap(maps);
   p->maps_decode.swap(decode);
@@ -377,10 +389,65 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   return kAny;
 }
 
+// E2M1 chunks of many row blocks: the batch's rows are first made 16 bits wide in the workspace (lsc_kv_expand.cu) and
+// the 16-bit chunk kernels take them.  The host knows the sequences' row blocks on average and the workspace by the
+// bounds of the lengths; beyond kExpandMost bytes of it, and below kExpandBlocks blocks, the E2M1 chunk kernel converts
+// each tile it meets.
+constexpr int64_t kExpandBlocks = 4;
+constexpr int64_t kExpandMost = (int64_t)4 << 30;
+
+int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
+
+// Bytes for n_seq sequences.
+int64_t expand_bytes(const lsc::KvAttendParams &r, int64_t n_seq) {
+  const int64_t blocks = n_seq * (((int64_t)r.max_kv + lsc::kExpandTokens - 1) / lsc::kExpandTokens);
+  const int64_t row = (int64_t)r.L.heads * r.L.head_dim * 2, most = kExpandMost + 1;
+  if (blocks > most / (lsc::kExpandTokens * 2) / row) return most;
+  return up16(blocks * 4) + 2 * blocks * lsc::kExpandTokens * row;
+}
+
+// Sequences that the step's rows fill with kExpandBlocks row blocks each.
+int64_t expand_seqs(const lsc::KvAttendParams &r, int M) { return (int64_t)r.b.total_tokens * r.group / (M * kExpandBlocks); }
+
+bool expands(const lsc_kv_pool *p, const lsc::KvAttendParams &r, const lsc::AttendPlan &plan) {
+  return r.L.dtype == LSC_E2M1 && p->encode && r.max_kv > 0 && r.b.n_seq <= expand_seqs(r, plan.M) &&
+         expand_bytes(r, r.b.n_seq) <= kExpandMost;
+}
+
+// The step's layer and batch as the 16-bit chunk kernels see them, over `space`; map receives its TMA map.
+bool expand_layer(const lsc_kv_pool *p, uint8_t *space, lsc::KvAttendParams *r, lsc::KvExpand *x, CUtensorMap *map) {
+  lsc::KvLayer &L = r->L;
+  const int32_t blocks = (r->max_kv + lsc::kExpandTokens - 1) / lsc::kExpandTokens;
+  const int64_t all = (int64_t)r->b.n_seq * blocks, page = (int64_t)lsc::kExpandTokens * L.heads * L.head_dim * 2;
+  *x = lsc::KvExpand{};
+  x->table = (int32_t *)space;
+  x->k = (uint16_t *)(space + up16(all * 4));
+  x->v = (uint16_t *)((uint8_t *)x->k + all * page);
+  x->blocks = blocks;
+  x->bf16 = r->dtype == LSC_BF16;
+  const int tile = chunk_tile(L.head_dim);
+  if (!encode_map(p->encode, map, x->k, r->dtype, 16, lsc::kExpandTokens, L.heads, L.head_dim, page, all, tile, tile))
+    return false;
+  L.k = (uint8_t *)x->k;
+  L.v = (uint8_t *)x->v;
+  L.page = page;
+  L.num_blocks = (int32_t)all;
+  L.block_tokens = lsc::kExpandTokens;
+  L.dtype = r->dtype;
+  L.scale_off = 0;
+  L.by_block.set(lsc::kExpandTokens);
+  r->b.table = x->table;
+  r->b.max_blocks = blocks;
+  r->b.held = (int32_t)std::min<int64_t>((int64_t)blocks * lsc::kExpandTokens, LSC_KV_MAX_TOKENS);
+  r->map = map;
+  r->box_rows = tile;
+  return true;
+}
+
 // What every call of these sizes or smaller ones needs: the most over the forms that one of them may take, each at its
 // largest sizes.  A form's need grows with every size; for decode with and without heads side by side, which smaller
 // sizes may do without.
-size_t attend_workspace(lsc::KvAttendParams r) {
+size_t attend_workspace(const lsc_kv_pool *p, lsc::KvAttendParams r) {
   if (!tensor_core_types(r)) return 0;
   const bool q8 = r.L.dtype == LSC_E4M3, q4 = r.L.dtype == LSC_E2M1;
   const int32_t max_seq = r.max_seq, few = q8 ? kRowsMost : kDecodeMost;
@@ -394,7 +461,14 @@ size_t attend_workspace(lsc::KvAttendParams r) {
   if ((q8 || r.box_decode == 0) && !q4 && rows_up_to(few)) most = std::max(most, lsc::plan_kv_attend_rows(r).ws_bytes);
   r.max_seq = max_seq;
   if (((int64_t)max_seq * r.group > few && !(q8 && r.dtype != LSC_BF16)) || (q4 && r.box_decode == 0))
-    most = std::max(most, lsc::plan_kv_attend_chunk(r).ws_bytes);
+  {
+    const lsc::AttendPlan plan = lsc::plan_kv_attend_chunk(r);
+    most = std::max(most, plan.ws_bytes);
+    if (q4 && p->encode && r.max_kv > 0) {  // the rows of fewer sequences, or of shorter ones, may be just within what is allowed
+      const int64_t seqs = std::min<int64_t>(r.b.n_seq, expand_seqs(r, plan.M));
+      if (seqs > 0) most = up16(most) + std::min(expand_bytes(r, seqs), kExpandMost);
+    }
+  }
   return most;
 }
 
@@ -681,7 +755,7 @@ int lsc_kv_attend_workspace_bytes(const lsc_kv_pool *p, const lsc_kv_attend_args
   const int rc = check_attend(p, 0, a, &r);
   if (rc != LSC_OK) return rc;
   if (p->device < 0) return LSC_ERR_CUDA;  // host-only pool: the need depends on the device
-  *bytes = r.b.n_seq == 0 || r.b.total_tokens == 0 ? 0 : attend_workspace(r);
+  *bytes = r.b.n_seq == 0 || r.b.total_tokens == 0 ? 0 : attend_workspace(p, r);
   return LSC_OK;
 }
 
@@ -697,24 +771,34 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
   const Form form = attend_form(r, &plan);
   cudaStream_t s = (cudaStream_t)stream;
   void *ws = a->workspace;
-  if (plan.ws_bytes > 0) {
-    if (ws && a->workspace_bytes < attend_workspace(r)) return LSC_ERR_INVALID_ARG;
-    if (!ws && cudaMallocAsync(&ws, plan.ws_bytes, s) != cudaSuccess) {
+  const bool expand = form == kChunk && expands(p, r, plan);
+  const size_t parts = expand ? up16(plan.ws_bytes) : plan.ws_bytes, need = parts + (expand ? expand_bytes(r, r.b.n_seq) : 0);
+  if (need > 0) {
+    if (ws && a->workspace_bytes < attend_workspace(p, r)) return LSC_ERR_INVALID_ARG;
+    if (!ws && cudaMallocAsync(&ws, need, s) != cudaSuccess) {
       cudaGetLastError();
       return LSC_ERR_NO_MEMORY;
     }
-    r.ws = (uint8_t *)ws;
   }
+  if (plan.ws_bytes > 0) r.ws = (uint8_t *)ws;
   r.whole = !plan.may_cut;
   r.min_run = plan.min_run;
   r.lead = plan.lead;
   r.groups = r.L.heads / std::max(plan.together, 1);
-  cudaError_t e = form == kAny    ? lsc::launch_kv_attend_any(r, s)
-                  : form == kDecode ? lsc::launch_kv_attend_decode(r, plan, s)
-                  : form == kRows ? lsc::launch_kv_attend_rows(r, plan, s)
-                                  : lsc::launch_kv_attend_chunk(r, plan, s);
+  cudaError_t e = cudaSuccess;
+  CUtensorMap map;
+  if (expand) {
+    const lsc::KvAttendParams held = r;
+    lsc::KvExpand x;
+    e = expand_layer(p, (uint8_t *)ws + parts, &r, &x, &map) ? lsc::launch_kv_expand(held, x, s) : cudaErrorUnknown;
+  }
+  if (e == cudaSuccess)
+    e = form == kAny      ? lsc::launch_kv_attend_any(r, s)
+        : form == kDecode ? lsc::launch_kv_attend_decode(r, plan, s)
+        : form == kRows   ? lsc::launch_kv_attend_rows(r, plan, s)
+                          : lsc::launch_kv_attend_chunk(r, plan, s);
   if (e == cudaSuccess && plan.may_cut) e = lsc::launch_kv_attend_join(r, plan, s);
-  if (plan.ws_bytes > 0 && !a->workspace && cudaFreeAsync(ws, s) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
+  if (need > 0 && !a->workspace && cudaFreeAsync(ws, s) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
   if (e != cudaSuccess) {
     cudaGetLastError();
     return LSC_ERR_CUDA;

@@ -84,18 +84,22 @@ struct Conf {
   static constexpr int ES = Q8 ? 1 : 2;         // bytes of an element
   static constexpr int row = D * ES, line = row < 128 ? row : 128;  // bytes of a row, of a swizzled line of it
   static constexpr int slot = TK * row;         // bytes of a K or V tile
-  static constexpr int NS = Q8 ? (D == 128 ? 6 : 8) : Q4 ? (D == 64 ? 8 : D == 128 ? 3 : 5) : (D == 64 ? 8 : D == 128 ? 4 : 6);
+  static constexpr int NS = Q8 ? (D == 128 ? 6 : 8) : Q4 ? (D == 64 ? 8 : D == 128 ? 3 : 4) : (D == 64 ? 8 : D == 128 ? 4 : 6);
   static constexpr int SR = Q8 ? 8 : 1;         // E4M3: tiles whose scales are held
-  static constexpr int threads = Q4 ? 512 : 384;  // warps: 0-7 softmax, 8 MMA, 9 K, 10 V, 11 idle; E2M1: 12-15 K and V
+  // warps: 0-7 softmax, 8 MMA, 9 K, 10 V, 11 idle; E2M1: K 12-15, V 9-11, or, with one row block, whose softmax does with
+  // fewer registers, 16-19
+  static constexpr int threads = !Q4 ? 384 : NQ == 2 ? 512 : 640;
   static constexpr int NH = 2 / NQ;             // threads of a row
   static constexpr int HC = TK / NH;            // columns of a thread
   // registers a thread of a softmax warpgroup and of the others' keeps of what it has at launch
-  static constexpr int soft = Q4 ? 192 : 208, mma = Q4 ? 64 : 80;
+  static constexpr int soft = !Q4 ? 208 : NQ == 2 ? 192 : 128, mma = !Q4 ? 80 : NQ == 2 ? 64 : 72;
   static constexpr int groups = threads / 128, launch = 65536 / threads / 8 * 8;
   static_assert(2 * soft + (groups - 2) * mma <= groups * launch, "more registers than the block has");
   // E2M1: of a warp's 32 lanes, a 16-byte piece of a row's codes each, 2 lanes side by side, 4 rows, the other pieces, rows
-  static constexpr int pieces = D / 32, RW = 32 / pieces, units = Q4 ? TK / (4 * RW) : 1;
-  static constexpr int LAG = Q4 ? (D == 256 ? 2 : 3) : 0;  // K or V tiles of codes on the way
+  static constexpr int pieces = D / 32, RW = 32 / pieces;
+  static constexpr int VW = NQ == 2 ? 3 : 4, v_warp = NQ == 2 ? 9 : 16;            // V's warps (K: 4, from 12)
+  static constexpr int k_units = Q4 ? TK / (4 * RW) : 1, v_units = Q4 ? (TK / RW + VW - 1) / VW : 1;
+  static constexpr int LAG = !Q4 ? 0 : D == 128 ? 1 : 2;  // K and V tiles of codes on the way
   // powers of two: how far a row's maximum may rise above the one that set the reference, and how far the reference
   // lies below that (f16 weights, whose smallest is 2^-24, take the room up to 2^15; bf16 has the exponents as it is)
   static constexpr float lag = Q8 ? 6.f : 8.f, lift = Q8 ? 9.f : BF16 ? 0.f : 7.f;
@@ -113,8 +117,9 @@ struct Smem {
   // E4M3, by tile and position: K's scale, V's exponent (bounded) and V's scale
   alignas(16) float ks[C::SR][Q8 ? C::TK : 4], ve[C::SR][Q8 ? C::TK : 4], vs[C::SR][Q8 ? C::TK : 4];
   float up[8][32];        // E4M3, E2M1, by softmax warp: the power of two of a row of q
-  alignas(16) uint4 codes[C::LAG + 1][C::units][Q4 ? 128 : 1];  // E2M1, by producer thread: its pieces, and the words that
-  uint32_t words[C::LAG + 1][C::units][Q4 ? 128 : 1];           // hold their scale bytes
+  // E2M1, by producer thread: its pieces, and the words that hold their scale bytes
+  alignas(16) uint4 kcodes[C::LAG + 1][C::k_units][Q4 ? 128 : 1], vcodes[C::LAG + 1][C::v_units][Q4 ? C::VW * 32 : 1];
+  uint32_t kwords[C::LAG + 1][C::k_units][Q4 ? 128 : 1], vwords[C::LAG + 1][C::v_units][Q4 ? C::VW * 32 : 1];
   alignas(16) uint8_t rows[8][32][80];  // by softmax warp: 64 bytes of each of its rows, between TMEM and memory
   int32_t bad[Q8 ? 1 : 3][Q8 ? 1 : D];  // first position whose v is NaN, +inf, -inf
   uint64_t full[C::NS], empty[C::NS], sfull[2], phalf[2], pfull[2], qfull[2], odone[2], fin[2], met, drain;
@@ -295,6 +300,11 @@ struct Ring {
     slot += 2;
     if (slot >= NS) slot -= NS, phase ^= 1;
   }
+};
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
 };
 
 // BF16: the products' type (f16 for E2M1 pools).  Q8: E4M3 pools.  Q4: E2M1 pools.
@@ -803,87 +813,91 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma));
   }
   if constexpr (Q4) {
-    if (w >= 12) {
-      // -------------------------------------------------------------- producers, E2M1
-      // A thread has the same 16 bytes of codes (32 elements) in `units` rows of each K and V tile: it copies them, and the
-      // words with their scale bytes, to shared memory of its own (LAG tiles ahead, so no other thread has to be waited
-      // for), and writes them out as f16, whose rows of 4 and pieces side by side meet no bank twice.
-      const int pt = tid - 384, cb = C::pieces == 8 ? 2 : C::pieces == 4 ? 1 : 0, rest = ln >> 3;
-      const int piece = (ln & 1) + 2 * (rest & ((1 << cb) - 1)), row0 = (ln >> 1 & 3) + 4 * (rest >> cb) + C::RW * (w - 12);
-      int slot = 0, pending = 0, in = 0, out = 0;
-      uint32_t phase = 0;
-      int32_t at[C::units], blk[C::units];  // a row's place in its block, -1 behind the last position; the next tile's blocks
-      int64_t page[C::units];
-      const int64_t row_bytes = (int64_t)L.heads * (D / 2), row_scales = (int64_t)L.heads * (D / 16);
-      auto look_up = [&](int j) {  // the blocks of tile j's rows; looked at one tile later
+    // -------------------------------------------------------------- producers, E2M1
+    // A thread has the same 16 bytes of codes (32 elements) in some rows of each K or V tile: it copies them, and the
+    // words with their scale bytes, to shared memory of its own (LAG tiles ahead, so no other thread has to be waited
+    // for), and writes them out as f16; 4 rows and two pieces side by side an instruction, which meet no bank twice.
+    auto produce = [&](auto units_c, auto &codes, auto &words, const uint8_t *base, int first_slot, int wi, auto warps_c) {
+      constexpr int U = decltype(units_c)::value, W = decltype(warps_c)::value;
+      constexpr int cb = C::pieces == 8 ? 2 : C::pieces == 4 ? 1 : 0;
+      const int pt = wi * 32 + ln, rest = ln >> 3;
+      const int piece = (ln & 1) + 2 * (rest & ((1 << cb) - 1)), row0 = (ln >> 1 & 3) + 4 * (rest >> cb) + C::RW * wi;
+      auto row_of = [&](int u) { return row0 + C::RW * W * u; };
+      auto has = [&](int u) { return TK % (C::RW * W) == 0 || u < U - 1 || row_of(u) < TK; };  // the same in a warp
+      Ring<NS> at(first_slot);
+      int pending = 0, in = 0, out = 0;
+      int32_t blk[U];  // of the next tile's rows; looked at a tile later
+      auto look_up = [&](int j) {
 #pragma unroll
-        for (int u = 0; u < C::units; ++u) {
-          const int32_t pos = (pc.t0 + j) * TK + row0 + 4 * C::RW * u;
+        for (int u = 0; u < U; ++u) {
+          const int32_t pos = (pc.t0 + j) * TK + row_of(u);
           blk[u] = pos < pc.s.kv ? __ldg(p.b.table + (int64_t)pc.seq * p.b.max_blocks + L.by_block.div(pos)) : 0;
         }
       };
       // the oldest tile on the way, as f16 into the ring
       auto convert = [&]() {
-        if (!(ok = wait_warp(&sm.empty[slot], phase ^ 1, limit))) return;
-        uint8_t *dst = sm.ring[slot];
+        // all loads before the first store, which they could not pass
+        uint4 c[U];
+        uint32_t sc[U];
 #pragma unroll
-        for (int u = 0; u < C::units; ++u) {
-          const uint4 c = sm.codes[out][u][pt];
-          const uint32_t sw = sm.words[out][u][pt] >> (piece & 1) * 16, w4[4] = {c.x, c.y, c.z, c.w};
-          const int r = row0 + 4 * C::RW * u;
+        for (int u = 0; u < U; ++u) c[u] = codes[out][u][pt], sc[u] = words[out][u][pt];
+        if (!(ok = wait_warp(&sm.empty[at.slot], at.phase ^ 1, limit))) return;
+        uint8_t *dst = sm.ring[at.slot];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (!has(u)) break;
+          const uint32_t sw = sc[u] >> (piece & 1) * 16, w4[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t h[4];
             e2m1x8_times(w4[x], e2m1_scale2(x < 2 ? sw & 0xffu : sw >> 8 & 0xffu), h);
-            *(uint4 *)(dst + chunk_at<128>(TK, r, piece * 4 + x)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *(uint4 *)(dst + chunk_at<128>(TK, row_of(u), piece * 4 + x)) = make_uint4(h[0], h[1], h[2], h[3]);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (ln == 0) mbar_arrive(&sm.full[slot]);
-        if (++slot == NS) slot = 0, phase ^= 1;
+        if (ln < (W == 3 && wi == 0 ? 2 : 1)) mbar_arrive(&sm.full[at.slot]);  // four in all
+        at.step();
         if (++out == C::LAG + 1) out = 0;
         --pending;
       };
       while (ok && next_piece<M, TK>(p, run, pc)) {
         const int nt = pc.t1 - pc.t0;
+        const uint8_t *from = base + pc.head * (D / 2) + piece * 16;
+        const uint8_t *scales = base + L.scale_off + pc.head * (D / 16) + (piece >> 1) * 4;
+        const int32_t row_bytes = L.heads * (D / 2), row_scales = L.heads * (D / 16);  // a block is below 2 GiB
         look_up(0);
         for (int j = 0; j < nt && ok; ++j) {
 #pragma unroll
-          for (int u = 0; u < C::units; ++u) {
-            const int32_t pos = (pc.t0 + j) * TK + row0 + 4 * C::RW * u, r = pos - L.by_block.div(pos) * L.block_tokens;
+          for (int u = 0; u < U; ++u) {
+            if (!has(u)) break;
+            const int32_t pos = (pc.t0 + j) * TK + row_of(u), r = pos - L.by_block.div(pos) * L.block_tokens;
             if ((uint32_t)blk[u] >= (uint32_t)L.num_blocks) {
               report(L.status, LSC_ERR_OUT_OF_RANGE);
               blk[u] = 0;
             }
-            at[u] = pos < pc.s.kv ? r : -1;
-            page[u] = (int64_t)blk[u] * L.page;
+            const bool on = pos < pc.s.kv;
+            const int64_t page = on ? (int64_t)blk[u] * L.page : 0;
+            const int32_t row = on ? r : 0;
+            cp_async16_or_zero(smem_u32(&codes[in][u][pt]), from + page + row * row_bytes, on);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&words[in][u][pt])),
+                         "l"(scales + page + row * row_scales), "r"(on ? 4 : 0)
+                         : "memory");
           }
+          cp_async_commit();
           if (j + 1 < nt) look_up(j + 1);
-#pragma unroll 1
-          for (int lane = 0; lane < 2 && ok; ++lane) {
-            const uint8_t *base = lane ? L.v : L.k;
-#pragma unroll
-            for (int u = 0; u < C::units; ++u) {
-              const bool on = at[u] >= 0;
-              const int64_t r = on ? at[u] : 0;
-              cp_async16_or_zero(smem_u32(&sm.codes[in][u][pt]), base + page[u] + r * row_bytes + pc.head * (D / 2) + piece * 16, on);
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sm.words[in][u][pt])),
-                           "l"(base + page[u] + L.scale_off + r * row_scales + pc.head * (D / 16) + (piece >> 1) * 4), "r"(on ? 4 : 0)
-                           : "memory");
-            }
-            cp_async_commit();
-            if (++in == C::LAG + 1) in = 0;
-            if (++pending > C::LAG) {
-              cp_async_wait<C::LAG>();
-              convert();
-            }
+          if (++in == C::LAG + 1) in = 0;
+          if (++pending > C::LAG) {
+            cp_async_wait<C::LAG>();
+            convert();
           }
         }
       }
       cp_async_wait<0>();
       while (ok && pending > 0) convert();
-    }
+    };
+    if (w >= 12 && w < 16) produce(Int<C::k_units>{}, sm.kcodes, sm.kwords, L.k, 0, w - 12, Int<4>{});
+    else if (w >= C::v_warp && w < C::v_warp + C::VW) produce(Int<C::v_units>{}, sm.vcodes, sm.vwords, L.v, 1, w - C::v_warp, Int<C::VW>{});
   } else if (w == 9 || w == 10) {
     // ---------------------------------------------------------------- producers
     const bool is_k = w == 9;

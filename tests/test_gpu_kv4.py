@@ -2,12 +2,10 @@
 plain 64-bit forms (tests/_kv4.py, tests/_kv.py).
 
 Tolerances.  append, gather and copy_prefix: equal bits (an element has 6 significant bits, so every float type holds
-it).  attend: test_gpu_kv_step.py's bound, with one change: with 16-bit q the products and the weights are f16
-whatever q's type, so a weight is off by 2^-11 of itself, which is within what that bound allows for either type.  q's
-rows are brought to f16 by a power of two: elements keep their bits down to 2^-14 of their row's largest and are off by
-2^-25 of it below, so a score is off by D 2^-25 of largest q times largest k at most; against `reach`, D 2^-23 times
-the sum of |q k|, which is at least the largest q times the k beside it, that fits as long as that k is 2^-2 of the
-row's largest or more; the bound of these tests adds it in full (`q_tail`).
+it).  attend: test_gpu_kv_step.py's bound.  Its weights are rounded to q's type at worst: f16 with f16 q, and with bf16
+q f16 (half a step, 2^-11) or, where many rows of q read the rows at 16 bits, bf16 (half a step of 8 bits, 2^-8).  Where
+they are f16, bf16 rows of q are brought to f16 by a power of two: elements keep their bits down to 2^-14 of their row's
+largest and are off by 2^-25 of it below, so a score is off by D 2^-25 of largest q times largest k at most (`q_tail`).
 """
 import numpy as np
 import pytest
@@ -217,7 +215,7 @@ def check4(host, layer, b, qx, dtype, scale, causal, out, ls, rows=None):
                                             for i in range(len(b.n))])), initial=0)
     q_tail = 0 if dtype == F32 else D * 2.0 ** -25 * np.abs(qx).max(-1) * kmax * scale
     es = D * 2.0 ** -23 * reach + q_tail
-    weight = 0.0 if dtype == F32 else HALF[F16]
+    weight = 0.0 if dtype == F32 else HALF[dtype]
     rel = weight + 2 * es + (N + 8) * 2.0 ** -23 + 2.0 ** -20
     tail = N * 2.0 ** -32 * vmax if dtype != F32 else 0 * vmax  # f16 weights: multiples of 2^-24 beside 2^7 or more
     bound = rel[..., None] * mass + tail[..., None] + HALF[dtype] * (np.abs(want) + rel[..., None] * mass) + 1e-30
