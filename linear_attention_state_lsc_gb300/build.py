@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblsc.so")
 SOURCES = ["lsc_host.cu", "lsc_copy.cu", "lsc_gdn.cu", "lsc_rec128.cu", "lsc_chunked_tc.cu", "lsc_chunk_prep.cu", "lsc_noalloc.cu", "lsc_decode_f32.cu", "lsc_decode_bf16.cu",
-           "lsc_prefill.cu", "lsc_kv.cu", "lsc_kv_rows.cu", "lsc_kv_rotary.cu", "lsc_kv_expand.cu", "lsc_kv_attend_any.cu", "lsc_kv_attend_join.cu",
+           "lsc_prefill.cu", "lsc_kv.cu", "lsc_kv_rows.cu", "lsc_kv_rotary.cu", "lsc_kv_rows4.cu", "lsc_kv_attend_any.cu", "lsc_kv_attend_join.cu",
            "lsc_kv_attend_decode_bf16.cu", "lsc_kv_attend_decode_f16.cu", "lsc_kv_attend_decode_e4m3.cu", "lsc_kv_attend_decode_e2m1.cu",
            "lsc_kv_attend_rows_bf16.cu", "lsc_kv_attend_rows_f16.cu", "lsc_kv_attend_rows_e4m3.cu",
            "lsc_kv_attend_chunk_bf16.cu", "lsc_kv_attend_chunk_f16.cu", "lsc_kv_attend_chunk_e4m3.cu", "lsc_kv_attend_chunk_e2m1.cu", "lsc_prefix_cache.cpp", "lsc_store.cpp"]

@@ -290,6 +290,9 @@ struct KvRowsParams {
 };
 cudaError_t launch_kv_append(const KvRowsParams &p, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_gather(const KvRowsParams &p, int num_sms, cudaStream_t stream);
+// E2M1 pools, dense rows aligned to 16 bytes
+cudaError_t launch_kv_append4(const KvRowsParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_gather4(const KvRowsParams &p, int num_sms, cudaStream_t stream);
 
 // Rotary positions: a pair's angle is positions[axis * axis_stride + t] * turns 2^-64 whole turns.
 constexpr int kRotaryPairs = 256;
@@ -341,15 +344,14 @@ struct KvAttendParams {
   uint64_t drain_limit_ns; // bound of the wait for issued MMAs at the end
   int32_t num_sms;
 };
-// A batch's cached rows of an E2M1 layer at 16 bits, in blocks of kExpandTokens positions (lsc_kv_expand.cu).
+// A batch's cached rows of an E2M1 layer at 16 bits, in blocks of kExpandTokens positions (lsc_kv_rows4.cu).
 constexpr int kExpandTokens = 128;
 struct KvExpand {
   uint16_t *k, *v;           // [n_seq * blocks][kExpandTokens][kv heads][head_dim]
   int32_t *table;            // [n_seq, blocks]
   int32_t blocks;            // of a sequence
-  int32_t bf16;              // 1: bf16, 0: f16
   int32_t chunks;            // set by the launch
-  FastDiv by_chunks, by_units;
+  FastDiv by_chunks;
 };
 cudaError_t launch_kv_expand(const KvAttendParams &p, KvExpand x, cudaStream_t stream);
 // the CUDA-core kernel: every type, head size and alignment (head_dim <= 512)

@@ -76,6 +76,7 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
   g->d = *d;
   g->bits = bits;
   const int64_t elements = (int64_t)d->num_kv_heads * d->head_dim;
+  if (bits == 4 && elements > INT32_MAX) return LSC_ERR_LAYOUT;
   g->row_bytes = bits == 4 ? elements / 2 : elements * (bits / 8);
   g->payload = g->row_bytes * d->block_tokens;
   if (bits <= 8) {  // codes, then one scale byte per (row, head), or per 16 elements of it, at the next 16 B boundary
@@ -389,7 +390,7 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   return kAny;
 }
 
-// E2M1 chunks of many row blocks: the batch's rows are first made 16 bits wide in the workspace (lsc_kv_expand.cu) and
+// E2M1 chunks of many row blocks: the batch's rows are first made 16 bits wide in the workspace (lsc_kv_rows4.cu) and
 // the 16-bit chunk kernels take them.  The host knows the sequences' row blocks on average and the workspace by the
 // bounds of the lengths; beyond kExpandMost bytes of it, and below kExpandBlocks blocks, the E2M1 chunk kernel converts
 // each tile it meets.
@@ -424,7 +425,6 @@ bool expand_layer(const lsc_kv_pool *p, uint8_t *space, lsc::KvAttendParams *r, 
   x->k = (uint16_t *)(space + up16(all * 4));
   x->v = (uint16_t *)((uint8_t *)x->k + all * page);
   x->blocks = blocks;
-  x->bf16 = r->dtype == LSC_BF16;
   const int tile = chunk_tile(L.head_dim);
   if (!encode_map(p->encode, map, x->k, r->dtype, 16, lsc::kExpandTokens, L.heads, L.head_dim, page, all, tile, tile))
     return false;

@@ -151,22 +151,33 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
   return r;
 }
 
-// What an element x over its scale s is rounded from, r = 1 / s.  x r is off by less than 2^-22 of itself; rounded to 20
-// bits, a quotient that is a tie (three bits) becomes that tie again.  Elements of 16-bit types have 11 bits and scales
-// 4: a quotient that is no tie is 2^-12 or more away from each, so that is enough.  With 32 bits (FULL) a quotient may
-// be nearer to a tie than that: then the sign of x - tie s, exact in one fma, moves it to the right side.
-template <bool FULL>
-__device__ __forceinline__ float e2m1_quotient(float x, float s, float r) {
+// Two values as the operand of the packed instructions, which do two lanes' worth a cycle.
+__device__ __forceinline__ uint64_t f32x2(float x, float y) {
+  return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
+}
+
+// What elements x over their scale s are rounded from, r = 1 / s.  x r is off by less than 2^-22 of itself; an element
+// of a 16-bit type has 11 bits and a scale 4, so a quotient that is no tie is 2^-11 or more of a tie away from it.
+// 96 + x r is rounded to 2^-17, which brings the others back to their ties exactly (below 8; the largest scale's
+// quotients may be larger, all of them 6), and 96 off again.
+__device__ __forceinline__ void e2m1_quotients(float x0, float x1, float r, float &y0, float &y1) {
+  uint64_t t;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(f32x2(x0, x1)), "l"(f32x2(r, r)), "l"(f32x2(96.f, 96.f)));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(t), "l"(f32x2(-96.f, -96.f)));
+  y0 = __uint_as_float((uint32_t)t | (__float_as_uint(x0) & 0x80000000u));  // a zero keeps its sign
+  y1 = __uint_as_float((uint32_t)(t >> 32) | (__float_as_uint(x1) & 0x80000000u));
+}
+// With 32 bits a quotient may be nearer to a tie than x r is exact: rounded to 20 bits it is that tie, and the sign of
+// x - tie s, exact in one fma, moves it to the right side.
+__device__ __forceinline__ float e2m1_quotient32(float x, float s, float r) {
   const float a = fabsf(x);
   uint32_t t = (__float_as_uint(a * r) + 4) & ~7u;
-  if constexpr (FULL) {
-    const float d = __fmaf_rn(-__uint_as_float(t), s, a);
-    t += (d > 0.f ? 1 : 0) - (d < 0.f ? 1 : 0);
-  }
+  const float d = __fmaf_rn(-__uint_as_float(t), s, a);
+  t += (d > 0.f ? 1 : 0) - (d < 0.f ? 1 : 0);
   return __uint_as_float(t | (__float_as_uint(x) & 0x80000000u));
 }
 
-// 16 elements with their scale byte -> 64 bits of codes.
+// 16 elements with their scale byte -> 64 bits of codes.  FULL: they may have more than 11 bits.
 template <bool FULL>
 __device__ __forceinline__ uint2 to_e2m1x16(const float (&x)[16], uint32_t byte) {
   if (byte == 0 || byte == 255) return make_uint2(0, 0);
@@ -176,8 +187,13 @@ __device__ __forceinline__ uint2 to_e2m1x16(const float (&x)[16], uint32_t byte)
   for (int h = 0; h < 2; ++h) {
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = to_e2m1x2(e2m1_quotient<FULL>(x[8 * h + 2 * i], s, r), e2m1_quotient<FULL>(x[8 * h + 2 * i + 1], s, r));
+    for (int i = 0; i < 4; ++i) {
+      const float x0 = x[8 * h + 2 * i], x1 = x[8 * h + 2 * i + 1];
+      float y0, y1;
+      if constexpr (FULL) y0 = e2m1_quotient32(x0, s, r), y1 = e2m1_quotient32(x1, s, r);
+      else e2m1_quotients(x0, x1, r, y0, y1);
+      c[i] = to_e2m1x2(y0, y1);
+    }
     w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
   }
   return make_uint2(w[0], w[1]);

@@ -58,8 +58,7 @@ __global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(cons
   const int groups = kThreads / lanes, g = threadIdx.x / lanes, sub = threadIdx.x & (lanes - 1);
   const bool on = sub * EV < L.head_dim;
   const int rows = n * 2 * L.heads;
-  const int64_t head_bytes = held<P>(L.head_dim);
-  const int scales = L.head_dim / 16;  // E2M1: of a head's row
+  const int64_t head_bytes = (int64_t)L.head_dim * kSize<P>;
   // Row r of the run is head r % heads of lane (r / heads) % 2 (K, V) of token r / (2 heads); a group's rows are `groups`
   // apart, so its walk steps by a whole number of tokens and a rest.
   const int per = 2 * L.heads, step_i = groups / per, step_w = groups - step_i * per;
@@ -120,11 +119,8 @@ __global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(cons
 #pragma unroll
         for (int v = 0; v < NV; ++v) x[u][v].zero();
         if (row[u] == -1 || !on) continue;
-        const uint8_t *src = page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes + held<P>(sub * EV);
-        if constexpr (Same<P, E2M1>::value) {
-          code[u][0] = __ldcs((const uint2 *)src);
-          byte[u] = __ldcs(page[u] + L.scale_off + ((int64_t)row[u] * L.heads + head[u]) * scales + sub);
-        } else if constexpr (Same<P, E4M3>::value) {
+        const uint8_t *src = page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes + sub * EV * kSize<P>;
+        if constexpr (Same<P, E4M3>::value) {
           if constexpr (NV == 2) {
             const uint4 c = __ldcs((const uint4 *)src);
             code[u][0] = make_uint2(c.x, c.y), code[u][1] = make_uint2(c.z, c.w);
@@ -147,19 +143,8 @@ __global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(cons
     for (int u = 0; u < kUnroll; ++u) {
       if constexpr (APPEND) {
         uint8_t *dst = row[u] < 0 ? nullptr : page[u] + ((int64_t)row[u] * L.heads + head[u]) * head_bytes +
-                                                  held<P>(sub * EV);
-        if constexpr (Same<P, E2M1>::value) {  // a lane has a group
-          const uint32_t sb = e2m1_scale_byte(x[u][0].bits(max(x[u][0].top(), x[u][1].top())));
-          if (dst && on) {
-            float lo[8], hi[8], f[16];
-            x[u][0].get(lo);
-            x[u][1].get(hi);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = lo[e], f[8 + e] = hi[e];
-            *(uint2 *)dst = to_e2m1x16<Same<D, float>::value>(f, sb);
-            page[u][L.scale_off + ((int64_t)row[u] * L.heads + head[u]) * scales + sub] = (uint8_t)sb;
-          }
-        } else if constexpr (Same<P, E4M3>::value) {
+                                                  sub * EV * kSize<P>;
+        if constexpr (Same<P, E4M3>::value) {
           uint32_t m = x[u][0].top();
           if constexpr (NV == 2) m = max(m, x[u][1].top());
           if (lanes == 32) m = __reduce_max_sync(0xffffffffu, m);
@@ -197,13 +182,6 @@ __global__ void __launch_bounds__(kThreads, (kOcc<APPEND, NV>)) rows_kernel(cons
         }
       } else {
         if (row[u] == -2 || !on) continue;
-        if constexpr (Same<P, E2M1>::value) {
-          if (row[u] >= 0) {
-            const __half2 k = e2m1_scale2(byte[u]);
-            e2m1_to<D>(code[u][0].x, k, x[u][0]);
-            e2m1_to<D>(code[u][0].y, k, x[u][1]);
-          }
-        }
         if constexpr (Same<P, E4M3>::value) {
           if (row[u] >= 0) {
             const float k = scale_of(byte[u]);
@@ -315,7 +293,6 @@ cudaError_t launch_dense(const KvRowsParams &p, int grid, int tok, cudaStream_t 
     case LSC_F32: return launch_typed<APPEND, D, float, 1>(p, grid, tok, stream);
     case LSC_BF16: return launch_typed<APPEND, D, __nv_bfloat16, 1>(p, grid, tok, stream);
     case LSC_F16: return launch_typed<APPEND, D, __half, 1>(p, grid, tok, stream);
-    case LSC_E2M1: return launch_typed<APPEND, D, E2M1, 2>(p, grid, tok, stream);
     default:
       return p.L.head_dim % 16 == 0 ? launch_typed<APPEND, D, E4M3, 2>(p, grid, tok, stream)
                                     : launch_typed<APPEND, D, E4M3, 1>(p, grid, tok, stream);
@@ -331,10 +308,12 @@ cudaError_t launch_rows(const KvRowsParams &p, int num_sms, cudaStream_t stream)
   while (tok > 1 && (T + tok - 1) / tok < 2 * (int64_t)num_sms) tok >>= 1;
   const int grid = (int)((T + tok - 1) / tok);
   const int es = p.dtype == LSC_F32 ? 4 : 2;
-  const bool vec = L.head_dim % 8 == 0 && L.head_dim <= 256 &&
+  const bool vec = L.head_dim % 8 == 0 && (L.head_dim <= 256 || L.dtype == LSC_E2M1) &&
                    (((uintptr_t)p.k | (uintptr_t)p.v | (uintptr_t)(p.k_stride * es) | (uintptr_t)(p.v_stride * es)) & 15) == 0;
   cudaError_t e;
-  if (!vec) {
+  if (vec && L.dtype == LSC_E2M1) {
+    e = APPEND ? launch_kv_append4(p, num_sms, stream) : launch_kv_gather4(p, num_sms, stream);
+  } else if (!vec) {
     e = launch_pdl(rows_any_kernel<APPEND>, grid, kThreads, 0, stream, p, tok);
   } else {
     e = p.dtype == LSC_F32    ? launch_dense<APPEND, float>(p, grid, tok, stream)
