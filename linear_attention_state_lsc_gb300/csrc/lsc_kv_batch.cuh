@@ -181,7 +181,9 @@ __device__ __forceinline__ float e2m1_quotient32(float x, float s, float r) {
 template <bool FULL>
 __device__ __forceinline__ uint2 to_e2m1x16(const float (&x)[16], uint32_t byte) {
   if (byte == 0 || byte == 255) return make_uint2(0, 0);
-  const float s = __half2float(__ushort_as_half((uint16_t)(byte << 7))), r = __frcp_rn(s);
+  const float s = __half2float(__ushort_as_half((uint16_t)(byte << 7)));
+  float r;  // off by 2^-23 at most
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

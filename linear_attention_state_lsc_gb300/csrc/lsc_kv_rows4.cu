@@ -5,9 +5,9 @@
 // Both directions move 2 bytes a dense element (16-bit types) and 9/16 of a byte in
 // the pool, once: HBM bounds a large call, the launch a small one.  A (token, lane) row
 // of all heads is one stretch of codes, one of scales and one dense row, so a warp takes
-// a stretch of such a row at a time, and what is left per element is the arithmetic: with
-// a group of lanes a head, as the other types have it (lsc_kv_rows.cu), finding each
-// head's addresses cost as much as the codes.
+// a stretch of such a row at a time (lsc_kv_walk.cuh), and what is left per element is
+// the arithmetic: with a group of lanes a head, as the other types have it (lsc_kv_rows.cu),
+// finding each head's addresses cost as much as the codes.
 //   * append: a lane has a group of 16 elements (two 16-byte loads) and stores its 8 bytes
 //     of codes and its scale byte; a warp's next stretches are loaded while one is
 //     worked on.
@@ -41,95 +41,105 @@ int run_tokens(int64_t T, int num_sms, int occ) {
 }
 
 // ---- append --------------------------------------------------------------------
-constexpr int kAppendOcc = 4;
+constexpr int kAppendOcc = 3;
 
-// items: stretches of 512 elements of a row
+// An item is a stretch of 512 elements of a token's K and V rows, `per` of them a row.
 template <typename D>
-__global__ void __launch_bounds__(kThreads, kAppendOcc) append4_kernel(const __grid_constant__ KvRowsParams p, int tok, FastDiv by_items) {
-  constexpr int U = sizeof(D) == 4 ? 1 : 2;  // stretches on the way, a warp
+__global__ void __launch_bounds__(kThreads, kAppendOcc) append4_kernel(const __grid_constant__ KvRowsParams p, int tok, int per, FastDiv by_per) {
+  constexpr int U = sizeof(D) == 4 ? 1 : 2;  // items on the way, a warp
   __shared__ Places s;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const KvLayer &L = p.L;
   const int32_t t0 = (int32_t)blockIdx.x * tok;
   const int n = p.b.total_tokens - t0 < tok ? p.b.total_tokens - t0 : tok;
-  const int ln = threadIdx.x & 31, row_el = L.heads * L.head_dim, items = by_items.d, all = 2 * n * items;
-  Eight<D> x[U][2];
+  const int ln = threadIdx.x & 31, row_el = L.heads * L.head_dim, all = n * per;
+  Eight<D> x[U][2][2];  // K's and V's
   auto load = [&](int u, int item) {
-    x[u][0].zero(), x[u][1].zero();
-    const int r2 = by_items.div(item), el = (item - r2 * items) * 512 + ln * 16;
-    if (item >= all || el >= row_el) return;
-    const uint8_t *src = (const uint8_t *)(r2 & 1 ? p.v : p.k) +
-                         ((int64_t)(t0 + (r2 >> 1)) * (r2 & 1 ? p.v_stride : p.k_stride) + el) * kSize<D>;
-    x[u][0].load(src);
-    x[u][1].load(src + 8 * kSize<D>);
+    const int i = by_per.div(item), el = (item - i * per) * 512 + ln * 16;
+    const bool on = item < all && el < row_el;
+    const uint8_t *k = (const uint8_t *)p.k + ((int64_t)(t0 + i) * p.k_stride + el) * kSize<D>;
+    const uint8_t *v = (const uint8_t *)p.v + ((int64_t)(t0 + i) * p.v_stride + el) * kSize<D>;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      x[u][0][e].zero(), x[u][1][e].zero();
+      if (on) x[u][0][e].load(k + e * 8 * kSize<D>), x[u][1][e].load(v + e * 8 * kSize<D>);
+    }
   };
   int ahead = threadIdx.x >> 5;
 #pragma unroll
   for (int u = 0; u < U; ++u, ahead += kWarps) load(u, ahead);
   if (blockIdx.x == 0) check_cu(L, p.b);
   find_places(L, p.b, t0, n, s);
+  const int64_t lane_off = L.v - L.k;
   for (int i0 = threadIdx.x >> 5; i0 < all; i0 += kWarps * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u, ahead += kWarps) {
-      const int item = i0 + u * kWarps, r2 = by_items.div(item), el = (item - r2 * items) * 512 + ln * 16;
-      const uint32_t sb = e2m1_scale_byte(x[u][0].bits(max(x[u][0].top(), x[u][1].top())));
-      float lo[8], hi[8], f[16];
-      x[u][0].get(lo);
-      x[u][1].get(hi);
+      uint2 code[2];
+      uint32_t sb[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = lo[e], f[8 + e] = hi[e];
+      for (int v = 0; v < 2; ++v) {
+        sb[v] = e2m1_scale_byte(x[u][v][0].bits(max(x[u][v][0].top(), x[u][v][1].top())));
+        float lo[8], hi[8], f[16];
+        x[u][v][0].get(lo);
+        x[u][v][1].get(hi);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = lo[e], f[8 + e] = hi[e];
+        code[v] = to_e2m1x16<sizeof(D) == 4>(f, sb[v]);
+      }
       load(u, ahead);
-      const uint2 code = to_e2m1x16<sizeof(D) == 4>(f, sb);
+      const int item = i0 + u * kWarps, i = by_per.div(item), el = (item - i * per) * 512 + ln * 16;
       if (item >= all || el >= row_el) continue;
-      const int32_t row = s.row[r2 >> 1];
+      const int32_t row = s.row[i];
       if (row < 0) continue;
       const uint32_t at = (uint32_t)row * row_el + el;  // a block has 2^32 elements at most
-      uint8_t *page = (r2 & 1 ? L.v : L.k) + s.page[r2 >> 1];
-      *(uint2 *)(page + (at >> 1)) = code;
-      page[L.scale_off + (at >> 4)] = (uint8_t)sb;
+      uint8_t *c = L.k + s.page[i] + (at >> 1), *b = L.k + s.page[i] + L.scale_off + (at >> 4);
+      *(uint2 *)c = code[0];
+      *(uint2 *)(c + lane_off) = code[1];
+      *b = (uint8_t)sb[0];
+      b[lane_off] = (uint8_t)sb[1];
     }
   }
 }
 
 // ---- gather --------------------------------------------------------------------
-// A warp's stretches of 256 elements of the run's rows: rows(r2, page, row, dst) says where row r2 (K and V of a token
-// in turn) is, and is false for one that is not written; row < 0: zeros.
-template <typename D, typename F>
-__device__ __forceinline__ void read_rows(const KvLayer &L, int n, const FastDiv &by_items, const F &rows) {
-  constexpr int U = 4;
-  const int ln = threadIdx.x & 31, row_el = L.heads * L.head_dim, items = by_items.d, all = 2 * n * items;
-  for (int i0 = threadIdx.x >> 5; i0 < all; i0 += kWarps * U) {
-    uint32_t code[U], byte[U];
-    uint8_t *dst[U];
+// An item: NS stretches of 256 elements of a token's K and V rows, whose addresses differ by constants.
+template <typename D, int NS>
+struct Item {
+  uint32_t code[NS][2], byte[NS][2];
+  // page: K's block, element `at` of it (row < 0: zeros); `left` elements of the row from this lane's first on
+  __device__ __forceinline__ void load(const uint8_t *page, int64_t lane_off, int32_t scale_off, int32_t row, uint32_t at, int left) {
+    const uint8_t *c = page + (at >> 1), *b = page + scale_off + (at >> 4);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int item = i0 + u * kWarps, r2 = by_items.div(item), el = (item - r2 * items) * 256 + ln * 8;
-      dst[u] = nullptr;
-      code[u] = byte[u] = 0;
-      if (item >= all || el >= row_el) continue;
-      const uint8_t *page;
-      int32_t row;
-      if (!rows(r2, page, row, dst[u])) continue;
-      dst[u] += (int64_t)el * kSize<D>;
-      if (row < 0) continue;
-      const uint32_t at = (uint32_t)row * row_el + el;
-      code[u] = __ldcs((const uint32_t *)(page + (at >> 1)));
-      byte[u] = __ldcs(page + L.scale_off + (at >> 4));
-    }
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      Eight<D> y;
-      e2m1_to<D>(code[u], e2m1_scale2(byte[u]), y);
-      if (dst[u]) y.store(dst[u]);
+      for (int v = 0; v < 2; ++v) {
+        code[n][v] = byte[n][v] = 0;
+        if (row >= 0 && n * 256 < left) {
+          code[n][v] = __ldcs((const uint32_t *)(c + (v ? lane_off : 0)) + n * 32);
+          byte[n][v] = __ldcs(b + (v ? lane_off : 0) + n * 16);
+        }
+      }
+  }
+  __device__ __forceinline__ void store(uint8_t *k, uint8_t *v, int left) const {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      if (n * 256 >= left) break;
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        Eight<D> y;
+        e2m1_to<D>(code[n][l], e2m1_scale2(byte[n][l]), y);
+        y.store((l ? v : k) + n * 256 * kSize<D>);
+      }
     }
   }
-}
+};
 
-constexpr int kGatherOcc = 6;
+constexpr int kGatherOcc = 5;
 
-template <typename D>
-__global__ void __launch_bounds__(kThreads, kGatherOcc) gather4_kernel(const __grid_constant__ KvRowsParams p, int tok, FastDiv by_items) {
+// U items on the way, a warp
+template <typename D, int NS, int U>
+__global__ void __launch_bounds__(kThreads, kGatherOcc) gather4_kernel(const __grid_constant__ KvRowsParams p, int tok, int per, FastDiv by_per) {
   __shared__ Places s;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -138,22 +148,35 @@ __global__ void __launch_bounds__(kThreads, kGatherOcc) gather4_kernel(const __g
   const int32_t t0 = (int32_t)blockIdx.x * tok;
   const int n = p.b.total_tokens - t0 < tok ? p.b.total_tokens - t0 : tok;
   find_places(L, p.b, t0, n, s);
-  read_rows<D>(L, n, by_items, [&](int r2, const uint8_t *&page, int32_t &row, uint8_t *&dst) {
-    const int i = r2 >> 1, v = r2 & 1;
-    row = s.row[i];
-    if (row == -2) return false;
-    page = (v ? L.v : L.k) + s.page[i];
-    dst = (uint8_t *)(v ? p.v : p.k) + (int64_t)(t0 + i) * (v ? p.v_stride : p.k_stride) * kSize<D>;
-    return true;
-  });
+  const int ln = threadIdx.x & 31, row_el = L.heads * L.head_dim, all = n * per;
+  const int64_t lane_off = L.v - L.k;
+  for (int i0 = threadIdx.x >> 5; i0 < all; i0 += kWarps * U) {
+    Item<D, NS> x[U];
+    int at[U], el[U];  // token of the run, -1: none
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int item = i0 + u * kWarps;
+      at[u] = by_per.div(item);
+      el[u] = (item - at[u] * per) * (256 * NS) + ln * 8;
+      const int32_t row = item < all ? s.row[at[u]] : -2;
+      x[u].load(L.k + (row < 0 ? 0 : s.page[at[u]]), lane_off, L.scale_off, row, (uint32_t)row * row_el + el[u], row_el - el[u]);
+      if (row == -2) el[u] = row_el;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + at[u];
+      x[u].store((uint8_t *)p.k + (t * p.k_stride + el[u]) * kSize<D>, (uint8_t *)p.v + (t * p.v_stride + el[u]) * kSize<D>,
+                 row_el - el[u]);
+    }
+  }
 }
 
 // ---- expanded rows ---------------------------------------------------------------
 constexpr int kExpandRows = 32;  // positions of a CTA
 
-template <typename D>
+template <typename D, int NS, int U>
 __global__ void __launch_bounds__(kThreads, kGatherOcc) expand_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ KvExpand x,
-                                                                      FastDiv by_items) {
+                                                                      int per, FastDiv by_per) {
   __shared__ int64_t s_page[kExpandRows];
   __shared__ int32_t s_row[kExpandRows];
   griddep_wait();
@@ -173,48 +196,80 @@ __global__ void __launch_bounds__(kThreads, kGatherOcc) expand_kernel(const __gr
   const int32_t block0 = i * x.blocks + pos0 / kExpandTokens;
   if (threadIdx.x == 0 && pos0 % kExpandTokens == 0) x.table[block0] = block0;
   __syncthreads();
-  const int64_t row_bytes = (int64_t)L.heads * L.head_dim * kSize<D>;
-  const int64_t out0 = ((int64_t)block0 * kExpandTokens + pos0 % kExpandTokens) * row_bytes;
-  read_rows<D>(L, n, by_items, [&](int r2, const uint8_t *&page, int32_t &row, uint8_t *&dst) {
-    const int j = r2 >> 1, v = r2 & 1;
-    row = s_row[j];
-    page = (v ? L.v : L.k) + s_page[j];
-    dst = (uint8_t *)(v ? x.v : x.k) + out0 + j * row_bytes;
-    return true;
-  });
+  const int ln = threadIdx.x & 31, row_el = L.heads * L.head_dim, all = n * per;
+  const int64_t row0 = (int64_t)block0 * kExpandTokens + pos0 % kExpandTokens, lane_off = L.v - L.k;
+  for (int i0 = threadIdx.x >> 5; i0 < all; i0 += kWarps * U) {
+    Item<D, NS> y[U];
+    int at[U], el[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int item = i0 + u * kWarps;
+      at[u] = by_per.div(item);
+      el[u] = (item - at[u] * per) * (256 * NS) + ln * 8;
+      if (item >= all) el[u] = row_el;
+      const int32_t row = item < all ? s_row[at[u]] : -1;
+      y[u].load(L.k + (row < 0 ? 0 : s_page[at[u]]), lane_off, L.scale_off, row, (uint32_t)row * row_el + el[u], row_el - el[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t to = ((row0 + at[u]) * row_el + el[u]) * kSize<D>;
+      y[u].store((uint8_t *)x.k + to, (uint8_t *)x.v + to, row_el - el[u]);
+    }
+  }
 }
 
-FastDiv items_of(const KvLayer &L, int el) {
+int stretches(const KvLayer &L, int el) { return (L.heads * L.head_dim + el - 1) / el; }
+
+FastDiv by(int n) {
   FastDiv d;
-  d.set((uint32_t)((L.heads * L.head_dim + el - 1) / el));
+  d.set((uint32_t)n);
   return d;
+}
+
+// Stretches of 256 elements of an item: as many as fill rows without a rest, so that no lane idles.
+int stretches_of_item(const KvLayer &L) {
+  const int row = L.heads * L.head_dim;
+  return row % 1024 == 0 ? 4 : row % 512 == 0 ? 2 : 1;
+}
+
+template <typename D>
+cudaError_t gather_typed(const KvRowsParams &p, int grid, int tok, cudaStream_t stream) {
+  const int ns = stretches_of_item(p.L), per = stretches(p.L, 256 * ns);
+  return ns == 4   ? launch_pdl(gather4_kernel<D, 4, 1>, grid, kThreads, 0, stream, p, tok, per, by(per))
+         : ns == 2 ? launch_pdl(gather4_kernel<D, 2, 2>, grid, kThreads, 0, stream, p, tok, per, by(per))
+                   : launch_pdl(gather4_kernel<D, 1, 4>, grid, kThreads, 0, stream, p, tok, per, by(per));
+}
+
+template <typename D>
+cudaError_t expand_typed(const KvAttendParams &p, const KvExpand &x, int grid, cudaStream_t stream) {
+  const int ns = stretches_of_item(p.L), per = stretches(p.L, 256 * ns);
+  return ns == 4   ? launch_pdl(expand_kernel<D, 4, 1>, grid, kThreads, 0, stream, p, x, per, by(per))
+         : ns == 2 ? launch_pdl(expand_kernel<D, 2, 2>, grid, kThreads, 0, stream, p, x, per, by(per))
+                   : launch_pdl(expand_kernel<D, 1, 4>, grid, kThreads, 0, stream, p, x, per, by(per));
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append4(const KvRowsParams &p, int num_sms, cudaStream_t stream) {
-  const int tok = run_tokens(p.b.total_tokens, num_sms, kAppendOcc), grid = (int)(((int64_t)p.b.total_tokens + tok - 1) / tok);
-  const FastDiv d = items_of(p.L, 512);
-  return p.dtype == LSC_F32    ? launch_pdl(append4_kernel<float>, grid, kThreads, 0, stream, p, tok, d)
-         : p.dtype == LSC_BF16 ? launch_pdl(append4_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, p, tok, d)
-                               : launch_pdl(append4_kernel<__half>, grid, kThreads, 0, stream, p, tok, d);
+  const int per = stretches(p.L, 512), tok = run_tokens(p.b.total_tokens, num_sms, kAppendOcc);
+  const int grid = (int)(((int64_t)p.b.total_tokens + tok - 1) / tok);
+  return p.dtype == LSC_F32    ? launch_pdl(append4_kernel<float>, grid, kThreads, 0, stream, p, tok, per, by(per))
+         : p.dtype == LSC_BF16 ? launch_pdl(append4_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, p, tok, per, by(per))
+                               : launch_pdl(append4_kernel<__half>, grid, kThreads, 0, stream, p, tok, per, by(per));
 }
 
 cudaError_t launch_kv_gather4(const KvRowsParams &p, int num_sms, cudaStream_t stream) {
   const int tok = run_tokens(p.b.total_tokens, num_sms, kGatherOcc), grid = (int)(((int64_t)p.b.total_tokens + tok - 1) / tok);
-  const FastDiv d = items_of(p.L, 256);
-  return p.dtype == LSC_F32    ? launch_pdl(gather4_kernel<float>, grid, kThreads, 0, stream, p, tok, d)
-         : p.dtype == LSC_BF16 ? launch_pdl(gather4_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, p, tok, d)
-                               : launch_pdl(gather4_kernel<__half>, grid, kThreads, 0, stream, p, tok, d);
+  return p.dtype == LSC_F32    ? gather_typed<float>(p, grid, tok, stream)
+         : p.dtype == LSC_BF16 ? gather_typed<__nv_bfloat16>(p, grid, tok, stream)
+                               : gather_typed<__half>(p, grid, tok, stream);
 }
 
 cudaError_t launch_kv_expand(const KvAttendParams &p, KvExpand x, cudaStream_t stream) {
   x.chunks = (p.max_kv + kExpandRows - 1) / kExpandRows;
   x.by_chunks.set((uint32_t)x.chunks);
   const int grid = p.b.n_seq * x.chunks;
-  const FastDiv d = items_of(p.L, 256);
-  const cudaError_t e = p.dtype == LSC_BF16 ? launch_pdl(expand_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, p, x, d)
-                                            : launch_pdl(expand_kernel<__half>, grid, kThreads, 0, stream, p, x, d);
+  const cudaError_t e = p.dtype == LSC_BF16 ? expand_typed<__nv_bfloat16>(p, x, grid, stream) : expand_typed<__half>(p, x, grid, stream);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
