@@ -134,14 +134,15 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
 constexpr uint32_t kE2M1Top = 226;  // scale byte of 10240: six times it is the largest magnitude that f16 holds
 
 // The group's scale byte for its largest magnitude, as fp32 bits (NaN counts as the
-// largest): the smallest scale s with 6 s >= top.  top / 6 is off by a rounding or
-// two, so the scale just below it is looked at: 6 s has 6 bits, the comparison is exact.
+// largest): the smallest scale s with 6 s >= top.  u = top / 1.5 is the scale it would
+// need, four times; its fp32 mantissa rounded up to 3 bits is the scale's.  Where top is
+// 6 s itself u comes out as 4 s: the factor is off by 2^-25, half an fp32 step at 4 s's
+// four bits is more.
 __device__ __forceinline__ uint32_t e2m1_scale_byte(uint32_t top_bits) {
-  if (top_bits >= 0x7f800000u) return 255;
-  const float top = __uint_as_float(top_bits);
-  uint32_t b = __half_as_ushort(__float2half_rz(top * (1.f / 6.f))) >> 7;
-  b = b < kE2M1Top ? b : kE2M1Top;
-  return b + (b < kE2M1Top && 6.f * __half2float(__ushort_as_half((uint16_t)(b << 7))) < top ? 1 : 0);
+  const float u = __uint_as_float(top_bits) * (2.f / 3.f);
+  const int32_t x = (int32_t)((__float_as_uint(u) + 0xfffffu) >> 20) - ((127 + 2 - 15) << 3);
+  const int32_t b = min(x < 8 ? (int32_t)ceilf(u * 32768.f) : x, (int32_t)kE2M1Top);  // below 2^-14: multiples of 2^-17
+  return top_bits >= 0x7f800000u ? 255 : (uint32_t)b;
 }
 
 // Two magnitudes over their scale -> codes (lo in the low nibble), to nearest even, 6 at most.
@@ -151,21 +152,18 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
   return r;
 }
 
-// Two values as the operand of the packed instructions, which do two lanes' worth a cycle.
+// What elements x over their scale s are rounded from: x / s rounded once to 32 bits, as x r + x rest with r just below
+// 1 / s and rest = (1 - s r) r, what it is off by (positive, so a zero keeps its sign).  An element of a 16-bit type has
+// 11 bits and a scale 4, so a quotient that is no tie between codes is 2^-11 or more of a tie away from it, and one that
+// is (three bits) comes out as it is.
 __device__ __forceinline__ uint64_t f32x2(float x, float y) {
   return (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32;
 }
-
-// What elements x over their scale s are rounded from, r = 1 / s.  x r is off by less than 2^-22 of itself; an element
-// of a 16-bit type has 11 bits and a scale 4, so a quotient that is no tie is 2^-11 or more of a tie away from it.
-// 96 + x r is rounded to 2^-17, which brings the others back to their ties exactly (below 8; the largest scale's
-// quotients may be larger, all of them 6), and 96 off again.
-__device__ __forceinline__ void e2m1_quotients(float x0, float x1, float r, float &y0, float &y1) {
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi, float r, float rest) {
   uint64_t t;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(f32x2(x0, x1)), "l"(f32x2(r, r)), "l"(f32x2(96.f, 96.f)));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(t), "l"(f32x2(-96.f, -96.f)));
-  y0 = __uint_as_float((uint32_t)t | (__float_as_uint(x0) & 0x80000000u));  // a zero keeps its sign
-  y1 = __uint_as_float((uint32_t)(t >> 32) | (__float_as_uint(x1) & 0x80000000u));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(f32x2(lo, hi)), "l"(f32x2(rest, rest)));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(t) : "l"(f32x2(lo, hi)), "l"(f32x2(r, r)));
+  return to_e2m1x2(__uint_as_float((uint32_t)t), __uint_as_float((uint32_t)(t >> 32)));
 }
 // With 32 bits a quotient may be nearer to a tie than x r is exact: rounded to 20 bits it is that tie, and the sign of
 // x - tie s, exact in one fma, moves it to the right side.
@@ -180,10 +178,10 @@ __device__ __forceinline__ float e2m1_quotient32(float x, float s, float r) {
 // 16 elements with their scale byte -> 64 bits of codes.  FULL: they may have more than 11 bits.
 template <bool FULL>
 __device__ __forceinline__ uint2 to_e2m1x16(const float (&x)[16], uint32_t byte) {
-  if (byte == 0 || byte == 255) return make_uint2(0, 0);
   const float s = __half2float(__ushort_as_half((uint16_t)(byte << 7)));
   float r;  // off by 2^-23 at most
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  const float low = __uint_as_float(__float_as_uint(r) - 2), rest = __fmaf_rn(-s, low, 1.f) * low;
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -191,14 +189,12 @@ __device__ __forceinline__ uint2 to_e2m1x16(const float (&x)[16], uint32_t byte)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x0 = x[8 * h + 2 * i], x1 = x[8 * h + 2 * i + 1];
-      float y0, y1;
-      if constexpr (FULL) y0 = e2m1_quotient32(x0, s, r), y1 = e2m1_quotient32(x1, s, r);
-      else e2m1_quotients(x0, x1, r, y0, y1);
-      c[i] = to_e2m1x2(y0, y1);
+      c[i] = FULL ? to_e2m1x2(e2m1_quotient32(x0, s, r), e2m1_quotient32(x1, s, r))
+                  : to_e2m1x2(x0, x1, low, rest);
     }
     w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
   }
-  return make_uint2(w[0], w[1]);
+  return byte == 0 || byte == 255 ? make_uint2(0, 0) : make_uint2(w[0], w[1]);
 }
 
 // Eight codes -> four pairs of halves, exactly.

@@ -101,6 +101,7 @@ struct Eight<float> {
     return m;
   }
   static __device__ uint32_t bits(uint32_t m) { return m; }
+  __device__ uint32_t top_with(const Eight &y) const { return max(top(), y.top()); }
   __device__ void put(const float (&x)[8]) {
     a = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     b = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
@@ -116,6 +117,13 @@ struct Eight16 {
   __device__ uint32_t top() const {  // two magnitudes a word
     const uint32_t k = 0x7fff7fffu, m = __vmaxu2(__vmaxu2(a.x & k, a.y & k), __vmaxu2(a.z & k, a.w & k));
     return max(m & 0xffffu, m >> 16);
+  }
+  __device__ uint32_t top_with(const Eight16 &y) const {  // of 16 elements, on the floats' own maximum
+    const auto most = [](H2 p, H2 q) { return __hmax2_nan(__habs2(p), __habs2(q)); };
+    const auto h = [](uint32_t w) { return *reinterpret_cast<const H2 *>(&w); };
+    const H2 m = most(most(most(h(a.x), h(a.y)), most(h(a.z), h(a.w))), most(most(h(y.a.x), h(y.a.y)), most(h(y.a.z), h(y.a.w))));
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(&m);
+    return max(w & 0xffffu, w >> 16);
   }
   static __device__ uint32_t bits(uint32_t m) { return __float_as_uint(two(m).x); }
   static __device__ uint32_t pack(float x, float y);

@@ -24,6 +24,7 @@
 #include "lsc_kv_attend.cuh"
 #include "lsc_kv_batch.cuh"
 #include "lsc_kv_rows.cuh"
+#include "lsc_kv_walk.cuh"
 #include "lsc_ptx.h"
 
 namespace lsc {
@@ -43,43 +44,49 @@ int run_tokens(int64_t T, int num_sms, int occ) {
 // ---- append --------------------------------------------------------------------
 constexpr int kAppendOcc = 3;
 
-// An item is a stretch of 512 elements of a token's K and V rows, `per` of them a row.
+// An item is a stretch of 512 elements of a token's K and V rows, `per` of them a row; the warps' runs of items are those of
+// lsc_kv_walk.cuh (with runs of 16 tokens a CTA, as gather has them, finding a run's places took as long as its rows).
 template <typename D>
-__global__ void __launch_bounds__(kThreads, kAppendOcc) append4_kernel(const __grid_constant__ KvRowsParams p, int tok, int per, FastDiv by_per) {
+__global__ void __launch_bounds__(kWalkThreads, kAppendOcc) append4_kernel(const __grid_constant__ KvRowsParams p, int per) {
   constexpr int U = sizeof(D) == 4 ? 1 : 2;  // items on the way, a warp
-  __shared__ Places s;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const KvLayer &L = p.L;
-  const int32_t t0 = (int32_t)blockIdx.x * tok;
-  const int n = p.b.total_tokens - t0 < tok ? p.b.total_tokens - t0 : tok;
-  const int ln = threadIdx.x & 31, row_el = L.heads * L.head_dim, all = n * per;
+  const int ln = threadIdx.x & 31, row_el = L.heads * L.head_dim;
+  const WarpRun run = warp_run((int64_t)p.b.total_tokens * per);
+  int32_t t = (int32_t)(run.begin / per), rest = (int32_t)(run.begin - (int64_t)t * per), left = (int32_t)(run.end - run.begin);
+  int32_t t_ahead = t, rest_ahead = rest, left_ahead = left;
   Eight<D> x[U][2][2];  // K's and V's
-  auto load = [&](int u, int item) {
-    const int i = by_per.div(item), el = (item - i * per) * 512 + ln * 16;
-    const bool on = item < all && el < row_el;
-    const uint8_t *k = (const uint8_t *)p.k + ((int64_t)(t0 + i) * p.k_stride + el) * kSize<D>;
-    const uint8_t *v = (const uint8_t *)p.v + ((int64_t)(t0 + i) * p.v_stride + el) * kSize<D>;
+  auto load = [&](int u) {
+    const int el = rest_ahead * 512 + ln * 16;
+    const bool on = left_ahead > 0 && el < row_el;
+    const uint8_t *k = (const uint8_t *)p.k + ((int64_t)t_ahead * p.k_stride + el) * kSize<D>;
+    const uint8_t *v = (const uint8_t *)p.v + ((int64_t)t_ahead * p.v_stride + el) * kSize<D>;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       x[u][0][e].zero(), x[u][1][e].zero();
       if (on) x[u][0][e].load(k + e * 8 * kSize<D>), x[u][1][e].load(v + e * 8 * kSize<D>);
     }
+    --left_ahead;
+    if (++rest_ahead == per) rest_ahead = 0, ++t_ahead;
   };
-  int ahead = threadIdx.x >> 5;
 #pragma unroll
-  for (int u = 0; u < U; ++u, ahead += kWarps) load(u, ahead);
+  for (int u = 0; u < U; ++u) load(u);
   if (blockIdx.x == 0) check_cu(L, p.b);
-  find_places(L, p.b, t0, n, s);
   const int64_t lane_off = L.v - L.k;
-  for (int i0 = threadIdx.x >> 5; i0 < all; i0 += kWarps * U) {
+  PlaceWalk place;
+  int32_t row = -1;
+  bool fresh = true;
+  while (left > 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u, ahead += kWarps) {
+    for (int u = 0; u < U; ++u) {
+      if (u > 0 && left <= 0) break;
+      if (fresh) row = place.at(L, p.b, t);
       uint2 code[2];
       uint32_t sb[2];
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        sb[v] = e2m1_scale_byte(x[u][v][0].bits(max(x[u][v][0].top(), x[u][v][1].top())));
+        sb[v] = e2m1_scale_byte(Eight<D>::bits(x[u][v][0].top_with(x[u][v][1])));
         float lo[8], hi[8], f[16];
         x[u][v][0].get(lo);
         x[u][v][1].get(hi);
@@ -87,17 +94,19 @@ __global__ void __launch_bounds__(kThreads, kAppendOcc) append4_kernel(const __g
         for (int e = 0; e < 8; ++e) f[e] = lo[e], f[8 + e] = hi[e];
         code[v] = to_e2m1x16<sizeof(D) == 4>(f, sb[v]);
       }
-      load(u, ahead);
-      const int item = i0 + u * kWarps, i = by_per.div(item), el = (item - i * per) * 512 + ln * 16;
-      if (item >= all || el >= row_el) continue;
-      const int32_t row = s.row[i];
-      if (row < 0) continue;
-      const uint32_t at = (uint32_t)row * row_el + el;  // a block has 2^32 elements at most
-      uint8_t *c = L.k + s.page[i] + (at >> 1), *b = L.k + s.page[i] + L.scale_off + (at >> 4);
-      *(uint2 *)c = code[0];
-      *(uint2 *)(c + lane_off) = code[1];
-      *b = (uint8_t)sb[0];
-      b[lane_off] = (uint8_t)sb[1];
+      load(u);
+      const int el = rest * 512 + ln * 16;
+      if (row >= 0 && el < row_el) {
+        const uint32_t at = (uint32_t)row * row_el + el;  // a block has 2^32 elements at most
+        uint8_t *c = L.k + place.page + (at >> 1), *b = L.k + place.page + L.scale_off + (at >> 4);
+        *(uint2 *)c = code[0];
+        *(uint2 *)(c + lane_off) = code[1];
+        *b = (uint8_t)sb[0];
+        b[lane_off] = (uint8_t)sb[1];
+      }
+      --left;
+      fresh = ++rest == per;
+      if (fresh) rest = 0, ++t;
     }
   }
 }
@@ -251,11 +260,10 @@ cudaError_t expand_typed(const KvAttendParams &p, const KvExpand &x, int grid, c
 }  // namespace
 
 cudaError_t launch_kv_append4(const KvRowsParams &p, int num_sms, cudaStream_t stream) {
-  const int per = stretches(p.L, 512), tok = run_tokens(p.b.total_tokens, num_sms, kAppendOcc);
-  const int grid = (int)(((int64_t)p.b.total_tokens + tok - 1) / tok);
-  return p.dtype == LSC_F32    ? launch_pdl(append4_kernel<float>, grid, kThreads, 0, stream, p, tok, per, by(per))
-         : p.dtype == LSC_BF16 ? launch_pdl(append4_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, p, tok, per, by(per))
-                               : launch_pdl(append4_kernel<__half>, grid, kThreads, 0, stream, p, tok, per, by(per));
+  const int per = stretches(p.L, 512), grid = walk_grid((int64_t)p.b.total_tokens * per, num_sms, kAppendOcc);
+  return p.dtype == LSC_F32    ? launch_pdl(append4_kernel<float>, grid, kWalkThreads, 0, stream, p, per)
+         : p.dtype == LSC_BF16 ? launch_pdl(append4_kernel<__nv_bfloat16>, grid, kWalkThreads, 0, stream, p, per)
+                               : launch_pdl(append4_kernel<__half>, grid, kWalkThreads, 0, stream, p, per);
 }
 
 cudaError_t launch_kv_gather4(const KvRowsParams &p, int num_sms, cudaStream_t stream) {
