@@ -175,26 +175,31 @@ __device__ __forceinline__ float e2m1_quotient32(float x, float s, float r) {
   return __uint_as_float(t | (__float_as_uint(x) & 0x80000000u));
 }
 
-// 16 elements with their scale byte -> 64 bits of codes.  FULL: they may have more than 11 bits.
+// A group's scale as its elements meet it.
+struct E2m1Scale {
+  float s, r, low, rest;
+  bool none;  // codes of 0: a group of zeros, or one that holds a NaN or an infinity
+};
+__device__ __forceinline__ E2m1Scale e2m1_scale(uint32_t byte) {
+  E2m1Scale g;
+  g.s = __half2float(__ushort_as_half((uint16_t)(byte << 7)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.r) : "f"(g.s));  // off by 2^-23 at most
+  g.low = __uint_as_float(__float_as_uint(g.r) - 2);
+  g.rest = __fmaf_rn(-g.s, g.low, 1.f) * g.low;
+  g.none = byte == 0 || byte == 255;
+  return g;
+}
+
+// Eight elements -> their codes.  FULL: they may have more than 11 bits.
 template <bool FULL>
-__device__ __forceinline__ uint2 to_e2m1x16(const float (&x)[16], uint32_t byte) {
-  const float s = __half2float(__ushort_as_half((uint16_t)(byte << 7)));
-  float r;  // off by 2^-23 at most
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  const float low = __uint_as_float(__float_as_uint(r) - 2), rest = __fmaf_rn(-s, low, 1.f) * low;
-  uint32_t w[2];
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&x)[8], const E2m1Scale &g) {
+  uint32_t c[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x0 = x[8 * h + 2 * i], x1 = x[8 * h + 2 * i + 1];
-      c[i] = FULL ? to_e2m1x2(e2m1_quotient32(x0, s, r), e2m1_quotient32(x1, s, r))
-                  : to_e2m1x2(x0, x1, low, rest);
-    }
-    w[h] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-  }
-  return byte == 0 || byte == 255 ? make_uint2(0, 0) : make_uint2(w[0], w[1]);
+  for (int i = 0; i < 4; ++i)
+    c[i] = FULL ? to_e2m1x2(e2m1_quotient32(x[2 * i], g.s, g.r), e2m1_quotient32(x[2 * i + 1], g.s, g.r))
+                : to_e2m1x2(x[2 * i], x[2 * i + 1], g.low, g.rest);
+  const uint32_t w = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  return g.none ? 0 : w;
 }
 
 // Eight codes -> four pairs of halves, exactly.

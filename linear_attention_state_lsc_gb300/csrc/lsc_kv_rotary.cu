@@ -12,16 +12,21 @@
 // fp32, go to sincospif.
 //
 // Each element is read once and written once: HBM bounds a large call, the launch a
-// small one.  A CTA takes a run of tokens and forms their cosines and sines in shared
-// memory once for all heads (a head's pairs are the same for each), then streams the
-// rows; a row is one group of a warp's lanes with 8 elements each (16 where the pool is
-// E2M1: a group of one scale), its pairs' other halves come from the lane that has
-// them by shuffles, so a row is read once and may be turned in place.
+// small one.  All rows of all tokens are cut into equal runs, one a warp
+// (lsc_kv_walk.cuh).  A warp forms a token's cosines and sines once, in shared memory,
+// for all its heads, and then takes its rows 512 elements at a time: a lane has 16, the
+// 8 first and the 8 second elements of 8 pairs (of neighbouring pairs: 4 and 4 pairs half
+// the turned elements apart; likewise of the elements that are not turned), so no
+// element is needed by another lane, rows may be turned in place, loads and stores of
+// neighbouring lanes lie side by side, and so do their cosines.  A first form, CTAs of 16
+// tokens whose lanes had 8 elements and fetched their pairs' others by shuffles, had the
+// shared memory 94 % busy: 30011 tokens, 40 heads of 128, 170 us.
 #include <cuda_runtime.h>
 
 #include "lsc_internal.h"
 #include "lsc_kv_batch.cuh"
 #include "lsc_kv_rows.cuh"
+#include "lsc_kv_walk.cuh"
 #include "lsc_ptx.h"
 
 namespace lsc {
@@ -32,8 +37,171 @@ using namespace kv::row;
 
 struct NoPool {};
 
-constexpr int kUnroll = 2;  // rows in flight per lane group
+// ---- vector kernel: head_dim and rotary_dim multiples of 16, head_dim at most 512 ---------
+constexpr int kOcc = 3;
 
+// Lane `ln`'s places of its item: slot 32 rest + ln of the token, head_dim / 16 slots a head.
+struct Slot {
+  int32_t head, s;
+  int32_t v0, v1;  // first elements of its two eights
+  bool turned;
+};
+
+template <typename D, typename P>
+__global__ void __launch_bounds__(kWalkThreads, kOcc) rotary_kernel(const __grid_constant__ KvRotaryParams p, int per, FastDiv by_slots) {
+  constexpr bool POOL = !Same<P, NoPool>::value;
+  constexpr int U = sizeof(D) == 4 ? 1 : 2;  // items on the way, a warp
+  __shared__ uint64_t s_turns[kRotaryPairs];
+  __shared__ uint8_t s_axis[kRotaryPairs];
+  __shared__ float4 s_cs[kWalkWarps][4][kRotaryPairs / 8];  // of two pairs; a slot's eight pairs are [0 .. 3][slot]
+  if ((int)threadIdx.x < p.r.half) s_turns[threadIdx.x] = p.r.turns[threadIdx.x], s_axis[threadIdx.x] = p.r.axis[threadIdx.x];
+  __syncthreads();
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const KvLayer &L = p.L;
+  const int ln = threadIdx.x & 31, half = p.r.half, sr = half / 8, rest_dim = p.head_dim - 2 * half;
+  const int kh = POOL ? L.heads : 0, heads = p.heads + 2 * kh;
+  float4(&cs)[4][kRotaryPairs / 8] = s_cs[threadIdx.x >> 5];
+  const WarpRun run = warp_run((int64_t)p.b.total_tokens * per);
+  int32_t t = (int32_t)(run.begin / per), rest = (int32_t)(run.begin - (int64_t)t * per), left = (int32_t)(run.end - run.begin);
+  int32_t t_ahead = t, rest_ahead = rest, left_ahead = left;
+  auto slot_of = [&](int32_t rest) {
+    Slot z;
+    const int32_t i = rest * 32 + ln;
+    z.head = by_slots.div(i);
+    z.s = i - z.head * (int32_t)by_slots.d;
+    z.turned = z.s < sr;
+    z.v0 = z.turned ? 8 * z.s : 2 * half + 8 * (z.s - sr);
+    z.v1 = z.v0 + (z.turned ? half : rest_dim / 2);
+    return z;
+  };
+  Eight<D> x[U][2];
+  auto load = [&](int u) {
+    const Slot z = slot_of(rest_ahead);
+    const bool q = z.head < p.heads, v = z.head >= p.heads + kh;
+    const uint8_t *src = (const uint8_t *)(q ? p.x : v ? p.v : p.k) +
+                         ((int64_t)t_ahead * (q ? p.x_stride : v ? p.v_stride : p.k_stride) +
+                          (int64_t)(z.head - (q ? 0 : v ? p.heads + kh : p.heads)) * p.head_dim) * kSize<D>;
+    x[u][0].zero(), x[u][1].zero();
+    if (left_ahead > 0 && z.head < heads) x[u][0].load(src + z.v0 * kSize<D>), x[u][1].load(src + z.v1 * kSize<D>);
+    --left_ahead;
+    if (++rest_ahead == per) rest_ahead = 0, ++t_ahead;
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u);
+  if constexpr (POOL)
+    if (blockIdx.x == 0) check_cu(L, p.b);
+  PlaceWalk place;
+  int32_t row = 0;
+  bool fresh = true;
+  while (left > 0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u > 0 && left <= 0) break;
+      if (fresh) {
+        if constexpr (POOL) row = place.at(L, p.b, t);
+        __syncwarp();  // the last token's have been read
+        if (row != -2) {
+          for (int j = ln; j < half; j += 32) {
+            const int64_t pos = p.r.positions[s_axis[j] * p.r.axis_stride + t];
+            const int32_t half_turns = (int32_t)(((uint64_t)pos * s_turns[j]) >> 32);  // in units of 2^-31
+            float sn, cn;
+            sincospif((float)half_turns * 0x1p-31f, &sn, &cn);
+            const int up = p.r.interleaved && j >= half / 2, i = j - (up ? half / 2 : 0);
+            const int slot = p.r.interleaved ? i >> 2 : i >> 3, at = p.r.interleaved ? 2 * up + (i >> 1 & 1) : i >> 1 & 3;
+            *((float2 *)&cs[at][slot] + (i & 1)) = make_float2(cn * p.r.scale, sn * p.r.scale);
+          }
+        }
+        __syncwarp();
+      }
+      const Slot z = slot_of(rest);
+      const bool on = z.head < heads, q = z.head < p.heads, v = z.head >= p.heads + kh, turn = z.turned && !v;
+      const int head = z.head - (q ? 0 : v ? p.heads + kh : p.heads);
+      Eight<D> raw[2] = {x[u][0], x[u][1]};
+      load(u);
+      float f[2][8];
+      raw[0].get(f[0]);
+      raw[1].get(f[1]);
+      if (turn && on) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 c = cs[i][z.s];
+          if (!p.r.interleaved) {
+            const float a0 = f[0][2 * i], b0 = f[1][2 * i], a1 = f[0][2 * i + 1], b1 = f[1][2 * i + 1];
+            f[0][2 * i] = fmaf(a0, c.x, -b0 * c.y), f[1][2 * i] = fmaf(b0, c.x, a0 * c.y);
+            f[0][2 * i + 1] = fmaf(a1, c.z, -b1 * c.w), f[1][2 * i + 1] = fmaf(b1, c.z, a1 * c.w);
+          } else {
+            float(&g)[8] = f[i >> 1];
+            const int e = 4 * (i & 1);
+            const float a0 = g[e], b0 = g[e + 1], a1 = g[e + 2], b1 = g[e + 3];
+            g[e] = fmaf(a0, c.x, -b0 * c.y), g[e + 1] = fmaf(b0, c.x, a0 * c.y);
+            g[e + 2] = fmaf(a1, c.z, -b1 * c.w), g[e + 3] = fmaf(b1, c.z, a1 * c.w);
+          }
+        }
+        raw[0].put(f[0]);  // what is not turned keeps its bits where its type stays
+        raw[1].put(f[1]);
+      }
+      if (q && on && row != -2 && (z.turned || p.out != p.x)) {
+        uint8_t *dst = (uint8_t *)p.out + ((int64_t)t * p.out_stride + (int64_t)head * p.head_dim) * kSize<D>;
+        raw[0].store(dst + z.v0 * kSize<D>);
+        raw[1].store(dst + z.v1 * kSize<D>);
+      }
+      if constexpr (POOL) {
+        const bool put = !q && on && row >= 0;
+        uint8_t *const page = L.k + (v ? L.v - L.k : 0) + (row >= 0 ? place.page : 0);
+        const int64_t first = ((int64_t)row * L.heads + head) * p.head_dim;  // element of the block
+        if constexpr (Same<P, E4M3>::value) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[i >> 3][i & 7]) & 0x7fffffffu);
+          for (int o = (int)by_slots.d >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const uint32_t sb = scale_byte(m);
+          const float inv = inv_scale_of(sb);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float(&y)[8] = f[e];
+            uint2 c = make_uint2(
+                __byte_perm(to_e4m3x2(y[0] * inv, y[1] * inv), to_e4m3x2(y[2] * inv, y[3] * inv), 0x5410),
+                __byte_perm(to_e4m3x2(y[4] * inv, y[5] * inv), to_e4m3x2(y[6] * inv, y[7] * inv), 0x5410));
+            if (sb == 255) c = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+            if (put) *(uint2 *)(page + first + (e ? z.v1 : z.v0)) = c;
+          }
+          if (put && z.s == 0) page[L.scale_off + (int64_t)row * L.heads + head] = (uint8_t)sb;
+        } else if constexpr (Same<P, E2M1>::value) {  // a group of 16 is the same eight of two neighbouring lanes
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[e][i]) & 0x7fffffffu);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            const uint32_t sb = e2m1_scale_byte(m), el = (uint32_t)first + (e ? z.v1 : z.v0);  // 2^32 a block at most
+            const uint32_t c = to_e2m1x8<true>(f[e], e2m1_scale(sb));  // a turned element has 24 bits
+            if (put) *(uint32_t *)(page + (el >> 1)) = c;
+            if (put && (ln & 1) == 0) page[L.scale_off + (el >> 4)] = (uint8_t)sb;
+          }
+        } else if (put) {
+          uint8_t *dst = page + first * kSize<P>;
+          if constexpr (Same<P, D>::value) {
+            raw[0].store(dst + z.v0 * kSize<P>);
+            raw[1].store(dst + z.v1 * kSize<P>);
+          } else {
+            Eight<P> y;
+            y.put(f[0]);
+            y.store(dst + z.v0 * kSize<P>);
+            y.put(f[1]);
+            y.store(dst + z.v1 * kSize<P>);
+          }
+        }
+      }
+      --left;
+      fresh = ++rest == per;
+      if (fresh) rest = 0, ++t;
+    }
+  }
+}
+
+// ---- element kernel: any head_dim, rotary_dim, types and alignment ------------------------------
+// A warp takes a row.
 // The run's cosines and sines times the factor, [token][pair]; a token of no sequence has none.  A thread has one pair:
 // its frequency and axis come from the constant bank, one address a lane.
 template <bool POOL>
@@ -46,7 +214,7 @@ __device__ __forceinline__ void fill_turns(const KvRotaryParams &p, int32_t t0, 
     for (int i = first; i < n; i += at_once) {
       if (POOL && s.row[i] == -2) continue;
       const int64_t pos = positions[i];
-      const int32_t half_turns = (int32_t)(((uint64_t)pos * turns) >> 32);  // in units of 2^-31
+      const int32_t half_turns = (int32_t)(((uint64_t)pos * turns) >> 32);
       float sn, cn;
       sincospif((float)half_turns * 0x1p-31f, &sn, &cn);
       cs[i * r.half + pair] = make_float2(cn * r.scale, sn * r.scale);
@@ -55,165 +223,6 @@ __device__ __forceinline__ void fill_turns(const KvRotaryParams &p, int32_t t0, 
   __syncthreads();
 }
 
-__device__ __forceinline__ uint4 shfl4(uint4 x, int from) {
-  return make_uint4(__shfl_sync(0xffffffffu, x.x, from), __shfl_sync(0xffffffffu, x.y, from),
-                    __shfl_sync(0xffffffffu, x.z, from), __shfl_sync(0xffffffffu, x.w, from));
-}
-__device__ __forceinline__ void shfl8(const Eight<float> &x, int from, Eight<float> &y) {
-  y.a = shfl4(x.a, from);
-  y.b = shfl4(x.b, from);
-}
-template <typename T>
-__device__ __forceinline__ void shfl8(const Eight<T> &x, int from, Eight<T> &y) {
-  y.a = shfl4(x.a, from);
-}
-
-// ---- vector kernel: head_dim a multiple of 8 and at most 256, pairs that lanes do not split ---------
-// A lane has NV vectors of 8 elements; lanes: of a row's group (a power of two >= head_dim / (8 NV)).
-template <typename D, typename P, int NV>
-__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ KvRotaryParams p, int tok, int lanes) {
-  constexpr bool POOL = !Same<P, NoPool>::value;
-  constexpr int EV = 8 * NV, U = kUnroll;
-  __shared__ Places s;
-  extern __shared__ float4 cs4[];
-  float2 *cs = reinterpret_cast<float2 *>(cs4);
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  const KvLayer &L = p.L;
-  const int32_t t0 = (int32_t)blockIdx.x * tok;
-  const int n = p.b.total_tokens - t0 < tok ? p.b.total_tokens - t0 : tok;
-  const int groups = kThreads / lanes, g = threadIdx.x / lanes, sub = threadIdx.x & (lanes - 1);
-  const int ln = threadIdx.x & 31;
-  const bool on = sub * EV < p.head_dim;
-  const int half = p.r.half, hl = half / EV;
-  const bool turned = sub * EV < 2 * half, upper = sub >= hl;  // halves: this lane has second elements of pairs
-  // the lane with the other elements of this one's pairs; its first pair (its own, when neighbours are the pairs)
-  const int from = (ln & ~(lanes - 1)) | (!turned ? sub : upper ? sub - hl : sub + hl);
-  const int pair0 = !turned ? 0 : p.r.interleaved ? sub * (EV / 2) : (upper ? sub - hl : sub) * EV;
-  // Row r of the run is row r % per of token r / per: q's heads, then k's, then v's; a group's rows are `groups` apart.
-  const int kh = POOL ? L.heads : 0, per = p.heads + 2 * kh, rows = n * per, step_i = groups / per, step_w = groups - step_i * per;
-  struct Walk {
-    int i, w;
-  };
-  auto next = [&](Walk &x) {
-    x.w += step_w;
-    x.i += step_i;
-    if (x.w >= per) x.w -= per, ++x.i;
-  };
-  Walk ahead, at;
-  ahead.i = g / per;
-  ahead.w = g - ahead.i * per;
-  at = ahead;
-  Eight<D> x[U][NV];
-  auto load_rows = [&]() {
-#pragma unroll
-    for (int u = 0; u < U; ++u, next(ahead)) {
-      const bool q = ahead.w < p.heads, v = ahead.w >= p.heads + kh;
-      const int head = q ? ahead.w : ahead.w - p.heads - (v ? kh : 0);
-      const uint8_t *src = (const uint8_t *)(q ? p.x : v ? p.v : p.k) +
-                           ((int64_t)(t0 + ahead.i) * (q ? p.x_stride : v ? p.v_stride : p.k_stride) +
-                            (int64_t)head * p.head_dim + sub * EV) * kSize<D>;
-#pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        x[u][e].zero();
-        if (ahead.i < n && on) x[u][e].load(src + e * 8 * kSize<D>);
-      }
-    }
-  };
-  load_rows();
-  if constexpr (POOL) {
-    if (blockIdx.x == 0) check_cu(L, p.b);
-    find_places(L, p.b, t0, n, s);
-  }
-  fill_turns<POOL>(p, t0, n, s, cs);
-  for (int r0 = 0; r0 < rows; r0 += groups * U) {  // the same trips in every thread: the groups shuffle
-    if (r0 > 0) load_rows();
-#pragma unroll
-    for (int u = 0; u < U; ++u, next(at)) {
-      const bool q = at.w < p.heads, v = at.w >= p.heads + kh, turn = turned && !v;
-      const int head = q ? at.w : at.w - p.heads - (v ? kh : 0);
-      int32_t row = at.i < n ? 0 : -2;
-      if constexpr (POOL)
-        if (row == 0) row = s.row[at.i];
-      float y[EV];
-#pragma unroll
-      for (int e = 0; e < NV; ++e) {
-        float f[8], o[8];
-        x[u][e].get(f);
-        const float2 *c = cs + (row == -2 ? 0 : at.i) * half + pair0;
-        if (!p.r.interleaved) {
-          Eight<D> other;
-          shfl8(x[u][e], from, other);
-          other.get(o);
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float4 z = *(const float4 *)(c + e * 8 + i);
-            const float o0 = upper ? o[i] : -o[i], o1 = upper ? o[i + 1] : -o[i + 1];
-            y[8 * e + i] = turn ? fmaf(f[i], z.x, o0 * z.y) : f[i];
-            y[8 * e + i + 1] = turn ? fmaf(f[i + 1], z.z, o1 * z.w) : f[i + 1];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float2 z = c[e * 4 + i / 2];
-            y[8 * e + i] = turn ? fmaf(f[i], z.x, -f[i + 1] * z.y) : f[i];
-            y[8 * e + i + 1] = turn ? fmaf(f[i + 1], z.x, f[i] * z.y) : f[i + 1];
-          }
-        }
-      }
-      auto as_eight = [&](int e) -> const float(&)[8] { return *reinterpret_cast<const float(*)[8]>(&y[8 * e]); };
-      // what is not turned keeps its bits where its type stays
-      auto store_same = [&](uint8_t *dst) {
-#pragma unroll
-        for (int e = 0; e < NV; ++e) {
-          if (turn) x[u][e].put(as_eight(e));
-          x[u][e].store(dst + e * 8 * kSize<D>);
-        }
-      };
-      if (q && row != -2 && on && (turned || p.out != p.x))
-        store_same((uint8_t *)p.out + ((int64_t)(t0 + at.i) * p.out_stride + (int64_t)head * p.head_dim + sub * EV) * kSize<D>);
-      if constexpr (POOL) {
-        uint8_t *page = (v ? L.v : L.k) + (row < 0 ? 0 : s.page[at.i]);
-        const bool put = !q && row >= 0 && on;
-        uint8_t *dst = page + ((int64_t)row * L.heads + head) * held<P>(p.head_dim) + held<P>(sub * EV);
-        if constexpr (Same<P, E4M3>::value) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < EV; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
-          for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const uint32_t sb = scale_byte(m);
-          const float inv = inv_scale_of(sb);
-          uint2 c = make_uint2(
-              __byte_perm(to_e4m3x2(y[0] * inv, y[1] * inv), to_e4m3x2(y[2] * inv, y[3] * inv), 0x5410),
-              __byte_perm(to_e4m3x2(y[4] * inv, y[5] * inv), to_e4m3x2(y[6] * inv, y[7] * inv), 0x5410));
-          if (sb == 255) c = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-          if (put) *(uint2 *)dst = c;
-          if (put && sub == 0) page[L.scale_off + (int64_t)row * L.heads + head] = (uint8_t)sb;
-        } else if constexpr (Same<P, E2M1>::value) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < EV; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
-          const uint32_t sb = e2m1_scale_byte(m);
-          if (put) {
-            *(uint2 *)dst = to_e2m1x16<true>(y, sb);  // a turned element has 24 bits
-            page[L.scale_off + ((int64_t)row * L.heads + head) * (p.head_dim / 16) + sub] = (uint8_t)sb;
-          }
-        } else if (put) {
-          if constexpr (Same<P, D>::value) {
-            store_same(dst);
-          } else {
-            Eight<P> z;
-            z.put(as_eight(0));
-            z.store(dst);
-          }
-        }
-      }
-    }
-  }
-}
-
-// ---- element kernel: any head_dim, rotary_dim, types and alignment ------------------------------
-// A warp takes a row.
 template <bool POOL>
 __global__ void __launch_bounds__(kThreads) rotary_any_kernel(const __grid_constant__ KvRotaryParams p, int tok) {
   __shared__ Places s;
@@ -267,15 +276,16 @@ __global__ void __launch_bounds__(kThreads) rotary_any_kernel(const __grid_const
       const int64_t in = ((int64_t)row * L.heads + head) * D;  // first element within the block
       if (L.dtype == LSC_E2M1) {
         for (int j = ln; j < D / 16; j += 32) {  // a lane has a group
-          float x[16];
+          float x[2][8];
           uint32_t m = 0;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            x[e] = value(16 * j + e);
-            m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+            x[e >> 3][e & 7] = value(16 * j + e);
+            m = max(m, __float_as_uint(x[e >> 3][e & 7]) & 0x7fffffffu);
           }
           const uint32_t sb = e2m1_scale_byte(m);
-          *(uint2 *)(page + (in >> 1) + 8 * j) = to_e2m1x16<true>(x, sb);
+          const E2m1Scale scale = e2m1_scale(sb);
+          *(uint2 *)(page + (in >> 1) + 8 * j) = make_uint2(to_e2m1x8<true>(x[0], scale), to_e2m1x8<true>(x[1], scale));
           page[L.scale_off + (in >> 4) + j] = (uint8_t)sb;
         }
       } else if (L.dtype == LSC_E4M3) {
@@ -296,47 +306,52 @@ __global__ void __launch_bounds__(kThreads) rotary_any_kernel(const __grid_const
   }
 }
 
-template <typename D, typename P, int NV>
-cudaError_t launch_typed(const KvRotaryParams &p, int grid, int tok, size_t smem, cudaStream_t stream) {
-  int lanes = 1;
-  while (lanes * 8 * NV < p.head_dim) lanes <<= 1;
-  return launch_pdl(rotary_kernel<D, P, NV>, grid, kThreads, smem, stream, p, tok, lanes);
+template <typename D, typename P>
+cudaError_t launch_typed(const KvRotaryParams &p, int num_sms, cudaStream_t stream) {
+  FastDiv by_slots;
+  by_slots.set((uint32_t)p.head_dim / 16);
+  const int64_t slots = ((int64_t)p.heads + (p.L.k ? 2 * p.L.heads : 0)) * (p.head_dim / 16);
+  const int per = (int)((slots + 31) / 32);
+  const int grid = walk_grid((int64_t)p.b.total_tokens * per, num_sms, kOcc);
+  return launch_pdl(rotary_kernel<D, P>, grid, kWalkThreads, 0, stream, p, per, by_slots);
 }
 
 template <typename D>
-cudaError_t launch_dense(const KvRotaryParams &p, int grid, int tok, size_t smem, cudaStream_t stream) {
-  if (!p.L.k) return launch_typed<D, NoPool, 1>(p, grid, tok, smem, stream);
+cudaError_t launch_dense(const KvRotaryParams &p, int num_sms, cudaStream_t stream) {
+  if (!p.L.k) return launch_typed<D, NoPool>(p, num_sms, stream);
   switch (p.L.dtype) {
-    case LSC_F32: return launch_typed<D, float, 1>(p, grid, tok, smem, stream);
-    case LSC_BF16: return launch_typed<D, __nv_bfloat16, 1>(p, grid, tok, smem, stream);
-    case LSC_F16: return launch_typed<D, __half, 1>(p, grid, tok, smem, stream);
-    case LSC_E4M3: return launch_typed<D, E4M3, 1>(p, grid, tok, smem, stream);
-    default: return launch_typed<D, E2M1, 2>(p, grid, tok, smem, stream);
+    case LSC_F32: return launch_typed<D, float>(p, num_sms, stream);
+    case LSC_BF16: return launch_typed<D, __nv_bfloat16>(p, num_sms, stream);
+    case LSC_F16: return launch_typed<D, __half>(p, num_sms, stream);
+    case LSC_E4M3: return launch_typed<D, E4M3>(p, num_sms, stream);
+    default: return launch_typed<D, E2M1>(p, num_sms, stream);
   }
 }
 
-}  // namespace
-
-cudaError_t launch_kv_rotary(const KvRotaryParams &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_any(const KvRotaryParams &p, int num_sms, cudaStream_t stream) {
   const int64_t T = p.b.total_tokens;
   // A run of kMaxTok tokens per CTA, shorter while the grid would leave SMs idle.
   int tok = kMaxTok;
   while (tok > 1 && (T + tok - 1) / tok < 2 * (int64_t)num_sms) tok >>= 1;
   const int grid = (int)((T + tok - 1) / tok);
-  const int es = p.dtype == LSC_F32 ? 4 : 2, ev = p.L.k && p.L.dtype == LSC_E2M1 ? 16 : 8;
   const size_t smem = (size_t)tok * p.r.half * sizeof(float2);
+  return p.L.k ? launch_pdl(rotary_any_kernel<true>, grid, kThreads, smem, stream, p, tok)
+               : launch_pdl(rotary_any_kernel<false>, grid, kThreads, smem, stream, p, tok);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_rotary(const KvRotaryParams &p, int num_sms, cudaStream_t stream) {
+  const int es = p.dtype == LSC_F32 ? 4 : 2, slots = p.head_dim / 16;
   uintptr_t mis = (uintptr_t)p.x | (uintptr_t)p.out | (uintptr_t)(p.x_stride * es) | (uintptr_t)(p.out_stride * es);
   if (p.L.k) mis |= (uintptr_t)p.k | (uintptr_t)p.v | (uintptr_t)(p.k_stride * es) | (uintptr_t)(p.v_stride * es);
-  const bool vec = p.head_dim % 8 == 0 && p.head_dim <= 256 && (p.r.interleaved ? 2 : 1) * p.r.half % ev == 0 && (mis & 15) == 0;
-  cudaError_t e;
-  if (!vec) {
-    e = p.L.k ? launch_pdl(rotary_any_kernel<true>, grid, kThreads, smem, stream, p, tok)
-              : launch_pdl(rotary_any_kernel<false>, grid, kThreads, smem, stream, p, tok);
-  } else {
-    e = p.dtype == LSC_F32    ? launch_dense<float>(p, grid, tok, smem, stream)
-        : p.dtype == LSC_BF16 ? launch_dense<__nv_bfloat16>(p, grid, tok, smem, stream)
-                              : launch_dense<__half>(p, grid, tok, smem, stream);
-  }
+  bool vec = p.head_dim % 16 == 0 && p.head_dim <= 512 && p.r.half % 8 == 0 && (mis & 15) == 0;
+  if (p.L.k && p.L.dtype == LSC_E4M3) vec = vec && 32 % slots == 0;  // a head's largest magnitude: its lanes, by shuffles
+  if (p.L.k && p.L.dtype == LSC_E2M1) vec = vec && slots % 2 == 0 && p.r.half % 16 == 0;  // groups are pairs of lanes
+  const cudaError_t e = !vec                   ? launch_any(p, num_sms, stream)
+                        : p.dtype == LSC_F32  ? launch_dense<float>(p, num_sms, stream)
+                        : p.dtype == LSC_BF16 ? launch_dense<__nv_bfloat16>(p, num_sms, stream)
+                                              : launch_dense<__half>(p, num_sms, stream);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

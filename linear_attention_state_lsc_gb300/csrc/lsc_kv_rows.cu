@@ -241,15 +241,16 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const __grid_constan
       for (int d = ln; d < D; d += 32) store_any(dense, at + d, p.dtype, 0.f);
     } else if (L.dtype == LSC_E2M1 && APPEND) {
       for (int j = ln; j < D / 16; j += 32) {  // a lane has a group
-        float x[16];
+        float x[2][8];
         uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          x[e] = load_any(dense, at + 16 * j + e, p.dtype);
-          m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+          x[e >> 3][e & 7] = load_any(dense, at + 16 * j + e, p.dtype);
+          m = max(m, __float_as_uint(x[e >> 3][e & 7]) & 0x7fffffffu);
         }
         const uint32_t sb = e2m1_scale_byte(m);
-        *(uint2 *)(page + (in >> 1) + 8 * j) = to_e2m1x16<true>(x, sb);
+        const E2m1Scale scale = e2m1_scale(sb);
+        *(uint2 *)(page + (in >> 1) + 8 * j) = make_uint2(to_e2m1x8<true>(x[0], scale), to_e2m1x8<true>(x[1], scale));
         page[L.scale_off + (in >> 4) + j] = (uint8_t)sb;
       }
     } else if (L.dtype == LSC_E2M1) {

@@ -87,12 +87,11 @@ __global__ void __launch_bounds__(kWalkThreads, kAppendOcc) append4_kernel(const
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         sb[v] = e2m1_scale_byte(Eight<D>::bits(x[u][v][0].top_with(x[u][v][1])));
-        float lo[8], hi[8], f[16];
-        x[u][v][0].get(lo);
-        x[u][v][1].get(hi);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = lo[e], f[8 + e] = hi[e];
-        code[v] = to_e2m1x16<sizeof(D) == 4>(f, sb[v]);
+        const E2m1Scale scale = e2m1_scale(sb[v]);
+        float f[2][8];
+        x[u][v][0].get(f[0]);
+        x[u][v][1].get(f[1]);
+        code[v] = make_uint2(to_e2m1x8<sizeof(D) == 4>(f[0], scale), to_e2m1x8<sizeof(D) == 4>(f[1], scale));
       }
       load(u);
       const int el = rest * 512 + ln * 16;
