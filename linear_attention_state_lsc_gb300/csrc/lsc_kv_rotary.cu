@@ -38,7 +38,7 @@ using namespace kv::row;
 struct NoPool {};
 
 // ---- vector kernel: head_dim and rotary_dim multiples of 16, head_dim at most 512 ---------
-constexpr int kOcc = 3;
+constexpr int kOcc = 4;
 
 // Lane `ln`'s places of its item: slot 32 rest + ln of the token, head_dim / 16 slots a head.
 struct Slot {

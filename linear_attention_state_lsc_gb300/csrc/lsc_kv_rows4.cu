@@ -143,7 +143,7 @@ struct Item {
   }
 };
 
-constexpr int kGatherOcc = 5;
+constexpr int kGatherOcc = 6;
 
 // U items on the way, a warp
 template <typename D, int NS, int U>
