@@ -258,9 +258,9 @@ struct FastDiv {
   __device__ __forceinline__ int32_t div(int32_t n) const { return (int32_t)(((uint64_t)(uint32_t)n * mul) >> shift); }
 };
 
-// Positions of a decode sub-tile: 8 to 16 KB of K and V rows.
+// Positions of a decode sub-tile: 8 to 16 KB of K and V rows (E2M1: 4 to 8 KB).
 __host__ __device__ constexpr int kv_decode_keys(int head_dim, int bits) {
-  return bits == 16 && head_dim >= 128 ? 16 : 32;
+  return bits == 4 && head_dim <= 128 ? 64 : bits == 16 && head_dim >= 128 ? 16 : 32;
 }
 
 // One attention layer of a K/V pool.

@@ -42,22 +42,31 @@ using rows::mma;
 constexpr int kTK = decode::kTK;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int KEYS = 32;  // positions of a sub-tile: one a lane
-
-template <int D>
+template <int D, int NR>
 struct Conf {
-  static_assert(kv_decode_keys(D, 4) == KEYS, "what the boxes are made for");
+  static constexpr int KEYS = kv_decode_keys(D, 4), HALVES = KEYS / 32;  // positions of a sub-tile; a lane has one of each 32
   static constexpr int RB = D / 2, SB = D / 16;  // bytes of a row's codes and scales
   static constexpr int half = KEYS * RB;         // bytes of a sub-tile's K or V codes
-  static constexpr int ST = D == 64 ? 4 : 3;     // sub-tiles in flight per warp
-  static constexpr int occ = D == 256 ? 2 : D == 128 ? 3 : 4;  // CTAs per SM
+  static constexpr int ST = D == 64 ? 3 : 2;     // sub-tiles in flight per warp
+  static constexpr int occ = D == 256 ? 2 : D == 128 ? (NR == 1 ? 3 : 2) : (NR == 1 ? 4 : 3);  // CTAs per SM
+  static constexpr bool QS = NR == 2;  // q's rows in shared memory: else in registers
 };
 
 template <int D>
+constexpr int occ_of(int rows) {
+  return rows == 8 ? Conf<D, 1>::occ : Conf<D, 2>::occ;
+}
+
+template <int D, int NR>
 struct Smem {
-  using C = Conf<D>;
-  alignas(1024) uint8_t ring[kWarps][C::ST][2][C::half];  // at a piece's end: the warps' weighted rows
-  alignas(16) uint8_t scale[kWarps][C::ST][2][KEYS][C::SB];
+  using C = Conf<D, NR>;
+  static constexpr int PS = D + 4;  // 32-bit columns of a weighted row at a piece's end (no bank twice in what follows)
+  static constexpr int rings = kWarps * C::ST * 2 * C::half, parts = kWarps * 8 * NR * PS * 4;
+  alignas(1024) uint8_t ring[rings > parts ? rings : parts];  // [warp][sub-tile][K, V]; at a piece's end: the warps' weighted rows
+  alignas(16) uint8_t scale[kWarps][C::ST][2][C::KEYS][C::SB];
+  // V's scales of 32 positions as f16, by group: positions 2 tq, 2 tq + 1 of each 8 side by side for lane tq
+  alignas(16) uint16_t v_scale[kWarps][C::SB][32];
+  alignas(16) uint4 q[C::QS ? kWarps : 1][C::QS ? 8 * NR : 1][C::QS ? D / 8 : 1];  // neighbouring rows' chunks xor 4: no bank twice
   float2 ml[kWarps][16];
   int32_t vis[16];
   int32_t bad[kWarps][C::SB];  // by head of the unit and group: the first position whose v is NaN
@@ -72,35 +81,21 @@ __device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, 
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
 }
 
-// SB scale bytes of a position, in 32-bit words.
-template <int SB>
-__device__ __forceinline__ void load_scales(uint32_t (&w)[SB / 4], const uint8_t *p) {
-  if constexpr (SB == 4) w[0] = *(const uint32_t *)p;
-  if constexpr (SB == 8) {
-    const uint2 x = *(const uint2 *)p;
-    w[0] = x.x, w[1] = x.y;
-  }
-  if constexpr (SB == 16) {
-    const uint4 x = *(const uint4 *)p;
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-  }
-}
-
 __device__ __forceinline__ uint32_t times(uint32_t h, uint32_t s) {
   const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&s));
   return *reinterpret_cast<const uint32_t *>(&y);
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kThreads, (Conf<D>::occ))
+__global__ void __launch_bounds__(kThreads, (Conf<D, NR>::occ))
 decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map, int together) {
-  using C = Conf<D>;
+  using C = Conf<D, NR>;
   constexpr int M = 8 * NR;         // rows of a head, NR tiles of 8
-  constexpr int ST = C::ST, RB = C::RB, SB = C::SB, NC = D / 32;  // NC: 16-byte chunks of a row, 32 elements each
+  constexpr int KEYS = C::KEYS, HALVES = C::HALVES, ST = C::ST, RB = C::RB, SB = C::SB, NC = D / 32;  // NC: 16-byte chunks of a row, 32 elements each
   constexpr int KS = D / 16;        // output tiles of 16 columns
   constexpr float lift = 7.f;       // powers of two that the reference lies below the maximum that set it
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+  Smem<D, NR> &sm = *reinterpret_cast<Smem<D, NR> *>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31, g = ln >> 2, tq = ln & 3;
   if (tid < kWarps * ST) mbar_init(&sm.full[tid / ST][tid % ST], 1);
   fence_mbar_init();
@@ -121,11 +116,11 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
   // TMA boxes of `box` rows: K's on lanes 0-15, V's on 16-31
   const int box = p.box_decode, boxes = KEYS / box;
   const int bi = ln & 15, br = bi < boxes ? bi * box : 0;
-  uint8_t *const ring = sm.ring[w][0][0];
-  // where a lane's scale bytes are in a word: its group of a chunk (K: by tq, V: by g), for even and odd chunks
-  const uint32_t kh = tq >> 1, vh = g >> 2;
-  const uint32_t ksel[2] = {0x4040u | kh | kh << 8, 0x4040u | (kh + 2) | (kh + 2) << 8};
-  const uint32_t vsel[2] = {vh | (vh + 4) << 8, (vh + 2) | (vh + 6) << 8};
+  uint8_t *const ring = sm.ring + w * ST * 2 * C::half;
+  // where a lane's K scale bytes are in a word: its group of an even chunk and of the odd one behind it
+  // ldmatrix rows: chunk c of K (c even) and V is the offset of chunk 0 xor 16 c
+  const uint32_t koff = chunk_at<RB>(KEYS, ln & 15, ln >> 4), voff = chunk_at<RB>(KEYS, ln, 0);
+  const uint32_t kh = tq >> 1, ksel = 0x4040u | kh | (kh + 2) << 8;
   int slot = 0;
   uint32_t phase = 0;
   __syncthreads();
@@ -135,75 +130,102 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
     const int32_t *table = p.b.table + (int64_t)pc.seq * p.b.max_blocks;
     const int nsub = hi > lo ? (hi - lo + KEYS - 1) / KEYS : 0, mine = nsub > wsp ? (nsub - wsp + splits - 1) / splits : 0, head = pc.head * together + wh;
     auto first_of = [&](int i) { return lo + (i * splits + wsp) * KEYS; };  // first position of this warp's sub-tile i
-    // Block of this lane's position of sub-tile i, 0 behind the last one.  Looked up a sub-tile ahead and checked only
-    // where it is used (a bad one is recorded and read as 0): a look at it any earlier would wait for the load.
-    auto block_at = [&](int i) {
-      const int32_t pos = first_of(i) + ln;
-      return i < mine && pos < kv ? __ldg(table + L.by_block.div(pos)) : 0;
-    };
-    auto issue = [&](int i, int st, int32_t blk) {
-      if ((uint32_t)blk >= (uint32_t)L.num_blocks) {
-        report(L.status, LSC_ERR_OUT_OF_RANGE);
-        blk = 0;
+    // Blocks of this lane's positions of sub-tile i, 0 behind the last one.  Looked up a sub-tile ahead and checked only
+    // where they are used (a bad one is recorded and read as 0): a look at them any earlier would wait for the loads.
+    int32_t blk[HALVES];
+    auto look_up = [&](int i) {
+#pragma unroll
+      for (int u = 0; u < HALVES; ++u) {
+        const int32_t pos = first_of(i) + 32 * u + ln;
+        blk[u] = i < mine && pos < kv ? __ldg(table + L.by_block.div(pos)) : 0;
       }
-      const int32_t pos = first_of(i) + ln, row = pos - L.by_block.div(pos) * L.block_tokens;
+    };
+    const int64_t lane_off = L.v - L.k;
+    auto issue = [&](int i, int st) {
+      const int32_t first = first_of(i);
+      int32_t row[HALVES];
       if (ln == 0) mbar_arrive_expect_tx(&sm.full[w][st], 2 * C::half);
       __syncwarp();
-      const int32_t box_blk = __shfl_sync(0xffffffffu, blk, br), box_row = __shfl_sync(0xffffffffu, row, br);
+#pragma unroll
+      for (int u = 0; u < HALVES; ++u) {
+        if ((uint32_t)blk[u] >= (uint32_t)L.num_blocks) {
+          report(L.status, LSC_ERR_OUT_OF_RANGE);
+          blk[u] = 0;
+        }
+        const int32_t pos = first + 32 * u + ln;
+        row[u] = pos - L.by_block.div(pos) * L.block_tokens;
+        const bool on = pos < kv;
+        const uint8_t *k = L.k + (on ? (int64_t)blk[u] * L.page + L.scale_off + ((int64_t)row[u] * L.heads + head) * SB : 0);
+        cp_async_or_zero<SB>(smem_u32(sm.scale[w][st][0][32 * u + ln]), k, on);
+        cp_async_or_zero<SB>(smem_u32(sm.scale[w][st][1][32 * u + ln]), k + lane_off, on);
+      }
+      int32_t box_blk = __shfl_sync(0xffffffffu, blk[0], br & 31), box_row = __shfl_sync(0xffffffffu, row[0], br & 31);
+      if constexpr (HALVES == 2) {
+        const int32_t b1 = __shfl_sync(0xffffffffu, blk[1], br & 31), r1 = __shfl_sync(0xffffffffu, row[1], br & 31);
+        if (br >= 32) box_blk = b1, box_row = r1;
+      }
       if (bi < boxes)
         tma_box(ring + (st * 2 + (ln >> 4)) * C::half + br * RB, &map, box_row, 0, head,
                 box_blk + (ln < 16 ? 0 : L.num_blocks), &sm.full[w][st]);
-      const int64_t at = (int64_t)blk * L.page + L.scale_off + ((int64_t)row * L.heads + head) * SB;
-      const bool on = pos < kv;
-      cp_async_or_zero<SB>(smem_u32(sm.scale[w][st][0][ln]), L.k + (on ? at : 0), on);
-      cp_async_or_zero<SB>(smem_u32(sm.scale[w][st][1][ln]), L.v + (on ? at : 0), on);
     };
     int st_in = slot;
 #pragma unroll
     for (int i = 0; i < ST; ++i) {
       if (i < mine) {
-        issue(i, st_in, block_at(i));
+        look_up(i);
+        issue(i, st_in);
         if (++st_in == ST) st_in = 0;
       }
       cp_async_commit();
     }
-    int32_t next_blk = block_at(ST);
+    look_up(ST);
 
     if (tid < M) sm.vis[tid] = tid < R ? visible(pc.s, p.by_group.div(tid), p.causal) : 0;
-    // q as operand registers: row g of each 8, elements 8 tq .. 8 tq + 7 of each 32, as f16
-    uint32_t qf[NR][NC][4];
+    // q as operands: row g of each 8, elements 8 tq .. 8 tq + 7 of each 32, as f16
+    uint32_t qf[C::QS ? 1 : NR][C::QS ? 1 : NC][4];
     float q_up[NR];  // of row g: scale * log2 e, times the power of two that bf16 rows were brought down by
 #pragma unroll
     for (int h = 0; h < NR; ++h) {
       const int r = 8 * h + g, tok = p.by_group.div(r);
       const uint16_t *src = (const uint16_t *)p.q + (int64_t)(pc.s.row0 + tok) * p.q_stride +
                             (int64_t)(head * p.group + (r - tok * p.group)) * D;
+      uint32_t x[NC][4];
       q_up[h] = p.scale_log2;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const uint4 x = r < R ? *(const uint4 *)(src + c * 32 + 8 * tq) : make_uint4(0, 0, 0, 0);
-        qf[h][c][0] = x.x, qf[h][c][1] = x.y, qf[h][c][2] = x.z, qf[h][c][3] = x.w;
+        const uint4 y = r < R ? *(const uint4 *)(src + c * 32 + 8 * tq) : make_uint4(0, 0, 0, 0);
+        x[c][0] = y.x, x[c][1] = y.y, x[c][2] = y.z, x[c][3] = y.w;
       }
       if (p.dtype == LSC_BF16) {
         uint32_t top = 0;  // magnitudes of 16-bit floats order as whole numbers
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = __vmaxu2(top, qf[h][c][e] & 0x7fff7fffu);
+          for (int e = 0; e < 4; ++e) top = __vmaxu2(top, x[c][e] & 0x7fff7fffu);
         top = max(top & 0xffffu, top >> 16);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const uint32_t ex = top >> 7;  // 2^k <= the largest magnitude < 2^(k + 1), where that is a normal number
         const bool plain = ex == 0 || ex == 255;
         const float down = plain ? 1.f : inv_scale_of(ex), more = plain ? 1.f : 16384.f;
-        if (!plain) q_up[h] = q_up[h] * __uint_as_float(ex << 23) * (1.f / 16384.f);
+        // (a hidden score is -infinity times this, so it may not be 0; products of q and k are below 2^39)
+        if (!plain) q_up[h] = fmaxf(q_up[h] * __uint_as_float(ex << 23) * (1.f / 16384.f), 0x1p-120f);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t b = qf[h][c][e];
-            qf[h][c][e] = pack2(__uint_as_float(b << 16) * down * more, __uint_as_float(b & 0xffff0000u) * down * more, 0);
+            const uint32_t b = x[c][e];
+            x[c][e] = pack2(__uint_as_float(b << 16) * down * more, __uint_as_float(b & 0xffff0000u) * down * more, 0);
           }
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if constexpr (C::QS) {
+          sm.q[w][r][(c * 4 + tq) ^ (r & 1) * 4] = make_uint4(x[c][0], x[c][1], x[c][2], x[c][3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qf[h][c][e] = x[c][e];
+        }
       }
     }
     // scores come with rows 2 tq, 2 tq + 1 of each 8
@@ -215,11 +237,11 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
     __syncthreads();  // vis; and the last piece's shared memory is free
     const int32_t sure = visible(pc.s, 0, p.causal);  // every row sees positions below this
     int32_t vis[NR][2];
-    float m[NR][2], l[NR][2], o[NR][KS][4];
+    float m[NR][2], ref[NR][2], l[NR][2], o[NR][KS][4];  // ref: m, 0 while no position has been seen
 #pragma unroll
     for (int h = 0; h < NR; ++h) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) vis[h][e] = sm.vis[8 * h + 2 * tq + e], m[h][e] = -INFINITY, l[h][e] = 0.f;
+      for (int e = 0; e < 2; ++e) vis[h][e] = sm.vis[8 * h + 2 * tq + e], m[h][e] = -INFINITY, ref[h][e] = l[h][e] = 0.f;
 #pragma unroll
       for (int n = 0; n < KS; ++n) o[h][n][0] = o[h][n][1] = o[h][n][2] = o[h][n][3] = 0.f;
     }
@@ -230,80 +252,102 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
       const int32_t first = first_of(i);
       cp_async_wait<ST - 1>();
       if (!(ok = wait_warp(&sm.full[w][slot], phase, p.wait_limit_ns))) break;
-      __syncwarp();
+      __syncwarp();  // every lane's scales are there
       const uint32_t ka = smem_u32(ring + slot * 2 * C::half), va = ka + C::half;
-      const uint8_t *kscale = sm.scale[w][slot][0][0], *vscale = sm.scale[w][slot][1][0];
-      if (first + KEYS > sure) {  // (some of) V's scales need a look before they meet a weight of 0
-        if (first + ln >= sure && first + ln < hi) {
-          uint8_t *v = sm.scale[w][slot][1][ln];
+      const uint8_t *kscale = sm.scale[w][slot][0][0];
 #pragma unroll 1
-          for (int x = 0; x < SB; ++x)
-            if (v[x] > kE2M1Top) {
-              atomicMin(&sm.bad[wh][x], first + ln);
-              sm.any_bad = 1;
-              v[x] = 0;
-            }
+      for (int u = 0; u < HALVES && (u == 0 || first + 32 * u < hi); ++u) {  // 32 positions at a time
+        const int32_t first32 = first + 32 * u;
+        {
+          // V's scales to f16, a position a lane.  Where some row does not see the position they need a look before they
+          // meet a weight of 0.
+          const int32_t pos = first32 + ln;
+          uint32_t b[SB / 4];
+#pragma unroll
+          for (int x = 0; x < SB / 4; ++x) b[x] = *(const uint32_t *)&sm.scale[w][slot][1][32 * u + ln][4 * x];
+          if (first32 + 32 > sure && pos >= sure && pos < hi) {
+#pragma unroll
+            for (int x = 0; x < SB; ++x)
+              if ((b[x / 4] >> (x % 4 * 8) & 0xff) > kE2M1Top) {
+                atomicMin(&sm.bad[wh][x], pos);
+                sm.any_bad = 1;
+                b[x / 4] &= ~(0xffu << (x % 4 * 8));
+              }
+          }
+          uint16_t *to = sm.v_scale[w][0] + (ln >> 1 & 3) * 8 + (ln >> 3) * 2 + (ln & 1);
+          __syncwarp();  // the last ones have been read
+#pragma unroll
+          for (int x = 0; x < SB / 4; ++x) {
+            const uint32_t even = (b[x] & 0x00ff00ffu) << 7, odd = (b[x] & 0xff00ff00u) >> 1;  // bytes 0 and 2, 1 and 3
+            to[(4 * x) * 32] = (uint16_t)even, to[(4 * x + 1) * 32] = (uint16_t)odd;
+            to[(4 * x + 2) * 32] = (uint16_t)(even >> 16), to[(4 * x + 3) * 32] = (uint16_t)(odd >> 16);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
       // ---- scores: lane (g, tq) gets positions g, g + 8 of each 16 and rows 2 tq, 2 tq + 1 of each 8
-      // (two sums a tile, all tiles in turn: a product waits for the one before it in its sum)
-      float s[2][NR][4], s2[2][NR][4];
+      float s[2][NR][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int h = 0; h < NR; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][h][e] = s2[n][h][e] = 0.f;
-      {
-        uint32_t ks[4][SB / 4];  // of positions g + 8 y
+          for (int e = 0; e < 4; ++e) s[n][h][e] = 0.f;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) load_scales<SB>(ks[y], kscale + (g + 8 * y) * SB);
+      for (int c = 0; c < NC; c += 2) {
+        uint32_t ks[4];  // chunk c's and c + 1's scales (f16) of positions g + 8 y
 #pragma unroll
-        for (int c = 0; c < NC; c += 2)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            uint32_t b[4];
-            ldsm4(b, ka + chunk_at<RB>(KEYS, 16 * n + (ln & 15), c + (ln >> 4)));
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {  // chunk c + y
-              uint32_t x[2][4];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {  // positions g, g + 8
-                const uint32_t sc = __byte_perm(ks[2 * n + z][c >> 1], 0, ksel[y]) << 7;
-                e2m1x8_times(b[2 * y + z], *reinterpret_cast<const __half2 *>(&sc), x[z]);
-              }
-              const uint32_t a0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]}, a1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
-#pragma unroll
-              for (int h = 0; h < NR; ++h) {
-                mma<false>(s[n][h], a0, qf[h][c + y][0], qf[h][c + y][1]);
-                mma<false>(s2[n][h], a1, qf[h][c + y][2], qf[h][c + y][3]);
-              }
-            }
-          }
-      }
-      // ---- weights
-      float top[NR][2];
-#pragma unroll
-      for (int h = 0; h < NR; ++h) top[h][0] = top[h][1] = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int key = 16 * n + 8 * y + g;
+        for (int y = 0; y < 4; ++y) ks[y] = __byte_perm(*(const uint32_t *)(kscale + (32 * u + g + 8 * y) * SB + 2 * c), 0, ksel) << 7;
+        uint32_t qs[NR][2][4];  // QS: both chunks' q
+        if constexpr (C::QS) {
 #pragma unroll
           for (int h = 0; h < NR; ++h)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = (s[n][h][2 * y + e] + s2[n][h][2 * y + e]) * qsc[h][e];
-              x = first + key < vis[h][e] ? x : -INFINITY;
-              s[n][h][2 * y + e] = x;
-              top[h][e] = fmaxf(top[h][e], x);
+            for (int y = 0; y < 2; ++y) {
+              const uint4 x = sm.q[w][8 * h + g][((c + y) * 4 + tq) ^ (g & 1) * 4];
+              qs[h][y][0] = x.x, qs[h][y][1] = x.y, qs[h][y][2] = x.z, qs[h][y][3] = x.w;
             }
         }
-      bool rise = false;
 #pragma unroll
-      for (int h = 0; h < NR; ++h) rise |= top[h][0] > m[h][0] + (8.f + lift) || top[h][1] > m[h][1] + (8.f + lift);
+        for (int n = 0; n < 2; ++n) {
+          uint32_t b[4];
+          ldsm4(b, ka + u * (32 * RB) + (koff ^ c << 4) + n * (16 * RB));
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {  // chunk c + y
+            auto q_of = [&](int h, int e) { return C::QS ? qs[h][y][e] : qf[C::QS ? 0 : h][C::QS ? 0 : c + y][e]; };
+            uint32_t x[2][4];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {  // positions g, g + 8
+              const __half2 sc = *reinterpret_cast<const __half2 *>(&ks[2 * n + z]);
+              e2m1x8_times(b[2 * y + z], y ? __high2half2(sc) : __low2half2(sc), x[z]);
+            }
+            const uint32_t a0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]}, a1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
+#pragma unroll
+            for (int h = 0; h < NR; ++h) {
+              mma<false>(s[n][h], a0, q_of(h, 0), q_of(h, 1));
+              mma<false>(s[n][h], a1, q_of(h, 2), q_of(h, 3));
+            }
+          }
+        }
+      }
+      // ---- weights
+      if (first32 + 32 > sure) {  // positions that some row does not see
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int h = 0; h < NR; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (first32 + 16 * n + 8 * (e >> 1) + g >= vis[h][e & 1]) s[n][h][e] = -INFINITY;
+      }
+      bool rise = false;
+      float top[NR][2];
+#pragma unroll
+      for (int h = 0; h < NR; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[h][e] = fmaxf(fmaxf(s[0][h][e], s[0][h][2 + e]), fmaxf(s[1][h][e], s[1][h][2 + e])) * qsc[h][e];
+          rise |= top[h][e] > m[h][e] + (8.f + lift);
+        }
       if (__any_sync(0xffffffffu, rise)) {  // also the first one's (m is -inf)
 #pragma unroll
         for (int h = 0; h < NR; ++h)
@@ -313,7 +357,9 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            const float to = fmaxf(m[h][e], t - lift), f = ex2(m[h][e] - (to == -INFINITY ? 0.f : to));
+            const float to = fmaxf(m[h][e], t - lift);
+            ref[h][e] = to == -INFINITY ? 0.f : to;
+            const float f = ex2(m[h][e] - ref[h][e]);
             m[h][e] = to;
             l[h][e] *= f;
 #pragma unroll
@@ -323,54 +369,49 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
       uint32_t a[2][NR][2];
 #pragma unroll
       for (int h = 0; h < NR; ++h) {
-        const float r0 = m[h][0] == -INFINITY ? 0.f : m[h][0], r1 = m[h][1] == -INFINITY ? 0.f : m[h][1];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float p0 = ex2(s[n][h][2 * y] - r0), p1 = ex2(s[n][h][2 * y + 1] - r1);
+            const float p0 = ex2(fmaf(s[n][h][2 * y], qsc[h][0], -ref[h][0])), p1 = ex2(fmaf(s[n][h][2 * y + 1], qsc[h][1], -ref[h][1]));
             l[h][0] += p0;
             l[h][1] += p1;
             a[n][h][y] = transposed(pack2(p0, p1, 0));
           }
       }
       // ---- V^T times weights
-      {
-        uint32_t vs[8][SB / 4];  // of positions 8 x + 2 tq, + 1
 #pragma unroll
-        for (int x = 0; x < 8; ++x) load_scales<SB>(vs[x], vscale + (8 * (x >> 1) + 2 * tq + (x & 1)) * SB);
+      for (int c = 0; c < NC; ++c) {  // 32 columns: m index g is column 4 g (+ 2), m index g + 8 the one behind it
+        uint32_t b[4];
+        ldsm4t(b, va + u * (32 * RB) + (voff ^ c << 4));
+        const uint4 sv4 = *(const uint4 *)&sm.v_scale[w][2 * c + (g >> 2)][tq * 8];  // of positions 2 tq, 2 tq + 1 of each 8
+        const uint32_t sv[4] = {sv4.x, sv4.y, sv4.z, sv4.w};
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {  // 32 columns: m index g is column 4 g (+ 2), m index g + 8 the one behind it
-          uint32_t b[4];
-          ldsm4t(b, va + chunk_at<RB>(KEYS, ln, c));
+        for (int n = 0; n < 2; ++n) {
+          uint32_t x[2][4];  // columns 4 g .. 4 g + 3 of positions 2 tq, 2 tq + 1 and 8 further
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            uint32_t x[2][4];  // columns 4 g .. 4 g + 3 of positions 2 tq, 2 tq + 1 and 8 further
+          for (int y = 0; y < 2; ++y) {
+            uint32_t h[4];
+            e2m1x8_to_f16(b[2 * n + y], h);
+            x[y][0] = times(__byte_perm(h[0], h[2], 0x5410), sv[2 * n + y]);
+            x[y][1] = times(__byte_perm(h[0], h[2], 0x7632), sv[2 * n + y]);
+            x[y][2] = times(__byte_perm(h[1], h[3], 0x5410), sv[2 * n + y]);
+            x[y][3] = times(__byte_perm(h[1], h[3], 0x7632), sv[2 * n + y]);
+          }
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              uint32_t h[4];
-              e2m1x8_to_f16(b[2 * n + y], h);
-              // the group's bytes of both positions, in the lower byte of a half each
-              const uint32_t sv = (__byte_perm(vs[4 * n + 2 * y][c >> 1], vs[4 * n + 2 * y + 1][c >> 1], vsel[c & 1]) & 0x00ff00ffu) << 7;
-              x[y][0] = times(__byte_perm(h[0], h[2], 0x5410), sv);
-              x[y][1] = times(__byte_perm(h[0], h[2], 0x7632), sv);
-              x[y][2] = times(__byte_perm(h[1], h[3], 0x5410), sv);
-              x[y][3] = times(__byte_perm(h[1], h[3], 0x7632), sv);
-            }
+          for (int z = 0; z < 2; ++z) {
+            const uint32_t v[4] = {x[0][2 * z], x[0][2 * z + 1], x[1][2 * z], x[1][2 * z + 1]};
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t v[4] = {x[0][2 * z], x[0][2 * z + 1], x[1][2 * z], x[1][2 * z + 1]};
-#pragma unroll
-              for (int h = 0; h < NR; ++h) mma<false>(o[h][2 * c + z], v, a[n][h][0], a[n][h][1]);
-            }
+            for (int h = 0; h < NR; ++h) mma<false>(o[h][2 * c + z], v, a[n][h][0], a[n][h][1]);
           }
         }
+      }
       }
       // ---- the slot's next sub-tile
       __syncwarp();
       if (i + ST < mine) {
-        issue(i + ST, slot, next_blk);
-        next_blk = block_at(i + ST + 1);
+        issue(i + ST, slot);
+        look_up(i + ST + 1);
       }
       cp_async_commit();
       if (++slot == ST) slot = 0, phase ^= 1;
@@ -395,9 +436,7 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
       }
     ok = __syncthreads_and(ok);
     if (!ok) break;
-    // [row][column] of 32 bits, rows padded by 4 (D + 4: no bank twice in what follows); the rings are empty
-    constexpr int PS = D + 4;
-    static_assert(sizeof(sm.ring) >= (size_t)kWarps * 16 * PS * 4, "the parts fit");
+    constexpr int PS = Smem<D, NR>::PS;  // the rings are empty
     float *parts = (float *)sm.ring;
 #pragma unroll
     for (int h = 0; h < NR; ++h)
@@ -459,7 +498,8 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
 template <int D, int NR>
 cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
   static SmemLimit limit;
-  const int smem = (int)sizeof(Smem<D>);
+  const int smem = (int)sizeof(Smem<D, NR>);
+  static_assert(Conf<D, NR>::occ * (sizeof(Smem<D, NR>) + 1024) <= 228 * 1024, "CTAs that an SM holds at once");
   auto *k = decode4_attend_kernel<D, NR>;
   const cudaError_t e = limit.ensure((const void *)k, smem);
   if (e != cudaSuccess) return e;
