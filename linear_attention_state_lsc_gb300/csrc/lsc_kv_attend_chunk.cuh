@@ -86,8 +86,8 @@ struct Conf {
   static constexpr int slot = TK * row;         // bytes of a K or V tile
   static constexpr int NS = Q8 ? (D == 128 ? 6 : 8) : Q4 ? (D == 64 ? 8 : D == 128 ? 3 : 4) : (D == 64 ? 8 : D == 128 ? 4 : 6);
   static constexpr int SR = Q8 ? 8 : 1;         // E4M3: tiles whose scales are held
-  // warps: 0-7 softmax, 8 MMA, 9 K, 10 V, 11 idle; E2M1: K 12-15, V 9-11, or, with one row block, whose softmax does with
-  // fewer registers, 16-19
+  // warps: 0-7 softmax, 8 MMA, 9 K, 10 V, 11 idle; E2M1: 9-15 K and V in turn, or, with one row block, whose softmax does
+  // with fewer registers, 12-15 K and 16-19 V
   static constexpr int threads = !Q4 ? 384 : NQ == 2 ? 512 : 640;
   static constexpr int NH = 2 / NQ;             // threads of a row
   static constexpr int HC = TK / NH;            // columns of a thread
@@ -97,9 +97,10 @@ struct Conf {
   static_assert(2 * soft + (groups - 2) * mma <= groups * launch, "more registers than the block has");
   // E2M1: of a warp's 32 lanes, a 16-byte piece of a row's codes each, 2 lanes side by side, 4 rows, the other pieces, rows
   static constexpr int pieces = D / 32, RW = 32 / pieces;
-  static constexpr int VW = NQ == 2 ? 3 : 4, v_warp = NQ == 2 ? 9 : 16;            // V's warps (K: 4, from 12)
-  static constexpr int k_units = Q4 ? TK / (4 * RW) : 1, v_units = Q4 ? (TK / RW + VW - 1) / VW : 1;
-  static constexpr int LAG = !Q4 ? 0 : D == 128 ? 1 : 2;  // K and V tiles of codes on the way
+  static constexpr bool both = NQ == 2;
+  static constexpr int PW = both ? 7 : 4, k_warp = both ? 9 : 12;  // producer warps of a tile; the first of K's
+  static constexpr int units = Q4 ? (TK / RW + PW - 1) / PW : 1;
+  static constexpr int LAG = !Q4 ? 0 : D == 64 ? 3 : 2;  // tiles of codes on the way to a producer
   // powers of two: how far a row's maximum may rise above the one that set the reference, and how far the reference
   // lies below that (f16 weights, whose smallest is 2^-24, take the room up to 2^15; bf16 has the exponents as it is)
   static constexpr float lag = Q8 ? 6.f : 8.f, lift = Q8 ? 9.f : BF16 ? 0.f : 7.f;
@@ -118,8 +119,9 @@ struct Smem {
   alignas(16) float ks[C::SR][Q8 ? C::TK : 4], ve[C::SR][Q8 ? C::TK : 4], vs[C::SR][Q8 ? C::TK : 4];
   float up[8][32];        // E4M3, E2M1, by softmax warp: the power of two of a row of q
   // E2M1, by producer thread: its pieces, and the words that hold their scale bytes
-  alignas(16) uint4 kcodes[C::LAG + 1][C::k_units][Q4 ? 128 : 1], vcodes[C::LAG + 1][C::v_units][Q4 ? C::VW * 32 : 1];
-  uint32_t kwords[C::LAG + 1][C::k_units][Q4 ? 128 : 1], vwords[C::LAG + 1][C::v_units][Q4 ? C::VW * 32 : 1];
+  static constexpr int staged = Q4 ? 32 * C::PW * (C::both ? 1 : 2) : 1;
+  alignas(16) uint4 codes[C::LAG + 1][C::units][staged];
+  uint32_t words[C::LAG + 1][C::units][staged];
   alignas(16) uint8_t rows[8][32][80];  // by softmax warp: 64 bytes of each of its rows, between TMEM and memory
   int32_t bad[Q8 ? 1 : 3][Q8 ? 1 : D];  // first position whose v is NaN, +inf, -inf
   uint64_t full[C::NS], empty[C::NS], sfull[2], phalf[2], pfull[2], qfull[2], odone[2], fin[2], met, drain;
@@ -302,11 +304,6 @@ struct Ring {
   }
 };
 
-template <int N>
-struct Int {
-  static constexpr int value = N;
-};
-
 // BF16: the products' type (f16 for E2M1 pools).  Q8: E4M3 pools.  Q4: E2M1 pools.
 template <bool BF16, bool Q8, int D, bool Q4>
 __global__ void __launch_bounds__((Conf<D, Q8, BF16, Q4>::threads), 1)
@@ -325,7 +322,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   if (C::NH == 2)
     for (int i = tid; i < 2 * 8 * 32; i += C::threads) (&sm.told[0][0][0])[i] = ~0ull;  // no turn's number
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], Q4 ? 4 : 1), mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], Q4 ? C::PW : 1), mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < C::SR; ++i) mbar_init(&sm.scaled[i], 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.sfull[i], 1), mbar_init(&sm.phalf[i], 4), mbar_init(&sm.pfull[i], 4 * C::NH), mbar_init(&sm.qfull[i], 4 * C::NH);
@@ -817,21 +814,20 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
     // A thread has the same 16 bytes of codes (32 elements) in some rows of each K or V tile: it copies them, and the
     // words with their scale bytes, to shared memory of its own (LAG tiles ahead, so no other thread has to be waited
     // for), and writes them out as f16; 4 rows and two pieces side by side an instruction, which meet no bank twice.
-    auto produce = [&](auto units_c, auto &codes, auto &words, const uint8_t *base, int first_slot, int wi, auto warps_c) {
-      constexpr int U = decltype(units_c)::value, W = decltype(warps_c)::value;
-      constexpr int cb = C::pieces == 8 ? 2 : C::pieces == 4 ? 1 : 0;
-      const int pt = wi * 32 + ln, rest = ln >> 3;
+    if (w >= C::k_warp && w < C::k_warp + C::PW * (C::both ? 1 : 2)) {
+      constexpr int U = C::units, W = C::PW, cb = C::pieces == 8 ? 2 : C::pieces == 4 ? 1 : 0;
+      const int pw = w - C::k_warp, wi = pw % W, pt = pw * 32 + ln, rest = ln >> 3;
       const int piece = (ln & 1) + 2 * (rest & ((1 << cb) - 1)), row0 = (ln >> 1 & 3) + 4 * (rest >> cb) + C::RW * wi;
       auto row_of = [&](int u) { return row0 + C::RW * W * u; };
-      auto has = [&](int u) { return TK % (C::RW * W) == 0 || u < U - 1 || row_of(u) < TK; };  // the same in a warp
-      Ring<NS> at(first_slot);
-      int pending = 0, in = 0, out = 0;
+      auto has = [&](int u) { return TK % (C::RW * W) == 0 || u < U - 1 || C::RW * (W * u + wi) < TK; };  // the same in a warp
+      int slot = C::both ? 0 : pw / W, pending = 0, in = 0, out = 0;
+      uint32_t phase = 0;
       int32_t blk[U];  // of the next tile's rows; looked at a tile later
       auto look_up = [&](int j) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int32_t pos = (pc.t0 + j) * TK + row_of(u);
-          blk[u] = pos < pc.s.kv ? __ldg(p.b.table + (int64_t)pc.seq * p.b.max_blocks + L.by_block.div(pos)) : 0;
+          blk[u] = has(u) && pos < pc.s.kv ? __ldg(p.b.table + (int64_t)pc.seq * p.b.max_blocks + L.by_block.div(pos)) : 0;
         }
       };
       // the oldest tile on the way, as f16 into the ring
@@ -840,9 +836,9 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         uint4 c[U];
         uint32_t sc[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) c[u] = codes[out][u][pt], sc[u] = words[out][u][pt];
-        if (!(ok = wait_warp(&sm.empty[at.slot], at.phase ^ 1, limit))) return;
-        uint8_t *dst = sm.ring[at.slot];
+        for (int u = 0; u < U; ++u) c[u] = sm.codes[out][u][pt], sc[u] = sm.words[out][u][pt];
+        if (!(ok = wait_warp(&sm.empty[slot], phase ^ 1, limit))) return;
+        uint8_t *dst = sm.ring[slot];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (!has(u)) break;
@@ -856,48 +852,58 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (ln < (W == 3 && wi == 0 ? 2 : 1)) mbar_arrive(&sm.full[at.slot]);  // four in all
-        at.step();
+        if (ln == 0) mbar_arrive(&sm.full[slot]);
+        slot += C::both ? 1 : 2;
+        if (slot >= NS) slot -= NS, phase ^= 1;
         if (++out == C::LAG + 1) out = 0;
         --pending;
       };
+      const int64_t lane_off = L.v - L.k;
       while (ok && next_piece<M, TK>(p, run, pc)) {
         const int nt = pc.t1 - pc.t0;
-        const uint8_t *from = base + pc.head * (D / 2) + piece * 16;
-        const uint8_t *scales = base + L.scale_off + pc.head * (D / 16) + (piece >> 1) * 4;
+        const uint8_t *codes = L.k + pc.head * (D / 2) + piece * 16;
+        const uint8_t *scales = L.k + L.scale_off + pc.head * (D / 16) + (piece >> 1) * 4;
         const int32_t row_bytes = L.heads * (D / 2), row_scales = L.heads * (D / 16);  // a block is below 2 GiB
         look_up(0);
         for (int j = 0; j < nt && ok; ++j) {
+          int32_t row[U];
+          int64_t page[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            if (!has(u)) break;
-            const int32_t pos = (pc.t0 + j) * TK + row_of(u), r = pos - L.by_block.div(pos) * L.block_tokens;
+            const int32_t pos = (pc.t0 + j) * TK + row_of(u);
             if ((uint32_t)blk[u] >= (uint32_t)L.num_blocks) {
               report(L.status, LSC_ERR_OUT_OF_RANGE);
               blk[u] = 0;
             }
-            const bool on = pos < pc.s.kv;
-            const int64_t page = on ? (int64_t)blk[u] * L.page : 0;
-            const int32_t row = on ? r : 0;
-            cp_async16_or_zero(smem_u32(&codes[in][u][pt]), from + page + row * row_bytes, on);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&words[in][u][pt])),
-                         "l"(scales + page + row * row_scales), "r"(on ? 4 : 0)
-                         : "memory");
+            row[u] = pos < pc.s.kv ? pos - L.by_block.div(pos) * L.block_tokens : -1;
+            page[u] = row[u] >= 0 ? (int64_t)blk[u] * L.page : 0;
           }
-          cp_async_commit();
           if (j + 1 < nt) look_up(j + 1);
-          if (++in == C::LAG + 1) in = 0;
-          if (++pending > C::LAG) {
-            cp_async_wait<C::LAG>();
-            convert();
+#pragma unroll
+          for (int v = C::both ? 0 : 1; v < 2 && ok; ++v) {
+            const int64_t lane = (C::both ? v : pw / W) ? lane_off : 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              if (!has(u)) break;
+              const bool on = row[u] >= 0;
+              const int32_t r = on ? row[u] : 0;
+              cp_async16_or_zero(smem_u32(&sm.codes[in][u][pt]), codes + lane + page[u] + r * row_bytes, on);
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&sm.words[in][u][pt])),
+                           "l"(scales + lane + page[u] + r * row_scales), "r"(on ? 4 : 0)
+                           : "memory");
+            }
+            cp_async_commit();
+            if (++in == C::LAG + 1) in = 0;
+            if (++pending > C::LAG) {
+              cp_async_wait<C::LAG>();
+              convert();
+            }
           }
         }
       }
       cp_async_wait<0>();
       while (ok && pending > 0) convert();
-    };
-    if (w >= 12 && w < 16) produce(Int<C::k_units>{}, sm.kcodes, sm.kwords, L.k, 0, w - 12, Int<4>{});
-    else if (w >= C::v_warp && w < C::v_warp + C::VW) produce(Int<C::v_units>{}, sm.vcodes, sm.vwords, L.v, 1, w - C::v_warp, Int<C::VW>{});
+    }
   } else if (w == 9 || w == 10) {
     // ---------------------------------------------------------------- producers
     const bool is_k = w == 9;
