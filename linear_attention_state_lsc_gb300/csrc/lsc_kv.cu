@@ -392,9 +392,10 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
 
 // E2M1 chunks of many row blocks: the batch's rows are first made 16 bits wide in the workspace (lsc_kv_rows4.cu) and
 // the 16-bit chunk kernels take them.  The host knows the sequences' row blocks on average and the workspace by the
-// bounds of the lengths; beyond kExpandMost bytes of it, and below kExpandBlocks blocks, the E2M1 chunk kernel converts
-// each tile it meets.
-constexpr int64_t kExpandBlocks = 4;
+// bounds of the lengths; beyond kExpandMost bytes of it, and below expand_blocks blocks, the E2M1 chunk kernel converts
+// each tile it meets.  16 sequences behind 4000 to 8000, 2, 4 and 6 blocks each, expanded and converted by tile: 8 heads of
+// 128: 301 and 277, 468 and 515, 589 and 758 us; 2 heads of 256: 125 and 82, 175 and 143, 184 and 202 us.
+int64_t expand_blocks(int head_dim) { return head_dim == 256 ? 6 : 4; }
 constexpr int64_t kExpandMost = (int64_t)4 << 30;
 
 int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
@@ -407,8 +408,10 @@ int64_t expand_bytes(const lsc::KvAttendParams &r, int64_t n_seq) {
   return up16(blocks * 4) + 2 * blocks * lsc::kExpandTokens * row;
 }
 
-// Sequences that the step's rows fill with kExpandBlocks row blocks each.
-int64_t expand_seqs(const lsc::KvAttendParams &r, int M) { return (int64_t)r.b.total_tokens * r.group / (M * kExpandBlocks); }
+// Sequences that the step's rows fill with that many row blocks each.
+int64_t expand_seqs(const lsc::KvAttendParams &r, int M) {
+  return (int64_t)r.b.total_tokens * r.group / (M * expand_blocks(r.L.head_dim));
+}
 
 bool expands(const lsc_kv_pool *p, const lsc::KvAttendParams &r, const lsc::AttendPlan &plan) {
   return r.L.dtype == LSC_E2M1 && p->encode && r.max_kv > 0 && r.b.n_seq <= expand_seqs(r, plan.M) &&
