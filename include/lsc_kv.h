@@ -319,8 +319,9 @@ typedef struct {
  * scores.  Its lse is not finite.  Positions it does not see, and rows behind a sequence's
  * last token, do not enter, whatever they hold.  Sums and softmax statistics
  * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded before they
- * meet v: to bf16 in bf16 pools, and in E2M1 pools where many rows of BF16 q read them
- * (there the batch's rows are first made 16 bits wide in the workspace); to f16 in f16, E4M3 and other E2M1 calls, in full down to
+ * meet v: to bf16 in bf16 pools, and in E2M1 pools read by many rows of BF16 q (four
+ * row blocks a sequence or more: the batch's cached rows are then first made 16 bits
+ * wide in the workspace); to f16 in f16 and E4M3 pools and elsewhere, in full down to
  * 2^-21 of a row's largest weight and to a multiple of 2^-31 of it below (E4M3
  * pools, more than 64 rows of q a kv head: to nine significant bits or more down
  * to 2^-17 of it, to a multiple of 2^-25 of it below, and elements of q below 2^-9
@@ -328,15 +329,18 @@ typedef struct {
  * one times the scale of its row of v).  E4M3 rows of v with a scale below 2^-76 add an
  * absolute error of up to 2^-93 a position; beside rows with a scale of 2^e above
  * 2^100, positions lighter than 2^(e - 133) of the heaviest drop out of the sums,
- * and rows of k with such a scale may overflow their scores.
+ * and rows of k with such a scale may overflow their scores.  Where an E2M1 pool's
+ * weights are f16, rows of BF16 q are brought to f16 by a power of two: elements
+ * below 2^-28 of their row's largest (and rows below 2^-111) lose bits.  A group of
+ * NaN in an E2M1 pool's v makes its 16 columns NaN in the rows that see the position.
  * Two calls with the same inputs give the same bits.
  * A sequence that exceeds max_kv_tokens is recorded as INVALID_ARG in the status
  * word and taken to have no cached tokens; one that exceeds max_seq_tokens is
  * recorded too, and its rows of out and lse stay as they are.  If a bounded device
  * wait expires (DEV_TIMEOUT in the status word), out and lse are
  * unspecified.
- * Supported: head_dim <= 512.  Pools of q's 16-bit type, and E4M3 pools with
- * 16-bit q, at head_dim 64, 128 and 256, with q and out 16-byte aligned in base
+ * Supported: head_dim <= 512.  Pools of q's 16-bit type, and E4M3 and E2M1 pools
+ * with 16-bit q, at head_dim 64, 128 and 256, with q and out 16-byte aligned in base
  * and stride, run on the tensor cores (E4M3 pools with F16 q: up to 64 rows of q
  * a kv head, max_seq_tokens times the group); every other combination (F32, q of
  * another type than the pool's, other head sizes) on the CUDA cores.
@@ -352,7 +356,9 @@ int lsc_kv_attend(lsc_kv_pool *pool, int32_t layer, const lsc_kv_attend_args *ar
  * serve every call over this pool of the same types and heads whose n_seq,
  * total_tokens, max_seq_tokens and max_kv_tokens (0 meaning total_tokens and
  * max_blocks * block_tokens) are no larger: asked once with the largest sizes, one
- * workspace serves every layer and step of a stream, prefill and decode alike.
+ * workspace serves every layer and step of a stream, prefill and decode alike.  E2M1
+ * pools whose steps may bring many rows ask for the 16-bit rows too, n_seq times
+ * max_kv_tokens of them (never more than 4 GiB: larger steps do without).
  * 0: none.  The pointers are checked and do not matter otherwise.  Errors: as
  * lsc_kv_attend's argument checks; CUDA (a host-only pool). */
 int lsc_kv_attend_workspace_bytes(const lsc_kv_pool *pool, const lsc_kv_attend_args *args, size_t *bytes);

@@ -59,6 +59,16 @@
 // 1120 TFLOP/s (687 with pauses; 2160 over blocks of 12, whose rows are copied one by
 // one); E4M3, 8 chunks behind up to 16384: 1039 us, 954 TFLOP/s (996 with pauses).
 //
+// E2M1 pools: the products run in f16 on K and V as f16 (6 bits: exact), which producer
+// warps make from the codes on the way into the ring: seven of them for K and V tiles in
+// turn, or four each at head_dim 256, whose softmax leaves registers for a fifth
+// warpgroup.  Each copies codes and scales with cp.async to shared memory of its own and
+// converts them there, so none waits for another; bf16 rows of q go to f16 by a power of two.  That is for few
+// row blocks a sequence (128 sequences of 8 tokens behind 500 to 8000, 8 heads of 128, 32 rows a head: 637 us; four
+// warps for K, three for V, 898; 64 of 4 tokens, 2 heads of 256: 102 us); with more
+// the batch's rows are expanded once (lsc_kv_rows4.cu) and the 16-bit forms take them: 24 sequences behind up to 8192, 2
+// heads of 256, 1121 us converted by tile and 776 expanded; 4096 tokens behind 28000, 8 of 128, 2055 and 1440.
+//
 // Positions that only some rows of a unit see may hold infinities and NaN: see
 // lsc_kv_attend_rows.cuh; here the softmax threads search such a tile's v.
 #pragma once

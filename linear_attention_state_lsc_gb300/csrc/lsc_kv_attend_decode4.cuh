@@ -12,7 +12,17 @@
 //   * V: ldmatrix transposes pairs of bytes, so a word is 4 columns of two neighbouring
 //     positions; the conversions pair columns, a byte permutation for each pairs
 //     positions, and the products with both positions' scales follow.
-//   * scales come with 4- to 16-byte cp.async, a position a lane, into a ring beside the codes'.
+//   * scales come with 4- to 16-byte cp.async, a position a lane, into a ring beside the codes'; V's go
+//     through shared memory once more as f16, pairs of positions side by side as the products want them.
+// What bounds it: the ALU, which does a conversion, a permutation, a logic or a shift every
+// second cycle (measured, each alone): 8 cycles a word of codes for conversions, 8 more for V's
+// permutations, and half again for scales, weights and addresses keep it 60 % busy, with the issue at
+// 63 %; one, two or four CTAs more an SM change nothing, nor do rows that lie in L2.  Measured, one token of 128
+// sequences behind 500 to 8000, 32 q heads, 8 heads of 128: 593 MB in 137 us (4.3 TB/s, 65 % of a copy's rate; the
+// same rows as E4M3 take 176); 64 behind 64 to 16384, 16 q heads, 2 of 256: 75 us, 57 %.
+// Tried and not kept: V's pairs made by two products with a zero beside each scale (the fp16 pipe for the ALU: 141 us
+// beside 141), sub-tiles of 32 positions (141 us), two sums a score tile (the same).
+//
 // q goes to f16: bf16 rows are brought to [2^14, 2^15) by a power of two that the scores
 // take back, so what bf16 holds down to 2^-28 of a row's largest is exact.
 //

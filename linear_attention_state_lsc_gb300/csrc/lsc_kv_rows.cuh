@@ -166,16 +166,6 @@ template <typename T>
 constexpr int kSize = (int)sizeof(T);
 template <>
 constexpr int kSize<E4M3> = 1;
-// Bytes of n elements in the pool.
-template <typename P>
-__device__ __forceinline__ int64_t held(int64_t n) {
-  return n * kSize<P>;
-}
-template <>
-__device__ __forceinline__ int64_t held<E2M1>(int64_t n) {
-  return n / 2;
-}
-
 template <typename A, typename B>
 struct Same {
   static constexpr bool value = false;
