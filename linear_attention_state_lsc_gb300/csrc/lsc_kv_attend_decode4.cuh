@@ -10,18 +10,24 @@
 //     exact values (6 bits), and they are the operands of two products as they are: which
 //     element of a head a product's place holds does not matter as long as q has the same.
 //   * V: ldmatrix transposes pairs of bytes, so a word is 4 columns of two neighbouring
-//     positions; the conversions pair columns, a byte permutation for each pairs
-//     positions, and the products with both positions' scales follow.
+//     positions; the conversions pair columns where a product wants pairs of positions.
+//     Up to 4 rows: a product of 8 positions and 32 columns runs over (position, column's
+//     parity), so that v's operands are the conversions' outputs times their scales, and the
+//     weights stand twice, for the even columns with a zero behind each and for the odd ones
+//     with a zero before it: half the product's places, which 4 rows leave empty anyhow.
+//     More rows: a byte permutation for each pair of columns makes two pairs of positions.
 //   * scales come with 4- to 16-byte cp.async, a position a lane, into a ring beside the codes'; V's go
 //     through shared memory once more as f16, pairs of positions side by side as the products want them.
-// What bounds it: the ALU, which does a conversion, a permutation, a logic or a shift every
-// second cycle (measured, each alone): 8 cycles a word of codes for conversions, 8 more for V's
-// permutations, and half again for scales, weights and addresses keep it 60 % busy, with the issue at
-// 63 %; one, two or four CTAs more an SM change nothing, nor do rows that lie in L2.  Measured, one token of 128
-// sequences behind 500 to 8000, 32 q heads, 8 heads of 128: 593 MB in 137 us (4.3 TB/s, 65 % of a copy's rate; the
-// same rows as E4M3 take 176); 64 behind 64 to 16384, 16 q heads, 2 of 256: 75 us, 57 %.
-// Tried and not kept: V's pairs made by two products with a zero beside each scale (the fp16 pipe for the ALU: 141 us
-// beside 141), sub-tiles of 32 positions (141 us), two sums a score tile (the same).
+// What bounds it: instructions.  The ALU does a conversion, a permutation, a logic or a shift every second cycle
+// (measured, each alone): 8 cycles a word of codes for conversions, 8 more for V's permutations where there are any.  Up
+// to 4 rows it is 43 % busy and the issue 54 %, with 12 warps an SM waiting for one another's results; behind the
+// permutations 60 and 63 %.  Rows that lie in L2 take 9 % less.  Measured, one token of 128 sequences behind 500 to 8000,
+// 32 q heads, 8 heads of 128: 593 MB in 125 us (4.75 TB/s, 71 % of a copy's rate; with the permutations 139 us, the same
+// rows as E4M3 176); 64 behind 64 to 16384, 16 q heads, 2 of 256: 75 us, 57 %.
+// The weights that stand twice cost 8 and 16 rows more products than the permutations they save: two tokens, 32 q heads, 4
+// heads of 128 71 us beside 63, 16 q heads, 2 of 256 84 beside 68, the 75 us above 81.
+// Tried and not kept: V's pairs made by two products with a zero beside each scale (141 us beside 141), sub-tiles of 32
+// positions (133 us beside 125), two sums a score tile and both halves of a sub-tile unrolled (the same).
 //
 // q goes to f16: bf16 rows are brought to [2^14, 2^15) by a power of two that the scores
 // take back, so what bf16 holds down to 2^-28 of a row's largest is exact.
@@ -52,31 +58,32 @@ using rows::mma;
 constexpr int kTK = decode::kTK;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-template <int D, int NR>
+// M: packed rows of a head, up to 4, 8 or 16.
+template <int D, int M>
 struct Conf {
   static constexpr int KEYS = kv_decode_keys(D, 4), HALVES = KEYS / 32;  // positions of a sub-tile; a lane has one of each 32
   static constexpr int RB = D / 2, SB = D / 16;  // bytes of a row's codes and scales
   static constexpr int half = KEYS * RB;         // bytes of a sub-tile's K or V codes
   static constexpr int ST = D == 64 ? 3 : 2;     // sub-tiles in flight per warp
-  static constexpr int occ = D == 256 ? 2 : D == 128 ? (NR == 1 ? 3 : 2) : (NR == 1 ? 4 : 3);  // CTAs per SM
-  static constexpr bool QS = NR == 2;  // q's rows in shared memory: else in registers
+  static constexpr int occ = D == 256 ? 2 : D == 128 ? (M < 16 ? 3 : 2) : (M < 16 ? 4 : 3);  // CTAs per SM
+  static constexpr bool QS = M == 16;            // q's rows in shared memory: else in registers
 };
 
 template <int D>
 constexpr int occ_of(int rows) {
-  return rows == 8 ? Conf<D, 1>::occ : Conf<D, 2>::occ;
+  return rows < 16 ? Conf<D, 8>::occ : Conf<D, 16>::occ;
 }
 
-template <int D, int NR>
+template <int D, int M>
 struct Smem {
-  using C = Conf<D, NR>;
+  using C = Conf<D, M>;
   static constexpr int PS = D + 4;  // 32-bit columns of a weighted row at a piece's end (no bank twice in what follows)
-  static constexpr int rings = kWarps * C::ST * 2 * C::half, parts = kWarps * 8 * NR * PS * 4;
+  static constexpr int rings = kWarps * C::ST * 2 * C::half, parts = kWarps * M * PS * 4;
   alignas(1024) uint8_t ring[rings > parts ? rings : parts];  // [warp][sub-tile][K, V]; at a piece's end: the warps' weighted rows
   alignas(16) uint8_t scale[kWarps][C::ST][2][C::KEYS][C::SB];
   // V's scales of 32 positions as f16, by group: positions 2 tq, 2 tq + 1 of each 8 side by side for lane tq
   alignas(16) uint16_t v_scale[kWarps][C::SB][32];
-  alignas(16) uint4 q[C::QS ? kWarps : 1][C::QS ? 8 * NR : 1][C::QS ? D / 8 : 1];  // neighbouring rows' chunks xor 4: no bank twice
+  alignas(16) uint4 q[C::QS ? kWarps : 1][C::QS ? M : 1][C::QS ? D / 8 : 1];  // neighbouring rows' chunks xor 4: no bank twice
   float2 ml[kWarps][16];
   int32_t vis[16];
   int32_t bad[kWarps][C::SB];  // by head of the unit and group: the first position whose v is NaN
@@ -91,21 +98,23 @@ __device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, 
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
 }
 
-__device__ __forceinline__ uint32_t times(uint32_t h, uint32_t s) {
-  const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&s));
+__device__ __forceinline__ uint32_t times(uint32_t h, __half2 s) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), s);
   return *reinterpret_cast<const uint32_t *>(&y);
 }
 
-template <int D, int NR>
-__global__ void __launch_bounds__(kThreads, (Conf<D, NR>::occ))
+template <int D, int M>
+__global__ void __launch_bounds__(kThreads, (Conf<D, M>::occ))
 decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map, int together) {
-  using C = Conf<D, NR>;
-  constexpr int M = 8 * NR;         // rows of a head, NR tiles of 8
+  using C = Conf<D, M>;
+  constexpr bool few = M == 4;
+  // Score tiles of 8 columns: 8 rows, or each of 4 rows twice, so that a lane has one row's scores alone and finds the
+  // weights that the second product wants of it without asking another lane.
+  constexpr int NR = M == 16 ? 2 : 1, E = few ? 1 : 2;
   constexpr int KEYS = C::KEYS, HALVES = C::HALVES, ST = C::ST, RB = C::RB, SB = C::SB, NC = D / 32;  // NC: 16-byte chunks of a row, 32 elements each
-  constexpr int KS = D / 16;        // output tiles of 16 columns
   constexpr float lift = 7.f;       // powers of two that the reference lies below the maximum that set it
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<D, NR> &sm = *reinterpret_cast<Smem<D, NR> *>(smem_raw);
+  Smem<D, M> &sm = *reinterpret_cast<Smem<D, M> *>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31, g = ln >> 2, tq = ln & 3;
   if (tid < kWarps * ST) mbar_init(&sm.full[tid / ST][tid % ST], 1);
   fence_mbar_init();
@@ -131,6 +140,9 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
   // ldmatrix rows: chunk c of K (c even) and V is the offset of chunk 0 xor 16 c
   const uint32_t koff = chunk_at<RB>(KEYS, ln & 15, ln >> 4), voff = chunk_at<RB>(KEYS, ln, 0);
   const uint32_t kh = tq >> 1, ksel = 0x4040u | kh | (kh + 2) << 8;
+  // few: the weights of positions 2 tq, 2 tq + 1 -> the operand for each: the weight, and a zero behind it where this
+  // lane's column of the product (g) is for v's even columns, before it where it is for the odd ones
+  const uint32_t wsel[2] = {g & 1 ? 0x1044u : 0x4410u, g & 1 ? 0x3244u : 0x4432u};
   int slot = 0;
   uint32_t phase = 0;
   __syncthreads();
@@ -196,7 +208,7 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
     float q_up[NR];  // of row g: scale * log2 e, times the power of two that bf16 rows were brought down by
 #pragma unroll
     for (int h = 0; h < NR; ++h) {
-      const int r = 8 * h + g, tok = p.by_group.div(r);
+      const int r = few ? g >> 1 : 8 * h + g, tok = p.by_group.div(r);
       const uint16_t *src = (const uint16_t *)p.q + (int64_t)(pc.s.row0 + tok) * p.q_stride +
                             (int64_t)(head * p.group + (r - tok * p.group)) * D;
       uint32_t x[NC][4];
@@ -238,23 +250,25 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
         }
       }
     }
-    // scores come with rows 2 tq, 2 tq + 1 of each 8
-    float qsc[NR][2];
+    // scores come with rows 2 tq, 2 tq + 1 of each 8 (few: row tq)
+    float qsc[NR][E];
 #pragma unroll
     for (int h = 0; h < NR; ++h)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) qsc[h][e] = __shfl_sync(0xffffffffu, q_up[h], (2 * tq + e) * 4);
+      for (int e = 0; e < E; ++e) qsc[h][e] = __shfl_sync(0xffffffffu, q_up[h], (2 * tq + e) * 4);
     __syncthreads();  // vis; and the last piece's shared memory is free
     const int32_t sure = visible(pc.s, 0, p.causal);  // every row sees positions below this
-    int32_t vis[NR][2];
-    float m[NR][2], ref[NR][2], l[NR][2], o[NR][KS][4];  // ref: m, 0 while no position has been seen
+    int32_t vis[NR][E];
+    float m[NR][E], ref[NR][E], l[NR][E];  // ref: m, 0 while no position has been seen
+    float o[NR][few ? NC : 2 * NC][4];     // few: of row tq, columns 4 g .. 4 g + 3 of each 32
 #pragma unroll
-    for (int h = 0; h < NR; ++h) {
+    for (int h = 0; h < NR; ++h)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) vis[h][e] = sm.vis[8 * h + 2 * tq + e], m[h][e] = -INFINITY, ref[h][e] = l[h][e] = 0.f;
+      for (int e = 0; e < E; ++e) vis[h][e] = sm.vis[few ? tq : 8 * h + 2 * tq + e], m[h][e] = -INFINITY, ref[h][e] = l[h][e] = 0.f;
 #pragma unroll
-      for (int n = 0; n < KS; ++n) o[h][n][0] = o[h][n][1] = o[h][n][2] = o[h][n][3] = 0.f;
-    }
+    for (int h = 0; h < NR; ++h)
+#pragma unroll
+      for (auto &x : o[h]) x[0] = x[1] = x[2] = x[3] = 0.f;
 
     int i = 0;
 #pragma unroll 1
@@ -347,14 +361,14 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
           for (int h = 0; h < NR; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (first32 + 16 * n + 8 * (e >> 1) + g >= vis[h][e & 1]) s[n][h][e] = -INFINITY;
+              if (first32 + 16 * n + 8 * (e >> 1) + g >= vis[h][(e & 1) % E]) s[n][h][e] = -INFINITY;
       }
       bool rise = false;
-      float top[NR][2];
+      float top[NR][E];
 #pragma unroll
       for (int h = 0; h < NR; ++h)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < E; ++e) {
           top[h][e] = fmaxf(fmaxf(s[0][h][e], s[0][h][2 + e]), fmaxf(s[1][h][e], s[1][h][2 + e])) * qsc[h][e];
           rise |= top[h][e] > m[h][e] + (8.f + lift);
         }
@@ -362,7 +376,7 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
 #pragma unroll
         for (int h = 0; h < NR; ++h)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < E; ++e) {
             float t = top[h][e];
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
@@ -373,46 +387,66 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
             m[h][e] = to;
             l[h][e] *= f;
 #pragma unroll
-            for (int n = 0; n < KS; ++n) o[h][n][e] *= f, o[h][n][2 + e] *= f;
+            for (auto &x : o[h]) {
+              x[e] *= f, x[2 + e] *= f;
+              if constexpr (few) x[1] *= f, x[3] *= f;
+            }
           }
       }
-      uint32_t a[2][NR][2];
+      uint32_t a[2][NR][2];  // of row g (few: g / 2): the weights of positions 2 tq, 2 tq + 1 of each 8
 #pragma unroll
       for (int h = 0; h < NR; ++h) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float p0 = ex2(fmaf(s[n][h][2 * y], qsc[h][0], -ref[h][0])), p1 = ex2(fmaf(s[n][h][2 * y + 1], qsc[h][1], -ref[h][1]));
-            l[h][0] += p0;
-            l[h][1] += p1;
-            a[n][h][y] = transposed(pack2(p0, p1, 0));
+            float x[2];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              x[e] = ex2(fmaf(s[n][h][2 * y + e], qsc[h][e], -ref[h][e]));
+              l[h][e] += x[e];
+            }
+            a[n][h][y] = transposed(pack2(x[0], x[E - 1], 0));
           }
       }
       // ---- V^T times weights
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {  // 32 columns: m index g is column 4 g (+ 2), m index g + 8 the one behind it
+      for (int c = 0; c < NC; ++c) {
         uint32_t b[4];
         ldsm4t(b, va + u * (32 * RB) + (voff ^ c << 4));
         const uint4 sv4 = *(const uint4 *)&sm.v_scale[w][2 * c + (g >> 2)][tq * 8];  // of positions 2 tq, 2 tq + 1 of each 8
         const uint32_t sv[4] = {sv4.x, sv4.y, sv4.z, sv4.w};
+        if constexpr (few) {  // m index g is columns 4 g, 4 g + 1 of 32, m index g + 8 the two behind them
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          uint32_t x[2][4];  // columns 4 g .. 4 g + 3 of positions 2 tq, 2 tq + 1 and 8 further
+          for (int y = 0; y < 4; ++y) {  // 8 positions
+            const __half2 sc = *reinterpret_cast<const __half2 *>(&sv[y]);
+            uint32_t x[4];
+            e2m1x8_to_f16(b[y], x);
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint32_t h[4];
-            e2m1x8_to_f16(b[2 * n + y], h);
-            x[y][0] = times(__byte_perm(h[0], h[2], 0x5410), sv[2 * n + y]);
-            x[y][1] = times(__byte_perm(h[0], h[2], 0x7632), sv[2 * n + y]);
-            x[y][2] = times(__byte_perm(h[1], h[3], 0x5410), sv[2 * n + y]);
-            x[y][3] = times(__byte_perm(h[1], h[3], 0x7632), sv[2 * n + y]);
+            for (int z = 0; z < 4; ++z) x[z] = times(x[z], z < 2 ? __low2half2(sc) : __high2half2(sc));
+            const uint32_t pair = a[y / 2][0][y % 2];
+            mma<false>(o[0][c], x, __byte_perm(pair, 0, wsel[0]), __byte_perm(pair, 0, wsel[1]));
           }
+        } else {  // m index g is column 4 g (+ 2), m index g + 8 the one behind it
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const uint32_t v[4] = {x[0][2 * z], x[0][2 * z + 1], x[1][2 * z], x[1][2 * z + 1]};
+          for (int n = 0; n < 2; ++n) {
+            uint32_t x[2][4];  // columns 4 g .. 4 g + 3 of positions 2 tq, 2 tq + 1 and 8 further
 #pragma unroll
-            for (int h = 0; h < NR; ++h) mma<false>(o[h][2 * c + z], v, a[n][h][0], a[n][h][1]);
+            for (int y = 0; y < 2; ++y) {
+              const __half2 sc = *reinterpret_cast<const __half2 *>(&sv[2 * n + y]);
+              uint32_t h[4];
+              e2m1x8_to_f16(b[2 * n + y], h);
+              x[y][0] = times(__byte_perm(h[0], h[2], 0x5410), sc);
+              x[y][1] = times(__byte_perm(h[0], h[2], 0x7632), sc);
+              x[y][2] = times(__byte_perm(h[1], h[3], 0x5410), sc);
+              x[y][3] = times(__byte_perm(h[1], h[3], 0x7632), sc);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t v[4] = {x[0][2 * z], x[0][2 * z + 1], x[1][2 * z], x[1][2 * z + 1]};
+#pragma unroll
+              for (int h = 0; h < NR; ++h) mma<false>(o[h][2 * c + z], v, a[n][h][0], a[n][h][1]);
+            }
           }
         }
       }
@@ -438,26 +472,28 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
 #pragma unroll
     for (int h = 0; h < NR; ++h)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < E; ++e) {
         l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 4);
         l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 8);
         l[h][e] += __shfl_xor_sync(0xffffffffu, l[h][e], 16);
-        if (g == 0) sm.ml[w][8 * h + 2 * tq + e] = make_float2(m[h][e], l[h][e]);
+        if (g == 0) sm.ml[w][few ? tq : 8 * h + 2 * tq + e] = make_float2(m[h][e], l[h][e]);
       }
     ok = __syncthreads_and(ok);
     if (!ok) break;
-    constexpr int PS = Smem<D, NR>::PS;  // the rings are empty
+    constexpr int PS = Smem<D, M>::PS;  // the rings are empty
     float *parts = (float *)sm.ring;
 #pragma unroll
     for (int h = 0; h < NR; ++h)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * h + 2 * tq + e;
+      for (int e = 0; e < E; ++e) {
+        const int r = few ? tq : 8 * h + 2 * tq + e;
         if (r < R) {
           float *row = parts + (w * M + r) * PS;
 #pragma unroll
           for (int c = 0; c < NC; ++c)  // columns 4 g .. 4 g + 3 of 32
-            *(float4 *)(row + c * 32 + 4 * g) = make_float4(o[h][2 * c][e], o[h][2 * c][2 + e], o[h][2 * c + 1][e], o[h][2 * c + 1][2 + e]);
+            *(float4 *)(row + c * 32 + 4 * g) =
+                few ? make_float4(o[h][c][0], o[h][c][1], o[h][c][2], o[h][c][3])
+                    : make_float4(o[h][2 * c][e], o[h][2 * c][2 + e], o[h][2 * c + 1][e], o[h][2 * c + 1][2 + e]);
         }
       }
     __syncthreads();
@@ -505,12 +541,12 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
   if (tid == 0 && p.ws) ws.cut[cta] = cut;
 }
 
-template <int D, int NR>
+template <int D, int M>
 cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
   static SmemLimit limit;
-  const int smem = (int)sizeof(Smem<D, NR>);
-  static_assert(Conf<D, NR>::occ * (sizeof(Smem<D, NR>) + 1024) <= 228 * 1024, "CTAs that an SM holds at once");
-  auto *k = decode4_attend_kernel<D, NR>;
+  const int smem = (int)sizeof(Smem<D, M>);
+  static_assert(Conf<D, M>::occ * (sizeof(Smem<D, M>) + 1024) <= 228 * 1024, "CTAs that an SM holds at once");
+  auto *k = decode4_attend_kernel<D, M>;
   const cudaError_t e = limit.ensure((const void *)k, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, plan.ctas, kThreads, smem, stream, p, *p.map_decode, plan.together);
@@ -518,7 +554,10 @@ cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStre
 
 template <int D>
 cudaError_t launch_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
-  return plan.M == 8 * plan.together ? launch_one<D, 1>(p, plan, stream) : launch_one<D, 2>(p, plan, stream);
+  const int rows = plan.M / plan.together;
+  return rows == 4   ? launch_one<D, 4>(p, plan, stream)
+         : rows == 8 ? launch_one<D, 8>(p, plan, stream)
+                     : launch_one<D, 16>(p, plan, stream);
 }
 
 }  // namespace decode4

@@ -113,7 +113,8 @@ AttendPlan plan_kv_attend_decode(const KvAttendParams &p, bool side_by_side) {
   const int row = q4 ? D / 2 : q8 ? D : 2 * D, H = p.L.heads;
   plan.together = !side_by_side ? 1 : H % 4 == 0 && row <= 256 ? 4 : H % 2 == 0 && row <= 512 ? 2 : 1;
   if ((int64_t)p.b.n_seq * (H / plan.together) * p.max_kv < (int64_t)p.num_sms * 4 * kTK) plan.together = 1;
-  const int rows = (int64_t)p.max_seq * p.group <= 8 ? 8 : 16;  // of a head
+  const int64_t most_rows = (int64_t)p.max_seq * p.group;
+  const int rows = q4 && most_rows <= 4 ? 4 : most_rows <= 8 ? 8 : 16;  // of a head
   plan.M = rows * plan.together;
   const int occ = q4   ? (D == 64 ? kv::decode4::occ_of<64>(rows) : D == 128 ? kv::decode4::occ_of<128>(rows) : kv::decode4::occ_of<256>(rows))
                   : q8 ? (D == 64 ? Conf<1, 64>::occ : D == 128 ? Conf<1, 128>::occ : Conf<1, 256>::occ)
