@@ -46,9 +46,10 @@
  * element is off by 3/16 of its group's largest magnitude at most (half the step from
  * 4 to 6, times a scale that is up to an eighth larger than that magnitude needs) or,
  * where the scale is below 2^-14, by the scale.  Magnitudes above 61440 become 61440.
- * A group of zeros has byte 0 and codes of 0 whatever the zeros' signs.  Byte 255 marks a group that held a NaN or an infinity (codes of
- * 0); its 16 elements read back as NaN.  What bytes 227 to 254, which append does not
- * write, read back as is unspecified.
+ * A group of zeros has byte 0 and codes of 0 whatever the zeros' signs.  Byte 255
+ * marks a group that held a NaN or an infinity (codes of 0); its 16 elements read back
+ * as NaN.  What bytes 227 to 254, which append does not write, read back as is
+ * unspecified.
  *
  * Conventions are those of lsc.h (return codes, host/device pointers, streams,
  * no host sync except create/destroy).

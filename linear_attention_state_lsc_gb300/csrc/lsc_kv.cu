@@ -441,7 +441,6 @@ bool expand_layer(const lsc_kv_pool *p, uint8_t *space, lsc::KvAttendParams *r, 
   L.by_block.set(lsc::kExpandTokens);
   r->b.table = x->table;
   r->b.max_blocks = blocks;
-  r->b.held = (int32_t)std::min<int64_t>((int64_t)blocks * lsc::kExpandTokens, LSC_KV_MAX_TOKENS);
   r->map = map;
   r->box_rows = tile;
   return true;
@@ -463,8 +462,7 @@ size_t attend_workspace(const lsc_kv_pool *p, lsc::KvAttendParams r) {
     most = std::max(lsc::plan_kv_attend_decode(r).ws_bytes, lsc::plan_kv_attend_decode(r, false).ws_bytes);
   if ((q8 || r.box_decode == 0) && !q4 && rows_up_to(few)) most = std::max(most, lsc::plan_kv_attend_rows(r).ws_bytes);
   r.max_seq = max_seq;
-  if (((int64_t)max_seq * r.group > few && !(q8 && r.dtype != LSC_BF16)) || (q4 && r.box_decode == 0))
-  {
+  if (((int64_t)max_seq * r.group > few && !(q8 && r.dtype != LSC_BF16)) || (q4 && r.box_decode == 0)) {
     const lsc::AttendPlan plan = lsc::plan_kv_attend_chunk(r);
     most = std::max(most, plan.ws_bytes);
     if (q4 && p->encode && r.max_kv > 0) {  // the rows of fewer sequences, or of shorter ones, may be just within what is allowed

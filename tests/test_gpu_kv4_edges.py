@@ -27,6 +27,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 # (dtype, new tokens, block, head_dim, q heads a kv head)
 FORMS = {"decode-bf16": (BF, 2, 64, 128, 4), "decode-f16": (F16, 2, 16, 256, 8), "decode-64": (BF, 1, 8, 64, 3),
+         "decode-4-rows": (F16, 2, 32, 128, 2), "decode-4-rows-256": (BF, 4, 64, 256, 1),
          "chunk-bf16": (BF, 20, 64, 128, 4), "chunk-f16": (F16, 20, 12, 64, 4), "chunk-256": (BF, 12, 5, 256, 8),
          "few-rows-no-box": (BF, 2, 12, 128, 2),
          "expanded-bf16": (BF, 300, 64, 128, 4), "expanded-f16": (F16, 300, 12, 64, 4), "expanded-256": (BF, 100, 16, 256, 8),

@@ -84,6 +84,59 @@ def test_rotate(lsc, dtype, shape, interleaved):
         assert torch.equal(x[:, H * D:].isnan(), between.isnan())
 
 
+@pytest.mark.parametrize("H,D,R,T,stride", [
+    (2, 64, 64, 5, 2 ** 30 + 8), (2, 64, 64, 5, 2 ** 30 + 1),  # rows whose bytes pass 33 bits, both kernels
+    (70001, 16, 16, 2, 0), (33000, 10, 6, 2, 0),               # more heads than a grid has rows
+    (2, 4096, 512, 3, 0), (1, 100000, 2, 2, 0)], ids=str)      # heads wider than the vector kernel takes
+def test_extreme_sizes(lsc, H, D, R, T, stride):
+    rng = np.random.default_rng(H + D)
+    pos, angle, axis = plan(rng, T, R, 3)
+    x, xx = dense(rng.standard_normal((T, H, D)), BF)
+    x = x.view(T, H * D)
+    rows = x if not stride else torch.empty(T * stride, dtype=TORCH[BF], device="cuda").view(T, stride)
+    if stride:
+        rows[:, :H * D] = x
+        rows[:, H * D:H * D + 64] = 7
+    r = L.rotary(R, pos, freqs(R), pair_axis=axis)
+    assert L.lsc_rotate(L.rotate_args(T, H, D, BF, rows, rows, r, stride, stride), cur()) == L.LSC_OK
+    want, size = turn(xx, R, angle, False)
+    check(rows[:, :H * D].double().cpu().numpy().reshape(T, H, D), want, size, BF)
+    assert (rows[:, H * D:H * D + 64] == 7).all()
+
+
+@pytest.mark.parametrize("D,R", [(128, 64), (80, 20)])
+def test_rotate_in_a_graph_of_another_stream(lsc, D, R):
+    """Captured in place and out of place behind each other, replayed with other positions and rows; frequencies are read
+    when the call is made."""
+    rng = np.random.default_rng(D)
+    H, T = 6, 50
+    pos, _, axis = plan(rng, T, R, 2)
+    x, _ = dense(rng.standard_normal((T, H, D)), BF)
+    y = torch.zeros_like(x)
+    freq = freqs(R).copy()
+    r = L.rotary(R, pos, freq, pair_axis=axis)
+    there, back = L.rotate_args(T, H, D, BF, x, y, r), L.rotate_args(T, H, D, BF, x, x, r)
+    s = torch.cuda.Stream()
+    s.wait_stream(cur())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        assert L.lsc_rotate(there, s) == L.LSC_OK
+        assert L.lsc_rotate(back, s) == L.LSC_OK
+        assert L.lsc_rotate(L.rotate_args(0, H, D, BF, None, None, r), s) == L.LSC_OK
+    freq[:] = 0
+    r._host[0][:] = 0
+    for _ in range(3):
+        p = rng.integers(-9, 9999, (2, T)).astype(np.int32)
+        pos.copy_(torch.from_numpy(p))
+        rows, xx = dense(rng.standard_normal((T, H, D)), BF)
+        x.copy_(rows)
+        g.replay()
+        torch.cuda.synchronize()
+        want, size = turn(xx, R, angles(p, freqs(R), axis), False)
+        check(y.double().cpu().numpy().reshape(T, H, D), want, size, BF)
+        assert torch.equal(x, y)
+
+
 def test_what_is_not_turned_keeps_its_bits(lsc):
     """NaN payloads, infinities and zeros behind rotary_dim, out of place and in place, both kernels."""
     for dtype, word in ((BF, torch.int16), (F16, torch.int16), (F32, torch.int32)):
