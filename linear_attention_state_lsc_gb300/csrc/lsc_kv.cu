@@ -252,7 +252,7 @@ uint64_t turns_of(double f) {
   constexpr double kInv2Pi = 0x1.45f306dc9c883p-3, kInv2PiLow = -0x1.6b01ec5417056p-57;
   if (f < 0) return 0 - turns_of(-f);
   const double hi = f * kInv2Pi, lo = std::fma(f, kInv2Pi, -hi) + f * kInv2PiLow;  // |lo| < 2^-38: see kMostFreq
-  return (uint64_t)std::ldexp(hi - std::floor(hi), 64) + (uint64_t)(int64_t)std::ldexp(lo, 64);
+  return (uint64_t)((hi - std::floor(hi)) * 0x1p64) + (uint64_t)(int64_t)(lo * 0x1p64);
 }
 constexpr double kMostFreq = 65536.0;
 
