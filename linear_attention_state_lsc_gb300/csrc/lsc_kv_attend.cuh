@@ -293,6 +293,7 @@ struct AttendPlan {
   bool may_cut;    // false: units are not cut
   int32_t min_run; // tiles of a run at least
   int32_t lead;    // tiles' worth of time that a unit takes besides its tiles
+  int32_t join_units;  // many parts a unit: units that the join may meet at most; 0: the plain join
 };
 cudaError_t launch_kv_attend_rows(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_decode(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);

@@ -6,6 +6,14 @@
 // in the order of the tiles, so the result does not depend on timing.  It reads
 // what the parts wrote (at most 2 M rows of D floats per run) once: a few us
 // even for 152 runs of 256 rows.
+//
+// E2M1 decode steps of few sequences: a unit then has dozens of parts or hundreds, and one warp's walk over them took as
+// long as the parts.  From kManyParts parts a unit on, on average, and up to two turns of CTAs, a CTA takes a row and each
+// of its warps every eighth part.  One token behind 544000, 32 q heads, 8 heads of 128: 183 -> 135 us; behind 32000 58
+// -> 26, 8000 22 -> 15; 4 sequences of 32000, 16 q heads, 2 heads of 256: 51 -> 37; 16 of 34000, 14 parts a unit: 123.4
+// -> 121.7; 32 of up to 16000, 7 parts: 66.5 and 66.7.  Beyond, the CTAs that each look for their run cost more: 4 rows of
+// 64 sequences, 4 heads of 128, 5 parts, 4096 CTAs: 63 and 73; 128 sequences, 2 parts: 125 and 137.  The other types'
+// parts stay in one warp's order of summation.
 #include <cuda_runtime.h>
 
 #include "lsc_internal.h"
@@ -74,9 +82,102 @@ __global__ void __launch_bounds__(kWarps * 32) join_kernel(const __grid_constant
   if (p.lse && ln == 0) p.lse[t * p.heads + h] = empty ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
+constexpr int kManyParts = 8, kMostCtas = 2048;
+
+// CTA (x, r): row r of the x-th run that begins a cut unit, in the runs' order.
+template <int NV>
+__global__ void __launch_bounds__(kWarps * 32) join_many_kernel(const __grid_constant__ KvAttendParams p, int ctas, int M, int together) {
+  __shared__ uint32_t s_begins[kMostCtas / 32];
+  __shared__ float2 s_ml[kWarps];
+  __shared__ float4 s_o[kWarps][32 * NV];
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const Workspace w = workspace_at(p.ws, ctas, M);
+  const int D = p.L.head_dim, ln = threadIdx.x & 31, wi = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i - ln < ctas; i += kWarps * 32) {
+    const uint32_t begins = __ballot_sync(0xffffffffu, i < ctas && w.cut[i < ctas ? i : 0].more > 0);
+    if (ln == 0) s_begins[i / 32] = begins;
+  }
+  __syncthreads();
+  int c = -1;
+  for (int i = 0, left = blockIdx.x; i * 32 < ctas; ++i) {
+    uint32_t begins = s_begins[i];
+    const int n = __popc(begins);
+    if (left < n) {
+      for (; left > 0; --left) begins &= begins - 1;
+      c = i * 32 + __ffs(begins) - 1;
+      break;
+    }
+    left -= n;
+  }
+  if (c < 0) return;
+  const Cut cut = w.cut[c];
+  const Seq s = attend_seq(p.L, p.b, cut.seq, p.max_seq, p.max_kv);
+  const int r = blockIdx.y, MR = M / together, hr = r / MR;  // row of the unit; rows of a head; which head of the unit
+  const int32_t R = cut.block * MR + r - hr * MR;
+  if (R >= s.n * p.group) return;
+  auto part = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+  float m = -INFINITY;
+  for (int i = wi + kWarps * ln; i <= cut.more; i += kWarps * 32) m = fmaxf(m, w.ml[(int64_t)part(i) * M + r].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float own = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 acc[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = wi; i <= cut.more; i += kWarps) {
+    const int64_t at = (int64_t)part(i) * M + r;
+    const float2 ml = w.ml[at];
+    const float k = exp2f(ml.x - own);
+    l += ml.y * k;
+    const float4 *src = (const float4 *)(w.o + at * D);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if ((ln + 32 * v) * 4 >= D) continue;
+      const float4 x = src[ln + 32 * v];
+      acc[v].x += k * x.x, acc[v].y += k * x.y, acc[v].z += k * x.z, acc[v].w += k * x.w;
+    }
+  }
+  if (ln == 0) s_ml[wi] = make_float2(m, l);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) s_o[wi][ln + 32 * v] = acc[v];
+  __syncthreads();
+  if ((int)threadIdx.x * 4 >= D) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) m = fmaxf(m, s_ml[i].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  l = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const float k = exp2f(s_ml[i].x - ref);
+    const float4 x = s_o[i][threadIdx.x];
+    l += s_ml[i].y * k;
+    y.x += k * x.x, y.y += k * x.y, y.z += k * x.z, y.w += k * x.w;
+  }
+  const int32_t tok = p.by_group.div(R);
+  const bool empty = visible(s, tok, p.causal) == 0;
+  const float inv = empty ? 0.f : 1.f / l;
+  const int64_t t = s.row0 + tok, h = (int64_t)(cut.head * together + hr) * p.group + (R - tok * p.group);
+  const int bf16 = p.dtype == LSC_BF16;
+  ((uint2 *)((uint16_t *)p.out + t * p.out_stride + h * D))[threadIdx.x] =
+      make_uint2(pack2(y.x * inv, y.y * inv, bf16), pack2(y.z * inv, y.w * inv, bf16));
+  if (p.lse && threadIdx.x == 0) p.lse[t * p.heads + h] = empty ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+}
+
 }  // namespace
 
 cudaError_t launch_kv_attend_join(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
+  if (plan.join_units > 0) {
+    const dim3 grid(plan.join_units, plan.M);
+    const cudaError_t e = p.L.head_dim <= 128
+                              ? launch_pdl(join_many_kernel<1>, grid, kWarps * 32, 0, stream, p, plan.ctas, plan.M, plan.together)
+                              : launch_pdl(join_many_kernel<2>, grid, kWarps * 32, 0, stream, p, plan.ctas, plan.M, plan.together);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+  }
   const dim3 grid(plan.ctas, (plan.M + kWarps - 1) / kWarps);
   const cudaError_t e = p.L.head_dim <= 128
                             ? launch_pdl(join_kernel<1>, grid, kWarps * 32, 0, stream, p, plan.ctas, plan.M, plan.together)
@@ -124,6 +225,8 @@ AttendPlan plan_kv_attend_decode(const KvAttendParams &p, bool side_by_side) {
   plan.may_cut = tiles > 1;
   plan.min_run = 1;
   plan.ctas = (int)(most < (int64_t)p.num_sms * occ ? most : (int64_t)p.num_sms * occ);
+  if (q4 && plan.ctas >= kManyParts * units && units * plan.M <= 16 * (int64_t)p.num_sms && plan.ctas <= kMostCtas)
+    plan.join_units = (int)units;
   plan.ws_bytes = plan.may_cut ? kv::workspace_size(plan.ctas, plan.M, D) : 0;
   return plan;
 }

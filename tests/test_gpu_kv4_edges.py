@@ -246,6 +246,36 @@ def test_runs_that_begin_and_end_anywhere(lsc, D, S, most):
         assert dev.status() == L.LSC_OK
 
 
+@pytest.mark.parametrize("dtype,H,G,D,n,kv", [
+    (BF, 8, 4, 128, [1], [31000]), (F16, 8, 1, 64, [1], [20011]), (BF, 2, 8, 256, [1, 1], [9000, 16001]),
+    (F16, 4, 4, 64, [4, 1], [5003, 12345]), (BF, 2, 2, 256, [8], [8001]), (BF, 1, 16, 128, [1, 1, 1], [7000, 0, 40])], ids=str)
+def test_few_long_sequences(lsc, dtype, H, G, D, n, kv):
+    """Units of dozens of parts: rows that see less than others, an empty cache, V that is NaN in a group, twice the same
+    bits."""
+    rng = np.random.default_rng(sum(kv) + D)
+    bt = 64
+    blocks = sum(-(-x // bt) for x in kv)
+    b = Batch(rng, n, kv, bt, blocks, spare=1)
+    host = filled4(rng, b, blocks, bt, H, D)
+    bl, r = b.places(0, kv[0] - 1, kv[0])  # the last token's v, seen by its own row alone
+    keep = host.read(1, 1, bl, r)
+    x = keep.copy()
+    x[0, H - 1, 21] = np.nan
+    host.write(1, 1, bl, r, x)
+    q, qx = dense(2 * rng.standard_normal((b.T, H * G, D)), dtype)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, dtype, H * G, D ** -0.5, True, max_seq_tokens=max(n), max_kv_tokens=max(kv))
+        again, ls2 = run_attend(dev, 1, b, q, dtype, H * G, D ** -0.5, True, max_seq_tokens=max(n), max_kv_tokens=max(kv))
+        assert dev.status() == L.LSC_OK
+    assert torch.equal(out.view(torch.uint8), again.view(torch.uint8)) and torch.equal(ls, ls2)
+    got, heads, t = out.view(b.T, H * G, D), slice((H - 1) * G, H * G), int(b.cu[1]) - 1
+    assert torch.isnan(got[t, heads, 16:32]).all()
+    host.write(1, 1, bl, r, keep)
+    want = _kv.attend(host, 1, b, qx, D ** -0.5, True)[0][t, heads]
+    got[t, heads, 16:32] = torch.from_numpy(want[:, 16:32]).to(got)
+    check4(host, 1, b, qx, dtype, D ** -0.5, True, out, ls)
+
+
 @pytest.mark.parametrize("n", [1, 2])
 @pytest.mark.parametrize("dtype,H,G,D", [(BF, 2, 2, 256), (BF, 4, 5, 128), (BF, 8, 1, 64), (BF, 2, 8, 128), (F16, 4, 3, 256),
                                          (F16, 4, 2, 64), (BF, 3, 4, 128)])
