@@ -64,7 +64,7 @@
 // turn, or four each at head_dim 256, whose softmax leaves registers for a fifth
 // warpgroup.  Each copies codes and scales with cp.async to shared memory of its own and
 // converts them there, so none waits for another; bf16 rows of q go to f16 by a power of two.  That is for few
-// row blocks a sequence (128 sequences of 8 tokens behind 500 to 8000, 8 heads of 128, 32 rows a head: 637 us; four
+// row blocks a sequence (128 sequences of 8 tokens behind 500 to 8000, 8 heads of 128, 32 rows a head: 630 us; four
 // warps for K, three for V, 898; 64 of 4 tokens, 2 heads of 256: 102 us); with more
 // the batch's rows are expanded once (lsc_kv_rows4.cu) and the 16-bit forms take them: 24 sequences behind up to 8192, 2
 // heads of 256, 1121 us converted by tile and 776 expanded; 4096 tokens behind 28000, 8 of 128, 2055 and 1440.

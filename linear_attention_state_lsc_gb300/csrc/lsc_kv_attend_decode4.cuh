@@ -27,7 +27,9 @@
 // The weights that stand twice cost 8 and 16 rows more products than the permutations they save: two tokens, 32 q heads, 4
 // heads of 128 71 us beside 63, 16 q heads, 2 of 256 84 beside 68, the 75 us above 81.
 // Tried and not kept: V's pairs made by two products with a zero beside each scale (141 us beside 141), sub-tiles of 32
-// positions (133 us beside 125), two sums a score tile and both halves of a sub-tile unrolled (the same).
+// positions (133 us beside 125), two sums a score tile and both halves of a sub-tile unrolled (the same); at 8 and 16
+// rows nibbles paired by shifts and selections in front of the conversions (82 us beside 75, 65 beside 63), three CTAs an
+// SM with sub-tiles of 32 (69 beside 63).
 //
 // q goes to f16: bf16 rows are brought to [2^14, 2^15) by a power of two that the scores
 // take back, so what bf16 holds down to 2^-28 of a row's largest is exact.
