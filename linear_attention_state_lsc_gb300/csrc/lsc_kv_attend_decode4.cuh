@@ -22,7 +22,7 @@
 // (measured, each alone): 8 cycles a word of codes for conversions, 8 more for V's permutations where there are any.  Up
 // to 4 rows it is 43 % busy and the issue 54 %, with 12 warps an SM waiting for one another's results; behind the
 // permutations 60 and 63 %.  Rows that lie in L2 take 9 % less.  Measured, one token of 128 sequences behind 500 to 8000,
-// 32 q heads, 8 heads of 128: 593 MB in 125 us (4.75 TB/s, 71 % of a copy's rate; with the permutations 139 us, the same
+// 32 q heads, 8 heads of 128: 593 MB in 124 us (4.8 TB/s, 72 % of a copy's rate; with the permutations 139 us, the same
 // rows as E4M3 176); 64 behind 64 to 16384, 16 q heads, 2 of 256: 75 us, 57 %.
 // The weights that stand twice cost 8 and 16 rows more products than the permutations they save: two tokens, 32 q heads, 4
 // heads of 128 71 us beside 63, 16 q heads, 2 of 256 84 beside 68, the 75 us above 81.

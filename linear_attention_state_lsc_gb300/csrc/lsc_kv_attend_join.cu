@@ -9,11 +9,11 @@
 //
 // E2M1 decode steps of few sequences: a unit then has dozens of parts or hundreds, and one warp's walk over them took as
 // long as the parts.  From kManyParts parts a unit on, on average, and up to two turns of CTAs, a CTA takes a row and each
-// of its warps every eighth part.  One token behind 544000, 32 q heads, 8 heads of 128: 183 -> 135 us; behind 32000 58
-// -> 26, 8000 22 -> 15; 4 sequences of 32000, 16 q heads, 2 heads of 256: 51 -> 37; 16 of 34000, 14 parts a unit: 123.4
-// -> 121.7; 32 of up to 16000, 7 parts: 66.5 and 66.7.  Beyond, the CTAs that each look for their run cost more: 4 rows of
-// 64 sequences, 4 heads of 128, 5 parts, 4096 CTAs: 63 and 73; 128 sequences, 2 parts: 125 and 137.  The other types'
-// parts stay in one warp's order of summation.
+// of its warps every eighth part.  One token behind 544000, 32 q heads, 8 heads of 128: 177 -> 131 us; behind 32000 57
+// -> 24, 8000 22 -> 14; 4 sequences of 32000, 16 q heads, 2 heads of 256: 49 -> 33; 16 of 34000, 14 parts a unit: 122.8
+// -> 120.6.  With fewer parts the CTAs that each look for their run cost more: 32 sequences of up to 16000, 7 parts: 65.7
+// and 66.6; two tokens of 64 sequences, 2 heads of 256, 5 parts: 69 and 73; 64 sequences, 8 heads of 128, 4 parts: 71 and
+// 76.  The other types' parts stay in one warp's order of summation.
 #include <cuda_runtime.h>
 
 #include "lsc_internal.h"
