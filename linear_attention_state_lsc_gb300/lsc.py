@@ -43,6 +43,7 @@ LSC_LAYER_ATTENTION, LSC_LAYER_GDN = 0, 1
 LSC_RECURRENT_AUTO, LSC_RECURRENT_TOKEN, LSC_RECURRENT_CHUNKED = 0, 1, 2
 LSC_DECODE_EARLY_STATE = 1
 LSC_F32, LSC_BF16, LSC_F16, LSC_E4M3, LSC_E2M1 = 0, 1, 2, 3, 4
+LSC_ROTARY_MAX_AXES = 8
 
 
 class LscError(RuntimeError):
@@ -561,8 +562,8 @@ def lsc_kv_append(pool, layer, args, stream=None):
 
 
 def rotary(rotary_dim, positions, inv_freq, pair_axis=None, interleaved=False, scale=1.0, axes=None, axis_stride=0):
-    """Rotary positions.  positions: an int32 device tensor, [tokens] or [axes, tokens] (rows may be further apart), or
-    an address with `axes` and `axis_stride`; inv_freq and pair_axis: host values of the rotary_dim / 2 pairs."""
+    """Rotary positions.  positions: an int32 device tensor, [tokens] or [axes, tokens] (rows may be further apart, or one
+    row expanded to all), or an address with `axes` and `axis_stride`; inv_freq and pair_axis: host values of the rotary_dim / 2 pairs."""
     freq = np.ascontiguousarray(inv_freq, np.float64)
     axis = None if pair_axis is None else np.ascontiguousarray(pair_axis, np.uint8)
     for a in (freq, axis):
@@ -573,6 +574,10 @@ def rotary(rotary_dim, positions, inv_freq, pair_axis=None, interleaved=False, s
             raise ValueError("positions: int32 [tokens] or [axes, tokens], tokens side by side")
         axes = positions.shape[0] if positions.dim() == 2 else 1
         axis_stride = positions.stride(0) if axes > 1 else 0
+        # p.expand(axes, tokens): one row for every axis.  A stride of 0 means total_tokens to the library, so that row is
+        # handed over as the one axis that all pairs take; what the library refuses goes to it as it is.
+        if axis_stride == 0 and 1 < axes <= LSC_ROTARY_MAX_AXES and (axis is None or axis.max(initial=0) < axes):
+            axes, axis = 1, None
     r = lsc_rotary(rotary_dim, 1 if axes is None else axes, int(interleaved), scale, freq.ctypes.data,
                    None if axis is None else axis.ctypes.data, ptr(positions), axis_stride)
     r._host = (freq, axis)  # the addresses above

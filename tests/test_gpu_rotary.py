@@ -411,3 +411,32 @@ def test_a_step_in_a_graph(lsc, pool, dtype, D):
             short.__dict__.update(b.__dict__)
             short.T = n
             (check4 if pool == L.LSC_E2M1 else check_attend)(held, 0, short, tq[:n], dtype, D ** -0.5, True, o, None)
+
+
+@pytest.mark.parametrize("D,R", [(128, 64), (80, 20)])
+def test_a_row_expanded_to_every_axis(lsc, D, R):
+    """positions.expand(axes, T), each axis the same row: as the row alone, out of place and with the append."""
+    rng = np.random.default_rng(R)
+    T, H, Hq = 37, 2, 3
+    p = rng.integers(0, 5000, T).astype(np.int32)
+    pos = torch.from_numpy(p).cuda()
+    axis = (np.arange(R // 2) % 3).astype(np.uint8)
+    x, xx = dense(rng.standard_normal((T, Hq, D)), BF)
+    k, kx = dense(rng.standard_normal((T, H, D)), BF)
+    want, size = turn(xx, R, angles(p[None], freqs(R), None), False)
+    kw, ksize = turn(kx, R, angles(p[None], freqs(R), None), False)
+    host = host_pool(BF, 10, 16, H, D)
+    b = Batch(rng, [T], [T + 9], 16, 10)
+    for rows in (pos.expand(3, T), pos[None].expand(3, T)):
+        r = L.rotary(R, rows, freqs(R), pair_axis=axis)
+        out = torch.full_like(x, 7.0)
+        assert L.lsc_rotate(L.rotate_args(T, Hq, D, BF, x, out, r), cur()) == L.LSC_OK
+        check(out.double().cpu().numpy().reshape(T, Hq, D), want, size, BF)
+        out.fill_(7.0)
+        with DevKv(host) as dev:
+            args = L.kv_append_rotated_args(L.kv_append_args(b.device(), k, k, BF), r, Hq, x, out)
+            assert L.lsc_kv_append_rotated(dev.pool, 1, args, cur()) == L.LSC_OK
+            assert dev.status() == L.LSC_OK
+            host.bytes[:] = dev.download()
+        check(out.double().cpu().numpy().reshape(T, Hq, D), want, size, BF)
+        check(host.read(1, 0, *b.places(0, 9, T + 9)), kw, ksize, BF)

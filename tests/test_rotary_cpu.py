@@ -93,3 +93,20 @@ def test_the_binding_reads_positions():
                 dict(inv_freq=FREQ[1:]), dict(pair_axis=[0])):
         with pytest.raises(ValueError):
             L.rotary(**{**dict(rotary_dim=32, positions=p, inv_freq=FREQ), **bad})
+
+
+def test_a_row_expanded_to_every_axis():
+    """Text: every axis takes the same position.  The library reads axis a at positions + a * (axis_stride or
+    total_tokens), so no pair may be given an axis behind the one row that there is."""
+    T = 9
+    p = torch.arange(T, dtype=torch.int32)
+    for pos in (p.expand(3, T), p[None].expand(3, T), p[:1].expand(3, 1), p.expand(8, T)):
+        for axis in (None, [0, 1, 2, 1] * 4):
+            r = L.rotary(32, pos, FREQ, pair_axis=axis)
+            most = 0 if not r.pair_axis else max(ctypes.string_at(r.pair_axis, 16))
+            last = most * (r.axis_stride or pos.shape[1]) + pos.shape[1]  # entries from `positions` on that may be read
+            assert r.positions == p.data_ptr() and last <= pos.shape[1]
+    # what is refused stays refused
+    base = dict(total_tokens=T, num_heads=3, head_dim=64, dtype=L.LSC_BF16, x=DEV, out=DEV + 4096)
+    for r in (L.rotary(32, p.expand(3, T), FREQ, pair_axis=np.full(16, 3)), L.rotary(32, p.expand(9, T), FREQ)):
+        assert L.lsc_rotate(L.rotate_args(**base, rotary=r)) == INV
