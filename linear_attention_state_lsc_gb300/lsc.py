@@ -563,9 +563,14 @@ def lsc_kv_append(pool, layer, args, stream=None):
 
 def rotary(rotary_dim, positions, inv_freq, pair_axis=None, interleaved=False, scale=1.0, axes=None, axis_stride=0):
     """Rotary positions.  positions: an int32 device tensor, [tokens] or [axes, tokens] (rows may be further apart, or one
-    row expanded to all), or an address with `axes` and `axis_stride`; inv_freq and pair_axis: host values of the rotary_dim / 2 pairs."""
+    row expanded to all), or an address with `axes` and `axis_stride`; inv_freq and pair_axis: host values of the
+    rotary_dim / 2 pairs."""
     freq = np.ascontiguousarray(inv_freq, np.float64)
-    axis = None if pair_axis is None else np.ascontiguousarray(pair_axis, np.uint8)
+    axis = None if pair_axis is None else np.asarray(pair_axis)
+    if axis is not None:
+        if not np.isin(axis, np.arange(256)).all():  # a byte each
+            raise ValueError("pair_axis: whole numbers from 0 on, below axes")
+        axis = np.ascontiguousarray(axis, np.uint8)
     for a in (freq, axis):
         if a is not None and a.shape != (rotary_dim // 2,):
             raise ValueError(f"rotary_dim {rotary_dim} has {rotary_dim // 2} pairs, not {a.shape}")

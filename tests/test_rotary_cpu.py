@@ -110,3 +110,15 @@ def test_a_row_expanded_to_every_axis():
     base = dict(total_tokens=T, num_heads=3, head_dim=64, dtype=L.LSC_BF16, x=DEV, out=DEV + 4096)
     for r in (L.rotary(32, p.expand(3, T), FREQ, pair_axis=np.full(16, 3)), L.rotary(32, p.expand(9, T), FREQ)):
         assert L.lsc_rotate(L.rotate_args(**base, rotary=r)) == INV
+
+
+def test_pair_axis_is_held_as_it_is():
+    """Axes that a byte does not hold are refused, not taken modulo 256 or cut to a whole number; those that it holds and
+    that are not there are the library's to refuse."""
+    p = torch.zeros(3, 9, dtype=torch.int32)
+    for bad in (256, 257, -1, -256, 1 << 32, 0.5, 1.75, float("nan")):
+        with pytest.raises(ValueError):
+            L.rotary(32, p, FREQ, pair_axis=np.array([0, 1] * 7 + [2, bad]))
+    for good in ([2] * 16, np.full(16, 2, np.int64), np.full(16, 2.0), [True] * 16, torch.full((16,), 1)):
+        r = L.rotary(32, p, FREQ, pair_axis=good)
+        assert list(ctypes.string_at(r.pair_axis, 16)) == [int(a) for a in good]
