@@ -586,10 +586,17 @@ def rotary(rotary_dim, positions, inv_freq, pair_axis=None, interleaved=False, s
     r = lsc_rotary(rotary_dim, 1 if axes is None else axes, int(interleaved), scale, freq.ctypes.data,
                    None if axis is None else axis.ctypes.data, ptr(positions), axis_stride)
     r._host = (freq, axis)  # the addresses above
+    r._tokens = positions.shape[-1] if hasattr(positions, "dim") else None
     return r
 
 
+def _check_positions(rotary, total_tokens):
+    if getattr(rotary, "_tokens", None) is not None and rotary._tokens < total_tokens:
+        raise ValueError(f"positions of {rotary._tokens} tokens for {total_tokens}")
+
+
 def rotate_args(total_tokens, num_heads, head_dim, dtype, x, out, rotary, x_stride=0, out_stride=0):
+    _check_positions(rotary, total_tokens)
     a = lsc_rotate_args(total_tokens, num_heads, head_dim, dtype, ptr(x), ptr(out), x_stride, out_stride, rotary)
     a._rotary = rotary
     return a
@@ -601,6 +608,7 @@ def lsc_rotate(args, stream=None):
 
 def kv_append_rotated_args(append, rotary, num_q_heads=0, q=None, q_out=None, q_stride=0, q_out_stride=0):
     """append: kv_append_args; q is of its dtype."""
+    _check_positions(rotary, append.batch.total_tokens)
     a = lsc_kv_append_rotated_args(append, rotary, num_q_heads, 0, ptr(q), ptr(q_out), q_stride, q_out_stride)
     a._rotary = rotary
     return a

@@ -122,3 +122,20 @@ def test_pair_axis_is_held_as_it_is():
     for good in ([2] * 16, np.full(16, 2, np.int64), np.full(16, 2.0), [True] * 16, torch.full((16,), 1)):
         r = L.rotary(32, p, FREQ, pair_axis=good)
         assert list(ctypes.string_at(r.pair_axis, 16)) == [int(a) for a in good]
+
+
+def test_positions_of_every_token():
+    """A tensor of positions shorter than the call's tokens would be read past its end: refused when the call's arguments
+    are made.  A longer one is fine (what lies behind is another call's)."""
+    p = torch.zeros(3, 9, dtype=torch.int32)
+    for pos, held in ((p[0], 9), (p[0, :4], 4), (p, 9), (p[:, :4], 4), (p[0, :4].expand(3, 4), 4), (p[0, :0], 0)):
+        r = L.rotary(32, pos, FREQ)
+        rotate = lambda t: L.rotate_args(t, 3, 64, L.LSC_BF16, DEV, DEV + 4096, r)
+        append = lambda t: L.kv_append_rotated_args(L.kv_append_args(batch(total=t), DEV, DEV, L.LSC_BF16), r)
+        for make in (rotate, append):
+            for t in range(held + 1):
+                make(t)
+            for t in (held + 1, 10, 1 << 30):
+                with pytest.raises(ValueError):
+                    make(t)
+    L.rotate_args(1 << 30, 3, 64, L.LSC_BF16, DEV, DEV, rotary())  # an address: the caller knows
