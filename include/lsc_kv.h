@@ -101,8 +101,9 @@ typedef struct {
 
 /* Bytes a pool with this description needs: num_layers * 2 * num_blocks *
  * page_bytes.  Errors: INVALID_ARG, LAYOUT (page smaller than the payload or
- * not a multiple of the element size, an E4M3 or E2M1 block of 2 GiB or more, or an
- * E2M1 head_dim that is no multiple of 16), MISALIGNED (page not a multiple of 16). */
+ * not a multiple of the element size, an E4M3 or E2M1 block of 2 GiB or more, an
+ * E2M1 head_dim that is no multiple of 16, or an E2M1 row of more than 2^31 - 1024
+ * elements), MISALIGNED (page not a multiple of 16). */
 int lsc_kv_pool_required_bytes(const lsc_kv_pool_desc *desc, size_t *total_bytes);
 
 /* Create a K/V pool; device_base == NULL allocates (cudaMalloc, owned),

@@ -76,7 +76,7 @@ int describe(const lsc_kv_pool_desc *d, lsc_kv_pool *g) {
   g->d = *d;
   g->bits = bits;
   const int64_t elements = (int64_t)d->num_kv_heads * d->head_dim;
-  if (bits == 4 && elements > INT32_MAX) return LSC_ERR_LAYOUT;
+  if (bits == 4 && elements > INT32_MAX - 1023) return LSC_ERR_LAYOUT;  // rows are walked in stretches of up to 1024, in 32 bits
   g->row_bytes = bits == 4 ? elements / 2 : elements * (bits / 8);
   g->payload = g->row_bytes * d->block_tokens;
   if (bits <= 8) {  // codes, then one scale byte per (row, head), or per 16 elements of it, at the next 16 B boundary

@@ -65,3 +65,13 @@ def test_plain_quantiser():
     full = ((byte >= 8) & (top <= held)).repeat(16, -1)  # scales with all their bits
     assert (best <= top.repeat(16, -1) * 3 / 16)[full].all() and full.any()
     np.testing.assert_array_equal(value4(*quantise4(y))[full], y[full])
+
+
+def test_rows_near_two_to_the_31_elements(lsc):
+    """The row kernels round a row up to whole stretches of 1024 elements and count them in 32 bits."""
+    for short, want in ((1024, L.LSC_OK), (1008, L.LSC_ERR_LAYOUT), (512, L.LSC_ERR_LAYOUT), (16, L.LSC_ERR_LAYOUT)):
+        d = L.lsc_kv_pool_desc(1, 2, 1, (2 ** 31 - short) // 16, 16, L.LSC_E2M1, 1 << 31)
+        rc, pool = L.lsc_kv_pool_create(d, FAKE_BASE, 1 << 50)
+        assert rc == want
+        if rc == L.LSC_OK:
+            L.lsc_kv_pool_destroy(pool)
