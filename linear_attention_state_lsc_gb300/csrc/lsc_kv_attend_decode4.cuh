@@ -234,8 +234,9 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
         const uint32_t ex = top >> 7;  // 2^k <= the largest magnitude < 2^(k + 1), where that is a normal number
         const bool plain = ex == 0 || ex == 255;
         const float down = plain ? 1.f : inv_scale_of(ex), more = plain ? 1.f : 16384.f;
-        // (a hidden score is -infinity times this, so it may not be 0; products of q and k are below 2^39)
-        if (!plain) q_up[h] = fmaxf(q_up[h] * __uint_as_float(ex << 23) * (1.f / 16384.f), 0x1p-120f);
+        // (a hidden score is -infinity times this, so it may not be 0; products of q and k are below 2^39; the power by
+        // itself first, 2^-140 to 2^113: with the scale in it 2^127 is too much before its 2^14 are taken back)
+        if (!plain) q_up[h] = fmaxf(q_up[h] * (__uint_as_float(ex << 23) * (1.f / 16384.f)), 0x1p-120f);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll

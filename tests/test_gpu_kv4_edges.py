@@ -170,6 +170,31 @@ def test_queries_too_small_to_count(lsc):
                 check4(host, 1, b, qx, BF, scale, True, out, ls)
 
 
+@every_form
+@pytest.mark.parametrize("scale", [1.0, 4.0, 64.0])
+def test_the_largest_queries_meet_zeros(lsc, form, scale):
+    """Rows of q whose one element is the largest power of two of their type, and K zero there: every score is 0, however
+    much the scale and that element come to together (2^133 at most, less than 2^14 beyond 32 bits)."""
+    dtype, n, bt, D, G = FORMS[form]
+    if dtype == F32:
+        pytest.skip("32-bit rows are scaled in 32 bits")
+    rng = np.random.default_rng(n + D)
+    b = Batch(rng, [n, 1], [n + 61, 20], bt, 120)
+    host = filled4(rng, b, 120, bt, 2, D)
+    for i in range(2):
+        bl, r = b.places(i, 0, int(b.kv[i]))
+        k = host.read(1, 0, bl, r)
+        k[:, :, 5] = 0
+        host.write(1, 0, bl, r, k)
+    x = np.zeros((b.T, 2 * G, D))
+    x[:, :, 5] = 2.0 ** 15 if dtype == F16 else 2.0 ** 127
+    q, qx = dense(x, dtype)
+    with DevKv(host) as dev:
+        out, ls = run_attend(dev, 1, b, q, dtype, 2 * G, scale, True, max_seq_tokens=n)
+        assert dev.status() == L.LSC_OK
+    check4(host, 1, b, qx, dtype, scale, True, out, ls)
+
+
 @pytest.mark.parametrize("gap", [3.0, 16.9, 24.9, 25.1])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dtype,n", [(BF, 1), (F16, 2), (BF, 20), (F16, 20)])
