@@ -321,9 +321,7 @@ typedef struct {
  * scores.  Its lse is not finite.  Positions it does not see, and rows behind a sequence's
  * last token, do not enter, whatever they hold.  Sums and softmax statistics
  * are 32-bit; with 16-bit q the weights exp(s_j - max) are rounded before they
- * meet v: to bf16 in bf16 pools, and in E2M1 pools read by many rows of BF16 q (four
- * row blocks a sequence or more: the batch's cached rows are then first made 16 bits
- * wide in the workspace); to f16 in f16 and E4M3 pools and elsewhere, in full down to
+ * meet v: to bf16 in bf16 pools; to f16 in f16, E4M3 and E2M1 pools, in full down to
  * 2^-21 of a row's largest weight and to a multiple of 2^-31 of it below (E4M3
  * pools, more than 64 rows of q a kv head: to nine significant bits or more down
  * to 2^-17 of it, to a multiple of 2^-25 of it below, and elements of q below 2^-9
@@ -331,9 +329,9 @@ typedef struct {
  * one times the scale of its row of v).  E4M3 rows of v with a scale below 2^-76 add an
  * absolute error of up to 2^-93 a position; beside rows with a scale of 2^e above
  * 2^100, positions lighter than 2^(e - 133) of the heaviest drop out of the sums,
- * and rows of k with such a scale may overflow their scores.  Where an E2M1 pool's
- * weights are f16, rows of BF16 q are brought to f16 by a power of two: elements
- * below 2^-28 of their row's largest (and rows below 2^-111) lose bits.  A group of
+ * and rows of k with such a scale may overflow their scores.  Over E2M1
+ * pools rows of BF16 q are brought to f16 by a power of two: elements below 2^-28 of
+ * their row's largest (and rows below 2^-111) lose bits.  A group of
  * NaN in an E2M1 pool's v makes its 16 columns NaN in the rows that see the position.
  * Two calls with the same inputs give the same bits.
  * A sequence that exceeds max_kv_tokens is recorded as INVALID_ARG in the status

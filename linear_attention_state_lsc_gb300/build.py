@@ -19,7 +19,7 @@ SOURCES = ["lsc_host.cu", "lsc_copy.cu", "lsc_gdn.cu", "lsc_rec128.cu", "lsc_chu
            "lsc_prefill.cu", "lsc_kv.cu", "lsc_kv_rows.cu", "lsc_kv_rotary.cu", "lsc_kv_rows4.cu", "lsc_kv_attend_any.cu", "lsc_kv_attend_join.cu",
            "lsc_kv_attend_decode_bf16.cu", "lsc_kv_attend_decode_f16.cu", "lsc_kv_attend_decode_e4m3.cu", "lsc_kv_attend_decode_e2m1.cu",
            "lsc_kv_attend_rows_bf16.cu", "lsc_kv_attend_rows_f16.cu", "lsc_kv_attend_rows_e4m3.cu",
-           "lsc_kv_attend_chunk_bf16.cu", "lsc_kv_attend_chunk_f16.cu", "lsc_kv_attend_chunk_e4m3.cu", "lsc_kv_attend_chunk_e2m1.cu", "lsc_prefix_cache.cpp", "lsc_store.cpp"]
+           "lsc_kv_attend_chunk_bf16.cu", "lsc_kv_attend_chunk_f16.cu", "lsc_kv_attend_chunk_e4m3.cu", "lsc_kv_attend_chunk_e2m1.cu", "lsc_kv_attend_chunk_f16_q_bf16.cu", "lsc_prefix_cache.cpp", "lsc_store.cpp"]
 HEADERS = [os.path.join(CSRC, h) for h in ("lsc_internal.h", "lsc_ptx.h", "lsc_tc.h", "lsc_chunk.h", "lsc_gdn_common.cuh", "lsc_decode.cuh", "lsc_kv_batch.cuh", "lsc_kv_rows.cuh", "lsc_kv_walk.cuh", "lsc_kv_attend.cuh",
                                               "lsc_kv_attend_rows.cuh", "lsc_kv_attend_decode.cuh", "lsc_kv_attend_decode4.cuh", "lsc_kv_attend_chunk.cuh")] + \
     [os.path.join(INCLUDE, h) for h in ("lsc.h", "lsc_prefix_cache.h", "lsc_kv.h", "lsc_store.h")]

@@ -344,7 +344,7 @@ struct KvAttendParams {
   uint64_t drain_limit_ns; // bound of the wait for issued MMAs at the end
   int32_t num_sms;
 };
-// A batch's cached rows of an E2M1 layer at 16 bits, in blocks of kExpandTokens positions (lsc_kv_rows4.cu).
+// A batch's cached rows of an E2M1 layer as f16, in blocks of kExpandTokens positions (lsc_kv_rows4.cu).
 constexpr int kExpandTokens = 128;
 struct KvExpand {
   uint16_t *k, *v;           // [n_seq * blocks][kExpandTokens][kv heads][head_dim]

@@ -390,8 +390,8 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   return kAny;
 }
 
-// E2M1 chunks of many row blocks: the batch's rows are first made 16 bits wide in the workspace (lsc_kv_rows4.cu) and
-// the 16-bit chunk kernels take them.  The host knows the sequences' row blocks on average and the workspace by the
+// E2M1 chunks of many row blocks: the batch's rows are first made f16 in the workspace (lsc_kv_rows4.cu) and
+// the f16 chunk kernels take them, so the numbers are those of the E2M1 chunk kernel.  The host knows the sequences' row blocks on average and the workspace by the
 // bounds of the lengths; beyond kExpandMost bytes of it, and below expand_blocks blocks, the E2M1 chunk kernel converts
 // each tile it meets.  16 sequences behind 4000 to 8000, 2, 4 and 6 blocks each, expanded and converted by tile: 8 heads of
 // 128: 301 and 277, 468 and 515, 589 and 758 us; 2 heads of 256: 125 and 82, 175 and 143, 184 and 202 us.
@@ -418,7 +418,7 @@ bool expands(const lsc_kv_pool *p, const lsc::KvAttendParams &r, const lsc::Atte
          expand_bytes(r, r.b.n_seq) <= kExpandMost;
 }
 
-// The step's layer and batch as the 16-bit chunk kernels see them, over `space`; map receives its TMA map.
+// The step's layer and batch as the f16 chunk kernels see them, over `space`; map receives its TMA map.
 bool expand_layer(const lsc_kv_pool *p, uint8_t *space, lsc::KvAttendParams *r, lsc::KvExpand *x, CUtensorMap *map) {
   lsc::KvLayer &L = r->L;
   const int32_t blocks = (r->max_kv + lsc::kExpandTokens - 1) / lsc::kExpandTokens;
@@ -429,14 +429,14 @@ bool expand_layer(const lsc_kv_pool *p, uint8_t *space, lsc::KvAttendParams *r, 
   x->v = (uint16_t *)((uint8_t *)x->k + all * page);
   x->blocks = blocks;
   const int tile = chunk_tile(L.head_dim);
-  if (!encode_map(p->encode, map, x->k, r->dtype, 16, lsc::kExpandTokens, L.heads, L.head_dim, page, all, tile, tile))
+  if (!encode_map(p->encode, map, x->k, LSC_F16, 16, lsc::kExpandTokens, L.heads, L.head_dim, page, all, tile, tile))
     return false;
   L.k = (uint8_t *)x->k;
   L.v = (uint8_t *)x->v;
   L.page = page;
   L.num_blocks = (int32_t)all;
   L.block_tokens = lsc::kExpandTokens;
-  L.dtype = r->dtype;
+  L.dtype = LSC_F16;  // code times scale is exact in it
   L.scale_off = 0;
   L.by_block.set(lsc::kExpandTokens);
   r->b.table = x->table;

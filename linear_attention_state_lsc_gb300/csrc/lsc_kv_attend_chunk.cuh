@@ -66,7 +66,7 @@
 // converts them there, so none waits for another; bf16 rows of q go to f16 by a power of two.  That is for few
 // row blocks a sequence (128 sequences of 8 tokens behind 500 to 8000, 8 heads of 128, 32 rows a head: 630 us; four
 // warps for K, three for V, 898; 64 of 4 tokens, 2 heads of 256: 102 us); with more
-// the batch's rows are expanded once (lsc_kv_rows4.cu) and the 16-bit forms take them: 24 sequences behind up to 8192, 2
+// the batch's rows are expanded to f16 once (lsc_kv_rows4.cu) and the f16 form takes them, with the same bits a weight: 24 sequences behind up to 8192, 2
 // heads of 256, 1121 us converted by tile and 776 expanded; 4096 tokens behind 28000, 8 of 128, 2055 and 1440.
 //
 // Positions that only some rows of a unit see may hold infinities and NaN: see
@@ -314,8 +314,9 @@ struct Ring {
   }
 };
 
-// BF16: the products' type (f16 for E2M1 pools).  Q8: E4M3 pools.  Q4: E2M1 pools.
-template <bool BF16, bool Q8, int D, bool Q4>
+// BF16: the products' type (f16 for E2M1 pools).  Q8: E4M3 pools.  Q4: E2M1 pools.  QB: q and out are bf16 beside f16 blocks
+// (the expanded rows of an E2M1 pool; with Q4 p.dtype says it).
+template <bool BF16, bool Q8, int D, bool Q4, bool QB>
 __global__ void __launch_bounds__((Conf<D, Q8, BF16, Q4>::threads), 1)
 chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ CUtensorMap map) {
   using C = Conf<D, Q8, BF16, Q4>;
@@ -324,7 +325,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   Smem<D, Q8, Q4> &sm = *reinterpret_cast<Smem<D, Q8, Q4> *>(smem_raw);
   const int tid = threadIdx.x, w = tid >> 5, ln = tid & 31;
   const KvLayer &L = p.L;
-  const bool out_bf16 = Q4 ? p.dtype == LSC_BF16 : BF16;
+  const bool q_bf16 = QB || (Q4 ? p.dtype == LSC_BF16 : BF16);
   if (w == 8) {
     tc::tmem_alloc(&sm.tmem, 512);
     tc::tmem_relinquish();
@@ -424,7 +425,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
           t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
           const uint32_t ex = t >> 7;  // 2^(ex - 127) <= the largest magnitude: brought to 2^7, where both powers are normal
-          if constexpr (Q4) {  // to 2^14, the last that f16 has: elements down to 2^-28 of the row's largest keep their bits
+          if constexpr (Q4 || QB) {  // to 2^14, the last that f16 has: elements down to 2^-28 of the row's largest keep their bits
             const bool plain = ex < 16 || ex == 255;
             down[i] = plain ? 1.f : __uint_as_float((268 - ex) << 23);
             if ((ln & 3) == 0) sm.up[w][i * 8 + oct] = plain ? 1.f : __uint_as_float((ex - 14) << 23);
@@ -438,8 +439,8 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
         __syncwarp();
         c_next = p.scale_log2 * sm.up[w][ln];
       };
-      if constexpr (Q4) {
-        if (p.dtype == LSC_BF16) {
+      if constexpr (Q4 || QB) {
+        if (q_bf16) {
           find_powers();
           // a score that is hidden is -infinity times this, so it may not be 0; products of q and k are below 2^39
           c_next = fmaxf(c_next, 0x1p-120f);
@@ -788,7 +789,7 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
           uint32_t v[16];
           if (whole) {
 #pragma unroll
-            for (int y = 0; y < 16; ++y) v[y] = pack2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]), out_bf16);
+            for (int y = 0; y < 16; ++y) v[y] = pack2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]), q_bf16);
             rows_out(v, x * 2);
           } else {
 #pragma unroll
@@ -1201,10 +1202,10 @@ chunk_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_const
   }
 }
 
-template <bool BF16, bool Q8, int D, bool Q4>
+template <bool BF16, bool Q8, int D, bool Q4, bool QB>
 cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
   static SmemLimit limit;
-  auto *k = chunk_attend_kernel<BF16, Q8, D, Q4>;
+  auto *k = chunk_attend_kernel<BF16, Q8, D, Q4, QB>;
   const int smem = (int)sizeof(Smem<D, Q8, Q4>);
   static_assert(sizeof(Smem<D, Q8, Q4>) <= 227 * 1024, "more shared memory than a block has");
   const cudaError_t e = limit.ensure((const void *)k, smem);
@@ -1212,12 +1213,12 @@ cudaError_t launch_one(const KvAttendParams &p, const AttendPlan &plan, cudaStre
   return launch_pdl(k, plan.ctas, Conf<D, Q8, BF16, Q4>::threads, smem, stream, p, p.map ? *p.map : CUtensorMap{});
 }
 
-template <bool BF16, bool Q8, bool Q4 = false>
+template <bool BF16, bool Q8, bool Q4 = false, bool QB = false>
 cudaError_t launch_type(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream) {
   switch (p.L.head_dim) {
-    case 64: return launch_one<BF16, Q8, 64, Q4>(p, plan, stream);
-    case 128: return launch_one<BF16, Q8, 128, Q4>(p, plan, stream);
-    default: return launch_one<BF16, Q8, 256, Q4>(p, plan, stream);
+    case 64: return launch_one<BF16, Q8, 64, Q4, QB>(p, plan, stream);
+    case 128: return launch_one<BF16, Q8, 128, Q4, QB>(p, plan, stream);
+    default: return launch_one<BF16, Q8, 256, Q4, QB>(p, plan, stream);
   }
 }
 
@@ -1228,5 +1229,6 @@ cudaError_t launch_kv_attend_chunk_bf16(const KvAttendParams &p, const AttendPla
 cudaError_t launch_kv_attend_chunk_f16(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_chunk_e4m3(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 cudaError_t launch_kv_attend_chunk_e2m1(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
+cudaError_t launch_kv_attend_chunk_f16_q_bf16(const KvAttendParams &p, const AttendPlan &plan, cudaStream_t stream);
 
 }  // namespace lsc

@@ -276,6 +276,7 @@ cudaError_t launch_kv_attend_chunk(const KvAttendParams &p, const AttendPlan &pl
   const cudaError_t e = p.L.dtype == LSC_E2M1   ? launch_kv_attend_chunk_e2m1(p, plan, stream)
                         : p.L.dtype == LSC_E4M3 ? launch_kv_attend_chunk_e4m3(p, plan, stream)
                         : p.L.dtype == LSC_BF16 ? launch_kv_attend_chunk_bf16(p, plan, stream)
+                        : p.dtype == LSC_BF16   ? launch_kv_attend_chunk_f16_q_bf16(p, plan, stream)
                                                 : launch_kv_attend_chunk_f16(p, plan, stream);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }

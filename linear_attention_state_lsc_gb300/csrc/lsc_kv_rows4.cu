@@ -1,5 +1,5 @@
 // lsc_kv_rows4.cu -- append and gather over an E2M1 layer of the K/V block pool
-// (include/lsc_kv.h), and a batch's cached rows at 16 bits in a workspace for prefill
+// (include/lsc_kv.h), and a batch's cached rows as f16 in a workspace for prefill
 // chunks (lsc_kv_attend).
 //
 // Both directions move 2 bytes a dense element (16-bit types) and 9/16 of a byte in
@@ -22,7 +22,7 @@
 // and gather 63.9 us in place of 62.8, 1000 tokens' gather in a captured graph 3.6 in place of 3.2).
 //
 // Expanded rows: blocks of kExpandTokens positions, sequence i's from block i *
-// blocks_of_a_sequence on, with a block table of their own, so the 16-bit chunk kernels
+// blocks_of_a_sequence on, with a block table of their own, so the f16 chunk kernels
 // read them as they read a pool.  The chunk kernel for E2M1 pools makes the codes f16 for
 // each row block anew; with many row blocks a sequence doing it once is cheaper.
 #include <cuda_runtime.h>
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, kGatherOcc) gather4_kernel(const __g
 // ---- expanded rows ---------------------------------------------------------------
 constexpr int kExpandRows = 32;  // positions of a CTA
 
-template <typename D, int NS, int U>
+template <int NS, int U>
 __global__ void __launch_bounds__(kThreads, kGatherOcc) expand_kernel(const __grid_constant__ KvAttendParams p, const __grid_constant__ KvExpand x,
                                                                       int per, FastDiv by_per) {
   __shared__ int64_t s_page[kExpandRows];
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, kGatherOcc) expand_kernel(const __gr
   const int ln = threadIdx.x & 31, row_el = L.heads * L.head_dim, all = n * per;
   const int64_t row0 = (int64_t)block0 * kExpandTokens + pos0 % kExpandTokens, lane_off = L.v - L.k;
   for (int i0 = threadIdx.x >> 5; i0 < all; i0 += kWarps * U) {
-    Item<D, NS> y[U];
+    Item<__half, NS> y[U];
     int at[U], el[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, kGatherOcc) expand_kernel(const __gr
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t to = ((row0 + at[u]) * row_el + el[u]) * kSize<D>;
+      const int64_t to = ((row0 + at[u]) * row_el + el[u]) * kSize<__half>;
       y[u].store((uint8_t *)x.k + to, (uint8_t *)x.v + to, row_el - el[u]);
     }
   }
@@ -252,12 +252,11 @@ cudaError_t gather_typed(const KvRowsParams &p, int grid, int tok, cudaStream_t 
                    : launch_pdl(gather4_kernel<D, 1, 4>, grid, kThreads, 0, stream, p, tok, per, by(per));
 }
 
-template <typename D>
 cudaError_t expand_typed(const KvAttendParams &p, const KvExpand &x, int grid, cudaStream_t stream) {
   const int ns = stretches_of_item(p.L), per = stretches(p.L, 256 * ns);
-  return ns == 4   ? launch_pdl(expand_kernel<D, 4, 1>, grid, kThreads, 0, stream, p, x, per, by(per))
-         : ns == 2 ? launch_pdl(expand_kernel<D, 2, 2>, grid, kThreads, 0, stream, p, x, per, by(per))
-                   : launch_pdl(expand_kernel<D, 1, 4>, grid, kThreads, 0, stream, p, x, per, by(per));
+  return ns == 4   ? launch_pdl(expand_kernel<4, 1>, grid, kThreads, 0, stream, p, x, per, by(per))
+         : ns == 2 ? launch_pdl(expand_kernel<2, 2>, grid, kThreads, 0, stream, p, x, per, by(per))
+                   : launch_pdl(expand_kernel<1, 4>, grid, kThreads, 0, stream, p, x, per, by(per));
 }
 
 }  // namespace
@@ -280,7 +279,7 @@ cudaError_t launch_kv_expand(const KvAttendParams &p, KvExpand x, cudaStream_t s
   x.chunks = (p.max_kv + kExpandRows - 1) / kExpandRows;
   x.by_chunks.set((uint32_t)x.chunks);
   const int grid = p.b.n_seq * x.chunks;
-  const cudaError_t e = p.dtype == LSC_BF16 ? expand_typed<__nv_bfloat16>(p, x, grid, stream) : expand_typed<__half>(p, x, grid, stream);
+  const cudaError_t e = expand_typed(p, x, grid, stream);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

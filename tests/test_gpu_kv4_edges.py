@@ -171,6 +171,36 @@ def test_queries_too_small_to_count(lsc):
 
 
 @every_form
+def test_weights_have_eleven_bits(lsc, form):
+    """V is zero but for two positions, +x and -x, whose weights differ little: what is left of them shows how many bits
+    they had.  f16's half step (2^-11) in every form, BF16 q among them; beside it what 32-bit sums are off by."""
+    dtype, n, bt, D, G = FORMS[form]
+    kv, H = n + 61, 2
+    rng = np.random.default_rng(n + 5 * D)
+    b = Batch(rng, [n], [kv], bt, 120)
+    host = Host4(120, bt, H, D)
+    bl, r = b.places(0, 0, kv)
+    host.write(1, 0, bl, r, 0.3 * rng.standard_normal((kv, H, D)))
+    v = np.zeros((kv, H, D))
+    v[7] = rng.standard_normal((H, D))
+    v[40] = -v[7]
+    host.write(1, 1, bl, r, v)
+    q, qx = dense(rng.standard_normal((b.T, H * G, D)), dtype)
+    scale = 0.5 * D ** -0.5
+    want, _, mass, reach, vmax = _kv.attend(host, 1, b, qx, scale, False)
+    kmax = np.abs(host.read(1, 0, bl, r)).max()
+    es = D * 2.0 ** -23 * reach + (0 if dtype == F32 else D * 2.0 ** -25 * np.abs(qx).max(-1) * kmax * scale)
+    rel = (2.0 ** -11 + 2 * es + (kv + 8) * 2.0 ** -23 + 2.0 ** -20)[..., None]
+    err = rel * mass + kv * 2.0 ** -32 * vmax[..., None]
+    bound = err + HALF[dtype] * (np.abs(want) + err) + 1e-30
+    with DevKv(host) as dev:
+        out, _ = run_attend(dev, 1, b, q, dtype, H * G, scale, False, max_seq_tokens=n)
+        assert dev.status() == L.LSC_OK
+    over = np.abs(out.double().cpu().numpy().reshape(want.shape) - want) / bound
+    assert over.max() <= 1, (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+@every_form
 @pytest.mark.parametrize("scale", [1.0, 4.0, 64.0])
 def test_the_largest_queries_meet_zeros(lsc, form, scale):
     """Rows of q whose one element is the largest power of two of their type, and K zero there: every score is 0, however
