@@ -306,7 +306,8 @@ typedef struct {
   void *workspace;        /* device scratch of workspace_bytes, what
                              lsc_kv_attend_workspace_bytes says or more, 16-byte aligned, untouched by
                              others until the call's work on the stream completes; NULL = the
-                             library takes it from the device's stream-ordered pool */
+                             library takes it from the device's stream-ordered pool (an E2M1
+                             pool's 16-bit rows, see there, only if it gets them) */
   size_t workspace_bytes;
 } lsc_kv_attend_args;
 

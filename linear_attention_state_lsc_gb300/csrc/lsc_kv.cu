@@ -772,14 +772,19 @@ int lsc_kv_attend(lsc_kv_pool *p, int32_t layer, const lsc_kv_attend_args *a, vo
   const Form form = attend_form(r, &plan);
   cudaStream_t s = (cudaStream_t)stream;
   void *ws = a->workspace;
-  const bool expand = form == kChunk && expands(p, r, plan);
-  const size_t parts = expand ? up16(plan.ws_bytes) : plan.ws_bytes, need = parts + (expand ? expand_bytes(r, r.b.n_seq) : 0);
-  if (need > 0) {
-    if (ws && a->workspace_bytes < attend_workspace(p, r)) return LSC_ERR_INVALID_ARG;
-    if (!ws && cudaMallocAsync(&ws, need, s) != cudaSuccess) {
-      cudaGetLastError();
-      return LSC_ERR_NO_MEMORY;
-    }
+  bool expand = form == kChunk && expands(p, r, plan);
+  const size_t parts = expand ? up16(plan.ws_bytes) : plan.ws_bytes;
+  size_t need = parts + (expand ? expand_bytes(r, r.b.n_seq) : 0);
+  if (ws && need > 0 && a->workspace_bytes < attend_workspace(p, r)) return LSC_ERR_INVALID_ARG;
+  if (!ws && expand && (fault("no_rows") || cudaMallocAsync(&ws, need, s) != cudaSuccess)) {  // by tile, then: the same bits
+    cudaGetLastError();
+    ws = nullptr;
+    expand = false;
+    need = plan.ws_bytes;
+  }
+  if (!ws && need > 0 && cudaMallocAsync(&ws, need, s) != cudaSuccess) {
+    cudaGetLastError();
+    return LSC_ERR_NO_MEMORY;
   }
   if (plan.ws_bytes > 0) r.ws = (uint8_t *)ws;
   r.whole = !plan.may_cut;

@@ -491,6 +491,32 @@ def test_workspace_rules(lsc, form):
             assert L.lsc_kv_attend(dev.pool, 1, args, cur()) == L.LSC_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("form", [f for f in FORMS if f.startswith("expanded")])
+@pytest.mark.parametrize("kv", [900, 5000])
+def test_without_memory_for_its_rows_a_step_goes_on(lsc, form, kv, monkeypatch):
+    """Without a workspace, where the device has no room for the expanded rows (injected): converted by tile, the same
+    bits, whole units and cut ones."""
+    dtype, n, bt, D, G = FORMS[form]
+    rng = np.random.default_rng(n + kv)
+    blocks = (n + kv) // bt + 40
+    b = Batch(rng, [n, n], [n + kv, n + 9], bt, blocks + n // bt)
+    host = filled4(rng, b, blocks + n // bt, bt, 2, D)
+    q, qx = dense(rng.standard_normal((b.T, 2 * G, D)), dtype)
+    with DevKv(host) as dev:
+        def call():
+            out, ls = torch.zeros(b.T, 2 * G * D, dtype=TORCH[dtype], device="cuda"), torch.zeros(b.T, 2 * G, device="cuda")
+            args = L.kv_attend_args(b.device(), 2 * G, q, out, dtype, 0.1, lse=ls, max_seq_tokens=n)
+            assert L.lsc_kv_attend(dev.pool, 1, args, cur()) == L.LSC_OK
+            assert dev.status() == L.LSC_OK
+            return out, ls
+        want = call()
+        monkeypatch.setenv("LSC_FAULT", "no_rows")
+        got = call()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    if kv < 1000:
+        check4(host, 1, b, qx, dtype, 0.1, True, *got)
+
+
 @pytest.mark.parametrize("form", ["decode-bf16", "chunk-bf16", "expanded-bf16", "expanded-256"])
 def test_graphs_with_workspaces_of_their_own(lsc, form):
     """Append and attend captured twice on a side stream, replayed in turn with other lengths and tables: the status word
