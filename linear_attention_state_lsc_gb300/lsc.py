@@ -585,7 +585,8 @@ def rotary(rotary_dim, positions, inv_freq, pair_axis=None, interleaved=False, s
             axes, axis = 1, None
     r = lsc_rotary(rotary_dim, 1 if axes is None else axes, int(interleaved), scale, freq.ctypes.data,
                    None if axis is None else axis.ctypes.data, ptr(positions), axis_stride)
-    r._host = (freq, axis)  # the addresses above
+    r._host = (freq, axis)  # the addresses above live as long as this does
+    r._positions = positions
     r._tokens = positions.shape[-1] if hasattr(positions, "dim") else None
     return r
 

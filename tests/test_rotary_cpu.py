@@ -1,6 +1,8 @@
 """What the rotary calls refuse before any device work, through the C ABI on host-only pools, and the binding's own
 checks.  Only refused calls are made where a GPU is visible."""
 import ctypes
+import gc
+import weakref
 
 import numpy as np
 import pytest
@@ -139,3 +141,17 @@ def test_positions_of_every_token():
                 with pytest.raises(ValueError):
                     make(t)
     L.rotate_args(1 << 30, 3, 64, L.LSC_BF16, DEV, DEV, rotary())  # an address: the caller knows
+
+
+def test_positions_live_as_long_as_the_arguments():
+    """positions made in place of an argument (a cast, a slice moved to the device) are not given back before the call."""
+    p = torch.zeros(9, dtype=torch.int64)
+    made = p.to(torch.int32)
+    alive = weakref.ref(made)
+    args = L.rotate_args(9, 3, 64, L.LSC_BF16, DEV, DEV, L.rotary(32, made, FREQ))
+    del made
+    gc.collect()
+    assert alive() is not None
+    del args
+    gc.collect()
+    assert alive() is None
