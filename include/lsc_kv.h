@@ -3,7 +3,8 @@
  * views of every attention layer; copy_prefix, the device copy that moves a
  * reused prefix's K/V rows into another sequence's blocks; and the calls of a
  * step over one layer's blocks: append (write the new tokens' K/V rows,
- * quantised when the pool holds e4m3), gather (read rows back dense) and
+ * quantised when the pool holds e4m3 or e2m1), the rotary positions of q and k before
+ * or with it, gather (read rows back dense) and
  * attend (softmax attention of the new tokens over the cached ones).  Pools hold
  * K and V at 32, 16, 8 (e4m3) or 4 bits (e2m1) an element.
  *
@@ -212,10 +213,11 @@ int lsc_kv_append(lsc_kv_pool *pool, int32_t layer, const lsc_kv_append_args *ar
  *   (x, y) -> scale * (x cos a - y sin a, x sin a + y cos a).
  * The elements behind rotary_dim stay as they are.  Several axes (time, height and
  * width of an image or video token) are given to the pairs in any pattern; text takes
- * the same position on each.  Angles are exact to 2^-31 turns or so at every position
- * of 32 bits, negative ones too, and cosines and sines to 2^-22; elements are turned in
- * 32 bits and rounded once.  With negated frequencies the turn is undone (and a
- * gradient of what came out becomes that of what went in).
+ * the same position on each.  Angles are exact to 2^-26 turns at every position of 32
+ * bits, negative ones too, and cosines and sines to 2^-22; elements are turned in 32
+ * bits and rounded once.  Negated frequencies transpose the turn: the gradient of what
+ * came out becomes that of what went in, with the factor, and with a scale of 1 the
+ * turn is undone.
  */
 typedef struct {
   int32_t rotary_dim;        /* even, 2 .. head_dim, at most 512 */
@@ -358,8 +360,11 @@ int lsc_kv_attend(lsc_kv_pool *pool, int32_t layer, const lsc_kv_attend_args *ar
  * total_tokens, max_seq_tokens and max_kv_tokens (0 meaning total_tokens and
  * max_blocks * block_tokens) are no larger: asked once with the largest sizes, one
  * workspace serves every layer and step of a stream, prefill and decode alike.  E2M1
- * pools whose steps may bring many rows ask for the 16-bit rows too, n_seq times
- * max_kv_tokens of them (never more than 4 GiB: larger steps do without).
+ * pools ask for the batch's cached rows at 16 bits too, n_seq times max_kv_tokens of
+ * them, where a step that brings more than 16 packed rows a kv head may bring 1024 of
+ * them a sequence or more (768 at head_dim 256) on average over all n_seq: attend then
+ * makes each cached row f16 once, and not for each tile of q (never more than 4 GiB:
+ * larger steps do without).  The numbers are the same either way.
  * 0: none.  The pointers are checked and do not matter otherwise.  Errors: as
  * lsc_kv_attend's argument checks; CUDA (a host-only pool). */
 int lsc_kv_attend_workspace_bytes(const lsc_kv_pool *pool, const lsc_kv_attend_args *args, size_t *bytes);

@@ -1,7 +1,8 @@
 // lsc_kv.cu -- host side of the attention K/V block pool (include/lsc_kv.h):
 // layout, views, copy_prefix's validation and launch plans, and the argument
-// checks of append, gather and attend.  The copy kernel is kv_copy_kernel in
-// lsc_copy.cu; append and gather are in lsc_kv_rows.cu.
+// checks of append, rotary positions, gather and attend.  The copy kernel is
+// kv_copy_kernel in lsc_copy.cu; append and gather are in lsc_kv_rows.cu (E2M1 pools:
+// lsc_kv_rows4.cu), rotary positions in lsc_kv_rotary.cu, attend in lsc_kv_attend_*.
 //
 // Sources, cited by page title and section:
 //   [VA] "非连续 KV Cache" §3, §3.2, §3.4 (page-strided block views, separate K
@@ -246,7 +247,7 @@ int check_rows(const lsc_kv_pool *p, int32_t layer, const lsc_kv_batch &b, const
   return check_device(p);
 }
 
-// 2^64 times the fraction of a turn in an angle of f radians, rounded: f / (2 pi) as a sum of two doubles (the product
+// 2^64 times the fraction of a turn in an angle of f radians, cut to whole numbers (off by 2 at most): f / (2 pi) as a sum of two doubles (the product
 // with 1 / (2 pi), itself two doubles, and what its rounding left).
 uint64_t turns_of(double f) {
   constexpr double kInv2Pi = 0x1.45f306dc9c883p-3, kInv2PiLow = -0x1.6b01ec5417056p-57;
@@ -390,11 +391,13 @@ Form attend_form(const lsc::KvAttendParams &r, lsc::AttendPlan *plan) {
   return kAny;
 }
 
-// E2M1 chunks of many row blocks: the batch's rows are first made f16 in the workspace (lsc_kv_rows4.cu) and
-// the f16 chunk kernels take them, so the numbers are those of the E2M1 chunk kernel.  The host knows the sequences' row blocks on average and the workspace by the
-// bounds of the lengths; beyond kExpandMost bytes of it, and below expand_blocks blocks, the E2M1 chunk kernel converts
-// each tile it meets.  16 sequences behind 4000 to 8000, 2, 4 and 6 blocks each, expanded and converted by tile: 8 heads of
-// 128: 301 and 277, 468 and 515, 589 and 758 us; 2 heads of 256: 125 and 82, 175 and 143, 184 and 202 us.
+// E2M1 chunks of many row blocks: the batch's rows are first made f16 in the workspace (lsc_kv_rows4.cu) and the f16
+// chunk kernels take them, to the bits of the E2M1 chunk kernel.  The host knows the sequences' row blocks on average and
+// the workspace by the bounds of the lengths; beyond kExpandMost bytes of it, and below expand_blocks blocks, the E2M1
+// chunk kernel converts each tile it meets.  16 sequences behind 4000 to 8000, 2, 4 and 6 blocks each, expanded and
+// converted by tile: 8 heads of 128: 301 and 277, 468 and 515, 589 and 758 us; 2 heads of 256: 125 and 82, 175 and 143, 184
+// and 202 us.  (Batches whose sequences differ are judged by their average all the same: 4096 tokens behind 28000 take
+// 1324 us, and with 16 single tokens beside them, not expanded, 2164.)
 int64_t expand_blocks(int head_dim) { return head_dim == 256 ? 6 : 4; }
 constexpr int64_t kExpandMost = (int64_t)4 << 30;
 

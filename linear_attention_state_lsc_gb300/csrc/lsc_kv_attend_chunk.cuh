@@ -66,8 +66,9 @@
 // converts them there, so none waits for another; bf16 rows of q go to f16 by a power of two.  That is for few
 // row blocks a sequence (128 sequences of 8 tokens behind 500 to 8000, 8 heads of 128, 32 rows a head: 630 us; four
 // warps for K, three for V, 898; 64 of 4 tokens, 2 heads of 256: 102 us); with more
-// the batch's rows are expanded to f16 once (lsc_kv_rows4.cu) and the f16 form takes them, with the same bits a weight: 24 sequences behind up to 8192, 2
-// heads of 256, 1121 us converted by tile and 776 expanded; 4096 tokens behind 28000, 8 of 128, 2055 and 1440.
+// the batch's rows are expanded to f16 once (lsc_kv_rows4.cu) and the f16 form takes them, to the same bits: 24 sequences
+// behind up to 8192, 2 heads of 256, 1121 us converted by tile and 738 to 792 expanded; 4096 tokens behind 28000, 8 of
+// 128, 2055 and 1411 to 1447.
 //
 // Positions that only some rows of a unit see may hold infinities and NaN: see
 // lsc_kv_attend_rows.cuh; here the softmax threads search such a tile's v.

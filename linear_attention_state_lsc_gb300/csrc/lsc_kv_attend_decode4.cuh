@@ -18,14 +18,14 @@
 //     More rows: a byte permutation for each pair of columns makes two pairs of positions.
 //   * scales come with 4- to 16-byte cp.async, a position a lane, into a ring beside the codes'; V's go
 //     through shared memory once more as f16, pairs of positions side by side as the products want them.
-// What bounds it: instructions.  The ALU does a conversion, a permutation, a logic or a shift every second cycle
-// (measured, each alone): 8 cycles a word of codes for conversions, 8 more for V's permutations where there are any.  Up
+// What bounds it: nothing that is full; the latency of chains of instructions on few warps.  The ALU does a conversion, a
+// permutation, a logic or a shift every second cycle (measured, each alone): 8 cycles a word of codes for conversions, 8 more for V's permutations where there are any.  Up
 // to 4 rows it is 43 % busy and the issue 54 %, with 12 warps an SM waiting for one another's results; behind the
 // permutations 60 and 63 %.  Rows that lie in L2 take 9 % less.  Measured, one token of 128 sequences behind 500 to 8000,
 // 32 q heads, 8 heads of 128: 593 MB in 124 us (4.8 TB/s, 72 % of a copy's rate; with the permutations 139 us, the same
 // rows as E4M3 176); 64 behind 64 to 16384, 16 q heads, 2 of 256: 75 us, 57 %.
 // The weights that stand twice cost 8 and 16 rows more products than the permutations they save: two tokens, 32 q heads, 4
-// heads of 128 71 us beside 63, 16 q heads, 2 of 256 84 beside 68, the 75 us above 81.
+// heads of 128 71 us beside 63, 16 q heads, 2 of 256 84 beside 68; the one token of 64 sequences above (8 rows) 81 beside 75.
 // Tried and not kept: V's pairs made by two products with a zero beside each scale (141 us beside 141), sub-tiles of 32
 // positions (133 us beside 125), two sums a score tile and both halves of a sub-tile unrolled (the same); at 8 and 16
 // rows nibbles paired by shifts and selections in front of the conversions (82 us beside 75, 65 beside 63), three CTAs an
@@ -140,9 +140,9 @@ decode4_attend_kernel(const __grid_constant__ KvAttendParams p, const __grid_con
   const int box = p.box_decode, boxes = KEYS / box;
   const int bi = ln & 15, br = bi < boxes ? bi * box : 0;
   uint8_t *const ring = sm.ring + w * ST * 2 * C::half;
-  // where a lane's K scale bytes are in a word: its group of an even chunk and of the odd one behind it
   // ldmatrix rows: chunk c of K (c even) and V is the offset of chunk 0 xor 16 c
   const uint32_t koff = chunk_at<RB>(KEYS, ln & 15, ln >> 4), voff = chunk_at<RB>(KEYS, ln, 0);
+  // where a lane's K scale bytes are in a word: its group of an even chunk and of the odd one behind it
   const uint32_t kh = tq >> 1, ksel = 0x4040u | kh | (kh + 2) << 8;
   // few: the weights of positions 2 tq, 2 tq + 1 -> the operand for each: the weight, and a zero behind it where this
   // lane's column of the product (g) is for v's even columns, before it where it is for the odd ones

@@ -9,7 +9,7 @@
 // exact fraction for every position of 32 bits (the fraction is within 2^-63 or so of
 // inv_freq's, 2^-32 turns at position 2^31), where a product in fp32 would have lost the
 // angle at a few thousand.  Its upper 32 bits, as a signed number of half turns in
-// fp32, go to sincospif.
+// fp32 (24 bits: off by 2^-26 turns at most), go to sincospif.
 //
 // Each element is read once and written once: HBM bounds a large call, the launch a
 // small one.  All rows of all tokens are cut into equal runs, one a warp
