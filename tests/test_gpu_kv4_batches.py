@@ -1,5 +1,6 @@
 """GPU: the row calls over E2M1 pools (append, rotated append, gather) with batches that do not fit, in their vector and
-their element kernels; and which kernels the calls of test_gpu_kv4_edges.py's forms take, as the device saw them."""
+their element kernels; which kernels the calls of test_gpu_kv4_edges.py's forms take, as the device saw them; and the
+layers of a step behind one another with one workspace."""
 import numpy as np
 import pytest
 import torch
@@ -156,3 +157,54 @@ def test_row_kernels_as_the_device_sees_them(lsc, dtype, D, stride, rotary_dim):
     assert ("gather4_kernel" if aligned else "rows_any_kernel") in got["gather"]
     vec = aligned and D % 32 == 0 and rotary_dim % 32 == 0
     assert ("rotary_kernel" in got["rotated"], "rotary_any_kernel" in got["rotated"]) == (vec, not vec), got["rotated"]
+
+
+@pytest.mark.parametrize("n,D,G", [(1, 128, 4), (2, 256, 8), (20, 128, 4), (300, 128, 4), (100, 256, 8)], ids=str)
+def test_layers_behind_one_another_share_a_workspace(lsc, n, D, G):
+    """A step of twelve layers, rotated append, attend and the rows read back of each, with one workspace and the next
+    layer's q made from this one's result: enqueued without a pause the bits are those of waiting after every call."""
+    rng = np.random.default_rng(n + D)
+    H, bt, layers, S, R = 2, 64, 12, 3, 32
+    kv = [n + 400, n, n + 900]
+    blocks = sum(-(-x // bt) for x in kv)
+    b = Batch(rng, [n] * S, kv, bt, blocks)
+    host = Host4(blocks, bt, H, D, layers=layers, fill=0)
+    for i in range(S):
+        bl, row = b.places(i, 0, kv[i])
+        x = rng.standard_normal((len(bl), H, D))
+        for layer in range(layers):
+            for lane in (0, 1):
+                host.write(layer, lane, bl, row, np.roll(x, layer + 7 * lane, 0))
+    (first, _), (k, _), (v, _) = (dense(rng.standard_normal((b.T, h, D)), BF) for h in (H * G, H, H))
+    pos = torch.arange(b.T, dtype=torch.int32, device="cuda").expand(3, b.T)
+    r = L.rotary(R, pos, freqs(R), pair_axis=np.arange(R // 2) % 3)
+    results, batch = [], b.device()
+    with DevKv(host) as dev:
+        for wait in (True, False, False):
+            dev.buf.copy_(torch.from_numpy(host.bytes.reshape(-1)))
+            q, out, ws, seen = first.clone(), torch.empty_like(first), None, []
+            backs = [[torch.empty_like(k) for _ in "kv"] for _ in range(layers)]
+            for layer in range(layers):
+                append = L.kv_append_args(batch, k, v, BF)
+                steps = [lambda: L.lsc_kv_append_rotated(dev.pool, layer, L.kv_append_rotated_args(append, r, H * G, q, q), cur())]
+                a = L.kv_attend_args(batch, H * G, q, out, BF, D ** -0.5, max_seq_tokens=n, max_kv_tokens=max(kv))
+                if ws is None:
+                    rc, need = L.lsc_kv_attend_workspace_bytes(dev.pool, a)
+                    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+                a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+                steps.append(lambda: L.lsc_kv_attend(dev.pool, layer, a, cur()))
+                steps.append(lambda: L.lsc_kv_gather(dev.pool, layer, L.kv_gather_args(batch, *backs[layer], BF), cur()))
+                for step in steps:
+                    assert step() == L.LSC_OK
+                    if wait:
+                        torch.cuda.synchronize()
+                q.copy_(out)
+                seen.append(out.clone())
+            results.append((seen, backs, dev.download()))
+            assert dev.status() == L.LSC_OK
+    for seen, backs, held in results[1:]:
+        for layer in range(layers):
+            assert torch.isfinite(seen[layer]).all()
+            assert torch.equal(seen[layer], results[0][0][layer]), layer
+            assert all(torch.equal(x, y) for x, y in zip(backs[layer], results[0][1][layer]))
+        np.testing.assert_array_equal(held, results[0][2])
