@@ -3,10 +3,10 @@
  * views of every attention layer; copy_prefix, the device copy that moves a
  * reused prefix's K/V rows into another sequence's blocks; and the calls of a
  * step over one layer's blocks: append (write the new tokens' K/V rows,
- * quantised when the pool holds e4m3 or e2m1), the rotary positions of q and k before
- * or with it, gather (read rows back dense) and
- * attend (softmax attention of the new tokens over the cached ones).  Pools hold
- * K and V at 32, 16, 8 (e4m3) or 4 bits (e2m1) an element.
+ * quantised when the pool holds e4m3 or e2m1; rotary positions of q and k with it
+ * or before it), gather (read rows back dense) and attend (softmax attention of the
+ * new tokens over the cached ones).  Pools hold K and V at 32, 16, 8 (e4m3) or 4 bits
+ * (e2m1) an element.
  *
  * Sources, cited by page title and section:
  *   [VA] "非连续 KV Cache" (vLLM-Ascend design document) §3 (block stride =
